@@ -175,6 +175,7 @@ def _loss(s, wide):
     z = x @ w.t()
     top = z.amax(1)
     lse = top + torch.log(torch.exp(z - top[:, None]).sum(1))
+    lse = torch.where(keep, lse, torch.zeros_like(lse))        # nothing is asked of a padded position
     loss = torch.where(keep, lse - z[row, at], torch.zeros_like(lse))
     if not c["grad"]:
         return {"loss": loss, "lse": lse}
@@ -254,12 +255,13 @@ def work(case):
         if case["bits8"]:       # the codes, and their values as they are read back
             moved += M * D * (1 + 2) + 4 * M
         return {"bytes": moved + D * e + 4 * M, "flops": 5 * M * D}
-    V = case["vocab"]
-    read = (M + V) * D * e + 8 * M
+    # a padded position needs no product: only its zeros are written
+    V, kept = case["vocab"], case["kept"] * M
+    read = (kept + V) * D * e + 8 * M
     if case["grad"]:
         # logits, logits again (they are not kept), and the two gradients
-        return {"bytes": read + (M + V) * D * e + 4, "flops": 8 * M * D * V}
-    return {"bytes": read + 8 * M, "flops": 2 * M * D * V}
+        return {"bytes": read + (M + V) * D * e + 4, "flops": 8 * kept * D * V}
+    return {"bytes": read + 8 * M, "flops": 2 * kept * D * V}
 
 
 # ---- the same results from the definitions, in 64 bits, written apart from the plain form
@@ -312,7 +314,7 @@ def _exact_loss(s):
     loss = torch.zeros(M, dtype=torch.float64, device="cuda")
     loss[kept] = lse[kept] - (x[kept] * w[t[kept]]).sum(1)
     if not c["grad"]:
-        return {"loss": loss, "lse": lse}
+        return {"loss": loss, "lse": torch.zeros_like(lse).index_copy_(0, kept, lse[kept])}
     weight = torch.zeros(M, dtype=torch.float64, device="cuda")
     weight[kept] = float(s["grad"]) / max(1, kept.numel())
     soft = torch.softmax(logits, 1)
