@@ -222,12 +222,12 @@ def _own(s):
             out["read_back"] = cg.rms_norm_expand(r.codes, r.scales, dtype=low)
         return out
     if not c["grad"]:
-        loss, lse, _ = cg.linear_cross_entropy_fwd(s["x"], s["table"], s["targets"], ignore_index=IGNORE,
+        loss, lse = cg.linear_cross_entropy_fwd(s["x"], s["table"], s["targets"], ignore_index=IGNORE,
                                                    reduction="none")
         return {"loss": loss, "lse": lse}
-    loss, lse, count = cg.linear_cross_entropy_fwd(s["x"], s["table"], s["targets"], ignore_index=IGNORE,
+    loss, lse = cg.linear_cross_entropy_fwd(s["x"], s["table"], s["targets"], ignore_index=IGNORE,
                                                    reduction="mean")
-    dx, dtable = cg.linear_cross_entropy_bwd(s["grad"], s["x"], s["table"], s["targets"], lse, count,
+    dx, dtable = cg.linear_cross_entropy_bwd(s["grad"], s["x"], s["table"], s["targets"], lse,
                                              ignore_index=IGNORE, reduction="mean")
     return {"loss": loss, "dx": dx, "dtable": dtable}
 
