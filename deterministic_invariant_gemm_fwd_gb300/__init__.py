@@ -9,11 +9,24 @@ and call it.  Weights are stored [in, out] (sgemm-bi page, "Use").
     dX = linear_dx(dY, W, tier="exact")      # dX = dY.W^T
     dW = linear_dw(X, dY, tier="exact")      # dW = X^T.dY
 
+The operators around a language model's linear layers (``include/carbon_lm.h``:
+token embedding, RMS norm with an 8-bit checkpoint, output layer with softmax
+cross entropy, and their gradients) are ``embedding_fwd`` / ``_bwd``,
+``rms_norm_fwd`` / ``_bwd`` / ``_expand`` and ``linear_cross_entropy_fwd`` /
+``_bwd``.
+
 ``deterministic_invariant_gemm_fwd_gb300.nn`` wraps them in an autograd
-``Linear`` / ``deterministic_linear`` (with a deterministic bias gradient).
+``Linear`` / ``deterministic_linear`` (with a deterministic bias gradient),
+``Embedding``, ``RMSNorm``, ``norm_linear`` and ``linear_cross_entropy``.
 """
 from __future__ import annotations
 
+from ._binding import (carbon_embedding_bwd,  # noqa: F401
+                       carbon_embedding_bwd_workspace, carbon_embedding_fwd,
+                       carbon_linear_xent_bwd, carbon_linear_xent_bwd_workspace,
+                       carbon_linear_xent_fwd, carbon_linear_xent_fwd_workspace,
+                       carbon_rms_norm_bwd, carbon_rms_norm_bwd_workspace,
+                       carbon_rms_norm_expand, carbon_rms_norm_fwd)
 from ._binding import (CarbonError, carbon_abi_version, carbon_debug_exact_y64,  # noqa: F401
                        carbon_debug_exact_path_counts, carbon_debug_exact_phase_time,
                        carbon_debug_kernel_time,
@@ -25,6 +38,8 @@ from ._binding import (CarbonError, carbon_abi_version, carbon_debug_exact_y64, 
                        carbon_get_device_status, carbon_measure_fp64_rate,
                        carbon_measure_int_mac_rate,
                        carbon_status_string)
+from .lm import (RmsNorm, embedding_bwd, embedding_fwd, linear_cross_entropy_bwd,  # noqa: F401
+                 linear_cross_entropy_fwd, rms_norm_bwd, rms_norm_expand, rms_norm_fwd)
 
 
 def _dtype_code(t):

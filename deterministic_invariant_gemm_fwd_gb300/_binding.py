@@ -1,4 +1,5 @@
-"""Thin ctypes binding of the carbon_gemm C ABI (include/carbon_gemm.h).
+"""Thin ctypes binding of the library's C ABI (include/carbon_gemm.h,
+include/carbon_lm.h).
 
 Argument marshalling only: every step of the GEMMs runs in the library's
 CUDA kernels.  Functions take torch tensors (or raw integer device pointers)
@@ -19,7 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 # bounds-checked libcarbon_gemm_bounds.so); default: the regular one.
 LIB_PATH = os.environ.get("CARBON_GEMM_LIBRARY") or os.path.join(HERE, "libcarbon_gemm.so")
 HEADERS = [os.path.join(os.path.dirname(HERE), "include", h)
-           for h in ("carbon_gemm.h", "carbon_gemm_debug.h")]
+           for h in ("carbon_gemm.h", "carbon_gemm_debug.h", "carbon_lm.h")]
 
 F32, BF16, F16 = 0, 1, 2
 TIER_EXACT, TIER_TC, TIER_SUPERACC = 0, 1, 2
@@ -29,6 +30,7 @@ STATUS = {0: "CARBON_OK", 1: "CARBON_ERR_INVALID_ARG", 2: "CARBON_ERR_UNSUPPORTE
           6: "CARBON_ERR_SCRATCH_LIMIT", 7: "CARBON_ERR_OUT_OF_BOUNDS"}
 DTYPES = {"f32": F32, "bf16": BF16, "f16": F16}
 TIERS = {"exact": TIER_EXACT, "tc": TIER_TC, "superacc": TIER_SUPERACC}
+REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 PASSES = {"fwd": PASS_FWD, "dx": PASS_DX, "dw": PASS_DW}
 
 
@@ -48,6 +50,7 @@ def _load() -> ctypes.CDLL:
             "`python deterministic_invariant_gemm_fwd_gb300/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i64, i32, dp = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double
+    f32 = ctypes.c_float
     sig = {
         "carbon_gemm_fwd": [vp, vp, vp, vp, i64, i64, i64, i32, i32, vp],
         "carbon_gemm_dx": [vp, vp, vp, i64, i64, i64, i32, i32, vp],
@@ -57,6 +60,13 @@ def _load() -> ctypes.CDLL:
         "carbon_gemm_exact_bf16_noalloc": [i32, vp, vp, vp, vp, i64, i64, i64, vp],
         "carbon_gemm_chunk_values": [i32, vp, vp, vp, i64, i64, i64, i32, vp],
         "carbon_chunk_values_combine": [vp, vp, i64, i64, i64, vp, i32, vp],
+        "carbon_embedding_fwd": [vp, vp, vp, i64, i64, i64, f32, i32, vp],
+        "carbon_embedding_bwd": [vp, vp, vp, i64, i64, i64, f32, i64, i32, vp, i64, i32, vp],
+        "carbon_rms_norm_fwd": [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, f32, i32, vp],
+        "carbon_rms_norm_bwd": [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, vp, i64, i32, vp],
+        "carbon_rms_norm_expand": [vp, vp, vp, vp, i64, i64, i32, vp],
+        "carbon_linear_xent_fwd": [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, vp, i64, i32, vp],
+        "carbon_linear_xent_bwd": [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, vp, i64, i32, vp],
         "carbon_debug_exact_y64": [i32, vp, vp, vp, vp, i64, i64, i64, i32, vp],
         "carbon_debug_tc_f32": [i32, vp, vp, vp, vp, i64, i64, i64, vp],
         "carbon_debug_round": [i32, vp, vp, i64, vp],
@@ -68,6 +78,11 @@ def _load() -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
+    for name in ("carbon_embedding_bwd_workspace", "carbon_rms_norm_bwd_workspace",
+                 "carbon_linear_xent_fwd_workspace", "carbon_linear_xent_bwd_workspace"):
+        fn = getattr(lib, name)
+        fn.argtypes = [i64] * (2 if "rms_norm" in name else 3)
+        fn.restype = i64
     lib.carbon_status_string.argtypes = [i32]
     lib.carbon_status_string.restype = ctypes.c_char_p
     lib.carbon_last_cuda_error.argtypes = []
@@ -190,6 +205,84 @@ def carbon_chunk_values_combine(out, P, nchunks, rows, cols, bias, dtype, stream
     _check(_lib().carbon_chunk_values_combine(_ptr(out), _ptr(P), nchunks, rows, cols, _ptr(bias),
                                               _code(DTYPES, dtype), _stream(stream)),
            "carbon_chunk_values_combine")
+
+
+def carbon_embedding_fwd(out, table, ids, M, V, D, scale, dtype, stream=None) -> None:
+    """out[m] = scale * table[ids[m]] (ids int64)."""
+    _check(_lib().carbon_embedding_fwd(_ptr(out), _ptr(table), _ptr(ids), M, V, D, scale,
+                                       _code(DTYPES, dtype), _stream(stream)),
+           "carbon_embedding_fwd")
+
+
+def carbon_embedding_bwd(dtable, dy, ids, M, V, D, scale, padding_idx, accumulate, workspace,
+                         workspace_bytes, dtype, stream=None) -> None:
+    """dtable[v] = (dtable[v] +) scale * sum of dy[m] over the tokens m of id v."""
+    _check(_lib().carbon_embedding_bwd(_ptr(dtable), _ptr(dy), _ptr(ids), M, V, D, scale, padding_idx,
+                                       1 if accumulate else 0, _ptr(workspace), workspace_bytes,
+                                       _code(DTYPES, dtype), _stream(stream)),
+           "carbon_embedding_bwd")
+
+
+def carbon_embedding_bwd_workspace(M, V, D) -> int:
+    return int(_lib().carbon_embedding_bwd_workspace(M, V, D))
+
+
+def carbon_rms_norm_fwd(y, h_out, rstd, codes, scales, x, residual, gamma, M, D, eps, dtype,
+                        stream=None) -> None:
+    """y = norm(x + residual) * gamma; h_out, rstd and the 8-bit checkpoint where they are given."""
+    _check(_lib().carbon_rms_norm_fwd(_ptr(y), _ptr(h_out), _ptr(rstd), _ptr(codes), _ptr(scales),
+                                      _ptr(x), _ptr(residual), _ptr(gamma), M, D, eps,
+                                      _code(DTYPES, dtype), _stream(stream)),
+           "carbon_rms_norm_fwd")
+
+
+def carbon_rms_norm_bwd(dx, dgamma, y_out, dy, h, codes, scales, rstd, gamma, dh, M, D, workspace,
+                        workspace_bytes, dtype, stream=None) -> None:
+    """Gradients of the norm from h, or from the 8-bit checkpoint."""
+    _check(_lib().carbon_rms_norm_bwd(_ptr(dx), _ptr(dgamma), _ptr(y_out), _ptr(dy), _ptr(h),
+                                      _ptr(codes), _ptr(scales), _ptr(rstd), _ptr(gamma), _ptr(dh),
+                                      M, D, _ptr(workspace), workspace_bytes,
+                                      _code(DTYPES, dtype), _stream(stream)),
+           "carbon_rms_norm_bwd")
+
+
+def carbon_rms_norm_bwd_workspace(M, D) -> int:
+    return int(_lib().carbon_rms_norm_bwd_workspace(M, D))
+
+
+def carbon_rms_norm_expand(out, codes, scales, gamma, M, D, dtype, stream=None) -> None:
+    """out = codes * scales (* gamma)."""
+    _check(_lib().carbon_rms_norm_expand(_ptr(out), _ptr(codes), _ptr(scales), _ptr(gamma), M, D,
+                                         _code(DTYPES, dtype), _stream(stream)),
+           "carbon_rms_norm_expand")
+
+
+def carbon_linear_xent_fwd(losses, total, lse, count, x, table, targets, M, D, V, ignore_index,
+                           reduction, workspace, workspace_bytes, dtype, stream=None) -> None:
+    """Softmax cross entropy of x . table^T against targets (int64), logits not stored."""
+    _check(_lib().carbon_linear_xent_fwd(_ptr(losses), _ptr(total), _ptr(lse), _ptr(count), _ptr(x),
+                                         _ptr(table), _ptr(targets), M, D, V, ignore_index,
+                                         _code(REDUCTIONS, reduction), _ptr(workspace),
+                                         workspace_bytes, _code(DTYPES, dtype), _stream(stream)),
+           "carbon_linear_xent_fwd")
+
+
+def carbon_linear_xent_fwd_workspace(M, D, V) -> int:
+    return int(_lib().carbon_linear_xent_fwd_workspace(M, D, V))
+
+
+def carbon_linear_xent_bwd(dx, dtable, grad, x, table, targets, lse, M, D, V, ignore_index,
+                           reduction, workspace, workspace_bytes, dtype, stream=None) -> None:
+    """Gradients of carbon_linear_xent_fwd with respect to x and the table."""
+    _check(_lib().carbon_linear_xent_bwd(_ptr(dx), _ptr(dtable), _ptr(grad), _ptr(x), _ptr(table),
+                                         _ptr(targets), _ptr(lse), M, D, V, ignore_index,
+                                         _code(REDUCTIONS, reduction), _ptr(workspace),
+                                         workspace_bytes, _code(DTYPES, dtype), _stream(stream)),
+           "carbon_linear_xent_bwd")
+
+
+def carbon_linear_xent_bwd_workspace(M, D, V) -> int:
+    return int(_lib().carbon_linear_xent_bwd_workspace(M, D, V))
 
 
 def carbon_get_device_status(stream=None) -> int:

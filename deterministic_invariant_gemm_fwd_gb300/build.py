@@ -33,7 +33,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 VARIANTS = {"regular": (LIB, BUILD_DIR, []),
             "bounds": (LIB_BOUNDS, os.path.join(HERE, "_build_bounds"), ["-DCARBON_DEBUG_BOUNDS"])}
 SOURCES = ["api.cu", "exact_kbn.cu", "exact_int.cu", "exact_tc.cu", "superacc.cu", "tc_gemm.cu",
-           "measure.cu"]
+           "embedding.cu", "rms_norm.cu", "linear_xent.cu", "measure.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

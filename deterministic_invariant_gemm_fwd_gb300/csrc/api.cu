@@ -266,12 +266,18 @@ carbon_status_t carbon_get_device_status(carbon_stream_t stream) {
     const carbon_status_t et = carbon::exact_tc_take_device_status();
     const carbon_status_t kb = carbon::kbn_take_device_status();
     const carbon_status_t sa = carbon::superacc_take_device_status();
+    const carbon_status_t em = carbon::embedding_take_device_status();
+    const carbon_status_t no = carbon::norm_take_device_status();
+    const carbon_status_t xe = carbon::xent_take_device_status();
     if (st != CARBON_OK) return st;
     if (tc != CARBON_OK) return tc;
     if (ex != CARBON_OK) return ex;
     if (et != CARBON_OK) return et;
     if (kb != CARBON_OK) return kb;
     if (sa != CARBON_OK) return sa;
+    if (em != CARBON_OK) return em;
+    if (no != CARBON_OK) return no;
+    if (xe != CARBON_OK) return xe;
     return ms;
 }
 

@@ -8,6 +8,7 @@
 
 #include "../../include/carbon_gemm.h"
 #include "../../include/carbon_gemm_debug.h"
+#include "../../include/carbon_lm.h"
 
 namespace carbon {
 
@@ -142,5 +143,10 @@ carbon_status_t measure_take_device_status();
 // (bounds-checked build).
 carbon_status_t kbn_take_device_status();
 carbon_status_t superacc_take_device_status();
+// Status words of the operators around the linear layers (embedding.cu,
+// rms_norm.cu, linear_xent.cu).
+carbon_status_t embedding_take_device_status();
+carbon_status_t norm_take_device_status();
+carbon_status_t xent_take_device_status();
 
 }  // namespace carbon

@@ -1,0 +1,962 @@
+// linear_xent.cu - output layer and softmax cross entropy without stored
+// logits, on the tensor cores.
+//
+//   z = x . table^T,  lse = log sum_v exp z,  loss = lse - z[target]
+//   G = g (softmax(z) - onehot),  dx = G . table,  dtable = G^T . x
+//
+// Positions that count are first gathered into a dense x (ignored ones cost
+// no product, and what they hold reaches no sum).  Then one persistent kernel
+// per direction works through units of one 128-row output tile:
+//   L  128 positions x 256 vocabulary entries of z, reduced over D.
+//      Loss: each row's running maximum and sum of exponentials over 128
+//      entries go out as one (max, sum) pair; a second kernel joins the pairs
+//      in order.  Gradient: exp(z - lse) - onehot goes out as G.
+//   T  128 vocabulary entries x up to 256 columns of dtable, reduced over
+//      the positions: G^T . x.
+//   X  128 positions x up to 256 columns of dx, reduced over kGranule
+//      vocabulary entries at a time: G . table.
+// The gradient takes the vocabulary in pieces: L units of piece p + 1 run
+// before the T and X units of piece p, and G keeps three pieces, so that a
+// unit rarely waits for the units it reads (counters in the workspace; every
+// unit only waits for units earlier in the list, and each CTA takes its units
+// in list order, so the waits end).
+//
+// Fixed order: a unit's k-blocks of 64 run in ascending order into one fp32
+// accumulator.  dx adds the granules' sums in order, so neither the piece
+// size nor the number of positions shows in a row's result.
+#include "bounds.cuh"
+#include "device_sync.cuh"
+#include "rowvec.cuh"
+#include "tcgen05.cuh"
+
+namespace carbon {
+namespace {
+
+__device__ unsigned int g_xent_status = 0;
+#define CHK(idx, len, n) in_bounds(&g_xent_status, (int64_t)(idx), (int64_t)(len), (int64_t)(n))
+
+constexpr int kBM = 128, kBN = 256, kBK = 64;
+constexpr int kStages = 4;
+constexpr int kThreads = 192;            // TMA producer, MMA issuer, 4 epilogue warps
+constexpr int kEpiWarps = 4;
+constexpr uint32_t kBlock = 64 * kBK * 2;             // one 64 x 64 box: 8 KiB
+constexpr uint32_t kABytes = kBM * kBK * 2;
+constexpr uint32_t kStageBytes = kABytes + kBN * kBK * 2;
+constexpr uint32_t kStagingOffset = kStages * kStageBytes;
+constexpr uint32_t kBarOffset = kStagingOffset + kEpiWarps * 4096;
+constexpr uint32_t kSmemBytes = kBarOffset + (2 * kStages + 4) * 8 + 16 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory per block");
+
+constexpr int kGroup = 128;              // vocabulary entries per (max, sum) pair
+constexpr int kGranule = 4096;           // vocabulary entries per partial sum of dx
+constexpr int kPieceBuffers = 3;         // pieces of G in the workspace
+constexpr int64_t kPieceBytes = 64ll << 20;   // largest piece of G, unless one granule is larger
+constexpr int64_t kSlotBytes = 64ll << 20;    // dx: granule sums side by side up to this size
+// G is formed times 2^k, so that probabilities far below the type's (fp16) or
+// fp32's (bf16) smallest normal value keep their bits; the gradients'
+// common factor takes it out again.  |G| <= 2^k: no sum comes near fp32's
+// range for operands of ordinary size.
+constexpr int kScaleBits16 = 12, kScaleBitsBf = 32;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct Head {
+    int kept;                            // positions that count
+    float gscale;                        // the gradients' common factor
+};
+
+// Sizes and workspace addresses, host and device.
+struct Plan {
+    int64_t M, Mp, D, V;                 // Mp: M rounded up to 128, at least 128
+    int vocab_groups;                    // pairs per row
+    int dtiles, dwidth;                  // column tiles of dx and dtable
+    int lwidth;                          // vocabulary entries per L unit
+    int pieces, buffers, piece_cols;
+    int granules;
+    int slots;                           // granule sums of dx kept side by side; 1: added in place
+    bool f16, grad;
+    Head *head;
+    unsigned int *done_l, *done_tx;      // per piece
+    int *rowmap, *inverse, *tgt;
+    float *lse2, *rfac;                  // gradient: lse log2(e) - k, g / max |g|
+    void *xc, *g;
+    float *acc;                          // [slots][Mp][D]
+    float2 *pairs;                       // [vocab_groups][Mp]
+    float *zt;                           // [Mp]
+};
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Fills the plan; returns the workspace bytes.
+int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, bool grad, bool f16) {
+    Plan p = {};
+    p.M = M; p.D = D; p.V = V; p.grad = grad; p.f16 = f16;
+    p.Mp = round_up(M > 0 ? M : 1, kBM);
+    p.vocab_groups = (int)((V + kGroup - 1) / kGroup);
+    p.dtiles = (int)((D + kBN - 1) / kBN);
+    p.dwidth = (int)round_up((D + p.dtiles - 1) / p.dtiles, 64);
+    p.dtiles = (int)((D + p.dwidth - 1) / p.dwidth);
+    p.granules = (int)((V + kGranule - 1) / kGranule);
+    const int64_t tiles256 = p.Mp / kBM * ((V + kBN - 1) / kBN);
+    // narrower tiles where 256-wide ones would leave SMs idle for most of a wave
+    p.lwidth = tiles256 < 152 * 4 ? 128 : 256;
+    int64_t per_piece = kPieceBytes / (p.Mp * 2 * kGranule);
+    if (per_piece < 1) per_piece = 1;
+    if (per_piece > p.granules) per_piece = p.granules;
+    p.piece_cols = (int)(per_piece * kGranule);
+    p.pieces = (int)((V + p.piece_cols - 1) / p.piece_cols);
+    p.buffers = p.pieces < kPieceBuffers ? p.pieces : kPieceBuffers;
+    p.slots = (int64_t)p.granules * p.Mp * D * 4 <= kSlotBytes ? p.granules : 1;
+
+    char *base = static_cast<char *>(ws);
+    int64_t used = 0;
+    auto take = [&](int64_t bytes) {
+        char *q = base + used;
+        used += round_up(bytes, 128);
+        return q;
+    };
+    p.head = reinterpret_cast<Head *>(take(sizeof(Head)));
+    p.done_l = reinterpret_cast<unsigned int *>(take(8 * (int64_t)p.pieces));
+    p.done_tx = p.done_l + p.pieces;
+    p.rowmap = reinterpret_cast<int *>(take(4 * p.Mp));
+    p.inverse = reinterpret_cast<int *>(take(4 * p.Mp));
+    p.tgt = reinterpret_cast<int *>(take(4 * p.Mp));
+    p.xc = take(2 * p.Mp * D);
+    if (grad) {
+        p.lse2 = reinterpret_cast<float *>(take(4 * p.Mp));
+        p.rfac = reinterpret_cast<float *>(take(4 * p.Mp));
+        p.g = take(2 * p.Mp * p.piece_cols * p.buffers);
+        p.acc = reinterpret_cast<float *>(take(4 * (int64_t)p.slots * p.Mp * D));
+    } else {
+        p.pairs = reinterpret_cast<float2 *>(take(8 * (int64_t)p.vocab_groups * p.Mp));
+        p.zt = reinterpret_cast<float *>(take(4 * p.Mp));
+    }
+    if (out) *out = p;
+    return used + 128;                   // room to align the base to 128 bytes
+}
+
+void *align128(void *p) {
+    return reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(p) + 127) & ~static_cast<uintptr_t>(127));
+}
+
+// ---- positions that count --------------------------------------------------------
+
+// One CTA: the list of positions that count, in order, and per position what
+// the tiles need of it.  Loss: writes the zeros of ignored positions.
+constexpr int kScanThreads = 1024, kPerThread = 8;
+
+struct ScanArgs {
+    const int64_t *targets;
+    int64_t ignore_index;
+    int reduction;
+    float *losses, *lse_out;             // loss
+    int64_t *count;
+    const float *grad, *lse_in;          // gradient
+};
+
+__global__ void __launch_bounds__(kScanThreads)
+xent_scan_kernel(const Plan p, const ScanArgs a) {
+    __shared__ int warp_total[32];
+    __shared__ float warp_max[32];
+    __shared__ int base_s;
+    wait_prior_grid();
+    allow_next_grid();
+    const int t = threadIdx.x, lane = t % 32, warp = t / 32;
+    const int bits = p.f16 ? kScaleBits16 : kScaleBitsBf;
+    for (int i = t; i < 2 * p.pieces; i += kScanThreads) p.done_l[i] = 0u;
+
+    auto counts = [&](int64_t m, int64_t *tgt) {
+        *tgt = a.targets[m];
+        return *tgt != a.ignore_index && *tgt >= 0 && *tgt < p.V;
+    };
+    // largest |g| over the positions that count (a gradient per position)
+    float gmax = 0.0f;
+    if (p.grad && a.reduction == CARBON_REDUCE_NONE) {
+        int64_t tgt;
+        for (int64_t m = t; m < p.M; m += kScanThreads)
+            if (counts(m, &tgt)) gmax = fmaxf(gmax, fabsf(a.grad[m]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) gmax = fmaxf(gmax, __shfl_xor_sync(0xffffffffu, gmax, o));
+        if (lane == 0) warp_max[warp] = gmax;
+        __syncthreads();
+        gmax = warp_max[0];
+        for (int w = 1; w < 32; ++w) gmax = fmaxf(gmax, warp_max[w]);
+    }
+    if (t == 0) base_s = 0;
+    __syncthreads();
+    for (int64_t m0 = 0; m0 < p.M; m0 += kScanThreads * kPerThread) {
+        int64_t tgt[kPerThread];
+        unsigned keep = 0u;
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < kPerThread; ++j) {
+            const int64_t m = m0 + (int64_t)t * kPerThread + j;
+            tgt[j] = a.ignore_index;
+            if (m < p.M && CHK(m, 1, p.M)) {
+                if (counts(m, &tgt[j])) { keep |= 1u << j; ++n; }
+                else if (tgt[j] != a.ignore_index) atomicExch(&g_xent_status, (unsigned)CARBON_ERR_OUT_OF_BOUNDS);
+            }
+        }
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) warp_total[warp] = incl;
+        __syncthreads();
+        int pos = base_s + incl - n;
+        for (int w = 0; w < warp; ++w) pos += warp_total[w];
+        __syncthreads();
+        if (t == kScanThreads - 1) base_s = pos + n;
+#pragma unroll
+        for (int j = 0; j < kPerThread; ++j) {
+            const int64_t m = m0 + (int64_t)t * kPerThread + j;
+            if (m >= p.M) break;
+            const bool k = (keep >> j) & 1u;
+            p.inverse[m] = k ? pos : -1;
+            if (k && CHK(pos, 1, p.Mp)) {
+                p.rowmap[pos] = (int)m;
+                p.tgt[pos] = (int)tgt[j];
+                if (p.grad) {
+                    p.lse2[pos] = fmaf(a.lse_in[m], kLog2e, (float)-bits);
+                    p.rfac[pos] = a.reduction != CARBON_REDUCE_NONE ? 1.0f
+                                  : gmax == 0.0f ? 0.0f : __fdiv_rn(a.grad[m], gmax);
+                }
+                ++pos;
+            } else if (!p.grad) {
+                a.losses[m] = 0.0f;
+                a.lse_out[m] = 0.0f;
+            }
+        }
+        __syncthreads();
+    }
+    const int kept = base_s;
+    for (int64_t i = kept + t; i < p.Mp; i += kScanThreads) {
+        p.rowmap[i] = -1;
+        p.tgt[i] = -1;
+        if (p.grad) p.lse2[i] = p.rfac[i] = 0.0f;
+    }
+    if (t == 0) {
+        p.head->kept = kept;
+        if (a.count) *a.count = kept;
+        if (p.grad) {
+            float g = a.reduction == CARBON_REDUCE_NONE ? gmax : a.grad[0];
+            if (a.reduction == CARBON_REDUCE_MEAN) g = __fdiv_rn(g, (float)(kept > 0 ? kept : 1));
+            p.head->gscale = ldexpf(g, -bits);
+        }
+    }
+}
+
+__device__ __forceinline__ int row_tiles(int kept) { return kept > kBM ? (kept + kBM - 1) / kBM : 1; }
+
+// Dense rows of x; zeros up to the last tile's end.  A warp per row.
+__global__ void __launch_bounds__(256)
+xent_gather_kernel(const Plan p, const uint4 *__restrict__ x) {
+    wait_prior_grid();
+    allow_next_grid();
+    const int lane = threadIdx.x % 32;
+    const int64_t nvec = p.D / 8;
+    const int64_t rows = (int64_t)row_tiles(p.head->kept) * kBM;
+    const int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    if (i >= rows) return;
+    const int64_t src = p.rowmap[i];
+    uint4 *dst = static_cast<uint4 *>(p.xc) + i * nvec;
+#pragma unroll 4
+    for (int64_t v = lane; v < nvec; v += 32)
+        if (CHK(i * nvec + v, 1, p.Mp * nvec)) dst[v] = src >= 0 ? x[src * nvec + v] : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// ---- the list of units -------------------------------------------------------------
+
+enum UnitType { UNIT_L = 0, UNIT_T = 1, UNIT_X = 2 };
+
+struct Unit {
+    int type, piece;
+    int m0, n0;              // output tile: first row, first column (rows of the output for T are table rows)
+    int width;               // columns, a multiple of 64
+    int parts;               // accumulations, one after the other (X: granules)
+    int granule;             // X: first granule
+};
+
+// Phases in list order: L(0), then for each piece p: L(p+1), T and X of p.
+struct Walk {
+    const Plan &p;
+    int tm;                  // row tiles of positions
+    int phase = 0;
+    int64_t base = 0, count = 0;
+
+    __device__ Walk(const Plan &plan, int tiles) : p(plan), tm(tiles) { count = size(0); }
+
+    __device__ int cols(int piece) const { return min(p.piece_cols, (int)(p.V - (int64_t)piece * p.piece_cols)); }
+    // phase 0: L(0); 2q+1: L(q+1) (empty for the last piece); 2q+2: T and X of q
+    __device__ int64_t n_l(int piece) const {
+        const int c = p.grad ? cols(piece) : (int)p.V;
+        return (int64_t)tm * ((c + p.lwidth - 1) / p.lwidth);
+    }
+    __device__ int64_t n_t(int piece) const { return (int64_t)((cols(piece) + kBM - 1) / kBM) * p.dtiles; }
+    __device__ int granules_of(int piece) const { return (cols(piece) + kGranule - 1) / kGranule; }
+    __device__ int64_t n_x(int piece) const { return (int64_t)tm * p.dtiles * (p.slots > 1 ? granules_of(piece) : 1); }
+    __device__ int64_t size(int ph) const {
+        if (ph == 0) return n_l(0);
+        if (ph & 1) return (ph + 1) / 2 < p.pieces ? n_l((ph + 1) / 2) : 0;
+        const int q = ph / 2 - 1;
+        return n_t(q) + n_x(q);
+    }
+    // The unit at position u of the list (u never decreases); false past the end.
+    __device__ bool at(int64_t u, Unit *out) {
+        const int last = p.grad ? 2 * p.pieces : 0;
+        while (u >= base + count) {
+            if (phase == last) return false;
+            base += count;
+            count = size(++phase);
+        }
+        int64_t i = u - base;
+        Unit o;
+        o.parts = 1;
+        o.granule = 0;
+        if (phase == 0 || (phase & 1)) {
+            o.type = UNIT_L;
+            o.piece = phase == 0 ? 0 : (phase + 1) / 2;
+            const int c = p.grad ? cols(o.piece) : (int)p.V;
+            o.m0 = (int)(i % tm) * kBM;
+            o.n0 = (int)(i / tm) * p.lwidth;
+            o.width = min(p.lwidth, (c - o.n0 + 63) / 64 * 64);
+        } else {
+            o.piece = phase / 2 - 1;
+            const int64_t nt = n_t(o.piece);
+            if (i < nt) {
+                o.type = UNIT_T;
+            } else {
+                o.type = UNIT_X;
+                i -= nt;
+                const int64_t tiles = (int64_t)tm * p.dtiles;
+                if (p.slots > 1) {
+                    o.granule = (int)(i / tiles);
+                    i -= o.granule * tiles;
+                } else {
+                    o.parts = granules_of(o.piece);
+                }
+            }
+            o.m0 = (int)(i / p.dtiles) * kBM;
+            o.n0 = (int)(i % p.dtiles) * p.dwidth;
+            o.width = min(p.dwidth, (int)(p.D - o.n0 + 63) / 64 * 64);
+        }
+        *out = o;
+        return true;
+    }
+    // k-blocks of part j of a unit.
+    __device__ int k_blocks(const Unit &o, int part) const {
+        if (o.type == UNIT_L) return (int)((p.D + kBK - 1) / kBK);
+        if (o.type == UNIT_T) return tm * (kBM / kBK);
+        const int c = cols(o.piece) - (o.granule + part) * kGranule;
+        return (min(c, kGranule) + kBK - 1) / kBK;
+    }
+};
+
+// ---- PTX pieces ----------------------------------------------------------------------
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(map), "r"(src), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void add_release(unsigned int *p, unsigned int v) {
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned int load_acquire(const unsigned int *p) {
+    unsigned int v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if (F16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Instruction descriptor, kind::f16: fp32 accumulate, A and B both bf16 or
+// both fp16, majorness (1: rows/columns contiguous), N, M = 128.
+__device__ __forceinline__ uint32_t instr_desc(int n, bool a_mn, bool b_mn, bool f16) {
+    return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+           ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+}
+
+// Descriptor of the K = 16 slice k of a tile: K-major rows of 128 bytes, or
+// 64-wide blocks whose rows are k (as in the tensor-core GEMM).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t base, bool mn, int k) {
+    return mn ? smem_desc(base + (uint32_t)k * 2048u, kBlock, 1024u) : smem_desc(base + (uint32_t)k * 32u, 16u, 1024u);
+}
+
+// ---- the tile kernel -------------------------------------------------------------------
+
+struct Maps {
+    CUtensorMap x, w, g;        // operand boxes 64 x 64, 128-byte swizzle
+    CUtensorMap g_out, dt_out;  // 32 x 32 store boxes, 64-byte swizzle
+};
+
+struct Ctx {
+    uint32_t sbase, bars, tmem;
+    volatile uint32_t *abort_flag;
+    __device__ uint32_t full(int s) const { return bars + 8u * s; }
+    __device__ uint32_t empty(int s) const { return bars + 8u * (kStages + s); }
+    __device__ uint32_t tfull(int b) const { return bars + 8u * (2 * kStages + b); }
+    __device__ uint32_t tempty(int b) const { return bars + 8u * (2 * kStages + 2 + b); }
+    __device__ bool wait(uint32_t bar, uint32_t parity) const {
+        if (mbar_wait(bar, parity)) return true;
+        give_up();
+        return false;
+    }
+    __device__ void give_up() const {
+        *abort_flag = 1u;
+        atomicExch(&g_xent_status, (unsigned)CARBON_ERR_TIMEOUT);
+    }
+    __device__ bool aborted() const { return *abort_flag != 0u; }
+    // Waits until *counter reaches n.
+    __device__ bool wait_count(const unsigned int *counter, unsigned int n) const {
+        if (load_acquire(counter) >= n) return true;
+        const uint64_t t0 = global_ns();
+        while (load_acquire(counter) < n) {
+            __nanosleep(64);
+            if (global_ns() - t0 > kWaitBudgetNs) { give_up(); return false; }
+        }
+        return true;
+    }
+};
+
+// What a unit's operands wait for.
+__device__ __forceinline__ bool wait_operands(const Plan &p, const Walk &w, const Unit &o, const Ctx &c) {
+    if (!p.grad) return true;
+    if (o.type == UNIT_L) {                       // its piece's buffer is free
+        const int q = o.piece - p.buffers;
+        return q < 0 || c.wait_count(p.done_tx + q, kEpiWarps * (unsigned)(w.n_t(q) + w.n_x(q)));
+    }
+    return c.wait_count(p.done_l + o.piece, kEpiWarps * (unsigned)w.n_l(o.piece));
+}
+
+__device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w, const Ctx &c) {
+    int s = 0;
+    uint32_t ph = 0;
+    Unit o;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && !c.aborted() && w.at(u, &o); u += gridDim.x) {
+        if (!wait_operands(p, w, o, c)) break;
+        fence_proxy_async_all();                  // other CTAs' G, before this CTA's TMA reads
+        const int gcol = (o.piece % (p.grad ? p.buffers : 1)) * p.piece_cols, v0 = o.piece * p.piece_cols;
+        const int nb = o.width / 64;
+        for (int part = 0; ok && part < o.parts; ++part) {
+            const int nkb = w.k_blocks(o, part), first = (o.granule + part) * (kGranule / kBK);
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!c.wait(c.empty(s), ph ^ 1u)) { ok = false; break; }
+                const uint32_t bar = c.full(s), sa = c.sbase + s * kStageBytes, sb = sa + kABytes;
+                mbar_arrive_expect_tx(bar, kABytes + nb * kBlock);
+                const int k0 = kb * kBK;
+                if (o.type == UNIT_L) {
+                    for (int i = 0; i < 2; ++i) tma_load_2d(sa + i * kBlock, &maps.x, bar, k0, o.m0 + 64 * i);
+                    for (int j = 0; j < nb; ++j) tma_load_2d(sb + j * kBlock, &maps.w, bar, k0, v0 + o.n0 + 64 * j);
+                } else if (o.type == UNIT_T) {
+                    for (int i = 0; i < 2; ++i) tma_load_2d(sa + i * kBlock, &maps.g, bar, gcol + o.m0 + 64 * i, k0);
+                    for (int j = 0; j < nb; ++j) tma_load_2d(sb + j * kBlock, &maps.x, bar, o.n0 + 64 * j, k0);
+                } else {
+                    const int kc = (first + kb) * kBK;
+                    for (int i = 0; i < 2; ++i) tma_load_2d(sa + i * kBlock, &maps.g, bar, gcol + kc, o.m0 + 64 * i);
+                    for (int j = 0; j < nb; ++j) tma_load_2d(sb + j * kBlock, &maps.w, bar, o.n0 + 64 * j, v0 + kc);
+                }
+                if (++s == kStages) { s = 0; ph ^= 1u; }
+            }
+        }
+    }
+    // every load lands before the CTA may exit (stages not armed in this pass
+    // completed earlier, so their wait returns at once)
+    for (int i = 0; i < kStages; ++i) {
+        if (--s < 0) { s = kStages - 1; ph ^= 1u; }
+        if (!mbar_wait(c.full(s), ph)) break;
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ void issue(Walk w, const Ctx &c) {
+    int s = 0, acc = 0;
+    uint32_t ph = 0, aph = 0;
+    Unit o;
+    for (int64_t u = blockIdx.x; !c.aborted() && w.at(u, &o); u += gridDim.x) {
+        const bool a_mn = o.type == UNIT_T, b_mn = o.type != UNIT_L;
+        const uint32_t idesc = instr_desc(o.width, a_mn, b_mn, F16);
+        for (int part = 0; part < o.parts; ++part) {
+            if (!c.wait(c.tempty(acc), aph ^ 1u)) return;
+            tc_fence_after();
+            const uint32_t d = c.tmem + (uint32_t)(acc * kBN);
+            const int nkb = w.k_blocks(o, part);
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!c.wait(c.full(s), ph)) return;
+                tc_fence_after();
+                const uint32_t sa = c.sbase + s * kStageBytes, sb = sa + kABytes;
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k)
+                    mma_bf16(d, operand_desc(sa, a_mn, k), operand_desc(sb, b_mn, k), idesc, (kb | k) != 0 ? 1u : 0u);
+                mma_commit(c.empty(s));
+                if (++s == kStages) { s = 0; ph ^= 1u; }
+            }
+            mma_commit(c.tfull(acc));
+            if (++acc == 2) { acc = 0; aph ^= 1u; }
+        }
+    }
+}
+
+// 32 x 32 sub-tiles to global memory through two staging buffers per warp.
+template <bool F16>
+struct Store {
+    uint32_t stg;
+    int lane, n = 0;
+    __device__ void put(const CUtensorMap *map, const float (&f)[32], int col, int row) {
+        const uint32_t buf = stg + (uint32_t)(n & 1) * 2048u;
+        if (n >= 2 && lane == 0) bulk_wait_read_1();
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < 4; ++g)                       // 16-byte pieces as the 64-byte swizzle expects them
+            st_shared_v4(buf + lane * 64 + 16 * (g ^ ((lane >> 1) & 3)),
+                         make_uint4(pack2<F16>(f[8 * g], f[8 * g + 1]), pack2<F16>(f[8 * g + 2], f[8 * g + 3]),
+                                    pack2<F16>(f[8 * g + 4], f[8 * g + 5]), pack2<F16>(f[8 * g + 6], f[8 * g + 7])));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(map, buf, col, row);
+            bulk_commit();
+        }
+        ++n;
+    }
+};
+
+// Loss: (max, sum) pairs and the targets' logits of this thread's row.
+__device__ __forceinline__ void loss_rows(const Plan &p, const Unit &o, uint32_t tmem, int row) {
+    const int tgt = p.tgt[row];
+    for (int g = 0; g < o.width; g += kGroup) {
+        float mx = -INFINITY, sum = 0.0f;                 // of z log2(e)
+#pragma unroll 1
+        for (int c = g; c < min(g + kGroup, o.width); c += 32) {
+            const int v0 = o.n0 + c;
+            if (v0 >= p.V) break;
+            uint32_t r[32];
+            tmem_ld32(tmem + (uint32_t)c, r);
+            const int n = (int)min((int64_t)32, p.V - v0);
+            float z[32];
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                z[i] = i < n ? __uint_as_float(r[i]) * kLog2e : -INFINITY;
+                top = fmaxf(top, z[i]);
+                if (v0 + i == tgt && CHK(row, 1, p.Mp)) p.zt[row] = __uint_as_float(r[i]);
+            }
+            const float now = fmaxf(mx, top), ref = now == -INFINITY ? 0.0f : now;
+            sum *= ex2(mx - ref);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum += ex2(z[i] - ref);
+            mx = now;
+        }
+        const int64_t group = (o.n0 + g) / kGroup;
+        if (o.n0 + g < p.V && CHK(group * p.Mp + row, 1, p.vocab_groups * p.Mp))
+            p.pairs[group * p.Mp + row] = make_float2(mx, sum);
+    }
+}
+
+template <bool GRAD, bool F16>
+__device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w, const Ctx &c, int warp, int lane) {
+    const int quarter = warp % 4;
+    Store<F16> store{c.sbase + kStagingOffset + (uint32_t)(warp - 2) * 4096u, lane};
+    const float gscale = GRAD ? p.head->gscale : 0.0f;
+    constexpr float kOne = (float)(1ull << (F16 ? kScaleBits16 : kScaleBitsBf));
+    int acc = 0;
+    uint32_t aph = 0;
+    Unit o;
+    for (int64_t u = blockIdx.x; !c.aborted() && w.at(u, &o); u += gridDim.x) {
+        const int row = o.m0 + quarter * 32 + lane;
+        float lse2 = 0.0f, rfac = 0.0f;
+        int tgt = -1;
+        if (GRAD && o.type == UNIT_L) {
+            lse2 = p.lse2[row];
+            rfac = p.rfac[row];
+            tgt = p.tgt[row] - o.piece * p.piece_cols - o.n0;     // column of this tile
+        }
+        for (int part = 0; part < o.parts; ++part) {
+            if (!c.wait(c.tfull(acc), aph)) return;
+            tc_fence_after();
+            const uint32_t tmem = c.tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kBN);
+            if (!GRAD) {
+                loss_rows(p, o, tmem, row);
+            } else if (o.type == UNIT_L) {
+                const int n = (int)(p.V - (int64_t)o.piece * p.piece_cols) - o.n0;   // valid columns of this tile
+                const int gcol = (o.piece % p.buffers) * p.piece_cols + o.n0;
+#pragma unroll 1
+                for (int cc = 0; cc < o.width; cc += 32) {
+                    uint32_t r[32];
+                    float f[32];
+                    tmem_ld32(tmem + (uint32_t)cc, r);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float e = ex2(fmaf(__uint_as_float(r[i]), kLog2e, -lse2));   // 2^k P
+                        f[i] = (cc + i == tgt ? e - kOne : e) * rfac;
+                        // no position, or no such entry: exactly zero, whatever z is
+                        if (rfac == 0.0f || cc + i >= n) f[i] = 0.0f;
+                    }
+                    store.put(&maps.g_out, f, gcol + cc, o.m0 + quarter * 32);
+                }
+            } else if (o.type == UNIT_T) {
+#pragma unroll 1
+                for (int cc = 0; cc < o.width && o.n0 + cc < p.D; cc += 32) {
+                    uint32_t r[32];
+                    float f[32];
+                    tmem_ld32(tmem + (uint32_t)cc, r);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]) * gscale;
+                    store.put(&maps.dt_out, f, o.n0 + cc, o.piece * p.piece_cols + o.m0 + quarter * 32);
+                }
+            } else {
+                // granule sums of dx: a slot each, or added in place in granule order
+                const int granule = o.piece * (p.piece_cols / kGranule) + o.granule + part;
+                const bool add = p.slots == 1 && granule > 0;
+                if (add && part == 0) {                  // the previous piece's sums
+                    const int q = o.piece - 1;
+                    const bool there = lane != 0 || c.wait_count(p.done_tx + q, kEpiWarps * (unsigned)(w.n_t(q) + w.n_x(q)));
+                    if (!__all_sync(0xffffffffu, there)) return;
+                }
+                float *dst = p.acc + ((p.slots > 1 ? (int64_t)granule * p.Mp : 0) + row) * p.D + o.n0;
+#pragma unroll 1
+                for (int cc = 0; cc < o.width && o.n0 + cc < p.D; cc += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(tmem + (uint32_t)cc, r);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        if (o.n0 + cc + i >= p.D ||
+                            !CHK(dst + cc + i - p.acc, 4, (int64_t)p.slots * p.Mp * p.D)) break;   // D is a multiple of 8
+                        float4 v = make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
+                                               __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+                        float4 *q = reinterpret_cast<float4 *>(dst + cc + i);
+                        if (add) {
+                            const float4 b = __ldcg(q);
+                            v.x = b.x + v.x; v.y = b.y + v.y; v.z = b.z + v.z; v.w = b.w + v.w;
+                        }
+                        __stcg(q, v);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.tempty(acc));
+            if (++acc == 2) { acc = 0; aph ^= 1u; }
+        }
+        if (GRAD) {                                       // this unit's output is in memory
+            if (lane == 0) {
+                bulk_wait_all();
+                fence_proxy_async_all();
+            }
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) add_release((o.type == UNIT_L ? p.done_l : p.done_tx) + o.piece, 1u);
+        }
+    }
+    if (lane == 0) bulk_wait_all();
+}
+
+template <bool GRAD, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint32_t *slot = reinterpret_cast<uint32_t *>(smem + kBarOffset + (2 * kStages + 4) * 8);
+    Ctx c;
+    c.sbase = smem_addr(smem);
+    c.bars = c.sbase + kBarOffset;
+    c.abort_flag = slot + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(c.full(s), 1);
+            mbar_init(c.empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(c.tfull(b), 1);
+            mbar_init(c.tempty(b), kEpiWarps);
+        }
+        *c.abort_flag = 0u;
+        fence_mbar_init();
+        prefetch_map(&maps.x);
+        prefetch_map(&maps.w);
+    }
+    if (warp == 1) tmem_alloc(smem_addr(slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    c.tmem = *slot;
+    wait_prior_grid();
+    allow_next_grid();
+    const Walk w(p, row_tiles(p.head->kept));
+
+    if (warp == 0) {
+        if (lane == 0) produce(p, maps, w, c);
+    } else if (warp == 1) {
+        if (lane == 0) issue<F16>(w, c);
+    } else {
+        epilogue<GRAD, F16>(p, maps, w, c, warp, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(c.tmem, 512);
+    }
+}
+
+// ---- joining ---------------------------------------------------------------------------
+
+// lse and loss of 32 rows: 32 threads per row take every 32nd pair, in order,
+// and their pairs are joined in thread order.
+__global__ void __launch_bounds__(1024)
+xent_join_kernel(const Plan p, float *__restrict__ losses, float *__restrict__ lse) {
+    __shared__ float2 part[32][33];
+    wait_prior_grid();
+    allow_next_grid();
+    const int r = threadIdx.x % 32, t = threadIdx.x / 32;
+    const int64_t row = (int64_t)blockIdx.x * 32 + r;
+    const int kept = p.head->kept;
+    if ((int64_t)blockIdx.x * 32 >= kept) return;         // CTA-uniform
+    float mx = -INFINITY, sum = 0.0f;
+    auto join = [&](float2 q) {
+        const float now = fmaxf(mx, q.x), ref = now == -INFINITY ? 0.0f : now;
+        sum = sum * ex2(mx - ref) + q.y * ex2(q.x - ref);
+        mx = now;
+    };
+#pragma unroll 4
+    for (int g = t; g < p.vocab_groups; g += 32)
+        if (CHK((int64_t)g * p.Mp + row, 1, p.vocab_groups * p.Mp)) join(p.pairs[(int64_t)g * p.Mp + row]);
+    part[t][r] = make_float2(mx, sum);
+    __syncthreads();
+    if (t != 0 || row >= kept) return;
+    for (int i = 1; i < 32; ++i) join(part[i][r]);
+    const float l = (mx + log2f(sum)) * kLn2;
+    const int64_t m = p.rowmap[row];
+    lse[m] = l;
+    losses[m] = l - p.zt[row];
+}
+
+// Sum (and mean) of the losses: one CTA, every thread its positions in order,
+// the threads' sums in a fixed tree, in float64.
+__global__ void __launch_bounds__(1024)
+xent_total_kernel(const Plan p, const float *__restrict__ losses, float *__restrict__ total, int mean) {
+    __shared__ double part[1024];
+    wait_prior_grid();
+    allow_next_grid();
+    double s = 0.0;
+    for (int64_t m = threadIdx.x; m < p.M; m += 1024) s += (double)losses[m];
+    part[threadIdx.x] = s;
+    __syncthreads();
+    for (int o = 512; o > 0; o >>= 1) {
+        if (threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        const int kept = p.head->kept;
+        total[0] = (float)(mean ? part[0] / (double)(kept > 0 ? kept : 1) : part[0]);
+    }
+}
+
+// dx rows: the granule sums in order, scaled and rounded; zeros for ignored
+// positions.  A warp per row.
+template <typename T>
+__global__ void __launch_bounds__(256)
+xent_dx_kernel(const Plan p, T *__restrict__ dx) {
+    wait_prior_grid();
+    allow_next_grid();
+    const int lane = threadIdx.x % 32;
+    const int64_t m = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    if (m >= p.M) return;
+    const int64_t i = p.inverse[m];
+    const float gscale = p.head->gscale;
+    for (int64_t j = lane * 8; j < p.D; j += 256) {
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = 0.0f;
+        if (i >= 0) {
+            for (int s = 0; s < p.slots; ++s) {
+                const float4 *src = reinterpret_cast<const float4 *>(p.acc + ((int64_t)s * p.Mp + i) * p.D + j);
+                const float4 a = src[0], b = src[1];
+                const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] = s == 0 ? v[k] : f[k] + v[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] *= gscale;
+        }
+        if (CHK(m * p.D + j, 8, p.M * p.D)) store_f32<T, 8>(dx + m * p.D + j, f);
+    }
+}
+
+// ---- host side ----------------------------------------------------------------
+
+cudaError_t encode(CUtensorMap *m, const void *base, int64_t inner, int64_t outer, int box, CUtensorMapSwizzle sw) {
+    return encode_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, (uint64_t)inner, (uint64_t)outer,
+                                (uint64_t)inner * 2, (uint32_t)box, (uint32_t)box, sw);
+}
+
+bool sizes_ok(int64_t M, int64_t D, int64_t V) {
+    int64_t t;
+    // tile coordinates and counters are 32-bit; element counts are 64-bit
+    return M >= 0 && D >= 0 && V >= 0 && M < (1ll << 30) && D < (1ll << 24) && V < (1ll << 30) &&
+           !__builtin_mul_overflow(M, D, &t) && !__builtin_mul_overflow(t, (int64_t)16, &t) &&
+           !__builtin_mul_overflow(V, D, &t) && !__builtin_mul_overflow(t, (int64_t)16, &t);
+}
+
+carbon_status_t check(const void *x, const void *table, const int64_t *targets, int64_t M, int64_t D, int64_t V,
+                      int reduction, int dtype) {
+    if (!sizes_ok(M, D, V)) return CARBON_ERR_INVALID_ARG;
+    if (dtype != CARBON_F32 && dtype != CARBON_BF16 && dtype != CARBON_F16) return CARBON_ERR_INVALID_ARG;
+    if (reduction < CARBON_REDUCE_NONE || reduction > CARBON_REDUCE_MEAN) return CARBON_ERR_INVALID_ARG;
+    if (dtype == CARBON_F32) return CARBON_ERR_UNSUPPORTED;
+    if (M > 0 && (D == 0 || V == 0)) return CARBON_ERR_INVALID_ARG;
+    if (M > 0 && (!x || !table || !targets)) return CARBON_ERR_INVALID_ARG;
+    if (D % 8 != 0 || !aligned16(x) || !aligned16(table)) return CARBON_ERR_MISALIGNED;
+    return CARBON_OK;
+}
+
+template <bool GRAD>
+cudaError_t launch_tiles(const Plan &p, const void *table, void *dtable, int sms, cudaStream_t s) {
+    Maps maps;
+    cudaError_t err = encode(&maps.x, p.xc, p.D, p.Mp, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (err == cudaSuccess) err = encode(&maps.w, table, p.D, p.V, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (GRAD) {
+        const int64_t cols = (int64_t)p.piece_cols * p.buffers;
+        if (err == cudaSuccess) err = encode(&maps.g, p.g, cols, p.Mp, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (err == cudaSuccess) err = encode(&maps.g_out, p.g, cols, p.Mp, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+        if (err == cudaSuccess) err = encode(&maps.dt_out, dtable, p.D, p.V, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    } else {
+        maps.g = maps.g_out = maps.dt_out = maps.x;       // unused
+    }
+    if (err != cudaSuccess) return err;
+    auto kern = p.f16 ? xent_tile_kernel<GRAD, true> : xent_tile_kernel<GRAD, false>;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (err != cudaSuccess) return err;
+    count_launch();
+    return launch_k(kern, dim3((unsigned)sms), dim3(kThreads), (size_t)kSmemBytes, s, 1, maps, p);
+}
+
+cudaError_t launch_gather(const Plan &p, const ScanArgs &a, const void *x, cudaStream_t s) {
+    count_launch(2);
+    const cudaError_t err = launch_k(xent_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, 1, p, a);
+    if (err != cudaSuccess) return err;
+    return launch_k(xent_gather_kernel, dim3((unsigned)(p.Mp / 8)), dim3(256), 0, s, 1, p,
+                    static_cast<const uint4 *>(x));
+}
+
+}  // namespace
+
+carbon_status_t xent_take_device_status() {
+    unsigned int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_xent_status, sizeof v) != cudaSuccess) return CARBON_OK;
+    if (v != 0) cudaMemcpyToSymbol(g_xent_status, &zero, sizeof zero);
+    return (carbon_status_t)v;
+}
+
+}  // namespace carbon
+
+using namespace carbon;
+
+extern "C" {
+
+int64_t carbon_linear_xent_fwd_workspace(int64_t M, int64_t D, int64_t V) {
+    return sizes_ok(M, D, V) ? make_plan(nullptr, nullptr, M, D > 0 ? D : 1, V, false, false) : -1;
+}
+
+int64_t carbon_linear_xent_bwd_workspace(int64_t M, int64_t D, int64_t V) {
+    return sizes_ok(M, D, V) ? make_plan(nullptr, nullptr, M, D > 0 ? D : 1, V > 0 ? V : 1, true, false) : -1;
+}
+
+carbon_status_t carbon_linear_xent_fwd(float *losses, float *total, float *lse, int64_t *count, const void *x,
+                                       const void *table, const int64_t *targets, int64_t M, int64_t D, int64_t V,
+                                       int64_t ignore_index, carbon_reduce_t reduction, void *workspace,
+                                       int64_t workspace_bytes, carbon_dtype_t dtype, carbon_stream_t stream) {
+    carbon_status_t st = check(x, table, targets, M, D, V, reduction, dtype);
+    if (st != CARBON_OK) return st;
+    if (reduction != CARBON_REDUCE_NONE && !total) return CARBON_ERR_INVALID_ARG;
+    if (M > 0 && (!losses || !lse || !workspace || !aligned16(workspace) ||
+                  workspace_bytes < carbon_linear_xent_fwd_workspace(M, D, V)))
+        return CARBON_ERR_INVALID_ARG;
+    if ((st = injected_launch_failure()) != CARBON_OK) return st;
+    int sms = 0;
+    if ((st = current_device(nullptr, &sms)) != CARBON_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        cudaError_t err = cudaSuccess;
+        if (total) err = cudaMemsetAsync(total, 0, sizeof(float), s);
+        if (err == cudaSuccess && count) err = cudaMemsetAsync(count, 0, sizeof(int64_t), s);
+        return note_cuda(err);
+    }
+    Plan p;
+    make_plan(&p, align128(workspace), M, D, V, false, dtype == CARBON_F16);
+    ScanArgs a = {};
+    a.targets = targets; a.ignore_index = ignore_index; a.reduction = reduction;
+    a.losses = losses; a.lse_out = lse; a.count = count;
+    cudaError_t err = launch_gather(p, a, x, s);
+    if (err == cudaSuccess) err = launch_tiles<false>(p, table, nullptr, sms, s);
+    if (err == cudaSuccess) {
+        count_launch();
+        err = launch_k(xent_join_kernel, dim3((unsigned)((M + 31) / 32)), dim3(1024), 0, s, 1, p, losses, lse);
+    }
+    if (err == cudaSuccess && reduction != CARBON_REDUCE_NONE) {
+        count_launch();
+        err = launch_k(xent_total_kernel, dim3(1), dim3(1024), 0, s, 1, p, (const float *)losses, total,
+                       reduction == CARBON_REDUCE_MEAN ? 1 : 0);
+    }
+    return note_cuda(err);
+}
+
+carbon_status_t carbon_linear_xent_bwd(void *dx, void *dtable, const float *grad, const void *x, const void *table,
+                                       const int64_t *targets, const float *lse, int64_t M, int64_t D, int64_t V,
+                                       int64_t ignore_index, carbon_reduce_t reduction, void *workspace,
+                                       int64_t workspace_bytes, carbon_dtype_t dtype, carbon_stream_t stream) {
+    carbon_status_t st = check(x, table, targets, M, D, V, reduction, dtype);
+    if (st != CARBON_OK) return st;
+    if (!aligned16(dx) || !aligned16(dtable)) return CARBON_ERR_MISALIGNED;
+    if (V * D > 0 && !dtable) return CARBON_ERR_INVALID_ARG;
+    if (M > 0 && (!dx || !grad || !lse || !workspace || !aligned16(workspace) ||
+                  workspace_bytes < carbon_linear_xent_bwd_workspace(M, D, V)))
+        return CARBON_ERR_INVALID_ARG;
+    if (V * D == 0) return CARBON_OK;                     // then M == 0
+    if ((st = injected_launch_failure()) != CARBON_OK) return st;
+    int sms = 0;
+    if ((st = current_device(nullptr, &sms)) != CARBON_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0) return note_cuda(cudaMemsetAsync(dtable, 0, (size_t)(V * D) * 2, s));
+    Plan p;
+    make_plan(&p, align128(workspace), M, D, V, true, dtype == CARBON_F16);
+    ScanArgs a = {};
+    a.targets = targets; a.ignore_index = ignore_index; a.reduction = reduction;
+    a.grad = grad; a.lse_in = lse;
+    cudaError_t err = launch_gather(p, a, x, s);
+    if (err == cudaSuccess) err = launch_tiles<true>(p, table, dtable, sms, s);
+    if (err == cudaSuccess) {
+        count_launch();
+        const dim3 grid((unsigned)((M + 7) / 8));
+        err = p.f16 ? launch_k(xent_dx_kernel<__half>, grid, dim3(256), 0, s, 1, p, static_cast<__half *>(dx))
+                    : launch_k(xent_dx_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1, p,
+                               static_cast<__nv_bfloat16 *>(dx));
+    }
+    return note_cuda(err);
+}
+
+}  // extern "C"

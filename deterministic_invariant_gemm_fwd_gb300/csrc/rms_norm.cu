@@ -1,0 +1,649 @@
+// rms_norm.cu - root-mean-square norm of a residual stream, its 8-bit
+// checkpoint, and the gradients.
+//
+//   h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  n = h * rstd,  y = n * gamma
+//   codes = round(n * (127 / max|n|)),  scales = max|n| / 127
+//   dx = rstd * (gamma*dy - n * mean(gamma*dy*n)) + dh,  dgamma = sum_m dy * n
+//
+// Bound: memory.  Each row is read once into registers: a group of threads
+// (a warp, four warps or sixteen, by the row's length) holds a row as up to
+// kHold vectors per thread, reduces across the group and writes.  Longer rows
+// and rows that 16-byte vectors do not fit take the same kernels with single
+// elements, or re-read the row.  The order of a row's sums depends on D, the
+// dtype and the alignment alone.
+//
+// dgamma: a group takes the rows g, g + groups, ... and adds its columns'
+// terms in registers; the groups' sums are added per CTA in group order, then
+// over the CTAs in order by a second kernel.
+#include "bounds.cuh"
+#include "device_sync.cuh"
+#include "rowvec.cuh"
+
+namespace carbon {
+namespace {
+
+__device__ unsigned int g_norm_status = 0;
+#define CHK(idx, len, n) in_bounds(&g_norm_status, (int64_t)(idx), (int64_t)(len), (int64_t)(n))
+
+constexpr int kMaxHold = 32;             // fp32 elements of a row that a thread holds
+constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100
+
+// Sum over the G threads of a group; every thread receives it.  buf: one
+// float per warp of the group.  The value is the warps' butterfly sums added
+// in warp order.
+template <int G>
+__device__ __forceinline__ float group_sum(float v, float *buf) {
+    v = warp_sum(v);
+    if constexpr (G == 32) {
+        return v;
+    } else {
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
+        __syncthreads();
+        const int w0 = threadIdx.x / G * (G / 32);
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < G / 32; ++w) s += buf[w0 + w];
+        return s;
+    }
+}
+
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t *buf) {
+    v = warp_max_u32(v);
+    if constexpr (G == 32) {
+        return v;
+    } else {
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
+        __syncthreads();
+        const int w0 = threadIdx.x / G * (G / 32);
+        uint32_t s = 0u;
+#pragma unroll
+        for (int w = 0; w < G / 32; ++w) s = max(s, buf[w0 + w]);
+        return s;
+    }
+}
+
+// Bits of |v|: ordered like the magnitudes, with NaN above infinity.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// The scale of a row's codes and the factor that makes them, from the bits
+// of the row's largest magnitude.
+__device__ __forceinline__ void code_scale(uint32_t top_bits, float *scale, float *factor) {
+    const float top = __uint_as_float(top_bits);
+    if (top_bits >= 0x7f800000u) {                        // infinity or NaN
+        *scale = __uint_as_float(0x7fc00000u);
+        *factor = 0.0f;
+    } else if (top < kTiny) {
+        *scale = 0.0f;
+        *factor = 0.0f;
+    } else {
+        *scale = __fdiv_rn(top, 127.0f);
+        *factor = __fdiv_rn(127.0f, top);
+    }
+}
+
+__device__ __forceinline__ int8_t code_of(float n, float factor) {
+    // a zero factor gives code 0 also for infinities and NaN
+    return factor == 0.0f ? (int8_t)0 : (int8_t)max(-127, min(127, __float2int_rn(n * factor)));
+}
+
+template <int N>
+__device__ __forceinline__ void store_codes(int8_t *p, const int8_t (&c)[N]) {
+    Pack<int8_t, N> v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v.e[i] = c[i];
+    *reinterpret_cast<Pack<int8_t, N> *>(p) = v;
+}
+
+template <typename T>
+struct FwdArgs {
+    T *y, *h_out;
+    float *rstd;
+    int8_t *codes;
+    float *scales;
+    const T *x, *residual, *gamma;
+    int64_t M, D;
+    float eps;
+};
+
+// G threads per row, N elements per vector, H vectors per thread.
+template <typename T, int G, int N, int H>
+__global__ void __launch_bounds__(G > 128 ? G : 128)
+norm_fwd_kernel(const FwdArgs<T> a) {
+    constexpr int kThreads = G > 128 ? G : 128, kRows = kThreads / G;
+    __shared__ float buf[kThreads / 32];
+    wait_prior_grid();
+    allow_next_grid();
+    const int64_t m0 = (int64_t)blockIdx.x * kRows + threadIdx.x / G;
+    const bool live = m0 < a.M;
+    const int64_t m = live ? m0 : a.M - 1;                // idle groups repeat the last row, unstored
+    const int t = threadIdx.x % G;
+    const int nvec = (int)(a.D / N);
+    const int64_t row = m * a.D;
+
+    float h[H][N];
+    float ss = 0.0f;
+#pragma unroll
+    for (int u = 0; u < H; ++u) {
+        const int i = t + G * u;
+        if (i < nvec && CHK(row + i * N, N, a.M * a.D)) {
+            load_f32<T, N>(a.x + row + i * N, h[u]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) h[u][k] = 0.0f;
+        }
+    }
+    if (a.residual) {
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+            const int i = t + G * u;
+            if (i < nvec) {
+                float r[N];
+                load_f32<T, N>(a.residual + row + i * N, r);
+#pragma unroll
+                for (int k = 0; k < N; ++k) h[u][k] += r[k];
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < H; ++u)
+#pragma unroll
+        for (int k = 0; k < N; ++k) ss = fmaf(h[u][k], h[u][k], ss);
+    ss = group_sum<G>(ss, buf);
+    const float rstd = rsqrtf(__fdiv_rn(ss, (float)a.D) + a.eps);
+
+    if (live) {
+        if (a.rstd && t == 0) a.rstd[m] = rstd;
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+            const int i = t + G * u;
+            if (i < nvec) {
+                if (a.h_out) store_f32<T, N>(a.h_out + row + i * N, h[u]);
+                float g[N], y[N];
+                load_f32<T, N>(a.gamma + i * N, g);
+#pragma unroll
+                for (int k = 0; k < N; ++k) y[k] = h[u][k] * rstd * g[k];
+                store_f32<T, N>(a.y + row + i * N, y);
+            }
+        }
+    }
+    if (a.codes) {                                        // the same for the whole grid
+        uint32_t top = 0u;
+#pragma unroll
+        for (int u = 0; u < H; ++u)
+#pragma unroll
+            for (int k = 0; k < N; ++k) top = max(top, magnitude(h[u][k] * rstd));
+        top = group_max<G>(top, reinterpret_cast<uint32_t *>(buf));
+        float scale, factor;
+        code_scale(top, &scale, &factor);
+        if (live) {
+            if (t == 0) a.scales[m] = scale;
+#pragma unroll
+            for (int u = 0; u < H; ++u) {
+                const int i = t + G * u;
+                if (i < nvec) {
+                    int8_t c[N];
+#pragma unroll
+                    for (int k = 0; k < N; ++k) c[k] = code_of(h[u][k] * rstd, factor);
+                    store_codes<N>(a.codes + row + i * N, c);
+                }
+            }
+        }
+    }
+}
+
+// Rows that do not fit a group's registers: a CTA per row, the row read again
+// for each pass.
+template <typename T>
+__global__ void __launch_bounds__(512)
+norm_fwd_long_kernel(const FwdArgs<T> a) {
+    __shared__ float buf[16];
+    wait_prior_grid();
+    allow_next_grid();
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        const int64_t row = m * a.D;
+        auto h_at = [&](int64_t j) {
+            return to_f32(a.x[row + j]) + (a.residual ? to_f32(a.residual[row + j]) : 0.0f);
+        };
+        float ss = 0.0f;
+        for (int64_t j = threadIdx.x; j < a.D; j += 512) {
+            const float h = h_at(j);
+            ss = fmaf(h, h, ss);
+        }
+        ss = group_sum<512>(ss, buf);
+        const float rstd = rsqrtf(__fdiv_rn(ss, (float)a.D) + a.eps);
+        if (a.rstd && threadIdx.x == 0) a.rstd[m] = rstd;
+        uint32_t top = 0u;
+        for (int64_t j = threadIdx.x; j < a.D; j += 512) {
+            const float h = h_at(j);
+            if (a.h_out) a.h_out[row + j] = from_f32<T>(h);
+            a.y[row + j] = from_f32<T>(h * rstd * to_f32(a.gamma[j]));
+            top = max(top, magnitude(h * rstd));
+        }
+        if (!a.codes) continue;
+        top = group_max<512>(top, reinterpret_cast<uint32_t *>(buf));
+        float scale, factor;
+        code_scale(top, &scale, &factor);
+        if (threadIdx.x == 0) a.scales[m] = scale;
+        for (int64_t j = threadIdx.x; j < a.D; j += 512) a.codes[row + j] = code_of(h_at(j) * rstd, factor);
+    }
+}
+
+template <typename T>
+struct BwdArgs {
+    T *dx, *y_out;
+    float *partial;                       // [CTAs][D], or null (no dgamma)
+    const T *dy, *h;
+    const int8_t *codes;
+    const float *scales, *rstd;
+    const T *gamma, *dh;
+    int64_t M, D;
+};
+
+template <int N>
+__device__ __forceinline__ void load_codes(const int8_t *p, float (&f)[N]) {
+    const Pack<int8_t, N> v = *reinterpret_cast<const Pack<int8_t, N> *>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = (float)v.e[i];
+}
+
+template <typename T, int G, int N, int H, bool CODES>
+__global__ void __launch_bounds__(G > 256 ? G : 256)
+norm_bwd_kernel(const BwdArgs<T> a) {
+    constexpr int kThreads = G > 256 ? G : 256, kRows = kThreads / G;
+    __shared__ float buf[kThreads / 32];
+    extern __shared__ float group_part[];                 // [kRows][D] for dgamma, kRows > 1
+    wait_prior_grid();
+    allow_next_grid();
+    const int t = threadIdx.x % G, group = threadIdx.x / G;
+    const int nvec = (int)(a.D / N);
+    const int64_t stride = (int64_t)gridDim.x * kRows;
+    float dg[H][N];
+#pragma unroll
+    for (int u = 0; u < H; ++u)
+#pragma unroll
+        for (int k = 0; k < N; ++k) dg[u][k] = 0.0f;
+
+    // every group of a CTA makes the same number of rounds (group_sum has CTA barriers)
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.M; r0 += stride) {
+        const int64_t m = r0 + group;
+        const bool live = m < a.M;
+        const int64_t row = (live ? m : 0) * a.D;
+        const float rstd = live ? a.rstd[m] : 0.0f;
+        const float factor = !live ? 0.0f : (CODES ? a.scales[m] : rstd);
+        float n[H][N], gdy[H][N];
+        float dot = 0.0f;
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+            const int i = t + G * u;
+            if (i < nvec && live && CHK(row + i * N, N, a.M * a.D)) {
+                if (CODES) load_codes<N>(a.codes + row + i * N, n[u]);
+                else load_f32<T, N>(a.h + row + i * N, n[u]);
+                load_f32<T, N>(a.dy + row + i * N, gdy[u]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < N; ++k) n[u][k] = gdy[u][k] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+            const int i = t + G * u;
+            if (i < nvec && live) {
+                float g[N];
+                load_f32<T, N>(a.gamma + i * N, g);
+                if (a.y_out) {
+                    float y[N];
+#pragma unroll
+                    for (int k = 0; k < N; ++k) y[k] = n[u][k] * factor * g[k];
+                    store_f32<T, N>(a.y_out + row + i * N, y);
+                }
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    n[u][k] *= factor;
+                    dg[u][k] = fmaf(gdy[u][k], n[u][k], dg[u][k]);
+                    gdy[u][k] *= g[k];
+                    dot = fmaf(gdy[u][k], n[u][k], dot);
+                }
+            }
+        }
+        dot = group_sum<G>(dot, buf);
+        const float mean = __fdiv_rn(dot, (float)a.D);
+        if (live) {
+#pragma unroll
+            for (int u = 0; u < H; ++u) {
+                const int i = t + G * u;
+                if (i < nvec) {
+                    float d[N];
+                    if (a.dh) {
+                        load_f32<T, N>(a.dh + row + i * N, d);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < N; ++k) d[k] = 0.0f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < N; ++k) d[k] = fmaf(rstd, fmaf(-n[u][k], mean, gdy[u][k]), d[k]);
+                    store_f32<T, N>(a.dx + row + i * N, d);
+                }
+            }
+        }
+    }
+    if (!a.partial) return;
+    float *out = a.partial + (int64_t)blockIdx.x * a.D;
+    if constexpr (kRows == 1) {
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+            const int i = t + G * u;
+            if (i < nvec)
+#pragma unroll
+                for (int k = 0; k < N; ++k) out[i * N + k] = dg[u][k];
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+            const int i = t + G * u;
+            if (i < nvec)
+#pragma unroll
+                for (int k = 0; k < N; ++k) group_part[group * (int)a.D + i * N + k] = dg[u][k];
+        }
+        __syncthreads();
+        for (int j = threadIdx.x; j < (int)a.D; j += kThreads) {
+            float s = 0.0f;
+#pragma unroll
+            for (int g = 0; g < kRows; ++g) s += group_part[g * (int)a.D + j];
+            out[j] = s;
+        }
+    }
+}
+
+// Long rows: a CTA per row; dgamma's terms are added into the CTA's own
+// partial row, which only its threads touch.
+template <typename T>
+__global__ void __launch_bounds__(512)
+norm_bwd_long_kernel(const BwdArgs<T> a) {
+    __shared__ float buf[16];
+    wait_prior_grid();
+    allow_next_grid();
+    float *out = a.partial ? a.partial + (int64_t)blockIdx.x * a.D : nullptr;
+    bool first = true;
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        const int64_t row = m * a.D;
+        const float rstd = a.rstd[m], factor = a.h ? rstd : a.scales[m];
+        auto n_at = [&](int64_t j) {
+            return (a.h ? to_f32(a.h[row + j]) : (float)a.codes[row + j]) * factor;
+        };
+        float dot = 0.0f;
+        for (int64_t j = threadIdx.x; j < a.D; j += 512) {
+            const float n = n_at(j), dy = to_f32(a.dy[row + j]), g = to_f32(a.gamma[j]);
+            if (a.y_out) a.y_out[row + j] = from_f32<T>(n * g);
+            if (out) out[j] = first ? dy * n : fmaf(dy, n, out[j]);
+            dot = fmaf(dy * g, n, dot);
+        }
+        first = false;
+        dot = group_sum<512>(dot, buf);
+        const float mean = __fdiv_rn(dot, (float)a.D);
+        for (int64_t j = threadIdx.x; j < a.D; j += 512) {
+            const float gdy = to_f32(a.dy[row + j]) * to_f32(a.gamma[j]);
+            const float d = a.dh ? to_f32(a.dh[row + j]) : 0.0f;
+            a.dx[row + j] = from_f32<T>(fmaf(rstd, fmaf(-n_at(j), mean, gdy), d));
+        }
+    }
+}
+
+// dgamma[j] = sum over the CTAs' partial rows, in order: 8 threads per column
+// take every 8th row, their sums are added in thread order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+dgamma_kernel(T *__restrict__ dgamma, const float *__restrict__ partial, int rows, int64_t D) {
+    __shared__ float part[8][33];
+    wait_prior_grid();
+    allow_next_grid();
+    const int c = threadIdx.x % 32, r = threadIdx.x / 32;
+    const int64_t j = (int64_t)blockIdx.x * 32 + c;
+    float s = 0.0f;
+    if (j < D) {
+#pragma unroll 8
+        for (int i = r; i < rows; i += 8)
+            if (CHK((int64_t)i * D + j, 1, rows * D)) s += partial[(int64_t)i * D + j];
+    }
+    part[r][c] = s;
+    __syncthreads();
+    if (r == 0 && j < D) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += part[i][c];
+        dgamma[j] = from_f32<T>(s);
+    }
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(256)
+norm_expand_kernel(T *__restrict__ out, const int8_t *__restrict__ codes, const float *__restrict__ scales,
+                   const T *__restrict__ gamma, int64_t M, int64_t D) {
+    wait_prior_grid();
+    allow_next_grid();
+    const int64_t nvec = D / N, total = M * nvec;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t m = i / nvec, v = i - m * nvec;
+        if (!CHK(i * N, N, M * D)) continue;
+        const float s = scales[m];
+        float f[N];
+        load_codes<N>(codes + i * N, f);
+#pragma unroll
+        for (int k = 0; k < N; ++k) f[k] *= s;
+        if (gamma) {
+            float g[N];
+            load_f32<T, N>(gamma + v * N, g);
+#pragma unroll
+            for (int k = 0; k < N; ++k) f[k] *= g[k];
+        }
+        store_f32<T, N>(out + i * N, f);
+    }
+}
+
+// ---- host side ----------------------------------------------------------------
+
+bool sizes_ok(int64_t M, int64_t D) {
+    int64_t t;
+    return M >= 0 && D >= 0 && D < 0x7fffffff && M < 0x7fffffff && !__builtin_mul_overflow(M, D, &t) &&
+           !__builtin_mul_overflow(t, (int64_t)8, &t);
+}
+
+bool dtype_ok(int dtype) { return dtype == CARBON_F32 || dtype == CARBON_BF16 || dtype == CARBON_F16; }
+
+// Calls f.template operator()<G, N, H>() for the group that holds a row of D
+// elements: vectors of N, at most kMaxHold elements per thread.  Returns
+// false where none does.
+template <int N, typename F>
+bool with_group(int64_t D, F &&f) {
+    const int64_t nvec = D / N;
+    constexpr int H = kMaxHold / N;
+    if (nvec <= 32) { f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>()); return true; }
+    if (nvec <= 32 * H) { f(std::integral_constant<int, 32>(), std::integral_constant<int, H>()); return true; }
+    if (nvec <= 128 * H) { f(std::integral_constant<int, 128>(), std::integral_constant<int, H>()); return true; }
+    if (nvec <= 512 * H) { f(std::integral_constant<int, 512>(), std::integral_constant<int, H>()); return true; }
+    return false;
+}
+
+template <typename T, int N>
+cudaError_t launch_fwd(const FwdArgs<T> &a, cudaStream_t s) {
+    cudaError_t err = cudaSuccess;
+    count_launch();
+    const bool held = with_group<N>(a.D, [&](auto g, auto h) {
+        constexpr int G = g(), H = h(), kRows = G > 128 ? 1 : 128 / G;
+        err = launch_k(norm_fwd_kernel<T, G, N, H>, dim3((unsigned)((a.M + kRows - 1) / kRows)),
+                       dim3(G > 128 ? G : 128), 0, s, 1, a);
+    });
+    if (!held)
+        err = launch_k(norm_fwd_long_kernel<T>, dim3((unsigned)(a.M < 65535 ? a.M : 65535)), dim3(512), 0, s, 1, a);
+    return err;
+}
+
+template <typename T>
+cudaError_t run_fwd(const FwdArgs<T> &a, cudaStream_t s) {
+    constexpr int N = kVec<T>;
+    const bool vec = a.D % N == 0 && aligned16(a.x) && aligned16(a.y) && aligned16(a.gamma) &&
+                     aligned16(a.residual) && aligned16(a.h_out) &&
+                     reinterpret_cast<uintptr_t>(a.codes) % N == 0;
+    return vec ? launch_fwd<T, N>(a, s) : launch_fwd<T, 1>(a, s);
+}
+
+// CTAs of the gradient kernels: enough to fill 152 SMs several times over,
+// and no more partial rows than that.
+constexpr int kBwdCtas = 152 * 4;
+
+template <typename T, int N, bool CODES>
+cudaError_t launch_bwd(const BwdArgs<T> &a, T *dgamma, cudaStream_t s) {
+    cudaError_t err = cudaSuccess;
+    int ctas = 0;
+    count_launch();
+    const bool held = with_group<N>(a.D, [&](auto g, auto h) {
+        constexpr int G = g(), H = h(), kThreads = G > 256 ? G : 256, kRows = kThreads / G;
+        const int64_t want = (a.M + kRows - 1) / kRows;
+        ctas = (int)(want < kBwdCtas ? want : kBwdCtas);
+        const size_t smem = kRows > 1 && a.partial ? (size_t)kRows * a.D * sizeof(float) : 0;
+        auto kern = norm_bwd_kernel<T, G, N, H, CODES>;
+        if (smem > 48 * 1024)
+            err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (err == cudaSuccess) err = launch_k(kern, dim3((unsigned)ctas), dim3(kThreads), smem, s, 1, a);
+    });
+    if (!held) {
+        ctas = (int)(a.M < kBwdCtas ? a.M : kBwdCtas);
+        err = launch_k(norm_bwd_long_kernel<T>, dim3((unsigned)ctas), dim3(512), 0, s, 1, a);
+    }
+    if (err != cudaSuccess || !a.partial) return err;
+    count_launch();
+    return launch_k(dgamma_kernel<T>, dim3((unsigned)((a.D + 31) / 32)), dim3(256), 0, s, 1, dgamma,
+                    (const float *)a.partial, ctas, a.D);
+}
+
+template <typename T>
+cudaError_t run_bwd(const BwdArgs<T> &a, void *dgamma, cudaStream_t s) {
+    constexpr int N = kVec<T>;
+    const bool vec = a.D % N == 0 && aligned16(a.dx) && aligned16(a.dy) && aligned16(a.gamma) && aligned16(a.h) &&
+                     aligned16(a.dh) && aligned16(a.y_out) && reinterpret_cast<uintptr_t>(a.codes) % N == 0;
+    T *dg = static_cast<T *>(dgamma);
+    if (a.h) return vec ? launch_bwd<T, N, false>(a, dg, s) : launch_bwd<T, 1, false>(a, dg, s);
+    return vec ? launch_bwd<T, N, true>(a, dg, s) : launch_bwd<T, 1, true>(a, dg, s);
+}
+
+template <typename T>
+cudaError_t run_expand(void *out, const int8_t *codes, const float *scales, const void *gamma, int64_t M,
+                       int64_t D, cudaStream_t s) {
+    constexpr int N = kVec<T>;
+    const bool vec = D % N == 0 && aligned16(out) && aligned16(gamma) && reinterpret_cast<uintptr_t>(codes) % N == 0;
+    const int64_t total = vec ? M * (D / N) : M * D, want = (total + 255) / 256;
+    const dim3 grid((unsigned)(want < 152 * 16 ? want : 152 * 16));
+    count_launch();
+    if (vec)
+        return launch_k(norm_expand_kernel<T, N>, grid, dim3(256), 0, s, 1, static_cast<T *>(out), codes, scales,
+                        static_cast<const T *>(gamma), M, D);
+    return launch_k(norm_expand_kernel<T, 1>, grid, dim3(256), 0, s, 1, static_cast<T *>(out), codes, scales,
+                    static_cast<const T *>(gamma), M, D);
+}
+
+}  // namespace
+
+carbon_status_t norm_take_device_status() {
+    unsigned int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_norm_status, sizeof v) != cudaSuccess) return CARBON_OK;
+    if (v != 0) cudaMemcpyToSymbol(g_norm_status, &zero, sizeof zero);
+    return (carbon_status_t)v;
+}
+
+namespace {
+
+carbon_status_t ready() {
+    const carbon_status_t st = injected_launch_failure();
+    return st != CARBON_OK ? st : current_device(nullptr, nullptr);
+}
+
+template <typename T>
+cudaError_t fwd_as(void *y, void *h_out, float *rstd, int8_t *codes, float *scales, const void *x,
+                   const void *residual, const void *gamma, int64_t M, int64_t D, float eps, cudaStream_t s) {
+    const FwdArgs<T> a{static_cast<T *>(y), static_cast<T *>(h_out), rstd, codes, scales,
+                       static_cast<const T *>(x), static_cast<const T *>(residual),
+                       static_cast<const T *>(gamma), M, D, eps};
+    return run_fwd(a, s);
+}
+
+template <typename T>
+cudaError_t bwd_as(void *dx, void *dgamma, void *y_out, const void *dy, const void *h, const int8_t *codes,
+                   const float *scales, const float *rstd, const void *gamma, const void *dh, int64_t M, int64_t D,
+                   float *partial, cudaStream_t s) {
+    const BwdArgs<T> a{static_cast<T *>(dx), static_cast<T *>(y_out), partial, static_cast<const T *>(dy),
+                       static_cast<const T *>(h), codes, scales, rstd, static_cast<const T *>(gamma),
+                       static_cast<const T *>(dh), M, D};
+    return run_bwd(a, dgamma, s);
+}
+
+}  // namespace
+}  // namespace carbon
+
+using namespace carbon;
+
+extern "C" {
+
+carbon_status_t carbon_rms_norm_fwd(void *y, void *h_out, float *rstd, int8_t *codes, float *scales,
+                                    const void *x, const void *residual, const void *gamma, int64_t M, int64_t D,
+                                    float eps, carbon_dtype_t dtype, carbon_stream_t stream) {
+    if (!sizes_ok(M, D) || !dtype_ok(dtype) || !(eps >= 0.0f)) return CARBON_ERR_INVALID_ARG;
+    if ((codes == nullptr) != (scales == nullptr)) return CARBON_ERR_INVALID_ARG;
+    if (M == 0 || D == 0) return CARBON_OK;
+    if (!y || !x || !gamma) return CARBON_ERR_INVALID_ARG;
+    const carbon_status_t st = ready();
+    if (st != CARBON_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    switch (dtype) {
+    case CARBON_F32: return note_cuda(fwd_as<float>(y, h_out, rstd, codes, scales, x, residual, gamma, M, D, eps, s));
+    case CARBON_BF16: return note_cuda(fwd_as<__nv_bfloat16>(y, h_out, rstd, codes, scales, x, residual, gamma, M, D, eps, s));
+    default: return note_cuda(fwd_as<__half>(y, h_out, rstd, codes, scales, x, residual, gamma, M, D, eps, s));
+    }
+}
+
+int64_t carbon_rms_norm_bwd_workspace(int64_t M, int64_t D) {
+    if (!sizes_ok(M, D)) return -1;
+    return (M < kBwdCtas ? M : kBwdCtas) * D * (int64_t)sizeof(float);
+}
+
+carbon_status_t carbon_rms_norm_bwd(void *dx, void *dgamma, void *y_out, const void *dy, const void *h,
+                                    const int8_t *codes, const float *scales, const float *rstd,
+                                    const void *gamma, const void *dh, int64_t M, int64_t D, void *workspace,
+                                    int64_t workspace_bytes, carbon_dtype_t dtype, carbon_stream_t stream) {
+    if (!sizes_ok(M, D) || !dtype_ok(dtype)) return CARBON_ERR_INVALID_ARG;
+    if (D == 0 || (M == 0 && !dgamma)) return CARBON_OK;
+    if (M > 0) {
+        if (!dx || !dy || !rstd || !gamma) return CARBON_ERR_INVALID_ARG;
+        // exactly one source of n
+        if (h ? (codes || scales) : (!codes || !scales)) return CARBON_ERR_INVALID_ARG;
+        if (dgamma && (!workspace || !aligned16(workspace) || workspace_bytes < carbon_rms_norm_bwd_workspace(M, D)))
+            return CARBON_ERR_INVALID_ARG;
+    }
+    const carbon_status_t st = ready();
+    if (st != CARBON_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0) return note_cuda(cudaMemsetAsync(dgamma, 0, (size_t)D * dtype_size(dtype), s));
+    float *partial = dgamma ? static_cast<float *>(workspace) : nullptr;
+    switch (dtype) {
+    case CARBON_F32: return note_cuda(bwd_as<float>(dx, dgamma, y_out, dy, h, codes, scales, rstd, gamma, dh, M, D, partial, s));
+    case CARBON_BF16: return note_cuda(bwd_as<__nv_bfloat16>(dx, dgamma, y_out, dy, h, codes, scales, rstd, gamma, dh, M, D, partial, s));
+    default: return note_cuda(bwd_as<__half>(dx, dgamma, y_out, dy, h, codes, scales, rstd, gamma, dh, M, D, partial, s));
+    }
+}
+
+carbon_status_t carbon_rms_norm_expand(void *out, const int8_t *codes, const float *scales, const void *gamma,
+                                       int64_t M, int64_t D, carbon_dtype_t dtype, carbon_stream_t stream) {
+    if (!sizes_ok(M, D) || !dtype_ok(dtype)) return CARBON_ERR_INVALID_ARG;
+    if (M == 0 || D == 0) return CARBON_OK;
+    if (!out || !codes || !scales) return CARBON_ERR_INVALID_ARG;
+    const carbon_status_t st = ready();
+    if (st != CARBON_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    switch (dtype) {
+    case CARBON_F32: return note_cuda(run_expand<float>(out, codes, scales, gamma, M, D, s));
+    case CARBON_BF16: return note_cuda(run_expand<__nv_bfloat16>(out, codes, scales, gamma, M, D, s));
+    default: return note_cuda(run_expand<__half>(out, codes, scales, gamma, M, D, s));
+    }
+}
+
+}  // extern "C"

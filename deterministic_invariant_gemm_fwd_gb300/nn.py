@@ -22,6 +22,11 @@ for every batch split into the same tokens, and to the CPU oracle.  A layer
 on the correctly rounded tier ("superacc") takes db from that tier too: the
 exact column sum rounded once.
 
+Around the linear layers: ``Embedding`` / ``embedding``, ``RMSNorm`` /
+``rms_norm``, ``norm_linear`` (norm and linear layer with an 8-bit
+checkpoint) and ``linear_cross_entropy`` (output layer and loss), each with a
+deterministic gradient.
+
 Leading dimensions of the input are flattened into the token dimension.
 There is no CPU path: inputs must be CUDA tensors (float32, bfloat16 or
 float16; the tensor-core tier takes bfloat16 or float16).
@@ -32,7 +37,9 @@ import math
 
 import torch
 
-from . import _dtype_code, carbon_gemm_dw, linear_dw, linear_dx, linear_fwd
+from . import (_dtype_code, carbon_gemm_dw, embedding_bwd, embedding_fwd,
+               linear_cross_entropy_bwd, linear_cross_entropy_fwd, linear_dw, linear_dx, linear_fwd,
+               rms_norm_bwd, rms_norm_fwd)
 
 
 def bias_grad(dY, stream=None, tier="exact"):
@@ -122,3 +129,152 @@ class Linear(torch.nn.Module):
     def extra_repr(self):
         return (f"in_features={self.in_features}, out_features={self.out_features}, "
                 f"bias={self.bias is not None}, tier={self.tier!r}")
+
+
+# ---- the operators around the linear layers -------------------------------------
+
+
+class _EmbeddingFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, table, scale, padding_idx):
+        ctx.save_for_backward(ids)
+        ctx.rows, ctx.scale, ctx.padding_idx = table.shape[0], scale, padding_idx
+        return embedding_fwd(table, ids, scale)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (ids,) = ctx.saved_tensors
+        return None, embedding_bwd(grad.contiguous(), ids, ctx.rows, ctx.scale, ctx.padding_idx), None, None
+
+
+def embedding(ids, table, scale=1.0, padding_idx=None):
+    """scale * table[ids], differentiable in table; the gradient adds a row's
+    tokens in the order of their positions (no atomics)."""
+    return _EmbeddingFunction.apply(ids.contiguous(), table, float(scale), -1 if padding_idx is None else padding_idx)
+
+
+class Embedding(torch.nn.Module):
+    """Token embedding [num_rows, width] with an output scale.  Its weight can
+    be the table of linear_cross_entropy as well (tied weights)."""
+
+    def __init__(self, num_rows, width, scale=1.0, padding_idx=None, device=None, dtype=None):
+        super().__init__()
+        self.scale, self.padding_idx = scale, padding_idx
+        self.weight = torch.nn.Parameter(torch.empty((num_rows, width), device=device, dtype=dtype))
+        torch.nn.init.normal_(self.weight, std=0.02)
+
+    def forward(self, ids):
+        return embedding(ids, self.weight, self.scale, self.padding_idx)
+
+    def extra_repr(self):
+        return f"{self.weight.shape[0]}, {self.weight.shape[1]}, scale={self.scale}, padding_idx={self.padding_idx}"
+
+
+def _flat(t, width):
+    return t.reshape(-1, width).contiguous()
+
+
+class _RmsNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, gamma, eps):
+        D = gamma.shape[0]
+        r = rms_norm_fwd(_flat(x, D), gamma, None if residual is None else _flat(residual, D), eps)
+        ctx.save_for_backward(r.h, r.rstd, gamma)
+        ctx.shape, ctx.has_residual = x.shape, residual is not None
+        y = r.y.view(x.shape)
+        return (y, r.h.view(x.shape)) if ctx.has_residual else y
+
+    @staticmethod
+    def backward(ctx, dy, dh=None):
+        h, rstd, gamma = ctx.saved_tensors
+        D = gamma.shape[0]
+        dx, dgamma = rms_norm_bwd(_flat(dy, D), gamma, rstd, h=h, dh=None if dh is None else _flat(dh, D))
+        dx = dx.view(ctx.shape)
+        return dx, dx if ctx.has_residual else None, dgamma, None
+
+
+def rms_norm(x, gamma, residual=None, eps=1e-6):
+    """y = norm(x + residual) * gamma over the last dimension; with a residual
+    returns (y, x + residual), the second being the residual stream that goes
+    on.  Differentiable in x, residual and gamma."""
+    return _RmsNormFunction.apply(x, residual, gamma, eps)
+
+
+class RMSNorm(torch.nn.Module):
+    """Root-mean-square norm over the last dimension; forward(x) -> y,
+    forward(x, residual) -> (y, x + residual)."""
+
+    def __init__(self, width, eps=1e-6, device=None, dtype=None):
+        super().__init__()
+        self.eps = eps
+        self.weight = torch.nn.Parameter(torch.ones(width, device=device, dtype=dtype))
+
+    def forward(self, x, residual=None):
+        return rms_norm(x, self.weight, residual, self.eps)
+
+    def extra_repr(self):
+        return f"{self.weight.shape[0]}, eps={self.eps}"
+
+
+class _NormLinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, gamma, weight, bias, eps, tier):
+        D = gamma.shape[0]
+        r = rms_norm_fwd(_flat(x, D), gamma, None if residual is None else _flat(residual, D), eps, quantize=True)
+        out = linear_fwd(r.y, weight, bias, tier)
+        ctx.save_for_backward(r.codes, r.scales, r.rstd, gamma, weight)
+        ctx.shape, ctx.tier, ctx.has_bias, ctx.has_residual = x.shape, tier, bias is not None, residual is not None
+        out = out.view(*x.shape[:-1], weight.shape[1])
+        return (out, r.h.view(x.shape)) if ctx.has_residual else out
+
+    @staticmethod
+    def backward(ctx, dout, dh=None):
+        codes, scales, rstd, gamma, weight = ctx.saved_tensors
+        D = gamma.shape[0]
+        g = _flat(dout, weight.shape[1])
+        dy = linear_dx(g, weight, ctx.tier)
+        dx, dgamma, y = rms_norm_bwd(dy, gamma, rstd, codes=codes, scales=scales,
+                                     dh=None if dh is None else _flat(dh, D), recompute=True)
+        dw = linear_dw(y, g, ctx.tier) if ctx.needs_input_grad[3] else None
+        db = None
+        if ctx.has_bias and ctx.needs_input_grad[4]:
+            db = bias_grad(g, tier="superacc" if ctx.tier == "superacc" else "exact")
+        dx = dx.view(ctx.shape)
+        return dx, dx if ctx.has_residual else None, dgamma, dw, db, None, None
+
+
+def norm_linear(x, gamma, weight, bias=None, residual=None, eps=1e-6, tier="exact"):
+    """deterministic_linear(rms_norm(x + residual), weight, bias) that keeps,
+    for the backward pass, the normalised rows in 8 bits with a scale per
+    token instead of the residual stream and the linear layer's input: one
+    byte per element where rms_norm followed by deterministic_linear keeps
+    two tensors of the input's type.  The forward pass is the same; the
+    backward pass reads the rows back to within scale / 2 = max|row| / 254.
+    With a residual returns (output, x + residual)."""
+    return _NormLinearFunction.apply(x, residual, gamma, weight, bias, eps, tier)
+
+
+class _LinearCrossEntropyFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, table, targets, ignore_index, reduction):
+        x2 = _flat(x, table.shape[1])
+        t = targets.reshape(-1).contiguous()
+        loss, lse = linear_cross_entropy_fwd(x2, table, t, ignore_index, reduction)
+        ctx.save_for_backward(x2, table, t, lse)
+        ctx.shape, ctx.ignore_index, ctx.reduction = x.shape, ignore_index, reduction
+        return loss.view(targets.shape) if reduction == "none" else loss
+
+    @staticmethod
+    def backward(ctx, grad):
+        x2, table, t, lse = ctx.saved_tensors
+        g = grad.reshape(-1).contiguous() if ctx.reduction == "none" else grad
+        dx, dtable = linear_cross_entropy_bwd(g, x2, table, t, lse, ctx.ignore_index, ctx.reduction)
+        return dx.view(ctx.shape), dtable, None, None, None
+
+
+def linear_cross_entropy(x, table, targets, ignore_index=-100, reduction="mean"):
+    """Softmax cross entropy of the logits x . table^T (table [V, D], e.g. an
+    Embedding's weight) against targets, without storing the logits;
+    differentiable in x and table.  reduction="mean" divides by the positions
+    that count and is 0 where there are none."""
+    return _LinearCrossEntropyFunction.apply(x, table, targets, ignore_index, reduction)

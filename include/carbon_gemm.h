@@ -137,7 +137,8 @@ typedef enum {
     CARBON_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed */
     CARBON_ERR_TIMEOUT = 5,       /* a bounded device-side wait gave up */
     CARBON_ERR_SCRATCH_LIMIT = 6, /* needs more than the fixed no-allocation workspace */
-    CARBON_ERR_OUT_OF_BOUNDS = 7  /* bounds-checked build only: a kernel skipped an access out of range */
+    CARBON_ERR_OUT_OF_BOUNDS = 7  /* bounds-checked build: a kernel skipped an access out of range; any build:
+                                   * a token id or target outside its table was left out (carbon_lm.h) */
 } carbon_status_t;
 
 /* Forward pass Y[M,N] = X[M,K] . W[K,N] + bias[N].
@@ -255,8 +256,9 @@ carbon_status_t carbon_chunk_values_combine(void *out, const double *P, int64_t 
  * that kernels set when a bounded wait gives up (CARBON_ERR_TIMEOUT) or, in
  * the bounds-checked build (libcarbon_gemm_bounds.so, compiled with
  * CARBON_DEBUG_BOUNDS), when a kernel skipped an access outside its buffer
- * (CARBON_ERR_OUT_OF_BOUNDS); or CARBON_ERR_CUDA if the stream reports an
- * error. */
+ * (CARBON_ERR_OUT_OF_BOUNDS, which carbon_lm.h's operators also set when an
+ * index names no row of its table); or CARBON_ERR_CUDA if the stream reports
+ * an error. */
 carbon_status_t carbon_get_device_status(carbon_stream_t stream);
 
 /* Static, human-readable name of a status code. */
