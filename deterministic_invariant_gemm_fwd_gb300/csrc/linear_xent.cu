@@ -6,20 +6,22 @@
 //
 // Positions that count are first gathered into a dense x (ignored ones cost
 // no product, and what they hold reaches no sum).  Then one persistent kernel
-// per direction works through units of one 128-row output tile:
-//   L  128 positions x 256 vocabulary entries of z, reduced over D.
+// per direction works through units of one output tile; a pair of CTAs (two
+// SMs, tcgen05 cta_group::2) shares a tile of 256 rows, each CTA staging its
+// own 128 rows of A and half the columns of B:
+//   L  256 positions x 256 vocabulary entries of z, reduced over D.
 //      Loss: each row's running maximum and sum of exponentials over 128
 //      entries go out as one (max, sum) pair; a second kernel joins the pairs
 //      in order.  Gradient: exp(z - lse) - onehot goes out as G.
-//   T  128 vocabulary entries x up to 256 columns of dtable, reduced over
+//   T  256 vocabulary entries x up to 256 columns of dtable, reduced over
 //      the positions: G^T . x.
-//   X  128 positions x up to 256 columns of dx, reduced over kGranule
+//   X  256 positions x up to 256 columns of dx, reduced over kGranule
 //      vocabulary entries at a time: G . table.
 // The gradient takes the vocabulary in pieces: L units of piece p + 1 run
 // before the T and X units of piece p, and G keeps three pieces, so that a
-// unit rarely waits for the units it reads (counters in the workspace; every
-// unit only waits for units earlier in the list, and each CTA takes its units
-// in list order, so the waits end).
+// unit rarely waits for the units it reads (counters in the workspace; units
+// are handed out in list order and wait only for earlier ones, so the waits
+// end).
 //
 // Fixed order: a unit's k-blocks of 64 run in ascending order into one fp32
 // accumulator.  dx adds the granules' sums in order, so neither the piece
@@ -35,17 +37,21 @@ namespace {
 __device__ unsigned int g_xent_status = 0;
 #define CHK(idx, len, n) in_bounds(&g_xent_status, (int64_t)(idx), (int64_t)(len), (int64_t)(n))
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;
-constexpr int kStages = 4;
-constexpr int kThreads = 192;            // TMA producer, MMA issuer, 4 epilogue warps
-constexpr int kEpiWarps = 4;
+constexpr int kBM = 256, kBN = 256, kBK = 64;        // a CTA pair's tile; each CTA has 128 rows
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (4 + kEpiWarps);        // TMA producer, MMA issuer, scheduler, (idle), epilogue
 constexpr uint32_t kBlock = 64 * kBK * 2;             // one 64 x 64 box: 8 KiB
-constexpr uint32_t kABytes = kBM * kBK * 2;
-constexpr uint32_t kStageBytes = kABytes + kBN * kBK * 2;
+constexpr uint32_t kABytes = 128 * kBK * 2;           // per CTA: 128 rows of A, half of B's columns
+constexpr uint32_t kStageBytes = kABytes + kBN / 2 * kBK * 2;
+constexpr int kSlots = 4;                             // units handed out ahead
 constexpr uint32_t kStagingOffset = kStages * kStageBytes;
 constexpr uint32_t kBarOffset = kStagingOffset + kEpiWarps * 4096;
-constexpr uint32_t kSmemBytes = kBarOffset + (2 * kStages + 4) * 8 + 16 + 1024;
+constexpr int kBars = 2 * kStages + 4 + 2 * kSlots;
+constexpr uint32_t kSmemBytes = kBarOffset + kBars * 8 + kSlots * 4 + 16 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
+// epilogue warps of a pair: each adds one to a unit's counter
+constexpr unsigned kDone = 2 * kEpiWarps;
 
 constexpr int kGroup = 128;              // vocabulary entries per (max, sum) pair
 constexpr int kGranule = 4096;           // vocabulary entries per partial sum of dx
@@ -66,7 +72,7 @@ struct Head {
 
 // Sizes and workspace addresses, host and device.
 struct Plan {
-    int64_t M, Mp, D, V;                 // Mp: M rounded up to 128, at least 128
+    int64_t M, Mp, D, V;                 // Mp: M rounded up to a tile's rows, at least one tile
     int vocab_groups;                    // pairs per row
     int dtiles, dwidth;                  // column tiles of dx and dtable
     int lwidth;                          // vocabulary entries per L unit
@@ -75,6 +81,7 @@ struct Plan {
     int slots;                           // granule sums of dx kept side by side; 1: added in place
     bool f16, grad;
     Head *head;
+    unsigned int *ticket;                // next unit
     unsigned int *done_l, *done_tx;      // per piece
     int *rowmap, *inverse, *tgt;
     float *lse2, *rfac;                  // gradient: lse log2(e) - k, g / max |g|
@@ -93,7 +100,7 @@ int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, bool gra
     p.Mp = round_up(M > 0 ? M : 1, kBM);
     p.vocab_groups = (int)((V + kGroup - 1) / kGroup);
     p.dtiles = (int)((D + kBN - 1) / kBN);
-    p.dwidth = (int)round_up((D + p.dtiles - 1) / p.dtiles, 64);
+    p.dwidth = (int)round_up((D + p.dtiles - 1) / p.dtiles, 128);
     p.dtiles = (int)((D + p.dwidth - 1) / p.dwidth);
     p.granules = (int)((V + kGranule - 1) / kGranule);
     const int64_t tiles256 = p.Mp / kBM * ((V + kBN - 1) / kBN);
@@ -115,7 +122,8 @@ int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, bool gra
         return q;
     };
     p.head = reinterpret_cast<Head *>(take(sizeof(Head)));
-    p.done_l = reinterpret_cast<unsigned int *>(take(8 * (int64_t)p.pieces));
+    p.ticket = reinterpret_cast<unsigned int *>(take(4 + 8 * (int64_t)p.pieces));
+    p.done_l = p.ticket + 1;
     p.done_tx = p.done_l + p.pieces;
     p.rowmap = reinterpret_cast<int *>(take(4 * p.Mp));
     p.inverse = reinterpret_cast<int *>(take(4 * p.Mp));
@@ -162,7 +170,7 @@ xent_scan_kernel(const Plan p, const ScanArgs a) {
     allow_next_grid();
     const int t = threadIdx.x, lane = t % 32, warp = t / 32;
     const int bits = p.f16 ? kScaleBits16 : kScaleBitsBf;
-    for (int i = t; i < 2 * p.pieces; i += kScanThreads) p.done_l[i] = 0u;
+    for (int i = t; i < 1 + 2 * p.pieces; i += kScanThreads) p.ticket[i] = 0u;
 
     auto counts = [&](int64_t m, int64_t *tgt) {
         *tgt = a.targets[m];
@@ -273,7 +281,7 @@ enum UnitType { UNIT_L = 0, UNIT_T = 1, UNIT_X = 2 };
 struct Unit {
     int type, piece;
     int m0, n0;              // output tile: first row, first column (rows of the output for T are table rows)
-    int width;               // columns, a multiple of 64
+    int width;               // columns, a multiple of 128
     int parts;               // accumulations, one after the other (X: granules)
     int granule;             // X: first granule
 };
@@ -282,10 +290,11 @@ struct Unit {
 struct Walk {
     const Plan &p;
     int tm;                  // row tiles of positions
+    int kept;
     int phase = 0;
     int64_t base = 0, count = 0;
 
-    __device__ Walk(const Plan &plan, int tiles) : p(plan), tm(tiles) { count = size(0); }
+    __device__ Walk(const Plan &plan, int n) : p(plan), tm(row_tiles(n)), kept(n) { count = size(0); }
 
     __device__ int cols(int piece) const { return min(p.piece_cols, (int)(p.V - (int64_t)piece * p.piece_cols)); }
     // phase 0: L(0); 2q+1: L(q+1) (empty for the last piece); 2q+2: T and X of q
@@ -320,7 +329,7 @@ struct Walk {
             const int c = p.grad ? cols(o.piece) : (int)p.V;
             o.m0 = (int)(i % tm) * kBM;
             o.n0 = (int)(i / tm) * p.lwidth;
-            o.width = min(p.lwidth, (c - o.n0 + 63) / 64 * 64);
+            o.width = min(p.lwidth, (c - o.n0 + 127) / 128 * 128);
         } else {
             o.piece = phase / 2 - 1;
             const int64_t nt = n_t(o.piece);
@@ -339,7 +348,7 @@ struct Walk {
             }
             o.m0 = (int)(i / p.dtiles) * kBM;
             o.n0 = (int)(i % p.dtiles) * p.dwidth;
-            o.width = min(p.dwidth, (int)(p.D - o.n0 + 63) / 64 * 64);
+            o.width = min(p.dwidth, (int)(p.D - o.n0 + 127) / 128 * 128);
         }
         *out = o;
         return true;
@@ -347,7 +356,7 @@ struct Walk {
     // k-blocks of part j of a unit.
     __device__ int k_blocks(const Unit &o, int part) const {
         if (o.type == UNIT_L) return (int)((p.D + kBK - 1) / kBK);
-        if (o.type == UNIT_T) return tm * (kBM / kBK);
+        if (o.type == UNIT_T) return kept > kBK ? (kept + kBK - 1) / kBK : 1;
         const int c = cols(o.piece) - (o.granule + part) * kGranule;
         return (min(c, kGranule) + kBK - 1) / kBK;
     }
@@ -391,8 +400,82 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// ---- a pair of CTAs: two SMs share one tile (tcgen05 cta_group::2) -----------
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of a shared-memory location of this CTA in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// An arrival that hands over no memory write of this thread.  (A release at
+// cluster scope waits for all of the thread's global stores.)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// TMA load into this CTA's shared memory, counted on a barrier of either CTA.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];"
+        ::"r"(dst), "l"(map), "r"(bar), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t slot_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(slot_smem), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once the MMAs so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
+
 // Instruction descriptor, kind::f16: fp32 accumulate, A and B both bf16 or
-// both fp16, majorness (1: rows/columns contiguous), N, M = 128.
+// both fp16, majorness (1: rows/columns contiguous), N, M = 256 (the pair's).
 __device__ __forceinline__ uint32_t instr_desc(int n, bool a_mn, bool b_mn, bool f16) {
     return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((a_mn ? 1u : 0u) << 15) |
            ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
@@ -412,16 +495,27 @@ struct Maps {
 };
 
 struct Ctx {
-    uint32_t sbase, bars, tmem;
+    uint32_t sbase, bars, tmem, rank;
+    volatile uint32_t *slots;            // units handed out
     volatile uint32_t *abort_flag;
-    __device__ uint32_t full(int s) const { return bars + 8u * s; }
+    __device__ uint32_t full(int s) const { return bars + 8u * s; }                          // used in CTA 0
     __device__ uint32_t empty(int s) const { return bars + 8u * (kStages + s); }
     __device__ uint32_t tfull(int b) const { return bars + 8u * (2 * kStages + b); }
-    __device__ uint32_t tempty(int b) const { return bars + 8u * (2 * kStages + 2 + b); }
+    __device__ uint32_t tempty(int b) const { return bars + 8u * (2 * kStages + 2 + b); }    // used in CTA 0
+    __device__ uint32_t sfull(int s) const { return bars + 8u * (2 * kStages + 4 + s); }
+    __device__ uint32_t sempty(int s) const { return bars + 8u * (2 * kStages + 4 + kSlots + s); }   // CTA 0
     __device__ bool wait(uint32_t bar, uint32_t parity) const {
         if (mbar_wait(bar, parity)) return true;
         give_up();
         return false;
+    }
+    // The same for a barrier that the other CTA's threads arrive on.
+    __device__ bool wait_cluster(uint32_t bar, uint32_t parity) const {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        const uint64_t t0 = global_ns();
+        while (!mbar_try_wait_cluster(bar, parity))
+            if (global_ns() - t0 > kWaitBudgetNs) { give_up(); return false; }
+        return true;
     }
     __device__ void give_up() const {
         *abort_flag = 1u;
@@ -440,80 +534,167 @@ struct Ctx {
     }
 };
 
+// Units are handed out in list order, one at a time, to whichever pair asks
+// next (a pair only waits for units that a running pair already has: the
+// kernel makes progress however few of its pairs the GPU runs at once).  One
+// thread of CTA 0 takes them; every role of both CTAs reads them here.
+struct Feed {
+    const Ctx &c;
+    int slot = 0;
+    uint32_t ph = 0;
+    // The next unit, for a whole warp.  false: none left, or gave up.  The
+    // shuffle makes the unit warp-uniform to the compiler, so that what the
+    // TMA and MMA instructions take from it lives in uniform registers (with
+    // one lane's branch instead, four TMA loads took 570 cycles to issue).
+    __device__ bool next(Walk &w, Unit *o) {
+        const bool ok = !c.aborted() && c.wait_cluster(c.sfull(slot), ph);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        const uint32_t u = __shfl_sync(0xffffffffu, c.slots[slot], 0);
+        const bool more = w.at(u, o);             // uses u: the slot has been read
+        if (threadIdx.x % 32 == 0) mbar_arrive_cluster_relaxed(map_rank(c.sempty(slot), 0));
+        if (++slot == kSlots) { slot = 0; ph ^= 1u; }
+        return more;
+    }
+};
+// readers of a unit: producers of both CTAs, the MMA issuer, both epilogues
+constexpr int kReaders = 2 + 1 + 2 * kEpiWarps;
+
+__device__ __forceinline__ void hand_out(const Plan &p, Walk w, const Ctx &c) {
+    Unit o;
+    int slot = 0;
+    uint32_t ph = 0;
+    for (bool more = true; more && !c.aborted();) {
+        if (!c.wait_cluster(c.sempty(slot), ph ^ 1u)) return;
+        const uint32_t u = atomicAdd(p.ticket, 1u);
+        more = w.at(u, &o);                       // the first one past the end tells the roles to stop
+        for (uint32_t r = 0; r < 2; ++r) {
+            st_cluster_u32(map_rank(smem_addr(const_cast<uint32_t *>(c.slots)) + 4u * slot, r), u);
+            mbar_arrive_cluster(map_rank(c.sfull(slot), r));
+        }
+        if (++slot == kSlots) { slot = 0; ph ^= 1u; }
+    }
+}
+
 // What a unit's operands wait for.
 __device__ __forceinline__ bool wait_operands(const Plan &p, const Walk &w, const Unit &o, const Ctx &c) {
     if (!p.grad) return true;
     if (o.type == UNIT_L) {                       // its piece's buffer is free
         const int q = o.piece - p.buffers;
-        return q < 0 || c.wait_count(p.done_tx + q, kEpiWarps * (unsigned)(w.n_t(q) + w.n_x(q)));
+        return q < 0 || c.wait_count(p.done_tx + q, kDone * (unsigned)(w.n_t(q) + w.n_x(q)));
     }
-    return c.wait_count(p.done_l + o.piece, kEpiWarps * (unsigned)w.n_l(o.piece));
+    return c.wait_count(p.done_l + o.piece, kDone * (unsigned)w.n_l(o.piece));
 }
 
+// Loads of one k-block: this CTA's rows of A and columns of B, in boxes of 64.
+// A: coordinates (ax, ay), the boxes (adx, ady) apart; B likewise.
+struct Loads {
+    const CUtensorMap *a, *b;
+    int ax, ay, adx, ady, bx, by, bdx, bdy;
+    int akx, aky, bkx, bky;                   // step per k-block
+};
+
+__device__ __forceinline__ Loads loads_of(const Plan &p, const Maps &maps, const Unit &o, int granule, uint32_t rank) {
+    const int v0 = o.piece * p.piece_cols;
+    const int gcol = p.grad ? (o.piece % p.buffers) * p.piece_cols : 0;
+    const int m0 = o.m0 + (int)rank * 128, n0 = o.n0 + (int)rank * (o.width / 2);
+    const int kc = granule * kGranule;
+    Loads l;
+    if (o.type == UNIT_L) {                   // x and the table, both along D
+        l.a = &maps.x; l.ax = 0; l.ay = m0; l.adx = 0; l.ady = 64; l.akx = kBK; l.aky = 0;
+        l.b = &maps.w; l.bx = 0; l.by = v0 + n0; l.bdx = 0; l.bdy = 64; l.bkx = kBK; l.bky = 0;
+    } else if (o.type == UNIT_T) {            // G^T and x, along the positions
+        l.a = &maps.g; l.ax = gcol + m0; l.ay = 0; l.adx = 64; l.ady = 0; l.akx = 0; l.aky = kBK;
+        l.b = &maps.x; l.bx = n0; l.by = 0; l.bdx = 64; l.bdy = 0; l.bkx = 0; l.bky = kBK;
+    } else {                                  // G and the table, along the vocabulary
+        l.a = &maps.g; l.ax = gcol + kc; l.ay = m0; l.adx = 0; l.ady = 64; l.akx = kBK; l.aky = 0;
+        l.b = &maps.w; l.bx = n0; l.by = v0 + kc; l.bdx = 64; l.bdy = 0; l.bkx = 0; l.bky = kBK;
+    }
+    return l;
+}
+
+// A whole warp runs the loop; one lane issues.
 __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w, const Ctx &c) {
     int s = 0;
     uint32_t ph = 0;
     Unit o;
+    Feed feed{c};
     bool ok = true;
-    for (int64_t u = blockIdx.x; ok && !c.aborted() && w.at(u, &o); u += gridDim.x) {
-        if (!wait_operands(p, w, o, c)) break;
+    while (ok && feed.next(w, &o)) {
+        if (!__all_sync(0xffffffffu, wait_operands(p, w, o, c))) break;
         fence_proxy_async_all();                  // other CTAs' G, before this CTA's TMA reads
-        const int gcol = (o.piece % (p.grad ? p.buffers : 1)) * p.piece_cols, v0 = o.piece * p.piece_cols;
-        const int nb = o.width / 64;
+        const bool two = o.width > 128;           // boxes of B per CTA
         for (int part = 0; ok && part < o.parts; ++part) {
-            const int nkb = w.k_blocks(o, part), first = (o.granule + part) * (kGranule / kBK);
+            Loads l = loads_of(p, maps, o, o.granule + part, c.rank);
+            const int nkb = w.k_blocks(o, part);
             for (int kb = 0; kb < nkb; ++kb) {
-                if (!c.wait(c.empty(s), ph ^ 1u)) { ok = false; break; }
-                const uint32_t bar = c.full(s), sa = c.sbase + s * kStageBytes, sb = sa + kABytes;
-                mbar_arrive_expect_tx(bar, kABytes + nb * kBlock);
-                const int k0 = kb * kBK;
-                if (o.type == UNIT_L) {
-                    for (int i = 0; i < 2; ++i) tma_load_2d(sa + i * kBlock, &maps.x, bar, k0, o.m0 + 64 * i);
-                    for (int j = 0; j < nb; ++j) tma_load_2d(sb + j * kBlock, &maps.w, bar, k0, v0 + o.n0 + 64 * j);
-                } else if (o.type == UNIT_T) {
-                    for (int i = 0; i < 2; ++i) tma_load_2d(sa + i * kBlock, &maps.g, bar, gcol + o.m0 + 64 * i, k0);
-                    for (int j = 0; j < nb; ++j) tma_load_2d(sb + j * kBlock, &maps.x, bar, o.n0 + 64 * j, k0);
-                } else {
-                    const int kc = (first + kb) * kBK;
-                    for (int i = 0; i < 2; ++i) tma_load_2d(sa + i * kBlock, &maps.g, bar, gcol + kc, o.m0 + 64 * i);
-                    for (int j = 0; j < nb; ++j) tma_load_2d(sb + j * kBlock, &maps.w, bar, o.n0 + 64 * j, v0 + kc);
+                ok = __all_sync(0xffffffffu, c.wait(c.empty(s), ph ^ 1u));
+                if (!ok) break;
+                const uint32_t sa = c.sbase + s * kStageBytes, sb = sa + kABytes;
+                if (elect_one()) {
+                    const uint32_t bar = map_rank(c.full(s), 0);
+                    // both CTAs' bytes
+                    if (c.rank == 0) mbar_arrive_expect_tx(c.full(s), two ? 2 * (kABytes + 2 * kBlock) : 2 * (kABytes + kBlock));
+                    tma_load_pair(sa, l.a, bar, l.ax, l.ay);
+                    tma_load_pair(sa + kBlock, l.a, bar, l.ax + l.adx, l.ay + l.ady);
+                    tma_load_pair(sb, l.b, bar, l.bx, l.by);
+                    if (two) tma_load_pair(sb + kBlock, l.b, bar, l.bx + l.bdx, l.by + l.bdy);
                 }
+                __syncwarp();
+                l.ax += l.akx; l.ay += l.aky; l.bx += l.bkx; l.by += l.bky;
                 if (++s == kStages) { s = 0; ph ^= 1u; }
             }
         }
     }
-    // every load lands before the CTA may exit (stages not armed in this pass
-    // completed earlier, so their wait returns at once)
-    for (int i = 0; i < kStages; ++i) {
+    // CTA 0 sees every load of both land before the pair may exit (stages not
+    // armed in this pass completed earlier, so their wait returns at once)
+    for (int i = 0; c.rank == 0 && i < kStages; ++i) {
         if (--s < 0) { s = kStages - 1; ph ^= 1u; }
-        if (!mbar_wait(c.full(s), ph)) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(c.full(s), ph))) break;
     }
 }
 
-template <bool F16>
+// k-blocks of one accumulation.
+template <bool A_MN, bool B_MN>
+__device__ __forceinline__ bool issue_blocks(const Ctx &c, uint32_t d, uint32_t idesc, int nkb, int &s, uint32_t &ph) {
+    for (int kb = 0; kb < nkb; ++kb) {
+        if (!__all_sync(0xffffffffu, c.wait(c.full(s), ph))) return false;
+        tc_fence_after();
+        const uint32_t sa = c.sbase + s * kStageBytes, sb = sa + kABytes;
+        if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k)
+                mma_pair(d, operand_desc(sa, A_MN, k), operand_desc(sb, B_MN, k), idesc, (kb | k) != 0 ? 1u : 0u);
+            mma_commit_pair(c.empty(s));
+        }
+        __syncwarp();
+        if (++s == kStages) { s = 0; ph ^= 1u; }
+    }
+    return true;
+}
+
+// CTA 0 issues the pair's MMAs.
+template <bool GRAD, bool F16>
 __device__ __forceinline__ void issue(Walk w, const Ctx &c) {
     int s = 0, acc = 0;
     uint32_t ph = 0, aph = 0;
     Unit o;
-    for (int64_t u = blockIdx.x; !c.aborted() && w.at(u, &o); u += gridDim.x) {
-        const bool a_mn = o.type == UNIT_T, b_mn = o.type != UNIT_L;
-        const uint32_t idesc = instr_desc(o.width, a_mn, b_mn, F16);
+    Feed feed{c};
+    while (feed.next(w, &o)) {
         for (int part = 0; part < o.parts; ++part) {
-            if (!c.wait(c.tempty(acc), aph ^ 1u)) return;
+            if (!__all_sync(0xffffffffu, c.wait_cluster(c.tempty(acc), aph ^ 1u))) return;
             tc_fence_after();
             const uint32_t d = c.tmem + (uint32_t)(acc * kBN);
             const int nkb = w.k_blocks(o, part);
-            for (int kb = 0; kb < nkb; ++kb) {
-                if (!c.wait(c.full(s), ph)) return;
-                tc_fence_after();
-                const uint32_t sa = c.sbase + s * kStageBytes, sb = sa + kABytes;
-#pragma unroll
-                for (int k = 0; k < kBK / 16; ++k)
-                    mma_bf16(d, operand_desc(sa, a_mn, k), operand_desc(sb, b_mn, k), idesc, (kb | k) != 0 ? 1u : 0u);
-                mma_commit(c.empty(s));
-                if (++s == kStages) { s = 0; ph ^= 1u; }
-            }
-            mma_commit(c.tfull(acc));
+            bool ok;
+            if (!GRAD || o.type == UNIT_L)
+                ok = issue_blocks<false, false>(c, d, instr_desc(o.width, false, false, F16), nkb, s, ph);
+            else if (o.type == UNIT_T)
+                ok = issue_blocks<true, true>(c, d, instr_desc(o.width, true, true, F16), nkb, s, ph);
+            else
+                ok = issue_blocks<false, true>(c, d, instr_desc(o.width, false, true, F16), nkb, s, ph);
+            if (!ok) return;
+            if (elect_one()) mma_commit_pair(c.tfull(acc));
+            __syncwarp();
             if (++acc == 2) { acc = 0; aph ^= 1u; }
         }
     }
@@ -544,9 +725,9 @@ struct Store {
 };
 
 // Loss: (max, sum) pairs and the targets' logits of this thread's row.
-__device__ __forceinline__ void loss_rows(const Plan &p, const Unit &o, uint32_t tmem, int row) {
+__device__ __forceinline__ void loss_rows(const Plan &p, const Unit &o, uint32_t tmem, int row, int half) {
     const int tgt = p.tgt[row];
-    for (int g = 0; g < o.width; g += kGroup) {
+    for (int g = half * kGroup; g < o.width; g += 2 * kGroup) {
         float mx = -INFINITY, sum = 0.0f;                 // of z log2(e)
 #pragma unroll 1
         for (int c = g; c < min(g + kGroup, o.width); c += 32) {
@@ -577,15 +758,17 @@ __device__ __forceinline__ void loss_rows(const Plan &p, const Unit &o, uint32_t
 
 template <bool GRAD, bool F16>
 __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w, const Ctx &c, int warp, int lane) {
-    const int quarter = warp % 4;
-    Store<F16> store{c.sbase + kStagingOffset + (uint32_t)(warp - 2) * 4096u, lane};
+    const int quarter = warp % 4, half = (warp - 4) / 4;  // 32 rows; one half of the columns
+    Store<F16> store{c.sbase + kStagingOffset + (uint32_t)(warp - 4) * 4096u, lane};
     const float gscale = GRAD ? p.head->gscale : 0.0f;
     constexpr float kOne = (float)(1ull << (F16 ? kScaleBits16 : kScaleBitsBf));
     int acc = 0;
     uint32_t aph = 0;
     Unit o;
-    for (int64_t u = blockIdx.x; !c.aborted() && w.at(u, &o); u += gridDim.x) {
-        const int row = o.m0 + quarter * 32 + lane;
+    Feed feed{c};
+    while (feed.next(w, &o)) {
+        const int row0 = o.m0 + (int)c.rank * 128 + quarter * 32, row = row0 + lane;
+        const int c0 = half * (o.width / 2), c1 = c0 + o.width / 2;
         float lse2 = 0.0f, rfac = 0.0f;
         int tgt = -1;
         if (GRAD && o.type == UNIT_L) {
@@ -598,12 +781,12 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
             tc_fence_after();
             const uint32_t tmem = c.tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kBN);
             if (!GRAD) {
-                loss_rows(p, o, tmem, row);
+                loss_rows(p, o, tmem, row, half);
             } else if (o.type == UNIT_L) {
                 const int n = (int)(p.V - (int64_t)o.piece * p.piece_cols) - o.n0;   // valid columns of this tile
                 const int gcol = (o.piece % p.buffers) * p.piece_cols + o.n0;
 #pragma unroll 1
-                for (int cc = 0; cc < o.width; cc += 32) {
+                for (int cc = c0; cc < c1; cc += 32) {
                     uint32_t r[32];
                     float f[32];
                     tmem_ld32(tmem + (uint32_t)cc, r);
@@ -614,17 +797,17 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
                         // no position, or no such entry: exactly zero, whatever z is
                         if (rfac == 0.0f || cc + i >= n) f[i] = 0.0f;
                     }
-                    store.put(&maps.g_out, f, gcol + cc, o.m0 + quarter * 32);
+                    store.put(&maps.g_out, f, gcol + cc, row0);
                 }
             } else if (o.type == UNIT_T) {
 #pragma unroll 1
-                for (int cc = 0; cc < o.width && o.n0 + cc < p.D; cc += 32) {
+                for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 32) {
                     uint32_t r[32];
                     float f[32];
                     tmem_ld32(tmem + (uint32_t)cc, r);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]) * gscale;
-                    store.put(&maps.dt_out, f, o.n0 + cc, o.piece * p.piece_cols + o.m0 + quarter * 32);
+                    store.put(&maps.dt_out, f, o.n0 + cc, o.piece * p.piece_cols + row0);
                 }
             } else {
                 // granule sums of dx: a slot each, or added in place in granule order
@@ -632,12 +815,12 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
                 const bool add = p.slots == 1 && granule > 0;
                 if (add && part == 0) {                  // the previous piece's sums
                     const int q = o.piece - 1;
-                    const bool there = lane != 0 || c.wait_count(p.done_tx + q, kEpiWarps * (unsigned)(w.n_t(q) + w.n_x(q)));
+                    const bool there = lane != 0 || c.wait_count(p.done_tx + q, kDone * (unsigned)(w.n_t(q) + w.n_x(q)));
                     if (!__all_sync(0xffffffffu, there)) return;
                 }
                 float *dst = p.acc + ((p.slots > 1 ? (int64_t)granule * p.Mp : 0) + row) * p.D + o.n0;
 #pragma unroll 1
-                for (int cc = 0; cc < o.width && o.n0 + cc < p.D; cc += 32) {
+                for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 32) {
                     uint32_t r[32];
                     tmem_ld32(tmem + (uint32_t)cc, r);
 #pragma unroll
@@ -657,10 +840,10 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(c.tempty(acc));
+            if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(c.tempty(acc), 0));
             if (++acc == 2) { acc = 0; aph ^= 1u; }
         }
-        if (GRAD) {                                       // this unit's output is in memory
+        if (GRAD) {                                       // this warp's part of the output is in memory
             if (lane == 0) {
                 bulk_wait_all();
                 fence_proxy_async_all();
@@ -674,17 +857,20 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
 }
 
 template <bool GRAD, bool F16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint32_t *slot = reinterpret_cast<uint32_t *>(smem + kBarOffset + (2 * kStages + 4) * 8);
+    uint32_t *words = reinterpret_cast<uint32_t *>(smem + kBarOffset + kBars * 8);
     Ctx c;
     c.sbase = smem_addr(smem);
     c.bars = c.sbase + kBarOffset;
-    c.abort_flag = slot + 1;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    c.rank = cluster_rank();
+    c.slots = words;
+    c.abort_flag = words + kSlots;
+    uint32_t *tmem_slot = words + kSlots + 1;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;   // warp-uniform
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(c.full(s), 1);
@@ -692,35 +878,44 @@ xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(c.tfull(b), 1);
-            mbar_init(c.tempty(b), kEpiWarps);
+            mbar_init(c.tempty(b), 2 * kEpiWarps);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(c.sfull(s), 1);
+            mbar_init(c.sempty(s), kReaders);
         }
         *c.abort_flag = 0u;
         fence_mbar_init();
         prefetch_map(&maps.x);
         prefetch_map(&maps.w);
     }
-    if (warp == 1) tmem_alloc(smem_addr(slot), 512);
+    if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();                                   // both CTAs' barriers are set up
     tc_fence_after();
-    c.tmem = *slot;
+    c.tmem = *tmem_slot;
     wait_prior_grid();
     allow_next_grid();
-    const Walk w(p, row_tiles(p.head->kept));
+    const Walk w(p, p.head->kept);
 
     if (warp == 0) {
-        if (lane == 0) produce(p, maps, w, c);
+        produce(p, maps, w, c);
     } else if (warp == 1) {
-        if (lane == 0) issue<F16>(w, c);
-    } else {
+        if (c.rank == 0) issue<GRAD, F16>(w, c);
+    } else if (warp == 2) {
+        if (lane == 0 && c.rank == 0) hand_out(p, w, c);
+    } else if (warp >= 4) {
         epilogue<GRAD, F16>(p, maps, w, c, warp, lane);
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();                                   // no arrival at, or MMA into, a CTA that has left
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(c.tmem, 512);
+        tmem_dealloc_pair(c.tmem, 512);
     }
+    cluster_sync_all();                                   // the pair gives its columns back together
 }
 
 // ---- joining ---------------------------------------------------------------------------
@@ -852,7 +1047,8 @@ cudaError_t launch_tiles(const Plan &p, const void *table, void *dtable, int sms
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (err != cudaSuccess) return err;
     count_launch();
-    return launch_k(kern, dim3((unsigned)sms), dim3(kThreads), (size_t)kSmemBytes, s, 1, maps, p);
+    // the pair is the kernel's compile-time cluster
+    return launch_k(kern, dim3((unsigned)(sms / 2 * 2)), dim3(kThreads), (size_t)kSmemBytes, s, 1, maps, p);
 }
 
 cudaError_t launch_gather(const Plan &p, const ScanArgs &a, const void *x, cudaStream_t s) {
