@@ -368,8 +368,17 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t sr
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
                  ::"l"(map), "r"(src), "r"(c0), "r"(c1) : "memory");
 }
+// *global += shared, element by element (fp32)
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap *map, uint32_t src, int c0, int c1) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(map), "r"(src), "r"(c0), "r"(c1) : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read_0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// all but the last n groups have written their data
+template <int N>
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
@@ -492,6 +501,7 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, bool mn, int k) 
 struct Maps {
     CUtensorMap x, w, g;        // operand boxes 64 x 64, 128-byte swizzle
     CUtensorMap g_out, dt_out;  // 32 x 32 store boxes, 64-byte swizzle
+    CUtensorMap acc;            // 32 x 32 fp32 boxes, 128-byte swizzle
 };
 
 struct Ctx {
@@ -700,14 +710,15 @@ __device__ __forceinline__ void issue(Walk w, const Ctx &c) {
     }
 }
 
-// 32 x 32 sub-tiles to global memory through two staging buffers per warp.
+// 32 x 32 sub-tiles to global memory through a warp's staging buffer (4 KiB:
+// two 16-bit sub-tiles or one of fp32).
 template <bool F16>
 struct Store {
     uint32_t stg;
     int lane, n = 0;
     __device__ void put(const CUtensorMap *map, const float (&f)[32], int col, int row) {
         const uint32_t buf = stg + (uint32_t)(n & 1) * 2048u;
-        if (n >= 2 && lane == 0) bulk_wait_read_1();
+        if (lane == 0) bulk_wait_read_1();                // the sub-tile before the last has left
         __syncwarp();
 #pragma unroll
         for (int g = 0; g < 4; ++g)                       // 16-byte pieces as the 64-byte swizzle expects them
@@ -721,6 +732,28 @@ struct Store {
             bulk_commit();
         }
         ++n;
+    }
+    // fp32, stored or added to what is there
+    __device__ void put_f32(const CUtensorMap *map, const uint32_t (&r)[32], int col, int row, bool add) {
+        if (lane == 0) bulk_wait_read_0();
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < 8; ++g)                       // 128-byte swizzle
+            st_shared_v4(stg + lane * 128 + 16 * (g ^ (lane & 7)),
+                         make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (add) tma_add_2d(map, stg, col, row);
+            else tma_store_2d(map, stg, col, row);
+            bulk_commit();
+        }
+        n = 0;                                            // the next 16-bit sub-tile goes to the first half
+    }
+    // After an fp32 sub-tile both halves are in use until it has left.
+    __device__ void begin_16() {
+        if (lane == 0) bulk_wait_read_0();
+        __syncwarp();
     }
 };
 
@@ -766,6 +799,18 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
     uint32_t aph = 0;
     Unit o;
     Feed feed{c};
+    // The unit whose output this warp has stored but not yet reported.  It is
+    // reported once its stores have landed: while the warp waits for its next
+    // unit, or after two sub-tiles of that one (reporting at the unit's own
+    // end cost 5600 cycles a unit).  Never later: other units wait for it.
+    unsigned int *pending = nullptr;
+    auto report = [&]() {
+        if (pending != nullptr && lane == 0) {
+            fence_proxy_async_all();
+            add_release(pending, 1u);
+        }
+        pending = nullptr;
+    };
     while (feed.next(w, &o)) {
         const int row0 = o.m0 + (int)c.rank * 128 + quarter * 32, row = row0 + lane;
         const int c0 = half * (o.width / 2), c1 = c0 + o.width / 2;
@@ -777,6 +822,10 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
             tgt = p.tgt[row] - o.piece * p.piece_cols - o.n0;     // column of this tile
         }
         for (int part = 0; part < o.parts; ++part) {
+            if (GRAD && pending != nullptr && !__all_sync(0xffffffffu, mbar_try_wait(c.tfull(acc), aph))) {
+                if (lane == 0) bulk_wait_all();
+                report();
+            }
             if (!c.wait(c.tfull(acc), aph)) return;
             tc_fence_after();
             const uint32_t tmem = c.tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kBN);
@@ -785,6 +834,7 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
             } else if (o.type == UNIT_L) {
                 const int n = (int)(p.V - (int64_t)o.piece * p.piece_cols) - o.n0;   // valid columns of this tile
                 const int gcol = (o.piece % p.buffers) * p.piece_cols + o.n0;
+                store.begin_16();
 #pragma unroll 1
                 for (int cc = c0; cc < c1; cc += 32) {
                     uint32_t r[32];
@@ -798,8 +848,13 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
                         if (rfac == 0.0f || cc + i >= n) f[i] = 0.0f;
                     }
                     store.put(&maps.g_out, f, gcol + cc, row0);
+                    if (pending != nullptr && cc == c0 + 32) {
+                        if (lane == 0) bulk_wait<2>();
+                        report();
+                    }
                 }
             } else if (o.type == UNIT_T) {
+                store.begin_16();
 #pragma unroll 1
                 for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 32) {
                     uint32_t r[32];
@@ -813,29 +868,22 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
                 // granule sums of dx: a slot each, or added in place in granule order
                 const int granule = o.piece * (p.piece_cols / kGranule) + o.granule + part;
                 const bool add = p.slots == 1 && granule > 0;
-                if (add && part == 0) {                  // the previous piece's sums
-                    const int q = o.piece - 1;
-                    const bool there = lane != 0 || c.wait_count(p.done_tx + q, kDone * (unsigned)(w.n_t(q) + w.n_x(q)));
-                    if (!__all_sync(0xffffffffu, there)) return;
+                if (add) {                               // the granule before is in memory
+                    if (lane == 0) bulk_wait_all();
+                    report();
+                    if (part == 0) {
+                        const int q = o.piece - 1;
+                        const bool there = lane != 0 || c.wait_count(p.done_tx + q, kDone * (unsigned)(w.n_t(q) + w.n_x(q)));
+                        if (!__all_sync(0xffffffffu, there)) return;
+                        if (lane == 0) fence_proxy_async_all();
+                    }
                 }
-                float *dst = p.acc + ((p.slots > 1 ? (int64_t)granule * p.Mp : 0) + row) * p.D + o.n0;
+                const int arow = (p.slots > 1 ? granule * (int)p.Mp : 0) + row0;
 #pragma unroll 1
                 for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 32) {
                     uint32_t r[32];
                     tmem_ld32(tmem + (uint32_t)cc, r);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        if (o.n0 + cc + i >= p.D ||
-                            !CHK(dst + cc + i - p.acc, 4, (int64_t)p.slots * p.Mp * p.D)) break;   // D is a multiple of 8
-                        float4 v = make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
-                                               __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
-                        float4 *q = reinterpret_cast<float4 *>(dst + cc + i);
-                        if (add) {
-                            const float4 b = __ldcg(q);
-                            v.x = b.x + v.x; v.y = b.y + v.y; v.z = b.z + v.z; v.w = b.w + v.w;
-                        }
-                        __stcg(q, v);
-                    }
+                    store.put_f32(&maps.acc, r, o.n0 + cc, arow, add);
                 }
             }
             tc_fence_before();
@@ -843,17 +891,16 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
             if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(c.tempty(acc), 0));
             if (++acc == 2) { acc = 0; aph ^= 1u; }
         }
-        if (GRAD) {                                       // this warp's part of the output is in memory
-            if (lane == 0) {
-                bulk_wait_all();
-                fence_proxy_async_all();
+        if (GRAD) {
+            if (pending != nullptr) {                     // not reported on the way
+                if (lane == 0) bulk_wait_all();
+                report();
             }
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) add_release((o.type == UNIT_L ? p.done_l : p.done_tx) + o.piece, 1u);
+            pending = (o.type == UNIT_L ? p.done_l : p.done_tx) + o.piece;
         }
     }
     if (lane == 0) bulk_wait_all();
+    report();
 }
 
 template <bool GRAD, bool F16>
@@ -1038,9 +1085,13 @@ cudaError_t launch_tiles(const Plan &p, const void *table, void *dtable, int sms
         const int64_t cols = (int64_t)p.piece_cols * p.buffers;
         if (err == cudaSuccess) err = encode(&maps.g, p.g, cols, p.Mp, 64, CU_TENSOR_MAP_SWIZZLE_128B);
         if (err == cudaSuccess) err = encode(&maps.g_out, p.g, cols, p.Mp, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+        if (err == cudaSuccess)
+            err = encode_tensor_map_2d(&maps.acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.acc, (uint64_t)p.D,
+                                       (uint64_t)(p.Mp * p.slots), (uint64_t)p.D * 4, 32, 32,
+                                       CU_TENSOR_MAP_SWIZZLE_128B);
         if (err == cudaSuccess) err = encode(&maps.dt_out, dtable, p.D, p.V, 32, CU_TENSOR_MAP_SWIZZLE_64B);
     } else {
-        maps.g = maps.g_out = maps.dt_out = maps.x;       // unused
+        maps.g = maps.g_out = maps.dt_out = maps.acc = maps.x;       // unused
     }
     if (err != cudaSuccess) return err;
     auto kern = p.f16 ? xent_tile_kernel<GRAD, true> : xent_tile_kernel<GRAD, false>;
