@@ -122,6 +122,12 @@ cudaError_t encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, co
                                  uint64_t inner, uint64_t outer, uint64_t row_bytes,
                                  uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
 
+// The same for a tensor of 2 or 3 dimensions, innermost first; stride_bytes
+// are those of dimensions 1 and up.
+cudaError_t encode_tensor_map(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint32_t rank,
+                              const uint64_t *extent, const uint64_t *stride_bytes, const uint32_t *box,
+                              CUtensorMapSwizzle swizzle);
+
 // Read and clear the exact tier's device status words (exact_int.cu,
 // exact_tc.cu).
 carbon_status_t exact_take_device_status();

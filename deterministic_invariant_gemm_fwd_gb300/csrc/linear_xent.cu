@@ -48,7 +48,9 @@ constexpr int kSlots = 4;                             // units handed out ahead
 constexpr uint32_t kStagingOffset = kStages * kStageBytes;
 constexpr uint32_t kBarOffset = kStagingOffset + kEpiWarps * 4096;
 constexpr int kBars = 2 * kStages + 4 + 2 * kSlots;
-constexpr uint32_t kSmemBytes = kBarOffset + kBars * 8 + kSlots * 4 + 16 + 1024;
+constexpr uint32_t kUnitOffset = kBarOffset + kBars * 8;
+constexpr uint32_t kSmemBytes = kUnitOffset + kSlots * 32 + 16 + 1024;
+static_assert(kUnitOffset % 16 == 0, "units are read as 16-byte vectors");
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 // epilogue warps of a pair: each adds one to a unit's counter
 constexpr unsigned kDone = 2 * kEpiWarps;
@@ -56,6 +58,12 @@ constexpr unsigned kDone = 2 * kEpiWarps;
 constexpr int kGroup = 128;              // vocabulary entries per (max, sum) pair
 constexpr int kGranule = 4096;           // vocabulary entries per partial sum of dx
 constexpr int kPieceBuffers = 3;         // pieces of G in the workspace
+// G is kept as blocks of 128 positions x 64 entries, each block as 8 planes
+// of 8 entries: plane p holds 16 bytes per position, so that a warp of 32
+// positions writes 512 contiguous bytes a store, straight from its registers.
+// A block is also a shared-memory image of the MMA's unswizzled operand, for
+// either orientation (core matrices of 8 positions x 16 bytes).
+constexpr int kGPlane = 128 * 8, kGBlock = 8 * kGPlane;       // elements
 constexpr int64_t kPieceBytes = 64ll << 20;   // largest piece of G, unless one granule is larger
 constexpr int64_t kSlotBytes = 64ll << 20;    // dx: granule sums side by side up to this size
 // G is formed times 2^k, so that probabilities far below the type's (fp16) or
@@ -278,12 +286,13 @@ xent_gather_kernel(const Plan p, const uint4 *__restrict__ x) {
 
 enum UnitType { UNIT_L = 0, UNIT_T = 1, UNIT_X = 2 };
 
-struct Unit {
+struct alignas(16) Unit {
     int type, piece;
     int m0, n0;              // output tile: first row, first column (rows of the output for T are table rows)
     int width;               // columns, a multiple of 128
     int parts;               // accumulations, one after the other (X: granules)
     int granule;             // X: first granule
+    int left;                // 0: the list has ended
 };
 
 // Phases in list order: L(0), then for each piece p: L(p+1), T and X of p.
@@ -292,66 +301,65 @@ struct Walk {
     int tm;                  // row tiles of positions
     int kept;
     int phase = 0;
-    int64_t base = 0, count = 0;
+    uint32_t base = 0, count = 0;        // the host has checked that the list is shorter than 2^31
 
     __device__ Walk(const Plan &plan, int n) : p(plan), tm(row_tiles(n)), kept(n) { count = size(0); }
 
     __device__ int cols(int piece) const { return min(p.piece_cols, (int)(p.V - (int64_t)piece * p.piece_cols)); }
     // phase 0: L(0); 2q+1: L(q+1) (empty for the last piece); 2q+2: T and X of q
-    __device__ int64_t n_l(int piece) const {
+    __device__ uint32_t n_l(int piece) const {
         const int c = p.grad ? cols(piece) : (int)p.V;
-        return (int64_t)tm * ((c + p.lwidth - 1) / p.lwidth);
+        return (uint32_t)tm * (uint32_t)((c + p.lwidth - 1) / p.lwidth);
     }
-    __device__ int64_t n_t(int piece) const { return (int64_t)((cols(piece) + kBM - 1) / kBM) * p.dtiles; }
+    __device__ uint32_t n_t(int piece) const { return (uint32_t)((cols(piece) + kBM - 1) / kBM) * (uint32_t)p.dtiles; }
     __device__ int granules_of(int piece) const { return (cols(piece) + kGranule - 1) / kGranule; }
-    __device__ int64_t n_x(int piece) const { return (int64_t)tm * p.dtiles * (p.slots > 1 ? granules_of(piece) : 1); }
-    __device__ int64_t size(int ph) const {
+    __device__ uint32_t n_x(int piece) const { return (uint32_t)(tm * p.dtiles) * (uint32_t)(p.slots > 1 ? granules_of(piece) : 1); }
+    __device__ uint32_t size(int ph) const {
         if (ph == 0) return n_l(0);
         if (ph & 1) return (ph + 1) / 2 < p.pieces ? n_l((ph + 1) / 2) : 0;
         const int q = ph / 2 - 1;
         return n_t(q) + n_x(q);
     }
-    // The unit at position u of the list (u never decreases); false past the end.
-    __device__ bool at(int64_t u, Unit *out) {
+    // The unit at position u of the list (u never decreases).
+    __device__ Unit at(uint32_t u) {
         const int last = p.grad ? 2 * p.pieces : 0;
+        Unit o = {};
         while (u >= base + count) {
-            if (phase == last) return false;
+            if (phase == last) return o;
             base += count;
             count = size(++phase);
         }
-        int64_t i = u - base;
-        Unit o;
+        uint32_t i = u - base;
         o.parts = 1;
-        o.granule = 0;
+        o.left = 1;
         if (phase == 0 || (phase & 1)) {
             o.type = UNIT_L;
             o.piece = phase == 0 ? 0 : (phase + 1) / 2;
             const int c = p.grad ? cols(o.piece) : (int)p.V;
-            o.m0 = (int)(i % tm) * kBM;
-            o.n0 = (int)(i / tm) * p.lwidth;
+            o.m0 = (int)(i % (uint32_t)tm) * kBM;
+            o.n0 = (int)(i / (uint32_t)tm) * p.lwidth;
             o.width = min(p.lwidth, (c - o.n0 + 127) / 128 * 128);
         } else {
             o.piece = phase / 2 - 1;
-            const int64_t nt = n_t(o.piece);
+            const uint32_t nt = n_t(o.piece);
             if (i < nt) {
                 o.type = UNIT_T;
             } else {
                 o.type = UNIT_X;
                 i -= nt;
-                const int64_t tiles = (int64_t)tm * p.dtiles;
+                const uint32_t tiles = (uint32_t)(tm * p.dtiles);
                 if (p.slots > 1) {
                     o.granule = (int)(i / tiles);
-                    i -= o.granule * tiles;
+                    i -= (uint32_t)o.granule * tiles;
                 } else {
                     o.parts = granules_of(o.piece);
                 }
             }
-            o.m0 = (int)(i / p.dtiles) * kBM;
-            o.n0 = (int)(i % p.dtiles) * p.dwidth;
+            o.m0 = (int)(i / (uint32_t)p.dtiles) * kBM;
+            o.n0 = (int)(i % (uint32_t)p.dtiles) * p.dwidth;
             o.width = min(p.dwidth, (int)(p.D - o.n0 + 127) / 128 * 128);
         }
-        *out = o;
-        return true;
+        return o;
     }
     // k-blocks of part j of a unit.
     __device__ int k_blocks(const Unit &o, int part) const {
@@ -374,11 +382,7 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap *map, uint32_t src,
                  ::"l"(map), "r"(src), "r"(c0), "r"(c1) : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read_0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-// all but the last n groups have written their data
-template <int N>
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
@@ -433,8 +437,11 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, int a, int b, int c, int d) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, int &a, int &b, int &c, int &d) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -459,6 +466,13 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *m
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4}], [%2];"
         ::"r"(dst), "l"(map), "r"(bar), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void tma_load_pair_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
+                                                 int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2) : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t slot_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -490,23 +504,31 @@ __device__ __forceinline__ uint32_t instr_desc(int n, bool a_mn, bool b_mn, bool
            ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
 }
 
-// Descriptor of the K = 16 slice k of a tile: K-major rows of 128 bytes, or
-// 64-wide blocks whose rows are k (as in the tensor-core GEMM).
-__device__ __forceinline__ uint64_t operand_desc(uint32_t base, bool mn, int k) {
+// Descriptors of the K = 16 slice k of an operand tile.
+// Boxes of 64 x 64 with the 128-byte swizzle: rows of 128 bytes along K, or
+// (mn) 64-wide blocks whose rows are k.
+__device__ __forceinline__ uint64_t box_desc(uint32_t base, bool mn, int k) {
     return mn ? smem_desc(base + (uint32_t)k * 2048u, kBlock, 1024u) : smem_desc(base + (uint32_t)k * 32u, 16u, 1024u);
+}
+// G: planes of 128 positions, K along the planes; or (mn) planes of 64
+// positions, K along the positions (the strides change places).
+__device__ __forceinline__ uint64_t g_desc(uint32_t base, bool mn, int k) {
+    return mn ? smem_desc_noswizzle(base + (uint32_t)k * 256u, 128u, 1024u)
+              : smem_desc_noswizzle(base + (uint32_t)k * 4096u, 2048u, 128u);
 }
 
 // ---- the tile kernel -------------------------------------------------------------------
 
 struct Maps {
-    CUtensorMap x, w, g;        // operand boxes 64 x 64, 128-byte swizzle
-    CUtensorMap g_out, dt_out;  // 32 x 32 store boxes, 64-byte swizzle
-    CUtensorMap acc;            // 32 x 32 fp32 boxes, 128-byte swizzle
+    CUtensorMap x, w;           // operand boxes 64 x 64, 128-byte swizzle
+    CUtensorMap g_x, g_t;       // G: a block; the halves of its planes that hold 64 positions
+    CUtensorMap dt_out;         // store boxes of 32 rows x 64
+    CUtensorMap acc;            // store boxes of 32 rows x 32 fp32
 };
 
 struct Ctx {
     uint32_t sbase, bars, tmem, rank;
-    volatile uint32_t *slots;            // units handed out
+    const Unit *slots;                   // units handed out
     volatile uint32_t *abort_flag;
     __device__ uint32_t full(int s) const { return bars + 8u * s; }                          // used in CTA 0
     __device__ uint32_t empty(int s) const { return bars + 8u * (kStages + s); }
@@ -547,95 +569,86 @@ struct Ctx {
 // Units are handed out in list order, one at a time, to whichever pair asks
 // next (a pair only waits for units that a running pair already has: the
 // kernel makes progress however few of its pairs the GPU runs at once).  One
-// thread of CTA 0 takes them; every role of both CTAs reads them here.
+// thread of CTA 0 takes them and decodes them for every role of both CTAs.
 struct Feed {
     const Ctx &c;
     int slot = 0;
     uint32_t ph = 0;
     // The next unit, for a whole warp.  false: none left, or gave up.  The
-    // shuffle makes the unit warp-uniform to the compiler, so that what the
+    // shuffles make the unit warp-uniform to the compiler, so that what the
     // TMA and MMA instructions take from it lives in uniform registers (with
     // one lane's branch instead, four TMA loads took 570 cycles to issue).
-    __device__ bool next(Walk &w, Unit *o) {
+    __device__ bool next(Unit *o) {
         const bool ok = !c.aborted() && c.wait_cluster(c.sfull(slot), ph);
         if (!__all_sync(0xffffffffu, ok)) return false;
-        const uint32_t u = __shfl_sync(0xffffffffu, c.slots[slot], 0);
-        const bool more = w.at(u, o);             // uses u: the slot has been read
+        int v[8];
+        ld_shared_v4(smem_addr(c.slots + slot), v[0], v[1], v[2], v[3]);
+        ld_shared_v4(smem_addr(c.slots + slot) + 16u, v[4], v[5], v[6], v[7]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);   // uses v: the slot has been read
         if (threadIdx.x % 32 == 0) mbar_arrive_cluster_relaxed(map_rank(c.sempty(slot), 0));
         if (++slot == kSlots) { slot = 0; ph ^= 1u; }
-        return more;
+        *o = Unit{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+        return v[7] != 0;
     }
 };
 // readers of a unit: producers of both CTAs, the MMA issuer, both epilogues
 constexpr int kReaders = 2 + 1 + 2 * kEpiWarps;
 
 __device__ __forceinline__ void hand_out(const Plan &p, Walk w, const Ctx &c) {
-    Unit o;
     int slot = 0;
     uint32_t ph = 0;
     for (bool more = true; more && !c.aborted();) {
+        const Unit o = w.at(atomicAdd(p.ticket, 1u));
         if (!c.wait_cluster(c.sempty(slot), ph ^ 1u)) return;
-        const uint32_t u = atomicAdd(p.ticket, 1u);
-        more = w.at(u, &o);                       // the first one past the end tells the roles to stop
         for (uint32_t r = 0; r < 2; ++r) {
-            st_cluster_u32(map_rank(smem_addr(const_cast<uint32_t *>(c.slots)) + 4u * slot, r), u);
+            const uint32_t to = map_rank(smem_addr(c.slots + slot), r);
+            st_cluster_v4(to, o.type, o.piece, o.m0, o.n0);
+            st_cluster_v4(to + 16u, o.width, o.parts, o.granule, o.left);
             mbar_arrive_cluster(map_rank(c.sfull(slot), r));
         }
+        more = o.left != 0;                       // the first one past the end tells the roles to stop
         if (++slot == kSlots) { slot = 0; ph ^= 1u; }
     }
 }
 
-// What a unit's operands wait for.
-__device__ __forceinline__ bool wait_operands(const Plan &p, const Walk &w, const Unit &o, const Ctx &c) {
-    if (!p.grad) return true;
-    if (o.type == UNIT_L) {                       // its piece's buffer is free
-        const int q = o.piece - p.buffers;
-        return q < 0 || c.wait_count(p.done_tx + q, kDone * (unsigned)(w.n_t(q) + w.n_x(q)));
+// What a unit's operands wait for.  Pieces seen complete are remembered (an
+// acquiring load costs about 1000 cycles).
+struct Ready {
+    int l = -1, tx = -1;                          // last pieces known complete
+    __device__ bool wait(const Plan &p, const Walk &w, const Unit &o, const Ctx &c) {
+        if (!p.grad) return true;
+        if (o.type == UNIT_L) {                   // its piece's buffer is free
+            const int q = o.piece - p.buffers;
+            if (q <= tx) return true;
+            tx = q;
+            return c.wait_count(p.done_tx + q, kDone * (w.n_t(q) + w.n_x(q)));
+        }
+        if (o.piece <= l) return true;
+        l = o.piece;
+        return c.wait_count(p.done_l + o.piece, kDone * w.n_l(o.piece));
     }
-    return c.wait_count(p.done_l + o.piece, kDone * (unsigned)w.n_l(o.piece));
-}
-
-// Loads of one k-block: this CTA's rows of A and columns of B, in boxes of 64.
-// A: coordinates (ax, ay), the boxes (adx, ady) apart; B likewise.
-struct Loads {
-    const CUtensorMap *a, *b;
-    int ax, ay, adx, ady, bx, by, bdx, bdy;
-    int akx, aky, bkx, bky;                   // step per k-block
 };
 
-__device__ __forceinline__ Loads loads_of(const Plan &p, const Maps &maps, const Unit &o, int granule, uint32_t rank) {
-    const int v0 = o.piece * p.piece_cols;
-    const int gcol = p.grad ? (o.piece % p.buffers) * p.piece_cols : 0;
-    const int m0 = o.m0 + (int)rank * 128, n0 = o.n0 + (int)rank * (o.width / 2);
-    const int kc = granule * kGranule;
-    Loads l;
-    if (o.type == UNIT_L) {                   // x and the table, both along D
-        l.a = &maps.x; l.ax = 0; l.ay = m0; l.adx = 0; l.ady = 64; l.akx = kBK; l.aky = 0;
-        l.b = &maps.w; l.bx = 0; l.by = v0 + n0; l.bdx = 0; l.bdy = 64; l.bkx = kBK; l.bky = 0;
-    } else if (o.type == UNIT_T) {            // G^T and x, along the positions
-        l.a = &maps.g; l.ax = gcol + m0; l.ay = 0; l.adx = 64; l.ady = 0; l.akx = 0; l.aky = kBK;
-        l.b = &maps.x; l.bx = n0; l.by = 0; l.bdx = 64; l.bdy = 0; l.bkx = 0; l.bky = kBK;
-    } else {                                  // G and the table, along the vocabulary
-        l.a = &maps.g; l.ax = gcol + kc; l.ay = m0; l.adx = 0; l.ady = 64; l.akx = kBK; l.aky = 0;
-        l.b = &maps.w; l.bx = n0; l.by = v0 + kc; l.bdx = 64; l.bdy = 0; l.bkx = 0; l.bky = kBK;
-    }
-    return l;
-}
-
-// A whole warp runs the loop; one lane issues.
+// A whole warp runs the loop; one lane issues the loads of this CTA's rows of
+// A and columns of B.
 __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w, const Ctx &c) {
     int s = 0;
     uint32_t ph = 0;
     Unit o;
     Feed feed{c};
+    Ready ready;
+    const int gblocks = p.grad ? p.piece_cols * p.buffers / 64 : 0;       // blocks of G per 128 positions
     bool ok = true;
-    while (ok && feed.next(w, &o)) {
-        if (!__all_sync(0xffffffffu, wait_operands(p, w, o, c))) break;
+    while (ok && feed.next(&o)) {
+        if (!__all_sync(0xffffffffu, ready.wait(p, w, o, c))) break;
         fence_proxy_async_all();                  // other CTAs' G, before this CTA's TMA reads
         const bool two = o.width > 128;           // boxes of B per CTA
+        const int v0 = o.piece * p.piece_cols;
+        const int m0 = o.m0 + (int)c.rank * 128, n0 = o.n0 + (int)c.rank * (o.width / 2);
+        const int gcol = p.grad ? (o.piece % p.buffers) * (p.piece_cols / 64) : 0;
         for (int part = 0; ok && part < o.parts; ++part) {
-            Loads l = loads_of(p, maps, o, o.granule + part, c.rank);
-            const int nkb = w.k_blocks(o, part);
+            const int nkb = w.k_blocks(o, part), k0 = (o.granule + part) * kGranule;
             for (int kb = 0; kb < nkb; ++kb) {
                 ok = __all_sync(0xffffffffu, c.wait(c.empty(s), ph ^ 1u));
                 if (!ok) break;
@@ -644,13 +657,25 @@ __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w,
                     const uint32_t bar = map_rank(c.full(s), 0);
                     // both CTAs' bytes
                     if (c.rank == 0) mbar_arrive_expect_tx(c.full(s), two ? 2 * (kABytes + 2 * kBlock) : 2 * (kABytes + kBlock));
-                    tma_load_pair(sa, l.a, bar, l.ax, l.ay);
-                    tma_load_pair(sa + kBlock, l.a, bar, l.ax + l.adx, l.ay + l.ady);
-                    tma_load_pair(sb, l.b, bar, l.bx, l.by);
-                    if (two) tma_load_pair(sb + kBlock, l.b, bar, l.bx + l.bdx, l.by + l.bdy);
+                    if (o.type == UNIT_L) {       // x and the table, both along D
+                        tma_load_pair(sa, &maps.x, bar, kb * kBK, m0);
+                        tma_load_pair(sa + kBlock, &maps.x, bar, kb * kBK, m0 + 64);
+                        tma_load_pair(sb, &maps.w, bar, kb * kBK, v0 + n0);
+                        if (two) tma_load_pair(sb + kBlock, &maps.w, bar, kb * kBK, v0 + n0 + 64);
+                    } else if (o.type == UNIT_T) {    // G^T and x, along the positions
+                        const int blk = (kb / 2) * gblocks + gcol + m0 / 64;
+                        tma_load_pair_3d(sa, &maps.g_t, bar, 0, (kb & 1) * 8, blk * 8);
+                        tma_load_pair_3d(sa + kBlock, &maps.g_t, bar, 0, (kb & 1) * 8, blk * 8 + 8);
+                        tma_load_pair(sb, &maps.x, bar, n0, kb * kBK);
+                        if (two) tma_load_pair(sb + kBlock, &maps.x, bar, n0 + 64, kb * kBK);
+                    } else {                      // G and the table, along the vocabulary
+                        const int blk = (m0 / 128) * gblocks + gcol + k0 / 64 + kb;
+                        tma_load_pair_3d(sa, &maps.g_x, bar, 0, 0, blk * 8);
+                        tma_load_pair(sb, &maps.w, bar, n0, v0 + k0 + kb * kBK);
+                        if (two) tma_load_pair(sb + kBlock, &maps.w, bar, n0 + 64, v0 + k0 + kb * kBK);
+                    }
                 }
                 __syncwarp();
-                l.ax += l.akx; l.ay += l.aky; l.bx += l.bkx; l.by += l.bky;
                 if (++s == kStages) { s = 0; ph ^= 1u; }
             }
         }
@@ -664,8 +689,10 @@ __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w,
 }
 
 // k-blocks of one accumulation.
-template <bool A_MN, bool B_MN>
-__device__ __forceinline__ bool issue_blocks(const Ctx &c, uint32_t d, uint32_t idesc, int nkb, int &s, uint32_t &ph) {
+template <int TYPE>
+__device__ __forceinline__ bool issue_blocks(const Ctx &c, uint32_t d, int width, bool f16, int nkb, int &s, uint32_t &ph) {
+    constexpr bool A_MN = TYPE == UNIT_T, B_MN = TYPE != UNIT_L;
+    const uint32_t idesc = instr_desc(width, A_MN, B_MN, f16);
     for (int kb = 0; kb < nkb; ++kb) {
         if (!__all_sync(0xffffffffu, c.wait(c.full(s), ph))) return false;
         tc_fence_after();
@@ -673,7 +700,8 @@ __device__ __forceinline__ bool issue_blocks(const Ctx &c, uint32_t d, uint32_t 
         if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
-                mma_pair(d, operand_desc(sa, A_MN, k), operand_desc(sb, B_MN, k), idesc, (kb | k) != 0 ? 1u : 0u);
+                mma_pair(d, TYPE == UNIT_L ? box_desc(sa, false, k) : g_desc(sa, A_MN, k), box_desc(sb, B_MN, k), idesc,
+                         (kb | k) != 0 ? 1u : 0u);
             mma_commit_pair(c.empty(s));
         }
         __syncwarp();
@@ -689,7 +717,7 @@ __device__ __forceinline__ void issue(Walk w, const Ctx &c) {
     uint32_t ph = 0, aph = 0;
     Unit o;
     Feed feed{c};
-    while (feed.next(w, &o)) {
+    while (feed.next(&o)) {
         for (int part = 0; part < o.parts; ++part) {
             if (!__all_sync(0xffffffffu, c.wait_cluster(c.tempty(acc), aph ^ 1u))) return;
             tc_fence_after();
@@ -697,11 +725,11 @@ __device__ __forceinline__ void issue(Walk w, const Ctx &c) {
             const int nkb = w.k_blocks(o, part);
             bool ok;
             if (!GRAD || o.type == UNIT_L)
-                ok = issue_blocks<false, false>(c, d, instr_desc(o.width, false, false, F16), nkb, s, ph);
+                ok = issue_blocks<UNIT_L>(c, d, o.width, F16, nkb, s, ph);
             else if (o.type == UNIT_T)
-                ok = issue_blocks<true, true>(c, d, instr_desc(o.width, true, true, F16), nkb, s, ph);
+                ok = issue_blocks<UNIT_T>(c, d, o.width, F16, nkb, s, ph);
             else
-                ok = issue_blocks<false, true>(c, d, instr_desc(o.width, false, true, F16), nkb, s, ph);
+                ok = issue_blocks<UNIT_X>(c, d, o.width, F16, nkb, s, ph);
             if (!ok) return;
             if (elect_one()) mma_commit_pair(c.tfull(acc));
             __syncwarp();
@@ -710,52 +738,54 @@ __device__ __forceinline__ void issue(Walk w, const Ctx &c) {
     }
 }
 
-// 32 x 32 sub-tiles to global memory through a warp's staging buffer (4 KiB:
-// two 16-bit sub-tiles or one of fp32).
-template <bool F16>
-struct Store {
-    uint32_t stg;
-    int lane, n = 0;
-    __device__ void put(const CUtensorMap *map, const float (&f)[32], int col, int row) {
-        const uint32_t buf = stg + (uint32_t)(n & 1) * 2048u;
-        if (lane == 0) bulk_wait_read_1();                // the sub-tile before the last has left
-        __syncwarp();
+// 32 lanes x 64 columns of 32-bit: thread t of the warp receives lane (base
+// lane + t).  One statement with its wait: no use of v can move above it.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        :
+          "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+          "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]),
+          "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]),
+          "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
+          "=r"(v[30]), "=r"(v[31]), "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]),
+          "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]), "=r"(v[41]),
+          "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
+          "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]),
+          "=r"(v[54]), "=r"(v[55]), "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]),
+          "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
+        : "r"(taddr) : "memory");
+}
+
+// Sub-tiles of 32 rows x 128 bytes (64 16-bit columns or 32 of fp32) to
+// global memory through the warp's 4 KiB staging buffer.  A lane holds a row;
+// its 16-byte pieces lie as the 128-byte swizzle expects them.  The elected
+// lane, the same one each time, issues every copy and waits for them.
+__device__ __forceinline__ void staging_free() {
+    if (elect_one()) bulk_wait_read_0();
+    __syncwarp();
+}
+__device__ __forceinline__ void put_rows(uint32_t stg, int lane, const CUtensorMap *map, const uint32_t *r, int col,
+                                         int row, bool add) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g)                       // 16-byte pieces as the 64-byte swizzle expects them
-            st_shared_v4(buf + lane * 64 + 16 * (g ^ ((lane >> 1) & 3)),
-                         make_uint4(pack2<F16>(f[8 * g], f[8 * g + 1]), pack2<F16>(f[8 * g + 2], f[8 * g + 3]),
-                                    pack2<F16>(f[8 * g + 4], f[8 * g + 5]), pack2<F16>(f[8 * g + 6], f[8 * g + 7])));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(map, buf, col, row);
-            bulk_commit();
-        }
-        ++n;
+    for (int g = 0; g < 8; ++g)
+        st_shared_v4(stg + lane * 128 + 16 * (g ^ (lane & 7)),
+                     make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]));
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (elect_one()) {
+        if (add) tma_add_2d(map, stg, col, row);
+        else tma_store_2d(map, stg, col, row);
+        bulk_commit();
     }
-    // fp32, stored or added to what is there
-    __device__ void put_f32(const CUtensorMap *map, const uint32_t (&r)[32], int col, int row, bool add) {
-        if (lane == 0) bulk_wait_read_0();
-        __syncwarp();
-#pragma unroll
-        for (int g = 0; g < 8; ++g)                       // 128-byte swizzle
-            st_shared_v4(stg + lane * 128 + 16 * (g ^ (lane & 7)),
-                         make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if (add) tma_add_2d(map, stg, col, row);
-            else tma_store_2d(map, stg, col, row);
-            bulk_commit();
-        }
-        n = 0;                                            // the next 16-bit sub-tile goes to the first half
-    }
-    // After an fp32 sub-tile both halves are in use until it has left.
-    __device__ void begin_16() {
-        if (lane == 0) bulk_wait_read_0();
-        __syncwarp();
-    }
-};
+    __syncwarp();
+}
 
 // Loss: (max, sum) pairs and the targets' logits of this thread's row.
 __device__ __forceinline__ void loss_rows(const Plan &p, const Unit &o, uint32_t tmem, int row, int half) {
@@ -790,9 +820,9 @@ __device__ __forceinline__ void loss_rows(const Plan &p, const Unit &o, uint32_t
 }
 
 template <bool GRAD, bool F16>
-__device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w, const Ctx &c, int warp, int lane) {
+__device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const Walk w, const Ctx &c, int warp, int lane) {
     const int quarter = warp % 4, half = (warp - 4) / 4;  // 32 rows; one half of the columns
-    Store<F16> store{c.sbase + kStagingOffset + (uint32_t)(warp - 4) * 4096u, lane};
+    const uint32_t stg = c.sbase + kStagingOffset + (uint32_t)(warp - 4) * 4096u;
     const float gscale = GRAD ? p.head->gscale : 0.0f;
     constexpr float kOne = (float)(1ull << (F16 ? kScaleBits16 : kScaleBitsBf));
     int acc = 0;
@@ -801,17 +831,21 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
     Feed feed{c};
     // The unit whose output this warp has stored but not yet reported.  It is
     // reported once its stores have landed: while the warp waits for its next
-    // unit, or after two sub-tiles of that one (reporting at the unit's own
-    // end cost 5600 cycles a unit).  Never later: other units wait for it.
+    // unit, or after the first sub-tile of that one (reporting at the unit's
+    // own end cost 5600 cycles a unit).  Never later: other units wait for it.
     unsigned int *pending = nullptr;
     auto report = [&]() {
-        if (pending != nullptr && lane == 0) {
+        if (pending == nullptr) return;
+        __syncwarp();
+        if (elect_one()) {
+            bulk_wait_all();
             fence_proxy_async_all();
             add_release(pending, 1u);
         }
+        __syncwarp();
         pending = nullptr;
     };
-    while (feed.next(w, &o)) {
+    while (feed.next(&o)) {
         const int row0 = o.m0 + (int)c.rank * 128 + quarter * 32, row = row0 + lane;
         const int c0 = half * (o.width / 2), c1 = c0 + o.width / 2;
         float lse2 = 0.0f, rfac = 0.0f;
@@ -822,68 +856,89 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
             tgt = p.tgt[row] - o.piece * p.piece_cols - o.n0;     // column of this tile
         }
         for (int part = 0; part < o.parts; ++part) {
-            if (GRAD && pending != nullptr && !__all_sync(0xffffffffu, mbar_try_wait(c.tfull(acc), aph))) {
-                if (lane == 0) bulk_wait_all();
-                report();
-            }
-            if (!c.wait(c.tfull(acc), aph)) return;
+            if (GRAD && pending != nullptr && !__all_sync(0xffffffffu, mbar_try_wait(c.tfull(acc), aph))) report();
+            if (!__all_sync(0xffffffffu, c.wait(c.tfull(acc), aph))) return;
             tc_fence_after();
             const uint32_t tmem = c.tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kBN);
             if (!GRAD) {
                 loss_rows(p, o, tmem, row, half);
             } else if (o.type == UNIT_L) {
                 const int n = (int)(p.V - (int64_t)o.piece * p.piece_cols) - o.n0;   // valid columns of this tile
-                const int gcol = (o.piece % p.buffers) * p.piece_cols + o.n0;
-                store.begin_16();
+                // this row's place in plane 0 of the first block
+                uint16_t *g_row = static_cast<uint16_t *>(p.g) +
+                    ((int64_t)(row0 / 128) * (p.piece_cols * p.buffers / 64) + ((o.piece % p.buffers) * p.piece_cols + o.n0) / 64) * kGBlock +
+                    (row % 128) * 8;
+                const bool dead = rfac == 0.0f;          // no position, or none of its gradient
 #pragma unroll 1
-                for (int cc = c0; cc < c1; cc += 32) {
-                    uint32_t r[32];
-                    float f[32];
-                    tmem_ld32(tmem + (uint32_t)cc, r);
+                for (int cc = c0; cc < c1; cc += 64) {
+                    uint32_t r[64], g[32];
+                    tmem_ld64(tmem + (uint32_t)cc, r);
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)          // 2^k P
+                        r[i] = __float_as_uint(ex2(fmaf(__uint_as_float(r[i]), kLog2e, -lse2)));
+                    if (__any_sync(0xffffffffu, (unsigned)(tgt - cc) < 64u)) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (cc + i == tgt) r[i] = __float_as_uint(__uint_as_float(r[i]) - kOne);
+                    }
+                    if (cc + 64 > n) {                    // past the vocabulary: exactly zero
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (cc + i >= n) r[i] = 0u;
+                    }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float e = ex2(fmaf(__uint_as_float(r[i]), kLog2e, -lse2));   // 2^k P
-                        f[i] = (cc + i == tgt ? e - kOne : e) * rfac;
-                        // no position, or no such entry: exactly zero, whatever z is
-                        if (rfac == 0.0f || cc + i >= n) f[i] = 0.0f;
+                        g[i] = pack2<F16>(__uint_as_float(r[2 * i]) * rfac, __uint_as_float(r[2 * i + 1]) * rfac);
+                        if (dead) g[i] = 0u;              // whatever z is
                     }
-                    store.put(&maps.g_out, f, gcol + cc, row0);
-                    if (pending != nullptr && cc == c0 + 32) {
-                        if (lane == 0) bulk_wait<2>();
-                        report();
-                    }
+                    uint16_t *dst = g_row + (int64_t)(cc / 64) * kGBlock;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (CHK(dst + q * kGPlane - static_cast<uint16_t *>(p.g), 8, p.Mp * p.piece_cols * p.buffers))
+                            *reinterpret_cast<uint4 *>(dst + q * kGPlane) =
+                                make_uint4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]);
+                    if (cc == c0) report();
                 }
             } else if (o.type == UNIT_T) {
-                store.begin_16();
 #pragma unroll 1
-                for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 32) {
-                    uint32_t r[32];
-                    float f[32];
-                    tmem_ld32(tmem + (uint32_t)cc, r);
+                for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 64) {
+                    uint32_t r[64], g[32];
+                    tmem_ld64(tmem + (uint32_t)cc, r);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]) * gscale;
-                    store.put(&maps.dt_out, f, o.n0 + cc, o.piece * p.piece_cols + row0);
+                    for (int i = 0; i < 32; ++i)
+                        g[i] = pack2<F16>(__uint_as_float(r[2 * i]) * gscale, __uint_as_float(r[2 * i + 1]) * gscale);
+                    staging_free();
+                    put_rows(stg, lane, &maps.dt_out, g, o.n0 + cc, o.piece * p.piece_cols + row0, false);
+                    report();
                 }
             } else {
                 // granule sums of dx: a slot each, or added in place in granule order
                 const int granule = o.piece * (p.piece_cols / kGranule) + o.granule + part;
                 const bool add = p.slots == 1 && granule > 0;
                 if (add) {                               // the granule before is in memory
-                    if (lane == 0) bulk_wait_all();
                     report();
-                    if (part == 0) {
+                    if (part > 0) {
+                        if (elect_one()) bulk_wait_all();
+                        __syncwarp();
+                    } else {
                         const int q = o.piece - 1;
-                        const bool there = lane != 0 || c.wait_count(p.done_tx + q, kDone * (unsigned)(w.n_t(q) + w.n_x(q)));
+                        const bool there = c.wait_count(p.done_tx + q, kDone * (unsigned)(w.n_t(q) + w.n_x(q)));
                         if (!__all_sync(0xffffffffu, there)) return;
-                        if (lane == 0) fence_proxy_async_all();
+                        fence_proxy_async_all();
                     }
                 }
                 const int arow = (p.slots > 1 ? granule * (int)p.Mp : 0) + row0;
 #pragma unroll 1
-                for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 32) {
-                    uint32_t r[32];
-                    tmem_ld32(tmem + (uint32_t)cc, r);
-                    store.put_f32(&maps.acc, r, o.n0 + cc, arow, add);
+                for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 64) {
+                    uint32_t r[64];
+                    tmem_ld64(tmem + (uint32_t)cc, r);
+                    staging_free();
+                    put_rows(stg, lane, &maps.acc, r, o.n0 + cc, arow, add);
+                    if (o.n0 + cc + 32 < p.D) {
+                        staging_free();
+                        put_rows(stg, lane, &maps.acc, r + 32, o.n0 + cc + 32, arow, add);
+                    }
+                    report();
                 }
             }
             tc_fence_before();
@@ -892,15 +947,11 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, Walk w
             if (++acc == 2) { acc = 0; aph ^= 1u; }
         }
         if (GRAD) {
-            if (pending != nullptr) {                     // not reported on the way
-                if (lane == 0) bulk_wait_all();
-                report();
-            }
+            report();                                 // a unit without a sub-tile of this warp's
             pending = (o.type == UNIT_L ? p.done_l : p.done_tx) + o.piece;
         }
     }
-    if (lane == 0) bulk_wait_all();
-    report();
+    if (GRAD) report();
 }
 
 template <bool GRAD, bool F16>
@@ -909,14 +960,14 @@ xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint32_t *words = reinterpret_cast<uint32_t *>(smem + kBarOffset + kBars * 8);
+    uint32_t *words = reinterpret_cast<uint32_t *>(smem + kUnitOffset + kSlots * sizeof(Unit));
     Ctx c;
     c.sbase = smem_addr(smem);
     c.bars = c.sbase + kBarOffset;
     c.rank = cluster_rank();
-    c.slots = words;
-    c.abort_flag = words + kSlots;
-    uint32_t *tmem_slot = words + kSlots + 1;
+    c.slots = reinterpret_cast<const Unit *>(smem + kUnitOffset);
+    c.abort_flag = words;
+    uint32_t *tmem_slot = words + 1;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;   // warp-uniform
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -954,6 +1005,7 @@ xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan
         if (lane == 0 && c.rank == 0) hand_out(p, w, c);
     } else if (warp >= 4) {
         epilogue<GRAD, F16>(p, maps, w, c, warp, lane);
+        if (elect_one()) bulk_wait_all();                  // also after giving up: no copy reads a CTA that has left
     }
     tc_fence_before();
     __syncthreads();
@@ -1051,9 +1103,11 @@ xent_dx_kernel(const Plan p, T *__restrict__ dx) {
 
 // ---- host side ----------------------------------------------------------------
 
-cudaError_t encode(CUtensorMap *m, const void *base, int64_t inner, int64_t outer, int box, CUtensorMapSwizzle sw) {
+// 16-bit elements, 128-byte swizzle.
+cudaError_t encode(CUtensorMap *m, const void *base, int64_t inner, int64_t outer, int box_inner, int box_outer) {
     return encode_tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, (uint64_t)inner, (uint64_t)outer,
-                                (uint64_t)inner * 2, (uint32_t)box, (uint32_t)box, sw);
+                                (uint64_t)inner * 2, (uint32_t)box_inner, (uint32_t)box_outer,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool sizes_ok(int64_t M, int64_t D, int64_t V) {
@@ -1076,22 +1130,36 @@ carbon_status_t check(const void *x, const void *table, const int64_t *targets, 
     return CARBON_OK;
 }
 
+// The list of units is counted in 32 bits.
+bool list_fits(const Plan &p) {
+    const int64_t tm = p.Mp / kBM, l = (p.V + 127) / 128, t = (p.V + kBM - 1) / kBM + p.pieces;
+    return tm * (l + p.pieces) + (t + tm * p.granules) * p.dtiles < (1ll << 31);
+}
+
 template <bool GRAD>
 cudaError_t launch_tiles(const Plan &p, const void *table, void *dtable, int sms, cudaStream_t s) {
     Maps maps;
-    cudaError_t err = encode(&maps.x, p.xc, p.D, p.Mp, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (err == cudaSuccess) err = encode(&maps.w, table, p.D, p.V, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    cudaError_t err = encode(&maps.x, p.xc, p.D, p.Mp, 64, 64);
+    if (err == cudaSuccess) err = encode(&maps.w, table, p.D, p.V, 64, 64);
     if (GRAD) {
-        const int64_t cols = (int64_t)p.piece_cols * p.buffers;
-        if (err == cudaSuccess) err = encode(&maps.g, p.g, cols, p.Mp, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-        if (err == cudaSuccess) err = encode(&maps.g_out, p.g, cols, p.Mp, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+        // G as [planes][16 groups of 8 positions][64 elements]
+        const uint64_t planes = (uint64_t)(p.Mp * p.piece_cols * p.buffers / kGPlane);
+        const uint64_t extent[3] = {64, 16, planes}, stride[2] = {128, 2048};
+        const uint32_t whole[3] = {64, 16, 8}, half[3] = {64, 8, 8};
+        if (planes >= (1ull << 31)) return cudaErrorInvalidValue;
+        if (err == cudaSuccess)
+            err = encode_tensor_map(&maps.g_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.g, 3, extent, stride, whole,
+                                    CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (err == cudaSuccess)
+            err = encode_tensor_map(&maps.g_t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.g, 3, extent, stride, half,
+                                    CU_TENSOR_MAP_SWIZZLE_NONE);
         if (err == cudaSuccess)
             err = encode_tensor_map_2d(&maps.acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.acc, (uint64_t)p.D,
                                        (uint64_t)(p.Mp * p.slots), (uint64_t)p.D * 4, 32, 32,
                                        CU_TENSOR_MAP_SWIZZLE_128B);
-        if (err == cudaSuccess) err = encode(&maps.dt_out, dtable, p.D, p.V, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+        if (err == cudaSuccess) err = encode(&maps.dt_out, dtable, p.D, p.V, 64, 32);
     } else {
-        maps.g = maps.g_out = maps.dt_out = maps.acc = maps.x;       // unused
+        maps.g_x = maps.g_t = maps.dt_out = maps.acc = maps.x;       // unused
     }
     if (err != cudaSuccess) return err;
     auto kern = p.f16 ? xent_tile_kernel<GRAD, true> : xent_tile_kernel<GRAD, false>;
@@ -1155,6 +1223,7 @@ carbon_status_t carbon_linear_xent_fwd(float *losses, float *total, float *lse, 
     }
     Plan p;
     make_plan(&p, align128(workspace), M, D, V, false, dtype == CARBON_F16);
+    if (!list_fits(p)) return CARBON_ERR_INVALID_ARG;
     ScanArgs a = {};
     a.targets = targets; a.ignore_index = ignore_index; a.reduction = reduction;
     a.losses = losses; a.lse_out = lse; a.count = count;
@@ -1191,6 +1260,7 @@ carbon_status_t carbon_linear_xent_bwd(void *dx, void *dtable, const float *grad
     if (M == 0) return note_cuda(cudaMemsetAsync(dtable, 0, (size_t)(V * D) * 2, s));
     Plan p;
     make_plan(&p, align128(workspace), M, D, V, true, dtype == CARBON_F16);
+    if (!list_fits(p)) return CARBON_ERR_INVALID_ARG;
     ScanArgs a = {};
     a.targets = targets; a.ignore_index = ignore_index; a.reduction = reduction;
     a.grad = grad; a.lse_in = lse;

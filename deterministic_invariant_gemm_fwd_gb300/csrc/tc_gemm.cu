@@ -826,19 +826,32 @@ cudaError_t get_encoder() {
 
 }  // namespace
 
-cudaError_t encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base,
-                                 uint64_t inner, uint64_t outer, uint64_t row_bytes,
-                                 uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+cudaError_t encode_tensor_map(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint32_t rank,
+                              const uint64_t *extent, const uint64_t *stride_bytes, const uint32_t *box,
+                              CUtensorMapSwizzle swizzle) {
     const cudaError_t err = get_encoder();
     if (err != cudaSuccess) return err;
-    cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-    cuuint32_t box[2] = {box_inner, box_outer};
-    cuuint32_t estr[2] = {1u, 1u};
-    const CUresult r = g_encode(map, dtype, 2, const_cast<void *>(base), dims, strides, box, estr,
+    cuuint64_t dims[3], strides[2];
+    cuuint32_t boxes[3], estr[3];
+    if (rank < 2 || rank > 3) return cudaErrorInvalidValue;
+    for (uint32_t i = 0; i < rank; ++i) {
+        dims[i] = (cuuint64_t)extent[i];
+        boxes[i] = (cuuint32_t)box[i];
+        estr[i] = 1u;
+        if (i > 0) strides[i - 1] = (cuuint64_t)stride_bytes[i - 1];
+    }
+    const CUresult r = g_encode(map, dtype, rank, const_cast<void *>(base), dims, strides, boxes, estr,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base,
+                                 uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                                 uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+    const uint64_t extent[2] = {inner, outer};
+    const uint32_t box[2] = {box_inner, box_outer};
+    return encode_tensor_map(map, dtype, base, 2, extent, &row_bytes, box, swizzle);
 }
 
 carbon_status_t tc_take_device_status() {
