@@ -40,20 +40,19 @@ __device__ unsigned int g_xent_status = 0;
 constexpr int kBM = 256, kBN = 256, kBK = 64;        // a CTA pair's tile; each CTA has 128 rows
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (4 + kEpiWarps);        // TMA producer, MMA issuer, scheduler, (idle), epilogue
+constexpr int kThreads = 32 * (4 + kEpiWarps);        // TMA producer, MMA issuer, scheduler, reporter, epilogue
 constexpr uint32_t kBlock = 64 * kBK * 2;             // one 64 x 64 box: 8 KiB
 constexpr uint32_t kABytes = 128 * kBK * 2;           // per CTA: 128 rows of A, half of B's columns
 constexpr uint32_t kStageBytes = kABytes + kBN / 2 * kBK * 2;
-constexpr int kSlots = 4;                             // units handed out ahead
+constexpr int kSlots = 6;                             // units handed out ahead
 constexpr uint32_t kStagingOffset = kStages * kStageBytes;
 constexpr uint32_t kBarOffset = kStagingOffset + kEpiWarps * 4096;
-constexpr int kBars = 2 * kStages + 4 + 2 * kSlots;
+constexpr int kBars = 2 * kStages + 4 + 3 * kSlots;
 constexpr uint32_t kUnitOffset = kBarOffset + kBars * 8;
 constexpr uint32_t kSmemBytes = kUnitOffset + kSlots * 32 + 16 + 1024;
 static_assert(kUnitOffset % 16 == 0, "units are read as 16-byte vectors");
 static_assert(kSmemBytes <= 232448, "shared memory per block");
-// epilogue warps of a pair: each adds one to a unit's counter
-constexpr unsigned kDone = 2 * kEpiWarps;
+constexpr unsigned kDone = 2;                         // reports of a finished unit: one per CTA
 
 constexpr int kGroup = 128;              // vocabulary entries per (max, sum) pair
 constexpr int kGranule = 4096;           // vocabulary entries per partial sum of dx
@@ -536,6 +535,7 @@ struct Ctx {
     __device__ uint32_t tempty(int b) const { return bars + 8u * (2 * kStages + 2 + b); }    // used in CTA 0
     __device__ uint32_t sfull(int s) const { return bars + 8u * (2 * kStages + 4 + s); }
     __device__ uint32_t sempty(int s) const { return bars + 8u * (2 * kStages + 4 + kSlots + s); }   // CTA 0
+    __device__ uint32_t stored(int s) const { return bars + 8u * (2 * kStages + 4 + 2 * kSlots + s); }
     __device__ bool wait(uint32_t bar, uint32_t parity) const {
         if (mbar_wait(bar, parity)) return true;
         give_up();
@@ -586,14 +586,22 @@ struct Feed {
         ld_shared_v4(smem_addr(c.slots + slot) + 16u, v[4], v[5], v[6], v[7]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);   // uses v: the slot has been read
-        if (threadIdx.x % 32 == 0) mbar_arrive_cluster_relaxed(map_rank(c.sempty(slot), 0));
-        if (++slot == kSlots) { slot = 0; ph ^= 1u; }
         *o = Unit{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
         return v[7] != 0;
     }
+    // The slot may be used again.
+    __device__ void release() {
+        if (threadIdx.x % 32 == 0) mbar_arrive_cluster_relaxed(map_rank(c.sempty(slot), 0));
+        if (++slot == kSlots) { slot = 0; ph ^= 1u; }
+    }
+    __device__ bool take(Unit *o) {
+        const bool more = next(o);
+        release();
+        return more;
+    }
 };
-// readers of a unit: producers of both CTAs, the MMA issuer, both epilogues
-constexpr int kReaders = 2 + 1 + 2 * kEpiWarps;
+// readers of a unit: producers of both CTAs, the MMA issuer, both reporters and epilogues
+constexpr int kReaders = 2 + 1 + 2 + 2 * kEpiWarps;
 
 __device__ __forceinline__ void hand_out(const Plan &p, Walk w, const Ctx &c) {
     int slot = 0;
@@ -640,7 +648,7 @@ __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w,
     Ready ready;
     const int gblocks = p.grad ? p.piece_cols * p.buffers / 64 : 0;       // blocks of G per 128 positions
     bool ok = true;
-    while (ok && feed.next(&o)) {
+    while (ok && feed.take(&o)) {
         if (!__all_sync(0xffffffffu, ready.wait(p, w, o, c))) break;
         fence_proxy_async_all();                  // other CTAs' G, before this CTA's TMA reads
         const bool two = o.width > 128;           // boxes of B per CTA
@@ -717,7 +725,7 @@ __device__ __forceinline__ void issue(Walk w, const Ctx &c) {
     uint32_t ph = 0, aph = 0;
     Unit o;
     Feed feed{c};
-    while (feed.next(&o)) {
+    while (feed.take(&o)) {
         for (int part = 0; part < o.parts; ++part) {
             if (!__all_sync(0xffffffffu, c.wait_cluster(c.tempty(acc), aph ^ 1u))) return;
             tc_fence_after();
@@ -829,23 +837,9 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
     uint32_t aph = 0;
     Unit o;
     Feed feed{c};
-    // The unit whose output this warp has stored but not yet reported.  It is
-    // reported once its stores have landed: while the warp waits for its next
-    // unit, or after the first sub-tile of that one (reporting at the unit's
-    // own end cost 5600 cycles a unit).  Never later: other units wait for it.
-    unsigned int *pending = nullptr;
-    auto report = [&]() {
-        if (pending == nullptr) return;
-        __syncwarp();
-        if (elect_one()) {
-            bulk_wait_all();
-            fence_proxy_async_all();
-            add_release(pending, 1u);
-        }
-        __syncwarp();
-        pending = nullptr;
-    };
-    while (feed.next(&o)) {
+    for (;;) {
+        const int slot = feed.slot;
+        if (!feed.take(&o)) return;
         const int row0 = o.m0 + (int)c.rank * 128 + quarter * 32, row = row0 + lane;
         const int c0 = half * (o.width / 2), c1 = c0 + o.width / 2;
         float lse2 = 0.0f, rfac = 0.0f;
@@ -856,7 +850,6 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
             tgt = p.tgt[row] - o.piece * p.piece_cols - o.n0;     // column of this tile
         }
         for (int part = 0; part < o.parts; ++part) {
-            if (GRAD && pending != nullptr && !__all_sync(0xffffffffu, mbar_try_wait(c.tfull(acc), aph))) report();
             if (!__all_sync(0xffffffffu, c.wait(c.tfull(acc), aph))) return;
             tc_fence_after();
             const uint32_t tmem = c.tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kBN);
@@ -897,7 +890,6 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
                         if (CHK(dst + q * kGPlane - static_cast<uint16_t *>(p.g), 8, p.Mp * p.piece_cols * p.buffers))
                             *reinterpret_cast<uint4 *>(dst + q * kGPlane) =
                                 make_uint4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]);
-                    if (cc == c0) report();
                 }
             } else if (o.type == UNIT_T) {
 #pragma unroll 1
@@ -909,14 +901,12 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
                         g[i] = pack2<F16>(__uint_as_float(r[2 * i]) * gscale, __uint_as_float(r[2 * i + 1]) * gscale);
                     staging_free();
                     put_rows(stg, lane, &maps.dt_out, g, o.n0 + cc, o.piece * p.piece_cols + row0, false);
-                    report();
                 }
             } else {
                 // granule sums of dx: a slot each, or added in place in granule order
                 const int granule = o.piece * (p.piece_cols / kGranule) + o.granule + part;
                 const bool add = p.slots == 1 && granule > 0;
                 if (add) {                               // the granule before is in memory
-                    report();
                     if (part > 0) {
                         if (elect_one()) bulk_wait_all();
                         __syncwarp();
@@ -938,7 +928,6 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
                         staging_free();
                         put_rows(stg, lane, &maps.acc, r + 32, o.n0 + cc + 32, arow, add);
                     }
-                    report();
                 }
             }
             tc_fence_before();
@@ -946,12 +935,28 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
             if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(c.tempty(acc), 0));
             if (++acc == 2) { acc = 0; aph ^= 1u; }
         }
-        if (GRAD) {
-            report();                                 // a unit without a sub-tile of this warp's
-            pending = (o.type == UNIT_L ? p.done_l : p.done_tx) + o.piece;
+        if (GRAD) {                                       // this warp's part has been stored
+            if (o.type != UNIT_L && elect_one()) bulk_wait_all();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.stored(slot));
         }
     }
-    if (GRAD) report();
+}
+
+// A warp of its own reports finished units, so that the epilogue does not
+// wait for its stores to land (5600 cycles a unit when it did).  It holds the
+// unit's slot until it has reported, so at most kSlots units are unreported.
+__device__ __forceinline__ void report(const Plan &p, const Ctx &c) {
+    Unit o;
+    Feed feed{c};
+    while (feed.next(&o)) {
+        if (!__all_sync(0xffffffffu, c.wait(c.stored(feed.slot), feed.ph))) return;
+        if (elect_one()) {
+            fence_proxy_async_all();                      // G is read by TMA
+            add_release((o.type == UNIT_L ? p.done_l : p.done_tx) + o.piece, 1u);
+        }
+        feed.release();
+    }
 }
 
 template <bool GRAD, bool F16>
@@ -980,7 +985,8 @@ xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan
         }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(c.sfull(s), 1);
-            mbar_init(c.sempty(s), kReaders);
+            mbar_init(c.sempty(s), GRAD ? kReaders : kReaders - 2);
+            mbar_init(c.stored(s), kEpiWarps);
         }
         *c.abort_flag = 0u;
         fence_mbar_init();
@@ -1003,7 +1009,9 @@ xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan
         if (c.rank == 0) issue<GRAD, F16>(w, c);
     } else if (warp == 2) {
         if (lane == 0 && c.rank == 0) hand_out(p, w, c);
-    } else if (warp >= 4) {
+    } else if (warp == 3) {
+        if (GRAD) report(p, c);
+    } else {
         epilogue<GRAD, F16>(p, maps, w, c, warp, lane);
         if (elect_one()) bulk_wait_all();                  // also after giving up: no copy reads a CTA that has left
     }
