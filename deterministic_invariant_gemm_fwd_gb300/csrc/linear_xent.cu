@@ -57,12 +57,13 @@ constexpr unsigned kDone = 2;                         // reports of a finished u
 constexpr int kGroup = 128;              // vocabulary entries per (max, sum) pair
 constexpr int kGranule = 4096;           // vocabulary entries per partial sum of dx
 constexpr int kPieceBuffers = 3;         // pieces of G in the workspace
-// G is kept as blocks of 128 positions x 64 entries, each block as 8 planes
-// of 8 entries: plane p holds 16 bytes per position, so that a warp of 32
-// positions writes 512 contiguous bytes a store, straight from its registers.
-// A block is also a shared-memory image of the MMA's unswizzled operand, for
-// either orientation (core matrices of 8 positions x 16 bytes).
-constexpr int kGPlane = 128 * 8, kGBlock = 8 * kGPlane;       // elements
+// x and G are kept as blocks of 128 positions x 64 columns, each block as 8
+// planes of 8 columns: a plane holds 16 bytes per position, so that a warp of
+// 32 positions writes 512 contiguous bytes a store, straight from its
+// registers, and a block is loaded as contiguous bytes.  It is also a
+// shared-memory image of the MMA's unswizzled operand, for either orientation
+// (core matrices of 8 positions x 16 bytes).
+constexpr int kPlane = 128 * 8, kPlanes = 8 * kPlane;         // elements of a plane, of a block
 constexpr int64_t kPieceBytes = 64ll << 20;   // largest piece of G, unless one granule is larger
 constexpr int64_t kSlotBytes = 64ll << 20;    // dx: granule sums side by side up to this size
 // G is formed times 2^k, so that probabilities far below the type's (fp16) or
@@ -82,6 +83,7 @@ struct Plan {
     int64_t M, Mp, D, V;                 // Mp: M rounded up to a tile's rows, at least one tile
     int vocab_groups;                    // pairs per row
     int dtiles, dwidth;                  // column tiles of dx and dtable
+    int xblocks;                         // blocks of x per 128 positions
     int lwidth;                          // vocabulary entries per L unit
     int pieces, buffers, piece_cols;
     int granules;
@@ -135,7 +137,8 @@ int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, bool gra
     p.rowmap = reinterpret_cast<int *>(take(4 * p.Mp));
     p.inverse = reinterpret_cast<int *>(take(4 * p.Mp));
     p.tgt = reinterpret_cast<int *>(take(4 * p.Mp));
-    p.xc = take(2 * p.Mp * D);
+    p.xblocks = (int)((D + 63) / 64);
+    p.xc = take(2 * p.Mp * p.xblocks * 64);
     if (grad) {
         p.lse2 = reinterpret_cast<float *>(take(4 * p.Mp));
         p.rfac = reinterpret_cast<float *>(take(4 * p.Mp));
@@ -264,21 +267,26 @@ xent_scan_kernel(const Plan p, const ScanArgs a) {
 
 __device__ __forceinline__ int row_tiles(int kept) { return kept > kBM ? (kept + kBM - 1) / kBM : 1; }
 
-// Dense rows of x; zeros up to the last tile's end.  A warp per row.
-__global__ void __launch_bounds__(256)
+// Dense rows of x in blocks; zeros up to the last tile's end and past D.  A
+// warp per 32 positions and 64 columns: lane = position, so the reads are 16
+// bytes of 32 rows (their lines stay in L1), the writes contiguous.
+__global__ void __launch_bounds__(128)
 xent_gather_kernel(const Plan p, const uint4 *__restrict__ x) {
     wait_prior_grid();
     allow_next_grid();
-    const int lane = threadIdx.x % 32;
-    const int64_t nvec = p.D / 8;
     const int64_t rows = (int64_t)row_tiles(p.head->kept) * kBM;
-    const int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    if (i >= rows) return;
-    const int64_t src = p.rowmap[i];
-    uint4 *dst = static_cast<uint4 *>(p.xc) + i * nvec;
-#pragma unroll 4
-    for (int64_t v = lane; v < nvec; v += 32)
-        if (CHK(i * nvec + v, 1, p.Mp * nvec)) dst[v] = src >= 0 ? x[src * nvec + v] : make_uint4(0u, 0u, 0u, 0u);
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;           // the CTA's 128 positions are a block's
+    if ((int64_t)blockIdx.x * 128 >= rows) return;
+    const int64_t src = p.rowmap[i], nvec = p.D / 8;
+    const int blk = blockIdx.y;
+    uint4 *dst = static_cast<uint4 *>(p.xc) + ((int64_t)blockIdx.x * p.xblocks + blk) * (kPlanes / 8) + threadIdx.x;
+    uint4 v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        v[q] = src >= 0 && blk * 8 + q < nvec ? x[src * nvec + blk * 8 + q] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (CHK(dst + q * 128 - static_cast<uint4 *>(p.xc), 1, p.Mp * p.xblocks * 8)) dst[q * 128] = v[q];
 }
 
 // ---- the list of units -------------------------------------------------------------
@@ -436,28 +444,21 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, int a, int b, int c, int d) {
-    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+// 16 bytes into a CTA's shared memory, counted on a barrier there.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t bar, int a, int b, int c, int d) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];"
+                 ::"r"(addr), "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_cluster(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void ld_shared_v4(uint32_t addr, int &a, int &b, int &c, int &d) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 // An arrival that hands over no memory write of this thread.  (A release at
 // cluster scope waits for all of the thread's global stores.)
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
 }
 // TMA load into this CTA's shared memory, counted on a barrier of either CTA.
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
@@ -509,9 +510,9 @@ __device__ __forceinline__ uint32_t instr_desc(int n, bool a_mn, bool b_mn, bool
 __device__ __forceinline__ uint64_t box_desc(uint32_t base, bool mn, int k) {
     return mn ? smem_desc(base + (uint32_t)k * 2048u, kBlock, 1024u) : smem_desc(base + (uint32_t)k * 32u, 16u, 1024u);
 }
-// G: planes of 128 positions, K along the planes; or (mn) planes of 64
+// x and G: planes of 128 positions, K along the planes; or (mn) planes of 64
 // positions, K along the positions (the strides change places).
-__device__ __forceinline__ uint64_t g_desc(uint32_t base, bool mn, int k) {
+__device__ __forceinline__ uint64_t plane_desc(uint32_t base, bool mn, int k) {
     return mn ? smem_desc_noswizzle(base + (uint32_t)k * 256u, 128u, 1024u)
               : smem_desc_noswizzle(base + (uint32_t)k * 4096u, 2048u, 128u);
 }
@@ -519,8 +520,9 @@ __device__ __forceinline__ uint64_t g_desc(uint32_t base, bool mn, int k) {
 // ---- the tile kernel -------------------------------------------------------------------
 
 struct Maps {
-    CUtensorMap x, w;           // operand boxes 64 x 64, 128-byte swizzle
-    CUtensorMap g_x, g_t;       // G: a block; the halves of its planes that hold 64 positions
+    CUtensorMap w;              // operand boxes 64 x 64, 128-byte swizzle
+    CUtensorMap x_k, g_k;       // x and G: a block, reduced along its columns
+    CUtensorMap x_mn, g_mn;     // the halves of a block's planes that hold 64 positions, reduced along those
     CUtensorMap dt_out;         // store boxes of 32 rows x 64
     CUtensorMap acc;            // store boxes of 32 rows x 32 fp32
 };
@@ -540,14 +542,6 @@ struct Ctx {
         if (mbar_wait(bar, parity)) return true;
         give_up();
         return false;
-    }
-    // The same for a barrier that the other CTA's threads arrive on.
-    __device__ bool wait_cluster(uint32_t bar, uint32_t parity) const {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        const uint64_t t0 = global_ns();
-        while (!mbar_try_wait_cluster(bar, parity))
-            if (global_ns() - t0 > kWaitBudgetNs) { give_up(); return false; }
-        return true;
     }
     __device__ void give_up() const {
         *abort_flag = 1u;
@@ -579,7 +573,7 @@ struct Feed {
     // TMA and MMA instructions take from it lives in uniform registers (with
     // one lane's branch instead, four TMA loads took 570 cycles to issue).
     __device__ bool next(Unit *o) {
-        const bool ok = !c.aborted() && c.wait_cluster(c.sfull(slot), ph);
+        const bool ok = !c.aborted() && c.wait(c.sfull(slot), ph);
         if (!__all_sync(0xffffffffu, ok)) return false;
         int v[8];
         ld_shared_v4(smem_addr(c.slots + slot), v[0], v[1], v[2], v[3]);
@@ -591,7 +585,7 @@ struct Feed {
     }
     // The slot may be used again.
     __device__ void release() {
-        if (threadIdx.x % 32 == 0) mbar_arrive_cluster_relaxed(map_rank(c.sempty(slot), 0));
+        if (threadIdx.x % 32 == 0) mbar_arrive_cluster(map_rank(c.sempty(slot), 0));
         if (++slot == kSlots) { slot = 0; ph ^= 1u; }
     }
     __device__ bool take(Unit *o) {
@@ -608,12 +602,12 @@ __device__ __forceinline__ void hand_out(const Plan &p, Walk w, const Ctx &c) {
     uint32_t ph = 0;
     for (bool more = true; more && !c.aborted();) {
         const Unit o = w.at(atomicAdd(p.ticket, 1u));
-        if (!c.wait_cluster(c.sempty(slot), ph ^ 1u)) return;
+        if (!c.wait(c.sempty(slot), ph ^ 1u)) return;
         for (uint32_t r = 0; r < 2; ++r) {
-            const uint32_t to = map_rank(smem_addr(c.slots + slot), r);
-            st_cluster_v4(to, o.type, o.piece, o.m0, o.n0);
-            st_cluster_v4(to + 16u, o.width, o.parts, o.granule, o.left);
-            mbar_arrive_cluster(map_rank(c.sfull(slot), r));
+            const uint32_t to = map_rank(smem_addr(c.slots + slot), r), bar = map_rank(c.sfull(slot), r);
+            mbar_expect_cluster(bar, 32u);
+            st_async_v4(to, bar, o.type, o.piece, o.m0, o.n0);
+            st_async_v4(to + 16u, bar, o.width, o.parts, o.granule, o.left);
         }
         more = o.left != 0;                       // the first one past the end tells the roles to stop
         if (++slot == kSlots) { slot = 0; ph ^= 1u; }
@@ -666,19 +660,18 @@ __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w,
                     // both CTAs' bytes
                     if (c.rank == 0) mbar_arrive_expect_tx(c.full(s), two ? 2 * (kABytes + 2 * kBlock) : 2 * (kABytes + kBlock));
                     if (o.type == UNIT_L) {       // x and the table, both along D
-                        tma_load_pair(sa, &maps.x, bar, kb * kBK, m0);
-                        tma_load_pair(sa + kBlock, &maps.x, bar, kb * kBK, m0 + 64);
+                        tma_load_pair_3d(sa, &maps.x_k, bar, 0, 0, ((m0 / 128) * p.xblocks + kb) * 8);
                         tma_load_pair(sb, &maps.w, bar, kb * kBK, v0 + n0);
                         if (two) tma_load_pair(sb + kBlock, &maps.w, bar, kb * kBK, v0 + n0 + 64);
                     } else if (o.type == UNIT_T) {    // G^T and x, along the positions
-                        const int blk = (kb / 2) * gblocks + gcol + m0 / 64;
-                        tma_load_pair_3d(sa, &maps.g_t, bar, 0, (kb & 1) * 8, blk * 8);
-                        tma_load_pair_3d(sa + kBlock, &maps.g_t, bar, 0, (kb & 1) * 8, blk * 8 + 8);
-                        tma_load_pair(sb, &maps.x, bar, n0, kb * kBK);
-                        if (two) tma_load_pair(sb + kBlock, &maps.x, bar, n0 + 64, kb * kBK);
+                        const int g = (kb / 2) * gblocks + gcol + m0 / 64, x = (kb / 2) * p.xblocks + n0 / 64;
+                        const int h = (kb & 1) * 8;
+                        tma_load_pair_3d(sa, &maps.g_mn, bar, 0, h, g * 8);
+                        tma_load_pair_3d(sa + kBlock, &maps.g_mn, bar, 0, h, g * 8 + 8);
+                        tma_load_pair_3d(sb, &maps.x_mn, bar, 0, h, x * 8);
+                        if (two) tma_load_pair_3d(sb + kBlock, &maps.x_mn, bar, 0, h, x * 8 + 8);
                     } else {                      // G and the table, along the vocabulary
-                        const int blk = (m0 / 128) * gblocks + gcol + k0 / 64 + kb;
-                        tma_load_pair_3d(sa, &maps.g_x, bar, 0, 0, blk * 8);
+                        tma_load_pair_3d(sa, &maps.g_k, bar, 0, 0, ((m0 / 128) * gblocks + gcol + k0 / 64 + kb) * 8);
                         tma_load_pair(sb, &maps.w, bar, n0, v0 + k0 + kb * kBK);
                         if (two) tma_load_pair(sb + kBlock, &maps.w, bar, n0 + 64, v0 + k0 + kb * kBK);
                     }
@@ -698,17 +691,18 @@ __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w,
 
 // k-blocks of one accumulation.
 template <int TYPE>
-__device__ __forceinline__ bool issue_blocks(const Ctx &c, uint32_t d, int width, bool f16, int nkb, int &s, uint32_t &ph) {
+__device__ __forceinline__ bool issue_blocks(const Ctx &c, uint32_t d, int width, bool f16, int from, int to, int &s,
+                                             uint32_t &ph) {
     constexpr bool A_MN = TYPE == UNIT_T, B_MN = TYPE != UNIT_L;
     const uint32_t idesc = instr_desc(width, A_MN, B_MN, f16);
-    for (int kb = 0; kb < nkb; ++kb) {
+    for (int kb = from; kb < to; ++kb) {
         if (!__all_sync(0xffffffffu, c.wait(c.full(s), ph))) return false;
         tc_fence_after();
         const uint32_t sa = c.sbase + s * kStageBytes, sb = sa + kABytes;
         if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
-                mma_pair(d, TYPE == UNIT_L ? box_desc(sa, false, k) : g_desc(sa, A_MN, k), box_desc(sb, B_MN, k), idesc,
+                mma_pair(d, plane_desc(sa, A_MN, k), TYPE == UNIT_T ? plane_desc(sb, true, k) : box_desc(sb, B_MN, k), idesc,
                          (kb | k) != 0 ? 1u : 0u);
             mma_commit_pair(c.empty(s));
         }
@@ -718,27 +712,30 @@ __device__ __forceinline__ bool issue_blocks(const Ctx &c, uint32_t d, int width
     return true;
 }
 
-// CTA 0 issues the pair's MMAs.
+// CTA 0 issues the pair's MMAs.  The next unit is taken before the current
+// one's last k-blocks are issued, so that the tensor cores have work meanwhile.
 template <bool GRAD, bool F16>
 __device__ __forceinline__ void issue(Walk w, const Ctx &c) {
     int s = 0, acc = 0;
     uint32_t ph = 0, aph = 0;
-    Unit o;
+    Unit o, next;
     Feed feed{c};
-    while (feed.take(&o)) {
+    bool more = feed.take(&next);
+    while (more) {
+        o = next;
         for (int part = 0; part < o.parts; ++part) {
-            if (!__all_sync(0xffffffffu, c.wait_cluster(c.tempty(acc), aph ^ 1u))) return;
+            if (!__all_sync(0xffffffffu, c.wait(c.tempty(acc), aph ^ 1u))) return;
             tc_fence_after();
             const uint32_t d = c.tmem + (uint32_t)(acc * kBN);
-            const int nkb = w.k_blocks(o, part);
-            bool ok;
-            if (!GRAD || o.type == UNIT_L)
-                ok = issue_blocks<UNIT_L>(c, d, o.width, F16, nkb, s, ph);
-            else if (o.type == UNIT_T)
-                ok = issue_blocks<UNIT_T>(c, d, o.width, F16, nkb, s, ph);
-            else
-                ok = issue_blocks<UNIT_X>(c, d, o.width, F16, nkb, s, ph);
-            if (!ok) return;
+            const int nkb = w.k_blocks(o, part), first = nkb > 4 ? nkb - 4 : 0;
+            auto blocks = [&](int from, int to) {
+                if (!GRAD || o.type == UNIT_L) return issue_blocks<UNIT_L>(c, d, o.width, F16, from, to, s, ph);
+                if (o.type == UNIT_T) return issue_blocks<UNIT_T>(c, d, o.width, F16, from, to, s, ph);
+                return issue_blocks<UNIT_X>(c, d, o.width, F16, from, to, s, ph);
+            };
+            if (!blocks(0, first)) return;
+            if (part == o.parts - 1) more = feed.take(&next);
+            if (!blocks(first, nkb)) return;
             if (elect_one()) mma_commit_pair(c.tfull(acc));
             __syncwarp();
             if (++acc == 2) { acc = 0; aph ^= 1u; }
@@ -859,7 +856,7 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
                 const int n = (int)(p.V - (int64_t)o.piece * p.piece_cols) - o.n0;   // valid columns of this tile
                 // this row's place in plane 0 of the first block
                 uint16_t *g_row = static_cast<uint16_t *>(p.g) +
-                    ((int64_t)(row0 / 128) * (p.piece_cols * p.buffers / 64) + ((o.piece % p.buffers) * p.piece_cols + o.n0) / 64) * kGBlock +
+                    ((int64_t)(row0 / 128) * (p.piece_cols * p.buffers / 64) + ((o.piece % p.buffers) * p.piece_cols + o.n0) / 64) * kPlanes +
                     (row % 128) * 8;
                 const bool dead = rfac == 0.0f;          // no position, or none of its gradient
 #pragma unroll 1
@@ -884,11 +881,11 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
                         g[i] = pack2<F16>(__uint_as_float(r[2 * i]) * rfac, __uint_as_float(r[2 * i + 1]) * rfac);
                         if (dead) g[i] = 0u;              // whatever z is
                     }
-                    uint16_t *dst = g_row + (int64_t)(cc / 64) * kGBlock;
+                    uint16_t *dst = g_row + (int64_t)(cc / 64) * kPlanes;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        if (CHK(dst + q * kGPlane - static_cast<uint16_t *>(p.g), 8, p.Mp * p.piece_cols * p.buffers))
-                            *reinterpret_cast<uint4 *>(dst + q * kGPlane) =
+                        if (CHK(dst + q * kPlane - static_cast<uint16_t *>(p.g), 8, p.Mp * p.piece_cols * p.buffers))
+                            *reinterpret_cast<uint4 *>(dst + q * kPlane) =
                                 make_uint4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]);
                 }
             } else if (o.type == UNIT_T) {
@@ -932,7 +929,7 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(c.tempty(acc), 0));
+            if (lane == 0) mbar_arrive_cluster(map_rank(c.tempty(acc), 0));
             if (++acc == 2) { acc = 0; aph ^= 1u; }
         }
         if (GRAD) {                                       // this warp's part has been stored
@@ -990,7 +987,7 @@ xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan
         }
         *c.abort_flag = 0u;
         fence_mbar_init();
-        prefetch_map(&maps.x);
+        prefetch_map(&maps.x_k);
         prefetch_map(&maps.w);
     }
     if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), 512);
@@ -1118,10 +1115,19 @@ cudaError_t encode(CUtensorMap *m, const void *base, int64_t inner, int64_t oute
                                 CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Blocks of planes (n elements) as [planes][16 groups of 8 positions][64
+// elements]: a box of 8 planes and `groups` groups.
+cudaError_t encode_blocks(CUtensorMap *m, const void *base, int64_t n, int groups) {
+    const uint64_t extent[3] = {64, 16, (uint64_t)(n / kPlane)}, stride[2] = {128, 2048};
+    const uint32_t box[3] = {64, (uint32_t)groups, 8};
+    return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, extent, stride, box,
+                             CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 bool sizes_ok(int64_t M, int64_t D, int64_t V) {
     int64_t t;
     // tile coordinates and counters are 32-bit; element counts are 64-bit
-    return M >= 0 && D >= 0 && V >= 0 && M < (1ll << 30) && D < (1ll << 24) && V < (1ll << 30) &&
+    return M >= 0 && D >= 0 && V >= 0 && M < (1ll << 30) && D < (1ll << 22) && V < (1ll << 30) &&
            !__builtin_mul_overflow(M, D, &t) && !__builtin_mul_overflow(t, (int64_t)16, &t) &&
            !__builtin_mul_overflow(V, D, &t) && !__builtin_mul_overflow(t, (int64_t)16, &t);
 }
@@ -1138,8 +1144,11 @@ carbon_status_t check(const void *x, const void *table, const int64_t *targets, 
     return CARBON_OK;
 }
 
-// The list of units is counted in 32 bits.
+// Units and planes are counted in 32 bits.
 bool list_fits(const Plan &p) {
+    // planes are numbered by TMA coordinates
+    if (p.Mp * p.xblocks * 64 / kPlane >= (1ll << 31) || (p.grad && p.Mp * p.piece_cols * p.buffers / kPlane >= (1ll << 31)))
+        return false;
     const int64_t tm = p.Mp / kBM, l = (p.V + 127) / 128, t = (p.V + kBM - 1) / kBM + p.pieces;
     return tm * (l + p.pieces) + (t + tm * p.granules) * p.dtiles < (1ll << 31);
 }
@@ -1147,27 +1156,20 @@ bool list_fits(const Plan &p) {
 template <bool GRAD>
 cudaError_t launch_tiles(const Plan &p, const void *table, void *dtable, int sms, cudaStream_t s) {
     Maps maps;
-    cudaError_t err = encode(&maps.x, p.xc, p.D, p.Mp, 64, 64);
-    if (err == cudaSuccess) err = encode(&maps.w, table, p.D, p.V, 64, 64);
+    cudaError_t err = encode(&maps.w, table, p.D, p.V, 64, 64);
+    if (err == cudaSuccess) err = encode_blocks(&maps.x_k, p.xc, p.Mp * p.xblocks * 64, 16);
     if (GRAD) {
-        // G as [planes][16 groups of 8 positions][64 elements]
-        const uint64_t planes = (uint64_t)(p.Mp * p.piece_cols * p.buffers / kGPlane);
-        const uint64_t extent[3] = {64, 16, planes}, stride[2] = {128, 2048};
-        const uint32_t whole[3] = {64, 16, 8}, half[3] = {64, 8, 8};
-        if (planes >= (1ull << 31)) return cudaErrorInvalidValue;
-        if (err == cudaSuccess)
-            err = encode_tensor_map(&maps.g_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.g, 3, extent, stride, whole,
-                                    CU_TENSOR_MAP_SWIZZLE_NONE);
-        if (err == cudaSuccess)
-            err = encode_tensor_map(&maps.g_t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.g, 3, extent, stride, half,
-                                    CU_TENSOR_MAP_SWIZZLE_NONE);
+        const int64_t n = p.Mp * p.piece_cols * p.buffers;
+        if (err == cudaSuccess) err = encode_blocks(&maps.x_mn, p.xc, p.Mp * p.xblocks * 64, 8);
+        if (err == cudaSuccess) err = encode_blocks(&maps.g_k, p.g, n, 16);
+        if (err == cudaSuccess) err = encode_blocks(&maps.g_mn, p.g, n, 8);
         if (err == cudaSuccess)
             err = encode_tensor_map_2d(&maps.acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.acc, (uint64_t)p.D,
                                        (uint64_t)(p.Mp * p.slots), (uint64_t)p.D * 4, 32, 32,
                                        CU_TENSOR_MAP_SWIZZLE_128B);
         if (err == cudaSuccess) err = encode(&maps.dt_out, dtable, p.D, p.V, 64, 32);
     } else {
-        maps.g_x = maps.g_t = maps.dt_out = maps.acc = maps.x;       // unused
+        maps.x_mn = maps.g_k = maps.g_mn = maps.dt_out = maps.acc = maps.x_k;     // unused
     }
     if (err != cudaSuccess) return err;
     auto kern = p.f16 ? xent_tile_kernel<GRAD, true> : xent_tile_kernel<GRAD, false>;
@@ -1182,7 +1184,7 @@ cudaError_t launch_gather(const Plan &p, const ScanArgs &a, const void *x, cudaS
     count_launch(2);
     const cudaError_t err = launch_k(xent_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, 1, p, a);
     if (err != cudaSuccess) return err;
-    return launch_k(xent_gather_kernel, dim3((unsigned)(p.Mp / 8)), dim3(256), 0, s, 1, p,
+    return launch_k(xent_gather_kernel, dim3((unsigned)(p.Mp / 128), (unsigned)p.xblocks), dim3(128), 0, s, 1, p,
                     static_cast<const uint4 *>(x));
 }
 
