@@ -632,52 +632,81 @@ struct Ready {
     }
 };
 
-// A whole warp runs the loop; one lane issues the loads of this CTA's rows of
-// A and columns of B.
+// Loads of one accumulation: this CTA's rows of A and columns of B, k-block by
+// k-block.  A whole warp runs the loop, one lane issues.  ca, cb: coordinates
+// of the first k-block (rows of the table; planes of x or G); TWO: two boxes
+// of B, else one.
+template <int TYPE, bool TWO>
+__device__ __forceinline__ bool load_blocks(const Maps &maps, const Ctx &c, int nkb, int ca, int cb, int n0, int gstep,
+                                            int xstep, int &s, uint32_t &ph) {
+    constexpr uint32_t kBytes = 2 * (kABytes + (TWO ? 2 : 1) * kBlock);      // both CTAs'
+    for (int kb = 0; kb < nkb; ++kb) {
+        if (!__all_sync(0xffffffffu, c.wait(c.empty(s), ph ^ 1u))) return false;
+        const uint32_t sa = c.sbase + s * kStageBytes, sb = sa + kABytes, bar = map_rank(c.full(s), 0);
+        if (elect_one()) {
+            if (c.rank == 0) mbar_arrive_expect_tx(c.full(s), kBytes);
+            if (TYPE == UNIT_L) {                 // x and the table, both along D
+                tma_load_pair_3d(sa, &maps.x_k, bar, 0, 0, ca);
+                tma_load_pair(sb, &maps.w, bar, kb * kBK, cb);
+                if (TWO) tma_load_pair(sb + kBlock, &maps.w, bar, kb * kBK, cb + 64);
+            } else if (TYPE == UNIT_T) {          // G^T and x, along the positions
+                const int h = (kb & 1) * 8;
+                tma_load_pair_3d(sa, &maps.g_mn, bar, 0, h, ca);
+                tma_load_pair_3d(sa + kBlock, &maps.g_mn, bar, 0, h, ca + 8);
+                tma_load_pair_3d(sb, &maps.x_mn, bar, 0, h, cb);
+                if (TWO) tma_load_pair_3d(sb + kBlock, &maps.x_mn, bar, 0, h, cb + 8);
+            } else {                              // G and the table, along the vocabulary
+                tma_load_pair_3d(sa, &maps.g_k, bar, 0, 0, ca);
+                tma_load_pair(sb, &maps.w, bar, n0, cb);
+                if (TWO) tma_load_pair(sb + kBlock, &maps.w, bar, n0 + 64, cb);
+            }
+        }
+        __syncwarp();
+        if (TYPE == UNIT_L) {
+            ca += 8;
+        } else if (TYPE == UNIT_T) {
+            ca += (kb & 1) * gstep;
+            cb += (kb & 1) * xstep;
+        } else {
+            ca += 8;
+            cb += kBK;
+        }
+        if (++s == kStages) { s = 0; ph ^= 1u; }
+    }
+    return true;
+}
+
+template <bool GRAD>
 __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w, const Ctx &c) {
     int s = 0;
     uint32_t ph = 0;
     Unit o;
     Feed feed{c};
     Ready ready;
-    const int gblocks = p.grad ? p.piece_cols * p.buffers / 64 : 0;       // blocks of G per 128 positions
+    const int gstep = GRAD ? p.piece_cols * p.buffers / 64 * 8 : 0, xstep = p.xblocks * 8;   // planes per 128 positions
     bool ok = true;
     while (ok && feed.take(&o)) {
-        if (!__all_sync(0xffffffffu, ready.wait(p, w, o, c))) break;
-        fence_proxy_async_all();                  // other CTAs' G, before this CTA's TMA reads
-        const bool two = o.width > 128;           // boxes of B per CTA
+        if (GRAD) {
+            if (!__all_sync(0xffffffffu, ready.wait(p, w, o, c))) break;
+            fence_proxy_async_all();              // other CTAs' G, before this CTA's TMA reads
+        }
         const int v0 = o.piece * p.piece_cols;
         const int m0 = o.m0 + (int)c.rank * 128, n0 = o.n0 + (int)c.rank * (o.width / 2);
-        const int gcol = p.grad ? (o.piece % p.buffers) * (p.piece_cols / 64) : 0;
+        const int g0 = GRAD ? (o.piece % p.buffers) * (p.piece_cols / 64) * 8 : 0;
         for (int part = 0; ok && part < o.parts; ++part) {
             const int nkb = w.k_blocks(o, part), k0 = (o.granule + part) * kGranule;
-            for (int kb = 0; kb < nkb; ++kb) {
-                ok = __all_sync(0xffffffffu, c.wait(c.empty(s), ph ^ 1u));
-                if (!ok) break;
-                const uint32_t sa = c.sbase + s * kStageBytes, sb = sa + kABytes;
-                if (elect_one()) {
-                    const uint32_t bar = map_rank(c.full(s), 0);
-                    // both CTAs' bytes
-                    if (c.rank == 0) mbar_arrive_expect_tx(c.full(s), two ? 2 * (kABytes + 2 * kBlock) : 2 * (kABytes + kBlock));
-                    if (o.type == UNIT_L) {       // x and the table, both along D
-                        tma_load_pair_3d(sa, &maps.x_k, bar, 0, 0, ((m0 / 128) * p.xblocks + kb) * 8);
-                        tma_load_pair(sb, &maps.w, bar, kb * kBK, v0 + n0);
-                        if (two) tma_load_pair(sb + kBlock, &maps.w, bar, kb * kBK, v0 + n0 + 64);
-                    } else if (o.type == UNIT_T) {    // G^T and x, along the positions
-                        const int g = (kb / 2) * gblocks + gcol + m0 / 64, x = (kb / 2) * p.xblocks + n0 / 64;
-                        const int h = (kb & 1) * 8;
-                        tma_load_pair_3d(sa, &maps.g_mn, bar, 0, h, g * 8);
-                        tma_load_pair_3d(sa + kBlock, &maps.g_mn, bar, 0, h, g * 8 + 8);
-                        tma_load_pair_3d(sb, &maps.x_mn, bar, 0, h, x * 8);
-                        if (two) tma_load_pair_3d(sb + kBlock, &maps.x_mn, bar, 0, h, x * 8 + 8);
-                    } else {                      // G and the table, along the vocabulary
-                        tma_load_pair_3d(sa, &maps.g_k, bar, 0, 0, ((m0 / 128) * gblocks + gcol + k0 / 64 + kb) * 8);
-                        tma_load_pair(sb, &maps.w, bar, n0, v0 + k0 + kb * kBK);
-                        if (two) tma_load_pair(sb + kBlock, &maps.w, bar, n0 + 64, v0 + k0 + kb * kBK);
-                    }
-                }
-                __syncwarp();
-                if (++s == kStages) { s = 0; ph ^= 1u; }
+            if (!GRAD || o.type == UNIT_L) {
+                const int ca = m0 / 128 * xstep, cb = v0 + n0;
+                ok = o.width > 128 ? load_blocks<UNIT_L, true>(maps, c, nkb, ca, cb, 0, 0, 0, s, ph)
+                                   : load_blocks<UNIT_L, false>(maps, c, nkb, ca, cb, 0, 0, 0, s, ph);
+            } else if (o.type == UNIT_T) {
+                const int ca = g0 + m0 / 64 * 8, cb = n0 / 64 * 8;
+                ok = o.width > 128 ? load_blocks<UNIT_T, true>(maps, c, nkb, ca, cb, 0, gstep, xstep, s, ph)
+                                   : load_blocks<UNIT_T, false>(maps, c, nkb, ca, cb, 0, gstep, xstep, s, ph);
+            } else {
+                const int ca = m0 / 128 * gstep + g0 + k0 / 64 * 8, cb = v0 + k0;
+                ok = o.width > 128 ? load_blocks<UNIT_X, true>(maps, c, nkb, ca, cb, n0, 0, 0, s, ph)
+                                   : load_blocks<UNIT_X, false>(maps, c, nkb, ca, cb, n0, 0, 0, s, ph);
             }
         }
     }
@@ -1001,7 +1030,7 @@ xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan
     const Walk w(p, p.head->kept);
 
     if (warp == 0) {
-        produce(p, maps, w, c);
+        produce<GRAD>(p, maps, w, c);
     } else if (warp == 1) {
         if (c.rank == 0) issue<GRAD, F16>(w, c);
     } else if (warp == 2) {
