@@ -57,12 +57,14 @@ constexpr unsigned kDone = 2;                         // reports of a finished u
 constexpr int kGroup = 128;              // vocabulary entries per (max, sum) pair
 constexpr int kGranule = 4096;           // vocabulary entries per partial sum of dx
 constexpr int kPieceBuffers = 3;         // pieces of G in the workspace
-// x and G are kept as blocks of 128 positions x 64 columns, each block as 8
-// planes of 8 columns: a plane holds 16 bytes per position, so that a warp of
-// 32 positions writes 512 contiguous bytes a store, straight from its
-// registers, and a block is loaded as contiguous bytes.  It is also a
-// shared-memory image of the MMA's unswizzled operand, for either orientation
-// (core matrices of 8 positions x 16 bytes).
+// x and G are kept as blocks of 128 positions x 64 columns that are images of
+// the MMA's operands in shared memory, for either orientation, so that a load
+// is contiguous bytes.
+// x: a row of 128 bytes per position, its 16-byte pieces in the order of the
+// 128-byte swizzle.
+// G: 8 planes of 8 columns, a plane holds 16 bytes per position (the
+// unswizzled layout, core matrices of 8 positions x 16 bytes): a warp of 32
+// positions writes 512 contiguous bytes a store, straight from its registers.
 constexpr int kPlane = 128 * 8, kPlanes = 8 * kPlane;         // elements of a plane, of a block
 constexpr int64_t kPieceBytes = 64ll << 20;   // largest piece of G, unless one granule is larger
 constexpr int64_t kSlotBytes = 64ll << 20;    // dx: granule sums side by side up to this size
@@ -268,25 +270,27 @@ xent_scan_kernel(const Plan p, const ScanArgs a) {
 __device__ __forceinline__ int row_tiles(int kept) { return kept > kBM ? (kept + kBM - 1) / kBM : 1; }
 
 // Dense rows of x in blocks; zeros up to the last tile's end and past D.  A
-// warp per 32 positions and 64 columns: lane = position, so the reads are 16
-// bytes of 32 rows (their lines stay in L1), the writes contiguous.
-__global__ void __launch_bounds__(128)
+// CTA per block; 8 threads per position and 128-byte row.
+__global__ void __launch_bounds__(256)
 xent_gather_kernel(const Plan p, const uint4 *__restrict__ x) {
     wait_prior_grid();
     allow_next_grid();
     const int64_t rows = (int64_t)row_tiles(p.head->kept) * kBM;
-    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;           // the CTA's 128 positions are a block's
     if ((int64_t)blockIdx.x * 128 >= rows) return;
-    const int64_t src = p.rowmap[i], nvec = p.D / 8;
-    const int blk = blockIdx.y;
-    uint4 *dst = static_cast<uint4 *>(p.xc) + ((int64_t)blockIdx.x * p.xblocks + blk) * (kPlanes / 8) + threadIdx.x;
-    uint4 v[8];
+    const int q = threadIdx.x % 8, blk = blockIdx.y;
+    const int64_t nvec = p.D / 8;
+    uint4 *dst = static_cast<uint4 *>(p.xc) + ((int64_t)blockIdx.x * p.xblocks + blk) * (128 * 8);
+    uint4 v[4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-        v[q] = src >= 0 && blk * 8 + q < nvec ? x[src * nvec + blk * 8 + q] : make_uint4(0u, 0u, 0u, 0u);
+    for (int u = 0; u < 4; ++u) {
+        const int64_t src = p.rowmap[blockIdx.x * 128 + u * 32 + threadIdx.x / 8];
+        v[u] = src >= 0 && blk * 8 + q < nvec ? x[src * nvec + blk * 8 + q] : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-        if (CHK(dst + q * 128 - static_cast<uint4 *>(p.xc), 1, p.Mp * p.xblocks * 8)) dst[q * 128] = v[q];
+    for (int u = 0; u < 4; ++u) {
+        const int r = u * 32 + threadIdx.x / 8;
+        if (CHK(dst + r * 8 - static_cast<uint4 *>(p.xc), 8, p.Mp * p.xblocks * 8)) dst[r * 8 + (q ^ (r & 7))] = v[u];
+    }
 }
 
 // ---- the list of units -------------------------------------------------------------
@@ -510,7 +514,7 @@ __device__ __forceinline__ uint32_t instr_desc(int n, bool a_mn, bool b_mn, bool
 __device__ __forceinline__ uint64_t box_desc(uint32_t base, bool mn, int k) {
     return mn ? smem_desc(base + (uint32_t)k * 2048u, kBlock, 1024u) : smem_desc(base + (uint32_t)k * 32u, 16u, 1024u);
 }
-// x and G: planes of 128 positions, K along the planes; or (mn) planes of 64
+// G: planes of 128 positions, K along the planes; or (mn) planes of 64
 // positions, K along the positions (the strides change places).
 __device__ __forceinline__ uint64_t plane_desc(uint32_t base, bool mn, int k) {
     return mn ? smem_desc_noswizzle(base + (uint32_t)k * 256u, 128u, 1024u)
@@ -520,9 +524,10 @@ __device__ __forceinline__ uint64_t plane_desc(uint32_t base, bool mn, int k) {
 // ---- the tile kernel -------------------------------------------------------------------
 
 struct Maps {
-    CUtensorMap w;              // operand boxes 64 x 64, 128-byte swizzle
-    CUtensorMap x_k, g_k;       // x and G: a block, reduced along its columns
-    CUtensorMap x_mn, g_mn;     // the halves of a block's planes that hold 64 positions, reduced along those
+    CUtensorMap w;              // boxes of 64 x 64, 128-byte swizzle
+    CUtensorMap x;              // half a block: the rows of 64 positions
+    CUtensorMap g_k;            // a block, reduced along its columns
+    CUtensorMap g_mn;           // the halves of a block's planes that hold 64 positions, reduced along those
     CUtensorMap dt_out;         // store boxes of 32 rows x 64
     CUtensorMap acc;            // store boxes of 32 rows x 32 fp32
 };
@@ -634,7 +639,7 @@ struct Ready {
 
 // Loads of one accumulation: this CTA's rows of A and columns of B, k-block by
 // k-block.  A whole warp runs the loop, one lane issues.  ca, cb: coordinates
-// of the first k-block (rows of the table; planes of x or G); TWO: two boxes
+// of the first k-block (rows of the table or of x's blocks; planes of G); TWO: two boxes
 // of B, else one.
 template <int TYPE, bool TWO>
 __device__ __forceinline__ bool load_blocks(const Maps &maps, const Ctx &c, int nkb, int ca, int cb, int n0, int gstep,
@@ -646,15 +651,16 @@ __device__ __forceinline__ bool load_blocks(const Maps &maps, const Ctx &c, int 
         if (elect_one()) {
             if (c.rank == 0) mbar_arrive_expect_tx(c.full(s), kBytes);
             if (TYPE == UNIT_L) {                 // x and the table, both along D
-                tma_load_pair_3d(sa, &maps.x_k, bar, 0, 0, ca);
+                tma_load_pair(sa, &maps.x, bar, 0, ca);
+                tma_load_pair(sa + kBlock, &maps.x, bar, 0, ca + 64);
                 tma_load_pair(sb, &maps.w, bar, kb * kBK, cb);
                 if (TWO) tma_load_pair(sb + kBlock, &maps.w, bar, kb * kBK, cb + 64);
             } else if (TYPE == UNIT_T) {          // G^T and x, along the positions
                 const int h = (kb & 1) * 8;
                 tma_load_pair_3d(sa, &maps.g_mn, bar, 0, h, ca);
                 tma_load_pair_3d(sa + kBlock, &maps.g_mn, bar, 0, h, ca + 8);
-                tma_load_pair_3d(sb, &maps.x_mn, bar, 0, h, cb);
-                if (TWO) tma_load_pair_3d(sb + kBlock, &maps.x_mn, bar, 0, h, cb + 8);
+                tma_load_pair(sb, &maps.x, bar, 0, cb);
+                if (TWO) tma_load_pair(sb + kBlock, &maps.x, bar, 0, cb + 128);
             } else {                              // G and the table, along the vocabulary
                 tma_load_pair_3d(sa, &maps.g_k, bar, 0, 0, ca);
                 tma_load_pair(sb, &maps.w, bar, n0, cb);
@@ -663,10 +669,10 @@ __device__ __forceinline__ bool load_blocks(const Maps &maps, const Ctx &c, int 
         }
         __syncwarp();
         if (TYPE == UNIT_L) {
-            ca += 8;
-        } else if (TYPE == UNIT_T) {
+            ca += 128;
+        } else if (TYPE == UNIT_T) {              // the block's other half, then the next 128 positions
             ca += (kb & 1) * gstep;
-            cb += (kb & 1) * xstep;
+            cb += (kb & 1) ? xstep - 64 : 64;
         } else {
             ca += 8;
             cb += kBK;
@@ -683,7 +689,7 @@ __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w,
     Unit o;
     Feed feed{c};
     Ready ready;
-    const int gstep = GRAD ? p.piece_cols * p.buffers / 64 * 8 : 0, xstep = p.xblocks * 8;   // planes per 128 positions
+    const int gstep = GRAD ? p.piece_cols * p.buffers / 64 * 8 : 0, xstep = p.xblocks * 128;   // planes of G, rows of x, per 128 positions
     bool ok = true;
     while (ok && feed.take(&o)) {
         if (GRAD) {
@@ -700,7 +706,7 @@ __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w,
                 ok = o.width > 128 ? load_blocks<UNIT_L, true>(maps, c, nkb, ca, cb, 0, 0, 0, s, ph)
                                    : load_blocks<UNIT_L, false>(maps, c, nkb, ca, cb, 0, 0, 0, s, ph);
             } else if (o.type == UNIT_T) {
-                const int ca = g0 + m0 / 64 * 8, cb = n0 / 64 * 8;
+                const int ca = g0 + m0 / 64 * 8, cb = n0 / 64 * 128;
                 ok = o.width > 128 ? load_blocks<UNIT_T, true>(maps, c, nkb, ca, cb, 0, gstep, xstep, s, ph)
                                    : load_blocks<UNIT_T, false>(maps, c, nkb, ca, cb, 0, gstep, xstep, s, ph);
             } else {
@@ -731,7 +737,7 @@ __device__ __forceinline__ bool issue_blocks(const Ctx &c, uint32_t d, int width
         if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
-                mma_pair(d, plane_desc(sa, A_MN, k), TYPE == UNIT_T ? plane_desc(sb, true, k) : box_desc(sb, B_MN, k), idesc,
+                mma_pair(d, TYPE == UNIT_L ? box_desc(sa, false, k) : plane_desc(sa, A_MN, k), box_desc(sb, B_MN, k), idesc,
                          (kb | k) != 0 ? 1u : 0u);
             mma_commit_pair(c.empty(s));
         }
@@ -821,36 +827,50 @@ __device__ __forceinline__ void put_rows(uint32_t stg, int lane, const CUtensorM
     __syncwarp();
 }
 
-// Loss: (max, sum) pairs and the targets' logits of this thread's row.
+// The element of v that lies at index i, by comparison (registers have no
+// index); 0 where i is not in [0, 64).
+__device__ __forceinline__ float pick(const uint32_t (&v)[64], int i) {
+    uint32_t r = 0u;
+#pragma unroll
+    for (int k = 0; k < 64; ++k)
+        if (k == i) r = v[k];
+    return __uint_as_float(r);
+}
+
+// Loss: this thread's row of 128 entries as a (max, sum) pair, and the
+// target's logit where it is among them.
 __device__ __forceinline__ void loss_rows(const Plan &p, const Unit &o, uint32_t tmem, int row, int half) {
-    const int tgt = p.tgt[row];
-    for (int g = half * kGroup; g < o.width; g += 2 * kGroup) {
-        float mx = -INFINITY, sum = 0.0f;                 // of z log2(e)
+    const int g = half * kGroup;                          // columns of this warp
+    if (g >= o.width || o.n0 + g >= p.V) return;
+    const int tgt = p.tgt[row] - o.n0;
+    float mx = -INFINITY, sum = 0.0f;                     // of z log2(e)
 #pragma unroll 1
-        for (int c = g; c < min(g + kGroup, o.width); c += 32) {
-            const int v0 = o.n0 + c;
-            if (v0 >= p.V) break;
-            uint32_t r[32];
-            tmem_ld32(tmem + (uint32_t)c, r);
-            const int n = (int)min((int64_t)32, p.V - v0);
-            float z[32];
-            float top = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                z[i] = i < n ? __uint_as_float(r[i]) * kLog2e : -INFINITY;
-                top = fmaxf(top, z[i]);
-                if (v0 + i == tgt && CHK(row, 1, p.Mp)) p.zt[row] = __uint_as_float(r[i]);
-            }
-            const float now = fmaxf(mx, top), ref = now == -INFINITY ? 0.0f : now;
-            sum *= ex2(mx - ref);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sum += ex2(z[i] - ref);
-            mx = now;
+    for (int c = g; c < g + kGroup && o.n0 + c < p.V; c += 64) {
+        uint32_t r[64];
+        tmem_ld64(tmem + (uint32_t)c, r);
+        if (__any_sync(0xffffffffu, (unsigned)(tgt - c) < 64u)) {
+            const float z = pick(r, tgt - c);
+            if ((unsigned)(tgt - c) < 64u && CHK(row, 1, p.Mp)) p.zt[row] = z;
         }
-        const int64_t group = (o.n0 + g) / kGroup;
-        if (o.n0 + g < p.V && CHK(group * p.Mp + row, 1, p.vocab_groups * p.Mp))
-            p.pairs[group * p.Mp + row] = make_float2(mx, sum);
+        const int64_t n = p.V - o.n0 - c;
+        if (n < 64) {                                     // past the vocabulary
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                if (i >= n) r[i] = __float_as_uint(-INFINITY);
+        }
+        float top = __uint_as_float(r[0]);
+#pragma unroll
+        for (int i = 1; i < 64; ++i) top = fmaxf(top, __uint_as_float(r[i]));
+        const float now = fmaxf(mx, top * kLog2e), ref = now == -INFINITY ? 0.0f : now;
+        sum *= ex2(mx - ref);
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 64; ++i) s[i % 4] += ex2(fmaf(__uint_as_float(r[i]), kLog2e, -ref));
+        sum += (s[0] + s[1]) + (s[2] + s[3]);
+        mx = now;
     }
+    const int64_t group = (o.n0 + g) / kGroup;
+    if (CHK(group * p.Mp + row, 1, p.vocab_groups * p.Mp)) p.pairs[group * p.Mp + row] = make_float2(mx, sum);
 }
 
 template <bool GRAD, bool F16>
@@ -888,6 +908,7 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
                     ((int64_t)(row0 / 128) * (p.piece_cols * p.buffers / 64) + ((o.piece % p.buffers) * p.piece_cols + o.n0) / 64) * kPlanes +
                     (row % 128) * 8;
                 const bool dead = rfac == 0.0f;          // no position, or none of its gradient
+                const bool plain = __all_sync(0xffffffffu, rfac == 1.0f);
 #pragma unroll 1
                 for (int cc = c0; cc < c1; cc += 64) {
                     uint32_t r[64], g[32];
@@ -905,11 +926,14 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
                         for (int i = 0; i < 64; ++i)
                             if (cc + i >= n) r[i] = 0u;
                     }
+                    if (!plain) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        g[i] = pack2<F16>(__uint_as_float(r[2 * i]) * rfac, __uint_as_float(r[2 * i + 1]) * rfac);
-                        if (dead) g[i] = 0u;              // whatever z is
+                        for (int i = 0; i < 64; ++i)      // a dead row is zero whatever z is
+                            r[i] = dead ? 0u : __float_as_uint(__uint_as_float(r[i]) * rfac);
                     }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        g[i] = pack2<F16>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
                     uint16_t *dst = g_row + (int64_t)(cc / 64) * kPlanes;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
@@ -1016,7 +1040,7 @@ xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan
         }
         *c.abort_flag = 0u;
         fence_mbar_init();
-        prefetch_map(&maps.x_k);
+        prefetch_map(&maps.x);
         prefetch_map(&maps.w);
     }
     if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), 512);
@@ -1144,7 +1168,7 @@ cudaError_t encode(CUtensorMap *m, const void *base, int64_t inner, int64_t oute
                                 CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Blocks of planes (n elements) as [planes][16 groups of 8 positions][64
+// G's blocks (n elements) as [planes][16 groups of 8 positions][64
 // elements]: a box of 8 planes and `groups` groups.
 cudaError_t encode_blocks(CUtensorMap *m, const void *base, int64_t n, int groups) {
     const uint64_t extent[3] = {64, 16, (uint64_t)(n / kPlane)}, stride[2] = {128, 2048};
@@ -1173,10 +1197,10 @@ carbon_status_t check(const void *x, const void *table, const int64_t *targets, 
     return CARBON_OK;
 }
 
-// Units and planes are counted in 32 bits.
+// Units, planes of G and rows of x's blocks are counted in 32 bits.
 bool list_fits(const Plan &p) {
     // planes are numbered by TMA coordinates
-    if (p.Mp * p.xblocks * 64 / kPlane >= (1ll << 31) || (p.grad && p.Mp * p.piece_cols * p.buffers / kPlane >= (1ll << 31)))
+    if (p.Mp * p.xblocks >= (1ll << 31) || (p.grad && p.Mp * p.piece_cols * p.buffers / kPlane >= (1ll << 31)))
         return false;
     const int64_t tm = p.Mp / kBM, l = (p.V + 127) / 128, t = (p.V + kBM - 1) / kBM + p.pieces;
     return tm * (l + p.pieces) + (t + tm * p.granules) * p.dtiles < (1ll << 31);
@@ -1186,10 +1210,11 @@ template <bool GRAD>
 cudaError_t launch_tiles(const Plan &p, const void *table, void *dtable, int sms, cudaStream_t s) {
     Maps maps;
     cudaError_t err = encode(&maps.w, table, p.D, p.V, 64, 64);
-    if (err == cudaSuccess) err = encode_blocks(&maps.x_k, p.xc, p.Mp * p.xblocks * 64, 16);
+    if (err == cudaSuccess)                              // already in the swizzle's order
+        err = encode_tensor_map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.xc, 64, (uint64_t)(p.Mp * p.xblocks), 128,
+                                   64, 64, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (GRAD) {
         const int64_t n = p.Mp * p.piece_cols * p.buffers;
-        if (err == cudaSuccess) err = encode_blocks(&maps.x_mn, p.xc, p.Mp * p.xblocks * 64, 8);
         if (err == cudaSuccess) err = encode_blocks(&maps.g_k, p.g, n, 16);
         if (err == cudaSuccess) err = encode_blocks(&maps.g_mn, p.g, n, 8);
         if (err == cudaSuccess)
@@ -1198,7 +1223,7 @@ cudaError_t launch_tiles(const Plan &p, const void *table, void *dtable, int sms
                                        CU_TENSOR_MAP_SWIZZLE_128B);
         if (err == cudaSuccess) err = encode(&maps.dt_out, dtable, p.D, p.V, 64, 32);
     } else {
-        maps.x_mn = maps.g_k = maps.g_mn = maps.dt_out = maps.acc = maps.x_k;     // unused
+        maps.g_k = maps.g_mn = maps.dt_out = maps.acc = maps.x;     // unused
     }
     if (err != cudaSuccess) return err;
     auto kern = p.f16 ? xent_tile_kernel<GRAD, true> : xent_tile_kernel<GRAD, false>;
@@ -1213,7 +1238,7 @@ cudaError_t launch_gather(const Plan &p, const ScanArgs &a, const void *x, cudaS
     count_launch(2);
     const cudaError_t err = launch_k(xent_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, 1, p, a);
     if (err != cudaSuccess) return err;
-    return launch_k(xent_gather_kernel, dim3((unsigned)(p.Mp / 128), (unsigned)p.xblocks), dim3(128), 0, s, 1, p,
+    return launch_k(xent_gather_kernel, dim3((unsigned)(p.Mp / 128), (unsigned)p.xblocks), dim3(256), 0, s, 1, p,
                     static_cast<const uint4 *>(x));
 }
 
