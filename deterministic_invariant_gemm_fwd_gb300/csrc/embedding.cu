@@ -7,15 +7,18 @@
 // in that order, in fp32, so that the result does not depend on scheduling
 // (the Carbon README replaces atomics in scatters with sorted indices, "How
 // It Works"):
-//   sort    least-significant-digit radix sort of (id, position) pairs with
-//           digits of at most 9 bits: one histogram kernel, then one stable
-//           scatter kernel per digit that also counts the next digit;
-//   runs    each row's range of sorted positions; every aligned chunk of
-//           kChunk positions that lies within one row's range is summed by a
-//           CTA of its own (a row that very many tokens name is then not one
-//           CTA's work);
-//   sum     a warp per table row: its positions in ascending order, whole
-//           chunks by their sums, one rounding; zeros where there are none.
+//   sort     least-significant-digit radix sort of (id, position) pairs with
+//            digits of at most 9 bits: lists of up to kOneCta tokens in one
+//            CTA's shared memory, longer ones with a histogram kernel and a
+//            stable scatter kernel per digit that also counts the next one.
+//            The other CTAs of these kernels clear the table's gradient,
+//            which takes longer than the sort and does not wait for it.
+//   chunks   a CTA per kChunk sorted positions adds the runs of equal ids in
+//            it: a run that lies within the chunk is a finished row, the
+//            parts of one that goes on in a neighbouring chunk are kept.
+//   joins    the CTA of the chunk in which such a run begins adds its parts in
+//            order.  However often a token occurs, no CTA adds more than
+//            kChunk rows and the parts of one run.
 #include "bounds.cuh"
 #include "device_sync.cuh"
 #include "rowvec.cuh"
@@ -31,8 +34,10 @@ constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigit = 9;             // bits
 constexpr int kBins = 1 << kMaxDigit;
-constexpr int kChunk = 64;               // sorted positions per chunk sum
-constexpr int kSumWarps = 8;             // table rows per CTA of the sum kernel
+constexpr int kOneCta = 8192;            // tokens that one CTA sorts
+constexpr int kOneThreads = 1024;
+constexpr int kChunk = 16;               // sorted positions per chunk
+constexpr int kFillCtas = 152 * 4;       // CTAs that clear the gradient beside a sort kernel
 
 // ---- lookup -------------------------------------------------------------------
 
@@ -95,13 +100,13 @@ SortPlan make_plan(int64_t M, int64_t V) {
     return s;
 }
 
-// Workspace: two (key, position) arrays, a histogram per pass and CTA, the
-// rows' ranges, the chunk sums.
+// Workspace: two (key, position) arrays, a histogram per pass and CTA, and
+// two partial rows per chunk: of a run that began before it, and of one that
+// goes on after it.
 struct Workspace {
     uint32_t *key[2], *pos[2];
     uint32_t *hist;              // [passes][blocks][kBins]
-    uint2 *range;                // [V]
-    float *chunk_sum;            // [M / kChunk][D]
+    float *part;                 // [chunks][2][D]
 };
 
 int64_t round16(int64_t b) { return (b + 15) & ~(int64_t)15; }
@@ -119,11 +124,29 @@ int64_t lay_out(Workspace *w, void *base, int64_t M, int64_t V, int64_t D, const
         t.key[i] = reinterpret_cast<uint32_t *>(take(4 * M));
         t.pos[i] = reinterpret_cast<uint32_t *>(take(4 * M));
     }
-    t.hist = reinterpret_cast<uint32_t *>(take(4 * s.passes * s.blocks * kBins));
-    t.range = reinterpret_cast<uint2 *>(take(8 * V));
-    t.chunk_sum = reinterpret_cast<float *>(take(4 * (M / kChunk) * D));
+    t.hist = reinterpret_cast<uint32_t *>(take(M <= kOneCta ? 0 : 4 * s.passes * s.blocks * kBins));
+    t.part = reinterpret_cast<float *>(take(4 * 2 * ((M + kChunk - 1) / kChunk) * D));
     if (w) *w = t;
     return used;
+}
+
+// Bytes of the gradient that a kernel clears: CTA `cta` of `ctas` takes every
+// ctas-th piece.
+struct Fill {
+    char *base;                  // null: nothing to clear
+    int64_t bytes;
+};
+
+__device__ __forceinline__ void fill(const Fill &f, int64_t cta, int64_t ctas) {
+    if (f.base == nullptr) return;
+    const int64_t head = min((int64_t)((16 - (reinterpret_cast<uintptr_t>(f.base) & 15)) & 15), f.bytes);
+    const int64_t nvec = (f.bytes - head) / 16, tail = head + nvec * 16;
+    uint4 *v = reinterpret_cast<uint4 *>(f.base + head);
+    const int64_t n = ctas * blockDim.x, me = cta * blockDim.x + threadIdx.x;
+#pragma unroll 4
+    for (int64_t i = me; i < nvec; i += n) v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (me < head) f.base[me] = 0;
+    if (me < f.bytes - tail) f.base[tail + me] = 0;
 }
 
 // The sort key of a token: its id, or V for one that adds to no row.
@@ -131,21 +154,134 @@ __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V, int64_t paddin
     return (id >= 0 && id < V && id != padding_idx) ? (uint32_t)id : (uint32_t)V;
 }
 
+// Places of one digit's keys, for the threads of a CTA with W warps: count
+// holds each warp's keys per digit and receives each warp's first place.
+// before[j], total[j]: keys of digit (thread * PER + j) placed ahead of this
+// CTA's, and of all CTAs.
+template <int W, int PER>
+__device__ __forceinline__ void digit_places(uint32_t (*count)[kBins], uint32_t *warp_total,
+                                             const uint32_t (&before)[PER], const uint32_t (&total)[PER]) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint32_t sum = 0u;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) sum += total[j];
+    uint32_t incl = sum;                                  // inclusive scan over the CTA's threads
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_total[warp] = incl;
+    __syncthreads();
+    uint32_t place = incl - sum;
+    for (int w = 0; w < warp; ++w) place += warp_total[w];
+    if (threadIdx.x * PER < kBins) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            uint32_t at = place + before[j];
+#pragma unroll 8
+            for (int w = 0; w < W; ++w) {
+                const uint32_t c = count[w][threadIdx.x * PER + j];
+                count[w][threadIdx.x * PER + j] = at;
+                at += c;
+            }
+            place += total[j];
+        }
+    }
+    __syncthreads();
+}
+
+// Place of this lane's key among the warp's (stable), given the warp's next
+// places per digit, which move on.  digit: out of range where there is none.
+__device__ __forceinline__ uint32_t next_place(uint32_t *place, uint32_t digit, bool have, int lane) {
+    const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+    const int rank = __popc(peers & ((1u << lane) - 1u));
+    const uint32_t at = have ? place[digit] + rank : 0u;
+    __syncwarp();
+    if (have && rank == 0) place[digit] += __popc(peers);
+    __syncwarp();
+    return at;
+}
+
+// The whole sort of a list of at most kOneCta tokens, by CTA 0.
+struct OneSmem {
+    uint32_t count[kOneThreads / 32][kBins];
+    uint32_t key[2][kOneCta];
+    uint16_t pos[2][kOneCta];
+    uint32_t warp_total[kOneThreads / 32];
+};
+
+__global__ void __launch_bounds__(kOneThreads)
+sort_one_kernel(const int64_t *__restrict__ ids, int M, int64_t V, int64_t padding_idx, int digit_bits, int passes,
+                uint32_t *__restrict__ key_out, uint32_t *__restrict__ pos_out, const Fill f) {
+    extern __shared__ __align__(16) uint8_t one_raw[];
+    OneSmem &s = *reinterpret_cast<OneSmem *>(one_raw);
+    wait_prior_grid();
+    allow_next_grid();
+    if (blockIdx.x > 0) {
+        fill(f, blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
+    constexpr int W = kOneThreads / 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t mask = (1u << digit_bits) - 1u;
+    const int per_warp = ((M + W - 1) / W + 31) / 32 * 32, first = warp * per_warp;
+    for (int i = threadIdx.x; i < M; i += kOneThreads) {
+        const int64_t id = ids[i];
+        if (id < 0 || id >= V) atomicExch(&g_embedding_status, (unsigned)CARBON_ERR_OUT_OF_BOUNDS);
+        s.key[0][i] = key_of(id, V, padding_idx);
+        s.pos[0][i] = (uint16_t)i;
+    }
+    for (int p = 0; p < passes; ++p) {
+        const int in = p & 1, shift = p * digit_bits;
+        for (int i = threadIdx.x; i < W * kBins; i += kOneThreads) (&s.count[0][0])[i] = 0u;
+        __syncthreads();
+        for (int r = 0; r < per_warp; r += 32) {
+            const int i = first + r + lane;
+            if (i < M) atomicAdd(&s.count[warp][(s.key[in][i] >> shift) & mask], 1u);
+        }
+        __syncthreads();
+        uint32_t before[1] = {0u}, total[1] = {0u};
+        if (threadIdx.x < kBins) {
+#pragma unroll 8
+            for (int w = 0; w < W; ++w) total[0] += s.count[w][threadIdx.x];
+        }
+        digit_places<W, 1>(s.count, s.warp_total, before, total);
+        for (int r = 0; r < per_warp; r += 32) {
+            const int i = first + r + lane;
+            const bool have = i < M;
+            const uint32_t key = have ? s.key[in][i] : 0u;
+            const uint32_t at = next_place(s.count[warp], have ? (key >> shift) & mask : 0xffffffffu, have, lane);
+            if (have) {
+                if (p + 1 < passes) {
+                    s.key[in ^ 1][at] = key;
+                    s.pos[in ^ 1][at] = s.pos[in][i];
+                } else if (CHK(at, 1, M)) {
+                    key_out[at] = key;
+                    pos_out[at] = s.pos[in][i];
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // Histogram of the first digit of each CTA's tile; clears the later passes'
-// histograms and the rows' ranges.
+// histograms.
 __global__ void __launch_bounds__(kSortThreads)
 sort_start_kernel(const int64_t *__restrict__ ids, int64_t M, int64_t V, int64_t padding_idx, int tile,
-                  int64_t blocks, int digit_bits, int passes, uint32_t *__restrict__ hist,
-                  uint2 *__restrict__ range) {
+                  int64_t blocks, int digit_bits, int passes, uint32_t *__restrict__ hist, const Fill f) {
     __shared__ uint32_t count[kBins];
     wait_prior_grid();
     allow_next_grid();
-    const int64_t nthreads = (int64_t)gridDim.x * kSortThreads;
-    const int64_t me = (int64_t)blockIdx.x * kSortThreads + threadIdx.x;
-    for (int64_t i = me; i < V; i += nthreads) range[i] = make_uint2(0u, 0u);
-    for (int64_t i = blocks * kBins + me; i < passes * blocks * kBins; i += nthreads) hist[i] = 0u;
-    if ((int64_t)blockIdx.x >= blocks) return;            // CTA-uniform
-    for (int d = threadIdx.x; d < kBins; d += kSortThreads) count[d] = 0u;
+    if ((int64_t)blockIdx.x >= blocks) {                  // CTA-uniform
+        fill(f, blockIdx.x - blocks, gridDim.x - blocks);
+        return;
+    }
+    for (int d = threadIdx.x; d < kBins; d += kSortThreads) {
+        count[d] = 0u;
+        for (int p = 1; p < passes; ++p) hist[((int64_t)p * blocks + blockIdx.x) * kBins + d] = 0u;
+    }
     __syncthreads();
     const uint32_t mask = (1u << digit_bits) - 1u;
     const int64_t first = (int64_t)blockIdx.x * tile;
@@ -169,11 +305,15 @@ sort_scatter_kernel(const int64_t *__restrict__ ids, const uint32_t *__restrict_
                     const uint32_t *__restrict__ pos_in, uint32_t *__restrict__ key_out,
                     uint32_t *__restrict__ pos_out, const uint32_t *__restrict__ hist,
                     uint32_t *__restrict__ hist_next, int64_t M, int64_t V, int64_t padding_idx, int tile,
-                    int64_t blocks, int digit_bits, int shift) {
+                    int64_t blocks, int digit_bits, int shift, const Fill f) {
     __shared__ uint32_t count[kSortWarps][kBins];         // per-warp digit counts, then next places
     __shared__ uint32_t warp_total[kSortWarps];
     wait_prior_grid();
     allow_next_grid();
+    if ((int64_t)blockIdx.x >= blocks) {
+        fill(f, blockIdx.x - blocks, gridDim.x - blocks);
+        return;
+    }
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t mask = (1u << digit_bits) - 1u;
     const int per_warp = tile / kSortWarps;               // a multiple of 32
@@ -191,7 +331,7 @@ sort_scatter_kernel(const int64_t *__restrict__ ids, const uint32_t *__restrict_
     __syncthreads();
     // two digits per thread: totals over all CTAs, and over earlier ones
     constexpr int kPer = kBins / kSortThreads;
-    uint32_t before[kPer], total[kPer], sum = 0u;
+    uint32_t before[kPer], total[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) before[j] = total[j] = 0u;
     for (int64_t b = 0; b < blocks; ++b) {
@@ -202,42 +342,12 @@ sort_scatter_kernel(const int64_t *__restrict__ ids, const uint32_t *__restrict_
             total[j] += c;
         }
     }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) sum += total[j];
-    uint32_t incl = sum;                                  // inclusive scan over the CTA's threads
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) warp_total[warp] = incl;
-    __syncthreads();
-    uint32_t place = incl - sum;
-    for (int w = 0; w < warp; ++w) place += warp_total[w];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        uint32_t at = place + before[j];
-#pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t c = count[w][threadIdx.x * kPer + j];
-            count[w][threadIdx.x * kPer + j] = at;
-            at += c;
-        }
-        place += total[j];
-    }
-    __syncthreads();
+    digit_places<kSortWarps, kPer>(count, warp_total, before, total);
     for (int r = 0; r < per_warp; r += 32) {
         const int64_t i = first + r + lane;
         const bool have = i < M;
         const uint32_t key = have ? key_at(i) : 0u;
-        // lanes past the end join no group (their digit is out of range)
-        const uint32_t digit = have ? (key >> shift) & mask : 0xffffffffu;
-        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-        const int rank = __popc(peers & ((1u << lane) - 1u));
-        uint32_t at = have ? count[warp][digit] + rank : 0u;
-        __syncwarp();
-        if (have && rank == 0) count[warp][digit] += __popc(peers);
-        __syncwarp();
+        const uint32_t at = next_place(count[warp], have ? (key >> shift) & mask : 0xffffffffu, have, lane);
         if (have && CHK(at, 1, M)) {
             key_out[at] = key;
             pos_out[at] = FIRST ? (uint32_t)i : pos_in[i];
@@ -250,93 +360,128 @@ sort_scatter_kernel(const int64_t *__restrict__ ids, const uint32_t *__restrict_
 
 // ---- sums -----------------------------------------------------------------------
 
-// Rows' ranges of sorted positions, and the sums of whole chunks.  One CTA
-// per chunk.
+// A finished row: scaled, added to what is there (accumulate), rounded once.
+template <typename T, int N>
+__device__ __forceinline__ void write_row(T *dst, float (&acc)[N], float scale, int accumulate) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] *= scale;
+    if (accumulate) {
+        float old[N];
+        load_f32<T, N>(dst, old);
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] += old[j];
+    }
+    store_f32<T, N>(dst, acc);
+}
+
+// A CTA per chunk; a thread per column vector.  All rows of the chunk are
+// loaded before the first addition.
 template <typename T, int N>
 __global__ void __launch_bounds__(256)
-chunk_sum_kernel(const T *__restrict__ dy, const uint32_t *__restrict__ key, const uint32_t *__restrict__ pos,
-                 uint2 *__restrict__ range, float *__restrict__ chunk_sum, int64_t M, int64_t V, int64_t D) {
+chunk_kernel(T *__restrict__ dtable, const T *__restrict__ dy, const uint32_t *__restrict__ key,
+             const uint32_t *__restrict__ pos, float *__restrict__ part, int64_t M, int64_t V, int64_t D,
+             float scale, int accumulate) {
+    __shared__ uint32_t k[kChunk + 2], m[kChunk];         // k[1 + q]: key of position q; V: none
     wait_prior_grid();
     allow_next_grid();
     const int64_t first = (int64_t)blockIdx.x * kChunk;
-    const int64_t i = first + threadIdx.x;
-    if (threadIdx.x < kChunk && i < M) {
-        const uint32_t k = key[i];
-        if (k < V && CHK(k, 1, V)) {
-            if (i == 0 || key[i - 1] != k) range[k].x = (uint32_t)i;
-            if (i == M - 1 || key[i + 1] != k) range[k].y = (uint32_t)i + 1u;
-        }
+    if (threadIdx.x < kChunk + 2) {
+        const int64_t i = first + (int)threadIdx.x - 1;
+        k[threadIdx.x] = i >= 0 && i < M ? key[i] : (uint32_t)V;
+        if (threadIdx.x >= 1 && threadIdx.x <= kChunk) m[threadIdx.x - 1] = i < M ? pos[i] : 0u;
     }
-    if (first + kChunk > M) return;
-    const uint32_t k = key[first];
-    if (k != key[first + kChunk - 1] || k >= V) return;
+    __syncthreads();
     for (int64_t v = threadIdx.x; v < D / N; v += blockDim.x) {
+        float f[kChunk][N];
+#pragma unroll
+        for (int q = 0; q < kChunk; ++q) {
+            if (k[1 + q] < V && CHK((int64_t)m[q] * D + v * N, N, M * D)) {
+                load_f32<T, N>(dy + (int64_t)m[q] * D + v * N, f[q]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j) f[q][j] = 0.0f;
+            }
+        }
         float acc[N];
+        bool before = k[0] == k[1];                       // the run began in an earlier chunk
 #pragma unroll
         for (int j = 0; j < N; ++j) acc[j] = 0.0f;
-#pragma unroll 8
+#pragma unroll
         for (int q = 0; q < kChunk; ++q) {
-            const int64_t m = pos[first + q];
-            float f[N];
-            if (!CHK(m * D + v * N, N, M * D)) continue;
-            load_f32<T, N>(dy + m * D + v * N, f);
+            const uint32_t id = k[1 + q];
+            if (id >= V) continue;                        // sorted last: nothing follows
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] += f[j];
+            for (int j = 0; j < N; ++j) acc[j] += f[q][j];
+            const bool ends = k[2 + q] != id;
+            if (!ends && q + 1 < kChunk) continue;
+            if (ends && !before) {
+                if (CHK(id, 1, V)) write_row<T, N>(dtable + (int64_t)id * D + v * N, acc, scale, accumulate);
+            } else {                                      // part 0: of a run from before; part 1: of one that goes on
+                float *dst = part + ((int64_t)blockIdx.x * 2 + (before ? 0 : 1)) * D + v * N;
+#pragma unroll
+                for (int j = 0; j < N; ++j) dst[j] = acc[j];
+            }
+            before = false;
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] = 0.0f;
         }
-#pragma unroll
-        for (int j = 0; j < N; ++j) chunk_sum[(first / kChunk) * D + v * N + j] = acc[j];
     }
 }
 
-// A warp per table row.
+// The parts of the run that begins in this CTA's chunk and goes on after it,
+// in order: 4 groups of threads take a quarter of the chunks each, their sums
+// are added in order.
+constexpr int kJoinColumns = 64, kJoinGroups = 4;
+
 template <typename T, int N>
-__global__ void __launch_bounds__(kSumWarps * 32)
-row_sum_kernel(T *__restrict__ dtable, const T *__restrict__ dy, const uint32_t *__restrict__ pos,
-               const uint2 *__restrict__ range, const float *__restrict__ chunk_sum, int64_t M, int64_t V,
-               int64_t D, float scale, int accumulate) {
+__global__ void __launch_bounds__(kJoinColumns * kJoinGroups)
+join_kernel(T *__restrict__ dtable, const uint32_t *__restrict__ key, const float *__restrict__ part, int64_t M,
+            int64_t V, int64_t D, float scale, int accumulate) {
+    __shared__ float sums[kJoinGroups][kJoinColumns][N];
     wait_prior_grid();
     allow_next_grid();
-    const int64_t v = (int64_t)blockIdx.x * kSumWarps + threadIdx.x / 32;
-    if (v >= V) return;
-    const int lane = threadIdx.x % 32;
-    const uint2 r = range[v];
-    T *dst = dtable + v * D;
-    const int64_t nvec = D / N;
-    if (r.x == r.y) {
-        if (accumulate) return;
-        float z[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) z[j] = 0.0f;
-        for (int64_t i = lane; i < nvec; i += 32) store_f32<T, N>(dst + i * N, z);
-        return;
+    const int64_t c = blockIdx.x, next = (c + 1) * kChunk;
+    if (next >= M) return;
+    const uint32_t id = key[next];
+    // CTA-uniform: does a run begin in this chunk and reach the next one?
+    if (id >= V || key[next - 1] != id || (c > 0 && key[c * kChunk] == id && key[c * kChunk - 1] == id)) return;
+    // chunks after c that hold a part of it
+    const int64_t chunks = (M + kChunk - 1) / kChunk;
+    int64_t n = 0;
+    for (;;) {
+        const int64_t e = c + 1 + n + threadIdx.x;
+        const int found = __syncthreads_count(e < chunks && key[e * kChunk] == id);
+        n += found;
+        if (found < (int)blockDim.x) break;
     }
-    for (int64_t i = lane; i < nvec; i += 32) {
+    const int col = threadIdx.x % kJoinColumns, group = threadIdx.x / kJoinColumns;
+    const int64_t per = (n + 1 + kJoinGroups - 1) / kJoinGroups;          // parts per group
+    for (int64_t v0 = 0; v0 < D / N; v0 += kJoinColumns) {
+        const int64_t v = v0 + col;
         float acc[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) acc[j] = 0.0f;
-        for (uint32_t p = r.x; p < r.y;) {
-            float f[N];
-            if (p % kChunk == 0 && p + kChunk <= r.y) {
-                const float *src = chunk_sum + (int64_t)(p / kChunk) * D + i * N;
+        if (v < D / N) {
+            const int64_t to = min(n + 1, (group + 1) * per);
+#pragma unroll 4
+            for (int64_t q = group * per; q < to; ++q) {
+                // part 1 of the first chunk, part 0 of the others
+                const float *src = part + ((c + q) * 2 + (q == 0 ? 1 : 0)) * D + v * N;
 #pragma unroll
-                for (int j = 0; j < N; ++j) f[j] = src[j];
-                p += kChunk;
-            } else {
-                load_f32<T, N>(dy + (int64_t)pos[p] * D + i * N, f);
-                ++p;
+                for (int j = 0; j < N; ++j) acc[j] += src[j];
             }
-#pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] += f[j];
         }
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] *= scale;
-        if (accumulate) {
-            float old[N];
-            load_f32<T, N>(dst + i * N, old);
+        for (int j = 0; j < N; ++j) sums[group][col][j] = acc[j];
+        __syncthreads();
+        if (group == 0 && v < D / N) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] += old[j];
+            for (int g = 1; g < kJoinGroups; ++g)
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[j] += sums[g][col][j];
+            if (CHK(id, 1, V)) write_row<T, N>(dtable + (int64_t)id * D + v * N, acc, scale, accumulate);
         }
-        store_f32<T, N>(dst + i * N, acc);
+        __syncthreads();
     }
 }
 
@@ -361,15 +506,59 @@ cudaError_t launch_fwd(void *out, const void *table, const int64_t *ids, int64_t
 template <typename T, int N>
 cudaError_t launch_sums(void *dtable, const void *dy, const Workspace &w, int sorted, int64_t M, int64_t V,
                         int64_t D, float scale, int accumulate, cudaStream_t s) {
-    count_launch(2);
-    cudaError_t err = launch_k(chunk_sum_kernel<T, N>, dim3((unsigned)((M + kChunk - 1) / kChunk)), dim3(256), 0,
-                               s, 1, static_cast<const T *>(dy), (const uint32_t *)w.key[sorted],
-                               (const uint32_t *)w.pos[sorted], w.range, w.chunk_sum, M, V, D);
-    if (err != cudaSuccess) return err;
-    return launch_k(row_sum_kernel<T, N>, dim3((unsigned)((V + kSumWarps - 1) / kSumWarps)),
-                    dim3(kSumWarps * 32), 0, s, 1, static_cast<T *>(dtable), static_cast<const T *>(dy),
-                    (const uint32_t *)w.pos[sorted], (const uint2 *)w.range, (const float *)w.chunk_sum, M, V, D,
-                    scale, accumulate);
+    const dim3 chunks((unsigned)((M + kChunk - 1) / kChunk));
+    const int64_t threads = (D / N + 31) / 32 * 32;
+    count_launch();
+    cudaError_t err = launch_k(chunk_kernel<T, N>, chunks, dim3((unsigned)(threads < 64 ? 64 : threads < 256 ? threads : 256)),
+                               0, s, 1, static_cast<T *>(dtable), static_cast<const T *>(dy),
+                               (const uint32_t *)w.key[sorted], (const uint32_t *)w.pos[sorted], w.part, M, V, D, scale,
+                               accumulate);
+    if (err != cudaSuccess || M <= kChunk) return err;    // one chunk: no run goes on
+    count_launch();
+    return launch_k(join_kernel<T, N>, chunks, dim3(kJoinColumns * kJoinGroups), 0, s, 1, static_cast<T *>(dtable),
+                    (const uint32_t *)w.key[sorted], (const float *)w.part, M, V, D, scale, accumulate);
+}
+
+// The kernels of the sort, each clearing its share of the gradient.
+cudaError_t launch_sort(const Workspace &w, const SortPlan &plan, const int64_t *ids, int64_t M, int64_t V,
+                        int64_t padding_idx, char *clear, int64_t clear_bytes, int *sorted, cudaStream_t s) {
+    cudaError_t err;
+    auto fill_ctas = [&](int64_t bytes) {                 // at least 16 KiB per CTA
+        const int64_t n = (bytes + 16383) / 16384;
+        return clear == nullptr ? 0 : n < kFillCtas ? n : (int64_t)kFillCtas;
+    };
+    if (M <= kOneCta) {
+        *sorted = 0;
+        if ((err = cudaFuncSetAttribute(sort_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)sizeof(OneSmem))) != cudaSuccess)
+            return err;
+        count_launch();
+        // its shared memory leaves room for one CTA per SM
+        const int64_t clearing = fill_ctas(clear_bytes);
+        return launch_k(sort_one_kernel, dim3((unsigned)(1 + (clearing < 151 ? clearing : 151))), dim3(kOneThreads), sizeof(OneSmem),
+                        s, 1, ids, (int)M, V, padding_idx, plan.digit_bits, plan.passes, w.key[0], w.pos[0],
+                        Fill{clear, clear_bytes});
+    }
+    *sorted = (plan.passes - 1) & 1;
+    const int64_t share = (clear_bytes / (plan.passes + 1) + 15) & ~(int64_t)15;
+    auto part = [&](int i) {                              // of kernel i
+        const int64_t from = share * i < clear_bytes ? share * i : clear_bytes;
+        const int64_t to = i == plan.passes || from + share > clear_bytes ? clear_bytes : from + share;
+        return Fill{clear == nullptr ? nullptr : clear + from, to - from};
+    };
+    count_launch(1 + plan.passes);
+    err = launch_k(sort_start_kernel, dim3((unsigned)(plan.blocks + fill_ctas(share))), dim3(kSortThreads), 0, s, 1, ids, M,
+                   V, padding_idx, plan.tile, plan.blocks, plan.digit_bits, plan.passes, w.hist, part(0));
+    for (int p = 0; p < plan.passes && err == cudaSuccess; ++p) {
+        const uint32_t *h = w.hist + (int64_t)p * plan.blocks * kBins;
+        uint32_t *next = p + 1 < plan.passes ? w.hist + (int64_t)(p + 1) * plan.blocks * kBins : nullptr;
+        auto kern = p == 0 ? sort_scatter_kernel<true> : sort_scatter_kernel<false>;
+        err = launch_k(kern, dim3((unsigned)(plan.blocks + fill_ctas(share))), dim3(kSortThreads), 0, s, 1, ids,
+                       (const uint32_t *)w.key[(p + 1) & 1], (const uint32_t *)w.pos[(p + 1) & 1], w.key[p & 1],
+                       w.pos[p & 1], h, next, M, V, padding_idx, plan.tile, plan.blocks, plan.digit_bits,
+                       p * plan.digit_bits, part(p + 1));
+    }
+    return err;
 }
 
 }  // namespace
@@ -436,24 +625,10 @@ carbon_status_t carbon_embedding_bwd(void *dtable, const void *dy, const int64_t
         return note_cuda(cudaMemsetAsync(dtable, 0, (size_t)(V * D) * dtype_size(dtype), s));
     }
 
-    // enough CTAs to clear the ranges quickly as well
-    const int64_t clear = (V + 4 * kSortThreads - 1) / (4 * kSortThreads);
-    const int64_t grid0 = plan.blocks > clear ? plan.blocks : (clear < 1024 ? clear : (plan.blocks > 1024 ? plan.blocks : 1024));
-    count_launch();
-    cudaError_t err = launch_k(sort_start_kernel, dim3((unsigned)grid0), dim3(kSortThreads), 0, s, 1, ids, M, V,
-                               padding_idx, plan.tile, plan.blocks, plan.digit_bits, plan.passes, w.hist, w.range);
-    for (int p = 0; p < plan.passes && err == cudaSuccess; ++p) {
-        const uint32_t *h = w.hist + (int64_t)p * plan.blocks * kBins;
-        uint32_t *next = p + 1 < plan.passes ? w.hist + (int64_t)(p + 1) * plan.blocks * kBins : nullptr;
-        auto kern = p == 0 ? sort_scatter_kernel<true> : sort_scatter_kernel<false>;
-        count_launch();
-        err = launch_k(kern, dim3((unsigned)plan.blocks), dim3(kSortThreads), 0, s, 1, ids,
-                       (const uint32_t *)w.key[(p + 1) & 1], (const uint32_t *)w.pos[(p + 1) & 1], w.key[p & 1],
-                       w.pos[p & 1], h, next, M, V, padding_idx, plan.tile, plan.blocks, plan.digit_bits,
-                       p * plan.digit_bits);
-    }
+    int sorted = 0;
+    cudaError_t err = launch_sort(w, plan, ids, M, V, padding_idx, accumulate ? nullptr : static_cast<char *>(dtable),
+                                  accumulate ? 0 : V * D * (int64_t)dtype_size(dtype), &sorted, s);
     if (err != cudaSuccess) return note_cuda(err);
-    const int sorted = (plan.passes - 1) & 1;
     const bool vec = (D * dtype_size(dtype)) % 16 == 0 && aligned16(dtable) && aligned16(dy);
     switch (dtype) {
     case CARBON_F32: err = vec ? launch_sums<float, 4>(dtable, dy, w, sorted, M, V, D, scale, accumulate, s)
