@@ -106,6 +106,7 @@ SortPlan make_plan(int64_t M, int64_t V) {
 struct Workspace {
     uint32_t *key[2], *pos[2];
     uint32_t *hist;              // [passes][blocks][kBins]
+    uint32_t *jobs;              // their count, then the chunks in which a run begins that goes on
     float *part;                 // [chunks][2][D]
 };
 
@@ -125,6 +126,7 @@ int64_t lay_out(Workspace *w, void *base, int64_t M, int64_t V, int64_t D, const
         t.pos[i] = reinterpret_cast<uint32_t *>(take(4 * M));
     }
     t.hist = reinterpret_cast<uint32_t *>(take(M <= kOneCta ? 0 : 4 * s.passes * s.blocks * kBins));
+    t.jobs = reinterpret_cast<uint32_t *>(take(4 * (1 + (M + kChunk - 1) / kChunk)));
     t.part = reinterpret_cast<float *>(take(4 * 2 * ((M + kChunk - 1) / kChunk) * D));
     if (w) *w = t;
     return used;
@@ -213,7 +215,7 @@ struct OneSmem {
 
 __global__ void __launch_bounds__(kOneThreads)
 sort_one_kernel(const int64_t *__restrict__ ids, int M, int64_t V, int64_t padding_idx, int digit_bits, int passes,
-                uint32_t *__restrict__ key_out, uint32_t *__restrict__ pos_out, const Fill f) {
+                uint32_t *__restrict__ key_out, uint32_t *__restrict__ pos_out, uint32_t *__restrict__ jobs, const Fill f) {
     extern __shared__ __align__(16) uint8_t one_raw[];
     OneSmem &s = *reinterpret_cast<OneSmem *>(one_raw);
     wait_prior_grid();
@@ -224,6 +226,7 @@ sort_one_kernel(const int64_t *__restrict__ ids, int M, int64_t V, int64_t paddi
     }
     constexpr int W = kOneThreads / 32;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) jobs[0] = 0u;
     const uint32_t mask = (1u << digit_bits) - 1u;
     const int per_warp = ((M + W - 1) / W + 31) / 32 * 32, first = warp * per_warp;
     for (int i = threadIdx.x; i < M; i += kOneThreads) {
@@ -270,7 +273,8 @@ sort_one_kernel(const int64_t *__restrict__ ids, int M, int64_t V, int64_t paddi
 // histograms.
 __global__ void __launch_bounds__(kSortThreads)
 sort_start_kernel(const int64_t *__restrict__ ids, int64_t M, int64_t V, int64_t padding_idx, int tile,
-                  int64_t blocks, int digit_bits, int passes, uint32_t *__restrict__ hist, const Fill f) {
+                  int64_t blocks, int digit_bits, int passes, uint32_t *__restrict__ hist,
+                  uint32_t *__restrict__ jobs, const Fill f) {
     __shared__ uint32_t count[kBins];
     wait_prior_grid();
     allow_next_grid();
@@ -278,6 +282,7 @@ sort_start_kernel(const int64_t *__restrict__ ids, int64_t M, int64_t V, int64_t
         fill(f, blockIdx.x - blocks, gridDim.x - blocks);
         return;
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) jobs[0] = 0u;
     for (int d = threadIdx.x; d < kBins; d += kSortThreads) {
         count[d] = 0u;
         for (int p = 1; p < passes; ++p) hist[((int64_t)p * blocks + blockIdx.x) * kBins + d] = 0u;
@@ -379,8 +384,8 @@ __device__ __forceinline__ void write_row(T *dst, float (&acc)[N], float scale, 
 template <typename T, int N>
 __global__ void __launch_bounds__(256)
 chunk_kernel(T *__restrict__ dtable, const T *__restrict__ dy, const uint32_t *__restrict__ key,
-             const uint32_t *__restrict__ pos, float *__restrict__ part, int64_t M, int64_t V, int64_t D,
-             float scale, int accumulate) {
+             const uint32_t *__restrict__ pos, uint32_t *__restrict__ jobs, float *__restrict__ part, int64_t M,
+             int64_t V, int64_t D, float scale, int accumulate) {
     __shared__ uint32_t k[kChunk + 2], m[kChunk];         // k[1 + q]: key of position q; V: none
     wait_prior_grid();
     allow_next_grid();
@@ -391,17 +396,15 @@ chunk_kernel(T *__restrict__ dtable, const T *__restrict__ dy, const uint32_t *_
         if (threadIdx.x >= 1 && threadIdx.x <= kChunk) m[threadIdx.x - 1] = i < M ? pos[i] : 0u;
     }
     __syncthreads();
+    // does a run begin here and go on? (the list's order does not matter: its runs are separate rows)
+    if (threadIdx.x == 0 && k[kChunk] < V && k[kChunk + 1] == k[kChunk] && (k[1] != k[kChunk] || k[0] != k[1]))
+        jobs[1 + atomicAdd(jobs, 1u)] = blockIdx.x;
     for (int64_t v = threadIdx.x; v < D / N; v += blockDim.x) {
-        float f[kChunk][N];
+        Pack<T, N> rows[kChunk];
 #pragma unroll
-        for (int q = 0; q < kChunk; ++q) {
-            if (k[1 + q] < V && CHK((int64_t)m[q] * D + v * N, N, M * D)) {
-                load_f32<T, N>(dy + (int64_t)m[q] * D + v * N, f[q]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; ++j) f[q][j] = 0.0f;
-            }
-        }
+        for (int q = 0; q < kChunk; ++q)
+            if (k[1 + q] < V && CHK((int64_t)m[q] * D + v * N, N, M * D))
+                rows[q] = *reinterpret_cast<const Pack<T, N> *>(dy + (int64_t)m[q] * D + v * N);
         float acc[N];
         bool before = k[0] == k[1];                       // the run began in an earlier chunk
 #pragma unroll
@@ -410,8 +413,10 @@ chunk_kernel(T *__restrict__ dtable, const T *__restrict__ dy, const uint32_t *_
         for (int q = 0; q < kChunk; ++q) {
             const uint32_t id = k[1 + q];
             if (id >= V) continue;                        // sorted last: nothing follows
+            float f[N];
+            widen(rows[q], f);
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] += f[q][j];
+            for (int j = 0; j < N; ++j) acc[j] += f[j];
             const bool ends = k[2 + q] != id;
             if (!ends && q + 1 < kChunk) continue;
             if (ends && !before) {
@@ -428,57 +433,55 @@ chunk_kernel(T *__restrict__ dtable, const T *__restrict__ dy, const uint32_t *_
     }
 }
 
-// The parts of the run that begins in this CTA's chunk and goes on after it,
-// in order: 4 groups of threads take a quarter of the chunks each, their sums
-// are added in order.
-constexpr int kJoinColumns = 64, kJoinGroups = 4;
+// A run that goes on after its first chunk: its parts in order.  A CTA takes 64
+// columns of a run at a time; 16 threads per vector of columns take a
+// sixteenth of the parts each, and their sums are added in order.
+constexpr int kJoinVec = 4, kJoinThreads = 256, kJoinColumns = 16, kJoinGroups = kJoinThreads / kJoinColumns;
 
 template <typename T, int N>
-__global__ void __launch_bounds__(kJoinColumns * kJoinGroups)
-join_kernel(T *__restrict__ dtable, const uint32_t *__restrict__ key, const float *__restrict__ part, int64_t M,
-            int64_t V, int64_t D, float scale, int accumulate) {
+__global__ void __launch_bounds__(kJoinThreads)
+join_kernel(T *__restrict__ dtable, const uint32_t *__restrict__ key, const uint32_t *__restrict__ jobs,
+            const float *__restrict__ part, int64_t M, int64_t V, int64_t D, float scale, int accumulate) {
+    static_assert(N == 1 || N == kJoinVec, "columns per thread");
     __shared__ float sums[kJoinGroups][kJoinColumns][N];
     wait_prior_grid();
     allow_next_grid();
-    const int64_t c = blockIdx.x, next = (c + 1) * kChunk;
-    if (next >= M) return;
-    const uint32_t id = key[next];
-    // CTA-uniform: does a run begin in this chunk and reach the next one?
-    if (id >= V || key[next - 1] != id || (c > 0 && key[c * kChunk] == id && key[c * kChunk - 1] == id)) return;
-    // chunks after c that hold a part of it
     const int64_t chunks = (M + kChunk - 1) / kChunk;
-    int64_t n = 0;
-    for (;;) {
-        const int64_t e = c + 1 + n + threadIdx.x;
-        const int found = __syncthreads_count(e < chunks && key[e * kChunk] == id);
-        n += found;
-        if (found < (int)blockDim.x) break;
-    }
-    const int col = threadIdx.x % kJoinColumns, group = threadIdx.x / kJoinColumns;
-    const int64_t per = (n + 1 + kJoinGroups - 1) / kJoinGroups;          // parts per group
-    for (int64_t v0 = 0; v0 < D / N; v0 += kJoinColumns) {
-        const int64_t v = v0 + col;
+    const int64_t blocks = (D / N + kJoinColumns - 1) / kJoinColumns, work = (int64_t)jobs[0] * blocks;
+    for (int64_t j = blockIdx.x; j < work; j += gridDim.x) {
+        const int64_t c = jobs[1 + j / blocks];
+        const uint32_t id = key[(c + 1) * kChunk];
+        int64_t n = 0;                                    // chunks after c that hold a part
+        for (;;) {
+            const int64_t e = c + 1 + n + threadIdx.x;
+            const int found = __syncthreads_count(e < chunks && key[e * kChunk] == id);
+            n += found;
+            if (found < kJoinThreads) break;
+        }
+        const int col = threadIdx.x % kJoinColumns, group = threadIdx.x / kJoinColumns;
+        const int64_t v = j % blocks * kJoinColumns + col, per = (n + 1 + kJoinGroups - 1) / kJoinGroups;
         float acc[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+        for (int q = 0; q < N; ++q) acc[q] = 0.0f;
         if (v < D / N) {
             const int64_t to = min(n + 1, (group + 1) * per);
 #pragma unroll 4
             for (int64_t q = group * per; q < to; ++q) {
                 // part 1 of the first chunk, part 0 of the others
-                const float *src = part + ((c + q) * 2 + (q == 0 ? 1 : 0)) * D + v * N;
+                const Pack<float, N> src =
+                    *reinterpret_cast<const Pack<float, N> *>(part + ((c + q) * 2 + (q == 0 ? 1 : 0)) * D + v * N);
 #pragma unroll
-                for (int j = 0; j < N; ++j) acc[j] += src[j];
+                for (int i = 0; i < N; ++i) acc[i] += src.e[i];
             }
         }
 #pragma unroll
-        for (int j = 0; j < N; ++j) sums[group][col][j] = acc[j];
+        for (int i = 0; i < N; ++i) sums[group][col][i] = acc[i];
         __syncthreads();
         if (group == 0 && v < D / N) {
 #pragma unroll
             for (int g = 1; g < kJoinGroups; ++g)
 #pragma unroll
-                for (int j = 0; j < N; ++j) acc[j] += sums[g][col][j];
+                for (int i = 0; i < N; ++i) acc[i] += sums[g][col][i];
             if (CHK(id, 1, V)) write_row<T, N>(dtable + (int64_t)id * D + v * N, acc, scale, accumulate);
         }
         __syncthreads();
@@ -511,12 +514,16 @@ cudaError_t launch_sums(void *dtable, const void *dy, const Workspace &w, int so
     count_launch();
     cudaError_t err = launch_k(chunk_kernel<T, N>, chunks, dim3((unsigned)(threads < 64 ? 64 : threads < 256 ? threads : 256)),
                                0, s, 1, static_cast<T *>(dtable), static_cast<const T *>(dy),
-                               (const uint32_t *)w.key[sorted], (const uint32_t *)w.pos[sorted], w.part, M, V, D, scale,
-                               accumulate);
+                               (const uint32_t *)w.key[sorted], (const uint32_t *)w.pos[sorted], w.jobs, w.part, M, V, D,
+                               scale, accumulate);
     if (err != cudaSuccess || M <= kChunk) return err;    // one chunk: no run goes on
     count_launch();
-    return launch_k(join_kernel<T, N>, chunks, dim3(kJoinColumns * kJoinGroups), 0, s, 1, static_cast<T *>(dtable),
-                    (const uint32_t *)w.key[sorted], (const float *)w.part, M, V, D, scale, accumulate);
+    // vectors of 4 columns where a row of the parts and of the table starts on their boundary
+    constexpr int J = N == 1 ? 1 : kJoinVec;
+    const int64_t most = (int64_t)chunks.x * ((D / J + kJoinColumns - 1) / kJoinColumns);
+    return launch_k(join_kernel<T, J>, dim3((unsigned)(most < 152 * 4 ? most : 152 * 4)), dim3(kJoinThreads), 0, s, 1,
+                    static_cast<T *>(dtable), (const uint32_t *)w.key[sorted], (const uint32_t *)w.jobs,
+                    (const float *)w.part, M, V, D, scale, accumulate);
 }
 
 // The kernels of the sort, each clearing its share of the gradient.
@@ -537,7 +544,7 @@ cudaError_t launch_sort(const Workspace &w, const SortPlan &plan, const int64_t 
         const int64_t clearing = fill_ctas(clear_bytes);
         return launch_k(sort_one_kernel, dim3((unsigned)(1 + (clearing < 151 ? clearing : 151))), dim3(kOneThreads), sizeof(OneSmem),
                         s, 1, ids, (int)M, V, padding_idx, plan.digit_bits, plan.passes, w.key[0], w.pos[0],
-                        Fill{clear, clear_bytes});
+                        w.jobs, Fill{clear, clear_bytes});
     }
     *sorted = (plan.passes - 1) & 1;
     const int64_t share = (clear_bytes / (plan.passes + 1) + 15) & ~(int64_t)15;
@@ -548,7 +555,7 @@ cudaError_t launch_sort(const Workspace &w, const SortPlan &plan, const int64_t 
     };
     count_launch(1 + plan.passes);
     err = launch_k(sort_start_kernel, dim3((unsigned)(plan.blocks + fill_ctas(share))), dim3(kSortThreads), 0, s, 1, ids, M,
-                   V, padding_idx, plan.tile, plan.blocks, plan.digit_bits, plan.passes, w.hist, part(0));
+                   V, padding_idx, plan.tile, plan.blocks, plan.digit_bits, plan.passes, w.hist, w.jobs, part(0));
     for (int p = 0; p < plan.passes && err == cudaSuccess; ++p) {
         const uint32_t *h = w.hist + (int64_t)p * plan.blocks * kBins;
         uint32_t *next = p + 1 < plan.passes ? w.hist + (int64_t)(p + 1) * plan.blocks * kBins : nullptr;

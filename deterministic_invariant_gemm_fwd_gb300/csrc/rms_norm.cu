@@ -19,6 +19,8 @@
 #include "device_sync.cuh"
 #include "rowvec.cuh"
 
+#include <type_traits>
+
 namespace carbon {
 namespace {
 
@@ -242,15 +244,11 @@ struct BwdArgs {
     int64_t M, D;
 };
 
-template <int N>
-__device__ __forceinline__ void load_codes(const int8_t *p, float (&f)[N]) {
-    const Pack<int8_t, N> v = *reinterpret_cast<const Pack<int8_t, N> *>(p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = (float)v.e[i];
-}
-
+// A group holds a row of n's source, dy and dh as they were loaded (all three
+// are in flight before the first is used) and widens them where they are
+// needed; the sum over the row is the only wait in between.
 template <typename T, int G, int N, int H, bool CODES>
-__global__ void __launch_bounds__(G > 256 ? G : 256)
+__global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : 2)
 norm_bwd_kernel(const BwdArgs<T> a) {
     constexpr int kThreads = G > 256 ? G : 256, kRows = kThreads / G;
     __shared__ float buf[kThreads / 32];
@@ -271,41 +269,38 @@ norm_bwd_kernel(const BwdArgs<T> a) {
         const int64_t m = r0 + group;
         const bool live = m < a.M;
         const int64_t row = (live ? m : 0) * a.D;
-        const float rstd = live ? a.rstd[m] : 0.0f;
-        const float factor = !live ? 0.0f : (CODES ? a.scales[m] : rstd);
-        float n[H][N], gdy[H][N];
-        float dot = 0.0f;
+        using Source = typename std::conditional<CODES, int8_t, T>::type;
+        const Source *source = CODES ? reinterpret_cast<const Source *>(a.codes) : reinterpret_cast<const Source *>(a.h);
+        Pack<Source, N> ns[H];
+        Pack<T, N> dys[H], dhs[H];
 #pragma unroll
         for (int u = 0; u < H; ++u) {
             const int i = t + G * u;
             if (i < nvec && live && CHK(row + i * N, N, a.M * a.D)) {
-                if (CODES) load_codes<N>(a.codes + row + i * N, n[u]);
-                else load_f32<T, N>(a.h + row + i * N, n[u]);
-                load_f32<T, N>(a.dy + row + i * N, gdy[u]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < N; ++k) n[u][k] = gdy[u][k] = 0.0f;
+                ns[u] = *reinterpret_cast<const Pack<Source, N> *>(source + row + i * N);
+                dys[u] = *reinterpret_cast<const Pack<T, N> *>(a.dy + row + i * N);
+                if (a.dh) dhs[u] = *reinterpret_cast<const Pack<T, N> *>(a.dh + row + i * N);
             }
         }
+        const float rstd = live ? a.rstd[m] : 0.0f;
+        const float factor = !live ? 0.0f : (CODES ? a.scales[m] : rstd);
+        float dot = 0.0f;
 #pragma unroll
         for (int u = 0; u < H; ++u) {
             const int i = t + G * u;
             if (i < nvec && live) {
-                float g[N];
+                float g[N], n[N], dy[N], y[N];
                 load_f32<T, N>(a.gamma + i * N, g);
-                if (a.y_out) {
-                    float y[N];
-#pragma unroll
-                    for (int k = 0; k < N; ++k) y[k] = n[u][k] * factor * g[k];
-                    store_f32<T, N>(a.y_out + row + i * N, y);
-                }
+                widen(ns[u], n);
+                widen(dys[u], dy);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    n[u][k] *= factor;
-                    dg[u][k] = fmaf(gdy[u][k], n[u][k], dg[u][k]);
-                    gdy[u][k] *= g[k];
-                    dot = fmaf(gdy[u][k], n[u][k], dot);
+                    n[k] *= factor;
+                    y[k] = n[k] * g[k];
+                    dg[u][k] = fmaf(dy[k], n[k], dg[u][k]);
+                    dot = fmaf(dy[k] * g[k], n[k], dot);
                 }
+                if (a.y_out) store_f32<T, N>(a.y_out + row + i * N, y);
             }
         }
         dot = group_sum<G>(dot, buf);
@@ -315,15 +310,19 @@ norm_bwd_kernel(const BwdArgs<T> a) {
             for (int u = 0; u < H; ++u) {
                 const int i = t + G * u;
                 if (i < nvec) {
-                    float d[N];
+                    float g[N], n[N], dy[N], d[N];
+                    load_f32<T, N>(a.gamma + i * N, g);
+                    widen(ns[u], n);
+                    widen(dys[u], dy);
                     if (a.dh) {
-                        load_f32<T, N>(a.dh + row + i * N, d);
+                        widen(dhs[u], d);
                     } else {
 #pragma unroll
                         for (int k = 0; k < N; ++k) d[k] = 0.0f;
                     }
 #pragma unroll
-                    for (int k = 0; k < N; ++k) d[k] = fmaf(rstd, fmaf(-n[u][k], mean, gdy[u][k]), d[k]);
+                    for (int k = 0; k < N; ++k)
+                        d[k] = fmaf(rstd, fmaf(-(n[k] * factor), mean, dy[k] * g[k]), d[k]);
                     store_f32<T, N>(a.dx + row + i * N, d);
                 }
             }
@@ -391,27 +390,29 @@ norm_bwd_long_kernel(const BwdArgs<T> a) {
     }
 }
 
-// dgamma[j] = sum over the CTAs' partial rows, in order: 8 threads per column
-// take every 8th row, their sums are added in thread order.
+// dgamma[j] = sum over the CTAs' partial rows: 32 threads per column take
+// every 32nd row, in order, and their sums are added in thread order.
+constexpr int kGammaRows = 32;
+
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kGammaRows)
 dgamma_kernel(T *__restrict__ dgamma, const float *__restrict__ partial, int rows, int64_t D) {
-    __shared__ float part[8][33];
+    __shared__ float part[kGammaRows][33];
     wait_prior_grid();
     allow_next_grid();
     const int c = threadIdx.x % 32, r = threadIdx.x / 32;
     const int64_t j = (int64_t)blockIdx.x * 32 + c;
     float s = 0.0f;
     if (j < D) {
-#pragma unroll 8
-        for (int i = r; i < rows; i += 8)
+#pragma unroll 10
+        for (int i = r; i < rows; i += kGammaRows)
             if (CHK((int64_t)i * D + j, 1, rows * D)) s += partial[(int64_t)i * D + j];
     }
     part[r][c] = s;
     __syncthreads();
     if (r == 0 && j < D) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += part[i][c];
+        for (int i = 1; i < kGammaRows; ++i) s += part[i][c];
         dgamma[j] = from_f32<T>(s);
     }
 }
@@ -428,7 +429,7 @@ norm_expand_kernel(T *__restrict__ out, const int8_t *__restrict__ codes, const 
         if (!CHK(i * N, N, M * D)) continue;
         const float s = scales[m];
         float f[N];
-        load_codes<N>(codes + i * N, f);
+        widen(*reinterpret_cast<const Pack<int8_t, N> *>(codes + i * N), f);
 #pragma unroll
         for (int k = 0; k < N; ++k) f[k] *= s;
         if (gamma) {
@@ -451,18 +452,34 @@ bool sizes_ok(int64_t M, int64_t D) {
 
 bool dtype_ok(int dtype) { return dtype == CARBON_F32 || dtype == CARBON_BF16 || dtype == CARBON_F16; }
 
-// Calls f.template operator()<G, N, H>() for the group that holds a row of D
-// elements: vectors of N, at most kMaxHold elements per thread.  Returns
-// false where none does.
+// Calls f(G, H) for the group that holds a row of D elements: G threads with H
+// vectors of N each, at most kMaxHold elements per thread.  Returns false
+// where none does.
 template <int N, typename F>
 bool with_group(int64_t D, F &&f) {
+    using std::integral_constant;
     const int64_t nvec = D / N;
     constexpr int H = kMaxHold / N;
-    if (nvec <= 32) { f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>()); return true; }
-    if (nvec <= 32 * H) { f(std::integral_constant<int, 32>(), std::integral_constant<int, H>()); return true; }
-    if (nvec <= 128 * H) { f(std::integral_constant<int, 128>(), std::integral_constant<int, H>()); return true; }
-    if (nvec <= 512 * H) { f(std::integral_constant<int, 512>(), std::integral_constant<int, H>()); return true; }
-    return false;
+    auto held = [&](auto g) {                             // fewest vectors per thread that hold the row
+        constexpr int G = g();
+        if (nvec > G * H) return false;
+        if constexpr (H == 8) {                           // fp32 vectors
+            if (nvec <= G * 2) f(g, integral_constant<int, 2>());
+            else if (nvec <= G * 4) f(g, integral_constant<int, 4>());
+            else if (nvec <= G * 6) f(g, integral_constant<int, 6>());
+            else f(g, integral_constant<int, 8>());
+        } else if constexpr (H == 4) {
+            if (nvec <= G) f(g, integral_constant<int, 1>());
+            else if (nvec <= G * 2) f(g, integral_constant<int, 2>());
+            else if (nvec <= G * 3) f(g, integral_constant<int, 3>());
+            else f(g, integral_constant<int, 4>());
+        } else {
+            if (nvec <= G * (H / 4)) f(g, integral_constant<int, H / 4>());
+            else f(g, integral_constant<int, H>());
+        }
+        return true;
+    };
+    return held(integral_constant<int, 32>()) || held(integral_constant<int, 128>()) || held(integral_constant<int, 512>());
 }
 
 template <typename T, int N>
@@ -488,9 +505,9 @@ cudaError_t run_fwd(const FwdArgs<T> &a, cudaStream_t s) {
     return vec ? launch_fwd<T, N>(a, s) : launch_fwd<T, 1>(a, s);
 }
 
-// CTAs of the gradient kernels: enough to fill 152 SMs several times over,
-// and no more partial rows than that.
-constexpr int kBwdCtas = 152 * 4;
+// CTAs of the gradient kernels: two per SM, as their registers allow, and no
+// more partial rows than that.
+constexpr int kBwdCtas = 152 * 2;
 
 template <typename T, int N, bool CODES>
 cudaError_t launch_bwd(const BwdArgs<T> &a, T *dgamma, cudaStream_t s) {
@@ -513,7 +530,7 @@ cudaError_t launch_bwd(const BwdArgs<T> &a, T *dgamma, cudaStream_t s) {
     }
     if (err != cudaSuccess || !a.partial) return err;
     count_launch();
-    return launch_k(dgamma_kernel<T>, dim3((unsigned)((a.D + 31) / 32)), dim3(256), 0, s, 1, dgamma,
+    return launch_k(dgamma_kernel<T>, dim3((unsigned)((a.D + 31) / 32)), dim3(32 * kGammaRows), 0, s, 1, dgamma,
                     (const float *)a.partial, ctas, a.D);
 }
 

@@ -14,6 +14,7 @@ namespace carbon {
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(int8_t v) { return (float)v; }
 
 // One rounding, to nearest-even.
 template <typename T>
@@ -35,11 +36,16 @@ struct alignas(sizeof(T) * N) Pack {
 template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);
 
+// By value: one access where v is in memory.
 template <typename T, int N>
-__device__ __forceinline__ void load_f32(const T *p, float (&f)[N]) {
-    const Pack<T, N> v = *reinterpret_cast<const Pack<T, N> *>(p);
+__device__ __forceinline__ void widen(const Pack<T, N> v, float (&f)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = to_f32(v.e[i]);
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void load_f32(const T *p, float (&f)[N]) {
+    widen(*reinterpret_cast<const Pack<T, N> *>(p), f);
 }
 
 template <typename T, int N>

@@ -14,7 +14,6 @@ from typing import NamedTuple, Optional
 
 from . import _binding as _b
 
-
 _CODES = {"torch.float32": _b.F32, "torch.bfloat16": _b.BF16, "torch.float16": _b.F16}
 
 
@@ -26,62 +25,83 @@ def _dtype(name, t):
 
 
 def _need(name, t, shape, dtype):
-    """A contiguous CUDA tensor of this shape and dtype."""
-    if t.dtype != dtype:
+    """Raises unless t is a contiguous CUDA tensor of this shape and dtype."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda or not t.is_contiguous():
+    if not (t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
 
 
 def _rows(name, t):
-    if t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+    if t.dim() != 2 or not (t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous 2-D CUDA tensor")
     return t.shape
 
 
-class _Launch:
-    """The stream of a call: its handle, and the outputs and workspace that
-    belong to it.  On a stream other than the current one the workspace is
-    taken under that stream, and the outputs are marked as used there, so
-    that the allocator hands neither out again while the kernels run."""
+class _On:
+    """Allocation on a stream that is not the current one: outputs and
+    workspace are taken under it, so that neither is memory that the current
+    stream still works on.  They belong to that stream, as any tensor made
+    under it."""
 
     def __init__(self, stream):
-        import torch
-        current = torch.cuda.current_stream()
-        if stream is None:
-            stream = current
-        elif isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-        self.stream, self.handle = stream, stream.cuda_stream
-        self.other = self.handle != current.cuda_stream
+        self.stream = stream
 
-    def out(self, shape, dtype, device):
+    def empty(self, shape, dtype, device):
         import torch
-        t = torch.empty(shape, dtype=dtype, device=device)
-        if self.other:
-            t.record_stream(self.stream)
-        return t
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=device)
 
     def workspace(self, nbytes, device):
         import torch
-        if nbytes < 0:
-            raise ValueError("sizes out of range")
-        if not self.other:
-            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        return self.empty(nbytes, torch.uint8, device)
+
+
+def _begin(t, stream):
+    """(stream handle, allocation of outputs, of a workspace) of a call whose
+    operands are on t's device."""
+    import torch
+    device = t.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError("the operands must be on the current CUDA device")
+    current = torch._C._cuda_getCurrentRawStream(device)
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        if stream.cuda_stream != current:
+            on = _On(stream)
+            return stream.cuda_stream, on.empty, on.workspace
+    return current, _empty, _workspace
+
+
+def _empty(shape, dtype, device):
+    import torch
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(nbytes, device):
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _bytes(nbytes):
+    if nbytes < 0:
+        raise ValueError("sizes out of range")
+    return nbytes
 
 
 def embedding_fwd(table, ids, scale=1.0, stream=None):
     """scale * table[ids]: table [V, D], ids int64 of any shape -> [*ids.shape, D]."""
     import torch
     V, D = _rows("table", table)
-    _need("ids", ids, ids.shape, torch.int64)
-    L = _Launch(stream)
-    out = L.out((*ids.shape, D), table.dtype, table.device)
-    _b.carbon_embedding_fwd(out, table, ids, ids.numel(), V, D, scale, _dtype("table", table), L.handle)
+    shape = ids.shape
+    _need("ids", ids, shape, torch.int64)
+    code = _dtype("table", table)
+    s, empty, _ = _begin(table, stream)
+    out = empty((*shape, D), table.dtype, table.device)
+    _b.carbon_embedding_fwd(out, table, ids, ids.numel(), V, D, scale, code, s)
     return out
 
 
@@ -91,20 +111,19 @@ def embedding_bwd(dy, ids, num_rows, scale=1.0, padding_idx=-1, accumulate_to=No
     sums are added to it in place and it is returned."""
     import torch
     D = dy.shape[-1]
-    _need("ids", ids, ids.shape, torch.int64)
-    _need("dy", dy, (*ids.shape, D), dy.dtype)
+    shape = ids.shape
+    _need("ids", ids, shape, torch.int64)
+    _need("dy", dy, (*shape, D), dy.dtype)
     code = _dtype("dy", dy)
-    L = _Launch(stream)
-    if accumulate_to is None:
-        out = L.out((num_rows, D), dy.dtype, dy.device)
-    else:
-        out = accumulate_to
-        _need("accumulate_to", out, (num_rows, D), dy.dtype)
+    if accumulate_to is not None:
+        _need("accumulate_to", accumulate_to, (num_rows, D), dy.dtype)
+    s, empty, workspace = _begin(dy, stream)
+    out = accumulate_to if accumulate_to is not None else empty((num_rows, D), dy.dtype, dy.device)
     M = ids.numel()
-    nbytes = _b.carbon_embedding_bwd_workspace(M, num_rows, D)
-    ws = L.workspace(nbytes, dy.device)
+    nbytes = _bytes(_b.carbon_embedding_bwd_workspace(M, num_rows, D))
+    ws = workspace(nbytes, dy.device)
     _b.carbon_embedding_bwd(out, dy, ids, M, num_rows, D, scale, padding_idx, accumulate_to is not None,
-                            ws, nbytes, code, L.handle)
+                            ws, nbytes, code, s)
     return out
 
 
@@ -121,22 +140,22 @@ def rms_norm_fwd(x, gamma, residual=None, eps=1e-6, quantize=False, stream=None)
     """RMS norm of x + residual, [M, D]; quantize=True also writes the 8-bit
     checkpoint of the normalised rows."""
     import torch
-    M, D = _rows("x", x)
+    shape = M, D = _rows("x", x)
+    dtype, device = x.dtype, x.device
     code = _dtype("x", x)
-    _need("gamma", gamma, (D,), x.dtype)
-    L = _Launch(stream)
-    h = x
+    _need("gamma", gamma, (D,), dtype)
     if residual is not None:
-        _need("residual", residual, (M, D), x.dtype)
-        h = L.out((M, D), x.dtype, x.device)
-    y = L.out((M, D), x.dtype, x.device)
-    rstd = L.out((M,), torch.float32, x.device)
+        _need("residual", residual, shape, dtype)
+    s, empty, _ = _begin(x, stream)
+    h = x if residual is None else empty(shape, dtype, device)
+    y = empty(shape, dtype, device)
+    rstd = empty(M, torch.float32, device)
     codes = scales = None
     if quantize:
-        codes = L.out((M, D), torch.int8, x.device)
-        scales = L.out((M,), torch.float32, x.device)
+        codes = empty(shape, torch.int8, device)
+        scales = empty(M, torch.float32, device)
     _b.carbon_rms_norm_fwd(y, None if residual is None else h, rstd, codes, scales, x, residual, gamma, M, D,
-                           eps, code, L.handle)
+                           eps, code, s)
     return RmsNorm(y, h, rstd, codes, scales)
 
 
@@ -145,51 +164,54 @@ def rms_norm_bwd(dy, gamma, rstd, h=None, codes=None, scales=None, dh=None, reco
     the gradient of x and of the residual.  dh: the gradient that reaches h
     from further on.  recompute=True returns (dx, dgamma, y)."""
     import torch
-    M, D = _rows("dy", dy)
+    shape = M, D = _rows("dy", dy)
+    dtype, device = dy.dtype, dy.device
     code = _dtype("dy", dy)
-    _need("gamma", gamma, (D,), dy.dtype)
+    _need("gamma", gamma, (D,), dtype)
     _need("rstd", rstd, (M,), torch.float32)
     if (h is None) == (codes is None) or (codes is None) != (scales is None):
         raise ValueError("give either h, or codes and scales")
     if h is not None:
-        _need("h", h, (M, D), dy.dtype)
+        _need("h", h, shape, dtype)
     else:
-        _need("codes", codes, (M, D), torch.int8)
+        _need("codes", codes, shape, torch.int8)
         _need("scales", scales, (M,), torch.float32)
     if dh is not None:
-        _need("dh", dh, (M, D), dy.dtype)
-    L = _Launch(stream)
-    dx = L.out((M, D), dy.dtype, dy.device)
-    dgamma = L.out((D,), dy.dtype, dy.device)
-    y = L.out((M, D), dy.dtype, dy.device) if recompute else None
-    nbytes = _b.carbon_rms_norm_bwd_workspace(M, D)
-    ws = L.workspace(nbytes, dy.device)
-    _b.carbon_rms_norm_bwd(dx, dgamma, y, dy, h, codes, scales, rstd, gamma, dh, M, D, ws, nbytes, code, L.handle)
+        _need("dh", dh, shape, dtype)
+    s, empty, workspace = _begin(dy, stream)
+    dx = empty(shape, dtype, device)
+    dgamma = empty(D, dtype, device)
+    y = empty(shape, dtype, device) if recompute else None
+    nbytes = _bytes(_b.carbon_rms_norm_bwd_workspace(M, D))
+    ws = workspace(nbytes, device)
+    _b.carbon_rms_norm_bwd(dx, dgamma, y, dy, h, codes, scales, rstd, gamma, dh, M, D, ws, nbytes, code, s)
     return (dx, dgamma, y) if recompute else (dx, dgamma)
 
 
 def rms_norm_expand(codes, scales, gamma=None, dtype=None, stream=None):
     """codes * scales (* gamma) in dtype (gamma's, or bfloat16)."""
     import torch
-    M, D = _rows("codes", codes)
-    _need("codes", codes, (M, D), torch.int8)
+    shape = M, D = _rows("codes", codes)
+    _need("codes", codes, shape, torch.int8)
     _need("scales", scales, (M,), torch.float32)
     dtype = dtype or (gamma.dtype if gamma is not None else torch.bfloat16)
     if gamma is not None:
         _need("gamma", gamma, (D,), dtype)
-    L = _Launch(stream)
-    out = L.out((M, D), dtype, codes.device)
-    _b.carbon_rms_norm_expand(out, codes, scales, gamma, M, D, _dtype("the output", out), L.handle)
+    s, empty, _ = _begin(codes, stream)
+    out = empty(shape, dtype, codes.device)
+    _b.carbon_rms_norm_expand(out, codes, scales, gamma, M, D, _dtype("the output", out), s)
     return out
 
 
-def _xent_args(x, table, targets):
+def _xent_args(x, table, targets, reduction):
     import torch
     M, D = _rows("x", x)
     V = _rows("table", table)[0]
     _need("table", table, (V, D), x.dtype)
     _need("targets", targets, (M,), torch.int64)
-    return M, D, V, _dtype("x", x)
+    if reduction not in _b.REDUCTIONS:
+        raise ValueError(f"reduction {reduction!r}; expected one of {sorted(_b.REDUCTIONS)}")
+    return M, D, V, _dtype("x", x), _b.REDUCTIONS[reduction]
 
 
 def linear_cross_entropy_fwd(x, table, targets, ignore_index=-100, reduction="mean", stream=None):
@@ -200,31 +222,31 @@ def linear_cross_entropy_fwd(x, table, targets, ignore_index=-100, reduction="me
     count, 0 where there are none); lse: fp32 [M], the rows' log-sum-exp,
     which the gradient takes."""
     import torch
-    M, D, V, code = _xent_args(x, table, targets)
-    red = _b.REDUCTIONS[reduction]
-    L = _Launch(stream)
-    losses = L.out((M,), torch.float32, x.device)
-    lse = L.out((M,), torch.float32, x.device)
-    total = L.out((), torch.float32, x.device) if red else None
-    nbytes = _b.carbon_linear_xent_fwd_workspace(M, D, V)
-    ws = L.workspace(nbytes, x.device)
+    M, D, V, code, red = _xent_args(x, table, targets, reduction)
+    device = x.device
+    s, empty, workspace = _begin(x, stream)
+    losses = empty(M, torch.float32, device)
+    lse = empty(M, torch.float32, device)
+    total = empty((), torch.float32, device) if red else None
+    nbytes = _bytes(_b.carbon_linear_xent_fwd_workspace(M, D, V))
+    ws = workspace(nbytes, device)
     _b.carbon_linear_xent_fwd(losses, total, lse, None, x, table, targets, M, D, V, ignore_index, red, ws, nbytes,
-                              code, L.handle)
+                              code, s)
     return (total if red else losses), lse
 
 
 def linear_cross_entropy_bwd(grad, x, table, targets, lse, ignore_index=-100, reduction="mean", stream=None):
     """(dx, dtable) from grad (fp32: [M] for reduction="none", else a scalar)."""
     import torch
-    M, D, V, code = _xent_args(x, table, targets)
-    red = _b.REDUCTIONS[reduction]
+    M, D, V, code, red = _xent_args(x, table, targets, reduction)
     _need("lse", lse, (M,), torch.float32)
     _need("grad", grad, () if red else (M,), torch.float32)
-    L = _Launch(stream)
-    dx = L.out((M, D), x.dtype, x.device)
-    dtable = L.out((V, D), x.dtype, x.device)
-    nbytes = _b.carbon_linear_xent_bwd_workspace(M, D, V)
-    ws = L.workspace(nbytes, x.device)
+    device = x.device
+    s, empty, workspace = _begin(x, stream)
+    dx = empty((M, D), x.dtype, device)
+    dtable = empty((V, D), x.dtype, device)
+    nbytes = _bytes(_b.carbon_linear_xent_bwd_workspace(M, D, V))
+    ws = workspace(nbytes, device)
     _b.carbon_linear_xent_bwd(dx, dtable, grad, x, table, targets, lse, M, D, V, ignore_index, red, ws, nbytes,
-                              code, L.handle)
+                              code, s)
     return dx, dtable
