@@ -5,12 +5,16 @@
 //   codes = round(n * (127 / max|n|)),  scales = max|n| / 127
 //   dx = rstd * (gamma*dy - n * mean(gamma*dy*n)) + dh,  dgamma = sum_m dy * n
 //
-// Bound: memory.  Each row is read once into registers: a group of threads
-// (a warp, four warps or sixteen, by the row's length) holds a row as up to
-// kHold vectors per thread, reduces across the group and writes.  Longer rows
-// and rows that 16-byte vectors do not fit take the same kernels with single
-// elements, or re-read the row.  The order of a row's sums depends on D, the
-// dtype and the alignment alone.
+// Bound: memory.  A group of threads (a warp, four warps or sixteen, by the
+// row's length) takes a row at a time: each of its threads has up to kMaxHold
+// elements, the group reduces and writes.  The forward pass reads a row once,
+// into registers.  The gradient, and the forward pass where 16-byte vectors do
+// not fit the rows, read them through a ring in shared memory that bulk copies
+// fill some rows ahead (held in registers, the gradient's rows arrived one at a
+// time: 97 us for 8192 x 4096 bf16).  A copy takes the 16-byte aligned bytes
+// around a row, so that odd rows are fetched as fast as aligned ones.  Rows
+// too long for a group are read again for each pass.  The order of a row's
+// sums depends on D, the dtype and the alignment of the tensors alone.
 //
 // dgamma: a group takes the rows g, g + groups, ... and adds its columns'
 // terms in registers; the groups' sums are added per CTA in group order, then
@@ -98,6 +102,90 @@ __device__ __forceinline__ void store_codes(int8_t *p, const int8_t (&c)[N]) {
     for (int i = 0; i < N; ++i) v.e[i] = c[i];
     *reinterpret_cast<Pack<int8_t, N> *>(p) = v;
 }
+
+// ---- rows through shared memory ------------------------------------------------
+
+// A tensor of rows of row_bytes bytes.
+struct Rows {
+    const uint8_t *base;
+    int64_t row_bytes, bytes;
+};
+
+__host__ __device__ inline uint32_t row_slot(int64_t row_bytes) {       // bytes of a row's place, any alignment
+    return (uint32_t)((row_bytes + 15) / 16 * 16 + 16);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// Starts the copies of row m of every tensor into a stage, by one warp; the
+// row lies at its address modulo 16 in its place.  The bulk copies take whole
+// 16-byte pieces inside the tensor; bytes of a piece that reaches past either
+// end of the tensor are copied here.
+template <int K>
+__device__ __forceinline__ void start_row(const Rows (&t)[K], int count, int64_t m, uint8_t *stage, uint32_t slot,
+                                          uint32_t bar) {
+    const int lane = threadIdx.x % 32;
+    uint32_t bytes = 0u;
+    const uint8_t *from[K];
+    uint32_t at[K], len[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        len[k] = 0u;
+        if (k >= count) continue;
+        const uint8_t *b0 = t[k].base + m * t[k].row_bytes, *b1 = b0 + t[k].row_bytes, *end = t[k].base + t[k].bytes;
+        const uintptr_t piece = reinterpret_cast<uintptr_t>(b0) & ~(uintptr_t)15;
+        const uint8_t *lo = reinterpret_cast<const uint8_t *>(piece);
+        const uint8_t *hi = reinterpret_cast<const uint8_t *>((reinterpret_cast<uintptr_t>(b1) + 15) & ~(uintptr_t)15);
+        if (lo < t[k].base) lo += 16;
+        if (hi > end) hi -= 16;
+        uint8_t *place = stage + k * slot;
+        for (const uint8_t *b = b0 + lane; b < (lo < b1 ? lo : b1); b += 32) place[b - reinterpret_cast<const uint8_t *>(piece)] = *b;
+        for (const uint8_t *b = (hi > b0 ? hi : b0) + lane; b < b1; b += 32)
+            if (b >= lo) place[b - reinterpret_cast<const uint8_t *>(piece)] = *b;
+        if (hi > lo) {
+            from[k] = lo;
+            at[k] = (uint32_t)(lo - reinterpret_cast<const uint8_t *>(piece));
+            len[k] = (uint32_t)(hi - lo);
+            bytes += len[k];
+        }
+    }
+    __syncwarp();
+    if (lane == 0) {
+        mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (len[k] > 0u) bulk_load(smem_addr(stage + k * slot) + at[k], from[k], len[k], bar);
+    }
+}
+
+// Where row m of tensor k lies in a stage.
+template <typename E>
+__device__ __forceinline__ const E *staged(const uint8_t *stage, uint32_t slot, int k, const Rows &t, int64_t m) {
+    return reinterpret_cast<const E *>(stage + k * slot + (reinterpret_cast<uintptr_t>(t.base + m * t.row_bytes) & 15u));
+}
+
+template <int G>
+__device__ __forceinline__ void group_sync() {
+    if constexpr (G == 32) __syncwarp();
+    else __syncthreads();
+}
+
+// Waits for a stage; a wait that gives up is recorded, and the later ones are
+// skipped (the rows' results are then meaningless, but the kernel ends).
+__device__ __forceinline__ bool wait_stage(uint64_t *bar, uint32_t parity, bool ok) {
+    if (!ok) return false;
+    if (__all_sync(0xffffffffu, mbar_wait(smem_addr(bar), parity))) return true;
+    atomicExch(&g_norm_status, (unsigned)CARBON_ERR_TIMEOUT);
+    return false;
+}
+
+// CTAs of G threads for G > 32 (one group), of 8 warps (8 groups) for G = 32.
+template <int G>
+constexpr int kRingThreads = G == 32 ? 256 : G;
+constexpr int kMaxStages = 4;
 
 template <typename T>
 struct FwdArgs {
@@ -196,6 +284,82 @@ norm_fwd_kernel(const FwdArgs<T> a) {
     }
 }
 
+// Rows that 16-byte vectors do not fit: through the ring, element by element.
+template <typename T, int G, int H>
+__global__ void __launch_bounds__(kRingThreads<G>)
+norm_fwd_ring_kernel(const FwdArgs<T> a, const int stages) {
+    constexpr int kThreads = kRingThreads<G>, kRows = kThreads / G;
+    __shared__ float buf[kThreads / 32];
+    __shared__ __align__(8) uint64_t bars[kRows][kMaxStages];
+    extern __shared__ __align__(16) uint8_t ring[];
+    const int t = threadIdx.x % G, group = threadIdx.x / G;
+    const uint32_t slot = row_slot(a.D * sizeof(T));
+    const int count = a.residual ? 2 : 1;
+    uint8_t *mine = ring + (size_t)group * stages * count * slot;
+    const Rows rows[2] = {
+        {reinterpret_cast<const uint8_t *>(a.x), a.D * (int64_t)sizeof(T), a.M * a.D * (int64_t)sizeof(T)},
+        {reinterpret_cast<const uint8_t *>(a.residual), a.D * (int64_t)sizeof(T), a.M * a.D * (int64_t)sizeof(T)}};
+    if (t == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(smem_addr(&bars[group][s]), 1);
+        fence_mbar_init();
+    }
+    group_sync<G>();
+    wait_prior_grid();
+    allow_next_grid();
+    const int64_t first = (int64_t)blockIdx.x * kRows + group, step = (int64_t)gridDim.x * kRows;
+    if (t < 32)
+        for (int s = 0; s < stages && first + s * step < a.M; ++s)
+            start_row(rows, count, first + s * step, mine + s * count * slot, slot, smem_addr(&bars[group][s]));
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const int D = (int)a.D;
+    for (int64_t m = first; m < a.M; m += step) {
+        ok = wait_stage(&bars[group][s], ph, ok);
+        const uint8_t *stage = mine + s * count * slot;
+        const T *x = staged<T>(stage, slot, 0, rows[0], m), *res = staged<T>(stage, slot, count - 1, rows[count - 1], m);
+        float h[H], ss = 0.0f;
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+            const int j = t + G * u;
+            h[u] = j < D ? to_f32(x[j]) : 0.0f;
+            if (j < D && a.residual) h[u] += to_f32(res[j]);
+            ss = fmaf(h[u], h[u], ss);
+        }
+        ss = group_sum<G>(ss, buf);
+        group_sync<G>();                                  // the row has been read
+        if (ok && t < 32 && m + stages * step < a.M)
+            start_row(rows, count, m + stages * step, mine + s * count * slot, slot, smem_addr(&bars[group][s]));
+        if (++s == stages) { s = 0; ph ^= 1u; }
+
+        const float rstd = rsqrtf(__fdiv_rn(ss, (float)a.D) + a.eps);
+        const int64_t row = m * a.D;
+        if (a.rstd && t == 0) a.rstd[m] = rstd;
+        uint32_t top = 0u;
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+            const int j = t + G * u;
+            if (j < D && CHK(row + j, 1, a.M * a.D)) {
+                if (a.h_out) a.h_out[row + j] = from_f32<T>(h[u]);
+                a.y[row + j] = from_f32<T>(h[u] * rstd * to_f32(a.gamma[j]));
+            }
+            top = max(top, magnitude(h[u] * rstd));
+        }
+        if (a.codes) {
+            top = group_max<G>(top, reinterpret_cast<uint32_t *>(buf));
+            float scale, factor;
+            code_scale(top, &scale, &factor);
+            if (t == 0) a.scales[m] = scale;
+#pragma unroll
+            for (int u = 0; u < H; ++u) {
+                const int j = t + G * u;
+                if (j < D) a.codes[row + j] = code_of(h[u] * rstd, factor);
+            }
+            group_sync<G>();
+        }
+    }
+}
+
 // Rows that do not fit a group's registers: a CTA per row, the row read again
 // for each pass.
 template <typename T>
@@ -244,55 +408,62 @@ struct BwdArgs {
     int64_t M, D;
 };
 
-// A group holds a row of n's source, dy and dh as they were loaded (all three
-// are in flight before the first is used) and widens them where they are
-// needed; the sum over the row is the only wait in between.
+// A group's rows come through its ring: n's source, dy and dh.  They are read
+// from it twice, for the sum over the row and for dx, so that a thread only
+// keeps its columns of dgamma.
 template <typename T, int G, int N, int H, bool CODES>
-__global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : 2)
-norm_bwd_kernel(const BwdArgs<T> a) {
-    constexpr int kThreads = G > 256 ? G : 256, kRows = kThreads / G;
+__global__ void __launch_bounds__(kRingThreads<G>)
+norm_bwd_kernel(const BwdArgs<T> a, const int stages) {
+    constexpr int kThreads = kRingThreads<G>, kRows = kThreads / G;
+    using Source = typename std::conditional<CODES, int8_t, T>::type;
     __shared__ float buf[kThreads / 32];
-    extern __shared__ float group_part[];                 // [kRows][D] for dgamma, kRows > 1
+    __shared__ __align__(8) uint64_t bars[kRows][kMaxStages];
+    extern __shared__ __align__(16) uint8_t ring[];       // afterwards [kRows][D] of dgamma, kRows > 1
+    const int t = threadIdx.x % G, group = threadIdx.x / G;
+    const int D = (int)a.D, nvec = D / N;
+    const uint32_t slot = row_slot(a.D * sizeof(T));
+    const int count = a.dh ? 3 : 2;
+    uint8_t *mine = ring + (size_t)group * stages * count * slot;
+    const int64_t wide = a.D * (int64_t)sizeof(T);
+    const Rows rows[3] = {{CODES ? reinterpret_cast<const uint8_t *>(a.codes) : reinterpret_cast<const uint8_t *>(a.h),
+                           a.D * (int64_t)sizeof(Source), a.M * a.D * (int64_t)sizeof(Source)},
+                          {reinterpret_cast<const uint8_t *>(a.dy), wide, a.M * wide},
+                          {reinterpret_cast<const uint8_t *>(a.dh), wide, a.M * wide}};
+    if (t == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(smem_addr(&bars[group][s]), 1);
+        fence_mbar_init();
+    }
+    group_sync<G>();
     wait_prior_grid();
     allow_next_grid();
-    const int t = threadIdx.x % G, group = threadIdx.x / G;
-    const int nvec = (int)(a.D / N);
-    const int64_t stride = (int64_t)gridDim.x * kRows;
+    const int64_t first = (int64_t)blockIdx.x * kRows + group, step = (int64_t)gridDim.x * kRows;
+    if (t < 32)
+        for (int s = 0; s < stages && first + s * step < a.M; ++s)
+            start_row(rows, count, first + s * step, mine + s * count * slot, slot, smem_addr(&bars[group][s]));
     float dg[H][N];
 #pragma unroll
     for (int u = 0; u < H; ++u)
 #pragma unroll
         for (int k = 0; k < N; ++k) dg[u][k] = 0.0f;
-
-    // every group of a CTA makes the same number of rounds (group_sum has CTA barriers)
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.M; r0 += stride) {
-        const int64_t m = r0 + group;
-        const bool live = m < a.M;
-        const int64_t row = (live ? m : 0) * a.D;
-        using Source = typename std::conditional<CODES, int8_t, T>::type;
-        const Source *source = CODES ? reinterpret_cast<const Source *>(a.codes) : reinterpret_cast<const Source *>(a.h);
-        Pack<Source, N> ns[H];
-        Pack<T, N> dys[H], dhs[H];
-#pragma unroll
-        for (int u = 0; u < H; ++u) {
-            const int i = t + G * u;
-            if (i < nvec && live && CHK(row + i * N, N, a.M * a.D)) {
-                ns[u] = *reinterpret_cast<const Pack<Source, N> *>(source + row + i * N);
-                dys[u] = *reinterpret_cast<const Pack<T, N> *>(a.dy + row + i * N);
-                if (a.dh) dhs[u] = *reinterpret_cast<const Pack<T, N> *>(a.dh + row + i * N);
-            }
-        }
-        const float rstd = live ? a.rstd[m] : 0.0f;
-        const float factor = !live ? 0.0f : (CODES ? a.scales[m] : rstd);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int64_t m = first; m < a.M; m += step) {
+        const float rstd = a.rstd[m], factor = CODES ? a.scales[m] : rstd;
+        ok = wait_stage(&bars[group][s], ph, ok);
+        const uint8_t *stage = mine + s * count * slot;
+        const Source *src = staged<Source>(stage, slot, 0, rows[0], m);
+        const T *dys = staged<T>(stage, slot, 1, rows[1], m), *dhs = staged<T>(stage, slot, count - 1, rows[count - 1], m);
+        const int64_t row = m * a.D;
         float dot = 0.0f;
 #pragma unroll
         for (int u = 0; u < H; ++u) {
             const int i = t + G * u;
-            if (i < nvec && live) {
+            if (i < nvec && CHK(row + i * N, N, a.M * a.D)) {
                 float g[N], n[N], dy[N], y[N];
                 load_f32<T, N>(a.gamma + i * N, g);
-                widen(ns[u], n);
-                widen(dys[u], dy);
+                load_f32<Source, N>(src + i * N, n);
+                load_f32<T, N>(dys + i * N, dy);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
                     n[k] *= factor;
@@ -305,28 +476,29 @@ norm_bwd_kernel(const BwdArgs<T> a) {
         }
         dot = group_sum<G>(dot, buf);
         const float mean = __fdiv_rn(dot, (float)a.D);
-        if (live) {
 #pragma unroll
-            for (int u = 0; u < H; ++u) {
-                const int i = t + G * u;
-                if (i < nvec) {
-                    float g[N], n[N], dy[N], d[N];
-                    load_f32<T, N>(a.gamma + i * N, g);
-                    widen(ns[u], n);
-                    widen(dys[u], dy);
-                    if (a.dh) {
-                        widen(dhs[u], d);
-                    } else {
+        for (int u = 0; u < H; ++u) {
+            const int i = t + G * u;
+            if (i < nvec && CHK(row + i * N, N, a.M * a.D)) {
+                float g[N], n[N], dy[N], d[N];
+                load_f32<T, N>(a.gamma + i * N, g);
+                load_f32<Source, N>(src + i * N, n);
+                load_f32<T, N>(dys + i * N, dy);
+                if (a.dh) {
+                    load_f32<T, N>(dhs + i * N, d);
+                } else {
 #pragma unroll
-                        for (int k = 0; k < N; ++k) d[k] = 0.0f;
-                    }
-#pragma unroll
-                    for (int k = 0; k < N; ++k)
-                        d[k] = fmaf(rstd, fmaf(-(n[k] * factor), mean, dy[k] * g[k]), d[k]);
-                    store_f32<T, N>(a.dx + row + i * N, d);
+                    for (int k = 0; k < N; ++k) d[k] = 0.0f;
                 }
+#pragma unroll
+                for (int k = 0; k < N; ++k) d[k] = fmaf(rstd, fmaf(-(n[k] * factor), mean, dy[k] * g[k]), d[k]);
+                store_f32<T, N>(a.dx + row + i * N, d);
             }
         }
+        group_sync<G>();                                  // the stage has been read
+        if (ok && t < 32 && m + stages * step < a.M)
+            start_row(rows, count, m + stages * step, mine + s * count * slot, slot, smem_addr(&bars[group][s]));
+        if (++s == stages) { s = 0; ph ^= 1u; }
     }
     if (!a.partial) return;
     float *out = a.partial + (int64_t)blockIdx.x * a.D;
@@ -339,19 +511,21 @@ norm_bwd_kernel(const BwdArgs<T> a) {
                 for (int k = 0; k < N; ++k) out[i * N + k] = dg[u][k];
         }
     } else {
+        float *group_part = reinterpret_cast<float *>(ring);
+        __syncthreads();                                  // every group is done with its ring
 #pragma unroll
         for (int u = 0; u < H; ++u) {
             const int i = t + G * u;
             if (i < nvec)
 #pragma unroll
-                for (int k = 0; k < N; ++k) group_part[group * (int)a.D + i * N + k] = dg[u][k];
+                for (int k = 0; k < N; ++k) group_part[group * D + i * N + k] = dg[u][k];
         }
         __syncthreads();
-        for (int j = threadIdx.x; j < (int)a.D; j += kThreads) {
-            float s = 0.0f;
+        for (int j = threadIdx.x; j < D; j += kThreads) {
+            float sum = 0.0f;
 #pragma unroll
-            for (int g = 0; g < kRows; ++g) s += group_part[g * (int)a.D + j];
-            out[j] = s;
+            for (int g = 0; g < kRows; ++g) sum += group_part[g * D + j];
+            out[j] = sum;
         }
     }
 }
@@ -417,28 +591,40 @@ dgamma_kernel(T *__restrict__ dgamma, const float *__restrict__ partial, int row
     }
 }
 
+// The rows as one line of M * D elements, N at a time; a vector may reach into
+// the next row.
 template <typename T, int N>
 __global__ void __launch_bounds__(256)
 norm_expand_kernel(T *__restrict__ out, const int8_t *__restrict__ codes, const float *__restrict__ scales,
                    const T *__restrict__ gamma, int64_t M, int64_t D) {
     wait_prior_grid();
     allow_next_grid();
-    const int64_t nvec = D / N, total = M * nvec;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t m = i / nvec, v = i - m * nvec;
-        if (!CHK(i * N, N, M * D)) continue;
-        const float s = scales[m];
-        float f[N];
-        widen(*reinterpret_cast<const Pack<int8_t, N> *>(codes + i * N), f);
+    const int64_t total = M * D, nvec = (total + N - 1) / N;
+    for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < nvec; v += (int64_t)gridDim.x * 256) {
+        const int64_t i = v * N;
+        // 32-bit division where it will do
+        int64_t m = total <= 0xffffffffll ? (int64_t)((uint32_t)i / (uint32_t)D) : i / D;
+        int64_t col = i - m * D;
+        if (i + N <= total && CHK(i, N, total)) {
+            float f[N];
+            load_f32<int8_t, N>(codes + i, f);
+            float s = scales[m];
 #pragma unroll
-        for (int k = 0; k < N; ++k) f[k] *= s;
-        if (gamma) {
-            float g[N];
-            load_f32<T, N>(gamma + v * N, g);
-#pragma unroll
-            for (int k = 0; k < N; ++k) f[k] *= g[k];
+            for (int k = 0; k < N; ++k) {
+                f[k] *= s;
+                if (gamma) f[k] *= to_f32(gamma[col]);
+                if (++col == D && k + 1 < N) {
+                    col = 0;
+                    s = scales[++m];
+                }
+            }
+            store_f32<T, N>(out + i, f);
+        } else {
+            for (int64_t j = i; j < total; ++j) {
+                const float f = (float)codes[j] * scales[j / D];
+                out[j] = from_f32<T>(gamma ? f * to_f32(gamma[j % D]) : f);
+            }
         }
-        store_f32<T, N>(out + i * N, f);
     }
 }
 
@@ -482,16 +668,58 @@ bool with_group(int64_t D, F &&f) {
     return held(integral_constant<int, 32>()) || held(integral_constant<int, 128>()) || held(integral_constant<int, 512>());
 }
 
+// The ring of a kernel: as many stages, of at least two, as half of an SM's
+// shared memory holds, so that two CTAs share it; else two stages.  bytes:
+// one stage of all the CTA's groups.  0 where two stages do not fit.
+constexpr int64_t kSharedHalf = 110 * 1024, kSharedMost = 226 * 1024;
+
+int ring_stages(int64_t bytes) {
+    int s = (int)(kSharedHalf / bytes);
+    if (s < 2) s = 2;
+    if (s > kMaxStages) s = kMaxStages;
+    return s * bytes <= kSharedMost ? s : 0;
+}
+
+// CTAs of the kernels with a ring: as many as run at once, and no more partial
+// rows of dgamma than that.
+constexpr int kRingCtas = 152 * 4;
+int ring_ctas(int64_t M, int rows_per_cta, int64_t smem) {
+    const int64_t per_sm = kSharedMost / (smem + 2048) < 4 ? kSharedMost / (smem + 2048) : 4;
+    const int64_t want = (M + rows_per_cta - 1) / rows_per_cta, most = 152 * (per_sm > 1 ? per_sm : 1);
+    return (int)(want < most ? want : most);
+}
+
+template <typename Kern>
+cudaError_t allow_shared(Kern kern, int64_t smem) {
+    return smem > 48 * 1024 - 2048 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                                   : cudaSuccess;
+}
+
 template <typename T, int N>
 cudaError_t launch_fwd(const FwdArgs<T> &a, cudaStream_t s) {
     cudaError_t err = cudaSuccess;
+    bool fits = true;
     count_launch();
     const bool held = with_group<N>(a.D, [&](auto g, auto h) {
-        constexpr int G = g(), H = h(), kRows = G > 128 ? 1 : 128 / G;
-        err = launch_k(norm_fwd_kernel<T, G, N, H>, dim3((unsigned)((a.M + kRows - 1) / kRows)),
-                       dim3(G > 128 ? G : 128), 0, s, 1, a);
+        constexpr int G = g(), H = h();
+        if constexpr (N > 1) {
+            constexpr int kRows = G > 128 ? 1 : 128 / G;
+            err = launch_k(norm_fwd_kernel<T, G, N, H>, dim3((unsigned)((a.M + kRows - 1) / kRows)),
+                           dim3(G > 128 ? G : 128), 0, s, 1, a);
+        } else {
+            constexpr int kRows = kRingThreads<G> / G;
+            const int64_t stage = (int64_t)kRows * (a.residual ? 2 : 1) * row_slot(a.D * sizeof(T));
+            const int stages = ring_stages(stage);
+            fits = stages > 0;                            // else fp32 rows too long for two stages
+            if (!fits) return;
+            auto kern = norm_fwd_ring_kernel<T, G, H>;
+            err = allow_shared(kern, stages * stage);
+            if (err == cudaSuccess)
+                err = launch_k(kern, dim3((unsigned)ring_ctas(a.M, kRows, stages * stage)), dim3(kRingThreads<G>),
+                               (size_t)(stages * stage), s, 1, a, stages);
+        }
     });
-    if (!held)
+    if (!held || !fits)
         err = launch_k(norm_fwd_long_kernel<T>, dim3((unsigned)(a.M < 65535 ? a.M : 65535)), dim3(512), 0, s, 1, a);
     return err;
 }
@@ -505,27 +733,27 @@ cudaError_t run_fwd(const FwdArgs<T> &a, cudaStream_t s) {
     return vec ? launch_fwd<T, N>(a, s) : launch_fwd<T, 1>(a, s);
 }
 
-// CTAs of the gradient kernels: two per SM, as their registers allow, and no
-// more partial rows than that.
-constexpr int kBwdCtas = 152 * 2;
-
 template <typename T, int N, bool CODES>
 cudaError_t launch_bwd(const BwdArgs<T> &a, T *dgamma, cudaStream_t s) {
     cudaError_t err = cudaSuccess;
     int ctas = 0;
-    count_launch();
-    const bool held = with_group<N>(a.D, [&](auto g, auto h) {
-        constexpr int G = g(), H = h(), kThreads = G > 256 ? G : 256, kRows = kThreads / G;
-        const int64_t want = (a.M + kRows - 1) / kRows;
-        ctas = (int)(want < kBwdCtas ? want : kBwdCtas);
-        const size_t smem = kRows > 1 && a.partial ? (size_t)kRows * a.D * sizeof(float) : 0;
+    bool held = with_group<N>(a.D, [&](auto g, auto h) {
+        constexpr int G = g(), H = h(), kRows = kRingThreads<G> / G;
+        const int64_t stage = (int64_t)kRows * (a.dh ? 3 : 2) * row_slot(a.D * sizeof(T));
+        const int stages = ring_stages(stage);
+        if (stages == 0) return;                          // fp32 rows too long for two stages: the long kernel
+        int64_t smem = stages * stage;
+        const int64_t parts = kRows > 1 ? (int64_t)kRows * a.D * (int64_t)sizeof(float) : 0;
+        if (smem < parts) smem = parts;
+        ctas = ring_ctas(a.M, kRows, smem);
         auto kern = norm_bwd_kernel<T, G, N, H, CODES>;
-        if (smem > 48 * 1024)
-            err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (err == cudaSuccess) err = launch_k(kern, dim3((unsigned)ctas), dim3(kThreads), smem, s, 1, a);
-    });
+        err = allow_shared(kern, smem);
+        if (err == cudaSuccess)
+            err = launch_k(kern, dim3((unsigned)ctas), dim3(kRingThreads<G>), (size_t)smem, s, 1, a, stages);
+    }) && ctas > 0;
+    count_launch();
     if (!held) {
-        ctas = (int)(a.M < kBwdCtas ? a.M : kBwdCtas);
+        ctas = (int)(a.M < kRingCtas ? a.M : kRingCtas);
         err = launch_k(norm_bwd_long_kernel<T>, dim3((unsigned)ctas), dim3(512), 0, s, 1, a);
     }
     if (err != cudaSuccess || !a.partial) return err;
@@ -548,8 +776,8 @@ template <typename T>
 cudaError_t run_expand(void *out, const int8_t *codes, const float *scales, const void *gamma, int64_t M,
                        int64_t D, cudaStream_t s) {
     constexpr int N = kVec<T>;
-    const bool vec = D % N == 0 && aligned16(out) && aligned16(gamma) && reinterpret_cast<uintptr_t>(codes) % N == 0;
-    const int64_t total = vec ? M * (D / N) : M * D, want = (total + 255) / 256;
+    const bool vec = aligned16(out) && reinterpret_cast<uintptr_t>(codes) % N == 0;
+    const int64_t total = vec ? (M * D + N - 1) / N : M * D, want = (total + 255) / 256;
     const dim3 grid((unsigned)(want < 152 * 16 ? want : 152 * 16));
     count_launch();
     if (vec)
@@ -620,7 +848,7 @@ carbon_status_t carbon_rms_norm_fwd(void *y, void *h_out, float *rstd, int8_t *c
 
 int64_t carbon_rms_norm_bwd_workspace(int64_t M, int64_t D) {
     if (!sizes_ok(M, D)) return -1;
-    return (M < kBwdCtas ? M : kBwdCtas) * D * (int64_t)sizeof(float);
+    return (M < kRingCtas ? M : kRingCtas) * D * (int64_t)sizeof(float);
 }
 
 carbon_status_t carbon_rms_norm_bwd(void *dx, void *dgamma, void *y_out, const void *dy, const void *h,
