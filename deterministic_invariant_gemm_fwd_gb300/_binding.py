@@ -116,9 +116,11 @@ def _lib() -> ctypes.CDLL:
 
 
 def __getattr__(name):
-    # ``_binding.lib`` loads the library on first access.
+    # ``_binding.lib`` loads the library on first access, and is an attribute
+    # of the module from then on.
     if name == "lib":
-        return _lib()
+        globals()["lib"] = _lib()
+        return globals()["lib"]
     raise AttributeError(name)
 
 

@@ -129,35 +129,38 @@ __device__ __forceinline__ void start_row(const Rows (&t)[K], int count, int64_t
                                           uint32_t bar) {
     const int lane = threadIdx.x % 32;
     uint32_t bytes = 0u;
-    const uint8_t *from[K];
-    uint32_t at[K], len[K];
+    auto range = [&](const Rows &r, const uint8_t **b0, const uint8_t **b1, const uint8_t **lo, const uint8_t **hi) {
+        *b0 = r.base + m * r.row_bytes;
+        *b1 = *b0 + r.row_bytes;
+        *lo = reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(*b0) & ~(uintptr_t)15);
+        *hi = reinterpret_cast<const uint8_t *>((reinterpret_cast<uintptr_t>(*b1) + 15) & ~(uintptr_t)15);
+        if (*lo < r.base) *lo += 16;
+        if (*hi > r.base + r.bytes) *hi -= 16;
+    };
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        len[k] = 0u;
-        if (k >= count) continue;
-        const uint8_t *b0 = t[k].base + m * t[k].row_bytes, *b1 = b0 + t[k].row_bytes, *end = t[k].base + t[k].bytes;
-        const uintptr_t piece = reinterpret_cast<uintptr_t>(b0) & ~(uintptr_t)15;
-        const uint8_t *lo = reinterpret_cast<const uint8_t *>(piece);
-        const uint8_t *hi = reinterpret_cast<const uint8_t *>((reinterpret_cast<uintptr_t>(b1) + 15) & ~(uintptr_t)15);
-        if (lo < t[k].base) lo += 16;
-        if (hi > end) hi -= 16;
-        uint8_t *place = stage + k * slot;
-        for (const uint8_t *b = b0 + lane; b < (lo < b1 ? lo : b1); b += 32) place[b - reinterpret_cast<const uint8_t *>(piece)] = *b;
-        for (const uint8_t *b = (hi > b0 ? hi : b0) + lane; b < b1; b += 32)
-            if (b >= lo) place[b - reinterpret_cast<const uint8_t *>(piece)] = *b;
-        if (hi > lo) {
-            from[k] = lo;
-            at[k] = (uint32_t)(lo - reinterpret_cast<const uint8_t *>(piece));
-            len[k] = (uint32_t)(hi - lo);
-            bytes += len[k];
+        if (k >= count) break;
+        const uint8_t *b0, *b1, *lo, *hi;
+        range(t[k], &b0, &b1, &lo, &hi);
+        if (lo > b0 || hi < b1) {                         // only in the tensor's first and last rows
+            uint8_t *place = stage + k * slot + (reinterpret_cast<uintptr_t>(b0) & 15u);
+            for (const uint8_t *b = b0 + lane; b < (lo < b1 ? lo : b1); b += 32) place[b - b0] = *b;
+            for (const uint8_t *b = (hi > b0 ? hi : b0) + lane; b < b1; b += 32)
+                if (b >= lo) place[b - b0] = *b;
         }
+        if (hi > lo) bytes += (uint32_t)(hi - lo);
     }
     __syncwarp();
     if (lane == 0) {
         mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (len[k] > 0u) bulk_load(smem_addr(stage + k * slot) + at[k], from[k], len[k], bar);
+        for (int k = 0; k < K; ++k) {
+            if (k >= count) break;
+            const uint8_t *b0, *b1, *lo, *hi;
+            range(t[k], &b0, &b1, &lo, &hi);
+            if (hi > lo)                                  // the row's own address modulo 16 is kept
+                bulk_load(smem_addr(stage + k * slot) + (lo > b0 ? 16u : 0u), lo, (uint32_t)(hi - lo), bar);
+        }
     }
 }
 
@@ -171,6 +174,16 @@ template <int G>
 __device__ __forceinline__ void group_sync() {
     if constexpr (G == 32) __syncwarp();
     else __syncthreads();
+}
+
+// gamma behind the ring, for the CTA's life (from global memory, its loads were
+// what the warps waited for most).
+template <typename T>
+__device__ __forceinline__ const T *stage_gamma(uint8_t *at, const T *gamma, int D) {
+    T *g = reinterpret_cast<T *>(at);
+    for (int j = threadIdx.x; j < D; j += blockDim.x) g[j] = gamma[j];
+    __syncthreads();
+    return g;
 }
 
 // Waits for a stage; a wait that gives up is recorded, and the later ones are
@@ -310,6 +323,7 @@ norm_fwd_ring_kernel(const FwdArgs<T> a, const int stages) {
     if (t < 32)
         for (int s = 0; s < stages && first + s * step < a.M; ++s)
             start_row(rows, count, first + s * step, mine + s * count * slot, slot, smem_addr(&bars[group][s]));
+    const T *gamma = stage_gamma(ring + (size_t)kRows * stages * count * slot, a.gamma, (int)a.D);
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -317,7 +331,7 @@ norm_fwd_ring_kernel(const FwdArgs<T> a, const int stages) {
     for (int64_t m = first; m < a.M; m += step) {
         ok = wait_stage(&bars[group][s], ph, ok);
         const uint8_t *stage = mine + s * count * slot;
-        const T *x = staged<T>(stage, slot, 0, rows[0], m), *res = staged<T>(stage, slot, count - 1, rows[count - 1], m);
+        const T *x = staged<T>(stage, slot, 0, rows[0], m), *res = staged<T>(stage, slot, 1, rows[1], m);   // res: if there is one
         float h[H], ss = 0.0f;
 #pragma unroll
         for (int u = 0; u < H; ++u) {
@@ -341,7 +355,7 @@ norm_fwd_ring_kernel(const FwdArgs<T> a, const int stages) {
             const int j = t + G * u;
             if (j < D && CHK(row + j, 1, a.M * a.D)) {
                 if (a.h_out) a.h_out[row + j] = from_f32<T>(h[u]);
-                a.y[row + j] = from_f32<T>(h[u] * rstd * to_f32(a.gamma[j]));
+                a.y[row + j] = from_f32<T>(h[u] * rstd * to_f32(gamma[j]));
             }
             top = max(top, magnitude(h[u] * rstd));
         }
@@ -408,11 +422,10 @@ struct BwdArgs {
     int64_t M, D;
 };
 
-// A group's rows come through its ring: n's source, dy and dh.  They are read
-// from it twice, for the sum over the row and for dx, so that a thread only
-// keeps its columns of dgamma.
+// A group's rows come through its ring: n's source, dy and dh.  n and gamma*dy
+// stay in registers between the sum over the row and dx.
 template <typename T, int G, int N, int H, bool CODES>
-__global__ void __launch_bounds__(kRingThreads<G>)
+__global__ void __launch_bounds__(kRingThreads<G>, G == 32 ? 2 : G == 128 ? 4 : 1)
 norm_bwd_kernel(const BwdArgs<T> a, const int stages) {
     constexpr int kThreads = kRingThreads<G>, kRows = kThreads / G;
     using Source = typename std::conditional<CODES, int8_t, T>::type;
@@ -440,6 +453,7 @@ norm_bwd_kernel(const BwdArgs<T> a, const int stages) {
     if (t < 32)
         for (int s = 0; s < stages && first + s * step < a.M; ++s)
             start_row(rows, count, first + s * step, mine + s * count * slot, slot, smem_addr(&bars[group][s]));
+    const T *gamma = stage_gamma(ring + (size_t)kRows * stages * count * slot, a.gamma, D);
     float dg[H][N];
 #pragma unroll
     for (int u = 0; u < H; ++u)
@@ -448,30 +462,41 @@ norm_bwd_kernel(const BwdArgs<T> a, const int stages) {
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
+    // the next row's statistics are loaded a row ahead
+    float next_rstd = first < a.M ? a.rstd[first] : 0.0f, next_scale = CODES && first < a.M ? a.scales[first] : 0.0f;
     for (int64_t m = first; m < a.M; m += step) {
-        const float rstd = a.rstd[m], factor = CODES ? a.scales[m] : rstd;
+        const float rstd = next_rstd, factor = CODES ? next_scale : rstd;
+        if (m + step < a.M) {
+            next_rstd = a.rstd[m + step];
+            if (CODES) next_scale = a.scales[m + step];
+        }
         ok = wait_stage(&bars[group][s], ph, ok);
         const uint8_t *stage = mine + s * count * slot;
         const Source *src = staged<Source>(stage, slot, 0, rows[0], m);
-        const T *dys = staged<T>(stage, slot, 1, rows[1], m), *dhs = staged<T>(stage, slot, count - 1, rows[count - 1], m);
+        const T *dys = staged<T>(stage, slot, 1, rows[1], m), *dhs = staged<T>(stage, slot, 2, rows[2], m);   // dhs: if there is one
         const int64_t row = m * a.D;
-        float dot = 0.0f;
+        float n[H][N], gdy[H][N], dot = 0.0f;
 #pragma unroll
         for (int u = 0; u < H; ++u) {
             const int i = t + G * u;
             if (i < nvec && CHK(row + i * N, N, a.M * a.D)) {
-                float g[N], n[N], dy[N], y[N];
-                load_f32<T, N>(a.gamma + i * N, g);
-                load_f32<Source, N>(src + i * N, n);
+                float g[N], dy[N];
+                load_f32<T, N>(gamma + i * N, g);
+                load_f32<Source, N>(src + i * N, n[u]);
                 load_f32<T, N>(dys + i * N, dy);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    n[k] *= factor;
-                    y[k] = n[k] * g[k];
-                    dg[u][k] = fmaf(dy[k], n[k], dg[u][k]);
-                    dot = fmaf(dy[k] * g[k], n[k], dot);
+                    n[u][k] *= factor;
+                    gdy[u][k] = dy[k] * g[k];
+                    dg[u][k] = fmaf(dy[k], n[u][k], dg[u][k]);
+                    dot = fmaf(gdy[u][k], n[u][k], dot);
                 }
-                if (a.y_out) store_f32<T, N>(a.y_out + row + i * N, y);
+                if (a.y_out) {
+                    float y[N];
+#pragma unroll
+                    for (int k = 0; k < N; ++k) y[k] = n[u][k] * g[k];
+                    store_f32<T, N>(a.y_out + row + i * N, y);
+                }
             }
         }
         dot = group_sum<G>(dot, buf);
@@ -480,10 +505,7 @@ norm_bwd_kernel(const BwdArgs<T> a, const int stages) {
         for (int u = 0; u < H; ++u) {
             const int i = t + G * u;
             if (i < nvec && CHK(row + i * N, N, a.M * a.D)) {
-                float g[N], n[N], dy[N], d[N];
-                load_f32<T, N>(a.gamma + i * N, g);
-                load_f32<Source, N>(src + i * N, n);
-                load_f32<T, N>(dys + i * N, dy);
+                float d[N];
                 if (a.dh) {
                     load_f32<T, N>(dhs + i * N, d);
                 } else {
@@ -491,7 +513,7 @@ norm_bwd_kernel(const BwdArgs<T> a, const int stages) {
                     for (int k = 0; k < N; ++k) d[k] = 0.0f;
                 }
 #pragma unroll
-                for (int k = 0; k < N; ++k) d[k] = fmaf(rstd, fmaf(-(n[k] * factor), mean, dy[k] * g[k]), d[k]);
+                for (int k = 0; k < N; ++k) d[k] = fmaf(rstd, fmaf(-n[u][k], mean, gdy[u][k]), d[k]);
                 store_f32<T, N>(a.dx + row + i * N, d);
             }
         }
@@ -609,13 +631,21 @@ norm_expand_kernel(T *__restrict__ out, const int8_t *__restrict__ codes, const 
             float f[N];
             load_f32<int8_t, N>(codes + i, f);
             float s = scales[m];
+            if (col + N <= D) {                           // within a row
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                f[k] *= s;
-                if (gamma) f[k] *= to_f32(gamma[col]);
-                if (++col == D && k + 1 < N) {
-                    col = 0;
-                    s = scales[++m];
+                for (int k = 0; k < N; ++k) f[k] *= s;
+                if (gamma)
+#pragma unroll
+                    for (int k = 0; k < N; ++k) f[k] *= to_f32(gamma[col + k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    f[k] *= s;
+                    if (gamma) f[k] *= to_f32(gamma[col]);
+                    if (++col == D && k + 1 < N) {
+                        col = 0;
+                        s = scales[++m];
+                    }
                 }
             }
             store_f32<T, N>(out + i, f);
@@ -668,16 +698,19 @@ bool with_group(int64_t D, F &&f) {
     return held(integral_constant<int, 32>()) || held(integral_constant<int, 128>()) || held(integral_constant<int, 512>());
 }
 
-// The ring of a kernel: as many stages, of at least two, as half of an SM's
-// shared memory holds, so that two CTAs share it; else two stages.  bytes:
-// one stage of all the CTA's groups.  0 where two stages do not fit.
-constexpr int64_t kSharedHalf = 110 * 1024, kSharedMost = 226 * 1024;
+// The ring of a kernel with groups of G threads: as many stages as leave room
+// for two CTAs per SM of 8 warps, four of 4 warps or one of 16 (more CTAs
+// rather than more stages: one CTA's warps work while another's wait), but at
+// least two.  bytes: one stage of all the CTA's groups; gamma: its bytes, behind
+// them.  0 where two stages do not fit.
+constexpr int64_t kSharedMost = 225 * 1024;
 
-int ring_stages(int64_t bytes) {
-    int s = (int)(kSharedHalf / bytes);
+template <int G>
+int ring_stages(int64_t bytes, int64_t gamma) {
+    int s = (int)(((G == 32 ? 110 * 1024 : G == 128 ? 54 * 1024 : kSharedMost) - gamma) / bytes);
     if (s < 2) s = 2;
     if (s > kMaxStages) s = kMaxStages;
-    return s * bytes <= kSharedMost ? s : 0;
+    return s * bytes + gamma <= kSharedMost ? s : 0;
 }
 
 // CTAs of the kernels with a ring: as many as run at once, and no more partial
@@ -709,14 +742,15 @@ cudaError_t launch_fwd(const FwdArgs<T> &a, cudaStream_t s) {
         } else {
             constexpr int kRows = kRingThreads<G> / G;
             const int64_t stage = (int64_t)kRows * (a.residual ? 2 : 1) * row_slot(a.D * sizeof(T));
-            const int stages = ring_stages(stage);
+            const int stages = ring_stages<G>(stage, a.D * (int64_t)sizeof(T));
             fits = stages > 0;                            // else fp32 rows too long for two stages
             if (!fits) return;
             auto kern = norm_fwd_ring_kernel<T, G, H>;
-            err = allow_shared(kern, stages * stage);
+            const int64_t smem = stages * stage + a.D * (int64_t)sizeof(T);
+            err = allow_shared(kern, smem);
             if (err == cudaSuccess)
-                err = launch_k(kern, dim3((unsigned)ring_ctas(a.M, kRows, stages * stage)), dim3(kRingThreads<G>),
-                               (size_t)(stages * stage), s, 1, a, stages);
+                err = launch_k(kern, dim3((unsigned)ring_ctas(a.M, kRows, smem)), dim3(kRingThreads<G>), (size_t)smem, s,
+                               1, a, stages);
         }
     });
     if (!held || !fits)
@@ -740,9 +774,9 @@ cudaError_t launch_bwd(const BwdArgs<T> &a, T *dgamma, cudaStream_t s) {
     bool held = with_group<N>(a.D, [&](auto g, auto h) {
         constexpr int G = g(), H = h(), kRows = kRingThreads<G> / G;
         const int64_t stage = (int64_t)kRows * (a.dh ? 3 : 2) * row_slot(a.D * sizeof(T));
-        const int stages = ring_stages(stage);
+        const int stages = ring_stages<G>(stage, a.D * (int64_t)sizeof(T));
         if (stages == 0) return;                          // fp32 rows too long for two stages: the long kernel
-        int64_t smem = stages * stage;
+        int64_t smem = stages * stage + a.D * (int64_t)sizeof(T);
         const int64_t parts = kRows > 1 ? (int64_t)kRows * a.D * (int64_t)sizeof(float) : 0;
         if (smem < parts) smem = parts;
         ctas = ring_ctas(a.M, kRows, smem);

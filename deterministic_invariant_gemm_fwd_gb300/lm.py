@@ -92,6 +92,10 @@ def _bytes(nbytes):
     return nbytes
 
 
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
 def embedding_fwd(table, ids, scale=1.0, stream=None):
     """scale * table[ids]: table [V, D], ids int64 of any shape -> [*ids.shape, D]."""
     import torch
@@ -101,7 +105,9 @@ def embedding_fwd(table, ids, scale=1.0, stream=None):
     code = _dtype("table", table)
     s, empty, _ = _begin(table, stream)
     out = empty((*shape, D), table.dtype, table.device)
-    _b.carbon_embedding_fwd(out, table, ids, ids.numel(), V, D, scale, code, s)
+    st = _b.lib.carbon_embedding_fwd(out.data_ptr(), table.data_ptr(), ids.data_ptr(), ids.numel(), V, D, scale, code, s)
+    if st:
+        _b._check(st, "carbon_embedding_fwd")
     return out
 
 
@@ -120,10 +126,12 @@ def embedding_bwd(dy, ids, num_rows, scale=1.0, padding_idx=-1, accumulate_to=No
     s, empty, workspace = _begin(dy, stream)
     out = accumulate_to if accumulate_to is not None else empty((num_rows, D), dy.dtype, dy.device)
     M = ids.numel()
-    nbytes = _bytes(_b.carbon_embedding_bwd_workspace(M, num_rows, D))
+    nbytes = _bytes(_b.lib.carbon_embedding_bwd_workspace(M, num_rows, D))
     ws = workspace(nbytes, dy.device)
-    _b.carbon_embedding_bwd(out, dy, ids, M, num_rows, D, scale, padding_idx, accumulate_to is not None,
-                            ws, nbytes, code, s)
+    st = _b.lib.carbon_embedding_bwd(out.data_ptr(), dy.data_ptr(), ids.data_ptr(), M, num_rows, D, scale, padding_idx,
+                                     0 if accumulate_to is None else 1, ws.data_ptr(), nbytes, code, s)
+    if st:
+        _b._check(st, "carbon_embedding_bwd")
     return out
 
 
@@ -154,8 +162,10 @@ def rms_norm_fwd(x, gamma, residual=None, eps=1e-6, quantize=False, stream=None)
     if quantize:
         codes = empty(shape, torch.int8, device)
         scales = empty(M, torch.float32, device)
-    _b.carbon_rms_norm_fwd(y, None if residual is None else h, rstd, codes, scales, x, residual, gamma, M, D,
-                           eps, code, s)
+    st = _b.lib.carbon_rms_norm_fwd(y.data_ptr(), None if residual is None else h.data_ptr(), rstd.data_ptr(), _p(codes),
+                                    _p(scales), x.data_ptr(), _p(residual), gamma.data_ptr(), M, D, eps, code, s)
+    if st:
+        _b._check(st, "carbon_rms_norm_fwd")
     return RmsNorm(y, h, rstd, codes, scales)
 
 
@@ -182,9 +192,12 @@ def rms_norm_bwd(dy, gamma, rstd, h=None, codes=None, scales=None, dh=None, reco
     dx = empty(shape, dtype, device)
     dgamma = empty(D, dtype, device)
     y = empty(shape, dtype, device) if recompute else None
-    nbytes = _bytes(_b.carbon_rms_norm_bwd_workspace(M, D))
+    nbytes = _bytes(_b.lib.carbon_rms_norm_bwd_workspace(M, D))
     ws = workspace(nbytes, device)
-    _b.carbon_rms_norm_bwd(dx, dgamma, y, dy, h, codes, scales, rstd, gamma, dh, M, D, ws, nbytes, code, s)
+    st = _b.lib.carbon_rms_norm_bwd(dx.data_ptr(), dgamma.data_ptr(), _p(y), dy.data_ptr(), _p(h), _p(codes), _p(scales),
+                                    rstd.data_ptr(), gamma.data_ptr(), _p(dh), M, D, ws.data_ptr(), nbytes, code, s)
+    if st:
+        _b._check(st, "carbon_rms_norm_bwd")
     return (dx, dgamma, y) if recompute else (dx, dgamma)
 
 
@@ -199,7 +212,10 @@ def rms_norm_expand(codes, scales, gamma=None, dtype=None, stream=None):
         _need("gamma", gamma, (D,), dtype)
     s, empty, _ = _begin(codes, stream)
     out = empty(shape, dtype, codes.device)
-    _b.carbon_rms_norm_expand(out, codes, scales, gamma, M, D, _dtype("the output", out), s)
+    st = _b.lib.carbon_rms_norm_expand(out.data_ptr(), codes.data_ptr(), scales.data_ptr(), _p(gamma), M, D,
+                                       _dtype("the output", out), s)
+    if st:
+        _b._check(st, "carbon_rms_norm_expand")
     return out
 
 
@@ -228,10 +244,12 @@ def linear_cross_entropy_fwd(x, table, targets, ignore_index=-100, reduction="me
     losses = empty(M, torch.float32, device)
     lse = empty(M, torch.float32, device)
     total = empty((), torch.float32, device) if red else None
-    nbytes = _bytes(_b.carbon_linear_xent_fwd_workspace(M, D, V))
+    nbytes = _bytes(_b.lib.carbon_linear_xent_fwd_workspace(M, D, V))
     ws = workspace(nbytes, device)
-    _b.carbon_linear_xent_fwd(losses, total, lse, None, x, table, targets, M, D, V, ignore_index, red, ws, nbytes,
-                              code, s)
+    st = _b.lib.carbon_linear_xent_fwd(losses.data_ptr(), _p(total), lse.data_ptr(), None, x.data_ptr(), table.data_ptr(),
+                                       targets.data_ptr(), M, D, V, ignore_index, red, ws.data_ptr(), nbytes, code, s)
+    if st:
+        _b._check(st, "carbon_linear_xent_fwd")
     return (total if red else losses), lse
 
 
@@ -245,8 +263,11 @@ def linear_cross_entropy_bwd(grad, x, table, targets, lse, ignore_index=-100, re
     s, empty, workspace = _begin(x, stream)
     dx = empty((M, D), x.dtype, device)
     dtable = empty((V, D), x.dtype, device)
-    nbytes = _bytes(_b.carbon_linear_xent_bwd_workspace(M, D, V))
+    nbytes = _bytes(_b.lib.carbon_linear_xent_bwd_workspace(M, D, V))
     ws = workspace(nbytes, device)
-    _b.carbon_linear_xent_bwd(dx, dtable, grad, x, table, targets, lse, M, D, V, ignore_index, red, ws, nbytes,
-                              code, s)
+    st = _b.lib.carbon_linear_xent_bwd(dx.data_ptr(), dtable.data_ptr(), grad.data_ptr(), x.data_ptr(), table.data_ptr(),
+                                       targets.data_ptr(), lse.data_ptr(), M, D, V, ignore_index, red, ws.data_ptr(),
+                                       nbytes, code, s)
+    if st:
+        _b._check(st, "carbon_linear_xent_bwd")
     return dx, dtable
