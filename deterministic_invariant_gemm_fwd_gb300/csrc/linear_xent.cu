@@ -73,11 +73,13 @@ constexpr int64_t kSlotBytes = 64ll << 20;    // dx: granule sums side by side u
 // common factor takes it out again.  |G| <= 2^k: no sum comes near fp32's
 // range for operands of ordinary size.
 constexpr int kScaleBits16 = 12, kScaleBitsBf = 32;
+constexpr int64_t kCountAhead = 16384;   // longer lists of positions are counted by a kernel of their own
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Head {
     int kept;                            // positions that count
     float gscale;                        // the gradients' common factor
+    float gmax;                          // largest |g|, where xent_count_kernel has run
 };
 
 // Sizes and workspace addresses, host and device.
@@ -92,7 +94,9 @@ struct Plan {
     int slots;                           // granule sums of dx kept side by side; 1: added in place
     bool f16, grad;
     Head *head;
+    int *ahead;                          // positions that count before each block of 128, or null
     unsigned int *ticket;                // next unit
+    unsigned int *joined;                // CTAs of xent_join_kernel that are done
     unsigned int *done_l, *done_tx;      // per piece
     int *rowmap, *inverse, *tgt;
     float *lse2, *rfac;                  // gradient: lse log2(e) - k, g / max |g|
@@ -133,8 +137,10 @@ int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, bool gra
         return q;
     };
     p.head = reinterpret_cast<Head *>(take(sizeof(Head)));
-    p.ticket = reinterpret_cast<unsigned int *>(take(4 + 8 * (int64_t)p.pieces));
-    p.done_l = p.ticket + 1;
+    if (M > kCountAhead) p.ahead = reinterpret_cast<int *>(take(4 * (p.Mp / 128)));
+    p.ticket = reinterpret_cast<unsigned int *>(take(4 * (2 + 2 * (int64_t)p.pieces)));
+    p.joined = p.ticket + 1;
+    p.done_l = p.ticket + 2;
     p.done_tx = p.done_l + p.pieces;
     p.rowmap = reinterpret_cast<int *>(take(4 * p.Mp));
     p.inverse = reinterpret_cast<int *>(take(4 * p.Mp));
@@ -160,10 +166,6 @@ void *align128(void *p) {
 
 // ---- positions that count --------------------------------------------------------
 
-// One CTA: the list of positions that count, in order, and per position what
-// the tiles need of it.  Loss: writes the zeros of ignored positions.
-constexpr int kScanThreads = 1024, kPerThread = 8;
-
 struct ScanArgs {
     const int64_t *targets;
     int64_t ignore_index;
@@ -173,123 +175,170 @@ struct ScanArgs {
     const float *grad, *lse_in;          // gradient
 };
 
-__global__ void __launch_bounds__(kScanThreads)
-xent_scan_kernel(const Plan p, const ScanArgs a) {
-    __shared__ int warp_total[32];
-    __shared__ float warp_max[32];
-    __shared__ int base_s;
-    wait_prior_grid();
-    allow_next_grid();
-    const int t = threadIdx.x, lane = t % 32, warp = t / 32;
-    const int bits = p.f16 ? kScaleBits16 : kScaleBitsBf;
-    for (int i = t; i < 1 + 2 * p.pieces; i += kScanThreads) p.ticket[i] = 0u;
-
-    auto counts = [&](int64_t m, int64_t *tgt) {
-        *tgt = a.targets[m];
-        return *tgt != a.ignore_index && *tgt >= 0 && *tgt < p.V;
-    };
-    // largest |g| over the positions that count (a gradient per position)
-    float gmax = 0.0f;
-    if (p.grad && a.reduction == CARBON_REDUCE_NONE) {
-        int64_t tgt;
-        for (int64_t m = t; m < p.M; m += kScanThreads)
-            if (counts(m, &tgt)) gmax = fmaxf(gmax, fabsf(a.grad[m]));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) gmax = fmaxf(gmax, __shfl_xor_sync(0xffffffffu, gmax, o));
-        if (lane == 0) warp_max[warp] = gmax;
-        __syncthreads();
-        gmax = warp_max[0];
-        for (int w = 1; w < 32; ++w) gmax = fmaxf(gmax, warp_max[w]);
-    }
-    if (t == 0) base_s = 0;
-    __syncthreads();
-    for (int64_t m0 = 0; m0 < p.M; m0 += kScanThreads * kPerThread) {
-        int64_t tgt[kPerThread];
-        unsigned keep = 0u;
-        int n = 0;
-#pragma unroll
-        for (int j = 0; j < kPerThread; ++j) {
-            const int64_t m = m0 + (int64_t)t * kPerThread + j;
-            tgt[j] = a.ignore_index;
-            if (m < p.M && CHK(m, 1, p.M)) {
-                if (counts(m, &tgt[j])) { keep |= 1u << j; ++n; }
-                else if (tgt[j] != a.ignore_index) atomicExch(&g_xent_status, (unsigned)CARBON_ERR_OUT_OF_BOUNDS);
-            }
-        }
-        int incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) warp_total[warp] = incl;
-        __syncthreads();
-        int pos = base_s + incl - n;
-        for (int w = 0; w < warp; ++w) pos += warp_total[w];
-        __syncthreads();
-        if (t == kScanThreads - 1) base_s = pos + n;
-#pragma unroll
-        for (int j = 0; j < kPerThread; ++j) {
-            const int64_t m = m0 + (int64_t)t * kPerThread + j;
-            if (m >= p.M) break;
-            const bool k = (keep >> j) & 1u;
-            p.inverse[m] = k ? pos : -1;
-            if (k && CHK(pos, 1, p.Mp)) {
-                p.rowmap[pos] = (int)m;
-                p.tgt[pos] = (int)tgt[j];
-                if (p.grad) {
-                    p.lse2[pos] = fmaf(a.lse_in[m], kLog2e, (float)-bits);
-                    p.rfac[pos] = a.reduction != CARBON_REDUCE_NONE ? 1.0f
-                                  : gmax == 0.0f ? 0.0f : __fdiv_rn(a.grad[m], gmax);
-                }
-                ++pos;
-            } else if (!p.grad) {
-                a.losses[m] = 0.0f;
-                a.lse_out[m] = 0.0f;
-            }
-        }
-        __syncthreads();
-    }
-    const int kept = base_s;
-    for (int64_t i = kept + t; i < p.Mp; i += kScanThreads) {
-        p.rowmap[i] = -1;
-        p.tgt[i] = -1;
-        if (p.grad) p.lse2[i] = p.rfac[i] = 0.0f;
-    }
-    if (t == 0) {
-        p.head->kept = kept;
-        if (a.count) *a.count = kept;
-        if (p.grad) {
-            float g = a.reduction == CARBON_REDUCE_NONE ? gmax : a.grad[0];
-            if (a.reduction == CARBON_REDUCE_MEAN) g = __fdiv_rn(g, (float)(kept > 0 ? kept : 1));
-            p.head->gscale = ldexpf(g, -bits);
-        }
-    }
+__device__ __forceinline__ bool counts(const Plan &p, const ScanArgs &a, int64_t m, int64_t *tgt) {
+    *tgt = a.targets[m];
+    return *tgt != a.ignore_index && *tgt >= 0 && *tgt < p.V;
 }
 
 __device__ __forceinline__ int row_tiles(int kept) { return kept > kBM ? (kept + kBM - 1) / kBM : 1; }
 
-// Dense rows of x in blocks; zeros up to the last tile's end and past D.  A
-// CTA per block; 8 threads per position and 128-byte row.
-__global__ void __launch_bounds__(256)
-xent_gather_kernel(const Plan p, const uint4 *__restrict__ x) {
+// Long lists: positions that count ahead of each block of 128, and the largest
+// |g| (a gradient per position).  One CTA, a warp per block.
+constexpr int kCountThreads = 1024;
+
+__global__ void __launch_bounds__(kCountThreads)
+xent_count_kernel(const Plan p, const ScanArgs a) {
+    __shared__ int counted[32];
+    __shared__ float top[32];
     wait_prior_grid();
     allow_next_grid();
-    const int64_t rows = (int64_t)row_tiles(p.head->kept) * kBM;
-    if ((int64_t)blockIdx.x * 128 >= rows) return;
-    const int q = threadIdx.x % 8, blk = blockIdx.y;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t blocks = (p.M + 127) / 128;
+    float gmax = 0.0f;
+    int base = 0;
+    for (int64_t b0 = 0; b0 < blocks; b0 += 32) {
+        int n = 0;
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = (b0 + warp) * 128 + j * 32 + lane;
+            int64_t tgt;
+            const bool k = m < p.M && counts(p, a, m, &tgt);
+            n += __popc(__ballot_sync(0xffffffffu, k));
+            if (k && p.grad && a.reduction == CARBON_REDUCE_NONE) gmax = fmaxf(gmax, fabsf(a.grad[m]));
+        }
+        if (lane == 0) counted[warp] = n;
+        __syncthreads();
+        int before = base;
+        for (int w = 0; w < 32; ++w) {
+            if (w == warp && lane == 0 && b0 + warp < blocks) p.ahead[b0 + warp] = before;
+            before += counted[w];
+        }
+        base = before;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) gmax = fmaxf(gmax, __shfl_xor_sync(0xffffffffu, gmax, o));
+    if (lane == 0) top[warp] = gmax;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 32; ++w) gmax = fmaxf(gmax, top[w]);
+        p.head->gmax = gmax;
+    }
+}
+
+// A CTA per 128 positions and 64 columns: the positions that count move up, in
+// order, into x's blocks, with zeros up to the last tile's end and past D; the
+// CTAs of the first columns also write what the tiles need of each position,
+// and the zeros of ignored ones.  Without `ahead` a CTA counts the positions
+// before its own by itself (up to kCountAhead of them: 1 us, a launch less).
+constexpr int kPrepThreads = 256;
+
+__global__ void __launch_bounds__(kPrepThreads)
+xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x) {
+    __shared__ int part[kPrepThreads / 32], flag_words[4];
+    __shared__ float part_max[kPrepThreads / 32];
+    __shared__ int place[128];                            // a position's place, or -1
+    wait_prior_grid();
+    allow_next_grid();
+    const int t = threadIdx.x, lane = t % 32, warp = t / 32;
+    const int64_t first = (int64_t)blockIdx.x * 128;
+    const bool lead = blockIdx.y == 0, last = blockIdx.x == gridDim.x - 1;
+    const bool each = p.grad && a.reduction == CARBON_REDUCE_NONE;
+
+    int n = 0;
+    float gmax = 0.0f;
+    int64_t tgt;
+    if (p.ahead == nullptr) {
+        const bool all = each && lead;                    // the largest |g| is taken over the whole list
+        for (int64_t m = t; m < (all ? p.M : first); m += kPrepThreads)
+            if (counts(p, a, m, &tgt)) {
+                n += m < first ? 1 : 0;
+                if (all) gmax = fmaxf(gmax, fabsf(a.grad[m]));
+            }
+        n = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) gmax = fmaxf(gmax, __shfl_xor_sync(0xffffffffu, gmax, o));
+        if (lane == 0) { part[warp] = n; part_max[warp] = gmax; }
+    }
+    int64_t mine = a.ignore_index;
+    bool keep = false;
+    if (t < 128) {
+        const int64_t m = first + t;
+        if (m < p.M && CHK(m, 1, p.M)) {
+            keep = counts(p, a, m, &mine);
+            if (lead && !keep && mine != a.ignore_index) atomicExch(&g_xent_status, (unsigned)CARBON_ERR_OUT_OF_BOUNDS);
+        }
+        const unsigned word = __ballot_sync(0xffffffffu, keep);
+        if (lane == 0) flag_words[warp] = (int)word;
+    }
+    __syncthreads();
+    int base = 0;
+    if (p.ahead == nullptr) {
+        gmax = 0.0f;
+        for (int w = 0; w < kPrepThreads / 32; ++w) { base += part[w]; gmax = fmaxf(gmax, part_max[w]); }
+    } else {
+        base = p.ahead[blockIdx.x];
+        gmax = p.head->gmax;
+    }
+    int here = 0;                                         // of this CTA's positions
+    for (int w = 0; w < 4; ++w) here += __popc((unsigned)flag_words[w]);
+    if (t < 128) {
+        int pos = base + __popc((unsigned)flag_words[warp] & ((1u << lane) - 1u));
+        for (int w = 0; w < warp; ++w) pos += __popc((unsigned)flag_words[w]);
+        place[t] = keep ? pos : -1;
+        const int64_t m = first + t;
+        if (lead && m < p.M) {
+            p.inverse[m] = keep ? pos : -1;
+            if (keep && CHK(pos, 1, p.Mp)) {
+                p.rowmap[pos] = (int)m;
+                p.tgt[pos] = (int)mine;
+                if (p.grad) {
+                    p.lse2[pos] = fmaf(a.lse_in[m], kLog2e, (float)-(p.f16 ? kScaleBits16 : kScaleBitsBf));
+                    p.rfac[pos] = !each ? 1.0f : gmax == 0.0f ? 0.0f : __fdiv_rn(a.grad[m], gmax);
+                }
+            } else if (!keep && !p.grad) {
+                a.losses[m] = 0.0f;
+                a.lse_out[m] = 0.0f;
+            }
+        }
+    }
+    __syncthreads();
+
+    // 8 threads per position and 128-byte row of a block
+    const int q = t % 8, blk = blockIdx.y;
     const int64_t nvec = p.D / 8;
-    uint4 *dst = static_cast<uint4 *>(p.xc) + ((int64_t)blockIdx.x * p.xblocks + blk) * (128 * 8);
+    uint4 *blocks = static_cast<uint4 *>(p.xc);
+    auto put = [&](int64_t pos, uint4 v) {
+        const int64_t row = (pos / 128 * p.xblocks + blk) * 128 + pos % 128;
+        if (CHK(row * 8, 8, p.Mp * p.xblocks * 8)) blocks[row * 8 + (q ^ (int)(pos & 7))] = v;
+    };
     uint4 v[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-        const int64_t src = p.rowmap[blockIdx.x * 128 + u * 32 + threadIdx.x / 8];
-        v[u] = src >= 0 && blk * 8 + q < nvec ? x[src * nvec + blk * 8 + q] : make_uint4(0u, 0u, 0u, 0u);
+        const int64_t m = first + u * 32 + t / 8;
+        v[u] = place[u * 32 + t / 8] >= 0 && blk * 8 + q < nvec ? x[m * nvec + blk * 8 + q] : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int r = u * 32 + threadIdx.x / 8;
-        if (CHK(dst + r * 8 - static_cast<uint4 *>(p.xc), 8, p.Mp * p.xblocks * 8)) dst[r * 8 + (q ^ (r & 7))] = v[u];
+    for (int u = 0; u < 4; ++u)
+        if (place[u * 32 + t / 8] >= 0) put(place[u * 32 + t / 8], v[u]);
+    if (!last) return;
+
+    const int kept = base + here;
+    const int64_t rows = (int64_t)row_tiles(kept) * kBM;
+    for (int64_t i = kept + t / 8; i < rows; i += kPrepThreads / 8) put(i, make_uint4(0u, 0u, 0u, 0u));
+    if (!lead) return;
+    for (int64_t i = kept + t; i < rows; i += kPrepThreads) {
+        p.tgt[i] = -1;
+        if (p.grad) p.lse2[i] = p.rfac[i] = 0.0f;
+    }
+    for (int i = t; i < 2 + 2 * p.pieces; i += kPrepThreads) p.ticket[i] = 0u;
+    if (t == 0) {
+        p.head->kept = kept;
+        if (a.count) *a.count = kept;
+        if (p.grad) {
+            float g = each ? gmax : a.grad[0];
+            if (a.reduction == CARBON_REDUCE_MEAN) g = __fdiv_rn(g, (float)(kept > 0 ? kept : 1));
+            p.head->gscale = ldexpf(g, -(p.f16 ? kScaleBits16 : kScaleBitsBf));
+        }
     }
 }
 
@@ -1078,54 +1127,58 @@ xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan
 // ---- joining ---------------------------------------------------------------------------
 
 // lse and loss of 32 rows: 32 threads per row take every 32nd pair, in order,
-// and their pairs are joined in thread order.
+// and their pairs are joined in thread order.  The CTA that finishes last adds
+// the losses (total not null): every thread its positions in order, the
+// threads' sums in a fixed tree, in float64.
 __global__ void __launch_bounds__(1024)
-xent_join_kernel(const Plan p, float *__restrict__ losses, float *__restrict__ lse) {
-    __shared__ float2 part[32][33];
+xent_join_kernel(const Plan p, float *__restrict__ losses, float *__restrict__ lse, float *__restrict__ total, int mean) {
+    __shared__ union {
+        float2 pair[32][33];
+        double sum[1024];
+    } sh;
+    __shared__ bool finish;
     wait_prior_grid();
     allow_next_grid();
     const int r = threadIdx.x % 32, t = threadIdx.x / 32;
     const int64_t row = (int64_t)blockIdx.x * 32 + r;
     const int kept = p.head->kept;
-    if ((int64_t)blockIdx.x * 32 >= kept) return;         // CTA-uniform
-    float mx = -INFINITY, sum = 0.0f;
-    auto join = [&](float2 q) {
-        const float now = fmaxf(mx, q.x), ref = now == -INFINITY ? 0.0f : now;
-        sum = sum * ex2(mx - ref) + q.y * ex2(q.x - ref);
-        mx = now;
-    };
+    if ((int64_t)blockIdx.x * 32 < kept) {                // CTA-uniform
+        float mx = -INFINITY, sum = 0.0f;
+        auto join = [&](float2 q) {
+            const float now = fmaxf(mx, q.x), ref = now == -INFINITY ? 0.0f : now;
+            sum = sum * ex2(mx - ref) + q.y * ex2(q.x - ref);
+            mx = now;
+        };
 #pragma unroll 4
-    for (int g = t; g < p.vocab_groups; g += 32)
-        if (CHK((int64_t)g * p.Mp + row, 1, p.vocab_groups * p.Mp)) join(p.pairs[(int64_t)g * p.Mp + row]);
-    part[t][r] = make_float2(mx, sum);
+        for (int g = t; g < p.vocab_groups; g += 32)
+            if (CHK((int64_t)g * p.Mp + row, 1, p.vocab_groups * p.Mp)) join(p.pairs[(int64_t)g * p.Mp + row]);
+        sh.pair[t][r] = make_float2(mx, sum);
+        __syncthreads();
+        if (t == 0 && row < kept) {
+            for (int i = 1; i < 32; ++i) join(sh.pair[i][r]);
+            const float l = (mx + log2f(sum)) * kLn2;
+            const int64_t m = p.rowmap[row];
+            lse[m] = l;
+            losses[m] = l - p.zt[row];
+        }
+    }
+    if (total == nullptr) return;
+    if (t == 0) __threadfence();                          // this CTA's losses, before its count
     __syncthreads();
-    if (t != 0 || row >= kept) return;
-    for (int i = 1; i < 32; ++i) join(part[i][r]);
-    const float l = (mx + log2f(sum)) * kLn2;
-    const int64_t m = p.rowmap[row];
-    lse[m] = l;
-    losses[m] = l - p.zt[row];
-}
-
-// Sum (and mean) of the losses: one CTA, every thread its positions in order,
-// the threads' sums in a fixed tree, in float64.
-__global__ void __launch_bounds__(1024)
-xent_total_kernel(const Plan p, const float *__restrict__ losses, float *__restrict__ total, int mean) {
-    __shared__ double part[1024];
-    wait_prior_grid();
-    allow_next_grid();
+    if (threadIdx.x == 0) finish = atomicAdd(p.joined, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!finish) return;
+    __threadfence();
     double s = 0.0;
-    for (int64_t m = threadIdx.x; m < p.M; m += 1024) s += (double)losses[m];
-    part[threadIdx.x] = s;
+#pragma unroll 8
+    for (int64_t m = threadIdx.x; m < p.M; m += 1024) s += (double)__ldcg(losses + m);
+    sh.sum[threadIdx.x] = s;
     __syncthreads();
     for (int o = 512; o > 0; o >>= 1) {
-        if (threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
+        if (threadIdx.x < o) sh.sum[threadIdx.x] += sh.sum[threadIdx.x + o];
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        const int kept = p.head->kept;
-        total[0] = (float)(mean ? part[0] / (double)(kept > 0 ? kept : 1) : part[0]);
-    }
+    if (threadIdx.x == 0) total[0] = (float)(mean ? sh.sum[0] / (double)(kept > 0 ? kept : 1) : sh.sum[0]);
 }
 
 // dx rows: the granule sums in order, scaled and rounded; zeros for ignored
@@ -1234,12 +1287,15 @@ cudaError_t launch_tiles(const Plan &p, const void *table, void *dtable, int sms
     return launch_k(kern, dim3((unsigned)(sms / 2 * 2)), dim3(kThreads), (size_t)kSmemBytes, s, 1, maps, p);
 }
 
-cudaError_t launch_gather(const Plan &p, const ScanArgs &a, const void *x, cudaStream_t s) {
-    count_launch(2);
-    const cudaError_t err = launch_k(xent_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, 1, p, a);
-    if (err != cudaSuccess) return err;
-    return launch_k(xent_gather_kernel, dim3((unsigned)(p.Mp / 128), (unsigned)p.xblocks), dim3(256), 0, s, 1, p,
-                    static_cast<const uint4 *>(x));
+cudaError_t launch_prepare(const Plan &p, const ScanArgs &a, const void *x, cudaStream_t s) {
+    if (p.ahead) {
+        count_launch();
+        const cudaError_t err = launch_k(xent_count_kernel, dim3(1), dim3(kCountThreads), 0, s, 1, p, a);
+        if (err != cudaSuccess) return err;
+    }
+    count_launch();
+    return launch_k(xent_prepare_kernel, dim3((unsigned)((p.M + 127) / 128), (unsigned)p.xblocks), dim3(kPrepThreads), 0, s,
+                    1, p, a, static_cast<const uint4 *>(x));
 }
 
 }  // namespace
@@ -1291,16 +1347,12 @@ carbon_status_t carbon_linear_xent_fwd(float *losses, float *total, float *lse, 
     ScanArgs a = {};
     a.targets = targets; a.ignore_index = ignore_index; a.reduction = reduction;
     a.losses = losses; a.lse_out = lse; a.count = count;
-    cudaError_t err = launch_gather(p, a, x, s);
+    cudaError_t err = launch_prepare(p, a, x, s);
     if (err == cudaSuccess) err = launch_tiles<false>(p, table, nullptr, sms, s);
     if (err == cudaSuccess) {
         count_launch();
-        err = launch_k(xent_join_kernel, dim3((unsigned)((M + 31) / 32)), dim3(1024), 0, s, 1, p, losses, lse);
-    }
-    if (err == cudaSuccess && reduction != CARBON_REDUCE_NONE) {
-        count_launch();
-        err = launch_k(xent_total_kernel, dim3(1), dim3(1024), 0, s, 1, p, (const float *)losses, total,
-                       reduction == CARBON_REDUCE_MEAN ? 1 : 0);
+        err = launch_k(xent_join_kernel, dim3((unsigned)((M + 31) / 32)), dim3(1024), 0, s, 1, p, losses, lse,
+                       reduction == CARBON_REDUCE_NONE ? nullptr : total, reduction == CARBON_REDUCE_MEAN ? 1 : 0);
     }
     return note_cuda(err);
 }
@@ -1328,7 +1380,7 @@ carbon_status_t carbon_linear_xent_bwd(void *dx, void *dtable, const float *grad
     ScanArgs a = {};
     a.targets = targets; a.ignore_index = ignore_index; a.reduction = reduction;
     a.grad = grad; a.lse_in = lse;
-    cudaError_t err = launch_gather(p, a, x, s);
+    cudaError_t err = launch_prepare(p, a, x, s);
     if (err == cudaSuccess) err = launch_tiles<true>(p, table, dtable, sms, s);
     if (err == cudaSuccess) {
         count_launch();

@@ -405,6 +405,27 @@ def test_cross_entropy_large_batch_matches_small_ones():
     assert same_bits(again[0], dx) and same_bits(again[1], dt)
 
 
+@pytest.mark.parametrize("reduction", ["none", "mean"])
+def test_cross_entropy_long_list(reduction):
+    """More positions than a tile kernel's preparation counts by itself."""
+    M, D, V = 20011, 64, 300
+    x, table, t = xent_case(M, D, V, "bf16", 21, kept=0.6)
+    grad = torch.randn(M, generator=gen(22), device="cuda") if reduction == "none" else torch.tensor(2.0, device="cuda")
+    count = int((t >= 0).sum())
+    rows = grad if reduction == "none" else torch.full((M,), 2.0 / count, device="cuda", dtype=torch.float64)
+    loss, lse, keep, eloss, dx, dt, edx, edt = xent_reference(x, table, t, rows)
+    got, glse = cg.linear_cross_entropy_fwd(x, table, t, reduction=reduction)
+    within(glse, torch.where(keep, lse, 0.0), eloss)
+    if reduction == "none":
+        within(got, loss, eloss)
+    else:
+        within(got, loss.sum() / count, eloss.sum() / count)
+    gdx, gdt = cg.linear_cross_entropy_bwd(grad, x, table, t, glse, reduction=reduction)
+    within(gdx, dx, edx + 2 * E * dx.abs())
+    within(gdt, dt, edt + 2 * E * dt.abs())
+    assert not bool(gdx[~keep].any()) and status() == 0
+
+
 def test_cross_entropy_ignored_positions_hold_anything():
     M, D, V = 300, 64, 500
     x, table, t = xent_case(M, D, V, "bf16", 8, kept=0.5)
