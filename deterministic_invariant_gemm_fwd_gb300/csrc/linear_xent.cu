@@ -15,17 +15,16 @@
 //      in order.  Gradient: exp(z - lse) - onehot goes out as G.
 //   T  256 vocabulary entries x up to 256 columns of dtable, reduced over
 //      the positions: G^T . x.
-//   X  256 positions x up to 256 columns of dx, reduced over kGranule
-//      vocabulary entries at a time: G . table.
-// The gradient takes the vocabulary in pieces: L units of piece p + 1 run
-// before the T and X units of piece p, and G keeps three pieces, so that a
-// unit rarely waits for the units it reads (counters in the workspace; units
-// are handed out in list order and wait only for earlier ones, so the waits
-// end).
+//   X  256 positions x up to 256 columns of dx, reduced over a piece of the
+//      vocabulary: G . table.
+// The gradient takes the vocabulary in pieces of kPiece entries: L units of
+// later pieces run before the T and X units of a piece, so that a unit rarely
+// waits for the units it reads (counters in the workspace; units are handed
+// out in list order and wait only for earlier ones, so the waits end).
 //
 // Fixed order: a unit's k-blocks of 64 run in ascending order into one fp32
-// accumulator.  dx adds the granules' sums in order, so neither the piece
-// size nor the number of positions shows in a row's result.
+// accumulator.  dx adds the pieces' sums in order, and a piece's size is
+// fixed, so the number of positions does not show in a row's result.
 #include "bounds.cuh"
 #include "device_sync.cuh"
 #include "rowvec.cuh"
@@ -38,7 +37,7 @@ __device__ unsigned int g_xent_status = 0;
 #define CHK(idx, len, n) in_bounds(&g_xent_status, (int64_t)(idx), (int64_t)(len), (int64_t)(n))
 
 constexpr int kBM = 256, kBN = 256, kBK = 64;        // a CTA pair's tile; each CTA has 128 rows
-constexpr int kStages = 6;
+constexpr int kStages = 5;                             // (six ran no faster)
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (4 + kEpiWarps);        // TMA producer, MMA issuer, scheduler, reporter, epilogue
 constexpr uint32_t kBlock = 64 * kBK * 2;             // one 64 x 64 box: 8 KiB
@@ -46,7 +45,8 @@ constexpr uint32_t kABytes = 128 * kBK * 2;           // per CTA: 128 rows of A,
 constexpr uint32_t kStageBytes = kABytes + kBN / 2 * kBK * 2;
 constexpr int kSlots = 6;                             // units handed out ahead
 constexpr uint32_t kStagingOffset = kStages * kStageBytes;
-constexpr uint32_t kBarOffset = kStagingOffset + kEpiWarps * 4096;
+constexpr uint32_t kStagingBytes = 2 * 4096;          // per epilogue warp: two sub-tiles
+constexpr uint32_t kBarOffset = kStagingOffset + kEpiWarps * kStagingBytes;
 constexpr int kBars = 2 * kStages + 4 + 3 * kSlots;
 constexpr uint32_t kUnitOffset = kBarOffset + kBars * 8;
 constexpr uint32_t kSmemBytes = kUnitOffset + kSlots * 32 + 16 + 1024;
@@ -55,8 +55,9 @@ static_assert(kSmemBytes <= 232448, "shared memory per block");
 constexpr unsigned kDone = 2;                         // reports of a finished unit: one per CTA
 
 constexpr int kGroup = 128;              // vocabulary entries per (max, sum) pair
-constexpr int kGranule = 4096;           // vocabulary entries per partial sum of dx
-constexpr int kPieceBuffers = 3;         // pieces of G in the workspace
+constexpr int kPiece = 4096;             // vocabulary entries per piece
+constexpr int64_t kGBytes = 64ll << 20;
+constexpr int64_t kSlotBytes = 64ll << 20;    // dx: the pieces' sums side by side up to this size, else added in place
 // x and G are kept as blocks of 128 positions x 64 columns that are images of
 // the MMA's operands in shared memory, for either orientation, so that a load
 // is contiguous bytes.
@@ -66,8 +67,6 @@ constexpr int kPieceBuffers = 3;         // pieces of G in the workspace
 // unswizzled layout, core matrices of 8 positions x 16 bytes): a warp of 32
 // positions writes 512 contiguous bytes a store, straight from its registers.
 constexpr int kPlane = 128 * 8, kPlanes = 8 * kPlane;         // elements of a plane, of a block
-constexpr int64_t kPieceBytes = 64ll << 20;   // largest piece of G, unless one granule is larger
-constexpr int64_t kSlotBytes = 64ll << 20;    // dx: granule sums side by side up to this size
 // G is formed times 2^k, so that probabilities far below the type's (fp16) or
 // fp32's (bf16) smallest normal value keep their bits; the gradients'
 // common factor takes it out again.  |G| <= 2^k: no sum comes near fp32's
@@ -88,16 +87,18 @@ struct Plan {
     int vocab_groups;                    // pairs per row
     int dtiles, dwidth;                  // column tiles of dx and dtable
     int xblocks;                         // blocks of x per 128 positions
+    int vocab_tiles;                     // rows of T units
     int lwidth;                          // vocabulary entries per L unit
-    int pieces, buffers, piece_cols;
-    int granules;
-    int slots;                           // granule sums of dx kept side by side; 1: added in place
+    int pieces, buffers;
+    int lead;                            // pieces whose L units run ahead of a piece's T and X units
+    int slots;                           // pieces' sums of dx kept side by side; 1: added in place
     bool f16, grad;
     Head *head;
     int *ahead;                          // positions that count before each block of 128, or null
     unsigned int *ticket;                // next unit
     unsigned int *joined;                // CTAs of xent_join_kernel that are done
-    unsigned int *done_l, *done_tx;      // per piece
+    unsigned int *done_l, *done_tx;      // finished L units, T and X units, per piece
+    unsigned int *done_v;                // finished L units per 256 vocabulary entries (what a T unit reads)
     int *rowmap, *inverse, *tgt;
     float *lse2, *rfac;                  // gradient: lse log2(e) - k, g / max |g|
     void *xc, *g;
@@ -114,20 +115,28 @@ int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, bool gra
     p.M = M; p.D = D; p.V = V; p.grad = grad; p.f16 = f16;
     p.Mp = round_up(M > 0 ? M : 1, kBM);
     p.vocab_groups = (int)((V + kGroup - 1) / kGroup);
-    p.dtiles = (int)((D + kBN - 1) / kBN);
-    p.dwidth = (int)round_up((D + p.dtiles - 1) / p.dtiles, 128);
+    p.pieces = grad ? (int)((V + kPiece - 1) / kPiece) : 1;
+    // tiles of at most 256 columns, of nearly equal widths
+    const int dtiles = (int)((D + kBN - 1) / kBN);
+    p.dwidth = (int)round_up((D + dtiles - 1) / dtiles, 128);
     p.dtiles = (int)((D + p.dwidth - 1) / p.dwidth);
-    p.granules = (int)((V + kGranule - 1) / kGranule);
     const int64_t tiles256 = p.Mp / kBM * ((V + kBN - 1) / kBN);
     // narrower tiles where 256-wide ones would leave SMs idle for most of a wave
     p.lwidth = tiles256 < 152 * 4 ? 128 : 256;
-    int64_t per_piece = kPieceBytes / (p.Mp * 2 * kGranule);
-    if (per_piece < 1) per_piece = 1;
-    if (per_piece > p.granules) per_piece = p.granules;
-    p.piece_cols = (int)(per_piece * kGranule);
-    p.pieces = (int)((V + p.piece_cols - 1) / p.piece_cols);
-    p.buffers = p.pieces < kPieceBuffers ? p.pieces : kPieceBuffers;
-    p.slots = (int64_t)p.granules * p.Mp * D * 4 <= kSlotBytes ? p.granules : 1;
+    // How many pieces' L units run ahead of a piece's T and X units: two units
+    // for each of the 76 pairs of CTAs, so that what a T or X unit reads is
+    // complete when its turn comes; all of them where that is at most eight
+    // each (1 x 768 x 50257: 119 us for the gradient with the loss against 146,
+    // 509 x 512 x 32003: 103 against 126; but 1200 x 768 x 50257: 333 against
+    // 319).  G has room for the pieces ahead, the one that is read and one
+    // more; small ones are all kept.
+    const int64_t l_units = p.Mp / kBM * ((kPiece + p.lwidth - 1) / p.lwidth);
+    const int64_t lead = l_units * p.pieces <= 8 * 76 ? p.pieces : (2 * 76 + l_units - 1) / l_units;
+    int64_t buffers = kGBytes / (p.Mp * 2 * kPiece);
+    if (buffers < lead + 2) buffers = lead + 2;
+    p.lead = (int)(lead < p.pieces ? lead : p.pieces);
+    p.buffers = (int)(buffers < p.pieces ? buffers : p.pieces);
+    p.slots = (int64_t)p.pieces * p.Mp * D * 4 <= kSlotBytes ? p.pieces : 1;
 
     char *base = static_cast<char *>(ws);
     int64_t used = 0;
@@ -138,10 +147,12 @@ int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, bool gra
     };
     p.head = reinterpret_cast<Head *>(take(sizeof(Head)));
     if (M > kCountAhead) p.ahead = reinterpret_cast<int *>(take(4 * (p.Mp / 128)));
-    p.ticket = reinterpret_cast<unsigned int *>(take(4 * (2 + 2 * (int64_t)p.pieces)));
+    p.vocab_tiles = grad ? (int)((V + kBM - 1) / kBM) : 0;
+    p.ticket = reinterpret_cast<unsigned int *>(take(4 * (2 + 2 * (int64_t)p.pieces + p.vocab_tiles)));
     p.joined = p.ticket + 1;
     p.done_l = p.ticket + 2;
     p.done_tx = p.done_l + p.pieces;
+    p.done_v = p.done_tx + p.pieces;
     p.rowmap = reinterpret_cast<int *>(take(4 * p.Mp));
     p.inverse = reinterpret_cast<int *>(take(4 * p.Mp));
     p.tgt = reinterpret_cast<int *>(take(4 * p.Mp));
@@ -150,7 +161,7 @@ int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, bool gra
     if (grad) {
         p.lse2 = reinterpret_cast<float *>(take(4 * p.Mp));
         p.rfac = reinterpret_cast<float *>(take(4 * p.Mp));
-        p.g = take(2 * p.Mp * p.piece_cols * p.buffers);
+        p.g = take(2 * p.Mp * kPiece * p.buffers);
         p.acc = reinterpret_cast<float *>(take(4 * (int64_t)p.slots * p.Mp * D));
     } else {
         p.pairs = reinterpret_cast<float2 *>(take(8 * (int64_t)p.vocab_groups * p.Mp));
@@ -249,6 +260,7 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
     int64_t tgt;
     if (p.ahead == nullptr) {
         const bool all = each && lead;                    // the largest |g| is taken over the whole list
+#pragma unroll 8
         for (int64_t m = t; m < (all ? p.M : first); m += kPrepThreads)
             if (counts(p, a, m, &tgt)) {
                 n += m < first ? 1 : 0;
@@ -330,7 +342,7 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
         p.tgt[i] = -1;
         if (p.grad) p.lse2[i] = p.rfac[i] = 0.0f;
     }
-    for (int i = t; i < 2 + 2 * p.pieces; i += kPrepThreads) p.ticket[i] = 0u;
+    for (int i = t; i < 2 + 2 * p.pieces + p.vocab_tiles; i += kPrepThreads) p.ticket[i] = 0u;
     if (t == 0) {
         p.head->kept = kept;
         if (a.count) *a.count = kept;
@@ -350,12 +362,14 @@ struct alignas(16) Unit {
     int type, piece;
     int m0, n0;              // output tile: first row, first column (rows of the output for T are table rows)
     int width;               // columns, a multiple of 128
-    int parts;               // accumulations, one after the other (X: granules)
-    int granule;             // X: first granule
     int left;                // 0: the list has ended
+    int unused[2];
 };
 
-// Phases in list order: L(0), then for each piece p: L(p+1), T and X of p.
+// Phases in list order: L of the first `lead` pieces, then for each piece p: L
+// of p + lead, and T and X of p, the longer of these first (T takes a k-block
+// per 64 positions, X one per 64 entries).  Where all L units come first, so
+// do all of the longer kind: the short units then even out the end.
 struct Walk {
     const Plan &p;
     int tm;                  // row tiles of positions
@@ -365,55 +379,58 @@ struct Walk {
 
     __device__ Walk(const Plan &plan, int n) : p(plan), tm(row_tiles(n)), kept(n) { count = size(0); }
 
-    __device__ int cols(int piece) const { return min(p.piece_cols, (int)(p.V - (int64_t)piece * p.piece_cols)); }
-    // phase 0: L(0); 2q+1: L(q+1) (empty for the last piece); 2q+2: T and X of q
+    __device__ int cols(int piece) const { return min(kPiece, (int)(p.V - (int64_t)piece * kPiece)); }
     __device__ uint32_t n_l(int piece) const {
         const int c = p.grad ? cols(piece) : (int)p.V;
         return (uint32_t)tm * (uint32_t)((c + p.lwidth - 1) / p.lwidth);
     }
     __device__ uint32_t n_t(int piece) const { return (uint32_t)((cols(piece) + kBM - 1) / kBM) * (uint32_t)p.dtiles; }
-    __device__ int granules_of(int piece) const { return (cols(piece) + kGranule - 1) / kGranule; }
-    __device__ uint32_t n_x(int piece) const { return (uint32_t)(tm * p.dtiles) * (uint32_t)(p.slots > 1 ? granules_of(piece) : 1); }
+    __device__ uint32_t n_x() const { return (uint32_t)(tm * p.dtiles); }
+    // A phase: its kind of units, or T and X of a piece, and the piece.
+    static constexpr int kBoth = 3;
+    __device__ int phases() const { return !p.grad ? 1 : p.lead == p.pieces ? 3 * p.pieces : p.lead + 2 * p.pieces; }
+    __device__ int kind_of(int ph, int *piece) const {
+        int q = ph - p.lead;
+        if (q < 0) { *piece = ph; return UNIT_L; }
+        if (p.lead == p.pieces) {
+            const bool second = q >= p.pieces;
+            *piece = second ? q - p.pieces : q;
+            return second == t_first() ? UNIT_X : UNIT_T;
+        }
+        *piece = q & 1 ? q / 2 : p.lead + q / 2;
+        return q & 1 ? kBoth : UNIT_L;
+    }
+    __device__ bool t_first() const { return kept >= kPiece; }
     __device__ uint32_t size(int ph) const {
-        if (ph == 0) return n_l(0);
-        if (ph & 1) return (ph + 1) / 2 < p.pieces ? n_l((ph + 1) / 2) : 0;
-        const int q = ph / 2 - 1;
-        return n_t(q) + n_x(q);
+        int q;
+        switch (kind_of(ph, &q)) {
+        case UNIT_L: return q < p.pieces ? n_l(q) : 0u;
+        case UNIT_T: return n_t(q);
+        case UNIT_X: return n_x();
+        default: return n_t(q) + n_x();
+        }
     }
     // The unit at position u of the list (u never decreases).
     __device__ Unit at(uint32_t u) {
-        const int last = p.grad ? 2 * p.pieces : 0;
         Unit o = {};
         while (u >= base + count) {
-            if (phase == last) return o;
+            if (phase == phases() - 1) return o;
             base += count;
             count = size(++phase);
         }
         uint32_t i = u - base;
-        o.parts = 1;
         o.left = 1;
-        if (phase == 0 || (phase & 1)) {
-            o.type = UNIT_L;
-            o.piece = phase == 0 ? 0 : (phase + 1) / 2;
+        o.type = kind_of(phase, &o.piece);
+        if (o.type == UNIT_L) {
             const int c = p.grad ? cols(o.piece) : (int)p.V;
             o.m0 = (int)(i % (uint32_t)tm) * kBM;
             o.n0 = (int)(i / (uint32_t)tm) * p.lwidth;
             o.width = min(p.lwidth, (c - o.n0 + 127) / 128 * 128);
         } else {
-            o.piece = phase / 2 - 1;
-            const uint32_t nt = n_t(o.piece);
-            if (i < nt) {
-                o.type = UNIT_T;
-            } else {
-                o.type = UNIT_X;
-                i -= nt;
-                const uint32_t tiles = (uint32_t)(tm * p.dtiles);
-                if (p.slots > 1) {
-                    o.granule = (int)(i / tiles);
-                    i -= (uint32_t)o.granule * tiles;
-                } else {
-                    o.parts = granules_of(o.piece);
-                }
+            if (o.type == kBoth) {
+                const uint32_t head = t_first() ? n_t(o.piece) : n_x();
+                o.type = (i < head) == t_first() ? UNIT_T : UNIT_X;
+                if (i >= head) i -= head;
             }
             o.m0 = (int)(i / (uint32_t)p.dtiles) * kBM;
             o.n0 = (int)(i % (uint32_t)p.dtiles) * p.dwidth;
@@ -421,12 +438,10 @@ struct Walk {
         }
         return o;
     }
-    // k-blocks of part j of a unit.
-    __device__ int k_blocks(const Unit &o, int part) const {
+    __device__ int k_blocks(const Unit &o) const {
         if (o.type == UNIT_L) return (int)((p.D + kBK - 1) / kBK);
         if (o.type == UNIT_T) return kept > kBK ? (kept + kBK - 1) / kBK : 1;
-        const int c = cols(o.piece) - (o.granule + part) * kGranule;
-        return (min(c, kGranule) + kBK - 1) / kBK;
+        return (cols(o.piece) + kBK - 1) / kBK;
     }
 };
 
@@ -442,7 +457,7 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap *map, uint32_t src,
                  ::"l"(map), "r"(src), "r"(c0), "r"(c1) : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read_0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
@@ -633,9 +648,9 @@ struct Feed {
         ld_shared_v4(smem_addr(c.slots + slot), v[0], v[1], v[2], v[3]);
         ld_shared_v4(smem_addr(c.slots + slot) + 16u, v[4], v[5], v[6], v[7]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);   // uses v: the slot has been read
-        *o = Unit{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
-        return v[7] != 0;
+        for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);   // uses v: the slot has been read
+        *o = Unit{v[0], v[1], v[2], v[3], v[4], v[5], {}};
+        return v[5] != 0;
     }
     // The slot may be used again.
     __device__ void release() {
@@ -661,7 +676,7 @@ __device__ __forceinline__ void hand_out(const Plan &p, Walk w, const Ctx &c) {
             const uint32_t to = map_rank(smem_addr(c.slots + slot), r), bar = map_rank(c.sfull(slot), r);
             mbar_expect_cluster(bar, 32u);
             st_async_v4(to, bar, o.type, o.piece, o.m0, o.n0);
-            st_async_v4(to + 16u, bar, o.width, o.parts, o.granule, o.left);
+            st_async_v4(to + 16u, bar, o.width, o.left, 0, 0);
         }
         more = o.left != 0;                       // the first one past the end tells the roles to stop
         if (++slot == kSlots) { slot = 0; ph ^= 1u; }
@@ -678,9 +693,13 @@ struct Ready {
             const int q = o.piece - p.buffers;
             if (q <= tx) return true;
             tx = q;
-            return c.wait_count(p.done_tx + q, kDone * (w.n_t(q) + w.n_x(q)));
+            return c.wait_count(p.done_tx + q, kDone * (w.n_t(q) + w.n_x()));
         }
         if (o.piece <= l) return true;
+        if (o.type == UNIT_T) {
+            const int cols = w.cols(o.piece) - o.m0, n = (min(cols, kBM) + p.lwidth - 1) / p.lwidth;
+            return c.wait_count(p.done_v + (o.piece * kPiece + o.m0) / kBM, kDone * (unsigned)(n * w.tm));
+        }
         l = o.piece;
         return c.wait_count(p.done_l + o.piece, kDone * w.n_l(o.piece));
     }
@@ -688,20 +707,25 @@ struct Ready {
 
 // Loads of one accumulation: this CTA's rows of A and columns of B, k-block by
 // k-block.  A whole warp runs the loop, one lane issues.  ca, cb: coordinates
-// of the first k-block (rows of the table or of x's blocks; planes of G); TWO: two boxes
+// of the first k-block (rows of the table or of x's blocks; planes of G); rows:
+// whether each CTA's rows of A hold positions (else they are not loaded: what
+// the MMA then reads gives rows that nothing reads); TWO: two boxes
 // of B, else one.
 template <int TYPE, bool TWO>
 __device__ __forceinline__ bool load_blocks(const Maps &maps, const Ctx &c, int nkb, int ca, int cb, int n0, int gstep,
-                                            int xstep, int &s, uint32_t &ph) {
-    constexpr uint32_t kBytes = 2 * (kABytes + (TWO ? 2 : 1) * kBlock);      // both CTAs'
+                                            int xstep, bool second, int &s, uint32_t &ph) {
+    const uint32_t bytes = (second ? 2u : 1u) * kABytes + 2u * (TWO ? 2u : 1u) * kBlock;      // both CTAs'
+    const bool load_a = c.rank == 0 || second;
     for (int kb = 0; kb < nkb; ++kb) {
         if (!__all_sync(0xffffffffu, c.wait(c.empty(s), ph ^ 1u))) return false;
         const uint32_t sa = c.sbase + s * kStageBytes, sb = sa + kABytes, bar = map_rank(c.full(s), 0);
         if (elect_one()) {
-            if (c.rank == 0) mbar_arrive_expect_tx(c.full(s), kBytes);
+            if (c.rank == 0) mbar_arrive_expect_tx(c.full(s), bytes);
             if (TYPE == UNIT_L) {                 // x and the table, both along D
-                tma_load_pair(sa, &maps.x, bar, 0, ca);
-                tma_load_pair(sa + kBlock, &maps.x, bar, 0, ca + 64);
+                if (load_a) {
+                    tma_load_pair(sa, &maps.x, bar, 0, ca);
+                    tma_load_pair(sa + kBlock, &maps.x, bar, 0, ca + 64);
+                }
                 tma_load_pair(sb, &maps.w, bar, kb * kBK, cb);
                 if (TWO) tma_load_pair(sb + kBlock, &maps.w, bar, kb * kBK, cb + 64);
             } else if (TYPE == UNIT_T) {          // G^T and x, along the positions
@@ -711,7 +735,7 @@ __device__ __forceinline__ bool load_blocks(const Maps &maps, const Ctx &c, int 
                 tma_load_pair(sb, &maps.x, bar, 0, cb);
                 if (TWO) tma_load_pair(sb + kBlock, &maps.x, bar, 0, cb + 128);
             } else {                              // G and the table, along the vocabulary
-                tma_load_pair_3d(sa, &maps.g_k, bar, 0, 0, ca);
+                if (load_a) tma_load_pair_3d(sa, &maps.g_k, bar, 0, 0, ca);
                 tma_load_pair(sb, &maps.w, bar, n0, cb);
                 if (TWO) tma_load_pair(sb + kBlock, &maps.w, bar, n0 + 64, cb);
             }
@@ -738,31 +762,30 @@ __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w,
     Unit o;
     Feed feed{c};
     Ready ready;
-    const int gstep = GRAD ? p.piece_cols * p.buffers / 64 * 8 : 0, xstep = p.xblocks * 128;   // planes of G, rows of x, per 128 positions
+    const int gstep = GRAD ? kPiece * p.buffers / 64 * 8 : 0, xstep = p.xblocks * 128;   // planes of G, rows of x, per 128 positions
     bool ok = true;
     while (ok && feed.take(&o)) {
         if (GRAD) {
             if (!__all_sync(0xffffffffu, ready.wait(p, w, o, c))) break;
             fence_proxy_async_all();              // other CTAs' G, before this CTA's TMA reads
         }
-        const int v0 = o.piece * p.piece_cols;
+        const int v0 = o.piece * kPiece;
         const int m0 = o.m0 + (int)c.rank * 128, n0 = o.n0 + (int)c.rank * (o.width / 2);
-        const int g0 = GRAD ? (o.piece % p.buffers) * (p.piece_cols / 64) * 8 : 0;
-        for (int part = 0; ok && part < o.parts; ++part) {
-            const int nkb = w.k_blocks(o, part), k0 = (o.granule + part) * kGranule;
-            if (!GRAD || o.type == UNIT_L) {
-                const int ca = m0 / 128 * xstep, cb = v0 + n0;
-                ok = o.width > 128 ? load_blocks<UNIT_L, true>(maps, c, nkb, ca, cb, 0, 0, 0, s, ph)
-                                   : load_blocks<UNIT_L, false>(maps, c, nkb, ca, cb, 0, 0, 0, s, ph);
-            } else if (o.type == UNIT_T) {
-                const int ca = g0 + m0 / 64 * 8, cb = n0 / 64 * 128;
-                ok = o.width > 128 ? load_blocks<UNIT_T, true>(maps, c, nkb, ca, cb, 0, gstep, xstep, s, ph)
-                                   : load_blocks<UNIT_T, false>(maps, c, nkb, ca, cb, 0, gstep, xstep, s, ph);
-            } else {
-                const int ca = m0 / 128 * gstep + g0 + k0 / 64 * 8, cb = v0 + k0;
-                ok = o.width > 128 ? load_blocks<UNIT_X, true>(maps, c, nkb, ca, cb, n0, 0, 0, s, ph)
-                                   : load_blocks<UNIT_X, false>(maps, c, nkb, ca, cb, n0, 0, 0, s, ph);
-            }
+        const int g0 = GRAD ? (o.piece % p.buffers) * (kPiece / 64) * 8 : 0;
+        const int nkb = w.k_blocks(o);
+        const bool second = o.m0 + 128 < w.kept;  // CTA 1's rows hold positions
+        if (!GRAD || o.type == UNIT_L) {
+            const int ca = m0 / 128 * xstep, cb = v0 + n0;
+            ok = o.width > 128 ? load_blocks<UNIT_L, true>(maps, c, nkb, ca, cb, 0, 0, 0, second, s, ph)
+                               : load_blocks<UNIT_L, false>(maps, c, nkb, ca, cb, 0, 0, 0, second, s, ph);
+        } else if (o.type == UNIT_T) {
+            const int ca = g0 + m0 / 64 * 8, cb = n0 / 64 * 128;
+            ok = o.width > 128 ? load_blocks<UNIT_T, true>(maps, c, nkb, ca, cb, 0, gstep, xstep, true, s, ph)
+                               : load_blocks<UNIT_T, false>(maps, c, nkb, ca, cb, 0, gstep, xstep, true, s, ph);
+        } else {
+            const int ca = m0 / 128 * gstep + g0;
+            ok = o.width > 128 ? load_blocks<UNIT_X, true>(maps, c, nkb, ca, v0, n0, 0, 0, second, s, ph)
+                               : load_blocks<UNIT_X, false>(maps, c, nkb, ca, v0, n0, 0, 0, second, s, ph);
         }
     }
     // CTA 0 sees every load of both land before the pair may exit (stages not
@@ -807,23 +830,21 @@ __device__ __forceinline__ void issue(Walk w, const Ctx &c) {
     bool more = feed.take(&next);
     while (more) {
         o = next;
-        for (int part = 0; part < o.parts; ++part) {
-            if (!__all_sync(0xffffffffu, c.wait(c.tempty(acc), aph ^ 1u))) return;
-            tc_fence_after();
-            const uint32_t d = c.tmem + (uint32_t)(acc * kBN);
-            const int nkb = w.k_blocks(o, part), first = nkb > 4 ? nkb - 4 : 0;
-            auto blocks = [&](int from, int to) {
-                if (!GRAD || o.type == UNIT_L) return issue_blocks<UNIT_L>(c, d, o.width, F16, from, to, s, ph);
-                if (o.type == UNIT_T) return issue_blocks<UNIT_T>(c, d, o.width, F16, from, to, s, ph);
-                return issue_blocks<UNIT_X>(c, d, o.width, F16, from, to, s, ph);
-            };
-            if (!blocks(0, first)) return;
-            if (part == o.parts - 1) more = feed.take(&next);
-            if (!blocks(first, nkb)) return;
-            if (elect_one()) mma_commit_pair(c.tfull(acc));
-            __syncwarp();
-            if (++acc == 2) { acc = 0; aph ^= 1u; }
-        }
+        if (!__all_sync(0xffffffffu, c.wait(c.tempty(acc), aph ^ 1u))) return;
+        tc_fence_after();
+        const uint32_t d = c.tmem + (uint32_t)(acc * kBN);
+        const int nkb = w.k_blocks(o), first = nkb > 4 ? nkb - 4 : 0;
+        auto blocks = [&](int from, int to) {
+            if (!GRAD || o.type == UNIT_L) return issue_blocks<UNIT_L>(c, d, o.width, F16, from, to, s, ph);
+            if (o.type == UNIT_T) return issue_blocks<UNIT_T>(c, d, o.width, F16, from, to, s, ph);
+            return issue_blocks<UNIT_X>(c, d, o.width, F16, from, to, s, ph);
+        };
+        if (!blocks(0, first)) return;
+        more = feed.take(&next);
+        if (!blocks(first, nkb)) return;
+        if (elect_one()) mma_commit_pair(c.tfull(acc));
+        __syncwarp();
+        if (++acc == 2) { acc = 0; aph ^= 1u; }
     }
 }
 
@@ -853,15 +874,16 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
 }
 
 // Sub-tiles of 32 rows x 128 bytes (64 16-bit columns or 32 of fp32) to
-// global memory through the warp's 4 KiB staging buffer.  A lane holds a row;
-// its 16-byte pieces lie as the 128-byte swizzle expects them.  The elected
-// lane, the same one each time, issues every copy and waits for them.
-__device__ __forceinline__ void staging_free() {
-    if (elect_one()) bulk_wait_read_0();
+// global memory through the warp's two staging buffers, by turns.  A lane
+// holds a row; its 16-byte pieces lie as the 128-byte swizzle expects them.
+// The elected lane, the same one each time, issues every copy and waits for
+// them.
+__device__ __forceinline__ void put_rows(uint32_t staging, uint32_t &turn, int lane, const CUtensorMap *map,
+                                         const uint32_t *r, int col, int row, bool add) {
+    const uint32_t stg = staging + turn;
+    turn ^= 4096u;
+    if (elect_one()) bulk_wait_read_1();                  // the sub-tile before the last has left
     __syncwarp();
-}
-__device__ __forceinline__ void put_rows(uint32_t stg, int lane, const CUtensorMap *map, const uint32_t *r, int col,
-                                         int row, bool add) {
 #pragma unroll
     for (int g = 0; g < 8; ++g)
         st_shared_v4(stg + lane * 128 + 16 * (g ^ (lane & 7)),
@@ -925,7 +947,8 @@ __device__ __forceinline__ void loss_rows(const Plan &p, const Unit &o, uint32_t
 template <bool GRAD, bool F16>
 __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const Walk w, const Ctx &c, int warp, int lane) {
     const int quarter = warp % 4, half = (warp - 4) / 4;  // 32 rows; one half of the columns
-    const uint32_t stg = c.sbase + kStagingOffset + (uint32_t)(warp - 4) * 4096u;
+    const uint32_t stg = c.sbase + kStagingOffset + (uint32_t)(warp - 4) * kStagingBytes;
+    uint32_t turn = 0u;
     const float gscale = GRAD ? p.head->gscale : 0.0f;
     constexpr float kOne = (float)(1ull << (F16 ? kScaleBits16 : kScaleBitsBf));
     int acc = 0;
@@ -942,100 +965,90 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
         if (GRAD && o.type == UNIT_L) {
             lse2 = p.lse2[row];
             rfac = p.rfac[row];
-            tgt = p.tgt[row] - o.piece * p.piece_cols - o.n0;     // column of this tile
+            tgt = p.tgt[row] - o.piece * kPiece - o.n0;     // column of this tile
         }
-        for (int part = 0; part < o.parts; ++part) {
-            if (!__all_sync(0xffffffffu, c.wait(c.tfull(acc), aph))) return;
-            tc_fence_after();
-            const uint32_t tmem = c.tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kBN);
-            if (!GRAD) {
-                loss_rows(p, o, tmem, row, half);
-            } else if (o.type == UNIT_L) {
-                const int n = (int)(p.V - (int64_t)o.piece * p.piece_cols) - o.n0;   // valid columns of this tile
-                // this row's place in plane 0 of the first block
-                uint16_t *g_row = static_cast<uint16_t *>(p.g) +
-                    ((int64_t)(row0 / 128) * (p.piece_cols * p.buffers / 64) + ((o.piece % p.buffers) * p.piece_cols + o.n0) / 64) * kPlanes +
-                    (row % 128) * 8;
-                const bool dead = rfac == 0.0f;          // no position, or none of its gradient
-                const bool plain = __all_sync(0xffffffffu, rfac == 1.0f);
+        if (!__all_sync(0xffffffffu, c.wait(c.tfull(acc), aph))) return;
+        tc_fence_after();
+        const uint32_t tmem = c.tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kBN);
+        if (!GRAD) {
+            loss_rows(p, o, tmem, row, half);
+        } else if (o.type == UNIT_L) {
+            const int n = (int)(p.V - (int64_t)o.piece * kPiece) - o.n0;   // valid columns of this tile
+            // this row's place in plane 0 of the first block
+            uint16_t *g_row = static_cast<uint16_t *>(p.g) +
+                ((int64_t)(row0 / 128) * (kPiece * p.buffers / 64) + ((o.piece % p.buffers) * kPiece + o.n0) / 64) * kPlanes +
+                (row % 128) * 8;
+            const bool dead = rfac == 0.0f;          // no position, or none of its gradient
+            const bool plain = __all_sync(0xffffffffu, rfac == 1.0f);
 #pragma unroll 1
-                for (int cc = c0; cc < c1; cc += 64) {
-                    uint32_t r[64], g[32];
-                    tmem_ld64(tmem + (uint32_t)cc, r);
+            for (int cc = c0; cc < c1; cc += 64) {
+                uint32_t r[64], g[32];
+                tmem_ld64(tmem + (uint32_t)cc, r);
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)          // 2^k P
-                        r[i] = __float_as_uint(ex2(fmaf(__uint_as_float(r[i]), kLog2e, -lse2)));
-                    if (__any_sync(0xffffffffu, (unsigned)(tgt - cc) < 64u)) {
+                for (int i = 0; i < 64; ++i)          // 2^k P
+                    r[i] = __float_as_uint(ex2(fmaf(__uint_as_float(r[i]), kLog2e, -lse2)));
+                if (__any_sync(0xffffffffu, (unsigned)(tgt - cc) < 64u)) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (cc + i == tgt) r[i] = __float_as_uint(__uint_as_float(r[i]) - kOne);
-                    }
-                    if (cc + 64 > n) {                    // past the vocabulary: exactly zero
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (cc + i >= n) r[i] = 0u;
-                    }
-                    if (!plain) {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)      // a dead row is zero whatever z is
-                            r[i] = dead ? 0u : __float_as_uint(__uint_as_float(r[i]) * rfac);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        g[i] = pack2<F16>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                    uint16_t *dst = g_row + (int64_t)(cc / 64) * kPlanes;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (CHK(dst + q * kPlane - static_cast<uint16_t *>(p.g), 8, p.Mp * p.piece_cols * p.buffers))
-                            *reinterpret_cast<uint4 *>(dst + q * kPlane) =
-                                make_uint4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]);
+                    for (int i = 0; i < 64; ++i)
+                        if (cc + i == tgt) r[i] = __float_as_uint(__uint_as_float(r[i]) - kOne);
                 }
-            } else if (o.type == UNIT_T) {
-#pragma unroll 1
-                for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 64) {
-                    uint32_t r[64], g[32];
-                    tmem_ld64(tmem + (uint32_t)cc, r);
+                if (cc + 64 > n) {                    // past the vocabulary: exactly zero
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        g[i] = pack2<F16>(__uint_as_float(r[2 * i]) * gscale, __uint_as_float(r[2 * i + 1]) * gscale);
-                    staging_free();
-                    put_rows(stg, lane, &maps.dt_out, g, o.n0 + cc, o.piece * p.piece_cols + row0, false);
+                    for (int i = 0; i < 64; ++i)
+                        if (cc + i >= n) r[i] = 0u;
                 }
-            } else {
-                // granule sums of dx: a slot each, or added in place in granule order
-                const int granule = o.piece * (p.piece_cols / kGranule) + o.granule + part;
-                const bool add = p.slots == 1 && granule > 0;
-                if (add) {                               // the granule before is in memory
-                    if (part > 0) {
-                        if (elect_one()) bulk_wait_all();
-                        __syncwarp();
-                    } else {
-                        const int q = o.piece - 1;
-                        const bool there = c.wait_count(p.done_tx + q, kDone * (unsigned)(w.n_t(q) + w.n_x(q)));
-                        if (!__all_sync(0xffffffffu, there)) return;
-                        fence_proxy_async_all();
-                    }
+                if (!plain) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)      // a dead row is zero whatever z is
+                        r[i] = dead ? 0u : __float_as_uint(__uint_as_float(r[i]) * rfac);
                 }
-                const int arow = (p.slots > 1 ? granule * (int)p.Mp : 0) + row0;
-#pragma unroll 1
-                for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 64) {
-                    uint32_t r[64];
-                    tmem_ld64(tmem + (uint32_t)cc, r);
-                    staging_free();
-                    put_rows(stg, lane, &maps.acc, r, o.n0 + cc, arow, add);
-                    if (o.n0 + cc + 32 < p.D) {
-                        staging_free();
-                        put_rows(stg, lane, &maps.acc, r + 32, o.n0 + cc + 32, arow, add);
-                    }
-                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    g[i] = pack2<F16>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                uint16_t *dst = g_row + (int64_t)(cc / 64) * kPlanes;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (CHK(dst + q * kPlane - static_cast<uint16_t *>(p.g), 8, p.Mp * kPiece * p.buffers))
+                        *reinterpret_cast<uint4 *>(dst + q * kPlane) =
+                            make_uint4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_rank(c.tempty(acc), 0));
-            if (++acc == 2) { acc = 0; aph ^= 1u; }
+        } else if (o.type == UNIT_T) {
+#pragma unroll 1
+            for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 64) {
+                uint32_t r[64], g[32];
+                tmem_ld64(tmem + (uint32_t)cc, r);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    g[i] = pack2<F16>(__uint_as_float(r[2 * i]) * gscale, __uint_as_float(r[2 * i + 1]) * gscale);
+                put_rows(stg, turn, lane, &maps.dt_out, g, o.n0 + cc, o.piece * kPiece + row0, false);
+            }
+        } else {
+            // the pieces' sums of dx: a slot each, or added in place in order
+            const bool add = p.slots == 1 && o.piece > 0;
+            if (add) {                               // the piece before is in memory
+                const int q = o.piece - 1;
+                const bool there = c.wait_count(p.done_tx + q, kDone * (unsigned)(w.n_t(q) + w.n_x()));
+                if (!__all_sync(0xffffffffu, there)) return;
+                fence_proxy_async_all();
+            }
+            const int arow = (p.slots > 1 ? o.piece * (int)p.Mp : 0) + row0;
+#pragma unroll 1
+            for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 64) {
+                uint32_t r[64];
+                tmem_ld64(tmem + (uint32_t)cc, r);
+                put_rows(stg, turn, lane, &maps.acc, r, o.n0 + cc, arow, add);
+                if (o.n0 + cc + 32 < p.D) put_rows(stg, turn, lane, &maps.acc, r + 32, o.n0 + cc + 32, arow, add);
+            }
         }
-        if (GRAD) {                                       // this warp's part has been stored
-            if (o.type != UNIT_L && elect_one()) bulk_wait_all();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_rank(c.tempty(acc), 0));
+        if (++acc == 2) { acc = 0; aph ^= 1u; }
+        if (GRAD) {
+            // what other units wait for: G, in memory once the reporter has
+            // fenced; sums of dx that the next piece adds to; of a T unit only
+            // that it has read G
+            if (o.type == UNIT_X && p.slots == 1 && elect_one()) bulk_wait_all();
             __syncwarp();
             if (lane == 0) mbar_arrive(c.stored(slot));
         }
@@ -1053,6 +1066,7 @@ __device__ __forceinline__ void report(const Plan &p, const Ctx &c) {
         if (elect_one()) {
             fence_proxy_async_all();                      // G is read by TMA
             add_release((o.type == UNIT_L ? p.done_l : p.done_tx) + o.piece, 1u);
+            if (o.type == UNIT_L) add_release(p.done_v + (o.piece * kPiece + o.n0) / kBM, 1u);
         }
         feed.release();
     }
@@ -1134,7 +1148,7 @@ __global__ void __launch_bounds__(1024)
 xent_join_kernel(const Plan p, float *__restrict__ losses, float *__restrict__ lse, float *__restrict__ total, int mean) {
     __shared__ union {
         float2 pair[32][33];
-        double sum[1024];
+        double sum[32];
     } sh;
     __shared__ bool finish;
     wait_prior_grid();
@@ -1172,44 +1186,57 @@ xent_join_kernel(const Plan p, float *__restrict__ losses, float *__restrict__ l
     double s = 0.0;
 #pragma unroll 8
     for (int64_t m = threadIdx.x; m < p.M; m += 1024) s += (double)__ldcg(losses + m);
-    sh.sum[threadIdx.x] = s;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (r == 0) sh.sum[t] = s;
     __syncthreads();
-    for (int o = 512; o > 0; o >>= 1) {
-        if (threadIdx.x < o) sh.sum[threadIdx.x] += sh.sum[threadIdx.x + o];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) total[0] = (float)(mean ? sh.sum[0] / (double)(kept > 0 ? kept : 1) : sh.sum[0]);
+    if (t != 0) return;
+    s = sh.sum[r];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (r == 0) total[0] = (float)(mean ? s / (double)(kept > 0 ? kept : 1) : s);
 }
 
-// dx rows: the granule sums in order, scaled and rounded; zeros for ignored
-// positions.  A warp per row.
-template <typename T>
+// dx: the pieces' sums in order, scaled and rounded; zeros for ignored
+// positions.  A warp per position and 256 columns; up to 8 sums are loaded
+// before the first is added (MANY: else there is one, and registers for more
+// would leave few warps to wait for it).
+template <typename T, bool MANY>
 __global__ void __launch_bounds__(256)
 xent_dx_kernel(const Plan p, T *__restrict__ dx) {
     wait_prior_grid();
     allow_next_grid();
-    const int lane = threadIdx.x % 32;
-    const int64_t m = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    if (m >= p.M) return;
+    const int64_t m = (int64_t)blockIdx.x * 8 + threadIdx.x / 32, j = ((int64_t)blockIdx.y * 32 + threadIdx.x % 32) * 8;
+    if (m >= p.M || j >= p.D) return;
     const int64_t i = p.inverse[m];
-    const float gscale = p.head->gscale;
-    for (int64_t j = lane * 8; j < p.D; j += 256) {
-        float f[8];
+    float f[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = 0.0f;
-        if (i >= 0) {
-            for (int s = 0; s < p.slots; ++s) {
-                const float4 *src = reinterpret_cast<const float4 *>(p.acc + ((int64_t)s * p.Mp + i) * p.D + j);
-                const float4 a = src[0], b = src[1];
-                const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    for (int k = 0; k < 8; ++k) f[k] = 0.0f;
+    if (i >= 0) {
+        const float gscale = p.head->gscale;
+        const float *src = p.acc + i * p.D + j;
+        constexpr int U = MANY ? 8 : 1;
+        for (int s0 = 0; s0 < p.slots; s0 += U) {
+            float4 lo[U], hi[U];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] = s == 0 ? v[k] : f[k] + v[k];
-            }
+            for (int s = 0; s < U; ++s)
+                if (s0 + s < p.slots) {
+                    const float4 *q = reinterpret_cast<const float4 *>(src + (int64_t)(s0 + s) * p.Mp * p.D);
+                    lo[s] = q[0];
+                    hi[s] = q[1];
+                }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] *= gscale;
+            for (int s = 0; s < U; ++s)
+                if (s0 + s < p.slots) {
+                    const float w[8] = {lo[s].x, lo[s].y, lo[s].z, lo[s].w, hi[s].x, hi[s].y, hi[s].z, hi[s].w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f[k] = s0 + s == 0 ? w[k] : f[k] + w[k];
+                }
         }
-        if (CHK(m * p.D + j, 8, p.M * p.D)) store_f32<T, 8>(dx + m * p.D + j, f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] *= gscale;
     }
+    if (CHK(m * p.D + j, 8, p.M * p.D)) store_f32<T, 8>(dx + m * p.D + j, f);
 }
 
 // ---- host side ----------------------------------------------------------------
@@ -1253,10 +1280,10 @@ carbon_status_t check(const void *x, const void *table, const int64_t *targets, 
 // Units, planes of G and rows of x's blocks are counted in 32 bits.
 bool list_fits(const Plan &p) {
     // planes are numbered by TMA coordinates
-    if (p.Mp * p.xblocks >= (1ll << 31) || (p.grad && p.Mp * p.piece_cols * p.buffers / kPlane >= (1ll << 31)))
+    if (p.Mp * p.xblocks >= (1ll << 31) || (p.grad && p.Mp * kPiece * p.buffers / kPlane >= (1ll << 31)))
         return false;
     const int64_t tm = p.Mp / kBM, l = (p.V + 127) / 128, t = (p.V + kBM - 1) / kBM + p.pieces;
-    return tm * (l + p.pieces) + (t + tm * p.granules) * p.dtiles < (1ll << 31);
+    return tm * (l + p.pieces) + (t + tm * p.pieces) * p.dtiles < (1ll << 31);
 }
 
 template <bool GRAD>
@@ -1267,7 +1294,7 @@ cudaError_t launch_tiles(const Plan &p, const void *table, void *dtable, int sms
         err = encode_tensor_map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.xc, 64, (uint64_t)(p.Mp * p.xblocks), 128,
                                    64, 64, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (GRAD) {
-        const int64_t n = p.Mp * p.piece_cols * p.buffers;
+        const int64_t n = p.Mp * kPiece * p.buffers;
         if (err == cudaSuccess) err = encode_blocks(&maps.g_k, p.g, n, 16);
         if (err == cudaSuccess) err = encode_blocks(&maps.g_mn, p.g, n, 8);
         if (err == cudaSuccess)
@@ -1384,10 +1411,14 @@ carbon_status_t carbon_linear_xent_bwd(void *dx, void *dtable, const float *grad
     if (err == cudaSuccess) err = launch_tiles<true>(p, table, dtable, sms, s);
     if (err == cudaSuccess) {
         count_launch();
-        const dim3 grid((unsigned)((M + 7) / 8));
-        err = p.f16 ? launch_k(xent_dx_kernel<__half>, grid, dim3(256), 0, s, 1, p, static_cast<__half *>(dx))
-                    : launch_k(xent_dx_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1, p,
-                               static_cast<__nv_bfloat16 *>(dx));
+        const dim3 grid((unsigned)((M + 7) / 8), (unsigned)((D + 255) / 256));
+        auto join = [&](auto kern, auto *to) { return launch_k(kern, grid, dim3(256), 0, s, 1, p, to); };
+        if (p.f16)
+            err = p.slots > 1 ? join(xent_dx_kernel<__half, true>, static_cast<__half *>(dx))
+                              : join(xent_dx_kernel<__half, false>, static_cast<__half *>(dx));
+        else
+            err = p.slots > 1 ? join(xent_dx_kernel<__nv_bfloat16, true>, static_cast<__nv_bfloat16 *>(dx))
+                              : join(xent_dx_kernel<__nv_bfloat16, false>, static_cast<__nv_bfloat16 *>(dx));
     }
     return note_cuda(err);
 }
