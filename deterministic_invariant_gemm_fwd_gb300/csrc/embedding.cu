@@ -382,7 +382,7 @@ __device__ __forceinline__ void write_row(T *dst, float (&acc)[N], float scale, 
 // A CTA per chunk; a thread per column vector.  All rows of the chunk are
 // loaded before the first addition.
 template <typename T, int N>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
 chunk_kernel(T *__restrict__ dtable, const T *__restrict__ dy, const uint32_t *__restrict__ key,
              const uint32_t *__restrict__ pos, uint32_t *__restrict__ jobs, float *__restrict__ part, int64_t M,
              int64_t V, int64_t D, float scale, int accumulate) {

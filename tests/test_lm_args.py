@@ -130,3 +130,22 @@ def test_python_refusals():
         cg.linear_cross_entropy_fwd(x, w, ids)
     with pytest.raises(ValueError):
         cg.rms_norm_expand(torch.zeros(4, 8, dtype=torch.int8), torch.zeros(4))
+
+
+def test_header_from_c(tmp_path):
+    """include/carbon_lm.h is plain C: a C99 program links against the library
+    and runs on paths that answer without a GPU."""
+    import os
+    import shutil
+    import subprocess
+    if shutil.which("gcc") is None:
+        pytest.skip("needs gcc")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe, libdir = tmp_path / "lm_abi_from_c", os.path.dirname(b.LIB_PATH)
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(root, "include"),
+                    os.path.join(root, "tests", "c", "lm_abi_from_c.c"), "-o", str(exe), f"-L{libdir}",
+                    "-l:libcarbon_gemm.so", f"-Wl,-rpath,{libdir}"], check=True, capture_output=True, text=True)
+    env = dict(os.environ)
+    env.pop("CARBON_FAULT", None)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, env=env, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr

@@ -269,6 +269,32 @@ def test_rms_norm_zero_rows_and_values_that_are_not_finite():
     assert bool(torch.isnan(cg.rms_norm_fwd(x[:1].contiguous(), gamma, None, 0.0).y).all())
 
 
+def test_rms_norm_without_rows():
+    x, gamma = torch.empty(0, 24, device="cuda"), torch.ones(24, device="cuda")
+    r = cg.rms_norm_fwd(x, gamma, x, quantize=True)
+    assert r.y.shape == (0, 24) and r.codes.shape == (0, 24)
+    dx, dgamma = cg.rms_norm_bwd(x, gamma, r.rstd, h=r.h)
+    assert dx.shape == (0, 24) and not bool(dgamma.any())
+    assert cg.rms_norm_expand(r.codes, r.scales, gamma).shape == (0, 24)
+    assert status() == 0
+
+
+def test_rms_norm_gradient_over_its_own_operand():
+    """dx may be dh's memory (the C call); also with odd rows, whose bulk
+    copies reach into their neighbours."""
+    M, D = 700, 515
+    g = gen(31)
+    h, dy, dh = (randn(g, M, D, dtype=torch.bfloat16) for _ in range(3))
+    gamma = randn(g, D, dtype=torch.bfloat16)
+    r = cg.rms_norm_fwd(h, gamma)
+    ref, dgamma = cg.rms_norm_bwd(dy, gamma, r.rstd, h=h, dh=dh)
+    n = cg.carbon_rms_norm_bwd_workspace(M, D)
+    ws, dg = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(gamma)
+    both = dh.clone()
+    cg.carbon_rms_norm_bwd(both, dg, None, dy, h, None, None, r.rstd, gamma, both, M, D, ws, n, "bf16")
+    assert same_bits(both, ref) and same_bits(dg, dgamma)
+
+
 def test_rms_norm_gradient_against_differences():
     """sum(y * w) and the residual stream's sum(h * v), in float64 central
     differences along random directions."""
