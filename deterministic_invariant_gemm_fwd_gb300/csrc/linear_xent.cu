@@ -37,21 +37,28 @@ __device__ unsigned int g_xent_status = 0;
 #define CHK(idx, len, n) in_bounds(&g_xent_status, (int64_t)(idx), (int64_t)(len), (int64_t)(n))
 
 constexpr int kBM = 256, kBN = 256, kBK = 64;        // a CTA pair's tile; each CTA has 128 rows
-constexpr int kStages = 5;                             // (six ran no faster)
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (4 + kEpiWarps);        // TMA producer, MMA issuer, scheduler, reporter, epilogue
 constexpr uint32_t kBlock = 64 * kBK * 2;             // one 64 x 64 box: 8 KiB
 constexpr uint32_t kABytes = 128 * kBK * 2;           // per CTA: 128 rows of A, half of B's columns
 constexpr uint32_t kStageBytes = kABytes + kBN / 2 * kBK * 2;
-constexpr int kSlots = 6;                             // units handed out ahead
-constexpr uint32_t kStagingOffset = kStages * kStageBytes;
-constexpr uint32_t kStagingBytes = 2 * 4096;          // per epilogue warp: two sub-tiles
-constexpr uint32_t kBarOffset = kStagingOffset + kEpiWarps * kStagingBytes;
-constexpr int kBars = 2 * kStages + 4 + 3 * kSlots + 2;   // an even number: units follow
-constexpr uint32_t kUnitOffset = kBarOffset + kBars * 8;
-constexpr uint32_t kSmemBytes = kUnitOffset + kSlots * 32 + 16 + 1024;
-static_assert(kUnitOffset % 16 == 0, "units are read as 16-byte vectors");
-static_assert(kSmemBytes <= 232448, "shared memory per block");
+constexpr int kSlots = 6;                             // units known to a CTA at a time
+
+// Shared memory.  As many stages as fit: the tensor cores wait for operands
+// more than for anything else (8192 x 768 x 50257, the loss and its gradients
+// with five stages and two staging buffers per warp: 1488 us, with six and
+// one: 1451).  The loss stores no tiles and needs no staging.
+template <bool GRAD>
+struct Layout {
+    static constexpr int kStages = GRAD ? 6 : 7;
+    static constexpr uint32_t kStagingOffset = kStages * kStageBytes;
+    static constexpr uint32_t kBarOffset = kStagingOffset + (GRAD ? kEpiWarps * 4096 : 0);
+    static constexpr int kBars = (2 * kStages + 4 + 3 * kSlots + 1 + 1) / 2 * 2;   // an even number: units follow
+    static constexpr uint32_t kUnitOffset = kBarOffset + kBars * 8;
+    static constexpr uint32_t kBytes = kUnitOffset + kSlots * 32 + 16 + 1024;
+    static_assert(kBytes <= 232448, "shared memory per block");
+    static_assert(kUnitOffset % 16 == 0, "units are read as 16-byte vectors");
+};
 constexpr unsigned kDone = 2;                         // reports of a finished unit: one per CTA
 
 constexpr int kGroup = 128;              // vocabulary entries per (max, sum) pair
@@ -457,7 +464,7 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap *map, uint32_t src,
                  ::"l"(map), "r"(src), "r"(c0), "r"(c1) : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read_0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
@@ -588,15 +595,17 @@ __device__ __forceinline__ uint64_t plane_desc(uint32_t base, bool mn, int k) {
 // ---- the tile kernel -------------------------------------------------------------------
 
 struct Maps {
-    CUtensorMap w;              // boxes of 64 x 64, 128-byte swizzle
-    CUtensorMap x;              // half a block: the rows of 64 positions
+    CUtensorMap w, w_k;         // boxes of 64 x 64 and (reduced along D) 128 rows x 64, 128-byte swizzle
+    CUtensorMap x, x_k;         // half a block, the rows of 64 positions, and (reduced along D) a block
     CUtensorMap g_k;            // a block, reduced along its columns
     CUtensorMap g_mn;           // the halves of a block's planes that hold 64 positions, reduced along those
     CUtensorMap dt_out;         // store boxes of 32 rows x 64
     CUtensorMap acc;            // store boxes of 32 rows x 32 fp32
 };
 
-struct Ctx {
+template <bool GRAD>
+struct Ctx : Layout<GRAD> {
+    using Layout<GRAD>::kStages;
     uint32_t sbase, bars, tmem, rank;
     const Unit *slots;                   // units handed out
     volatile uint32_t *abort_flag;
@@ -634,8 +643,9 @@ struct Ctx {
 // next (a pair only waits for units that a running pair already has: the
 // kernel makes progress however few of its pairs the GPU runs at once).  One
 // thread of CTA 0 takes them and decodes them for every role of both CTAs.
+template <class C>
 struct Feed {
-    const Ctx &c;
+    const C &c;
     int slot = 0;
     uint32_t ph = 0;
     // The next unit, for a whole warp.  false: none left, or gave up.  The
@@ -667,7 +677,8 @@ struct Feed {
 // readers of a unit: producers of both CTAs, the MMA issuer, both reporters and epilogues
 constexpr int kReaders = 2 + 1 + 2 + 2 * kEpiWarps;
 
-__device__ __forceinline__ void hand_out(const Plan &p, Walk w, const Ctx &c) {
+template <class C>
+__device__ __forceinline__ void hand_out(const Plan &p, Walk w, const C &c) {
     int slot = 0;
     uint32_t ph = 0;
     uint32_t taken = 0;
@@ -697,7 +708,8 @@ __device__ __forceinline__ void hand_out(const Plan &p, Walk w, const Ctx &c) {
 // acquiring load costs about 1000 cycles).
 struct Ready {
     int l = -1, tx = -1;                          // last pieces known complete
-    __device__ bool wait(const Plan &p, const Walk &w, const Unit &o, const Ctx &c) {
+    template <class C>
+    __device__ bool wait(const Plan &p, const Walk &w, const Unit &o, const C &c) {
         if (!p.grad) return true;
         if (o.type == UNIT_L) {                   // its piece's buffer is free
             const int q = o.piece - p.buffers;
@@ -721,8 +733,8 @@ struct Ready {
 // whether each CTA's rows of A hold positions (else they are not loaded: what
 // the MMA then reads gives rows that nothing reads); TWO: two boxes
 // of B, else one.
-template <int TYPE, bool TWO>
-__device__ __forceinline__ bool load_blocks(const Maps &maps, const Ctx &c, int nkb, int ca, int cb, int n0, int gstep,
+template <int TYPE, bool TWO, class C>
+__device__ __forceinline__ bool load_blocks(const Maps &maps, const C &c, int nkb, int ca, int cb, int n0, int gstep,
                                             int xstep, bool second, int &s, uint32_t &ph) {
     const uint32_t bytes = (second ? 2u : 1u) * kABytes + 2u * (TWO ? 2u : 1u) * kBlock;      // both CTAs'
     const bool load_a = c.rank == 0 || second;
@@ -732,12 +744,8 @@ __device__ __forceinline__ bool load_blocks(const Maps &maps, const Ctx &c, int 
         if (elect_one()) {
             if (c.rank == 0) mbar_arrive_expect_tx(c.full(s), bytes);
             if (TYPE == UNIT_L) {                 // x and the table, both along D
-                if (load_a) {
-                    tma_load_pair(sa, &maps.x, bar, 0, ca);
-                    tma_load_pair(sa + kBlock, &maps.x, bar, 0, ca + 64);
-                }
-                tma_load_pair(sb, &maps.w, bar, kb * kBK, cb);
-                if (TWO) tma_load_pair(sb + kBlock, &maps.w, bar, kb * kBK, cb + 64);
+                if (load_a) tma_load_pair(sa, &maps.x_k, bar, 0, ca);
+                tma_load_pair(sb, TWO ? &maps.w_k : &maps.w, bar, kb * kBK, cb);
             } else if (TYPE == UNIT_T) {          // G^T and x, along the positions
                 const int h = (kb & 1) * 8;
                 tma_load_pair_3d(sa, &maps.g_mn, bar, 0, h, ca);
@@ -760,17 +768,17 @@ __device__ __forceinline__ bool load_blocks(const Maps &maps, const Ctx &c, int 
             ca += 8;
             cb += kBK;
         }
-        if (++s == kStages) { s = 0; ph ^= 1u; }
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
     }
     return true;
 }
 
-template <bool GRAD>
-__device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w, const Ctx &c) {
+template <bool GRAD, class C>
+__device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w, const C &c) {
     int s = 0;
     uint32_t ph = 0;
     Unit o;
-    Feed feed{c};
+    Feed<C> feed{c};
     Ready ready;
     const int gstep = GRAD ? kPiece * p.buffers / 64 * 8 : 0, xstep = p.xblocks * 128;   // planes of G, rows of x, per 128 positions
     bool ok = true;
@@ -801,15 +809,15 @@ __device__ __forceinline__ void produce(const Plan &p, const Maps &maps, Walk w,
     }
     // CTA 0 sees every load of both land before the pair may exit (stages not
     // armed in this pass completed earlier, so their wait returns at once)
-    for (int i = 0; c.rank == 0 && i < kStages; ++i) {
-        if (--s < 0) { s = kStages - 1; ph ^= 1u; }
+    for (int i = 0; c.rank == 0 && i < C::kStages; ++i) {
+        if (--s < 0) { s = C::kStages - 1; ph ^= 1u; }
         if (!__all_sync(0xffffffffu, mbar_wait(c.full(s), ph))) break;
     }
 }
 
 // k-blocks of one accumulation.
-template <int TYPE>
-__device__ __forceinline__ bool issue_blocks(const Ctx &c, uint32_t d, int width, bool f16, int from, int to, int &s,
+template <int TYPE, class C>
+__device__ __forceinline__ bool issue_blocks(const C &c, uint32_t d, int width, bool f16, int from, int to, int &s,
                                              uint32_t &ph) {
     constexpr bool A_MN = TYPE == UNIT_T, B_MN = TYPE != UNIT_L;
     const uint32_t idesc = instr_desc(width, A_MN, B_MN, f16);
@@ -825,19 +833,19 @@ __device__ __forceinline__ bool issue_blocks(const Ctx &c, uint32_t d, int width
             mma_commit_pair(c.empty(s));
         }
         __syncwarp();
-        if (++s == kStages) { s = 0; ph ^= 1u; }
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
     }
     return true;
 }
 
 // CTA 0 issues the pair's MMAs.  The next unit is taken before the current
 // one's last k-blocks are issued, so that the tensor cores have work meanwhile.
-template <bool GRAD, bool F16>
-__device__ __forceinline__ void issue(Walk w, const Ctx &c) {
+template <bool GRAD, bool F16, class C>
+__device__ __forceinline__ void issue(Walk w, const C &c) {
     int s = 0, acc = 0;
     uint32_t ph = 0, aph = 0;
     Unit o, next;
-    Feed feed{c};
+    Feed<C> feed{c};
     bool more = feed.take(&next);
     while (more) {
         o = next;
@@ -885,15 +893,12 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
 }
 
 // Sub-tiles of 32 rows x 128 bytes (64 16-bit columns or 32 of fp32) to
-// global memory through the warp's two staging buffers, by turns.  A lane
-// holds a row; its 16-byte pieces lie as the 128-byte swizzle expects them.
-// The elected lane, the same one each time, issues every copy and waits for
-// them.
-__device__ __forceinline__ void put_rows(uint32_t staging, uint32_t &turn, int lane, const CUtensorMap *map,
-                                         const uint32_t *r, int col, int row, bool add) {
-    const uint32_t stg = staging + turn;
-    turn ^= 4096u;
-    if (elect_one()) bulk_wait_read_1();                  // the sub-tile before the last has left
+// global memory through the warp's 4 KiB staging buffer.  A lane holds a row;
+// its 16-byte pieces lie as the 128-byte swizzle expects them.  The elected
+// lane, the same one each time, issues every copy and waits for them.
+__device__ __forceinline__ void put_rows(uint32_t stg, int lane, const CUtensorMap *map, const uint32_t *r, int col,
+                                         int row, bool add) {
+    if (elect_one()) bulk_wait_read_0();                  // the last sub-tile has left
     __syncwarp();
 #pragma unroll
     for (int g = 0; g < 8; ++g)
@@ -955,17 +960,16 @@ __device__ __forceinline__ void loss_rows(const Plan &p, const Unit &o, uint32_t
     if (CHK(group * p.Mp + row, 1, p.vocab_groups * p.Mp)) p.pairs[group * p.Mp + row] = make_float2(mx, sum);
 }
 
-template <bool GRAD, bool F16>
-__device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const Walk w, const Ctx &c, int warp, int lane) {
+template <bool GRAD, bool F16, class C>
+__device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const Walk w, const C &c, int warp, int lane) {
     const int quarter = warp % 4, half = (warp - 4) / 4;  // 32 rows; one half of the columns
-    const uint32_t stg = c.sbase + kStagingOffset + (uint32_t)(warp - 4) * kStagingBytes;
-    uint32_t turn = 0u;
+    const uint32_t stg = c.sbase + C::kStagingOffset + (uint32_t)(warp - 4) * 4096u;
     const float gscale = GRAD ? p.head->gscale : 0.0f;
     constexpr float kOne = (float)(1ull << (F16 ? kScaleBits16 : kScaleBitsBf));
     int acc = 0;
     uint32_t aph = 0;
     Unit o;
-    Feed feed{c};
+    Feed<C> feed{c};
     for (;;) {
         const int slot = feed.slot;
         if (!feed.take(&o)) return;
@@ -1031,7 +1035,7 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     g[i] = pack2<F16>(__uint_as_float(r[2 * i]) * gscale, __uint_as_float(r[2 * i + 1]) * gscale);
-                put_rows(stg, turn, lane, &maps.dt_out, g, o.n0 + cc, o.piece * kPiece + row0, false);
+                put_rows(stg, lane, &maps.dt_out, g, o.n0 + cc, o.piece * kPiece + row0, false);
             }
         } else {
             // the pieces' sums of dx: a slot each, or added in place in order
@@ -1047,8 +1051,8 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
             for (int cc = c0; cc < c1 && o.n0 + cc < p.D; cc += 64) {
                 uint32_t r[64];
                 tmem_ld64(tmem + (uint32_t)cc, r);
-                put_rows(stg, turn, lane, &maps.acc, r, o.n0 + cc, arow, add);
-                if (o.n0 + cc + 32 < p.D) put_rows(stg, turn, lane, &maps.acc, r + 32, o.n0 + cc + 32, arow, add);
+                put_rows(stg, lane, &maps.acc, r, o.n0 + cc, arow, add);
+                if (o.n0 + cc + 32 < p.D) put_rows(stg, lane, &maps.acc, r + 32, o.n0 + cc + 32, arow, add);
             }
         }
         tc_fence_before();
@@ -1069,9 +1073,10 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
 // A warp of its own reports finished units, so that the epilogue does not
 // wait for its stores to land (5600 cycles a unit when it did).  It holds the
 // unit's slot until it has reported, so at most kSlots units are unreported.
-__device__ __forceinline__ void report(const Plan &p, const Ctx &c) {
+template <class C>
+__device__ __forceinline__ void report(const Plan &p, const C &c) {
     Unit o;
-    Feed feed{c};
+    Feed<C> feed{c};
     while (feed.next(&o)) {
         if (!__all_sync(0xffffffffu, c.wait(c.stored(feed.slot), feed.ph))) return;
         if (elect_one()) {
@@ -1089,17 +1094,18 @@ xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint32_t *words = reinterpret_cast<uint32_t *>(smem + kUnitOffset + kSlots * sizeof(Unit));
-    Ctx c;
+    using L = Layout<GRAD>;
+    uint32_t *words = reinterpret_cast<uint32_t *>(smem + L::kUnitOffset + kSlots * sizeof(Unit));
+    Ctx<GRAD> c;
     c.sbase = smem_addr(smem);
-    c.bars = c.sbase + kBarOffset;
+    c.bars = c.sbase + L::kBarOffset;
     c.rank = cluster_rank();
-    c.slots = reinterpret_cast<const Unit *>(smem + kUnitOffset);
+    c.slots = reinterpret_cast<const Unit *>(smem + L::kUnitOffset);
     c.abort_flag = words;
     uint32_t *tmem_slot = words + 1;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;   // warp-uniform
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < L::kStages; ++s) {
             mbar_init(c.full(s), 1);
             mbar_init(c.empty(s), 1);
         }
@@ -1115,8 +1121,8 @@ xent_tile_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Plan
         mbar_init(c.wanted(), 1);
         *c.abort_flag = 0u;
         fence_mbar_init();
-        prefetch_map(&maps.x);
-        prefetch_map(&maps.w);
+        prefetch_map(&maps.x_k);
+        prefetch_map(&maps.w_k);
     }
     if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), 512);
     tc_fence_before();
@@ -1302,7 +1308,11 @@ template <bool GRAD>
 cudaError_t launch_tiles(const Plan &p, const void *table, void *dtable, int sms, cudaStream_t s) {
     Maps maps;
     cudaError_t err = encode(&maps.w, table, p.D, p.V, 64, 64);
+    if (err == cudaSuccess) err = encode(&maps.w_k, table, p.D, p.V, 64, 128);
     if (err == cudaSuccess)                              // already in the swizzle's order
+        err = encode_tensor_map_2d(&maps.x_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.xc, 64, (uint64_t)(p.Mp * p.xblocks), 128,
+                                   64, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (GRAD && err == cudaSuccess)
         err = encode_tensor_map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.xc, 64, (uint64_t)(p.Mp * p.xblocks), 128,
                                    64, 64, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (GRAD) {
@@ -1315,15 +1325,15 @@ cudaError_t launch_tiles(const Plan &p, const void *table, void *dtable, int sms
                                        CU_TENSOR_MAP_SWIZZLE_128B);
         if (err == cudaSuccess) err = encode(&maps.dt_out, dtable, p.D, p.V, 64, 32);
     } else {
-        maps.g_k = maps.g_mn = maps.dt_out = maps.acc = maps.x;     // unused
+        maps.x = maps.g_k = maps.g_mn = maps.dt_out = maps.acc = maps.x_k;     // unused
     }
     if (err != cudaSuccess) return err;
     auto kern = p.f16 ? xent_tile_kernel<GRAD, true> : xent_tile_kernel<GRAD, false>;
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<GRAD>::kBytes);
     if (err != cudaSuccess) return err;
     count_launch();
     // the pair is the kernel's compile-time cluster
-    return launch_k(kern, dim3((unsigned)(sms / 2 * 2)), dim3(kThreads), (size_t)kSmemBytes, s, 1, maps, p);
+    return launch_k(kern, dim3((unsigned)(sms / 2 * 2)), dim3(kThreads), (size_t)Layout<GRAD>::kBytes, s, 1, maps, p);
 }
 
 cudaError_t launch_prepare(const Plan &p, const ScanArgs &a, const void *x, cudaStream_t s) {
