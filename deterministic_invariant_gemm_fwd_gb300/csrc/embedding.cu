@@ -3,6 +3,11 @@
 //
 // The lookup moves bytes: a warp per token, 16-byte vectors.
 //
+// Bound of the gradient: the table's bytes (written once whole, 77 MB for
+// 50257 x 768 bf16, 11.6 us), then latency: two short kernels that wait for the
+// sort.  8192 tokens of 768, cold: sort with clearing 14.8 us, chunks 11, joins
+// 8; one after the other 37 us with the host's call.
+//
 // The gradient sorts the tokens by (id, position) and adds each row's tokens
 // in that order, in fp32, so that the result does not depend on scheduling
 // (the Carbon README replaces atomics in scatters with sorted indices, "How

@@ -25,6 +25,15 @@
 // Fixed order: a unit's k-blocks of 64 run in ascending order into one fp32
 // accumulator.  dx adds the pieces' sums in order, and a piece's size is
 // fixed, so the number of positions does not show in a row's result.
+//
+// Bound: the tensor cores, for all but few positions: 2 M D V flops for the
+// loss and three times that for the gradients (z is formed again; storing it
+// would cost 2 M V fp32 or rounded values).  8192 x 768 x 50257 bf16, alone
+// in the trace: loss 297 us, 2.1 PFLOP/s, the tensor pipe active in 87% of the
+// cycles; gradients 1.03 ms, 1.85 PFLOP/s, 78%: G passes through HBM about
+// once each way, and operands arrive late at times.  Called again and again
+// they run into the power limit: 359 us and 1.64 ms for both.  One position:
+// the table's bytes, 77 MB in 26 us.
 #include "bounds.cuh"
 #include "device_sync.cuh"
 #include "rowvec.cuh"
@@ -62,7 +71,12 @@ struct Layout {
 constexpr unsigned kDone = 2;                         // reports of a finished unit: one per CTA
 
 constexpr int kGroup = 128;              // vocabulary entries per (max, sum) pair
-constexpr int kPiece = 4096;             // vocabulary entries per piece
+// Vocabulary entries per piece.  With 2048 dx adds twice as many sums
+// (8192 x 768 x 50257, the loss and its gradients: 1.77 ms instead of 1.54);
+// 8192 took 1.50 with twice the memory for G.
+constexpr int kPiece = 4096;
+// G has room for pieces up to this size, and at least for those in use: half
+// of L2 holds what it can of them.
 constexpr int64_t kGBytes = 64ll << 20;
 constexpr int64_t kSlotBytes = 64ll << 20;    // dx: the pieces' sums side by side up to this size, else added in place
 // x and G are kept as blocks of 128 positions x 64 columns that are images of

@@ -16,6 +16,12 @@
 // too long for a group are read again for each pass.  The order of a row's
 // sums depends on D, the dtype and the alignment of the tensors alone.
 //
+// Measured cold, bf16: forward with residual and 8-bit rows, 8192 x 768: 11 us;
+// 8192 x 4096: 45 us, the bytes at the rate of a copy (6.7 TB/s).  Gradient
+// 15 us and 67 us (a copy's rate: 40): a row's two sums wait for each other.
+// Rows of 1001 elements, 8192 of them: 24.5 and 25 us.  dgamma's second kernel:
+// 7 us, a launch and one dependent read of the partial rows.
+//
 // dgamma: a group takes the rows g, g + groups, ... and adds its columns'
 // terms in registers; the groups' sums are added per CTA in group order, then
 // over the CTAs in order by a second kernel.

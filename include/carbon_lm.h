@@ -21,7 +21,14 @@
  * Workspace: where a function takes one, the caller passes a 16-byte aligned
  * device buffer of at least the bytes that its _workspace query returns; the
  * library allocates nothing.  Its contents need not be set and mean nothing
- * afterwards; two calls that may overlap on the GPU need one each.
+ * afterwards; two calls that may overlap on the GPU need one each.  About:
+ *   carbon_embedding_bwd     M (16 + D / 2) bytes (a histogram per 1024 or 8192
+ *                            tokens more above 8192 tokens)
+ *   carbon_rms_norm_bwd      at most 608 rows of D fp32 values
+ *   carbon_linear_xent_fwd   M (2 D + V / 16) bytes
+ *   carbon_linear_xent_bwd   M (6 D + 24576) bytes (the logits would take
+ *                            4 M V), and up to 128 MiB more below about 2500
+ *                            positions.  M = 8192, D = 768: 240 MB
  *
  * Indices that name no row (a token id outside [0, V); a target that is
  * neither ignore_index nor in [0, V)): the lookup gives a row of zeros, the
