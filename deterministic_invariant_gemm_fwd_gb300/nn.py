@@ -149,8 +149,15 @@ class _EmbeddingFunction(torch.autograd.Function):
 
 def embedding(ids, table, scale=1.0, padding_idx=None):
     """scale * table[ids], differentiable in table; the gradient adds a row's
-    tokens in the order of their positions (no atomics)."""
-    return _EmbeddingFunction.apply(ids.contiguous(), table, float(scale), -1 if padding_idx is None else padding_idx)
+    tokens in the order of their positions (no atomics).  The row padding_idx
+    (negative: counted from the end) gets no gradient."""
+    padding = -1
+    if padding_idx is not None:
+        rows = table.shape[0]
+        if not -rows <= padding_idx < rows:
+            raise ValueError(f"padding_idx {padding_idx} is outside a table of {rows} rows")
+        padding = padding_idx % rows
+    return _EmbeddingFunction.apply(ids.contiguous(), table, float(scale), padding)
 
 
 class Embedding(torch.nn.Module):
@@ -172,6 +179,15 @@ class Embedding(torch.nn.Module):
 
 def _flat(t, width):
     return t.reshape(-1, width).contiguous()
+
+
+def _width(x, width, residual=None):
+    """Raises unless x has rows of this width, and residual x's shape: rows
+    are flattened, which would regroup the elements of others."""
+    if x.dim() < 1 or x.shape[-1] != width:
+        raise ValueError(f"x has shape {tuple(x.shape)}; expected [..., {width}]")
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
 
 
 class _RmsNormFunction(torch.autograd.Function):
@@ -197,6 +213,7 @@ def rms_norm(x, gamma, residual=None, eps=1e-6):
     """y = norm(x + residual) * gamma over the last dimension; with a residual
     returns (y, x + residual), the second being the residual stream that goes
     on.  Differentiable in x, residual and gamma."""
+    _width(x, gamma.shape[0], residual)
     return _RmsNormFunction.apply(x, residual, gamma, eps)
 
 
@@ -251,6 +268,7 @@ def norm_linear(x, gamma, weight, bias=None, residual=None, eps=1e-6, tier="exac
     two tensors of the input's type.  The forward pass is the same; the
     backward pass reads the rows back to within scale / 2 = max|row| / 254.
     With a residual returns (output, x + residual)."""
+    _width(x, gamma.shape[0], residual)
     return _NormLinearFunction.apply(x, residual, gamma, weight, bias, eps, tier)
 
 
@@ -277,4 +295,7 @@ def linear_cross_entropy(x, table, targets, ignore_index=-100, reduction="mean")
     Embedding's weight) against targets, without storing the logits;
     differentiable in x and table.  reduction="mean" divides by the positions
     that count and is 0 where there are none."""
+    _width(x, table.shape[1])
+    if targets.shape != x.shape[:-1]:
+        raise ValueError(f"targets has shape {tuple(targets.shape)}; expected {tuple(x.shape[:-1])}")
     return _LinearCrossEntropyFunction.apply(x, table, targets, ignore_index, reduction)
