@@ -5,7 +5,7 @@
 //   codes = round(n * (127 / max|n|)),  scales = max|n| / 127
 //   dx = rstd * (gamma*dy - n * mean(gamma*dy*n)) + dh,  dgamma = sum_m dy * n
 //
-// Bound: memory.  A group of threads (a warp, four warps or sixteen, by the
+// Bound: memory.  A group of threads (1, 4, 8 or 16 warps, by the
 // row's length) takes a row at a time: each of its threads has up to kMaxHold
 // elements, the group reduces and writes.  The forward pass reads a row once,
 // into registers.  The gradient, and the forward pass where 16-byte vectors do
@@ -18,7 +18,7 @@
 //
 // Measured cold, bf16: forward with residual and 8-bit rows, 8192 x 768: 11 us;
 // 8192 x 4096: 45 us, the bytes at the rate of a copy (6.7 TB/s).  Gradient
-// 15 us and 67 us (a copy's rate: 40): a row's two sums wait for each other.
+// 15 us and 55 us (a copy's rate: 40).
 // Rows of 1001 elements, 8192 of them: 24.5 and 25 us.  dgamma's second kernel:
 // 7 us, a launch and one dependent read of the partial rows.
 //
@@ -431,7 +431,7 @@ struct BwdArgs {
 // A group's rows come through its ring: n's source, dy and dh.  n and gamma*dy
 // stay in registers between the sum over the row and dx.
 template <typename T, int G, int N, int H, bool CODES>
-__global__ void __launch_bounds__(kRingThreads<G>, G == 32 ? 2 : G == 128 ? 4 : 1)
+__global__ void __launch_bounds__(kRingThreads<G>, G == 128 ? 4 : G == 512 ? 1 : 2)
 norm_bwd_kernel(const BwdArgs<T> a, const int stages) {
     constexpr int kThreads = kRingThreads<G>, kRows = kThreads / G;
     using Source = typename std::conditional<CODES, int8_t, T>::type;
@@ -676,44 +676,57 @@ bool dtype_ok(int dtype) { return dtype == CARBON_F32 || dtype == CARBON_BF16 ||
 
 // Calls f(G, H) for the group that holds a row of D elements: G threads with H
 // vectors of N each, at most kMaxHold elements per thread.  Returns false
-// where none does.
-template <int N, typename F>
+// where none does.  The gradient, which holds three values per element, takes
+// rows of vectors at half as many elements per thread where more than a warp
+// shares a row and a larger group is left (bf16, the gradient with dh: 8192 x
+// 4096 58 us with 256 threads, 72 with 128; 8192 x 2048 37 us with 128, 44 with
+// 256; 4096 x 8192 61 us with 512, 114 with 256).
+template <int N, bool GRAD, typename F>
 bool with_group(int64_t D, F &&f) {
     using std::integral_constant;
     const int64_t nvec = D / N;
-    constexpr int H = kMaxHold / N;
-    auto held = [&](auto g) {                             // fewest vectors per thread that hold the row
-        constexpr int G = g();
-        if (nvec > G * H) return false;
+    constexpr int H = kMaxHold / N, kMiddle = GRAD && N > 1 ? H / 2 : H;
+    auto held = [&](auto g, auto most) {                  // fewest vectors per thread that hold the row
+        constexpr int G = g(), kMost = most();
+        if (nvec > G * kMost) return false;
+        auto with = [&](auto h) {
+            if constexpr (h() <= kMost) f(g, h);
+        };
         if constexpr (H == 8) {                           // fp32 vectors
-            if (nvec <= G * 2) f(g, integral_constant<int, 2>());
-            else if (nvec <= G * 4) f(g, integral_constant<int, 4>());
-            else if (nvec <= G * 6) f(g, integral_constant<int, 6>());
-            else f(g, integral_constant<int, 8>());
+            if (nvec <= G * 2) with(integral_constant<int, 2>());
+            else if (nvec <= G * 4) with(integral_constant<int, 4>());
+            else if (nvec <= G * 6) with(integral_constant<int, 6>());
+            else with(integral_constant<int, 8>());
         } else if constexpr (H == 4) {
-            if (nvec <= G) f(g, integral_constant<int, 1>());
-            else if (nvec <= G * 2) f(g, integral_constant<int, 2>());
-            else if (nvec <= G * 3) f(g, integral_constant<int, 3>());
-            else f(g, integral_constant<int, 4>());
+            if (nvec <= G) with(integral_constant<int, 1>());
+            else if (nvec <= G * 2) with(integral_constant<int, 2>());
+            else if (nvec <= G * 3) with(integral_constant<int, 3>());
+            else with(integral_constant<int, 4>());
         } else {
-            if (nvec <= G * (H / 4)) f(g, integral_constant<int, H / 4>());
-            else f(g, integral_constant<int, H>());
+            if (nvec <= G * (H / 4)) with(integral_constant<int, H / 4>());
+            else with(integral_constant<int, H>());
         }
         return true;
     };
-    return held(integral_constant<int, 32>()) || held(integral_constant<int, 128>()) || held(integral_constant<int, 512>());
+    constexpr integral_constant<int, H> all;
+    constexpr integral_constant<int, kMiddle> middle;
+    if (held(integral_constant<int, 32>(), all) || held(integral_constant<int, 128>(), middle)) return true;
+    if constexpr (kMiddle < H)
+        if (held(integral_constant<int, 256>(), middle)) return true;
+    return held(integral_constant<int, 512>(), all);
 }
 
 // The ring of a kernel with groups of G threads: as many stages as leave room
 // for two CTAs per SM of 8 warps, four of 4 warps or one of 16 (more CTAs
-// rather than more stages: one CTA's warps work while another's wait), but at
-// least two.  bytes: one stage of all the CTA's groups; gamma: its bytes, behind
+// rather than more stages: one CTA's warps work while another's wait; but three
+// CTAs of 8 warps with two stages took 70 us where two with four take 58), but
+// at least two.  bytes: one stage of all the CTA's groups; gamma: its bytes, behind
 // them.  0 where two stages do not fit.
 constexpr int64_t kSharedMost = 225 * 1024;
 
 template <int G>
 int ring_stages(int64_t bytes, int64_t gamma) {
-    int s = (int)(((G == 32 ? 110 * 1024 : G == 128 ? 54 * 1024 : kSharedMost) - gamma) / bytes);
+    int s = (int)(((G == 32 || G == 256 ? 110 * 1024 : G == 128 ? 54 * 1024 : kSharedMost) - gamma) / bytes);
     if (s < 2) s = 2;
     if (s > kMaxStages) s = kMaxStages;
     return s * bytes + gamma <= kSharedMost ? s : 0;
@@ -739,7 +752,7 @@ cudaError_t launch_fwd(const FwdArgs<T> &a, cudaStream_t s) {
     cudaError_t err = cudaSuccess;
     bool fits = true;
     count_launch();
-    const bool held = with_group<N>(a.D, [&](auto g, auto h) {
+    const bool held = with_group<N, false>(a.D, [&](auto g, auto h) {
         constexpr int G = g(), H = h();
         if constexpr (N > 1) {
             constexpr int kRows = G > 128 ? 1 : 128 / G;
@@ -777,7 +790,7 @@ template <typename T, int N, bool CODES>
 cudaError_t launch_bwd(const BwdArgs<T> &a, T *dgamma, cudaStream_t s) {
     cudaError_t err = cudaSuccess;
     int ctas = 0;
-    bool held = with_group<N>(a.D, [&](auto g, auto h) {
+    bool held = with_group<N, true>(a.D, [&](auto g, auto h) {
         constexpr int G = g(), H = h(), kRows = kRingThreads<G> / G;
         const int64_t stage = (int64_t)kRows * (a.dh ? 3 : 2) * row_slot(a.D * sizeof(T));
         const int stages = ring_stages<G>(stage, a.D * (int64_t)sizeof(T));
