@@ -20,7 +20,7 @@
 // The gradient takes the vocabulary in pieces of kPiece entries: L units of
 // later pieces run before the T and X units of a piece, so that a unit rarely
 // waits for the units it reads (counters in the workspace; units are handed
-// out in list order and wait only for earlier ones, so the waits end).
+// out in list order and wait only for earlier ones, so the waits end: xent_units.h).
 //
 // Fixed order: a unit's k-blocks of 64 run in ascending order into one fp32
 // accumulator.  dx adds the pieces' sums in order, and a piece's size is
@@ -38,6 +38,7 @@
 #include "device_sync.cuh"
 #include "rowvec.cuh"
 #include "tcgen05.cuh"
+#include "xent_units.h"
 
 namespace carbon {
 namespace {
@@ -45,7 +46,6 @@ namespace {
 __device__ unsigned int g_xent_status = 0;
 #define CHK(idx, len, n) in_bounds(&g_xent_status, (int64_t)(idx), (int64_t)(len), (int64_t)(n))
 
-constexpr int kBM = 256, kBN = 256, kBK = 64;        // a CTA pair's tile; each CTA has 128 rows
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (4 + kEpiWarps);        // TMA producer, MMA issuer, scheduler, reporter, epilogue
 constexpr uint32_t kBlock = 64 * kBK * 2;             // one 64 x 64 box: 8 KiB
@@ -68,17 +68,6 @@ struct Layout {
     static_assert(kBytes <= 232448, "shared memory per block");
     static_assert(kUnitOffset % 16 == 0, "units are read as 16-byte vectors");
 };
-constexpr unsigned kDone = 2;                         // reports of a finished unit: one per CTA
-
-constexpr int kGroup = 128;              // vocabulary entries per (max, sum) pair
-// Vocabulary entries per piece.  With 2048 dx adds twice as many sums
-// (8192 x 768 x 50257, the loss and its gradients: 1.77 ms instead of 1.54);
-// 8192 took 1.50 with twice the memory for G.
-constexpr int kPiece = 4096;
-// G has room for pieces up to this size, and at least for those in use: half
-// of L2 holds what it can of them.
-constexpr int64_t kGBytes = 64ll << 20;
-constexpr int64_t kSlotBytes = 64ll << 20;    // dx: the pieces' sums side by side up to this size, else added in place
 // x and G are kept as blocks of 128 positions x 64 columns that are images of
 // the MMA's operands in shared memory, for either orientation, so that a load
 // is contiguous bytes.
@@ -93,104 +82,7 @@ constexpr int kPlane = 128 * 8, kPlanes = 8 * kPlane;         // elements of a p
 // common factor takes it out again.  |G| <= 2^k: no sum comes near fp32's
 // range for operands of ordinary size.
 constexpr int kScaleBits16 = 12, kScaleBitsBf = 32;
-constexpr int64_t kCountAhead = 16384;   // longer lists of positions are counted by a kernel of their own
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-struct Head {
-    int kept;                            // positions that count
-    float gscale;                        // the gradients' common factor
-    float gmax;                          // largest |g|, where xent_count_kernel has run
-};
-
-// Sizes and workspace addresses, host and device.
-struct Plan {
-    int64_t M, Mp, D, V;                 // Mp: M rounded up to a tile's rows, at least one tile
-    int vocab_groups;                    // pairs per row
-    int dtiles, dwidth;                  // column tiles of dx and dtable
-    int xblocks;                         // blocks of x per 128 positions
-    int vocab_tiles;                     // rows of T units
-    int lwidth;                          // vocabulary entries per L unit
-    int pieces, buffers;
-    int lead;                            // pieces whose L units run ahead of a piece's T and X units
-    int slots;                           // pieces' sums of dx kept side by side; 1: added in place
-    bool f16, grad;
-    Head *head;
-    int *ahead;                          // positions that count before each block of 128, or null
-    unsigned int *ticket;                // next unit
-    unsigned int *joined;                // CTAs of xent_join_kernel that are done
-    unsigned int *done_l, *done_tx;      // finished L units, T and X units, per piece
-    unsigned int *done_v;                // finished L units per 256 vocabulary entries (what a T unit reads)
-    int *rowmap, *inverse, *tgt;
-    float *lse2, *rfac;                  // gradient: lse log2(e) - k, g / max |g|
-    void *xc, *g;
-    float *acc;                          // [slots][Mp][D]
-    float2 *pairs;                       // [vocab_groups][Mp]
-    float *zt;                           // [Mp]
-};
-
-int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-
-// Fills the plan; returns the workspace bytes.
-int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, bool grad, bool f16) {
-    Plan p = {};
-    p.M = M; p.D = D; p.V = V; p.grad = grad; p.f16 = f16;
-    p.Mp = round_up(M > 0 ? M : 1, kBM);
-    p.vocab_groups = (int)((V + kGroup - 1) / kGroup);
-    p.pieces = grad ? (int)((V + kPiece - 1) / kPiece) : 1;
-    // tiles of at most 256 columns, of nearly equal widths
-    const int dtiles = (int)((D + kBN - 1) / kBN);
-    p.dwidth = (int)round_up((D + dtiles - 1) / dtiles, 128);
-    p.dtiles = (int)((D + p.dwidth - 1) / p.dwidth);
-    const int64_t tiles256 = p.Mp / kBM * ((V + kBN - 1) / kBN);
-    // narrower tiles where 256-wide ones would leave SMs idle for most of a wave
-    p.lwidth = tiles256 < 152 * 4 ? 128 : 256;
-    // How many pieces' L units run ahead of a piece's T and X units: two units
-    // for each of the 76 pairs of CTAs, so that what a T or X unit reads is
-    // complete when its turn comes; all of them where that is at most eight
-    // each (1 x 768 x 50257: 119 us for the gradient with the loss against 146,
-    // 509 x 512 x 32003: 103 against 126; but 1200 x 768 x 50257: 333 against
-    // 319).  G has room for the pieces ahead, the one that is read and one
-    // more; small ones are all kept.
-    const int64_t l_units = p.Mp / kBM * ((kPiece + p.lwidth - 1) / p.lwidth);
-    const int64_t lead = l_units * p.pieces <= 8 * 76 ? p.pieces : (2 * 76 + l_units - 1) / l_units;
-    int64_t buffers = kGBytes / (p.Mp * 2 * kPiece);
-    if (buffers < lead + 2) buffers = lead + 2;
-    p.lead = (int)(lead < p.pieces ? lead : p.pieces);
-    p.buffers = (int)(buffers < p.pieces ? buffers : p.pieces);
-    p.slots = (int64_t)p.pieces * p.Mp * D * 4 <= kSlotBytes ? p.pieces : 1;
-
-    char *base = static_cast<char *>(ws);
-    int64_t used = 0;
-    auto take = [&](int64_t bytes) {
-        char *q = base + used;
-        used += round_up(bytes, 128);
-        return q;
-    };
-    p.head = reinterpret_cast<Head *>(take(sizeof(Head)));
-    if (M > kCountAhead) p.ahead = reinterpret_cast<int *>(take(4 * (p.Mp / 128)));
-    p.vocab_tiles = grad ? (int)((V + kBM - 1) / kBM) : 0;
-    p.ticket = reinterpret_cast<unsigned int *>(take(4 * (2 + 2 * (int64_t)p.pieces + p.vocab_tiles)));
-    p.joined = p.ticket + 1;
-    p.done_l = p.ticket + 2;
-    p.done_tx = p.done_l + p.pieces;
-    p.done_v = p.done_tx + p.pieces;
-    p.rowmap = reinterpret_cast<int *>(take(4 * p.Mp));
-    p.inverse = reinterpret_cast<int *>(take(4 * p.Mp));
-    p.tgt = reinterpret_cast<int *>(take(4 * p.Mp));
-    p.xblocks = (int)((D + 63) / 64);
-    p.xc = take(2 * p.Mp * p.xblocks * 64);
-    if (grad) {
-        p.lse2 = reinterpret_cast<float *>(take(4 * p.Mp));
-        p.rfac = reinterpret_cast<float *>(take(4 * p.Mp));
-        p.g = take(2 * p.Mp * kPiece * p.buffers);
-        p.acc = reinterpret_cast<float *>(take(4 * (int64_t)p.slots * p.Mp * D));
-    } else {
-        p.pairs = reinterpret_cast<float2 *>(take(8 * (int64_t)p.vocab_groups * p.Mp));
-        p.zt = reinterpret_cast<float *>(take(4 * p.Mp));
-    }
-    if (out) *out = p;
-    return used + 128;                   // room to align the base to 128 bytes
-}
 
 void *align128(void *p) {
     return reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(p) + 127) & ~static_cast<uintptr_t>(127));
@@ -211,8 +103,6 @@ __device__ __forceinline__ bool counts(const Plan &p, const ScanArgs &a, int64_t
     *tgt = a.targets[m];
     return *tgt != a.ignore_index && *tgt >= 0 && *tgt < p.V;
 }
-
-__device__ __forceinline__ int row_tiles(int kept) { return kept > kBM ? (kept + kBM - 1) / kBM : 1; }
 
 // Long lists: positions that count ahead of each block of 128, and the largest
 // |g| (a gradient per position).  One CTA, a warp per block.
@@ -363,7 +253,7 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
         p.tgt[i] = -1;
         if (p.grad) p.lse2[i] = p.rfac[i] = 0.0f;
     }
-    for (int i = t; i < 2 + 2 * p.pieces + p.vocab_tiles; i += kPrepThreads) p.ticket[i] = 0u;
+    for (int i = t; i < counters(p); i += kPrepThreads) p.ticket[i] = 0u;
     if (t == 0) {
         p.head->kept = kept;
         if (a.count) *a.count = kept;
@@ -374,97 +264,6 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
         }
     }
 }
-
-// ---- the list of units -------------------------------------------------------------
-
-enum UnitType { UNIT_L = 0, UNIT_T = 1, UNIT_X = 2 };
-
-struct alignas(16) Unit {
-    int type, piece;
-    int m0, n0;              // output tile: first row, first column (rows of the output for T are table rows)
-    int width;               // columns, a multiple of 128
-    int left;                // 0: the list has ended
-    int unused[2];
-};
-
-// Phases in list order: L of the first `lead` pieces, then for each piece p: L
-// of p + lead, and T and X of p, the longer of these first (T takes a k-block
-// per 64 positions, X one per 64 entries).  Where all L units come first, so
-// do all of the longer kind: the short units then even out the end.
-struct Walk {
-    const Plan &p;
-    int tm;                  // row tiles of positions
-    int kept;
-    int phase = 0;
-    uint32_t base = 0, count = 0;        // the host has checked that the list is shorter than 2^31
-
-    __device__ Walk(const Plan &plan, int n) : p(plan), tm(row_tiles(n)), kept(n) { count = size(0); }
-
-    __device__ int cols(int piece) const { return min(kPiece, (int)(p.V - (int64_t)piece * kPiece)); }
-    __device__ uint32_t n_l(int piece) const {
-        const int c = p.grad ? cols(piece) : (int)p.V;
-        return (uint32_t)tm * (uint32_t)((c + p.lwidth - 1) / p.lwidth);
-    }
-    __device__ uint32_t n_t(int piece) const { return (uint32_t)((cols(piece) + kBM - 1) / kBM) * (uint32_t)p.dtiles; }
-    __device__ uint32_t n_x() const { return (uint32_t)(tm * p.dtiles); }
-    // A phase: its kind of units, or T and X of a piece, and the piece.
-    static constexpr int kBoth = 3;
-    __device__ int phases() const { return !p.grad ? 1 : p.lead == p.pieces ? 3 * p.pieces : p.lead + 2 * p.pieces; }
-    __device__ int kind_of(int ph, int *piece) const {
-        int q = ph - p.lead;
-        if (q < 0) { *piece = ph; return UNIT_L; }
-        if (p.lead == p.pieces) {
-            const bool second = q >= p.pieces;
-            *piece = second ? q - p.pieces : q;
-            return second == t_first() ? UNIT_X : UNIT_T;
-        }
-        *piece = q & 1 ? q / 2 : p.lead + q / 2;
-        return q & 1 ? kBoth : UNIT_L;
-    }
-    __device__ bool t_first() const { return kept >= kPiece; }
-    __device__ uint32_t size(int ph) const {
-        int q;
-        switch (kind_of(ph, &q)) {
-        case UNIT_L: return q < p.pieces ? n_l(q) : 0u;
-        case UNIT_T: return n_t(q);
-        case UNIT_X: return n_x();
-        default: return n_t(q) + n_x();
-        }
-    }
-    // The unit at position u of the list (u never decreases).
-    __device__ Unit at(uint32_t u) {
-        Unit o = {};
-        while (u >= base + count) {
-            if (phase == phases() - 1) return o;
-            base += count;
-            count = size(++phase);
-        }
-        uint32_t i = u - base;
-        o.left = 1;
-        o.type = kind_of(phase, &o.piece);
-        if (o.type == UNIT_L) {
-            const int c = p.grad ? cols(o.piece) : (int)p.V;
-            o.m0 = (int)(i % (uint32_t)tm) * kBM;
-            o.n0 = (int)(i / (uint32_t)tm) * p.lwidth;
-            o.width = min(p.lwidth, (c - o.n0 + 127) / 128 * 128);
-        } else {
-            if (o.type == kBoth) {
-                const uint32_t head = t_first() ? n_t(o.piece) : n_x();
-                o.type = (i < head) == t_first() ? UNIT_T : UNIT_X;
-                if (i >= head) i -= head;
-            }
-            o.m0 = (int)(i / (uint32_t)p.dtiles) * kBM;
-            o.n0 = (int)(i % (uint32_t)p.dtiles) * p.dwidth;
-            o.width = min(p.dwidth, (int)(p.D - o.n0 + 127) / 128 * 128);
-        }
-        return o;
-    }
-    __device__ int k_blocks(const Unit &o) const {
-        if (o.type == UNIT_L) return (int)((p.D + kBK - 1) / kBK);
-        if (o.type == UNIT_T) return kept > kBK ? (kept + kBK - 1) / kBK : 1;
-        return (cols(o.piece) + kBK - 1) / kBK;
-    }
-};
 
 // ---- PTX pieces ----------------------------------------------------------------------
 
@@ -641,6 +440,7 @@ struct Ctx : Layout<GRAD> {
         atomicExch(&g_xent_status, (unsigned)CARBON_ERR_TIMEOUT);
     }
     __device__ bool aborted() const { return *abort_flag != 0u; }
+    __device__ void add(unsigned int *counter) const { add_release(counter, 1u); }
     // Waits until *counter reaches n.
     __device__ bool wait_count(const unsigned int *counter, unsigned int n) const {
         if (load_acquire(counter) >= n) return true;
@@ -717,29 +517,6 @@ __device__ __forceinline__ void hand_out(const Plan &p, Walk w, const C &c) {
         if (++slot == kSlots) { slot = 0; ph ^= 1u; }
     }
 }
-
-// What a unit's operands wait for.  Pieces seen complete are remembered (an
-// acquiring load costs about 1000 cycles).
-struct Ready {
-    int l = -1, tx = -1;                          // last pieces known complete
-    template <class C>
-    __device__ bool wait(const Plan &p, const Walk &w, const Unit &o, const C &c) {
-        if (!p.grad) return true;
-        if (o.type == UNIT_L) {                   // its piece's buffer is free
-            const int q = o.piece - p.buffers;
-            if (q <= tx) return true;
-            tx = q;
-            return c.wait_count(p.done_tx + q, kDone * (w.n_t(q) + w.n_x()));
-        }
-        if (o.piece <= l) return true;
-        if (o.type == UNIT_T) {
-            const int cols = w.cols(o.piece) - o.m0, n = (min(cols, kBM) + p.lwidth - 1) / p.lwidth;
-            return c.wait_count(p.done_v + (o.piece * kPiece + o.m0) / kBM, kDone * (unsigned)(n * w.tm));
-        }
-        l = o.piece;
-        return c.wait_count(p.done_l + o.piece, kDone * w.n_l(o.piece));
-    }
-};
 
 // Loads of one accumulation: this CTA's rows of A and columns of B, k-block by
 // k-block.  A whole warp runs the loop, one lane issues.  ca, cb: coordinates
@@ -1053,11 +830,9 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
             }
         } else {
             // the pieces' sums of dx: a slot each, or added in place in order
-            const bool add = p.slots == 1 && o.piece > 0;
-            if (add) {                               // the piece before is in memory
-                const int q = o.piece - 1;
-                const bool there = c.wait_count(p.done_tx + q, kDone * (unsigned)(w.n_t(q) + w.n_x()));
-                if (!__all_sync(0xffffffffu, there)) return;
+            const bool add = adds(p, o);
+            if (add) {
+                if (!__all_sync(0xffffffffu, wait_sums(p, w, o, c))) return;
                 fence_proxy_async_all();
             }
             const int arow = (p.slots > 1 ? o.piece * (int)p.Mp : 0) + row0;
@@ -1095,8 +870,7 @@ __device__ __forceinline__ void report(const Plan &p, const C &c) {
         if (!__all_sync(0xffffffffu, c.wait(c.stored(feed.slot), feed.ph))) return;
         if (elect_one()) {
             fence_proxy_async_all();                      // G is read by TMA
-            add_release((o.type == UNIT_L ? p.done_l : p.done_tx) + o.piece, 1u);
-            if (o.type == UNIT_L) add_release(p.done_v + (o.piece * kPiece + o.n0) / kBM, 1u);
+            report_done(p, o, c);
         }
         feed.release();
     }

@@ -1,0 +1,48 @@
+"""The gradient of the output layer's cross entropy on the GPU where its units
+depend on each other: sums of dx added in place, small last pieces of the
+vocabulary, and gradients that differ from row to row.  References and
+tolerances as in test_lm_gpu.py."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import deterministic_invariant_gemm_fwd_gb300 as cg  # noqa: E402
+from tests.test_lm_gpu import gen, same_bits, status, within, xent_case, xent_reference  # noqa: E402
+
+
+def sums_bytes(M, D, V):
+    """Bytes of the pieces' sums of dx side by side; above 64 MiB they are added in place."""
+    return -(-V // 4096) * (-(-M // 256) * 256) * D * 4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,D,V", [
+    (512, 5120, 32000), (300, 5120, 32000),      # all X units before all T units
+    (1, 8192, 50257),
+    (4500, 1024, 13000),                         # T units first, pieces one after the other
+])
+def test_sums_added_in_place(M, D, V, dtype):
+    assert sums_bytes(M, D, V) > 64 << 20 and V > 4096
+    x, table, t = xent_case(M, D, V, dtype, M + V, kept=1.0)
+    g = torch.ones(M, device="cuda")
+    _, _, _, eloss, wdx, wdt, edx, edt = xent_reference(x, table, t, g)
+    _, lse = cg.linear_cross_entropy_fwd(x, table, t, reduction="none")
+    dx, dt = cg.linear_cross_entropy_bwd(g, x, table, t, lse, reduction="none")
+    assert status() == 0
+    within(dx, wdx, edx)
+    within(dt, wdt, edt)
+    again = cg.linear_cross_entropy_bwd(g, x, table, t, lse, reduction="none")
+    assert same_bits(again[0], dx) and same_bits(again[1], dt)
+    # a few rows alone: their sums lie side by side
+    for a, b in ((0, 1), (M // 2, M // 2 + 100), (M - 1, M)):
+        sl = slice(a, min(b, M))
+        rows = sl.stop - sl.start
+        if rows < 1 or sums_bytes(rows, D, V) > 64 << 20:
+            continue
+        part = cg.linear_cross_entropy_bwd(g[sl], x[sl], table, t[sl], lse[sl], reduction="none")[0]
+        assert same_bits(part, dx[sl])
+    assert status() == 0
