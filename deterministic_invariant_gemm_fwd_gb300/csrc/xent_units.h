@@ -230,20 +230,21 @@ struct Walk {
 // until *counter has reached n, c.add(counter) counts one of a unit's kDone
 // reports.
 
-// Before a unit's operands are loaded.  A piece seen complete is remembered (an
-// acquiring load costs about 1000 cycles).
+// Before a unit's operands are loaded.  The last piece seen complete is
+// remembered (an acquiring load costs about 1000 cycles); it says nothing about
+// the pieces before it, whose units may still run.
 struct Ready {
-    int l = -1, tx = -1;                          // last pieces known complete
+    int l = -1, tx = -1;                          // the pieces last seen complete
     template <class C>
     XENT_HD bool wait(const Plan &p, const Walk &w, const Unit &o, const C &c) {
         if (!p.grad) return true;
         if (o.type == UNIT_L) {                   // its piece's buffer is free
             const int q = o.piece - p.buffers;
-            if (q <= tx) return true;
+            if (q < 0 || q == tx) return true;
             tx = q;
             return c.wait_count(p.done_t + q, kDone * w.n_t(q)) && c.wait_count(p.done_x + q, kDone * w.n_x());
         }
-        if (o.piece <= l) return true;
+        if (o.piece == l) return true;
         if (o.type == UNIT_T) {
             const int cols = w.cols(o.piece) - o.m0, n = (lesser(cols, kBM) + p.lwidth - 1) / p.lwidth;
             return c.wait_count(p.done_v + (o.piece * kPiece + o.m0) / kBM, kDone * (unsigned)(n * w.tm));

@@ -3,13 +3,19 @@
 //
 //   order    whatever a unit waits for is done once all units ahead of it in
 //            the list are: the kernel makes progress with any number of CTAs.
+//   enough   whichever units of the list a pair of CTAs has had before, the
+//            waits it has made by the time it runs a unit imply that all units
+//            whose output this one reads, or whose input it overwrites, are done.
 //
-// Over a grid of sizes, random ones, and numbers of positions that count.
+// Over a grid of sizes, random ones, and numbers of positions that count.  The
+// argument names the rule; the default is `order`.
 #include "xent_units.h"
 
 #include <cmath>
 #include <cstdio>
+#include <cstring>
 #include <random>
+#include <utility>
 #include <vector>
 
 using namespace carbon;
@@ -80,6 +86,88 @@ void order(const Case &k) {
             return fail("order: units missing", k, p, q, Unit{});
 }
 
+// Notes the waits that were made, and the counters a unit reports to.
+struct Notes {
+    mutable std::vector<std::pair<const unsigned *, unsigned>> waits;
+    mutable std::vector<unsigned *> adds;
+    bool wait_count(const unsigned *counter, unsigned n) const {
+        waits.push_back({counter, n});
+        return true;
+    }
+    void add(unsigned *counter) const { adds.push_back(counter); }
+};
+
+// A pair that runs each unit of the list with probability `share`.
+void enough(const Case &k, double share, std::mt19937 &rng) {
+    std::vector<unsigned> total;
+    const Plan p = plan_of(k, &total);
+    Walk w(p, k.kept);
+    struct Listed {
+        Unit o;
+        std::vector<size_t> reports;                      // counters, as indexes into `total`
+    };
+    std::vector<Listed> list;
+    std::vector<std::vector<size_t>> of[3];               // per type and piece: places in the list
+    for (auto &t : of) t.resize(p.pieces);
+    for (uint32_t u = 0;; ++u) {
+        const Unit o = w.at(u);
+        if (o.left == 0) break;
+        const Notes n;
+        report_done(p, o, n);
+        Listed l{o, {}};
+        for (unsigned *a : n.adds) {
+            l.reports.push_back((size_t)(a - total.data()));
+            *a += kDone;
+        }
+        of[o.type][o.piece].push_back(list.size());
+        list.push_back(l);
+    }
+    std::vector<char> complete(total.size(), 0);          // counters that this pair has seen at their last value
+    auto note = [&](const Notes &n) {
+        for (const auto &q : n.waits)
+            if (q.second >= *q.first) complete[(size_t)(q.first - total.data())] = 1;
+    };
+    auto done = [&](const Listed &l) {
+        for (size_t r : l.reports)
+            if (complete[r]) return true;
+        return false;
+    };
+    Ready ready;
+    std::bernoulli_distribution runs(share);
+    for (size_t u = 0; u < list.size(); ++u) {
+        if (!runs(rng)) continue;
+        const Unit &o = list[u].o;
+        Notes n;
+        ready.wait(p, w, o, n);
+        note(n);
+        auto all_done = [&](int type, int piece, int from, int to) {      // units of these output columns
+            for (size_t i : of[type][piece]) {
+                const Unit &q = list[i].o;
+                if ((type != UNIT_L || (q.n0 < to && q.n0 + q.width > from)) && !done(list[i])) return false;
+            }
+            return true;
+        };
+        bool ok = true;
+        if (o.type == UNIT_L) {                           // writes G over that of an earlier piece
+            const int q = o.piece - p.buffers;
+            ok = q < 0 || (all_done(UNIT_T, q, 0, 0) && all_done(UNIT_X, q, 0, 0));
+        } else if (o.type == UNIT_T) {                    // G of 256 vocabulary entries, all positions
+            ok = all_done(UNIT_L, o.piece, o.m0, o.m0 + kBM);
+        } else {                                          // G of the piece
+            ok = all_done(UNIT_L, o.piece, 0, kPiece);
+            if (ok && p.slots == 1 && o.piece > 0) {      // and, before its sums go out, the piece before
+                Notes s;
+                wait_sums(p, w, o, s);
+                std::vector<char> before = complete;
+                note(s);
+                ok = all_done(UNIT_X, o.piece - 1, 0, 0);
+                complete = before;                        // another warp has seen this
+            }
+        }
+        if (!ok) return fail("enough", k, p, (int64_t)u, o);
+    }
+}
+
 std::vector<Case> cases() {
     std::vector<Case> all;
     auto add = [&](int64_t M, int64_t D, int64_t V) {
@@ -103,15 +191,20 @@ std::vector<Case> cases() {
 
 }  // namespace
 
-int main() {
+int main(int argc, char **argv) {
+    const bool walk_enough = argc > 1 && std::strcmp(argv[1], "enough") == 0;
     const std::vector<Case> all = cases();
+    std::mt19937 rng(2);
     size_t in_place = 0, x_first = 0;
     for (const Case &k : all) {
         Plan p;
         make_plan(&p, nullptr, k.M, k.D, k.V, true, false);
         in_place += p.slots == 1 && p.pieces > 1;
         x_first += p.slots == 1 && p.pieces > 1 && p.lead == p.pieces && k.kept < kPiece;
-        order(k);
+        if (!walk_enough) order(k);
+        if (!walk_enough || units_of(Walk(p, k.kept)) > 4000) continue;
+        for (double share : {1.0, 0.3, 1.0 / 76})
+            for (int i = 0; i < 3; ++i) enough(k, share, rng);
     }
     // the sizes reach the in-place sums, also where all X units come first
     if (in_place < 100 || x_first < 100) {

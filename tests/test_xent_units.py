@@ -22,6 +22,14 @@ def program(tmp_path_factory):
     return exe
 
 
-def test_units_wait_only_for_earlier_ones(program):
-    r = subprocess.run([program], capture_output=True, text=True, timeout=600)
+def run(program, rule):
+    r = subprocess.run([program, rule], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr
+
+
+def test_units_wait_only_for_earlier_ones(program):
+    run(program, "order")
+
+
+def test_waits_imply_what_a_unit_needs(program):
+    run(program, "enough")
