@@ -104,8 +104,15 @@ __device__ __forceinline__ bool counts(const Plan &p, const ScanArgs &a, int64_t
     return *tgt != a.ignore_index && *tgt >= 0 && *tgt < p.V;
 }
 
+// |g|, or 0 where it is no finite number: NaN and infinity stay in their own
+// rows of G and do not set the others' scale.
+__device__ __forceinline__ float finite_size(float g) {
+    const float v = fabsf(g);
+    return v < INFINITY ? v : 0.0f;
+}
+
 // Long lists: positions that count ahead of each block of 128, and the largest
-// |g| (a gradient per position).  One CTA, a warp per block.
+// finite |g| (a gradient per position).  One CTA, a warp per block.
 constexpr int kCountThreads = 1024;
 
 __global__ void __launch_bounds__(kCountThreads)
@@ -125,7 +132,7 @@ xent_count_kernel(const Plan p, const ScanArgs a) {
             int64_t tgt;
             const bool k = m < p.M && counts(p, a, m, &tgt);
             n += __popc(__ballot_sync(0xffffffffu, k));
-            if (k && p.grad && a.reduction == CARBON_REDUCE_NONE) gmax = fmaxf(gmax, fabsf(a.grad[m]));
+            if (k && p.grad && a.reduction == CARBON_REDUCE_NONE) gmax = fmaxf(gmax, finite_size(a.grad[m]));
         }
         if (lane == 0) counted[warp] = n;
         __syncthreads();
@@ -170,12 +177,12 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
     float gmax = 0.0f;
     int64_t tgt;
     if (p.ahead == nullptr) {
-        const bool all = each && lead;                    // the largest |g| is taken over the whole list
+        const bool all = each && lead;                    // gmax is taken over the whole list
 #pragma unroll 8
         for (int64_t m = t; m < (all ? p.M : first); m += kPrepThreads)
             if (counts(p, a, m, &tgt)) {
                 n += m < first ? 1 : 0;
-                if (all) gmax = fmaxf(gmax, fabsf(a.grad[m]));
+                if (all) gmax = fmaxf(gmax, finite_size(a.grad[m]));
             }
         n = __reduce_add_sync(0xffffffffu, n);
 #pragma unroll
@@ -216,7 +223,7 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
                 p.tgt[pos] = (int)mine;
                 if (p.grad) {
                     p.lse2[pos] = fmaf(a.lse_in[m], kLog2e, (float)-(p.f16 ? kScaleBits16 : kScaleBitsBf));
-                    p.rfac[pos] = !each ? 1.0f : gmax == 0.0f ? 0.0f : __fdiv_rn(a.grad[m], gmax);
+                    p.rfac[pos] = !each ? 1.0f : __fdiv_rn(a.grad[m], gmax == 0.0f ? 1.0f : gmax);
                 }
             } else if (!keep && !p.grad) {
                 a.losses[m] = 0.0f;
@@ -258,7 +265,7 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
         p.head->kept = kept;
         if (a.count) *a.count = kept;
         if (p.grad) {
-            float g = each ? gmax : a.grad[0];
+            float g = !each ? a.grad[0] : gmax == 0.0f ? 1.0f : gmax;
             if (a.reduction == CARBON_REDUCE_MEAN) g = __fdiv_rn(g, (float)(kept > 0 ? kept : 1));
             p.head->gscale = ldexpf(g, -(p.f16 ? kScaleBits16 : kScaleBitsBf));
         }
@@ -768,10 +775,13 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
         const int c0 = half * (o.width / 2), c1 = c0 + o.width / 2;
         float lse2 = 0.0f, rfac = 0.0f;
         int tgt = -1;
+        bool dead = false;                                 // a row without a position
         if (GRAD && o.type == UNIT_L) {
             lse2 = p.lse2[row];
             rfac = p.rfac[row];
-            tgt = p.tgt[row] - o.piece * kPiece - o.n0;     // column of this tile
+            tgt = p.tgt[row];
+            dead = tgt < 0;
+            tgt -= o.piece * kPiece + o.n0;                 // column of this tile
         }
         if (!__all_sync(0xffffffffu, c.wait(c.tfull(acc), aph))) return;
         tc_fence_after();
@@ -784,7 +794,6 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
             uint16_t *g_row = static_cast<uint16_t *>(p.g) +
                 ((int64_t)(row0 / 128) * (kPiece * p.buffers / 64) + ((o.piece % p.buffers) * kPiece + o.n0) / 64) * kPlanes +
                 (row % 128) * 8;
-            const bool dead = rfac == 0.0f;          // no position, or none of its gradient
             const bool plain = __all_sync(0xffffffffu, rfac == 1.0f);
 #pragma unroll 1
             for (int cc = c0; cc < c1; cc += 64) {

@@ -31,7 +31,7 @@ constexpr int64_t kCountAhead = 16384;   // longer lists of positions are counte
 struct Head {
     int kept;                            // positions that count
     float gscale;                        // the gradients' common factor
-    float gmax;                          // largest |g|, where xent_count_kernel has run
+    float gmax;                          // largest finite |g|, where xent_count_kernel has run
 };
 
 // Sizes and workspace addresses, host and device.

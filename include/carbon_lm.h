@@ -147,8 +147,9 @@ int64_t carbon_linear_xent_fwd_workspace(int64_t M, int64_t D, int64_t V);
  *   G[m,v] = g[m] * (P[m,v] - [v == targets[m]]),  dx = G . table,  dtable = G^T . x
  *
  * The logits are formed again, a piece of the vocabulary at a time.  G enters
- * the tensor cores in dtype, scaled so that the largest |g| is a power of
- * two; the sums are fp32.  dtable is written whole.
+ * the tensor cores in dtype, scaled so that the largest finite |g| is a power
+ * of two; the sums are fp32.  A g that is not finite makes its own row of dx,
+ * and dtable, not finite, and no other row of dx.  dtable is written whole.
  * Workspace: carbon_linear_xent_bwd_workspace bytes. */
 carbon_status_t carbon_linear_xent_bwd(void *dx, void *dtable, const float *grad, const void *x,
                                        const void *table, const int64_t *targets, const float *lse,

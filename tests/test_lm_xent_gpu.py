@@ -69,3 +69,43 @@ def test_small_last_piece(M, V):
         within(dt, wdt, edt)
         first = first or (dx.clone(), dt.clone())
         assert same_bits(dx, first[0]) and same_bits(dt, first[1])
+
+
+@pytest.mark.parametrize("M", [70, 20011])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gradients_that_are_not_finite(M, dtype):
+    """NaN and infinity reach their own row of dx and the table's gradient, and
+    no other row of dx."""
+    x, table, t = xent_case(M, 64, 300, dtype, M, kept=0.8)
+    kept = (t >= 0).nonzero()[:, 0]
+    a, b = int(kept[3]), int(kept[-1])
+    _, lse = cg.linear_cross_entropy_fwd(x, table, t, reduction="none")
+
+    def bwd(grad, rows=x):
+        return cg.linear_cross_entropy_bwd(grad, rows, table, t, lse, reduction="none")
+
+    base = torch.randn(M, generator=gen(1), device="cuda")
+    base[a] = base[b] = 0.0
+    ref, _ = bwd(base)
+    for others in (base, torch.zeros_like(base)):
+        want, _ = bwd(others)
+        for bad in (float("nan"), float("inf"), float("-inf")):
+            g = others.clone()
+            g[a], g[b] = bad, float("nan")
+            dx, dt = bwd(g)
+            assert not bool(torch.isfinite(dx[a]).any()) and bool(torch.isnan(dx[b]).all())
+            assert bool(torch.isnan(dt).all())
+            rest = torch.ones(M, dtype=torch.bool, device="cuda")
+            rest[a] = rest[b] = False
+            assert same_bits(dx[rest], want[rest])
+    dx, dt = bwd(torch.full_like(base, float("nan")))
+    assert bool(torch.isnan(dx[kept]).all()) and not bool(dx[t < 0].any()) and bool(torch.isnan(dt).all())
+    # 0 * NaN: a gradient of zero does not hide a row that is not finite
+    holed = x.clone()
+    holed[a] = float("nan")
+    dx, dt = bwd(base, holed)
+    assert bool(torch.isnan(dx[a]).all()) and bool(torch.isnan(dt).all())
+    # what an ignored position's gradient holds does not matter
+    g = base.clone()
+    g[t < 0] = float("nan")
+    assert same_bits(bwd(g)[0], ref)
