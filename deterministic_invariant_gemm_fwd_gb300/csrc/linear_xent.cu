@@ -79,7 +79,7 @@ struct Layout {
 constexpr int kPlane = 128 * 8, kPlanes = 8 * kPlane;         // elements of a plane, of a block
 // G is formed times 2^k, so that probabilities far below the type's (fp16) or
 // fp32's (bf16) smallest normal value keep their bits; the gradients'
-// common factor takes it out again.  |G| <= 2^k: no sum comes near fp32's
+// common factor takes it out again.  |G| <= 2^(k+1): no sum comes near fp32's
 // range for operands of ordinary size.
 constexpr int kScaleBits16 = 12, kScaleBitsBf = 32;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -110,6 +110,11 @@ __device__ __forceinline__ float finite_size(float g) {
     const float v = fabsf(g);
     return v < INFINITY ? v : 0.0f;
 }
+
+// The exponent of the scale that a gradient per position takes out of G: a
+// power of two, so that G's rows are rounded as they would be on their own
+// (divided by gmax itself, every row's rounding depended on the largest one).
+__device__ __forceinline__ int scale_exponent(float gmax) { return gmax == 0.0f ? 0 : ilogbf(gmax); }
 
 // Long lists: positions that count ahead of each block of 128, and the largest
 // finite |g| (a gradient per position).  One CTA, a warp per block.
@@ -223,7 +228,7 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
                 p.tgt[pos] = (int)mine;
                 if (p.grad) {
                     p.lse2[pos] = fmaf(a.lse_in[m], kLog2e, (float)-(p.f16 ? kScaleBits16 : kScaleBitsBf));
-                    p.rfac[pos] = !each ? 1.0f : __fdiv_rn(a.grad[m], gmax == 0.0f ? 1.0f : gmax);
+                    p.rfac[pos] = !each ? 1.0f : ldexpf(a.grad[m], -scale_exponent(gmax));
                 }
             } else if (!keep && !p.grad) {
                 a.losses[m] = 0.0f;
@@ -265,7 +270,7 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
         p.head->kept = kept;
         if (a.count) *a.count = kept;
         if (p.grad) {
-            float g = !each ? a.grad[0] : gmax == 0.0f ? 1.0f : gmax;
+            float g = !each ? a.grad[0] : ldexpf(1.0f, scale_exponent(gmax));
             if (a.reduction == CARBON_REDUCE_MEAN) g = __fdiv_rn(g, (float)(kept > 0 ? kept : 1));
             p.head->gscale = ldexpf(g, -(p.f16 ? kScaleBits16 : kScaleBitsBf));
         }

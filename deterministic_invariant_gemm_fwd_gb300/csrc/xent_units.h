@@ -53,7 +53,7 @@ struct Plan {
     unsigned int *done_l, *done_t, *done_x;   // finished L, T and X units per piece
     unsigned int *done_v;                // finished L units per 256 vocabulary entries (what a T unit reads)
     int *rowmap, *inverse, *tgt;
-    float *lse2, *rfac;                  // gradient: lse log2(e) - k, g / max |g|
+    float *lse2, *rfac;                  // gradient: lse log2(e) - k, g / 2^e
     void *xc, *g;
     float *acc;                          // [slots][Mp][D]
     struct float2 *pairs;                // [vocab_groups][Mp]

@@ -9,10 +9,11 @@
  * Determinism: no floating-point atomics; every sum has a fixed order, so
  * every result is bit-identical from run to run.  A row's result of
  * carbon_embedding_fwd, carbon_rms_norm_fwd and the dx of carbon_rms_norm_bwd,
- * and a position's loss, lse and dX of carbon_linear_xent_*, do not depend on
- * the other rows of the call (batch invariance).  Sums over tokens (the
- * gradients of the table and of gamma) depend on all of them, in a fixed
- * order.
+ * and a position's loss, lse and dX of carbon_linear_xent_* (dX of
+ * CARBON_REDUCE_MEAN but for the count; of CARBON_REDUCE_NONE above the smallest
+ * values of G, see there), do not depend on the other rows of the call (batch
+ * invariance).  Sums over tokens (the gradients of the table and of gamma)
+ * depend on all of them, in a fixed order.
  *
  * Sums, norms and softmax statistics are held in fp32; each output is rounded
  * once, to nearest-even.  dtype is that of every 16- or 32-bit operand and
@@ -147,9 +148,13 @@ int64_t carbon_linear_xent_fwd_workspace(int64_t M, int64_t D, int64_t V);
  *   G[m,v] = g[m] * (P[m,v] - [v == targets[m]]),  dx = G . table,  dtable = G^T . x
  *
  * The logits are formed again, a piece of the vocabulary at a time.  G enters
- * the tensor cores in dtype, scaled so that the largest finite |g| is a power
- * of two; the sums are fp32.  A g that is not finite makes its own row of dx,
- * and dtable, not finite, and no other row of dx.  dtable is written whole.
+ * the tensor cores in dtype, with |g| between 1 and 2 for the largest finite
+ * one (a power of two is taken out); the sums are fp32.  Entries of G then keep
+ * the type's precision down to 2^-26 (CARBON_F16) or 2^-158 (CARBON_BF16) and
+ * lose bits below: with CARBON_REDUCE_NONE the only way in which the gradients
+ * of other positions reach a row of dx.  A g that is not finite makes its own
+ * row of dx, and dtable, not finite, and no other row of dx.  dtable is written
+ * whole.
  * Workspace: carbon_linear_xent_bwd_workspace bytes. */
 carbon_status_t carbon_linear_xent_bwd(void *dx, void *dtable, const float *grad, const void *x,
                                        const void *table, const int64_t *targets, const float *lse,
