@@ -78,8 +78,9 @@ struct Layout {
 // positions writes 512 contiguous bytes a store, straight from its registers.
 constexpr int kPlane = 128 * 8, kPlanes = 8 * kPlane;         // elements of a plane, of a block
 // G is formed times 2^k, so that probabilities far below the type's (fp16) or
-// fp32's (bf16) smallest normal value keep their bits; the gradients'
-// common factor takes it out again.  |G| <= 2^(k+1): no sum comes near fp32's
+// fp32's (bf16) smallest normal value keep their bits; the sums are multiplied
+// by 2^-k before the gradients' common factor (a product of the two factors
+// underflows for small gradients).  |G| <= 2^(k+1): no sum comes near fp32's
 // range for operands of ordinary size.
 constexpr int kScaleBits16 = 12, kScaleBitsBf = 32;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -272,7 +273,7 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
         if (p.grad) {
             float g = !each ? a.grad[0] : ldexpf(1.0f, scale_exponent(gmax));
             if (a.reduction == CARBON_REDUCE_MEAN) g = __fdiv_rn(g, (float)(kept > 0 ? kept : 1));
-            p.head->gscale = ldexpf(g, -(p.f16 ? kScaleBits16 : kScaleBitsBf));
+            p.head->gscale = g;
         }
     }
 }
@@ -768,7 +769,7 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
     const int quarter = warp % 4, half = (warp - 4) / 4;  // 32 rows; one half of the columns
     const uint32_t stg = c.sbase + C::kStagingOffset + (uint32_t)(warp - 4) * 4096u;
     const float gscale = GRAD ? p.head->gscale : 0.0f;
-    constexpr float kOne = (float)(1ull << (F16 ? kScaleBits16 : kScaleBitsBf));
+    constexpr float kOne = (float)(1ull << (F16 ? kScaleBits16 : kScaleBitsBf)), kDown = 1.0f / kOne;
     int acc = 0;
     uint32_t aph = 0;
     Unit o;
@@ -839,7 +840,7 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
                 tmem_ld64(tmem + (uint32_t)cc, r);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    g[i] = pack2<F16>(__uint_as_float(r[2 * i]) * gscale, __uint_as_float(r[2 * i + 1]) * gscale);
+                    g[i] = pack2<F16>(__uint_as_float(r[2 * i]) * kDown * gscale, __uint_as_float(r[2 * i + 1]) * kDown * gscale);
                 put_rows(stg, lane, &maps.dt_out, g, o.n0 + cc, o.piece * kPiece + row0, false);
             }
         } else {
@@ -1033,7 +1034,7 @@ xent_dx_kernel(const Plan p, T *__restrict__ dx) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] = 0.0f;
     if (i >= 0) {
-        const float gscale = p.head->gscale;
+        const float gscale = p.head->gscale, down = 1.0f / (float)(1ull << (p.f16 ? kScaleBits16 : kScaleBitsBf));
         const float *src = p.acc + i * p.D + j;
         constexpr int U = MANY ? 8 : 1;
         for (int s0 = 0; s0 < p.slots; s0 += U) {
@@ -1054,7 +1055,7 @@ xent_dx_kernel(const Plan p, T *__restrict__ dx) {
                 }
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] *= gscale;
+        for (int k = 0; k < 8; ++k) f[k] = f[k] * down * gscale;
     }
     if (CHK(m * p.D + j, 8, p.M * p.D)) store_f32<T, 8>(dx + m * p.D + j, f);
 }

@@ -139,3 +139,18 @@ def test_rows_with_gradients_of_different_sizes(dtype):
     if dtype == "bf16":
         dx4, dt4 = cg.linear_cross_entropy_bwd(grad * 0.25, x, table, t, lse, reduction="none")
         assert same_bits(dx4 * 4, dx) and same_bits(dt4 * 4, dt)
+
+
+@pytest.mark.parametrize("reduction", ["none", "sum"])
+@pytest.mark.parametrize("size", [2.0 ** -120, 2.0 ** -90, 2.0 ** 100])
+def test_gradients_of_extreme_size(size, reduction):
+    """The common factor of the gradients neither vanishes nor overflows."""
+    M, D, V = 130, 72, 500
+    x, table, t = xent_case(M, D, V, "bf16", 3)
+    rows = torch.full((M,), size, device="cuda")
+    grad = rows if reduction == "none" else rows[0]
+    _, lse = cg.linear_cross_entropy_fwd(x, table, t, reduction="none")
+    dx, dt = cg.linear_cross_entropy_bwd(grad, x, table, t, lse, reduction=reduction)
+    _, _, _, _, wdx, wdt, edx, edt = xent_reference(x, table, t, rows)
+    within(dx, wdx, edx)
+    within(dt, wdt, edt)
