@@ -24,14 +24,15 @@ def _dtype(name, t):
     return code
 
 
-def _need(name, t, shape, dtype):
-    """Raises unless t is a contiguous CUDA tensor of this shape and dtype."""
+def _need(name, t, shape, dtype, device):
+    """Raises unless t is a contiguous tensor of this shape and dtype on this
+    CUDA device (its index; that of the call's first operand)."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if device < 0 or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on the device of the call's other operands")
 
 
 def _rows(name, t):
@@ -101,7 +102,7 @@ def embedding_fwd(table, ids, scale=1.0, stream=None):
     import torch
     V, D = _rows("table", table)
     shape = ids.shape
-    _need("ids", ids, shape, torch.int64)
+    _need("ids", ids, shape, torch.int64, table.get_device())
     code = _dtype("table", table)
     s, empty, _ = _begin(table, stream)
     out = empty((*shape, D), table.dtype, table.device)
@@ -116,13 +117,13 @@ def embedding_bwd(dy, ids, num_rows, scale=1.0, padding_idx=-1, accumulate_to=No
     accumulate_to (a gradient of the same table, e.g. the output layer's) the
     sums are added to it in place and it is returned."""
     import torch
-    D = dy.shape[-1]
+    D, at = dy.shape[-1], dy.get_device()
     shape = ids.shape
-    _need("ids", ids, shape, torch.int64)
-    _need("dy", dy, (*shape, D), dy.dtype)
+    _need("ids", ids, shape, torch.int64, at)
+    _need("dy", dy, (*shape, D), dy.dtype, at)
     code = _dtype("dy", dy)
     if accumulate_to is not None:
-        _need("accumulate_to", accumulate_to, (num_rows, D), dy.dtype)
+        _need("accumulate_to", accumulate_to, (num_rows, D), dy.dtype, at)
     s, empty, workspace = _begin(dy, stream)
     out = accumulate_to if accumulate_to is not None else empty((num_rows, D), dy.dtype, dy.device)
     M = ids.numel()
@@ -149,11 +150,11 @@ def rms_norm_fwd(x, gamma, residual=None, eps=1e-6, quantize=False, stream=None)
     checkpoint of the normalised rows."""
     import torch
     shape = M, D = _rows("x", x)
-    dtype, device = x.dtype, x.device
+    dtype, device, at = x.dtype, x.device, x.get_device()
     code = _dtype("x", x)
-    _need("gamma", gamma, (D,), dtype)
+    _need("gamma", gamma, (D,), dtype, at)
     if residual is not None:
-        _need("residual", residual, shape, dtype)
+        _need("residual", residual, shape, dtype, at)
     s, empty, _ = _begin(x, stream)
     h = x if residual is None else empty(shape, dtype, device)
     y = empty(shape, dtype, device)
@@ -175,19 +176,19 @@ def rms_norm_bwd(dy, gamma, rstd, h=None, codes=None, scales=None, dh=None, reco
     from further on.  recompute=True returns (dx, dgamma, y)."""
     import torch
     shape = M, D = _rows("dy", dy)
-    dtype, device = dy.dtype, dy.device
+    dtype, device, at = dy.dtype, dy.device, dy.get_device()
     code = _dtype("dy", dy)
-    _need("gamma", gamma, (D,), dtype)
-    _need("rstd", rstd, (M,), torch.float32)
+    _need("gamma", gamma, (D,), dtype, at)
+    _need("rstd", rstd, (M,), torch.float32, at)
     if (h is None) == (codes is None) or (codes is None) != (scales is None):
         raise ValueError("give either h, or codes and scales")
     if h is not None:
-        _need("h", h, shape, dtype)
+        _need("h", h, shape, dtype, at)
     else:
-        _need("codes", codes, shape, torch.int8)
-        _need("scales", scales, (M,), torch.float32)
+        _need("codes", codes, shape, torch.int8, at)
+        _need("scales", scales, (M,), torch.float32, at)
     if dh is not None:
-        _need("dh", dh, shape, dtype)
+        _need("dh", dh, shape, dtype, at)
     s, empty, workspace = _begin(dy, stream)
     dx = empty(shape, dtype, device)
     dgamma = empty(D, dtype, device)
@@ -205,11 +206,12 @@ def rms_norm_expand(codes, scales, gamma=None, dtype=None, stream=None):
     """codes * scales (* gamma) in dtype (gamma's, or bfloat16)."""
     import torch
     shape = M, D = _rows("codes", codes)
-    _need("codes", codes, shape, torch.int8)
-    _need("scales", scales, (M,), torch.float32)
+    at = codes.get_device()
+    _need("codes", codes, shape, torch.int8, at)
+    _need("scales", scales, (M,), torch.float32, at)
     dtype = dtype or (gamma.dtype if gamma is not None else torch.bfloat16)
     if gamma is not None:
-        _need("gamma", gamma, (D,), dtype)
+        _need("gamma", gamma, (D,), dtype, at)
     s, empty, _ = _begin(codes, stream)
     out = empty(shape, dtype, codes.device)
     st = _b.lib.carbon_rms_norm_expand(out.data_ptr(), codes.data_ptr(), scales.data_ptr(), _p(gamma), M, D,
@@ -222,9 +224,9 @@ def rms_norm_expand(codes, scales, gamma=None, dtype=None, stream=None):
 def _xent_args(x, table, targets, reduction):
     import torch
     M, D = _rows("x", x)
-    V = _rows("table", table)[0]
-    _need("table", table, (V, D), x.dtype)
-    _need("targets", targets, (M,), torch.int64)
+    V, at = _rows("table", table)[0], x.get_device()
+    _need("table", table, (V, D), x.dtype, at)
+    _need("targets", targets, (M,), torch.int64, at)
     if reduction not in _b.REDUCTIONS:
         raise ValueError(f"reduction {reduction!r}; expected one of {sorted(_b.REDUCTIONS)}")
     return M, D, V, _dtype("x", x), _b.REDUCTIONS[reduction]
@@ -257,9 +259,9 @@ def linear_cross_entropy_bwd(grad, x, table, targets, lse, ignore_index=-100, re
     """(dx, dtable) from grad (fp32: [M] for reduction="none", else a scalar)."""
     import torch
     M, D, V, code, red = _xent_args(x, table, targets, reduction)
-    _need("lse", lse, (M,), torch.float32)
-    _need("grad", grad, () if red else (M,), torch.float32)
-    device = x.device
+    device, at = x.device, x.get_device()
+    _need("lse", lse, (M,), torch.float32, at)
+    _need("grad", grad, () if red else (M,), torch.float32, at)
     s, empty, workspace = _begin(x, stream)
     dx = empty((M, D), x.dtype, device)
     dtable = empty((V, D), x.dtype, device)

@@ -149,3 +149,56 @@ def test_header_from_c(tmp_path):
     env.pop("CARBON_FAULT", None)
     r = subprocess.run([str(exe)], capture_output=True, text=True, env=env, timeout=120)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr
+
+
+class _Tensor:
+    """What the checks of lm.py look at, of a tensor on any device."""
+
+    def __init__(self, shape, dtype, device):
+        import torch
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device("cuda", device)
+        self.is_cuda = True
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return self.device.index
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        raise AssertionError("the operands reached the library")
+
+    def numel(self):
+        return self.shape.numel()
+
+
+def _calls():
+    """(function, its tensors by name as (shape, dtype), the first operand, further arguments)."""
+    import torch
+    b, f, i, c = torch.bfloat16, torch.float32, torch.int64, torch.int8
+    rows = dict(dy=((4, 8), b), gamma=((8,), b), rstd=((4,), f), dh=((4, 8), b))
+    loss = dict(x=((4, 8), b), table=((5, 8), b), targets=((4,), i))
+    return [
+        (cg.embedding_fwd, dict(table=((5, 8), b), ids=((4,), i)), "table", {}),
+        (cg.embedding_bwd, dict(dy=((4, 8), b), ids=((4,), i), accumulate_to=((5, 8), b)), "dy", dict(num_rows=5)),
+        (cg.rms_norm_fwd, dict(x=((4, 8), b), gamma=((8,), b), residual=((4, 8), b)), "x", {}),
+        (cg.rms_norm_bwd, dict(rows, h=((4, 8), b)), "dy", {}),
+        (cg.rms_norm_bwd, dict(rows, codes=((4, 8), c), scales=((4,), f)), "dy", {}),
+        (cg.rms_norm_expand, dict(codes=((4, 8), c), scales=((4,), f), gamma=((8,), b)), "codes", {}),
+        (cg.linear_cross_entropy_fwd, loss, "x", {}),
+        (cg.linear_cross_entropy_bwd, dict(loss, lse=((4,), f), grad=((), f)), "x", {}),
+    ]
+
+
+def test_operands_on_different_devices_are_refused(monkeypatch):
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    for fn, tensors, first, more in _calls():
+        for away in tensors:
+            args = {k: _Tensor(*v, device=1 if k == away else 0) for k, v in tensors.items()}
+            with pytest.raises(ValueError, match="device"):
+                fn(**args, **more)
