@@ -33,6 +33,7 @@ float16; the tensor-core tier takes bfloat16 or float16).
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -134,6 +135,35 @@ class Linear(torch.nn.Module):
 # ---- the operators around the linear layers -------------------------------------
 
 
+class _NoDerivative(torch.autograd.Function):
+    """Its first n tensors, from all of them; differentiating raises."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the gradients of this package's operators have no derivative of their own")
+
+
+def _once(backward):
+    """A backward pass that can be differentiated once: with create_graph=True
+    its results raise where a second derivative reaches them (as constants,
+    which is what kernels return, they would drop out of it unseen)."""
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        behind = [t for t in (*ctx.saved_tensors, *grads) if t is not None and t.requires_grad]
+        made = [t.detach().requires_grad_() for t in out if t is not None]
+        made = iter(_NoDerivative.apply(len(made), *made, *behind))
+        return tuple(None if t is None else next(made) for t in out)
+    return run
+
+
 class _EmbeddingFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ids, table, scale, padding_idx):
@@ -142,6 +172,7 @@ class _EmbeddingFunction(torch.autograd.Function):
         return embedding_fwd(table, ids, scale)
 
     @staticmethod
+    @_once
     def backward(ctx, grad):
         (ids,) = ctx.saved_tensors
         return None, embedding_bwd(grad.contiguous(), ids, ctx.rows, ctx.scale, ctx.padding_idx), None, None
@@ -201,6 +232,7 @@ class _RmsNormFunction(torch.autograd.Function):
         return (y, r.h.view(x.shape)) if ctx.has_residual else y
 
     @staticmethod
+    @_once
     def backward(ctx, dy, dh=None):
         h, rstd, gamma = ctx.saved_tensors
         D = gamma.shape[0]
@@ -245,6 +277,7 @@ class _NormLinearFunction(torch.autograd.Function):
         return (out, r.h.view(x.shape)) if ctx.has_residual else out
 
     @staticmethod
+    @_once
     def backward(ctx, dout, dh=None):
         codes, scales, rstd, gamma, weight = ctx.saved_tensors
         D = gamma.shape[0]
@@ -283,6 +316,7 @@ class _LinearCrossEntropyFunction(torch.autograd.Function):
         return loss.view(targets.shape) if reduction == "none" else loss
 
     @staticmethod
+    @_once
     def backward(ctx, grad):
         x2, table, t, lse = ctx.saved_tensors
         g = grad.reshape(-1).contiguous() if ctx.reduction == "none" else grad

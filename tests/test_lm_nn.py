@@ -4,6 +4,7 @@ into other rows."""
 import pytest
 import torch
 
+import deterministic_invariant_gemm_fwd_gb300 as cg
 from deterministic_invariant_gemm_fwd_gb300 import nn as cnn
 
 D = 8
@@ -46,3 +47,66 @@ def test_padding_row(padding_idx, row):
     if row is not None:
         want[row] = 0
     assert torch.equal(table.grad.cpu(), want)
+
+
+# ---- the autograd functions with plain CPU stand-ins for the kernels ---------------
+
+def _fwd(x, gamma, residual=None, eps=1e-6, quantize=False):
+    h = x if residual is None else x + residual
+    rstd = (h.square().mean(1) + eps).rsqrt()
+    n = h * rstd[:, None]
+    return cg.RmsNorm(n * gamma, h, rstd, n if quantize else None, torch.ones_like(rstd) if quantize else None)
+
+
+def _bwd(dy, gamma, rstd, h=None, codes=None, scales=None, dh=None, recompute=False):
+    n = codes if h is None else h * rstd[:, None]
+    dx = rstd[:, None] * (gamma * dy - n * (gamma * dy * n).mean(1, keepdim=True)) + (0 if dh is None else dh)
+    return (dx, (dy * n).sum(0)) + ((n * gamma,) if recompute else ())
+
+
+@pytest.fixture
+def stand_ins(monkeypatch):
+    calls = []
+
+    def bwd(*args, **kw):
+        calls.append(kw)
+        return _bwd(*args, **kw)
+
+    monkeypatch.setattr(cnn, "rms_norm_fwd", _fwd)
+    monkeypatch.setattr(cnn, "rms_norm_bwd", bwd)
+    monkeypatch.setattr(cnn, "linear_fwd", lambda x, w, b, tier: x @ w + (0 if b is None else b))
+    monkeypatch.setattr(cnn, "linear_dx", lambda g, w, tier: g @ w.t())
+    monkeypatch.setattr(cnn, "linear_dw", lambda x, g, tier: x.t() @ g)
+    monkeypatch.setattr(cnn, "bias_grad", lambda g, tier: g.sum(0))
+    monkeypatch.setattr(cnn, "embedding_fwd", lambda table, ids, scale: scale * table[ids])
+    monkeypatch.setattr(cnn, "embedding_bwd", lambda dy, ids, rows, scale, pad: scale * torch.zeros(
+        rows, dy.shape[-1]).index_add_(0, ids.reshape(-1), dy.reshape(-1, dy.shape[-1])))
+    monkeypatch.setattr(cnn, "linear_cross_entropy_fwd", lambda x, w, t, i, r: (
+        torch.nn.functional.cross_entropy(x @ w.t(), t, ignore_index=i, reduction=r), torch.logsumexp(x @ w.t(), 1)))
+    monkeypatch.setattr(cnn, "linear_cross_entropy_bwd", lambda g, x, w, t, lse, i, r: (
+        torch.zeros_like(x) + g.sum(), torch.zeros_like(w) + g.sum()))
+    return calls
+
+
+def _leaves(*shapes):
+    g = torch.Generator().manual_seed(1)
+    return [torch.randn(s, generator=g).requires_grad_() for s in shapes]
+
+
+def test_gradients_of_gradients_raise(stand_ins):
+    """Also where the incoming gradient is a constant, as a loss's is."""
+    x, res, gamma, w, b, table = _leaves((4, D), (4, D), (D,), (D, 3), (3,), (5, D))
+    ids = torch.tensor([0, 4, 4, 1])
+    cases = [(lambda: cnn.embedding(ids, table), [table]), (lambda: cnn.rms_norm(x, gamma), [x, gamma]),
+             (lambda: cnn.rms_norm(x, gamma, res)[0], [x, res, gamma]),
+             (lambda: cnn.norm_linear(x, gamma, w, b), [x, gamma, w, b]),
+             (lambda: cnn.linear_cross_entropy(x, table, ids), [x, table])]
+    for make, leaves in cases:
+        for power in (1, 2):
+            for k in range(len(leaves)):
+                out = make().pow(power).sum()
+                g = torch.autograd.grad(out, leaves, create_graph=True)
+                plain = torch.autograd.grad(make().pow(power).sum(), leaves)
+                assert all(torch.equal(a, p) for a, p in zip(g, plain))
+                with pytest.raises(RuntimeError, match="no derivative"):
+                    (out + g[k].square().sum()).backward()
