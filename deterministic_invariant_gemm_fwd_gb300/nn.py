@@ -228,6 +228,7 @@ class _RmsNormFunction(torch.autograd.Function):
         r = rms_norm_fwd(_flat(x, D), gamma, None if residual is None else _flat(residual, D), eps)
         ctx.save_for_backward(r.h, r.rstd, gamma)
         ctx.shape, ctx.has_residual = x.shape, residual is not None
+        ctx.set_materialize_grads(False)        # an output that goes nowhere: None, not a tensor of zeros
         y = r.y.view(x.shape)
         return (y, r.h.view(x.shape)) if ctx.has_residual else y
 
@@ -236,6 +237,8 @@ class _RmsNormFunction(torch.autograd.Function):
     def backward(ctx, dy, dh=None):
         h, rstd, gamma = ctx.saved_tensors
         D = gamma.shape[0]
+        if dy is None:                          # only the residual stream goes on
+            return dh, dh if ctx.has_residual else None, torch.zeros_like(gamma), None
         dx, dgamma = rms_norm_bwd(_flat(dy, D), gamma, rstd, h=h, dh=None if dh is None else _flat(dh, D))
         dx = dx.view(ctx.shape)
         return dx, dx if ctx.has_residual else None, dgamma, None
@@ -273,6 +276,7 @@ class _NormLinearFunction(torch.autograd.Function):
         out = linear_fwd(r.y, weight, bias, tier)
         ctx.save_for_backward(r.codes, r.scales, r.rstd, gamma, weight)
         ctx.shape, ctx.tier, ctx.has_bias, ctx.has_residual = x.shape, tier, bias is not None, residual is not None
+        ctx.set_materialize_grads(False)
         out = out.view(*x.shape[:-1], weight.shape[1])
         return (out, r.h.view(x.shape)) if ctx.has_residual else out
 
@@ -281,6 +285,9 @@ class _NormLinearFunction(torch.autograd.Function):
     def backward(ctx, dout, dh=None):
         codes, scales, rstd, gamma, weight = ctx.saved_tensors
         D = gamma.shape[0]
+        if dout is None:
+            db = weight.new_zeros(weight.shape[1]) if ctx.has_bias else None
+            return dh, dh if ctx.has_residual else None, torch.zeros_like(gamma), torch.zeros_like(weight), db, None, None
         g = _flat(dout, weight.shape[1])
         dy = linear_dx(g, weight, ctx.tier)
         dx, dgamma, y = rms_norm_bwd(dy, gamma, rstd, codes=codes, scales=scales,

@@ -110,3 +110,28 @@ def test_gradients_of_gradients_raise(stand_ins):
                 assert all(torch.equal(a, p) for a, p in zip(g, plain))
                 with pytest.raises(RuntimeError, match="no derivative"):
                     (out + g[k].square().sum()).backward()
+
+
+@pytest.mark.parametrize("layer", ["norm", "norm_linear"])
+def test_outputs_that_go_nowhere(stand_ins, layer):
+    """The last norm's residual stream has no gradient: none is made up and
+    read.  Nor does a norm of which only the residual stream goes on run its
+    gradient; what it would have given is zero."""
+    shapes = [(2, 3, D), (2, 3, D), (D,)] + ([(D, 4), (4,)] if layer == "norm_linear" else [])
+
+    def grads(used, other):
+        leaves = _leaves(*shapes)
+        x, res, gamma, *rest = leaves
+        outs = cnn.norm_linear(x, gamma, *rest, residual=res) if rest else cnn.rms_norm(x, gamma, res)
+        total = outs[used].sum()
+        (total + other * outs[1 - used].sum() if other is not None else total).backward()
+        return [leaf.grad for leaf in leaves]
+
+    for used in (0, 1):
+        stand_ins.clear()
+        alone = grads(used, None)
+        assert [c["dh"] for c in stand_ins] == ([None] if used == 0 else [])
+        stand_ins.clear()
+        both = grads(used, 0.0)
+        assert len(stand_ins) == 1 and stand_ins[0]["dh"] is not None
+        assert all(a.shape == b.shape and torch.equal(a, b) for a, b in zip(alone, both))
