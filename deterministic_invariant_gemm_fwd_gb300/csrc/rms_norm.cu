@@ -381,7 +381,8 @@ norm_fwd_ring_kernel(const FwdArgs<T> a, const int stages) {
 }
 
 // Rows that do not fit a group's registers: a CTA per row, the row read again
-// for each pass.
+// for each pass.  The last pass alone writes, each thread the elements that it
+// reads, so that y or h_out may lie over x or residual.
 template <typename T>
 __global__ void __launch_bounds__(512)
 norm_fwd_long_kernel(const FwdArgs<T> a) {
@@ -401,19 +402,21 @@ norm_fwd_long_kernel(const FwdArgs<T> a) {
         ss = group_sum<512>(ss, buf);
         const float rstd = rsqrtf(__fdiv_rn(ss, (float)a.D) + a.eps);
         if (a.rstd && threadIdx.x == 0) a.rstd[m] = rstd;
-        uint32_t top = 0u;
+        float factor = 0.0f;
+        if (a.codes) {
+            uint32_t top = 0u;
+            for (int64_t j = threadIdx.x; j < a.D; j += 512) top = max(top, magnitude(h_at(j) * rstd));
+            top = group_max<512>(top, reinterpret_cast<uint32_t *>(buf));
+            float scale;
+            code_scale(top, &scale, &factor);
+            if (threadIdx.x == 0) a.scales[m] = scale;
+        }
         for (int64_t j = threadIdx.x; j < a.D; j += 512) {
             const float h = h_at(j);
             if (a.h_out) a.h_out[row + j] = from_f32<T>(h);
             a.y[row + j] = from_f32<T>(h * rstd * to_f32(a.gamma[j]));
-            top = max(top, magnitude(h * rstd));
+            if (a.codes) a.codes[row + j] = code_of(h * rstd, factor);
         }
-        if (!a.codes) continue;
-        top = group_max<512>(top, reinterpret_cast<uint32_t *>(buf));
-        float scale, factor;
-        code_scale(top, &scale, &factor);
-        if (threadIdx.x == 0) a.scales[m] = scale;
-        for (int64_t j = threadIdx.x; j < a.D; j += 512) a.codes[row + j] = code_of(h_at(j) * rstd, factor);
     }
 }
 

@@ -79,7 +79,8 @@ int64_t carbon_embedding_bwd_workspace(int64_t M, int64_t V, int64_t D);
  * to the nearest integer (n times the fp32 quotient 127 / max).  A row whose
  * maximum is below 2^-100 has scale 0 and codes 0; a row with a NaN or an
  * infinity has scale NaN and codes 0, so that it reads back as NaN.
- * gamma[D].  D = 0 or M = 0: nothing to do. */
+ * y and h_out may each lie over x or residual (the same address); else no
+ * operands overlap.  gamma[D].  D = 0 or M = 0: nothing to do. */
 carbon_status_t carbon_rms_norm_fwd(void *y, void *h_out, float *rstd, int8_t *codes, float *scales,
                                     const void *x, const void *residual, const void *gamma,
                                     int64_t M, int64_t D, float eps, carbon_dtype_t dtype,
@@ -93,8 +94,8 @@ carbon_status_t carbon_rms_norm_fwd(void *y, void *h_out, float *rstd, int8_t *c
  *
  * dh: the gradient that reaches h along the residual stream, or NULL.
  * dgamma may be NULL.  y_out (may be NULL): y = n * gamma once more, e.g. for
- * the weight gradient of the linear layer that took y.  dx may not overlap
- * another operand, except dx == dh.  Workspace: carbon_rms_norm_bwd_workspace
+ * the weight gradient of the linear layer that took y.  dx and y_out may not
+ * overlap another operand, except dx == dh.  Workspace: carbon_rms_norm_bwd_workspace
  * bytes (the partial sums of dgamma). */
 carbon_status_t carbon_rms_norm_bwd(void *dx, void *dgamma, void *y_out, const void *dy,
                                     const void *h, const int8_t *codes, const float *scales,
