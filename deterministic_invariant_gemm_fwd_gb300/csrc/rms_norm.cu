@@ -28,6 +28,7 @@
 #include "bounds.cuh"
 #include "device_sync.cuh"
 #include "rowvec.cuh"
+#include "tcgen05.cuh"
 
 #include <type_traits>
 
@@ -153,6 +154,9 @@ __device__ __forceinline__ void start_row(const Rows (&t)[K], int count, int64_t
             for (const uint8_t *b = b0 + lane; b < (lo < b1 ? lo : b1); b += 32) place[b - b0] = *b;
             for (const uint8_t *b = (hi > b0 ? hi : b0) + lane; b < b1; b += 32)
                 if (b >= lo) place[b - b0] = *b;
+            // the stage's next row may come here by a bulk copy: ordered after
+            // these writes
+            fence_proxy_async_smem();
         }
         if (hi > lo) bytes += (uint32_t)(hi - lo);
     }

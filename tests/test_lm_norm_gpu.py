@@ -29,3 +29,28 @@ def test_forward_over_its_own_operands(D, dtype, over):
     assert status() == 0
     for a, b in zip((y, h, rstd, codes, scales), want):
         assert same_bits(a, b)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("M,D", [(5000, 1), (5000, 3), (4000, 1001), (700, 4099)])
+def test_odd_rows_at_any_offset(M, D, dtype):
+    """Rows that no 16-byte vector fits give the same bits wherever the tensors
+    start: the pieces at both ends that bulk copies cannot take, and what
+    follows them in their place."""
+    g, dt = gen(M + D), DT[dtype]
+    x, res, dy, gamma = (randn(g, *s, dtype=dt) for s in ((M, D), (M, D), (M, D), (D,)))
+    want = cg.rms_norm_fwd(x, gamma, res, 1e-5, quantize=True)
+    grads = [cg.rms_norm_bwd(dy, gamma, want.rstd, dh=res, recompute=True, **k)
+             for k in (dict(h=want.h), dict(codes=want.codes, scales=want.scales))]
+
+    def at(t, offset):
+        room = torch.empty(t.numel() + offset, dtype=t.dtype, device="cuda")[offset:].view(t.shape)
+        return room.copy_(t)
+
+    for offset in (1, 2, 5):
+        r = cg.rms_norm_fwd(at(x, offset), at(gamma, offset), at(res, offset), 1e-5, quantize=True)
+        assert all(same_bits(a, b) for a, b in zip(r, want))
+        for k, ref in zip((dict(h=at(want.h, offset)), dict(codes=at(want.codes, offset), scales=want.scales)), grads):
+            got = cg.rms_norm_bwd(at(dy, offset), at(gamma, offset), want.rstd, dh=at(res, offset), recompute=True, **k)
+            assert all(same_bits(a, b) for a, b in zip(got, ref))
+    assert status() == 0
