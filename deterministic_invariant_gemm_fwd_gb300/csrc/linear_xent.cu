@@ -1080,8 +1080,9 @@ cudaError_t encode_blocks(CUtensorMap *m, const void *base, int64_t n, int group
 
 bool sizes_ok(int64_t M, int64_t D, int64_t V) {
     int64_t t;
-    // tile coordinates and counters are 32-bit; element counts are 64-bit
-    return M >= 0 && D >= 0 && V >= 0 && M < (1ll << 30) && D < (1ll << 22) && V < (1ll << 30) &&
+    // tile coordinates and counters are 32-bit; element counts are 64-bit; a
+    // launch has up to 65535 column blocks of 64
+    return M >= 0 && D >= 0 && V >= 0 && M < (1ll << 30) && D <= 65535ll * 64 && V < (1ll << 30) &&
            !__builtin_mul_overflow(M, D, &t) && !__builtin_mul_overflow(t, (int64_t)16, &t) &&
            !__builtin_mul_overflow(V, D, &t) && !__builtin_mul_overflow(t, (int64_t)16, &t);
 }

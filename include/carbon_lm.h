@@ -123,8 +123,10 @@ carbon_status_t carbon_rms_norm_expand(void *out, const int8_t *codes, const flo
  * and neither they nor their x (NaN included) reach any other result.
  *
  * dtype: CARBON_BF16 or CARBON_F16 (CARBON_F32: CARBON_ERR_UNSUPPORTED, as
- * on the tensor-core tier).  Pointers 16-byte aligned and D a multiple of 8,
- * else CARBON_ERR_MISALIGNED.  V, M: any (V >= 1 where M > 0). */
+ * on the tensor-core tier).  x, table, dx and dtable 16-byte aligned and D a
+ * multiple of 8, else CARBON_ERR_MISALIGNED.  M, V < 2^30, D <= 4194240 and fewer
+ * than 2^31 tiles of 256 x 128 among the logits, else
+ * CARBON_ERR_INVALID_ARG (as for V = 0 or D = 0 where M > 0). */
 typedef enum {
     CARBON_REDUCE_NONE = 0,     /* a loss per position */
     CARBON_REDUCE_SUM = 1,      /* their sum */

@@ -202,3 +202,14 @@ def test_operands_on_different_devices_are_refused(monkeypatch):
             args = {k: _Tensor(*v, device=1 if k == away else 0) for k, v in tensors.items()}
             with pytest.raises(ValueError, match="device"):
                 fn(**args, **more)
+
+
+@pytest.mark.parametrize("call", [xent_fwd, xent_bwd])
+def test_xent_widest_rows(call, monkeypatch):
+    """The launch's limit of column blocks is the widest row: more is refused
+    before anything is launched."""
+    monkeypatch.setenv("CARBON_FAULT", "launch")
+    assert call(D=65535 * 64, M=1, V=1) == CUDA_ERR              # past the checks
+    assert call(D=65535 * 64 + 8, M=1, V=1) == INVALID
+    query = b.carbon_linear_xent_fwd_workspace if call is xent_fwd else b.carbon_linear_xent_bwd_workspace
+    assert query(1, 65535 * 64, 1) > 0 and query(1, 65535 * 64 + 8, 1) == -1
