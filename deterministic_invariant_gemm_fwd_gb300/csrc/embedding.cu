@@ -598,6 +598,7 @@ carbon_status_t carbon_embedding_fwd(void *out, const void *table, const int64_t
     if (dtype != CARBON_F32 && dtype != CARBON_BF16 && dtype != CARBON_F16) return CARBON_ERR_INVALID_ARG;
     if (M == 0 || D == 0) return CARBON_OK;
     if (!out || !ids || (V > 0 && !table)) return CARBON_ERR_INVALID_ARG;
+    if (!aligned_to(dtype_size(dtype), out, table) || !aligned_to(8, ids)) return CARBON_ERR_MISALIGNED;
     carbon_status_t st = injected_launch_failure();
     if (st != CARBON_OK) return st;
     if ((st = current_device(nullptr, nullptr)) != CARBON_OK) return st;
@@ -632,6 +633,7 @@ carbon_status_t carbon_embedding_bwd(void *dtable, const void *dy, const int64_t
     const SortPlan plan = make_plan(M, V);
     Workspace w;
     if (M > 0 && workspace_bytes < lay_out(&w, workspace, M, V, D, plan)) return CARBON_ERR_INVALID_ARG;
+    if (!aligned_to(dtype_size(dtype), dtable, dy) || !aligned_to(8, ids)) return CARBON_ERR_MISALIGNED;
     carbon_status_t st = injected_launch_failure();
     if (st != CARBON_OK) return st;
     if ((st = current_device(nullptr, nullptr)) != CARBON_OK) return st;

@@ -1184,6 +1184,7 @@ carbon_status_t carbon_linear_xent_fwd(float *losses, float *total, float *lse, 
     if (M > 0 && (!losses || !lse || !workspace || !aligned16(workspace) ||
                   workspace_bytes < carbon_linear_xent_fwd_workspace(M, D, V)))
         return CARBON_ERR_INVALID_ARG;
+    if (!aligned_to(4, losses, total, lse) || !aligned_to(8, count, targets)) return CARBON_ERR_MISALIGNED;
     if ((st = injected_launch_failure()) != CARBON_OK) return st;
     int sms = 0;
     if ((st = current_device(nullptr, &sms)) != CARBON_OK) return st;
@@ -1221,6 +1222,7 @@ carbon_status_t carbon_linear_xent_bwd(void *dx, void *dtable, const float *grad
     if (M > 0 && (!dx || !grad || !lse || !workspace || !aligned16(workspace) ||
                   workspace_bytes < carbon_linear_xent_bwd_workspace(M, D, V)))
         return CARBON_ERR_INVALID_ARG;
+    if (!aligned_to(4, grad, lse) || !aligned_to(8, targets)) return CARBON_ERR_MISALIGNED;
     if (V * D == 0) return CARBON_OK;                     // then M == 0
     if ((st = injected_launch_failure()) != CARBON_OK) return st;
     int sms = 0;

@@ -896,6 +896,8 @@ carbon_status_t carbon_rms_norm_fwd(void *y, void *h_out, float *rstd, int8_t *c
     if ((codes == nullptr) != (scales == nullptr)) return CARBON_ERR_INVALID_ARG;
     if (M == 0 || D == 0) return CARBON_OK;
     if (!y || !x || !gamma) return CARBON_ERR_INVALID_ARG;
+    if (!aligned_to(dtype_size(dtype), y, h_out, x, residual, gamma) || !aligned_to(4, rstd, scales))
+        return CARBON_ERR_MISALIGNED;
     const carbon_status_t st = ready();
     if (st != CARBON_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -924,6 +926,8 @@ carbon_status_t carbon_rms_norm_bwd(void *dx, void *dgamma, void *y_out, const v
         if (dgamma && (!workspace || !aligned16(workspace) || workspace_bytes < carbon_rms_norm_bwd_workspace(M, D)))
             return CARBON_ERR_INVALID_ARG;
     }
+    if (!aligned_to(dtype_size(dtype), dx, dgamma, y_out, dy, h, gamma, dh) || !aligned_to(4, scales, rstd))
+        return CARBON_ERR_MISALIGNED;
     const carbon_status_t st = ready();
     if (st != CARBON_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -941,6 +945,7 @@ carbon_status_t carbon_rms_norm_expand(void *out, const int8_t *codes, const flo
     if (!sizes_ok(M, D) || !dtype_ok(dtype)) return CARBON_ERR_INVALID_ARG;
     if (M == 0 || D == 0) return CARBON_OK;
     if (!out || !codes || !scales) return CARBON_ERR_INVALID_ARG;
+    if (!aligned_to(dtype_size(dtype), out, gamma) || !aligned_to(4, scales)) return CARBON_ERR_MISALIGNED;
     const carbon_status_t st = ready();
     if (st != CARBON_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -64,7 +64,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 __device__ __forceinline__ uint32_t warp_max_u32(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 
-inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether every pointer (null ones too) is a multiple of `size`, a power of two.
+template <typename... P>
+inline bool aligned_to(size_t size, const P *...p) {
+    return (((0 | ... | reinterpret_cast<uintptr_t>(p)) & (size - 1)) == 0);
+}
+inline bool aligned16(const void *p) { return aligned_to(16, p); }
 
 inline size_t dtype_size(int dtype) { return dtype == CARBON_F32 ? 4 : 2; }
 

@@ -133,7 +133,7 @@ typedef enum {
     CARBON_OK = 0,
     CARBON_ERR_INVALID_ARG = 1,   /* bad size, pointer, dtype or tier */
     CARBON_ERR_UNSUPPORTED = 2,   /* device or dtype/tier combination */
-    CARBON_ERR_MISALIGNED = 3,    /* TC tier: pointer/pitch not 16-byte aligned */
+    CARBON_ERR_MISALIGNED = 3,    /* TC tier: pointer/pitch not 16-byte aligned; carbon_lm.h: as stated there */
     CARBON_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed */
     CARBON_ERR_TIMEOUT = 5,       /* a bounded device-side wait gave up */
     CARBON_ERR_SCRATCH_LIMIT = 6, /* needs more than the fixed no-allocation workspace */

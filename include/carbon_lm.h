@@ -17,7 +17,8 @@
  *
  * Sums, norms and softmax statistics are held in fp32; each output is rounded
  * once, to nearest-even.  dtype is that of every 16- or 32-bit operand and
- * output unless a type is named.
+ * output unless a type is named.  Pointers that are not multiples of their
+ * element's size: CARBON_ERR_MISALIGNED.
  *
  * Workspace: where a function takes one, the caller passes a 16-byte aligned
  * device buffer of at least the bytes that its _workspace query returns; the

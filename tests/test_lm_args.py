@@ -213,3 +213,32 @@ def test_xent_widest_rows(call, monkeypatch):
     assert call(D=65535 * 64 + 8, M=1, V=1) == INVALID
     query = b.carbon_linear_xent_fwd_workspace if call is xent_fwd else b.carbon_linear_xent_bwd_workspace
     assert query(1, 65535 * 64, 1) > 0 and query(1, 65535 * 64 + 8, 1) == -1
+
+
+# a pointer that is no multiple of its element's size would fault in a kernel
+ODD = [(embed_fwd, "out table"), (embed_bwd, "dtable dy"), (norm_fwd, "y h x res gamma"),
+       (norm_bwd, "dx dgamma y dy h gamma dh"), (expand, "out gamma")]
+WIDE = [(embed_fwd, dict(ids=8)), (embed_bwd, dict(ids=8)), (norm_fwd, dict(rstd=4)), (norm_bwd, dict(rstd=4)),
+        (expand, dict(scales=4)), (xent_fwd, dict(losses=4, total=4, lse=4, count=8, targets=8)),
+        (xent_bwd, dict(grad=4, lse=4, targets=8))]
+
+
+@pytest.mark.parametrize("call,names", ODD, ids=lambda v: v.__name__ if callable(v) else "")
+def test_pointers_between_elements_are_refused(call, names, monkeypatch):
+    monkeypatch.setenv("CARBON_FAULT", "launch")
+    for dtype, size in ((0, 4), (1, 2), (2, 2)):
+        for name in names.split():
+            assert call(**{name: P + size // 2, "dtype": dtype}) == MISALIGNED, name
+            assert call(**{name: P + size, "dtype": dtype}) == CUDA_ERR, name      # elements need no more
+
+
+@pytest.mark.parametrize("call,names", WIDE, ids=lambda v: v.__name__ if callable(v) else "")
+def test_pointers_between_wider_elements_are_refused(call, names, monkeypatch):
+    monkeypatch.setenv("CARBON_FAULT", "launch")
+    for name, size in names.items():
+        assert call(**{name: P + size // 2}) == MISALIGNED, name
+        assert call(**{name: P + size}) == CUDA_ERR, name
+    if call in (norm_fwd, norm_bwd):
+        source = dict(h=None) if call is norm_bwd else {}
+        assert call(codes=P + 1, scales=P + 4, **source) == CUDA_ERR
+        assert call(codes=P + 1, scales=P + 2, **source) == MISALIGNED
