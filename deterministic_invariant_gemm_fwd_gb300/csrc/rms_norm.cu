@@ -893,9 +893,8 @@ carbon_status_t carbon_rms_norm_fwd(void *y, void *h_out, float *rstd, int8_t *c
                                     const void *x, const void *residual, const void *gamma, int64_t M, int64_t D,
                                     float eps, carbon_dtype_t dtype, carbon_stream_t stream) {
     if (!sizes_ok(M, D) || !dtype_ok(dtype) || !(eps >= 0.0f)) return CARBON_ERR_INVALID_ARG;
-    if ((codes == nullptr) != (scales == nullptr)) return CARBON_ERR_INVALID_ARG;
     if (M == 0 || D == 0) return CARBON_OK;
-    if (!y || !x || !gamma) return CARBON_ERR_INVALID_ARG;
+    if (!y || !x || !gamma || (codes == nullptr) != (scales == nullptr)) return CARBON_ERR_INVALID_ARG;
     if (!aligned_to(dtype_size(dtype), y, h_out, x, residual, gamma) || !aligned_to(4, rstd, scales))
         return CARBON_ERR_MISALIGNED;
     const carbon_status_t st = ready();

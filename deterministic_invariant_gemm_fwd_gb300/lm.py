@@ -167,6 +167,11 @@ def rms_norm_fwd(x, gamma, residual=None, eps=1e-6, quantize=False, stream=None)
                                     _p(scales), x.data_ptr(), _p(residual), gamma.data_ptr(), M, D, eps, code, s)
     if st:
         _b._check(st, "carbon_rms_norm_fwd")
+    if D == 0:                                   # no elements, no kernel: the mean of nothing, codes of nothing
+        with torch.cuda.stream(torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()):
+            rstd.fill_(float("nan"))
+            if quantize:
+                scales.zero_()
     return RmsNorm(y, h, rstd, codes, scales)
 
 

@@ -54,3 +54,21 @@ def test_odd_rows_at_any_offset(M, D, dtype):
             got = cg.rms_norm_bwd(at(dy, offset), at(gamma, offset), want.rstd, dh=at(res, offset), recompute=True, **k)
             assert all(same_bits(a, b) for a, b in zip(got, ref))
     assert status() == 0
+
+
+@pytest.mark.parametrize("other_stream", [False, True])
+def test_rows_without_elements(other_stream):
+    """No statistics are left unwritten: the mean of nothing is NaN."""
+    stream = torch.cuda.Stream() if other_stream else None
+    for _ in range(3):
+        junk = torch.full((512,), 7.0, device="cuda")
+        torch.cuda.synchronize()
+        del junk
+        x, gamma = torch.empty(5, 0, device="cuda"), torch.empty(0, device="cuda")
+        r = cg.rms_norm_fwd(x, gamma, x, quantize=True, stream=stream)
+        torch.cuda.synchronize()
+        assert r.y.shape == r.h.shape == r.codes.shape == (5, 0)
+        assert bool(torch.isnan(r.rstd).all()) and not bool(r.scales.any())
+        dx, dgamma = cg.rms_norm_bwd(x, gamma, r.rstd, h=r.h)
+        assert dx.shape == (5, 0) and dgamma.shape == (0,)
+    assert status() == 0
