@@ -32,8 +32,9 @@
 // in the trace: loss 297 us, 2.1 PFLOP/s, the tensor pipe active in 87% of the
 // cycles; gradients 1.03 ms, 1.85 PFLOP/s, 78%: G passes through HBM about
 // once each way, and operands arrive late at times.  Called again and again
-// they run into the power limit: 359 us and 1.64 ms for both.  One position:
-// the table's bytes, 77 MB in 26 us.
+// they run into the power limit: 359 us, and 1.63 ms for both directions (the
+// times of calls below are those of short bursts, before it is reached).  One
+// position: the table's bytes, 77 MB in 26 us.
 #include "bounds.cuh"
 #include "device_sync.cuh"
 #include "rowvec.cuh"
@@ -164,7 +165,10 @@ xent_count_kernel(const Plan p, const ScanArgs a) {
 // order, into x's blocks, with zeros up to the last tile's end and past D; the
 // CTAs of the first columns also write what the tiles need of each position,
 // and the zeros of ignored ones.  Without `ahead` a CTA counts the positions
-// before its own by itself (up to kCountAhead of them: 1 us, a launch less).
+// before its own by itself, up to kCountAhead of them: a launch less, and less
+// time (16384 positions of width 768, cold: 24 us, with `ahead` 10 and 23 for
+// the counting kernel; every block of columns counts, so at width 8192 it is
+// 150 against 82 and 23).
 constexpr int kPrepThreads = 256;
 
 __global__ void __launch_bounds__(kPrepThreads)

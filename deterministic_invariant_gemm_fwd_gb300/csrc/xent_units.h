@@ -19,7 +19,8 @@ constexpr unsigned kDone = 2;                         // reports of a finished u
 
 constexpr int kGroup = 128;              // vocabulary entries per (max, sum) pair
 // Vocabulary entries per piece.  With 2048 dx adds twice as many sums
-// (8192 x 768 x 50257, the loss and its gradients: 1.77 ms instead of 1.54);
+// (8192 x 768 x 50257, the loss and its gradients in short bursts: 1.77 ms
+// instead of 1.54);
 // 8192 took 1.50 with twice the memory for G.
 constexpr int kPiece = 4096;
 // G has room for pieces up to this size, and at least for those in use: half

@@ -134,7 +134,12 @@ typedef enum {
     CARBON_REDUCE_MEAN = 2      /* their sum / max(positions that count, 1) */
 } carbon_reduce_t;
 
-/* losses: fp32 [M].  total: fp32 [1], the sum or mean (fixed order), NULL for
+/* Errors: a logit is within D 2^-23 sum_j |x_j w_j| of the exact one (exact
+ * products, the tensor cores' fp32 accumulator); lse within the largest of these
+ * of its row plus (16 + log2 V) 2^-23 (|lse| + |z| + 1), z the target's logit; a
+ * loss within twice the former plus the latter.
+ *
+ * losses: fp32 [M].  total: fp32 [1], the sum or mean (fixed order), NULL for
  * CARBON_REDUCE_NONE.  lse: fp32 [M].  count: int64 [1], the number of
  * positions that count.  Workspace: carbon_linear_xent_fwd_workspace bytes. */
 carbon_status_t carbon_linear_xent_fwd(float *losses, float *total, float *lse, int64_t *count,
