@@ -21,8 +21,11 @@ cross entropy, and their gradients) are ``embedding_fwd`` / ``_bwd``,
 """
 from __future__ import annotations
 
-from ._binding import (carbon_embedding_bwd,  # noqa: F401
+from ._binding import (carbon_clip_grads, carbon_clip_grads_workspace,  # noqa: F401
+                       carbon_embedding_bwd,
                        carbon_embedding_bwd_workspace, carbon_embedding_fwd,
+                       carbon_linear_logp_bwd, carbon_linear_logp_bwd_workspace,
+                       carbon_linear_logp_fwd, carbon_linear_logp_fwd_workspace,
                        carbon_linear_xent_bwd, carbon_linear_xent_bwd_workspace,
                        carbon_linear_xent_fwd, carbon_linear_xent_fwd_workspace,
                        carbon_rms_norm_bwd, carbon_rms_norm_bwd_workspace,
@@ -38,8 +41,8 @@ from ._binding import (CarbonError, carbon_abi_version, carbon_debug_exact_y64, 
                        carbon_get_device_status, carbon_measure_fp64_rate,
                        carbon_measure_int_mac_rate,
                        carbon_status_string)
-from .lm import (RmsNorm, embedding_bwd, embedding_fwd, linear_cross_entropy_bwd,  # noqa: F401
-                 linear_cross_entropy_fwd, rms_norm_bwd, rms_norm_expand, rms_norm_fwd)
+from .lm import (LogProbs, RmsNorm, clip_grads, embedding_bwd, embedding_fwd, grad_norm, linear_cross_entropy_bwd,  # noqa: F401
+                 linear_cross_entropy_fwd, linear_log_probs_bwd, linear_log_probs_fwd, rms_norm_bwd, rms_norm_expand, rms_norm_fwd)
 
 
 def _dtype_code(t):

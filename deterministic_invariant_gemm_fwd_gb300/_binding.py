@@ -67,6 +67,9 @@ def _load() -> ctypes.CDLL:
         "carbon_rms_norm_expand": [vp, vp, vp, vp, i64, i64, i32, vp],
         "carbon_linear_xent_fwd": [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, vp, i64, i32, vp],
         "carbon_linear_xent_bwd": [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, vp, i64, i32, vp],
+        "carbon_linear_logp_fwd": [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, f32, i64, vp, i64, i32, vp],
+        "carbon_linear_logp_bwd": [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, f32, i64, vp, i64, i32, vp],
+        "carbon_clip_grads": [vp, vp, vp, vp, vp, i64, f32, f32, vp, i64, vp],
         "carbon_debug_exact_y64": [i32, vp, vp, vp, vp, i64, i64, i64, i32, vp],
         "carbon_debug_tc_f32": [i32, vp, vp, vp, vp, i64, i64, i64, vp],
         "carbon_debug_round": [i32, vp, vp, i64, vp],
@@ -83,6 +86,12 @@ def _load() -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.argtypes = [i64] * (2 if "rms_norm" in name else 3)
         fn.restype = i64
+    lib.carbon_linear_logp_fwd_workspace.argtypes = [i64] * 4
+    lib.carbon_linear_logp_fwd_workspace.restype = i64
+    lib.carbon_linear_logp_bwd_workspace.argtypes = [i64] * 3
+    lib.carbon_linear_logp_bwd_workspace.restype = i64
+    lib.carbon_clip_grads_workspace.argtypes = [vp, i64]
+    lib.carbon_clip_grads_workspace.restype = i64
     lib.carbon_status_string.argtypes = [i32]
     lib.carbon_status_string.restype = ctypes.c_char_p
     lib.carbon_last_cuda_error.argtypes = []
@@ -283,6 +292,44 @@ def carbon_linear_xent_bwd(dx, dtable, grad, x, table, targets, lse, M, D, V, ig
 
 def carbon_linear_xent_bwd_workspace(M, D, V) -> int:
     return int(_lib().carbon_linear_xent_bwd_workspace(M, D, V))
+
+
+def carbon_linear_logp_fwd(log_probs, entropy, lse, top_ids, top_log_probs, x, table, tokens, M, D, V, top,
+                           temperature, ignore_index, workspace, workspace_bytes, dtype, stream=None) -> None:
+    """Log probabilities of tokens under x . table^T / temperature, entropy and top alternatives."""
+    _check(_lib().carbon_linear_logp_fwd(_ptr(log_probs), _ptr(entropy), _ptr(lse), _ptr(top_ids), _ptr(top_log_probs),
+                                         _ptr(x), _ptr(table), _ptr(tokens), M, D, V, top, temperature, ignore_index,
+                                         _ptr(workspace), workspace_bytes, _code(DTYPES, dtype), _stream(stream)),
+           "carbon_linear_logp_fwd")
+
+
+def carbon_linear_logp_fwd_workspace(M, D, V, top) -> int:
+    return int(_lib().carbon_linear_logp_fwd_workspace(M, D, V, top))
+
+
+def carbon_linear_logp_bwd(dx, dtable, grad_log_probs, grad_entropy, x, table, tokens, lse, entropy, M, D, V,
+                           temperature, ignore_index, workspace, workspace_bytes, dtype, stream=None) -> None:
+    """Gradients of carbon_linear_logp_fwd with respect to x and the table."""
+    _check(_lib().carbon_linear_logp_bwd(_ptr(dx), _ptr(dtable), _ptr(grad_log_probs), _ptr(grad_entropy), _ptr(x),
+                                         _ptr(table), _ptr(tokens), _ptr(lse), _ptr(entropy), M, D, V, temperature,
+                                         ignore_index, _ptr(workspace), workspace_bytes, _code(DTYPES, dtype),
+                                         _stream(stream)), "carbon_linear_logp_bwd")
+
+
+def carbon_linear_logp_bwd_workspace(M, D, V) -> int:
+    return int(_lib().carbon_linear_logp_bwd_workspace(M, D, V))
+
+
+def carbon_clip_grads(norm, out, grads, sizes, dtypes, count, max_norm, eps, workspace, workspace_bytes,
+                      stream=None) -> None:
+    """Norm of all gradients and their clipping; out, grads, sizes and dtypes
+    are addresses of host arrays (void *, void *, int64, int)."""
+    _check(_lib().carbon_clip_grads(_ptr(norm), out, grads, sizes, dtypes, count, max_norm, eps, _ptr(workspace),
+                                    workspace_bytes, _stream(stream)), "carbon_clip_grads")
+
+
+def carbon_clip_grads_workspace(sizes, count) -> int:
+    return int(_lib().carbon_clip_grads_workspace(sizes, count))
 
 
 def carbon_get_device_status(stream=None) -> int:

@@ -269,6 +269,8 @@ carbon_status_t carbon_get_device_status(carbon_stream_t stream) {
     const carbon_status_t em = carbon::embedding_take_device_status();
     const carbon_status_t no = carbon::norm_take_device_status();
     const carbon_status_t xe = carbon::xent_take_device_status();
+    const carbon_status_t lp = carbon::logp_take_device_status();
+    const carbon_status_t cl = carbon::clip_take_device_status();
     if (st != CARBON_OK) return st;
     if (tc != CARBON_OK) return tc;
     if (ex != CARBON_OK) return ex;
@@ -278,6 +280,8 @@ carbon_status_t carbon_get_device_status(carbon_stream_t stream) {
     if (em != CARBON_OK) return em;
     if (no != CARBON_OK) return no;
     if (xe != CARBON_OK) return xe;
+    if (lp != CARBON_OK) return lp;
+    if (cl != CARBON_OK) return cl;
     return ms;
 }
 

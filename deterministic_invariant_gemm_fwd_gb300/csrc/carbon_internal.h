@@ -154,5 +154,8 @@ carbon_status_t superacc_take_device_status();
 carbon_status_t embedding_take_device_status();
 carbon_status_t norm_take_device_status();
 carbon_status_t xent_take_device_status();
+// Of log probabilities and gradient clipping (linear_logprob.cu, grad_clip.cu).
+carbon_status_t logp_take_device_status();
+carbon_status_t clip_take_device_status();
 
 }  // namespace carbon

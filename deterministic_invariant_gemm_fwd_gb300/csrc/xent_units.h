@@ -27,6 +27,9 @@ constexpr int kPiece = 4096;
 // of L2 holds what it can of them.
 constexpr int64_t kGBytes = 64ll << 20;
 constexpr int64_t kSlotBytes = 64ll << 20;    // dx: the pieces' sums side by side up to this size, else added in place
+constexpr int kTopSpare = 4;             // alternatives kept beyond those asked for, see linear_logprob.cu
+constexpr int kTopMost = 32 - kTopSpare;
+constexpr int kSpan = 8;                 // tiles that a pair takes one after another for the alternatives, at most
 constexpr int64_t kCountAhead = 16384;   // longer lists of positions are counted by a kernel of their own
 
 struct Head {
@@ -59,6 +62,18 @@ struct Plan {
     float *acc;                          // [slots][Mp][D]
     struct float2 *pairs;                // [vocab_groups][Mp]
     float *zt;                           // [Mp]
+    // log probabilities
+    bool logp;
+    float zscale, inv_t;                 // log2(e) / temperature, 1 / temperature
+    float range;                         // largest entropy + 1: bounds the gradient's entries
+    float *weighted;                     // [vocab_groups][Mp]: sum of e^(z - max) (z - max), binary
+    float *c1, *g1;                      // gradient per position: slope along log P, and that of the token's own entry
+    int top, listed;                     // alternatives asked for and kept
+    int span, spans;                     // tiles of a row tile that form a unit of the ticket, and their number
+    int lists;                           // lists of candidates per row: one per span and column half
+    unsigned int *bound;                 // [Mp]: a value (ordered) that at least `listed` logits of the row reach, or 0
+    unsigned long long *list;            // [lists][listed][Mp]: (ordered logit, ~entry)
+    int *list_count;                     // [lists][Mp]
 };
 
 // 32-bit words that start at zero: ticket, joined and the counters.
@@ -66,9 +81,12 @@ XENT_HD inline int64_t counters(const Plan &p) { return 2 + 3 * (int64_t)p.piece
 
 inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// Fills the plan; returns the workspace bytes.
-inline int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, bool grad, bool f16) {
+// Fills the plan; returns the workspace bytes.  top: alternatives per position
+// (log probabilities), or -1 for the loss.
+inline int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, bool grad, bool f16, int top = -1) {
     Plan p = {};
+    p.logp = top >= 0;
+    p.top = top > 0 ? top : 0;
     p.M = M; p.D = D; p.V = V; p.grad = grad; p.f16 = f16;
     p.Mp = round_up(M > 0 ? M : 1, kBM);
     p.vocab_groups = (int)((V + kGroup - 1) / kGroup);
@@ -119,11 +137,28 @@ inline int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, b
     if (grad) {
         p.lse2 = reinterpret_cast<float *>(take(4 * p.Mp));
         p.rfac = reinterpret_cast<float *>(take(4 * p.Mp));
+        if (p.logp) {
+            p.c1 = reinterpret_cast<float *>(take(4 * p.Mp));
+            p.g1 = reinterpret_cast<float *>(take(4 * p.Mp));
+        }
         p.g = take(2 * p.Mp * kPiece * p.buffers);
         p.acc = reinterpret_cast<float *>(take(4 * (int64_t)p.slots * p.Mp * D));
     } else {
         p.pairs = reinterpret_cast<struct float2 *>(take(8 * (int64_t)p.vocab_groups * p.Mp));
         p.zt = reinterpret_cast<float *>(take(4 * p.Mp));
+        if (p.logp) p.weighted = reinterpret_cast<float *>(take(4 * (int64_t)p.vocab_groups * p.Mp));
+        if (p.top > 0) {
+            p.listed = p.top + kTopSpare;
+            // long spans start few lists; about eight spans for each pair of
+            // CTAs keep the pairs busy to the end
+            const int64_t tiles = (V + p.lwidth - 1) / p.lwidth, span = p.Mp / kBM * tiles / (8 * 76);
+            p.span = (int)(span < 1 ? 1 : span > kSpan ? kSpan : span);
+            p.spans = (int)((tiles + p.span - 1) / p.span);
+            p.lists = p.spans * (p.lwidth / kGroup);
+            p.bound = reinterpret_cast<unsigned int *>(take(4 * p.Mp));
+            p.list_count = reinterpret_cast<int *>(take(4 * (int64_t)p.lists * p.Mp));
+            p.list = reinterpret_cast<unsigned long long *>(take(8 * (int64_t)p.lists * p.listed * p.Mp));
+        }
     }
     if (out) *out = p;
     return used + 128;                   // room to align the base to 128 bytes
@@ -140,9 +175,11 @@ struct alignas(16) Unit {
     int type, piece;
     int m0, n0;              // output tile: first row, first column (rows of the output for T are table rows)
     int width;               // columns, a multiple of 128
-    int left;                // 0: the list has ended
+    int left;                // 0: the list has ended; of a span: kFirst, kLast and its place in its row
     int unused[2];
 };
+
+constexpr int kFirst = 2, kLast = 4, kSpanShift = 3;
 
 // Phases in list order: L of the first `lead` pieces, then for each piece p: L
 // of p + lead, and T and X of p, the longer of these first (T takes a k-block
@@ -214,6 +251,19 @@ struct Walk {
             o.n0 = (int)(i % (uint32_t)p.dtiles) * p.dwidth;
             o.width = lesser(p.dwidth, (int)(p.D - o.n0 + 127) / 128 * 128);
         }
+        return o;
+    }
+    // Tile j of span s: `span` neighbouring tiles of a row tile, spans in the
+    // order of the tiles above.
+    XENT_HD Unit in_span(uint32_t s, int j) const {
+        Unit o = {};
+        if (s >= (uint32_t)tm * (uint32_t)p.spans) return o;
+        const int tiles = (int)((p.V + p.lwidth - 1) / p.lwidth), q = (int)(s / (uint32_t)tm), tile = q * p.span + j;
+        o.type = UNIT_L;
+        o.m0 = (int)(s % (uint32_t)tm) * kBM;
+        o.n0 = tile * p.lwidth;
+        o.width = lesser(p.lwidth, ((int)p.V - o.n0 + 127) / 128 * 128);
+        o.left = 1 | (j == 0 ? kFirst : 0) | (j == p.span - 1 || tile == tiles - 1 ? kLast : 0) | q << kSpanShift;
         return o;
     }
     XENT_HD int k_blocks(const Unit &o) const {

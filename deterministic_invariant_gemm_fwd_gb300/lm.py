@@ -10,6 +10,7 @@ the functions in autograd.
 """
 from __future__ import annotations
 
+import array
 from typing import NamedTuple, Optional
 
 from . import _binding as _b
@@ -95,6 +96,24 @@ def _bytes(nbytes):
 
 def _p(t):
     return None if t is None else t.data_ptr()
+
+
+_codes = {}                      # torch dtype -> code, filled on first use
+
+
+def _tensors(name, tensors, device):
+    """Host arrays (addresses, sizes, type codes) of contiguous tensors on one device."""
+    if not _codes:
+        import torch
+        _codes.update({torch.float32: _b.F32, torch.bfloat16: _b.BF16, torch.float16: _b.F16})
+    try:
+        kinds = [_codes[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise TypeError(f"{name} holds dtype {e.args[0]}; expected float32, bfloat16 or float16") from None
+    if not all([t.get_device() == device and t.is_contiguous() for t in tensors]) or device < 0:
+        raise ValueError(f"{name} must be contiguous CUDA tensors on one device")
+    return (array.array("Q", [t.data_ptr() for t in tensors]), array.array("q", [t.numel() for t in tensors]),
+            array.array("i", kinds))
 
 
 def embedding_fwd(table, ids, scale=1.0, stream=None):
@@ -278,3 +297,114 @@ def linear_cross_entropy_bwd(grad, x, table, targets, lse, ignore_index=-100, re
     if st:
         _b._check(st, "carbon_linear_xent_bwd")
     return dx, dtable
+
+
+class LogProbs(NamedTuple):
+    """What linear_log_probs_fwd returns; the last two are None for top=0."""
+    log_probs: object                    # fp32 [M]
+    entropy: object                      # fp32 [M]
+    lse: object                          # fp32 [M], which the gradient takes
+    top_log_probs: Optional[object]      # fp32 [M, top]
+    top_ids: Optional[object]            # int64 [M, top]
+
+
+def _logp_args(x, table, tokens, temperature):
+    import torch
+    M, D = _rows("x", x)
+    V, at = _rows("table", table)[0], x.get_device()
+    _need("table", table, (V, D), x.dtype, at)
+    _need("tokens", tokens, (M,), torch.int64, at)
+    if not 0.0 < temperature < float("inf"):
+        raise ValueError(f"temperature {temperature!r}; expected a positive number")
+    return M, D, V, _dtype("x", x)
+
+
+def linear_log_probs_fwd(x, table, tokens, temperature=1.0, top=0, ignore_index=-100, stream=None):
+    """LogProbs of tokens (int64 [M]) under the logits x . table^T / temperature:
+    x [M, D], table [V, D].  Each position's log probability and its
+    distribution's entropy, and the `top` (at most 28) most probable entries,
+    most probable first.  Positions of token ignore_index give zeros, and -1
+    among the ids."""
+    import torch
+    M, D, V, code = _logp_args(x, table, tokens, temperature)
+    if not 0 <= top <= min(28, V):
+        raise ValueError(f"top {top!r}; expected 0 to 28, and at most the {V} rows of the table")
+    device = x.device
+    s, empty, workspace = _begin(x, stream)
+    log_probs, entropy, lse = empty((3, M), torch.float32, device).unbind(0)
+    best = ids = None
+    if top:
+        best = empty((M, top), torch.float32, device)
+        ids = empty((M, top), torch.int64, device)
+    nbytes = _bytes(_b.lib.carbon_linear_logp_fwd_workspace(M, D, V, top))
+    ws = workspace(nbytes, device)
+    st = _b.lib.carbon_linear_logp_fwd(log_probs.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _p(ids), _p(best),
+                                       x.data_ptr(), table.data_ptr(), tokens.data_ptr(), M, D, V, top, temperature,
+                                       ignore_index, ws.data_ptr(), nbytes, code, s)
+    if st:
+        _b._check(st, "carbon_linear_logp_fwd")
+    return LogProbs(log_probs, entropy, lse, best, ids)
+
+
+def linear_log_probs_bwd(grad_log_probs, grad_entropy, x, table, tokens, lse, entropy=None, temperature=1.0,
+                         ignore_index=-100, stream=None):
+    """(dx, dtable) from the gradients of log_probs and of entropy (fp32 [M];
+    either may be None) and the forward's lse and entropy."""
+    import torch
+    M, D, V, code = _logp_args(x, table, tokens, temperature)
+    device, at = x.device, x.get_device()
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("the gradient of the entropy takes the entropy")
+    for name, t in (("grad_log_probs", grad_log_probs), ("grad_entropy", grad_entropy), ("lse", lse),
+                    ("entropy", entropy)):
+        if t is not None:
+            _need(name, t, (M,), torch.float32, at)
+    s, empty, workspace = _begin(x, stream)
+    dx = empty((M, D), x.dtype, device)
+    dtable = empty((V, D), x.dtype, device)
+    nbytes = _bytes(_b.lib.carbon_linear_logp_bwd_workspace(M, D, V))
+    ws = workspace(nbytes, device)
+    st = _b.lib.carbon_linear_logp_bwd(dx.data_ptr(), dtable.data_ptr(), _p(grad_log_probs), _p(grad_entropy),
+                                       x.data_ptr(), table.data_ptr(), tokens.data_ptr(), lse.data_ptr(), _p(entropy),
+                                       M, D, V, temperature, ignore_index, ws.data_ptr(), nbytes, code, s)
+    if st:
+        _b._check(st, "carbon_linear_logp_bwd")
+    return dx, dtable
+
+
+def _clip(grads, out, max_norm, eps, stream):
+    import torch
+    at = grads[0].get_device() if grads else torch.cuda.current_device()
+    first = grads[0] if grads else torch.empty(0, device=torch.device("cuda", at))
+    pointers, sizes, kinds = _tensors("grads", grads, at)
+    to = None
+    if out is not None:
+        to, out_sizes, out_kinds = (pointers, sizes, kinds) if out is grads else _tensors("out", out, at)
+        if out_sizes != sizes or out_kinds != kinds:
+            raise ValueError("out must hold tensors of the sizes and types of grads")
+    s, empty, workspace = _begin(first, stream)
+    norm = empty((), torch.float32, first.device)
+    n, at_sizes = len(grads), sizes.buffer_info()[0]
+    nbytes = _bytes(_b.lib.carbon_clip_grads_workspace(at_sizes, n))
+    ws = workspace(nbytes, first.device)
+    st = _b.lib.carbon_clip_grads(norm.data_ptr(), None if to is None else to.buffer_info()[0], pointers.buffer_info()[0],
+                                  at_sizes, kinds.buffer_info()[0], n, max_norm, eps, ws.data_ptr(), nbytes, s)
+    if st:
+        _b._check(st, "carbon_clip_grads")
+    return norm
+
+
+def grad_norm(grads, stream=None):
+    """The norm of all elements of a list of gradients: fp32 scalar tensor."""
+    return _clip(list(grads), None, 0.0, 0.0, stream)
+
+
+def clip_grads(grads, max_norm, eps=1e-6, out=None, stream=None):
+    """Multiplies a list of gradients by min(1, max_norm / (norm + eps)), norm
+    being that of all their elements, in place or into the tensors of out, and
+    returns the norm (fp32 scalar tensor).  The tensors may be of any of the
+    three types, also mixed."""
+    grads = list(grads)
+    if not (max_norm >= 0 and eps >= 0):
+        raise ValueError("max_norm and eps must not be negative")
+    return _clip(grads, grads if out is None else list(out), max_norm, eps, stream)

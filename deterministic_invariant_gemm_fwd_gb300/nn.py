@@ -38,9 +38,9 @@ import math
 
 import torch
 
-from . import (_dtype_code, carbon_gemm_dw, embedding_bwd, embedding_fwd,
+from . import (_dtype_code, carbon_gemm_dw, clip_grads, embedding_bwd, embedding_fwd,
                linear_cross_entropy_bwd, linear_cross_entropy_fwd, linear_dw, linear_dx, linear_fwd,
-               rms_norm_bwd, rms_norm_fwd)
+               linear_log_probs_bwd, linear_log_probs_fwd, rms_norm_bwd, rms_norm_fwd)
 
 
 def bias_grad(dY, stream=None, tier="exact"):
@@ -340,3 +340,66 @@ def linear_cross_entropy(x, table, targets, ignore_index=-100, reduction="mean")
     if targets.shape != x.shape[:-1]:
         raise ValueError(f"targets has shape {tuple(targets.shape)}; expected {tuple(x.shape[:-1])}")
     return _LinearCrossEntropyFunction.apply(x, table, targets, ignore_index, reduction)
+
+
+class _LinearLogProbsFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, table, tokens, temperature, ignore_index):
+        x2 = _flat(x, table.shape[1])
+        t = tokens.reshape(-1).contiguous()
+        r = linear_log_probs_fwd(x2, table, t, temperature, 0, ignore_index)
+        ctx.save_for_backward(x2, table, t, r.lse, r.entropy)
+        ctx.shape, ctx.temperature, ctx.ignore_index = x.shape, temperature, ignore_index
+        ctx.set_materialize_grads(False)
+        # copies: views of one allocation could not be changed in place by their user
+        return r.log_probs.view(tokens.shape).clone(), r.entropy.view(tokens.shape).clone()
+
+    @staticmethod
+    @_once
+    def backward(ctx, dlogp, dentropy):
+        x2, table, t, lse, entropy = ctx.saved_tensors
+        flat = [None if g is None else g.reshape(-1).contiguous() for g in (dlogp, dentropy)]
+        dx, dtable = linear_log_probs_bwd(*flat, x2, table, t, lse, entropy, ctx.temperature, ctx.ignore_index)
+        return dx.view(ctx.shape), dtable, None, None, None
+
+
+def _token_shape(x, table, tokens):
+    _width(x, table.shape[1])
+    if tokens.shape != x.shape[:-1]:
+        raise ValueError(f"tokens has shape {tuple(tokens.shape)}; expected {tuple(x.shape[:-1])}")
+
+
+def linear_log_probs(x, table, tokens, temperature=1.0, ignore_index=-100):
+    """(log probabilities, entropies), fp32 of tokens' shape: of tokens under the
+    logits x . table^T / temperature, and of each position's distribution,
+    without storing the logits; both differentiable in x and table.  Zero where
+    the token is ignore_index."""
+    _token_shape(x, table, tokens)
+    return _LinearLogProbsFunction.apply(x, table, tokens, float(temperature), ignore_index)
+
+
+def top_log_probs(x, table, tokens, top, temperature=1.0, ignore_index=-100):
+    """LogProbs of tokens of any shape with the `top` most probable entries of
+    each position (last dimension); not differentiable."""
+    _token_shape(x, table, tokens)
+    with torch.no_grad():
+        r = linear_log_probs_fwd(_flat(x, table.shape[1]), table, tokens.reshape(-1).contiguous(), temperature, top,
+                                 ignore_index)
+    shape = tokens.shape
+    return type(r)(*(v.view(shape) for v in r[:3]), *(None if v is None else v.view(*shape, top) for v in r[3:]))
+
+
+@torch.no_grad()
+def clip_grad_norm_(parameters, max_norm, eps=1e-6):
+    """Scales the gradients of the parameters (one tensor or several; those
+    without a gradient are left out) in place so that their common norm is at
+    most max_norm, and returns the norm before that, an fp32 scalar tensor on
+    their device.  The norm's sum has a fixed order, so it and the gradients
+    are the same bits in every run.  Gradients: contiguous CUDA tensors of one
+    device, none of them sharing memory."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = [p.grad for p in parameters if p.grad is not None]
+    if not grads:
+        return torch.zeros(())
+    return clip_grads(grads, max_norm, eps)

@@ -173,6 +173,86 @@ carbon_status_t carbon_linear_xent_bwd(void *dx, void *dtable, const float *grad
                                        carbon_stream_t stream);
 int64_t carbon_linear_xent_bwd_workspace(int64_t M, int64_t D, int64_t V);
 
+/* ---- log probabilities of given tokens ------------------------------------------
+ *
+ * x[M,D], table[V,D] and tokens[M] as x, table and targets above, and with the
+ * same limits.  With z[m] = table . x[m] / temperature and P = softmax(z):
+ *
+ *   lse[m] = log sum_v exp z[m,v],   log_probs[m] = z[m,tokens[m]] - lse[m]
+ *   entropy[m] = -sum_v P[m,v] log P[m,v]
+ *
+ * all fp32 [M].  top_ids (int64) and top_log_probs (fp32), [M,top]: the `top`
+ * largest entries of P with their logarithms, largest first; not read or written
+ * for top = 0.  top <= 28 and top <= V, temperature > 0, else
+ * CARBON_ERR_INVALID_ARG.  Positions whose token is ignore_index (or names no
+ * entry, see above) cost nothing: log_probs, entropy, lse and top_log_probs 0,
+ * top_ids -1.  Places for which no logit above -infinity is left: -1, -infinity.
+ *
+ * Order of the alternatives: the top + 4 largest logits as the tensor cores form
+ * them (their error: see carbon_linear_xent_fwd), ordered by their logits as
+ * sums of the exact products in about 48 bits, equal ones by the lower entry;
+ * top_log_probs come from these sums.
+ *
+ * Errors of log_probs and lse: those of the loss above, of z / temperature;
+ * entropy: (16 + log2 V) 2^-23 (entropy + 1) and 2 (entropy + 1) times the largest
+ * error of a logit, over the temperature.  A position's results do not depend on
+ * the other positions. */
+carbon_status_t carbon_linear_logp_fwd(float *log_probs, float *entropy, float *lse,
+                                       int64_t *top_ids, float *top_log_probs, const void *x,
+                                       const void *table, const int64_t *tokens, int64_t M,
+                                       int64_t D, int64_t V, int64_t top, float temperature,
+                                       int64_t ignore_index, void *workspace,
+                                       int64_t workspace_bytes, carbon_dtype_t dtype,
+                                       carbon_stream_t stream);
+int64_t carbon_linear_logp_fwd_workspace(int64_t M, int64_t D, int64_t V, int64_t top);
+
+/* dx[M,D] and dtable[V,D] from the gradients of log_probs and of entropy (fp32
+ * [M], either may be NULL: zeros) and the forward's lse and entropy (entropy may
+ * be NULL with grad_entropy):
+ *
+ *   G[m,v] = grad_log_probs[m] ([v == tokens[m]] - P[m,v])
+ *            - grad_entropy[m] P[m,v] (log P[m,v] + entropy[m])
+ *   dx = G . table / temperature,   dtable = G^T . x / temperature
+ *
+ * G is rounded to dtype as for the loss with CARBON_REDUCE_NONE, the power of two
+ * being that of the largest finite |grad_log_probs| + (1 + log V) |grad_entropy|.
+ * Workspace: carbon_linear_logp_bwd_workspace bytes, about those of the loss. */
+carbon_status_t carbon_linear_logp_bwd(void *dx, void *dtable, const float *grad_log_probs,
+                                       const float *grad_entropy, const void *x,
+                                       const void *table, const int64_t *tokens, const float *lse,
+                                       const float *entropy, int64_t M, int64_t D, int64_t V,
+                                       float temperature, int64_t ignore_index, void *workspace,
+                                       int64_t workspace_bytes, carbon_dtype_t dtype,
+                                       carbon_stream_t stream);
+int64_t carbon_linear_logp_bwd_workspace(int64_t M, int64_t D, int64_t V);
+
+/* ---- norm of all gradients, and clipping -------------------------------------
+ *
+ *   norm = sqrt(sum over the `count` tensors and their elements of g^2)
+ *   out  = g * min(1, max_norm / (norm + eps))
+ *
+ * grads, out, sizes (elements) and dtypes (carbon_dtype_t) are arrays on the
+ * host, read during the call; the tensors are contiguous and on the device.
+ * norm: fp32 [1] on the device, may be NULL; the quotient takes the norm as it
+ * is written there.  out may be NULL (the norm alone), and out[i] may be
+ * grads[i] (in place: where the factor is 1 nothing is written); what is written
+ * may not overlap anything else (CARBON_ERR_INVALID_ARG).  A NaN among the
+ * gradients makes the norm and all of out NaN; an infinity makes the norm
+ * infinite and the factor 0.
+ *
+ * Squares are summed in fp32 by 64, in float64 from there on; squares outside
+ * fp32's range are scaled, so that the norm overflows only where it is no fp32
+ * number itself.  An element's place in the sum depends on the sizes and the
+ * order of the tensors, not on their addresses.  max_norm >= 0, eps >= 0.
+ * Workspace: carbon_clip_grads_workspace bytes, at most 64 KiB and 8 more per
+ * tensor. */
+carbon_status_t carbon_clip_grads(float *norm, void *const *out, const void *const *grads,
+                                  const int64_t *sizes, const int *dtypes, int64_t count,
+                                  float max_norm, float eps, void *workspace,
+                                  int64_t workspace_bytes, carbon_stream_t stream);
+/* Bytes, or -1 where the sizes are invalid. */
+int64_t carbon_clip_grads_workspace(const int64_t *sizes, int64_t count);
+
 #ifdef __cplusplus
 }
 #endif
