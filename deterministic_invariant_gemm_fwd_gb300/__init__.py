@@ -28,6 +28,9 @@ from ._binding import (carbon_clip_grads, carbon_clip_grads_workspace,  # noqa: 
                        carbon_linear_logp_fwd, carbon_linear_logp_fwd_workspace,
                        carbon_linear_xent_bwd, carbon_linear_xent_bwd_workspace,
                        carbon_linear_xent_fwd, carbon_linear_xent_fwd_workspace,
+                       carbon_lora_linear_bwd, carbon_lora_linear_bwd_workspace,
+                       carbon_lora_linear_fwd, carbon_lora_linear_fwd_workspace,
+                       carbon_lora_linear_u_elements,
                        carbon_rms_norm_bwd, carbon_rms_norm_bwd_workspace,
                        carbon_rms_norm_expand, carbon_rms_norm_fwd)
 from ._binding import (CarbonError, carbon_abi_version, carbon_debug_exact_y64,  # noqa: F401
@@ -42,7 +45,8 @@ from ._binding import (CarbonError, carbon_abi_version, carbon_debug_exact_y64, 
                        carbon_measure_int_mac_rate,
                        carbon_status_string)
 from .lm import (LogProbs, RmsNorm, clip_grads, embedding_bwd, embedding_fwd, grad_norm, linear_cross_entropy_bwd,  # noqa: F401
-                 linear_cross_entropy_fwd, linear_log_probs_bwd, linear_log_probs_fwd, rms_norm_bwd, rms_norm_expand, rms_norm_fwd)
+                 linear_cross_entropy_fwd, linear_log_probs_bwd, linear_log_probs_fwd,
+                 lora_linear_bwd, lora_linear_fwd, rms_norm_bwd, rms_norm_expand, rms_norm_fwd)
 
 
 def _dtype_code(t):

@@ -69,6 +69,8 @@ def _load() -> ctypes.CDLL:
         "carbon_linear_xent_bwd": [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, vp, i64, i32, vp],
         "carbon_linear_logp_fwd": [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, f32, i64, vp, i64, i32, vp],
         "carbon_linear_logp_bwd": [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, f32, i64, vp, i64, i32, vp],
+        "carbon_lora_linear_fwd": [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, i32, vp],
+        "carbon_lora_linear_bwd": [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, i32, vp],
         "carbon_clip_grads": [vp, vp, vp, vp, vp, i64, f32, f32, vp, i64, vp],
         "carbon_debug_exact_y64": [i32, vp, vp, vp, vp, i64, i64, i64, i32, vp],
         "carbon_debug_tc_f32": [i32, vp, vp, vp, vp, i64, i64, i64, vp],
@@ -90,6 +92,10 @@ def _load() -> ctypes.CDLL:
     lib.carbon_linear_logp_fwd_workspace.restype = i64
     lib.carbon_linear_logp_bwd_workspace.argtypes = [i64] * 3
     lib.carbon_linear_logp_bwd_workspace.restype = i64
+    for name, sizes in (("u_elements", 2), ("fwd_workspace", 5), ("bwd_workspace", 5)):
+        fn = getattr(lib, "carbon_lora_linear_" + name)
+        fn.argtypes = [i64] * sizes
+        fn.restype = i64
     lib.carbon_clip_grads_workspace.argtypes = [vp, i64]
     lib.carbon_clip_grads_workspace.restype = i64
     lib.carbon_status_string.argtypes = [i32]
@@ -318,6 +324,36 @@ def carbon_linear_logp_bwd(dx, dtable, grad_log_probs, grad_entropy, x, table, t
 
 def carbon_linear_logp_bwd_workspace(M, D, V) -> int:
     return int(_lib().carbon_linear_logp_bwd_workspace(M, D, V))
+
+
+def carbon_lora_linear_fwd(y, u, x, w, bias, a, b, adapters, scales, M, K, N, n, r, workspace, workspace_bytes,
+                           dtype, stream=None) -> None:
+    """y = x . w + bias + u . b[adapter], u = scale (x . a[adapter])."""
+    _check(_lib().carbon_lora_linear_fwd(_ptr(y), _ptr(u), _ptr(x), _ptr(w), _ptr(bias), _ptr(a), _ptr(b),
+                                         _ptr(adapters), _ptr(scales), M, K, N, n, r, _ptr(workspace),
+                                         workspace_bytes, _code(DTYPES, dtype), _stream(stream)),
+           "carbon_lora_linear_fwd")
+
+
+def carbon_lora_linear_bwd(dx, da, db, dy, x, w, a, b, adapters, scales, u, M, K, N, n, r, workspace,
+                           workspace_bytes, dtype, stream=None) -> None:
+    """Gradients of carbon_lora_linear_fwd with respect to x, a and b."""
+    _check(_lib().carbon_lora_linear_bwd(_ptr(dx), _ptr(da), _ptr(db), _ptr(dy), _ptr(x), _ptr(w), _ptr(a), _ptr(b),
+                                         _ptr(adapters), _ptr(scales), _ptr(u), M, K, N, n, r, _ptr(workspace),
+                                         workspace_bytes, _code(DTYPES, dtype), _stream(stream)),
+           "carbon_lora_linear_bwd")
+
+
+def carbon_lora_linear_u_elements(M, r) -> int:
+    return int(_lib().carbon_lora_linear_u_elements(M, r))
+
+
+def carbon_lora_linear_fwd_workspace(M, K, N, n, r) -> int:
+    return int(_lib().carbon_lora_linear_fwd_workspace(M, K, N, n, r))
+
+
+def carbon_lora_linear_bwd_workspace(M, K, N, n, r) -> int:
+    return int(_lib().carbon_lora_linear_bwd_workspace(M, K, N, n, r))
 
 
 def carbon_clip_grads(norm, out, grads, sizes, dtypes, count, max_norm, eps, workspace, workspace_bytes,

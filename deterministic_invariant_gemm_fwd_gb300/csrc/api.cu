@@ -270,6 +270,7 @@ carbon_status_t carbon_get_device_status(carbon_stream_t stream) {
     const carbon_status_t no = carbon::norm_take_device_status();
     const carbon_status_t xe = carbon::xent_take_device_status();
     const carbon_status_t lp = carbon::logp_take_device_status();
+    const carbon_status_t lr = carbon::lora_take_device_status();
     const carbon_status_t cl = carbon::clip_take_device_status();
     if (st != CARBON_OK) return st;
     if (tc != CARBON_OK) return tc;
@@ -281,6 +282,7 @@ carbon_status_t carbon_get_device_status(carbon_stream_t stream) {
     if (no != CARBON_OK) return no;
     if (xe != CARBON_OK) return xe;
     if (lp != CARBON_OK) return lp;
+    if (lr != CARBON_OK) return lr;
     if (cl != CARBON_OK) return cl;
     return ms;
 }

@@ -154,7 +154,9 @@ carbon_status_t superacc_take_device_status();
 carbon_status_t embedding_take_device_status();
 carbon_status_t norm_take_device_status();
 carbon_status_t xent_take_device_status();
-// Of log probabilities and gradient clipping (linear_logprob.cu, grad_clip.cu).
+// Of log probabilities, low-rank adapters and gradient clipping
+// (linear_logprob.cu, lora.cu, grad_clip.cu).
+carbon_status_t lora_take_device_status();
 carbon_status_t logp_take_device_status();
 carbon_status_t clip_take_device_status();
 

@@ -372,6 +372,72 @@ def linear_log_probs_bwd(grad_log_probs, grad_entropy, x, table, tokens, lse, en
     return dx, dtable
 
 
+def _lora_args(first, rows, name, weight, a, b, adapters, scales):
+    """(M, K, N, n, r, type code) of a call whose rows (x, or dy) are `first`."""
+    import torch
+    at, dtype = first.get_device(), first.dtype
+    M = _rows(name, first)[0]
+    K, N = _rows("weight", weight)
+    _need(name, first, (M, rows(K, N)), dtype, at)
+    _need("weight", weight, (K, N), dtype, at)
+    if a.dim() != 3:
+        raise ValueError(f"a has shape {tuple(a.shape)}; expected [adapters, {K}, rank]")
+    n, r = a.shape[0], a.shape[2]
+    _need("a", a, (n, K, r), dtype, at)
+    _need("b", b, (n, r, N), dtype, at)
+    _need("adapters", adapters, (M,), torch.int64, at)
+    _need("scales", scales, (n,), torch.float32, at)
+    return M, K, N, n, r, _dtype(name, first)
+
+
+def lora_linear_fwd(x, weight, a, b, adapters, scales, bias=None, keep=False, stream=None):
+    """y[m] = x[m] . weight + bias + scales[i] (x[m] . a[i]) . b[i] with i = adapters[m],
+    or without the last term where that is -1: x [M, K], weight [K, N], a
+    [n, K, r], b [n, r, N], adapters int64 [M], scales fp32 [n].  keep=True
+    returns (y, u), u being what the gradient takes."""
+    import torch
+    M, K, N, n, r, code = _lora_args(x, lambda K, N: K, "x", weight, a, b, adapters, scales)
+    device, dtype = x.device, x.dtype
+    if bias is not None:
+        _need("bias", bias, (N,), dtype, x.get_device())
+    s, empty, workspace = _begin(x, stream)
+    y = empty((M, N), dtype, device)
+    nu = _bytes(_b.lib.carbon_lora_linear_u_elements(M, r))
+    u = empty((M, 3, nu // (3 * M) if M else 0), dtype, device)
+    nbytes = _bytes(_b.lib.carbon_lora_linear_fwd_workspace(M, K, N, n, r))
+    ws = workspace(nbytes, device)
+    st = _b.lib.carbon_lora_linear_fwd(y.data_ptr(), u.data_ptr(), x.data_ptr(), weight.data_ptr(), _p(bias), a.data_ptr(),
+                                       b.data_ptr(), adapters.data_ptr(), scales.data_ptr(), M, K, N, n, r, ws.data_ptr(),
+                                       nbytes, code, s)
+    if st:
+        _b._check(st, "carbon_lora_linear_fwd")
+    return (y, u) if keep else y
+
+
+def lora_linear_bwd(dy, x, weight, a, b, adapters, scales, u, need_dx=True, need_adapters=True, stream=None):
+    """(dx, da, db) of lora_linear_fwd from its u; None for those not needed."""
+    import torch
+    M, K, N, n, r, code = _lora_args(dy, lambda K, N: N, "dy", weight, a, b, adapters, scales)
+    device, dtype, at = dy.device, dy.dtype, dy.get_device()
+    _need("x", x, (M, K), dtype, at)
+    nu = _bytes(_b.lib.carbon_lora_linear_u_elements(M, r))
+    _need("u", u, (M, 3, nu // (3 * M) if M else 0), dtype, at)
+    if not (need_dx or need_adapters):
+        return None, None, None
+    s, empty, workspace = _begin(dy, stream)
+    dx = empty((M, K), dtype, device) if need_dx else None
+    da = empty((n, K, r), dtype, device) if need_adapters else None
+    db = empty((n, r, N), dtype, device) if need_adapters else None
+    nbytes = _bytes(_b.lib.carbon_lora_linear_bwd_workspace(M, K, N, n, r))
+    ws = workspace(nbytes, device)
+    st = _b.lib.carbon_lora_linear_bwd(_p(dx), _p(da), _p(db), dy.data_ptr(), x.data_ptr(), weight.data_ptr(), a.data_ptr(),
+                                       b.data_ptr(), adapters.data_ptr(), scales.data_ptr(), u.data_ptr(), M, K, N, n, r,
+                                       ws.data_ptr(), nbytes, code, s)
+    if st:
+        _b._check(st, "carbon_lora_linear_bwd")
+    return dx, da, db
+
+
 def _clip(grads, out, max_norm, eps, stream):
     import torch
     at = grads[0].get_device() if grads else torch.cuda.current_device()

@@ -40,7 +40,7 @@ import torch
 
 from . import (_dtype_code, carbon_gemm_dw, clip_grads, embedding_bwd, embedding_fwd,
                linear_cross_entropy_bwd, linear_cross_entropy_fwd, linear_dw, linear_dx, linear_fwd,
-               linear_log_probs_bwd, linear_log_probs_fwd, rms_norm_bwd, rms_norm_fwd)
+               linear_log_probs_bwd, linear_log_probs_fwd, lora_linear_bwd, lora_linear_fwd, rms_norm_bwd, rms_norm_fwd)
 
 
 def bias_grad(dY, stream=None, tier="exact"):
@@ -340,6 +340,71 @@ def linear_cross_entropy(x, table, targets, ignore_index=-100, reduction="mean")
     if targets.shape != x.shape[:-1]:
         raise ValueError(f"targets has shape {tuple(targets.shape)}; expected {tuple(x.shape[:-1])}")
     return _LinearCrossEntropyFunction.apply(x, table, targets, ignore_index, reduction)
+
+
+class _LoraLinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, a, b, adapters, scales):
+        K, N = weight.shape
+        x2, ids = _flat(x, K), adapters.reshape(-1).contiguous()
+        y, u = lora_linear_fwd(x2, weight, a, b, ids, scales, bias, keep=True)
+        ctx.save_for_backward(x2, weight, a, b, ids, scales, u)
+        ctx.shape, ctx.has_bias = x.shape, bias is not None
+        return y.view(*x.shape[:-1], N)
+
+    @staticmethod
+    @_once
+    def backward(ctx, grad):
+        x2, weight, a, b, ids, scales, u = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        g = _flat(grad, weight.shape[1])
+        dx, da, db = lora_linear_bwd(g, x2, weight, a, b, ids, scales, u, need_dx=need[0], need_adapters=need[3] or need[4])
+        dw = linear_dw(x2, g, "tc") if need[1] else None
+        dbias = bias_grad(g) if ctx.has_bias and need[2] else None
+        return None if dx is None else dx.view(ctx.shape), dw, dbias, da, db, None, None
+
+
+def lora_linear(x, weight, a, b, adapters, scales, bias=None):
+    """deterministic_linear(x, weight, bias, tier="tc") with low-rank adapters:
+    plus scales[i] (x . a[i]) . b[i] for the rows whose adapter is i, in the same
+    accumulator.  x [..., K], weight [K, N], a [n, K, r], b [n, r, N], adapters
+    int64 of x's leading shape (-1: none), scales fp32 [n].  Differentiable in x,
+    weight, bias, a and b; gradients of what does not require one are not formed."""
+    _width(x, weight.shape[0])
+    if adapters.shape != x.shape[:-1]:
+        raise ValueError(f"adapters has shape {tuple(adapters.shape)}; expected {tuple(x.shape[:-1])}")
+    return _LoraLinearFunction.apply(x, weight, bias, a, b, adapters, scales)
+
+
+class LoraLinear(torch.nn.Module):
+    """A linear layer, frozen unless train_base, with `adapters` low-rank adapters
+    of rank `rank` and factor alpha / rank: forward(x, adapters) -> y, adapters
+    int64 of x's leading shape or one number for all rows.  b starts at zero: a
+    new adapter changes nothing."""
+
+    def __init__(self, linear: Linear, adapters, rank, alpha=None, train_base=False):
+        super().__init__()
+        K, N = linear.weight.shape
+        self.weight, self.bias = linear.weight, linear.bias
+        if not train_base:
+            for p in (self.weight, self.bias):
+                if p is not None:
+                    p.requires_grad_(False)
+        make = dict(device=linear.weight.device, dtype=linear.weight.dtype)
+        self.a = torch.nn.Parameter(torch.empty((adapters, K, rank), **make))
+        self.b = torch.nn.Parameter(torch.zeros((adapters, rank, N), **make))
+        torch.nn.init.normal_(self.a, std=1.0 / math.sqrt(K))
+        factor = (rank if alpha is None else alpha) / rank
+        self.register_buffer("scales", torch.full((adapters,), factor, device=linear.weight.device))
+
+    def forward(self, x, adapters):
+        if not isinstance(adapters, torch.Tensor):
+            adapters = torch.full(x.shape[:-1], adapters, dtype=torch.int64, device=x.device)
+        return lora_linear(x, self.weight, self.a, self.b, adapters, self.scales, self.bias)
+
+    def extra_repr(self):
+        n, K, r = self.a.shape
+        return f"in_features={K}, out_features={self.b.shape[2]}, adapters={n}, rank={r}, bias={self.bias is not None}"
 
 
 class _LinearLogProbsFunction(torch.autograd.Function):

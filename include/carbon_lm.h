@@ -226,6 +226,67 @@ carbon_status_t carbon_linear_logp_bwd(void *dx, void *dtable, const float *grad
                                        carbon_stream_t stream);
 int64_t carbon_linear_logp_bwd_workspace(int64_t M, int64_t D, int64_t V);
 
+/* ---- linear layer with low-rank adapters ---------------------------------------
+ *
+ * x[M,K], w[K,N], bias[N] (may be NULL) as on the tensor-core tier; n adapters of
+ * rank r, a[n,K,r] and b[n,r,N], their factors scales[n] (fp32, e.g. alpha / r);
+ * adapters[M] (int64): the adapter i of each row, -1 for none.
+ *
+ *   u[m] = scales[i] (x[m] . a[i]),   y[m] = x[m] . w + bias + u[m] . b[i]
+ *
+ * in one accumulator, rounded once.  Rows of any order and mix; a row takes
+ * nothing from other rows or their adapters (NaN included), and its bits do not
+ * depend on them.  A row without an adapter is that of the layer alone.  Another
+ * number in adapters than -1 .. n-1 counts as -1 and CARBON_ERR_OUT_OF_BOUNDS is
+ * reported by carbon_get_device_status().  Rows that stand together (a request's
+ * tokens) cost least: each adapter's products run for every tile of 256 rows that
+ * has a row of it.
+ *
+ * u: carbon_lora_linear_u_elements 16-bit elements, 16-byte aligned, written by
+ * the forward and read by the backward pass: [M][3][r rounded up to 16], the
+ * 16-bit terms hi and lo of u (u = hi + lo to 2^-17 in bf16, 2^-22 in fp16,
+ * relative, and to fp16's smallest step 2^-24), and lo times 2^11.  With fp16 a
+ * |u| above 65504 is infinite.
+ *
+ * dtype: CARBON_BF16 or CARBON_F16 (CARBON_F32: CARBON_ERR_UNSUPPORTED).  K, N
+ * and r multiples of 8, and y, u, x, w, a, b (dx, da, db, dy) 16-byte aligned, else
+ * CARBON_ERR_MISALIGNED.  1 <= r <= 128, K, N <= 2^21, n < 2^24, M < 2^30.  M = 0:
+ * nothing to do, and zeros for da and db.
+ *
+ * Errors: y within (K + 2 r) 2^-23 (sum |x w| + sum |u b|) and the two terms'
+ * sum |u b| 2^-16 (2^-21 in fp16) of the exact value, before its rounding; u within
+ * (K + 2) 2^-23 scales sum |x a|.
+ * Workspace: carbon_lora_linear_fwd_workspace bytes (about 48 M). */
+carbon_status_t carbon_lora_linear_fwd(void *y, void *u, const void *x, const void *w,
+                                       const void *bias, const void *a, const void *b,
+                                       const int64_t *adapters, const float *scales, int64_t M,
+                                       int64_t K, int64_t N, int64_t n, int64_t r, void *workspace,
+                                       int64_t workspace_bytes, carbon_dtype_t dtype,
+                                       carbon_stream_t stream);
+/* M * 3 * (r rounded up to 16), or -1 where the sizes are invalid. */
+int64_t carbon_lora_linear_u_elements(int64_t M, int64_t r);
+int64_t carbon_lora_linear_fwd_workspace(int64_t M, int64_t K, int64_t N, int64_t n, int64_t r);
+
+/* Gradients, from the forward's u:
+ *
+ *   du[m] = scales[i] (dy[m] . b[i]^T),   dx[m] = dy[m] . w^T + du[m] . a[i]^T
+ *   da[i] = sum over the rows m of adapter i of x[m]^T . du[m]
+ *   db[i] = sum over them of u[m]^T . dy[m]
+ *
+ * da and db (both or neither may be NULL) are written whole, zeros for adapters
+ * that no row names; dx may be NULL, then w and a may be; without da, x and u
+ * may be.  Each adapter's sum takes its rows in their order, 512 at a time, and
+ * depends on them alone.
+ * Workspace: carbon_lora_linear_bwd_workspace bytes: 6 M r for du, 52 M, 8 n, and
+ * M / 256 partial sums of (K + N) r fp32 numbers. */
+carbon_status_t carbon_lora_linear_bwd(void *dx, void *da, void *db, const void *dy, const void *x,
+                                       const void *w, const void *a, const void *b,
+                                       const int64_t *adapters, const float *scales, const void *u,
+                                       int64_t M, int64_t K, int64_t N, int64_t n, int64_t r,
+                                       void *workspace, int64_t workspace_bytes,
+                                       carbon_dtype_t dtype, carbon_stream_t stream);
+int64_t carbon_lora_linear_bwd_workspace(int64_t M, int64_t K, int64_t N, int64_t n, int64_t r);
+
 /* ---- norm of all gradients, and clipping -------------------------------------
  *
  *   norm = sqrt(sum over the `count` tensors and their elements of g^2)
