@@ -17,13 +17,14 @@
 // Alternatives: a thread keeps the largest logits that it sees of its row, top + 4
 // of them, and a threshold that only a larger logit passes: after a thousand
 // entries hardly one in a hundred does.  So that it sees many, the tiles of a row
-// tile go to a pair of CTAs in spans of up to eight, and a span starts from what
-// the row's finished spans have proved (a value that top + 4 logits reach).  The
-// join takes the top + 4 largest of all spans' lists, forms their logits again,
-// from exact products with a compensated sum (about 2^-44 relative to the sum of
-// the products' magnitudes), and orders them by these: logits that fp32
-// accumulators cannot tell apart come in the order of float64, equal ones by
-// entry.  (The tensor cores' values differ from these by a few units of 2^-24;
+// tile go to a pair of CTAs in spans of up to eight; and the largest logits of 16 (or
+// 32) classes of entries, which all CTAs keep up to date in global memory, prove
+// others too small: the 12th largest of 16 is about the 21st largest of all
+// logits so far.  A warp per position takes the top + 4 largest of all
+// lists, forms their logits again, from exact products with a compensated sum
+// (about 2^-44 relative to the sum of the products' magnitudes), and orders them by
+// these: logits that fp32 accumulators cannot tell apart come in the order of
+// float64, equal ones by entry.  (The tensor cores' values differ from these by a few units of 2^-24;
 // four spare candidates make room for as many that such an error could move
 // across the last place.)
 //
@@ -33,14 +34,11 @@
 namespace carbon {
 namespace {
 
-constexpr int kJoinRows = 32;            // per CTA, a warp each; a multiple of a warp for the first part
-constexpr int kFound = 64;               // candidates of a row that the join holds in shared memory
 
 struct JoinArgs {
     float *log_probs, *lse, *entropy, *top_logp;
     int64_t *top_ids;
     const void *x, *table;
-    double inv_t;
 };
 
 // a + b = s + r exactly
@@ -98,55 +96,87 @@ __device__ __forceinline__ void exact_logits(const uint4 *x, const uint4 *table,
     }
 }
 
-// The alternatives of one position, by a warp.  found: room for kFound keys.
-template <bool F16>
-__device__ __forceinline__ void join_top(const Plan &p, const JoinArgs &a, int64_t row, float lse, uint64_t *found) {
-    const int lane = threadIdx.x % 32;
-    const unsigned below = (1u << lane) - 1u;
-    const uint32_t bound = p.bound[row];
-    const int64_t m = p.rowmap[row];
-    // every key that reaches the bound: at least `listed` of them where it is set
-    int n = 0;
-    for (int l0 = 0; l0 < p.lists; l0 += 32) {
+// The alternatives of a position, by W warps: eight where few positions would leave
+// most of the GPU idle (8 x 768 x 50257: 26 us with one), else one.
+constexpr int kTopThreads = 256;
+
+template <bool F16, bool FEW, int W>
+__global__ void __launch_bounds__(kTopThreads)
+logp_top_kernel(const Plan p, const JoinArgs a) {
+    // candidates: about twice the places asked for, up to four times where these are many
+    constexpr int kFound = FEW ? 64 : 256, Q = kFound / 32, kRows = kTopThreads / 32 / W;
+    constexpr int S = FEW ? kTopClassesFew : kTopClassesMany;
+    __shared__ uint64_t found_all[kRows][kFound];
+    __shared__ int count_all[kRows];
+    __shared__ float hi_all[kRows][32], lo_all[kRows][32];
+    const int lane = threadIdx.x % 32, part = threadIdx.x / 32 % W, mine_at = threadIdx.x / 32 / W;
+    auto sync = [] {
+        if (W == 1) __syncwarp();
+        else __syncthreads();                             // then a CTA has one position
+    };
+    uint64_t *found = found_all[mine_at];
+    int &found_count = count_all[mine_at];
+    if (lane == 0 && part == 0) found_count = 0;
+    wait_prior_grid();
+    allow_next_grid();
+    const int64_t row = (int64_t)blockIdx.x * kRows + mine_at;
+    if (row >= p.head->kept) return;                      // the same for all threads that sync
+    sync();
+    // every key that reaches what the tile kernel knew in the end
+    const uint32_t bound = class_bound<S>(p.largest + row * S, p.listed);
+    constexpr int U = 4;
+    for (int l0 = part * 32; l0 < p.lists; l0 += 32 * W) {
         const int l = l0 + lane;
-        const int count = l < p.lists && CHK((int64_t)l * p.Mp + row, 1, (int64_t)p.lists * p.Mp)
-            ? p.list_count[(int64_t)l * p.Mp + row] : 0;
-        const int most = __reduce_max_sync(0xffffffffu, count);
-        for (int e = 0; e < most; ++e) {
-            const uint64_t key = e < count ? p.list[((int64_t)l * p.listed + e) * p.Mp + row] : 0ull;
-            const bool take = e < count && (uint32_t)(key >> 32) >= bound;
-            const unsigned mask = __ballot_sync(0xffffffffu, take);
-            const int at = n + __popc(mask & below);
-            if (take && at < kFound) found[at] = key;
-            n += __popc(mask);
+        const unsigned long long *from = list_of(p, row, l < p.lists ? l : 0);
+        const int count = l < p.lists ? (int)from[0] : 0;
+        for (int e = 0; e < count; e += U) {
+            uint64_t key[U];
+#pragma unroll
+            for (int q = 0; q < U; ++q) key[q] = e + q < count ? from[1 + e + q] : 0ull;
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+                if (key[q] != 0ull && (uint32_t)(key[q] >> 32) >= bound) {
+                    const int at = atomicAdd(&found_count, 1);    // in any order: places come from comparisons
+                    if (at < kFound) found[at] = key[q];
+                }
         }
     }
-    __syncwarp();
+    sync();
     // lane e: the key of place e
+    const int n = found_count, places = n < p.listed ? n : p.listed;
     uint64_t mine = 0ull;
-    int places = n < p.listed ? n : p.listed;
     if (n <= kFound) {
-        const uint64_t u = lane < n ? found[lane] : 0ull, v = lane + 32 < n ? found[lane + 32] : 0ull;
-        int ru = 0, rv = 0;
+        // a key's place: the number of keys above it
+        uint64_t u[Q];
+        int above[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            u[q] = q * 32 + lane < n ? found[q * 32 + lane] : 0ull;
+            above[q] = 0;
+        }
         for (int i = 0; i < n; ++i) {
             const uint64_t w = found[i];
-            ru += w > u ? 1 : 0;
-            rv += w > v ? 1 : 0;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) above[q] += w > u[q] ? 1 : 0;
         }
-        __syncwarp();
-        if (u != 0ull && ru < places) found[ru] = u;
-        if (v != 0ull && rv < places) found[rv] = v;
-        __syncwarp();
+        sync();
+        if (part == 0) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                if (u[q] != 0ull && above[q] < places) found[above[q]] = u[q];
+        }
+        sync();
         if (lane < places) mine = found[lane];
     } else {
-        // many equal logits: the largest key below the last one, over and over
+        // too many for that (equal logits): the largest key below the last one, over and over
         uint64_t last = ~0ull;
         for (int e = 0; e < places; ++e) {
             uint64_t best = 0ull;
             for (int l = lane; l < p.lists; l += 32) {
-                const int count = p.list_count[(int64_t)l * p.Mp + row];
+                const unsigned long long *from = list_of(p, row, l);
+                const int count = (int)from[0];
                 for (int i = 0; i < count; ++i) {
-                    const uint64_t key = p.list[((int64_t)l * p.listed + i) * p.Mp + row];
+                    const uint64_t key = from[1 + i];
                     if (key < last && key > best) best = key;
                 }
             }
@@ -159,24 +189,31 @@ __device__ __forceinline__ void join_top(const Plan &p, const JoinArgs &a, int64
             last = best;
         }
     }
-    // their logits, four at a time; lane e keeps that of place e
+    // their logits again, G at a time; lane e then has that of place e
     const uint32_t entry = ~(uint32_t)mine;
+    const int64_t m = p.rowmap[row];
     const int nvec = (int)(p.D / 8);
     const uint4 *x = static_cast<const uint4 *>(a.x) + m * nvec, *table = static_cast<const uint4 *>(a.table);
-    float hi = 0.0f, lo = 0.0f;
-    for (int e = 0; e < places; e += 4) {
-        int64_t rows[4];
-        float h[4], l[4];
+    constexpr int G = W == 1 ? 4 : 1;
+    for (int e = part * G; e < places; e += W * G) {
+        int64_t rows[G];
+        float h[G], l[G];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < G; ++q) {
             const uint32_t r = __shfl_sync(0xffffffffu, entry, e + q < places ? e + q : e);
             rows[q] = CHK(r, 1, p.V) ? r : 0;
         }
-        exact_logits<F16, 4>(x, table, rows, nvec, h, l);
+        exact_logits<F16, G>(x, table, rows, nvec, h, l);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (lane == e + q) { hi = h[q]; lo = l[q]; }
+        for (int q = 0; q < G; ++q)
+            if (lane == q && e + q < places) {
+                hi_all[mine_at][e + q] = h[q];
+                lo_all[mine_at][e + q] = l[q];
+            }
     }
+    sync();
+    if (part != 0) return;
+    float hi = lane < places ? hi_all[mine_at][lane] : 0.0f, lo = lane < places ? lo_all[mine_at][lane] : 0.0f;
     if (!(fabsf(hi) < INFINITY) || lo != lo) lo = 0.0f;
     if (hi != hi) hi = -INFINITY;
     int rank = 0;
@@ -186,32 +223,37 @@ __device__ __forceinline__ void join_top(const Plan &p, const JoinArgs &a, int64
         const bool same = ho == hi && lo_o == lo;
         rank += ho > hi || (ho == hi && lo_o > lo) || (same && eo < entry) ? 1 : 0;
     }
-    if (lane < places && rank < p.top && CHK(m * p.top + rank, 1, p.M * p.top)) {
-        a.top_ids[m * p.top + rank] = (int64_t)entry;
-        a.top_logp[m * p.top + rank] = (float)(((double)hi + (double)lo) * a.inv_t - (double)lse);
+    // The logarithms from the same logits as log_probs and lse, whose errors have
+    // the same sign: those of the difference mostly cancel.  Not increasing: where
+    // the order was decided by less than these errors, the one before counts.
+    const float lse = a.lse[m];
+    float z = unordered((uint32_t)(mine >> 32)) * p.inv_t - lse;
+    int from = lane;                                      // the lane whose rank is this lane's number
+    for (int i = 0; i < places; ++i)
+        if (__shfl_sync(0xffffffffu, rank, i) == lane) from = i;
+    z = __shfl_sync(0xffffffffu, z, from);
+    const uint32_t id = __shfl_sync(0xffffffffu, entry, from);
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const float before = __shfl_up_sync(0xffffffffu, z, o);
+        if (lane >= o) z = fminf(z, before);
     }
-    // fewer logits than places: the rest of them are -infinity
-    if (lane >= places && lane < p.top) {
-        a.top_ids[m * p.top + lane] = -1;
-        a.top_logp[m * p.top + lane] = lse != lse ? lse : -INFINITY;
+    if (lane < p.top && CHK(m * p.top + lane, 1, p.M * p.top)) {
+        // fewer logits than places: the rest of them are -infinity
+        a.top_ids[m * p.top + lane] = lane < places ? (int64_t)id : -1;
+        a.top_logp[m * p.top + lane] = lse != lse ? lse : lane < places ? z : -INFINITY;
     }
 }
 
 // 32 positions per CTA.  32 threads per position take every 32nd triple, in
-// order, and theirs are joined in thread order; then a warp per position joins
-// its alternatives.
-template <bool F16>
-__global__ void __launch_bounds__(32 * kJoinRows)
+// order, and theirs are joined in thread order.
+__global__ void __launch_bounds__(1024)
 logp_join_kernel(const Plan p, const JoinArgs a) {
-    __shared__ union {
-        struct { float max, sum, weighted; } part[32][33];
-        uint64_t found[kJoinRows][kFound];
-    } sh;
-    __shared__ float lse_of[kJoinRows];
+    __shared__ struct { float max, sum, weighted; } part[32][33];
     wait_prior_grid();
     allow_next_grid();
     const int r = threadIdx.x % 32, t = threadIdx.x / 32;
-    const int64_t first = (int64_t)blockIdx.x * kJoinRows, row = first + r;
+    const int64_t first = (int64_t)blockIdx.x * 32, row = first + r;
     const int kept = p.head->kept;
     if (first >= kept) return;                            // CTA-uniform
     float mx = -INFINITY, sum = 0.0f, weighted = 0.0f;
@@ -232,22 +274,25 @@ logp_join_kernel(const Plan p, const JoinArgs a) {
         const float2 q = p.pairs[at];
         join(q.x, q.y, p.weighted[at]);
     }
-    sh.part[t][r] = {mx, sum, weighted};
+    part[t][r] = {mx, sum, weighted};
     __syncthreads();
-    if (t == 0) {
-        for (int i = 1; i < 32; ++i) join(sh.part[i][r].max, sh.part[i][r].sum, sh.part[i][r].weighted);
+    if (t == 0 && row < kept) {
+        for (int i = 1; i < 32; ++i) join(part[i][r].max, part[i][r].sum, part[i][r].weighted);
         const float l = (mx + log2f(sum)) * kLn2;
-        lse_of[r] = l;
-        if (row < kept) {
-            const int64_t m = p.rowmap[row];
-            a.lse[m] = l;
-            a.log_probs[m] = p.zt[row] * p.inv_t - l;
-            a.entropy[m] = (log2f(sum) - __fdiv_rn(weighted, sum)) * kLn2;
-        }
+        const int64_t m = p.rowmap[row];
+        a.lse[m] = l;
+        a.log_probs[m] = p.zt[row] * p.inv_t - l;
+        a.entropy[m] = (log2f(sum) - __fdiv_rn(weighted, sum)) * kLn2;
     }
-    if (p.top == 0) return;
-    __syncthreads();
-    if (first + t < kept) join_top<F16>(p, a, first + t, lse_of[t], sh.found[t]);
+}
+
+template <bool F16>
+cudaError_t launch_top(const Plan &p, const JoinArgs &j, int sms, cudaStream_t s) {
+    const bool wide = p.M <= sms * (kTopThreads / 32), few = p.listed <= kTopFew;
+    const int64_t rows = wide ? 1 : kTopThreads / 32;
+    return launch_k(wide ? (few ? logp_top_kernel<F16, true, 8> : logp_top_kernel<F16, false, 8>)
+                         : (few ? logp_top_kernel<F16, true, 1> : logp_top_kernel<F16, false, 1>),
+                    dim3((unsigned)((p.M + rows - 1) / rows)), dim3(kTopThreads), 0, s, 1, p, j);
 }
 
 carbon_status_t check_logp(const void *x, const void *table, const int64_t *tokens, int64_t M, int64_t D, int64_t V,
@@ -315,13 +360,16 @@ carbon_status_t carbon_linear_logp_fwd(float *log_probs, float *entropy, float *
     cudaError_t err = launch_prepare<true>(p, a, x, s);
     if (err == cudaSuccess)
         err = top == 0 ? launch_tiles<false, true, 0>(p, table, nullptr, sms, s)
-            : p.listed <= 12 ? launch_tiles<false, true, 12>(p, table, nullptr, sms, s)
+            : p.listed <= kTopFew ? launch_tiles<false, true, kTopFew>(p, table, nullptr, sms, s)
                              : launch_tiles<false, true, 32>(p, table, nullptr, sms, s);
     if (err == cudaSuccess) {
-        const JoinArgs j = {log_probs, lse, entropy, top_log_probs, top_ids, x, table, 1.0 / (double)temperature};
+        const JoinArgs j = {log_probs, lse, entropy, top_log_probs, top_ids, x, table};
         count_launch();
-        err = launch_k(p.f16 ? logp_join_kernel<true> : logp_join_kernel<false>, dim3((unsigned)((M + kJoinRows - 1) / kJoinRows)),
-                       dim3(32 * kJoinRows), 0, s, 1, p, j);
+        err = launch_k(logp_join_kernel, dim3((unsigned)((M + 31) / 32)), dim3(1024), 0, s, 1, p, j);
+        if (err == cudaSuccess && top > 0) {
+            count_launch();
+            err = p.f16 ? launch_top<true>(p, j, sms, s) : launch_top<false>(p, j, sms, s);
+        }
     }
     return note_cuda(err);
 }

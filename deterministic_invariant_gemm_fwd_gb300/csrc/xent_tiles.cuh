@@ -235,7 +235,8 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
                         p.g1[pos] = g;
                     }
                 } else if (LOGP && p.top > 0) {
-                    p.bound[pos] = 0u;
+                    p.floor[pos] = 0u;
+                    for (int i = 0; i < top_classes(p.listed); ++i) p.largest[(int64_t)pos * top_classes(p.listed) + i] = 0u;
                 }
             } else if (!keep && !p.grad) {
                 a.losses[m] = 0.0f;
@@ -625,17 +626,20 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 struct TopList {
     uint32_t at;             // this thread's column; the next key kEpiWarps * 256 bytes on
     int k, n, least;
-    float floor, cut;        // only larger ones are taken: floor from elsewhere, cut from here as well
+    float floor, cut;        // only larger ones are taken: floor from other threads, cut from here as well
     __device__ uint32_t addr(int e) const { return at + (uint32_t)e * (kEpiWarps * 32 * 8); }
     __device__ uint64_t get(int e) const {
         uint64_t v;
         asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v) : "r"(addr(e)) : "memory");
         return v;
     }
-    // bound: a value that k logits of the row reach, 0 where none is known
-    __device__ void reset(uint32_t bound, bool dead) {
+    __device__ void reset() {
         n = 0;
-        cut = floor = dead ? INFINITY : bound == 0u ? -INFINITY : unordered(bound - 1u);
+        cut = floor;
+    }
+    __device__ void raise(float f) {
+        floor = fmaxf(floor, f);
+        cut = fmaxf(cut, f);
     }
     template <int LIST>
     __device__ void add(float z, int entry) {
@@ -653,6 +657,48 @@ struct TopList {
         cut = fmaxf(floor, unordered((uint32_t)(low >> 32)));
     }
 };
+
+// The k-th largest of S values, 1 <= k <= S: a bitonic sort.
+template <int S>
+__device__ __forceinline__ uint32_t kth_largest(uint32_t (&v)[S], int k) {
+#pragma unroll
+    for (int size = 2; size <= S; size *= 2)
+#pragma unroll
+        for (int step = size / 2; step > 0; step /= 2)
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+                if ((i & step) == 0) {
+                    const uint32_t hi = max(v[i], v[i + step]), lo = min(v[i], v[i + step]);
+                    const bool down = (i & size) == 0;
+                    v[i] = down ? hi : lo;
+                    v[i + step] = down ? lo : hi;
+                }
+    uint32_t t = 0u;
+#pragma unroll
+    for (int i = 0; i < S; ++i) t = max(t, i >= k - 1 ? v[i] : 0u);
+    return t;
+}
+
+// The number just below an ordered one; -infinity for 0, which stands for none.
+__device__ __forceinline__ float just_below(uint32_t t) {
+    if (t == 0u) return -INFINITY;
+    const float below = unordered(t - 1u);
+    return below == 0.0f ? -0x1p-149f : below;            // 0 is not above -0
+}
+
+// A logit below the k-th largest of the largest logits of S classes of entries is
+// none of the row's k largest.  (Of 16 classes the 12th largest is about the 21st
+// largest logit of all entries so far.)  Ordered; 0: fewer than k classes so far.
+template <int S>
+__device__ __forceinline__ uint32_t class_bound(const unsigned int *largest, int k) {
+    uint32_t v[S];
+#pragma unroll
+    for (int i = 0; i < S; i += 4) {
+        const uint4 q = __ldcg(reinterpret_cast<const uint4 *>(largest + i));
+        v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+    }
+    return kth_largest(v, k);
+}
 
 // v[i] of 32 values, i per thread: five rounds of halves.
 __device__ __forceinline__ float select32(const uint32_t *v, int i) {
@@ -676,6 +722,9 @@ __device__ __forceinline__ void logp_rows(const Plan &p, const Unit &o, uint32_t
     if (g >= o.width || o.n0 + g >= p.V) return;
     const int tgt = p.tgt[row] - o.n0;
     float mx = -INFINITY, sum = 0.0f, weighted = 0.0f;    // of z log2(e) / temperature
+    float largest = -INFINITY;                            // logit of the chunks that had a candidate
+    // only what exceeds it can raise the floor
+    const float floor = LIST > 0 ? list.floor : 0.0f;
 #pragma unroll 1
     for (int c = g; c < g + kGroup && o.n0 + c < p.V; c += 64) {
         uint32_t r[64];
@@ -695,6 +744,15 @@ __device__ __forceinline__ void logp_rows(const Plan &p, const Unit &o, uint32_t
         for (int i = 1; i < 64; ++i) top = fmaxf(top, __uint_as_float(r[i]));
         if constexpr (LIST > 0) {
             if (__any_sync(0xffffffffu, top > list.cut)) {
+                if (LIST <= kTopFew && __any_sync(0xffffffffu, list.cut == -INFINITY)) {
+                    // nothing is known: these entries' own 16 classes of four say what can be left out
+                    uint32_t v[kTopClassesFew];
+#pragma unroll
+                    for (int i = 0; i < kTopClassesFew; ++i)
+                        v[i] = ordered(fmaxf(fmaxf(__uint_as_float(r[i]), __uint_as_float(r[i + 16])),
+                                             fmaxf(__uint_as_float(r[i + 32]), __uint_as_float(r[i + 48]))));
+                    list.raise(just_below(kth_largest(v, list.k)));
+                }
 #pragma unroll
                 for (int h = 0; h < 64; h += 32) {
                     uint32_t more = 0u;
@@ -707,6 +765,7 @@ __device__ __forceinline__ void logp_rows(const Plan &p, const Unit &o, uint32_t
                         more &= more - 1u;
                     }
                 }
+                largest = fmaxf(largest, top);
             }
         }
         const float now = fmaxf(mx, top * p.zscale), ref = now == -INFINITY ? 0.0f : now;
@@ -728,18 +787,24 @@ __device__ __forceinline__ void logp_rows(const Plan &p, const Unit &o, uint32_t
         p.pairs[at] = make_float2(mx, sum);
         p.weighted[at] = weighted;
     }
+    if constexpr (LIST > 0) {
+        constexpr int S = LIST <= kTopFew ? kTopClassesFew : kTopClassesMany;
+        if (largest > floor && CHK(row, 1, p.Mp))
+            atomicMax(p.largest + (int64_t)row * S + (o.n0 + g) / kGroup % S, ordered(largest));
+    }
 }
 
-// The end of a span: its keys for the join, and what they say about the row's.
+__device__ __forceinline__ unsigned long long *list_of(const Plan &p, int64_t row, int64_t l) {
+    return p.list + (row * p.lists + l) * (p.listed + 1);
+}
+
+// The end of a span: its keys, for the join.
 __device__ __forceinline__ void put_list(const Plan &p, const Unit &o, int row, int half, const TopList &list) {
     if (half >= p.lwidth / kGroup) return;                // one list per row
-    const int64_t l = (int64_t)(o.left >> kSpanShift) * (p.lwidth / kGroup) + half;
-    const int most = __reduce_max_sync(0xffffffffu, list.n);
-    for (int e = 0; e < most; ++e)
-        if (e < list.n && CHK((l * p.listed + e) * p.Mp + row, 1, (int64_t)p.lists * p.listed * p.Mp))
-            p.list[(l * p.listed + e) * p.Mp + row] = list.get(e);
-    if (CHK(l * p.Mp + row, 1, (int64_t)p.lists * p.Mp)) p.list_count[l * p.Mp + row] = list.n;
-    if (list.n == list.k && CHK(row, 1, p.Mp)) atomicMax(p.bound + row, (uint32_t)(list.get(list.least) >> 32));
+    unsigned long long *to = list_of(p, row, (int64_t)(o.left >> kSpanShift) * (p.lwidth / kGroup) + half);
+    if (!CHK(to - p.list, p.listed + 1, p.Mp * p.lists * (p.listed + 1))) return;
+    to[0] = (unsigned long long)list.n;
+    for (int e = 0; e < list.n; ++e) to[1 + e] = list.get(e);
 }
 
 template <bool GRAD, bool F16, bool LOGP, int LIST, class C>
@@ -764,7 +829,25 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
         const int row0 = o.m0 + (int)c.rank * 128 + quarter * 32, row = row0 + lane;
         const int c0 = half * (o.width / 2), c1 = c0 + o.width / 2;
         float lse2 = 0.0f, rfac = 0.0f, slope = 0.0f, hit = 0.0f;
-        if (LIST > 0 && (o.left & kFirst) != 0) list.reset(__ldcg(p.bound + row), p.tgt[row] < 0);
+        if constexpr (LIST > 0) {
+            // What other spans have proved.  Classes are looked at where a span
+            // starts, and as long as nothing is known; their result is left for
+            // the other threads of the row, which a tile costs one load.
+            constexpr int S = LIST <= kTopFew ? kTopClassesFew : kTopClassesMany;
+            const bool first = (o.left & kFirst) != 0;
+            if (first) {
+                list.floor = p.tgt[row] < 0 ? INFINITY : -INFINITY;
+                list.reset();
+            }
+            list.raise(just_below(__ldcg(p.floor + row)));
+            if (__any_sync(0xffffffffu, first || list.floor == -INFINITY)) {
+                const uint32_t t = class_bound<S>(p.largest + (int64_t)row * S, p.listed);
+                if (just_below(t) > list.floor) {
+                    list.raise(just_below(t));
+                    if (CHK(row, 1, p.Mp)) atomicMax(p.floor + row, t);
+                }
+            }
+        }
         int tgt = -1;
         bool dead = false;                                 // a row without a position
         if (GRAD && o.type == UNIT_L) {

@@ -29,6 +29,8 @@ constexpr int64_t kGBytes = 64ll << 20;
 constexpr int64_t kSlotBytes = 64ll << 20;    // dx: the pieces' sums side by side up to this size, else added in place
 constexpr int kTopSpare = 4;             // alternatives kept beyond those asked for, see linear_logprob.cu
 constexpr int kTopMost = 32 - kTopSpare;
+constexpr int kTopFew = 12, kTopClassesFew = 16, kTopClassesMany = 32;
+XENT_HD inline int top_classes(int listed) { return listed <= kTopFew ? kTopClassesFew : kTopClassesMany; }
 constexpr int kSpan = 8;                 // tiles that a pair takes one after another for the alternatives, at most
 constexpr int64_t kCountAhead = 16384;   // longer lists of positions are counted by a kernel of their own
 
@@ -71,9 +73,9 @@ struct Plan {
     int top, listed;                     // alternatives asked for and kept
     int span, spans;                     // tiles of a row tile that form a unit of the ticket, and their number
     int lists;                           // lists of candidates per row: one per span and column half
-    unsigned int *bound;                 // [Mp]: a value (ordered) that at least `listed` logits of the row reach, or 0
-    unsigned long long *list;            // [lists][listed][Mp]: (ordered logit, ~entry)
-    int *list_count;                     // [lists][Mp]
+    unsigned int *largest;               // [Mp][top_classes]: largest logits (ordered) so far of classes of entries; 0: none
+    unsigned int *floor;                 // [Mp]: a value (ordered) that `listed` logits of the row reach, or 0
+    unsigned long long *list;            // [Mp][lists][1 + listed]: the number of keys, and keys (ordered logit, ~entry)
 };
 
 // 32-bit words that start at zero: ticket, joined and the counters.
@@ -149,15 +151,17 @@ inline int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, b
         if (p.logp) p.weighted = reinterpret_cast<float *>(take(4 * (int64_t)p.vocab_groups * p.Mp));
         if (p.top > 0) {
             p.listed = p.top + kTopSpare;
-            // long spans start few lists; about eight spans for each pair of
-            // CTAs keep the pairs busy to the end
-            const int64_t tiles = (V + p.lwidth - 1) / p.lwidth, span = p.Mp / kBM * tiles / (8 * 76);
+            // Long spans start few lists: one for each pair of CTAs where that is
+            // no more than kSpan tiles, else three or more
+            const int64_t tiles = (V + p.lwidth - 1) / p.lwidth, all = p.Mp / kBM * tiles;
+            int64_t span = (all + 75) / 76;
+            if (span > kSpan) span = all / (3 * 76);
             p.span = (int)(span < 1 ? 1 : span > kSpan ? kSpan : span);
             p.spans = (int)((tiles + p.span - 1) / p.span);
             p.lists = p.spans * (p.lwidth / kGroup);
-            p.bound = reinterpret_cast<unsigned int *>(take(4 * p.Mp));
-            p.list_count = reinterpret_cast<int *>(take(4 * (int64_t)p.lists * p.Mp));
-            p.list = reinterpret_cast<unsigned long long *>(take(8 * (int64_t)p.lists * p.listed * p.Mp));
+            p.largest = reinterpret_cast<unsigned int *>(take(4 * p.Mp * top_classes(p.listed)));
+            p.floor = reinterpret_cast<unsigned int *>(take(4 * p.Mp));
+            p.list = reinterpret_cast<unsigned long long *>(take(8 * (int64_t)p.lists * (p.listed + 1) * p.Mp));
         }
     }
     if (out) *out = p;

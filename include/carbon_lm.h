@@ -190,8 +190,9 @@ int64_t carbon_linear_xent_bwd_workspace(int64_t M, int64_t D, int64_t V);
  *
  * Order of the alternatives: the top + 4 largest logits as the tensor cores form
  * them (their error: see carbon_linear_xent_fwd), ordered by their logits as
- * sums of the exact products in about 48 bits, equal ones by the lower entry;
- * top_log_probs come from these sums.
+ * sums of the exact products in about 48 bits, equal ones by the lower entry.
+ * top_log_probs come from the tensor cores' logits, as log_probs do (the same bits
+ * for the same entry), but are never above the one before.
  *
  * Errors of log_probs and lse: those of the loss above, of z / temperature;
  * entropy: (16 + log2 V) 2^-23 (entropy + 1) and 2 (entropy + 1) times the largest
