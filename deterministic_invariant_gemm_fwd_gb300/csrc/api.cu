@@ -45,6 +45,9 @@ carbon_status_t current_device(int *device, int *sm_count) {
         g_device_sms[dev].store(cached, std::memory_order_release);
     }
     if (cached < 0) return CARBON_ERR_UNSUPPORTED;
+    // A thread's first CUDA call may be this one (an autograd worker's): the
+    // driver's tensor-map encoder needs a context that is bound to the thread.
+    if ((err = cudaSetDevice(dev)) != cudaSuccess) return note_cuda(err);
     if (device) *device = dev;
     if (sm_count) *sm_count = cached;
     return CARBON_OK;

@@ -280,3 +280,18 @@ def test_autograd_and_module():
     (gx,) = torch.autograd.grad(layer(x, ids).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="no derivative"):
         gx.sum().backward()
+
+
+def test_first_call_of_a_thread():
+    """Tensor maps are encoded in a thread that has made no CUDA call yet."""
+    import threading
+    c = Case(64, 64, 72, 2, 8, "bf16", 13)
+    y, u = c.fwd()
+    ref = c.bwd(u)
+    dx = cg.linear_dx(c.dy, c.w, tier="tc")
+    for call, want in ((lambda: c.bwd(u), ref), (lambda: (cg.linear_dx(c.dy, c.w, tier="tc"),), (dx,))):
+        got = []
+        t = threading.Thread(target=lambda: got.append(call()))
+        t.start()
+        t.join()
+        assert got and all(same_bits(p, q) for p, q in zip(got[0], want))
