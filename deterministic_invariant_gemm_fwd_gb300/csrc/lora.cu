@@ -12,12 +12,12 @@
 // hold, and its bits do not depend on its neighbours.
 //
 //   lora_shrink_kernel   u or du: 128 rows and a piece of the reduction per CTA, up
-//                        to eight pieces as a cluster that adds them in order.
+//                        to eight pieces as a cluster that adds them in order; other
+//                        CTAs list the adapters of 256 rows and sort the rows by adapter.
 //   lora_layer_kernel    y or dx: a pair of CTAs per tile of 256 rows, persistent;
 //                        behind the layer's own k-blocks the adapters' are added to
 //                        the same accumulator: one rounding, no second pass over y.
-//   lora_order_kernel    rows sorted by adapter.
-//   lora_grads_kernel    dA and dB: 128 columns and up to 512 rows of one adapter per
+//   lora_grads_kernel    dA and dB: 128 columns and up to 1024 rows of one adapter per
 //                        CTA, gathered by row number (no other row enters a sum).
 //   lora_join_kernel     adds the pieces of adapters with more rows, in order.
 //
@@ -43,7 +43,7 @@ constexpr int kMaxRank = 128;
 constexpr int kBK = 64;                               // k-block: one 128-byte swizzle row
 constexpr int kPlanes = 3;                            // hi, lo, lo 2^11
 constexpr float kLoScale = 2048.0f;
-constexpr int kPiece = 512;                           // rows per piece of an adapter's gradient
+constexpr int kPiece = 1024;                          // rows per piece of an adapter's gradient
 
 __device__ __forceinline__ bool give_up(volatile uint32_t *abort_flag) {
     *abort_flag = 1u;
@@ -96,7 +96,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t local, uint32_t rank) {
 // ---- which adapters a tile's rows name ----------------------------------------------
 
 template <int ROWS>
-struct Groups {
+struct alignas(16) Groups {
     int id[ROWS];                        // a row's adapter, or -1
     int first[ROWS];                     // the tile's first row with the same one
     int place[ROWS];                     // of a first row: its adapter's place in the list
@@ -121,8 +121,12 @@ __device__ __forceinline__ void find_groups(Groups<ROWS> &g, const int64_t *ids,
     __syncthreads();
     for (int i = t; i < ROWS; i += nt) {
         const int id = g.id[i];
-        int j = 0;
-        while (g.id[j] != id) ++j;                        // ends at i at the latest
+        int j = g.id[0] == id ? 0 : i;
+        if (j != 0 && id >= 0)
+            for (int q = 0; q < ROWS; q += 4) {           // independent loads: a search that stops waits for each
+                const int4 v = *reinterpret_cast<const int4 *>(g.id + q);
+                j = min(min(j, v.x == id ? q : j), min(min(v.y == id ? q + 1 : j, v.z == id ? q + 2 : j), v.w == id ? q + 3 : j));
+            }
         g.first[i] = id < 0 ? -1 : j;
     }
     __syncthreads();
@@ -166,37 +170,87 @@ struct ShrinkArgs {
     int64_t M, n;
     int rp;                              // rank, rounded up to 16
     int k_blocks, per_piece, pieces;
+    int stages_b;                        // stages of adapters
+    // clusters ahead of those of the rows: lists of 256 rows, then rows in the order of adapters
+    int extra, wide_tiles;
+    int64_t sorted;                      // adapters to sort rows by: n, or 0
+    int *order, *counts, *starts;
 };
 
 constexpr int kShrinkThreads = 192;      // producer, MMA issuer, epilogue
-constexpr int kShrinkA = 3, kShrinkB = 4;             // stages of rows and of adapters
+constexpr int kShrinkA = 3, kShrinkB = 12;            // stages of rows, and of adapters at most
 
 struct ShrinkLayout {
-    uint32_t b_stage, b, groups, wide, bars, total;
+    uint32_t b_stage, b, groups, bars, total;
 };
-__host__ __device__ inline ShrinkLayout shrink_layout(bool bwd, int rp) {
+__host__ __device__ inline ShrinkLayout shrink_layout(bool bwd, int rp, int stages_b) {
     ShrinkLayout l;
     l.b_stage = bwd ? (uint32_t)rp * 128u : (rp > 64 ? 2u : 1u) * kBlock;
     l.b = kShrinkA * 2 * kBlock;
-    uint32_t ring = l.b + kShrinkB * l.b_stage;
+    uint32_t ring = l.b + (uint32_t)stages_b * l.b_stage;
     const uint32_t partial = 128u * (uint32_t)(rp + 4) * 4u;       // over the ring, once it has been used
     if (ring < partial) ring = partial;
     l.groups = ring;
-    l.wide = l.groups + (uint32_t)sizeof(Groups<128>);
-    l.bars = (l.wide + (uint32_t)sizeof(Groups<256>) + 15u) / 16u * 16u;
+    l.bars = (l.groups + (uint32_t)sizeof(Groups<128>) + 15u) / 16u * 16u;
     l.total = l.bars + (2 * kShrinkA + 2 * kShrinkB + 1) * 8 + 16 + 1024;
     return l;
 }
+static_assert(sizeof(Groups<256>) <= kShrinkA * 2 * kBlock, "lists of 256 rows are made where the ring lies");
+
+// order[starts[i] ..]: the rows of adapter i, ascending.  By a CTA: each warp
+// takes a run of rows, twice.
+__device__ __forceinline__ void sort_rows(const ShrinkArgs &a, int64_t mine, int *part) {
+    constexpr int W = kShrinkThreads / 32, U = 8;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t per = ((a.M + W - 1) / W + 31) / 32 * 32, from = warp * per, to = min(from + per, a.M);
+    int before = 0, here = 0;
+    for (int64_t m = from + lane; m - lane < to; m += 32 * U) {
+        int64_t id[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q) id[q] = m + 32 * q < to ? a.ids[m + 32 * q] : -1;
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            before += id[q] >= 0 && id[q] < mine ? 1 : 0;
+            here += id[q] == mine ? 1 : 0;
+        }
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    here = __reduce_add_sync(0xffffffffu, here);
+    if (lane == 0) { part[warp] = before; part[W + warp] = here; }
+    __syncthreads();
+    int start = 0, at = 0, count = 0;
+    for (int w = 0; w < W; ++w) {
+        start += part[w];
+        at += w < warp ? part[W + w] : 0;
+        count += part[W + w];
+    }
+    if (threadIdx.x == 0 && CHK(mine, 1, a.n)) { a.counts[mine] = count; a.starts[mine] = start; }
+    if (here == 0) return;                                // warp-uniform
+    at += start;
+    for (int64_t m = from + lane; m - lane < to; m += 32 * U) {
+        int64_t id[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q) id[q] = m + 32 * q < to ? a.ids[m + 32 * q] : -1;
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const unsigned hit = __ballot_sync(0xffffffffu, id[q] == mine);
+            const int to_at = at + __popc(hit & ((1u << lane) - 1u));
+            if (id[q] == mine && CHK(to_at, 1, a.M)) a.order[to_at] = (int)(m + 32 * q);
+            at += __popc(hit);
+        }
+    }
+}
 
 // rows [128 t, ..) of X times P_i, X [M][R]; P_i is A_i [R][r] or the transpose of
-// B_i [r][R] (BWD).  Cluster: the pieces of the reduction.
+// B_i [r][R] (BWD).  Cluster: the pieces of the reduction.  The CTAs of the first
+// clusters make what later kernels need of the adapters' numbers.
 template <bool BWD, bool F16>
 __global__ void __launch_bounds__(kShrinkThreads)
 lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_p, const ShrinkArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const ShrinkLayout l = shrink_layout(BWD, a.rp);
+    const ShrinkLayout l = shrink_layout(BWD, a.rp, a.stages_b);
     const uint32_t sbase = smem_addr(smem), bars = sbase + l.bars;
     auto a_full = [&](int s) { return bars + 8u * s; };
     auto a_empty = [&](int s) { return bars + 8u * (kShrinkA + s); };
@@ -207,6 +261,25 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     volatile uint32_t *abort_flag = tmem_slot + 1;
     Groups<128> &g = *reinterpret_cast<Groups<128> *>(smem + l.groups);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int piece = a.pieces > 1 ? (int)cluster_rank() : 0, cluster = (int)blockIdx.x / a.pieces;
+    if (cluster < a.extra) {                              // the whole cluster: nothing here waits for its other CTAs
+        wait_prior_grid();
+        allow_next_grid();
+        const int64_t i = (int64_t)cluster * a.pieces + piece, sort = i - a.wide_tiles;
+        if (i < a.wide_tiles) {
+            Groups<256> &w = *reinterpret_cast<Groups<256> *>(smem);
+            find_groups(w, a.ids, i * kPairRows, a.M, a.n, true);
+            TileList &out = a.lists[i];
+            if (threadIdx.x == 0) out.count = w.count;
+            for (int e = threadIdx.x; e < w.count; e += kShrinkThreads) {
+                out.e[e].adapter = w.adapter[e];
+                for (int q = 0; q < 8; ++q) out.e[e].off[q] = w.off[e][q];
+            }
+        } else if (sort < a.sorted) {
+            sort_rows(a, sort, reinterpret_cast<int *>(smem));
+        }
+        return;
+    }
     const uint32_t cols = a.rp <= 32 ? 32u : a.rp <= 64 ? 64u : 128u;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kShrinkA; ++s) { mbar_init(a_full(s), 1); mbar_init(a_empty(s), 1); }
@@ -225,22 +298,32 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     wait_prior_grid();
     allow_next_grid();
 
-    const int piece = a.pieces > 1 ? (int)cluster_rank() : 0;
-    const int tile = (int)blockIdx.x / a.pieces;
-    const int64_t m0 = (int64_t)tile * 128;
-    find_groups(g, a.ids, m0, a.M, a.n, piece == 0);
+    const int64_t m0 = (int64_t)(cluster - a.extra) * 128;
     const int kb0 = min(piece * a.per_piece, a.k_blocks), kb1 = min(kb0 + a.per_piece, a.k_blocks);
+    // the first rows are on their way while the adapters are looked up
+    const int ahead = min(kb1 - kb0, kShrinkA);
+    if (threadIdx.x == 0)
+        for (int s = 0; s < ahead; ++s) {
+            mbar_arrive_expect_tx(a_full(s), 2 * kBlock);
+            tma_load_2d(sbase + s * 2 * kBlock, &map_x, a_full(s), (kb0 + s) * kBK, (int)m0);
+        }
+    __syncwarp();
+    find_groups(g, a.ids, m0, a.M, a.n, false);
     const bool any = g.count > 0 && kb1 > kb0;
 
     if (warp == 0) {
-        if (lane == 0 && any) {
+        if (lane == 0 && !any) {
+            for (int s = 0; s < ahead; ++s) mbar_wait(a_full(s), 0);
+        } else if (lane == 0) {
             int sa = 0, sb = 0;
             uint32_t pa = 0, pb = 0;
             bool ok = true;
             for (int kb = kb0; ok && kb < kb1; ++kb) {
-                if (!(ok = wait_bar(a_empty(sa), pa ^ 1u, abort_flag))) break;
-                mbar_arrive_expect_tx(a_full(sa), 2 * kBlock);
-                tma_load_2d(sbase + sa * 2 * kBlock, &map_x, a_full(sa), kb * kBK, (int)m0);
+                if (kb - kb0 >= kShrinkA) {
+                    if (!(ok = wait_bar(a_empty(sa), pa ^ 1u, abort_flag))) break;
+                    mbar_arrive_expect_tx(a_full(sa), 2 * kBlock);
+                    tma_load_2d(sbase + sa * 2 * kBlock, &map_x, a_full(sa), kb * kBK, (int)m0);
+                }
                 if (++sa == kShrinkA) { sa = 0; pa ^= 1u; }
                 for (int i = 0; i < g.count; ++i) {
                     if (!(ok = wait_bar(b_empty(sb), pb ^ 1u, abort_flag))) break;
@@ -252,7 +335,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                         tma_load_3d(dst, &map_p, b_full(sb), 0, kb * kBK, g.adapter[i]);
                         if (a.rp > 64) tma_load_3d(dst + kBlock, &map_p, b_full(sb), 64, kb * kBK, g.adapter[i]);
                     }
-                    if (++sb == kShrinkB) { sb = 0; pb ^= 1u; }
+                    if (++sb == a.stages_b) { sb = 0; pb ^= 1u; }
                 }
             }
             // every load has landed before the ring is used again, and before the CTA may exit
@@ -260,8 +343,8 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 if (--sa < 0) { sa = kShrinkA - 1; pa ^= 1u; }
                 if (!mbar_wait(a_full(sa), pa)) break;
             }
-            for (int i = 0; i < kShrinkB; ++i) {
-                if (--sb < 0) { sb = kShrinkB - 1; pb ^= 1u; }
+            for (int i = 0; i < a.stages_b; ++i) {
+                if (--sb < 0) { sb = a.stages_b - 1; pb ^= 1u; }
                 if (!mbar_wait(b_full(sb), pb)) break;
             }
         }
@@ -284,7 +367,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                         mma_masked(tmem, box_desc(rows, false, k), box_desc(p, !BWD, k), idesc, off,
                                    kb > kb0 || k > 0 ? 1u : 0u);
                     mma_commit(b_empty(sb));
-                    if (++sb == kShrinkB) { sb = 0; pb ^= 1u; }
+                    if (++sb == a.stages_b) { sb = 0; pb ^= 1u; }
                 }
                 if (!ok) break;
                 mma_commit(a_empty(sa));
@@ -349,17 +432,6 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         *reinterpret_cast<uint2 *>(u + at + 2 * a.rp) =
             make_uint2(pack2<F16>(lo[0] * kLoScale, lo[1] * kLoScale), pack2<F16>(lo[2] * kLoScale, lo[3] * kLoScale));
     }
-    // the lists of 256 rows for the layer's tiles
-    if (piece == a.pieces - 1 && tile % 2 == 0) {
-        Groups<256> &w = *reinterpret_cast<Groups<256> *>(smem + l.wide);
-        find_groups(w, a.ids, m0, a.M, a.n, false);
-        TileList &out = a.lists[tile / 2];
-        if (threadIdx.x == 0) out.count = w.count;
-        for (int i = threadIdx.x; i < w.count; i += kShrinkThreads) {
-            out.e[i].adapter = w.adapter[i];
-            for (int q = 0; q < 8; ++q) out.e[i].off[q] = w.off[i][q];
-        }
-    }
     cluster_sync_all();                                   // the others have read this CTA's piece
     if (warp == 1) {
         tc_fence_after();
@@ -375,6 +447,7 @@ struct LayerArgs {
     int64_t M, cols;
     int rp, k_blocks;
     int bn, tiles_n, tiles;
+    int batch;                           // adapters per stage
 };
 
 constexpr int kEpiWarps = 8;
@@ -393,10 +466,11 @@ struct LayerSmem {
     static_assert(kBytes <= 232448, "shared memory per block");
 };
 
-// The adapters of a tile, for a whole warp: f(adapter, off) for each; off only
-// where OFF.  false: f gave up.
+// The adapters of a tile in batches of G (a power of two up to 32), for a whole
+// warp: f(n, at, mine, off) for a batch of n whose adapters and disabled lanes
+// lanes at .. at + n - 1 hold (off only where OFF).  false: f gave up.
 template <bool OFF, typename F>
-__device__ __forceinline__ bool each_adapter(const TileList &list, int count, F f) {
+__device__ __forceinline__ bool each_batch(const TileList &list, int count, int G, F f) {
     const int lane = threadIdx.x % 32;
     for (int e0 = 0; e0 < count; e0 += 32) {
         const int e = e0 + lane < count ? e0 + lane : e0;
@@ -408,13 +482,8 @@ __device__ __forceinline__ bool each_adapter(const TileList &list, int count, F 
             off[0] = lo.x; off[1] = lo.y; off[2] = lo.z; off[3] = lo.w;
             off[4] = hi.x; off[5] = hi.y; off[6] = hi.z; off[7] = hi.w;
         }
-        const int n = min(32, count - e0);
-        for (int i = 0; i < n; ++i) {
-            uint32_t o[8];
-#pragma unroll
-            for (int w = 0; w < 8; ++w) o[w] = OFF ? __shfl_sync(0xffffffffu, off[w], i) : 0u;
-            if (!f(__shfl_sync(0xffffffffu, mine, i), o)) return false;
-        }
+        for (int at = 0; at < 32 && e0 + at < count; at += G)
+            if (!f(min(G, count - e0 - at), at, mine, off)) return false;
     }
     return true;
 }
@@ -464,6 +533,9 @@ lora_layer_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
     allow_next_grid();
     const int pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
     const int half = a.bn / 2;
+    // an adapter's part of a stage: 64 of the columns, or (BWD) of the rank, each
+    const uint32_t low_blocks = BWD ? (a.rp > 64 ? 2u : 1u) : (uint32_t)(half + 63) / 64u;
+    const uint32_t low_block = BWD ? (uint32_t)half * 128u : (uint32_t)a.rp * 128u;
 
     if (warp == 0) {
         int s = 0;
@@ -475,7 +547,7 @@ lora_layer_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
             const int rows = (int)(m0 + rank * 128), n0 = t % a.tiles_n * a.bn + (int)rank * half;
             const bool second = m0 + 128 < a.M;           // CTA 1 has rows (else none are loaded: nothing reads what the MMA makes of them)
             const bool load_a = rank == 0 || second;
-            const uint32_t b_bytes = (uint32_t)half * 128u;
+            const uint32_t b_bytes = BWD ? (uint32_t)half * 128u : (uint32_t)(half + 63) / 64u * kBlock;
             const uint32_t bytes = (second ? 2u : 1u) * 2u * kBlock + 2u * b_bytes;
             for (int kb = 0; kb < a.k_blocks; ++kb) {
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(empty(s), ph ^ 1u, abort_flag)))) break;
@@ -509,17 +581,18 @@ lora_layer_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
                     tma_load_pair(sbase + L::kU + q * 2 * kBlock, &map_u, map_rank(ufull, 0), q * 64, rows);
             }
             __syncwarp();
-            const uint32_t blocks = BWD ? (a.rp > 64 ? 2u : 1u) : (uint32_t)half / 64u;
-            const uint32_t block = BWD ? b_bytes : (uint32_t)a.rp * 128u;
-            ok = each_adapter<false>(list, count, [&](int adapter, const uint32_t (&)[8]) {
+            ok = each_batch<false>(list, count, a.batch, [&](int n, int at, int mine, const uint32_t (&)[8]) {
                 if (!__all_sync(0xffffffffu, wait_bar(empty(s), ph ^ 1u, abort_flag))) return false;
-                const uint32_t sb = sbase + s * kStageBytes, bar = map_rank(full(s), 0);
-                if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(full(s), 2u * blocks * block);
-                    for (uint32_t q = 0; q < blocks; ++q) {
-                        if (BWD) tma_load_pair_3d(sb + q * block, &map_p, bar, (int)q * 64, n0, adapter);
-                        else tma_load_pair_3d(sb + q * block, &map_p, bar, n0 + (int)q * 64, 0, adapter);
-                    }
+                const uint32_t bar = map_rank(full(s), 0);
+                if (rank == 0 && elect_one()) mbar_arrive_expect_tx(full(s), 2u * (uint32_t)n * low_blocks * low_block);
+                for (int i = 0; i < n; ++i) {
+                    const int adapter = __shfl_sync(0xffffffffu, mine, at + i);
+                    const uint32_t sb = sbase + s * kStageBytes + (uint32_t)i * low_blocks * low_block;
+                    if (elect_one())
+                        for (uint32_t q = 0; q < low_blocks; ++q) {
+                            if (BWD) tma_load_pair_3d(sb + q * low_block, &map_p, bar, (int)q * 64, n0, adapter);
+                            else tma_load_pair_3d(sb + q * low_block, &map_p, bar, n0 + (int)q * 64, 0, adapter);
+                        }
                 }
                 __syncwarp();
                 next();
@@ -565,22 +638,27 @@ lora_layer_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
             if (count > 0) {
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(ufull, uph, abort_flag)))) break;
                 uph ^= 1u;
-                ok = each_adapter<true>(list, count, [&](int, const uint32_t (&off)[8]) {
+                ok = each_batch<true>(list, count, a.batch, [&](int n, int at, int, const uint32_t (&off)[8]) {
                     if (!__all_sync(0xffffffffu, wait_bar(full(s), ph, abort_flag))) return false;
                     tc_fence_after();
-                    const uint32_t sb = sbase + s * kStageBytes;
-                    if (elect_one()) {
-                        for (int j = 0; j < a.rp / 16; ++j) {
-                            const uint64_t b = BWD ? smem_desc(sb + (uint32_t)(j / 4) * (uint32_t)half * 128u + (uint32_t)(j % 4) * 32u, 16u, 1024u)
-                                                   : smem_desc(sb + (uint32_t)j * 2048u, (uint32_t)a.rp * 128u, 1024u);
+                    for (int i = 0; i < n; ++i) {
+                        uint32_t skip[8];
 #pragma unroll
-                            for (int plane = 0; plane < 2; ++plane) {       // hi, lo
-                                const uint32_t c = (uint32_t)(plane * a.rp + j * 16);
-                                mma_pair_masked(d, smem_desc(sbase + L::kU + c / 64u * 2u * kBlock + c % 64u * 2u, 16u, 1024u), b, idesc, off);
+                        for (int w = 0; w < 8; ++w) skip[w] = __shfl_sync(0xffffffffu, off[w], at + i);
+                        const uint32_t sb = sbase + s * kStageBytes + (uint32_t)i * low_blocks * low_block;
+                        if (elect_one())
+                            for (int j = 0; j < a.rp / 16; ++j) {
+                                const uint64_t b = BWD ? smem_desc(sb + (uint32_t)(j / 4) * low_block + (uint32_t)(j % 4) * 32u, 16u, 1024u)
+                                                       : smem_desc(sb + (uint32_t)j * 2048u, low_block, 1024u);
+#pragma unroll
+                                for (int plane = 0; plane < 2; ++plane) {       // hi, lo
+                                    const uint32_t c = (uint32_t)(plane * a.rp + j * 16);
+                                    mma_pair_masked(d, smem_desc(sbase + L::kU + c / 64u * 2u * kBlock + c % 64u * 2u, 16u, 1024u), b, idesc, skip);
+                                }
                             }
-                        }
-                        mma_commit_pair(empty(s));
+                        __syncwarp();
                     }
+                    if (elect_one()) mma_commit_pair(empty(s));
                     __syncwarp();
                     if (++s == kStages) { s = 0; ph ^= 1u; }
                     return true;
@@ -602,12 +680,12 @@ lora_layer_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
         uint32_t aph = 0;
         for (int t = pair; t < a.tiles && *abort_flag == 0u; t += pairs) {
             const int64_t row0 = (int64_t)(t / a.tiles_n) * kPairRows + rank * 128 + quarter * 32;
-            const int n0 = t % a.tiles_n * a.bn, c0 = part * half, c1 = c0 + half;
+            const int n0 = t % a.tiles_n * a.bn;
             if (!__all_sync(0xffffffffu, wait_bar(tfull(acc), aph, abort_flag))) break;
             tc_fence_after();
             const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * 256);
 #pragma unroll 1
-            for (int c = c0; c < c1 && n0 + c < a.cols && row0 < a.M; c += 64) {
+            for (int c = part * 64; c < a.bn && n0 + c < a.cols && row0 < a.M; c += 128) {
                 uint32_t r[64], o[32];
                 tmem_ld64(from + (uint32_t)c, r);
                 if (a.bias) {
@@ -650,49 +728,6 @@ lora_layer_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
 }
 
 // ---- dA and dB ---------------------------------------------------------------------------
-
-// order[starts[i] ..]: the rows of adapter i, ascending.  A CTA per adapter: each
-// thread takes a run of rows, twice.
-constexpr int kOrderThreads = 1024;
-
-__global__ void __launch_bounds__(kOrderThreads)
-lora_order_kernel(const int64_t *__restrict__ ids, int64_t M, int64_t n, int *__restrict__ order, int *__restrict__ counts,
-                  int *__restrict__ starts) {
-    __shared__ int part[2][32];
-    wait_prior_grid();
-    allow_next_grid();
-    const int64_t mine = blockIdx.x;
-    const int t = threadIdx.x, lane = t % 32, warp = t / 32;
-    const int64_t per = (M + kOrderThreads - 1) / kOrderThreads, from = t * per, to = min(from + per, M);
-    int before = 0, here = 0;
-#pragma unroll 8
-    for (int64_t m = from; m < to; ++m) {
-        const int64_t id = ids[m];
-        before += id >= 0 && id < mine ? 1 : 0;
-        here += id == mine ? 1 : 0;
-    }
-    before = __reduce_add_sync(0xffffffffu, before);
-    int scan = here;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += v;
-    }
-    if (lane == 31) { part[0][warp] = before; part[1][warp] = scan; }
-    __syncthreads();
-    int start = 0, at = scan - here, count = 0;
-    for (int w = 0; w < 32; ++w) {
-        start += part[0][w];
-        if (w < warp) at += part[1][w];
-        count += part[1][w];
-    }
-    if (t == 0 && CHK(mine, 1, n)) { counts[mine] = count; starts[mine] = start; }
-    if (here == 0) return;
-    at += start;
-#pragma unroll 8
-    for (int64_t m = from; m < to; ++m)
-        if (ids[m] == mine && CHK(at, 1, M)) order[at++] = (int)m;
-}
 
 struct GradArgs {
     const uint16_t *x, *dy;              // [M][K], [M][N]
@@ -927,23 +962,30 @@ lora_join_kernel(const GradArgs a) {
     const bool is_a = tile < a.tiles_k;
     const int64_t width = is_a ? a.K : a.N, c0 = (int64_t)(tile - (is_a ? 0 : a.tiles_k)) * 128;
     const int64_t stride = (int64_t)a.tiles * a.rp * 128;
-    for (int i = threadIdx.x; i < a.r * 128; i += 256) {
-        const int j = i / 128, row = i % 128;
-        const int64_t c = c0 + row;
-        if (c >= width) continue;
-        float f = 0.0f;
-        if (of > 1) {
-            const int64_t at = ((int64_t)first_slot * a.tiles + tile) * a.rp * 128 + i;
-#pragma unroll 4
-            for (int q = 0; q < of; ++q)
-                if (CHK(at + q * stride, 1, a.slots * stride)) f = q == 0 ? a.parts[at] : f + a.parts[at + q * stride];
+    // four columns of the tile at one place of the rank
+    const int i = ((int)blockIdx.z * 256 + (int)threadIdx.x) * 4, j = i / 128;
+    const int64_t c = c0 + i % 128;
+    if (j >= a.r || c >= width) return;                   // widths are multiples of 8
+    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (of > 1) {
+        const int64_t at = ((int64_t)first_slot * a.tiles + tile) * a.rp * 128 + i;
+#pragma unroll 8
+        for (int q = 0; q < of; ++q) {
+            if (!CHK(at + q * stride, 4, a.slots * stride)) continue;
+            const float4 v = *reinterpret_cast<const float4 *>(a.parts + at + q * stride);
+            f = q == 0 ? v : make_float4(f.x + v.x, f.y + v.y, f.z + v.z, f.w + v.w);
         }
-        const uint16_t v = (uint16_t)pack2<F16>(f, 0.0f);
-        if (is_a) {
-            if (CHK((adapter * a.K + c) * a.r + j, 1, a.n * a.K * a.r)) a.da[(adapter * a.K + c) * a.r + j] = v;
-        } else if (CHK((adapter * a.r + j) * a.N + c, 1, a.n * a.N * a.r)) {
-            a.db[(adapter * a.r + j) * a.N + c] = v;
-        }
+    }
+    const uint32_t lo = pack2<F16>(f.x, f.y), hi = pack2<F16>(f.z, f.w);
+    if (is_a) {
+        uint16_t *to = a.da + (adapter * a.K + c) * a.r + j;
+        if (!CHK(to - a.da, 3 * a.r + 1, a.n * a.K * a.r)) return;
+        to[0] = (uint16_t)lo;
+        to[a.r] = (uint16_t)(lo >> 16);
+        to[2 * a.r] = (uint16_t)hi;
+        to[3 * a.r] = (uint16_t)(hi >> 16);
+    } else if (CHK((adapter * a.r + j) * a.N + c, 4, a.n * a.N * a.r)) {
+        *reinterpret_cast<uint2 *>(a.db + (adapter * a.r + j) * a.N + c) = make_uint2(lo, hi);
     }
 }
 
@@ -1009,7 +1051,7 @@ cudaError_t encode_stack(CUtensorMap *m, const void *base, int64_t inner, int64_
 // u (x and A) or du (dy and B).
 template <bool BWD>
 cudaError_t launch_shrink(const Sizes &z, bool f16, const void *rows, const void *stack, const int64_t *ids, const float *scales,
-                          void *u, TileList *lists, cudaStream_t s) {
+                          void *u, const Work &k, bool sort, cudaStream_t s) {
     const int64_t R = BWD ? z.N : z.K;
     CUtensorMap mx, mp;
     cudaError_t err = encode(&mx, rows, R, z.M, 64, 128);
@@ -1017,19 +1059,28 @@ cudaError_t launch_shrink(const Sizes &z, bool f16, const void *rows, const void
         err = BWD ? encode_stack(&mp, stack, z.N, z.r, z.n, z.rp()) : encode_stack(&mp, stack, z.r, z.K, z.n, 64);
     if (err != cudaSuccess) return err;
     ShrinkArgs a = {};
-    a.ids = ids; a.scales = scales; a.u = u; a.lists = lists;
+    a.ids = ids; a.scales = scales; a.u = u; a.lists = k.lists;
     a.M = z.M; a.n = z.n; a.rp = z.rp();
     a.k_blocks = (int)((R + kBK - 1) / kBK);
     // pieces by the reduction's length alone, so that a row's sum does not depend
-    // on the number of rows: about four k-blocks each
-    a.pieces = a.k_blocks > 16 ? 8 : a.k_blocks > 8 ? 4 : a.k_blocks > 4 ? 2 : 1;
+    // on the number of rows
+    a.pieces = a.k_blocks > 8 ? 8 : a.k_blocks > 4 ? 4 : a.k_blocks > 2 ? 2 : 1;
     a.per_piece = (a.k_blocks + a.pieces - 1) / a.pieces;
+    const int64_t tiles = (z.M + 127) / 128;
+    a.wide_tiles = (int)((z.M + kPairRows - 1) / kPairRows);
+    a.sorted = sort ? z.n : 0;
+    a.order = k.order; a.counts = k.counts; a.starts = k.starts;
+    a.extra = (int)((a.wide_tiles + a.sorted + a.pieces - 1) / a.pieces);
+    // few CTAs: a tile's adapters one behind another are what takes the time, and
+    // nothing else needs the shared memory
+    const int most = a.rp > 64 ? 8 : kShrinkB;
+    a.stages_b = tiles * a.pieces <= 152 ? most : 4;
     auto kern = f16 ? lora_shrink_kernel<BWD, true> : lora_shrink_kernel<BWD, false>;
-    const size_t smem = shrink_layout(BWD, a.rp).total;
+    const size_t smem = shrink_layout(BWD, a.rp, a.stages_b).total;
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     count_launch();
-    return launch_k(kern, dim3((unsigned)((z.M + 127) / 128 * a.pieces)), dim3(kShrinkThreads), smem, s,
+    return launch_k(kern, dim3((unsigned)((tiles + a.extra) * a.pieces)), dim3(kShrinkThreads), smem, s,
                     (unsigned)a.pieces, mx, mp, a);
 }
 
@@ -1053,13 +1104,18 @@ cudaError_t launch_layer(const Sizes &z, bool f16, const void *rows, const void 
     a.M = z.M; a.cols = BWD ? z.K : z.N;
     a.rp = z.rp();
     a.k_blocks = (int)(((BWD ? z.N : z.K) + kBK - 1) / kBK);
-    // 128 columns where that leaves fewer SMs idle in the last wave; a 256-wide
-    // tile takes fewer operand bytes for its products
+    // The width that leaves the least idle in the last wave; narrower tiles take
+    // more operand bytes for their products.  (The width does not show in a result.)
     const int64_t tm = (z.M + kPairRows - 1) / kPairRows, pairs = sms / 2;
-    auto work = [&](int64_t bn) { return (tm * ((a.cols + bn - 1) / bn) + pairs - 1) / pairs * (bn == 128 ? 140 : 256); };
-    a.bn = work(128) < work(256) ? 128 : 256;
+    auto work = [&](int64_t bn, int64_t each) { return (tm * ((a.cols + bn - 1) / bn) + pairs - 1) / pairs * each; };
+    a.bn = 256;
+    if (work(192, 205) < work(256, 256)) a.bn = 192;
+    if (work(128, 150) < (a.bn == 192 ? work(192, 205) : work(256, 256))) a.bn = 128;
     a.tiles_n = (int)((a.cols + a.bn - 1) / a.bn);
     a.tiles = (int)(tm * a.tiles_n);
+    const int low = BWD ? (a.rp > 64 ? 2 : 1) * a.bn / 2 * 128 : (a.bn / 2 + 63) / 64 * a.rp * 128;
+    a.batch = 1;
+    while (a.batch < 32 && 2 * a.batch * low <= (int)kStageBytes) a.batch *= 2;
     CUtensorMap m[5];
     cudaError_t err = encode(&m[0], rows, BWD ? z.N : z.K, z.M, 64, 128);
     if (err == cudaSuccess) err = encode(&m[1], w, z.N, z.K, 64, BWD ? a.bn / 2 : 64);
@@ -1131,7 +1187,7 @@ carbon_status_t carbon_lora_linear_fwd(void *y, void *u, const void *x, const vo
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool f16 = dtype == CARBON_F16;
     const Work k = plan_work(workspace, z, false, false);
-    cudaError_t err = launch_shrink<false>(z, f16, x, a, adapters, scales, u, k.lists, s);
+    cudaError_t err = launch_shrink<false>(z, f16, x, a, adapters, scales, u, k, false, s);
     if (err == cudaSuccess) err = launch_layer<false>(z, f16, x, w, bias, u, b, y, k.lists, sms, s);
     return note_cuda(err);
 }
@@ -1163,12 +1219,7 @@ carbon_status_t carbon_lora_linear_bwd(void *dx, void *da, void *db, const void 
         return note_cuda(err);
     }
     const Work k = plan_work(workspace, z, true, da != nullptr);
-    cudaError_t err = cudaSuccess;
-    if (da) {
-        count_launch();
-        err = launch_k(lora_order_kernel, dim3((unsigned)n), dim3(kOrderThreads), 0, s, 1, adapters, M, n, k.order, k.counts, k.starts);
-    }
-    if (err == cudaSuccess) err = launch_shrink<true>(z, f16, dy, b, adapters, scales, k.du, k.lists, s);
+    cudaError_t err = launch_shrink<true>(z, f16, dy, b, adapters, scales, k.du, k, da != nullptr, s);
     if (err == cudaSuccess && dx) err = launch_layer<true>(z, f16, dy, w, nullptr, k.du, a, dx, k.lists, sms, s);
     if (err == cudaSuccess && da) {
         GradArgs g = {};
@@ -1192,8 +1243,8 @@ carbon_status_t carbon_lora_linear_bwd(void *dx, void *da, void *db, const void 
         }
         if (err == cudaSuccess) {
             count_launch();
-            err = launch_k(f16 ? lora_join_kernel<true> : lora_join_kernel<false>, dim3((unsigned)n, (unsigned)g.tiles), dim3(256),
-                           0, s, 1, g);
+            err = launch_k(f16 ? lora_join_kernel<true> : lora_join_kernel<false>, 
+                           dim3((unsigned)n, (unsigned)g.tiles, (unsigned)((r + 7) / 8)), dim3(256), 0, s, 1, g);
         }
     }
     return note_cuda(err);

@@ -276,10 +276,10 @@ int64_t carbon_lora_linear_fwd_workspace(int64_t M, int64_t K, int64_t N, int64_
  *
  * da and db (both or neither may be NULL) are written whole, zeros for adapters
  * that no row names; dx may be NULL, then w and a may be; without da, x and u
- * may be.  Each adapter's sum takes its rows in their order, 512 at a time, and
+ * may be.  Each adapter's sum takes its rows in their order, 1024 at a time, and
  * depends on them alone.
  * Workspace: carbon_lora_linear_bwd_workspace bytes: 6 M r for du, 52 M, 8 n, and
- * M / 256 partial sums of (K + N) r fp32 numbers. */
+ * M / 512 partial sums of (K + N) r fp32 numbers. */
 carbon_status_t carbon_lora_linear_bwd(void *dx, void *da, void *db, const void *dy, const void *x,
                                        const void *w, const void *a, const void *b,
                                        const int64_t *adapters, const float *scales, const void *u,
