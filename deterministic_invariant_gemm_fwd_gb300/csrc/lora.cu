@@ -18,7 +18,8 @@
 //                        behind the layer's own k-blocks the adapters' are added to
 //                        the same accumulator: one rounding, no second pass over y.
 //   lora_grads_kernel    dA and dB: 128 columns and up to 1024 rows of one adapter per
-//                        CTA, gathered by row number (no other row enters a sum).
+//                        CTA, by bulk copies where 64 of them follow each other, else
+//                        gathered one by one (no other row enters a sum).
 //   lora_join_kernel     adds the pieces of adapters with more rows, in order.
 //
 // u and du are kept as a pair of 16-bit terms, hi + lo: 16 bits of bf16, 22 of
@@ -169,7 +170,8 @@ struct ShrinkArgs {
     TileList *lists;                     // [row tiles of 256]
     int64_t M, n;
     int rp;                              // rank, rounded up to 16
-    int k_blocks, per_piece, pieces;
+    int k_blocks, per_piece, pieces;     // the reduction in 1, 2, 4 or 8 pieces of per_piece k-blocks
+    int cluster, each;                   // CTAs per tile, and their pieces each
     int stages_b;                        // stages of adapters
     // clusters ahead of those of the rows: lists of 256 rows, then rows in the order of adapters
     int extra, wide_tiles;
@@ -241,9 +243,15 @@ __device__ __forceinline__ void sort_rows(const ShrinkArgs &a, int64_t mine, int
     }
 }
 
+// Whole warps run the loops that issue loads and products, one lane issues: what
+// these take then lives in uniform registers (one lane's loop took 600 cycles per
+// load; 24 adapters in a tile: 20 us).
+//
 // rows [128 t, ..) of X times P_i, X [M][R]; P_i is A_i [R][r] or the transpose of
-// B_i [r][R] (BWD).  Cluster: the pieces of the reduction.  The CTAs of the first
-// clusters make what later kernels need of the adapters' numbers.
+// B_i [r][R] (BWD).  The reduction's pieces depend on R alone and are added as a
+// balanced tree, so a row's sum is the same however the cluster's CTAs share them.
+// The CTAs of the first clusters make what later kernels need of the adapters'
+// numbers.
 template <bool BWD, bool F16>
 __global__ void __launch_bounds__(kShrinkThreads)
 lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_p, const ShrinkArgs a) {
@@ -261,11 +269,11 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     volatile uint32_t *abort_flag = tmem_slot + 1;
     Groups<128> &g = *reinterpret_cast<Groups<128> *>(smem + l.groups);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int piece = a.pieces > 1 ? (int)cluster_rank() : 0, cluster = (int)blockIdx.x / a.pieces;
+    const int rank = a.cluster > 1 ? (int)cluster_rank() : 0, cluster = (int)blockIdx.x / a.cluster;
     if (cluster < a.extra) {                              // the whole cluster: nothing here waits for its other CTAs
         wait_prior_grid();
         allow_next_grid();
-        const int64_t i = (int64_t)cluster * a.pieces + piece, sort = i - a.wide_tiles;
+        const int64_t i = (int64_t)cluster * a.cluster + rank, sort = i - a.wide_tiles;
         if (i < a.wide_tiles) {
             Groups<256> &w = *reinterpret_cast<Groups<256> *>(smem);
             find_groups(w, a.ids, i * kPairRows, a.M, a.n, true);
@@ -280,7 +288,8 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         }
         return;
     }
-    const uint32_t cols = a.rp <= 32 ? 32u : a.rp <= 64 ? 64u : 128u;
+    const int wide = a.rp * a.each;                       // accumulators of this CTA's pieces, at most 128 columns
+    const uint32_t cols = wide <= 32 ? 32u : wide <= 64 ? 64u : 128u;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kShrinkA; ++s) { mbar_init(a_full(s), 1); mbar_init(a_empty(s), 1); }
         for (int s = 0; s < kShrinkB; ++s) { mbar_init(b_full(s), 1); mbar_init(b_empty(s), 1); }
@@ -299,7 +308,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     allow_next_grid();
 
     const int64_t m0 = (int64_t)(cluster - a.extra) * 128;
-    const int kb0 = min(piece * a.per_piece, a.k_blocks), kb1 = min(kb0 + a.per_piece, a.k_blocks);
+    const int share = a.each * a.per_piece, kb0 = min(rank * share, a.k_blocks), kb1 = min(kb0 + share, a.k_blocks);
     // the first rows are on their way while the adapters are looked up
     const int ahead = min(kb1 - kb0, kShrinkA);
     if (threadIdx.x == 0)
@@ -312,33 +321,42 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     const bool any = g.count > 0 && kb1 > kb0;
 
     if (warp == 0) {
-        if (lane == 0 && !any) {
-            for (int s = 0; s < ahead; ++s) mbar_wait(a_full(s), 0);
-        } else if (lane == 0) {
-            int sa = 0, sb = 0;
-            uint32_t pa = 0, pb = 0;
-            bool ok = true;
-            for (int kb = kb0; ok && kb < kb1; ++kb) {
-                if (kb - kb0 >= kShrinkA) {
-                    if (!(ok = wait_bar(a_empty(sa), pa ^ 1u, abort_flag))) break;
+        int sa = 0, sb = 0;
+        uint32_t pa = 0, pb = 0;
+        bool ok = any;
+        const int count = __shfl_sync(0xffffffffu, g.count, 0);
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
+            if (kb - kb0 >= kShrinkA) {
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(a_empty(sa), pa ^ 1u, abort_flag)))) break;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(a_full(sa), 2 * kBlock);
                     tma_load_2d(sbase + sa * 2 * kBlock, &map_x, a_full(sa), kb * kBK, (int)m0);
                 }
-                if (++sa == kShrinkA) { sa = 0; pa ^= 1u; }
-                for (int i = 0; i < g.count; ++i) {
-                    if (!(ok = wait_bar(b_empty(sb), pb ^ 1u, abort_flag))) break;
-                    const uint32_t dst = sbase + l.b + sb * l.b_stage;
+                __syncwarp();
+            }
+            if (++sa == kShrinkA) { sa = 0; pa ^= 1u; }
+            for (int i = 0; i < count; ++i) {
+                const int adapter = __shfl_sync(0xffffffffu, g.adapter[i], 0);
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(b_empty(sb), pb ^ 1u, abort_flag)))) break;
+                const uint32_t dst = sbase + l.b + sb * l.b_stage;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(b_full(sb), l.b_stage);
                     if (BWD) {
-                        tma_load_3d(dst, &map_p, b_full(sb), kb * kBK, 0, g.adapter[i]);
+                        tma_load_3d(dst, &map_p, b_full(sb), kb * kBK, 0, adapter);
                     } else {
-                        tma_load_3d(dst, &map_p, b_full(sb), 0, kb * kBK, g.adapter[i]);
-                        if (a.rp > 64) tma_load_3d(dst + kBlock, &map_p, b_full(sb), 64, kb * kBK, g.adapter[i]);
+                        tma_load_3d(dst, &map_p, b_full(sb), 0, kb * kBK, adapter);
+                        if (a.rp > 64) tma_load_3d(dst + kBlock, &map_p, b_full(sb), 64, kb * kBK, adapter);
                     }
-                    if (++sb == a.stages_b) { sb = 0; pb ^= 1u; }
                 }
+                __syncwarp();
+                if (++sb == a.stages_b) { sb = 0; pb ^= 1u; }
             }
-            // every load has landed before the ring is used again, and before the CTA may exit
+        }
+        // Every load has landed before the ring is used again, and before the CTA
+        // may exit: the first rows also where nothing is multiplied.
+        if (!any) {
+            for (int s = 0; s < ahead; ++s) mbar_wait(a_full(s), 0);
+        } else {
             for (int i = 0; i < kShrinkA; ++i) {
                 if (--sa < 0) { sa = kShrinkA - 1; pa ^= 1u; }
                 if (!mbar_wait(a_full(sa), pa)) break;
@@ -348,33 +366,40 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 if (!mbar_wait(b_full(sb), pb)) break;
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0 && any) {
-            const uint32_t idesc = instr_desc_single(a.rp, false, !BWD, F16);
-            int sa = 0, sb = 0;
-            uint32_t pa = 0, pb = 0;
-            bool ok = true;
-            for (int kb = kb0; ok && kb < kb1; ++kb) {
-                if (!(ok = wait_bar(a_full(sa), pa, abort_flag))) break;
-                const uint32_t rows = sbase + sa * 2 * kBlock;
-                for (int i = 0; i < g.count; ++i) {
-                    if (!(ok = wait_bar(b_full(sb), pb, abort_flag))) break;
-                    tc_fence_after();
-                    const uint32_t p = sbase + l.b + sb * l.b_stage;
-                    const uint32_t off[4] = {g.off[i][0], g.off[i][1], g.off[i][2], g.off[i][3]};
+    } else if (warp == 1 && any) {
+        const uint32_t idesc = instr_desc_single(a.rp, false, !BWD, F16);
+        int sa = 0, sb = 0, in_piece = 0;
+        uint32_t pa = 0, pb = 0, d = tmem;
+        bool ok = true;
+        const int count = __shfl_sync(0xffffffffu, g.count, 0);
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
+            if (!(ok = __all_sync(0xffffffffu, wait_bar(a_full(sa), pa, abort_flag)))) break;
+            const uint32_t rows = sbase + sa * 2 * kBlock;
+            for (int i = 0; i < count; ++i) {
+                uint32_t off[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) off[w] = __shfl_sync(0xffffffffu, g.off[i][w], 0);
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(b_full(sb), pb, abort_flag)))) break;
+                tc_fence_after();
+                const uint32_t p = sbase + l.b + sb * l.b_stage;
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kBK / 16; ++k)
-                        mma_masked(tmem, box_desc(rows, false, k), box_desc(p, !BWD, k), idesc, off,
-                                   kb > kb0 || k > 0 ? 1u : 0u);
+                        mma_masked(d, box_desc(rows, false, k), box_desc(p, !BWD, k), idesc, off,
+                                   in_piece > 0 || k > 0 ? 1u : 0u);
                     mma_commit(b_empty(sb));
-                    if (++sb == a.stages_b) { sb = 0; pb ^= 1u; }
                 }
-                if (!ok) break;
-                mma_commit(a_empty(sa));
-                if (++sa == kShrinkA) { sa = 0; pa ^= 1u; }
+                __syncwarp();
+                if (++sb == a.stages_b) { sb = 0; pb ^= 1u; }
             }
-            if (ok) mma_commit(done);
+            if (!ok) break;
+            if (elect_one()) mma_commit(a_empty(sa));
+            __syncwarp();
+            if (++sa == kShrinkA) { sa = 0; pa ^= 1u; }
+            if (++in_piece == a.per_piece) { in_piece = 0; d += (uint32_t)a.rp; }
         }
+        if (ok && elect_one()) mma_commit(done);
+        __syncwarp();
     }
     // the products are complete and the producer has seen its last load
     bool have = any;
@@ -388,33 +413,64 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     if (warp >= 2) {
         const int quarter = warp % 4, row = quarter * 32 + lane;
         const bool mine = have && g.id[row] >= 0;
+        const int filled = (kb1 - kb0 + a.per_piece - 1) / a.per_piece;       // pieces that hold something
+        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
         for (int c = 0; c < a.rp; c += 16) {
-            uint32_t v[16];
-            if (have) tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c, v);
+            // pieces 2 j and 2 j + 1, and so on: the tree's levels within this CTA
+            float sum[3][16];
+            for (int q = 0; q < a.each; ++q) {
+                uint32_t v[16];
+                if (have && q < filled) tmem_ld16(from + (uint32_t)(q * a.rp + c), v);
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4 *>(part + row * pitch + c + i) =
-                    mine ? make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
-                                       __uint_as_float(v[i + 3]))
-                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int i = 0; i < 16; ++i) {
+                    float f = mine && q < filled ? __uint_as_float(v[i]) : 0.0f;
+                    if ((q & 1) == 0) {
+                        sum[0][i] = f;
+                    } else {
+                        f = sum[0][i] + f;
+                        if ((q & 2) == 0) {
+                            sum[1][i] = f;
+                        } else {
+                            f = sum[1][i] + f;
+                            if ((q & 4) == 0) sum[2][i] = f;
+                            else sum[0][i] = sum[2][i] + f;
+                        }
+                    }
+                }
+            }
+            const int level = a.each == 2 ? 1 : a.each == 4 ? 2 : 0;          // 8: back in 0
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                float f[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[k] = level == 0 ? sum[0][i + k] : level == 1 ? sum[1][i + k] : sum[2][i + k];
+                *reinterpret_cast<float4 *>(part + row * pitch + c + i) = make_float4(f[0], f[1], f[2], f[3]);
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();                                   // every piece is in its CTA's shared memory
 
-    // this CTA's share of the rows: the pieces in order, the scale, the terms
-    const int rows = 128 / a.pieces, vecs = a.rp / 4;
+    // this CTA's share of the rows: the rest of the tree, the scale, the terms
+    const int rows = 128 / a.cluster, vecs = a.rp / 4;
     uint16_t *u = static_cast<uint16_t *>(a.u);
     for (int i = threadIdx.x; i < rows * vecs; i += kShrinkThreads) {
-        const int row = piece * rows + i / vecs, c = i % vecs * 4;
+        const int row = rank * rows + i / vecs, c = i % vecs * 4;
         if (m0 + row >= a.M) continue;
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int q = 0; q < a.pieces; ++q) {
-            const uint32_t at = smem_addr(part + row * pitch + c);
-            const float4 v = a.pieces > 1 ? ld_cluster_f4(at, (uint32_t)q) : *reinterpret_cast<const float4 *>(part + row * pitch + c);
-            s = q == 0 ? v : make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-        }
+        const uint32_t mine = smem_addr(part + row * pitch + c);
+        float4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            v[q] = q >= a.cluster ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                 : a.cluster > 1 ? ld_cluster_f4(mine, (uint32_t)q) : *reinterpret_cast<const float4 *>(part + row * pitch + c);
+#pragma unroll
+        for (int step = 1; step < 8; step *= 2)
+#pragma unroll
+            for (int q = 0; q < 8; q += 2 * step)         // beyond the cluster's CTAs nothing changes
+                if (q + step < a.cluster)
+                    v[q] = make_float4(v[q].x + v[q + step].x, v[q].y + v[q + step].y, v[q].z + v[q + step].z, v[q].w + v[q + step].w);
+        const float4 s = v[0];
         const int id = g.id[row];
         const float scale = id >= 0 ? a.scales[id] : 0.0f;
         const float w[4] = {s.x * scale, s.y * scale, s.z * scale, s.w * scale};
@@ -786,6 +842,10 @@ __host__ __device__ inline GradLayout grad_layout(int rp) {
     return l;
 }
 
+// Bytes that a barrier's phase waits for, without an arrival.
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 // 16 bytes, or zeros where there is nothing to read.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -797,7 +857,8 @@ __device__ __forceinline__ void copies_wait() {
 
 template <bool F16>
 __global__ void __launch_bounds__(kGradThreads)
-lora_grads_kernel(const GradArgs a) {
+lora_grads_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy,
+                  const __grid_constant__ CUtensorMap map_u, const __grid_constant__ CUtensorMap map_du, const GradArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -842,25 +903,50 @@ lora_grads_kernel(const GradArgs a) {
             int s = 0, sent = 0, sent_s = 0;
             uint32_t ph = 0;
             bool ok = true;
-            int m = q < count ? rows[q] : -1;
+            // a block's row of this thread, and whether its 64 rows follow each other
+            auto row_of = [&](int b, bool *run) {
+                const int at = b * 64;
+                *run = at + 64 <= count && rows[at + 63] == rows[at] + 63;
+                return at + q < count ? rows[at + q] : -1;
+            };
+            bool run;
+            int m = row_of(0, &run);
+            int issued = 0;
             for (int b = 0; ok && b < blocks; ++b) {
-                const int at = (b + 1) * 64 + q, next = at < count ? rows[at] : -1;
+                bool next_run = false;
+                const int next = b + 1 < blocks ? row_of(b + 1, &next_run) : -1;
                 if (!(ok = wait_bar(empty(s), ph ^ 1u, abort_flag))) break;
                 const uint32_t to = sbase + s * l.stage;
-                const bool live = m >= 0 && CHK(m, 1, a.M);
-                const uint16_t *x = src + (live ? (int64_t)m * width : 0);
+                if (run) {                                // by bulk copies
+                    if (threadIdx.x == 0) {
+                        const CUtensorMap *rows_map = is_a ? &map_x : &map_dy, *low_map = is_a ? &map_du : &map_u;
+                        const uint32_t lows = a.rp > 64 ? 2u : 1u;
+                        mbar_expect_tx(full(s), 2 * kBlock + 2 * l.plane);
+                        tma_load_2d(to, rows_map, full(s), (int)c0, m);
+                        tma_load_2d(to + kBlock, rows_map, full(s), (int)c0 + 64, m);
+                        for (uint32_t p = 0; p < lows; ++p) {
+                            tma_load_2d(to + 2 * kBlock + p * kBlock, low_map, full(s), (int)p * 64, m);
+                            tma_load_2d(to + 2 * kBlock + l.plane + p * kBlock, low_map, full(s), 2 * a.rp + (int)p * 64, m);
+                        }
+                    }
+                } else {
+                    const bool live = m >= 0 && CHK(m, 1, a.M);
+                    const uint16_t *x = src + (live ? (int64_t)m * width : 0);
 #pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    const int64_t c = c0 + h * 64 + p * 8;
-                    const bool there = live && c < width;
-                    copy16(to + h * kBlock + line + (uint32_t)((p ^ (q & 7)) * 16), there ? x + c : src, there);
+                    for (int p = 0; p < 8; ++p) {
+                        const int64_t c = c0 + h * 64 + p * 8;
+                        const bool there = live && c < width;
+                        copy16(to + h * kBlock + line + (uint32_t)((p ^ (q & 7)) * 16), there ? x + c : src, there);
+                    }
+                    const uint16_t *u = planes + ((live ? (int64_t)m * kPlanes : 0) + h * 2) * a.rp;      // hi, lo 2^11
+                    for (int p = 0; p < a.rp / 8; ++p)
+                        copy16(to + 2 * kBlock + h * l.plane + (uint32_t)(p / 8) * kBlock + line + (uint32_t)((p % 8 ^ (q & 7)) * 16),
+                               u + p * 8, live);
                 }
-                const uint16_t *u = planes + ((live ? (int64_t)m * kPlanes : 0) + h * 2) * a.rp;      // hi, lo 2^11
-                for (int p = 0; p < a.rp / 8; ++p)
-                    copy16(to + 2 * kBlock + h * l.plane + (uint32_t)(p / 8) * kBlock + line + (uint32_t)((p % 8 ^ (q & 7)) * 16),
-                           u + p * 8, live);
                 asm volatile("cp.async.commit_group;" ::: "memory");
+                ++issued;
                 m = next;
+                run = next_run;
                 if (++s == kGradStages) { s = 0; ph ^= 1u; }
                 if (b - sent == kGradStages - 1) {
                     copies_wait<kGradStages - 1>();
@@ -872,29 +958,37 @@ lora_grads_kernel(const GradArgs a) {
             }
             copies_wait<0>();
             fence_proxy_async_smem();
-            for (; ok && sent < blocks; ++sent) {
+            for (; sent < issued; ++sent) {
                 mbar_arrive(full(sent_s));
                 if (++sent_s == kGradStages) sent_s = 0;
             }
-        } else if (lane == 0) {
+            // after giving up: no bulk copy into a CTA that has left
+            for (int i = 0; !ok && i < kGradStages && i < issued; ++i) {
+                if (--s < 0) { s = kGradStages - 1; ph ^= 1u; }
+                if (!mbar_wait(full(s), ph)) break;
+            }
+        } else {
             const uint32_t idesc = instr_desc_single(a.rp, true, true, F16);
             int s = 0;
             uint32_t ph = 0;
             bool ok = true;
             for (int b = 0; b < blocks; ++b) {
-                if (!(ok = wait_bar(full(s), ph, abort_flag))) break;
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(full(s), ph, abort_flag)))) break;
                 tc_fence_after();
                 const uint32_t x = sbase + s * l.stage, u = x + 2 * kBlock;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kBK / 16; ++k)
+                    for (int k = 0; k < kBK / 16; ++k)
 #pragma unroll
-                    for (int term = 0; term < 2; ++term)
-                        mma_bf16(tmem + (uint32_t)(term * a.rp), box_desc(x, true, k), box_desc(u + term * l.plane, true, k),
-                                 idesc, (b | k) != 0 ? 1u : 0u);
-                mma_commit(empty(s));
+                        for (int term = 0; term < 2; ++term)
+                            mma_bf16(tmem + (uint32_t)(term * a.rp), box_desc(x, true, k), box_desc(u + term * l.plane, true, k),
+                                     idesc, (b | k) != 0 ? 1u : 0u);
+                    mma_commit(empty(s));
+                }
+                __syncwarp();
                 if (++s == kGradStages) { s = 0; ph ^= 1u; }
             }
-            if (ok) mma_commit(done);
+            if (ok && elect_one()) mma_commit(done);
         }
         __syncwarp();
         if (warp < 4 && wait_bar(done, 0, abort_flag)) {
@@ -1067,21 +1161,26 @@ cudaError_t launch_shrink(const Sizes &z, bool f16, const void *rows, const void
     a.pieces = a.k_blocks > 8 ? 8 : a.k_blocks > 4 ? 4 : a.k_blocks > 2 ? 2 : 1;
     a.per_piece = (a.k_blocks + a.pieces - 1) / a.pieces;
     const int64_t tiles = (z.M + 127) / 128;
+    // as many CTAs as run at once (two per SM); several accumulators a CTA: at most
+    // 128 columns, so that CTAs of a cluster on one SM never wait for each other's
+    a.cluster = a.pieces;
+    while (a.cluster > 1 && tiles * a.cluster > 256 && a.pieces / (a.cluster / 2) * a.rp <= 128) a.cluster /= 2;
+    a.each = a.pieces / a.cluster;
     a.wide_tiles = (int)((z.M + kPairRows - 1) / kPairRows);
     a.sorted = sort ? z.n : 0;
     a.order = k.order; a.counts = k.counts; a.starts = k.starts;
-    a.extra = (int)((a.wide_tiles + a.sorted + a.pieces - 1) / a.pieces);
+    a.extra = (int)((a.wide_tiles + a.sorted + a.cluster - 1) / a.cluster);
     // few CTAs: a tile's adapters one behind another are what takes the time, and
     // nothing else needs the shared memory
     const int most = a.rp > 64 ? 8 : kShrinkB;
-    a.stages_b = tiles * a.pieces <= 152 ? most : 4;
+    a.stages_b = tiles * a.cluster <= 152 ? most : 4;
     auto kern = f16 ? lora_shrink_kernel<BWD, true> : lora_shrink_kernel<BWD, false>;
     const size_t smem = shrink_layout(BWD, a.rp, a.stages_b).total;
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     count_launch();
-    return launch_k(kern, dim3((unsigned)((tiles + a.extra) * a.pieces)), dim3(kShrinkThreads), smem, s,
-                    (unsigned)a.pieces, mx, mp, a);
+    return launch_k(kern, dim3((unsigned)((tiles + a.extra) * a.cluster)), dim3(kShrinkThreads), smem, s,
+                    (unsigned)a.cluster, mx, mp, a);
 }
 
 template <bool BWD, int UB>
@@ -1234,12 +1333,18 @@ carbon_status_t carbon_lora_linear_bwd(void *dx, void *da, void *db, const void 
         g.tiles = g.tiles_k + (int)(up128(N) / 128);
         auto kern = f16 ? lora_grads_kernel<true> : lora_grads_kernel<false>;
         const size_t smem = grad_layout(g.rp).total;
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        CUtensorMap m[4];
+        err = encode(&m[0], x, K, M, 64, 64);
+        if (err == cudaSuccess) err = encode(&m[1], dy, N, M, 64, 64);
+        if (err == cudaSuccess) err = encode(&m[2], u, kPlanes * g.rp, M, 64, 64);
+        if (err == cudaSuccess) err = encode(&m[3], k.du, kPlanes * g.rp, M, 64, 64);
+        if (err == cudaSuccess) err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         // at most this many pieces: one per adapter with rows, and one for every whole piece of rows
         const int64_t pieces = (n < M ? n : M) + M / kPiece;
         if (err == cudaSuccess) {
             count_launch();
-            err = launch_k(kern, dim3((unsigned)pieces, (unsigned)g.tiles), dim3(kGradThreads), smem, s, 1, g);
+            err = launch_k(kern, dim3((unsigned)pieces, (unsigned)g.tiles), dim3(kGradThreads), smem, s, 1, m[0], m[1], m[2],
+                           m[3], g);
         }
         if (err == cudaSuccess) {
             count_launch();
