@@ -172,6 +172,7 @@ struct ShrinkArgs {
     int rp;                              // rank, rounded up to 16
     int k_blocks, per_piece, pieces;     // the reduction in 1, 2, 4 or 8 pieces of per_piece k-blocks
     int cluster, each;                   // CTAs per tile, and their pieces each
+    int subsets;                         // clusters per tile: each takes part of the tile's adapters
     int stages_b;                        // stages of adapters
     // clusters ahead of those of the rows: lists of 256 rows, then rows in the order of adapters
     int extra, wide_tiles;
@@ -307,7 +308,8 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     wait_prior_grid();
     allow_next_grid();
 
-    const int64_t m0 = (int64_t)(cluster - a.extra) * 128;
+    const int subset = (cluster - a.extra) % a.subsets;
+    const int64_t m0 = (int64_t)((cluster - a.extra) / a.subsets) * 128;
     const int share = a.each * a.per_piece, kb0 = min(rank * share, a.k_blocks), kb1 = min(kb0 + share, a.k_blocks);
     // the first rows are on their way while the adapters are looked up
     const int ahead = min(kb1 - kb0, kShrinkA);
@@ -318,13 +320,21 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         }
     __syncwarp();
     find_groups(g, a.ids, m0, a.M, a.n, false);
-    const bool any = g.count > 0 && kb1 > kb0;
+    const int part_of = (g.count + a.subsets - 1) / a.subsets;
+    const int first = __shfl_sync(0xffffffffu, min(subset * part_of, g.count), 0);
+    const int last = __shfl_sync(0xffffffffu, min(first + part_of, g.count), 0);
+    const bool any = last > first && kb1 > kb0;
+    // the rows this cluster makes: those of its adapters, and the first subset's also those without one
+    auto has = [&](int row) {
+        if (g.id[row] < 0) return subset == 0;
+        const int place = g.place[g.first[row]];
+        return place >= first && place < last;
+    };
 
     if (warp == 0) {
         int sa = 0, sb = 0;
         uint32_t pa = 0, pb = 0;
         bool ok = any;
-        const int count = __shfl_sync(0xffffffffu, g.count, 0);
         for (int kb = kb0; ok && kb < kb1; ++kb) {
             if (kb - kb0 >= kShrinkA) {
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(a_empty(sa), pa ^ 1u, abort_flag)))) break;
@@ -335,7 +345,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 __syncwarp();
             }
             if (++sa == kShrinkA) { sa = 0; pa ^= 1u; }
-            for (int i = 0; i < count; ++i) {
+            for (int i = first; i < last; ++i) {
                 const int adapter = __shfl_sync(0xffffffffu, g.adapter[i], 0);
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(b_empty(sb), pb ^ 1u, abort_flag)))) break;
                 const uint32_t dst = sbase + l.b + sb * l.b_stage;
@@ -371,11 +381,10 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         int sa = 0, sb = 0, in_piece = 0;
         uint32_t pa = 0, pb = 0, d = tmem;
         bool ok = true;
-        const int count = __shfl_sync(0xffffffffu, g.count, 0);
         for (int kb = kb0; ok && kb < kb1; ++kb) {
             if (!(ok = __all_sync(0xffffffffu, wait_bar(a_full(sa), pa, abort_flag)))) break;
             const uint32_t rows = sbase + sa * 2 * kBlock;
-            for (int i = 0; i < count; ++i) {
+            for (int i = first; i < last; ++i) {
                 uint32_t off[4];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) off[w] = __shfl_sync(0xffffffffu, g.off[i][w], 0);
@@ -412,7 +421,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     const int pitch = a.rp + 4;
     if (warp >= 2) {
         const int quarter = warp % 4, row = quarter * 32 + lane;
-        const bool mine = have && g.id[row] >= 0;
+        const bool mine = have && g.id[row] >= 0 && has(row);
         const int filled = (kb1 - kb0 + a.per_piece - 1) / a.per_piece;       // pieces that hold something
         const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
         for (int c = 0; c < a.rp; c += 16) {
@@ -457,7 +466,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     uint16_t *u = static_cast<uint16_t *>(a.u);
     for (int i = threadIdx.x; i < rows * vecs; i += kShrinkThreads) {
         const int row = rank * rows + i / vecs, c = i % vecs * 4;
-        if (m0 + row >= a.M) continue;
+        if (m0 + row >= a.M || !has(row)) continue;
         const uint32_t mine = smem_addr(part + row * pitch + c);
         float4 v[8];
 #pragma unroll
@@ -522,24 +531,32 @@ struct LayerSmem {
     static_assert(kBytes <= 232448, "shared memory per block");
 };
 
-// The adapters of a tile in batches of G (a power of two up to 32), for a whole
-// warp: f(n, at, mine, off) for a batch of n whose adapters and disabled lanes
-// lanes at .. at + n - 1 hold (off only where OFF).  false: f gave up.
-template <bool OFF, typename F>
-__device__ __forceinline__ bool each_batch(const TileList &list, int count, int G, F f) {
-    const int lane = threadIdx.x % 32;
-    for (int e0 = 0; e0 < count; e0 += 32) {
-        const int e = e0 + lane < count ? e0 + lane : e0;
-        const int mine = __ldcg(&list.e[e].adapter);
-        uint32_t off[8] = {};
+// A tile's adapters in a warp: lane e holds entry e0 + e of the list (off only
+// where OFF).
+template <bool OFF>
+struct Entries {
+    int count, adapter;
+    uint32_t off[8];
+    __device__ void load(const TileList &list, int e0) {
+        const TileEntry &e = list.e[e0 + threadIdx.x % 32];       // of 256 places, whatever the count
+        count = __ldcg(&list.count);
+        adapter = __ldcg(&e.adapter);
         if (OFF) {
-            const uint4 lo = __ldcg(reinterpret_cast<const uint4 *>(list.e[e].off));
-            const uint4 hi = __ldcg(reinterpret_cast<const uint4 *>(list.e[e].off) + 1);
+            const uint4 lo = __ldcg(reinterpret_cast<const uint4 *>(e.off)), hi = __ldcg(reinterpret_cast<const uint4 *>(e.off) + 1);
             off[0] = lo.x; off[1] = lo.y; off[2] = lo.z; off[3] = lo.w;
             off[4] = hi.x; off[5] = hi.y; off[6] = hi.z; off[7] = hi.w;
         }
-        for (int at = 0; at < 32 && e0 + at < count; at += G)
-            if (!f(min(G, count - e0 - at), at, mine, off)) return false;
+    }
+};
+
+// The adapters in batches of G (a power of two up to 32), for a whole warp:
+// f(n, at) for n adapters that lanes at .. at + n - 1 hold.  false: f gave up.
+template <bool OFF, typename F>
+__device__ __forceinline__ bool each_batch(const TileList &list, Entries<OFF> &e, int G, F f) {
+    for (int e0 = 0; e0 < e.count; e0 += 32) {
+        if (e0 > 0) e.load(list, e0);
+        for (int at = 0; at < 32 && e0 + at < e.count; at += G)
+            if (!f(min(G, e.count - e0 - at), at)) return false;
     }
     return true;
 }
@@ -597,6 +614,7 @@ lora_layer_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
         int s = 0;
         uint32_t ph = 0, uph = 0;
         bool ok = true, waited = false;
+        Entries<false> entries;
         auto next = [&] { if (++s == kStages) { s = 0; ph ^= 1u; } };
         for (int t = pair; ok && t < a.tiles && *abort_flag == 0u; t += pairs) {
             const int64_t m0 = (int64_t)(t / a.tiles_n) * kPairRows;
@@ -605,7 +623,26 @@ lora_layer_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
             const bool load_a = rank == 0 || second;
             const uint32_t b_bytes = BWD ? (uint32_t)half * 128u : (uint32_t)(half + 63) / 64u * kBlock;
             const uint32_t bytes = (second ? 2u : 1u) * 2u * kBlock + 2u * b_bytes;
+            const TileList &list = a.lists[t / a.tiles_n];
+            bool have_u = false;
+            auto load_u = [&] {                           // this CTA's rows of u
+                have_u = true;
+                if (entries.count == 0) return true;
+                if (!__all_sync(0xffffffffu, wait_bar(uempty, uph ^ 1u, abort_flag))) return false;
+                uph ^= 1u;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(ufull, (second ? 2u : 1u) * UB * 2u * kBlock);
+                    for (int q = 0; q < UB && load_a; ++q)
+                        tma_load_pair(sbase + L::kU + q * 2 * kBlock, &map_u, map_rank(ufull, 0), q * 64, rows);
+                }
+                __syncwarp();
+                return true;
+            };
+            // the list is on its way during the k-blocks; u follows when the last
+            // tile's products are done with its place
+            if (waited) entries.load(list, 0);
             for (int kb = 0; kb < a.k_blocks; ++kb) {
+                if (waited && kb == kStages && !(ok = load_u())) break;
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(empty(s), ph ^ 1u, abort_flag)))) break;
                 const uint32_t sa = sbase + s * kStageBytes, sb = sa + 2 * kBlock, bar = map_rank(full(s), 0);
                 if (elect_one()) {
@@ -625,24 +662,15 @@ lora_layer_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
             if (!waited) {
                 wait_prior_grid();
                 waited = true;
+                entries.load(list, 0);
             }
-            const TileList &list = a.lists[t / a.tiles_n];
-            const int count = __ldcg(&list.count);
-            if (count == 0) continue;
-            if (!(ok = __all_sync(0xffffffffu, wait_bar(uempty, uph ^ 1u, abort_flag)))) break;
-            uph ^= 1u;
-            if (elect_one()) {
-                if (rank == 0) mbar_arrive_expect_tx(ufull, (second ? 2u : 1u) * UB * 2u * kBlock);
-                for (int q = 0; q < UB && load_a; ++q)
-                    tma_load_pair(sbase + L::kU + q * 2 * kBlock, &map_u, map_rank(ufull, 0), q * 64, rows);
-            }
-            __syncwarp();
-            ok = each_batch<false>(list, count, a.batch, [&](int n, int at, int mine, const uint32_t (&)[8]) {
+            if (!have_u && !(ok = load_u())) break;
+            ok = each_batch<false>(list, entries, a.batch, [&](int n, int at) {
                 if (!__all_sync(0xffffffffu, wait_bar(empty(s), ph ^ 1u, abort_flag))) return false;
                 const uint32_t bar = map_rank(full(s), 0);
                 if (rank == 0 && elect_one()) mbar_arrive_expect_tx(full(s), 2u * (uint32_t)n * low_blocks * low_block);
                 for (int i = 0; i < n; ++i) {
-                    const int adapter = __shfl_sync(0xffffffffu, mine, at + i);
+                    const int adapter = __shfl_sync(0xffffffffu, entries.adapter, at + i);
                     const uint32_t sb = sbase + s * kStageBytes + (uint32_t)i * low_blocks * low_block;
                     if (elect_one())
                         for (uint32_t q = 0; q < low_blocks; ++q) {
@@ -666,11 +694,14 @@ lora_layer_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
         int s = 0, acc = 0;
         uint32_t ph = 0, aph = 0, uph = 0;
         bool ok = true, waited = false;
+        Entries<true> entries;
         const uint32_t idesc = instr_desc(a.bn, false, !BWD, F16);
         for (int t = pair; ok && t < a.tiles && *abort_flag == 0u; t += pairs) {
             if (!(ok = __all_sync(0xffffffffu, wait_bar(tempty(acc), aph ^ 1u, abort_flag)))) break;
             tc_fence_after();
             const uint32_t d = tmem + (uint32_t)(acc * 256);
+            const TileList &list = a.lists[t / a.tiles_n];
+            if (waited) entries.load(list, 0);
             for (int kb = 0; kb < a.k_blocks; ++kb) {
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(full(s), ph, abort_flag)))) break;
                 tc_fence_after();
@@ -688,19 +719,18 @@ lora_layer_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
             if (!waited) {
                 wait_prior_grid();
                 waited = true;
+                entries.load(list, 0);
             }
-            const TileList &list = a.lists[t / a.tiles_n];
-            const int count = __ldcg(&list.count);
-            if (count > 0) {
+            if (entries.count > 0) {
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(ufull, uph, abort_flag)))) break;
                 uph ^= 1u;
-                ok = each_batch<true>(list, count, a.batch, [&](int n, int at, int, const uint32_t (&off)[8]) {
+                ok = each_batch<true>(list, entries, a.batch, [&](int n, int at) {
                     if (!__all_sync(0xffffffffu, wait_bar(full(s), ph, abort_flag))) return false;
                     tc_fence_after();
                     for (int i = 0; i < n; ++i) {
                         uint32_t skip[8];
 #pragma unroll
-                        for (int w = 0; w < 8; ++w) skip[w] = __shfl_sync(0xffffffffu, off[w], at + i);
+                        for (int w = 0; w < 8; ++w) skip[w] = __shfl_sync(0xffffffffu, entries.off[w], at + i);
                         const uint32_t sb = sbase + s * kStageBytes + (uint32_t)i * low_blocks * low_block;
                         if (elect_one())
                             for (int j = 0; j < a.rp / 16; ++j) {
@@ -1166,6 +1196,9 @@ cudaError_t launch_shrink(const Sizes &z, bool f16, const void *rows, const void
     a.cluster = a.pieces;
     while (a.cluster > 1 && tiles * a.cluster > 256 && a.pieces / (a.cluster / 2) * a.rp <= 128) a.cluster /= 2;
     a.each = a.pieces / a.cluster;
+    // where that leaves CTAs idle, a tile of many adapters goes to several clusters
+    const int64_t idle = 152 / (tiles * a.cluster), adapters = z.n < 128 ? z.n : 128;
+    a.subsets = (int)(idle < 1 ? 1 : idle < (adapters + 3) / 4 ? idle : (adapters + 3) / 4);
     a.wide_tiles = (int)((z.M + kPairRows - 1) / kPairRows);
     a.sorted = sort ? z.n : 0;
     a.order = k.order; a.counts = k.counts; a.starts = k.starts;
@@ -1179,7 +1212,7 @@ cudaError_t launch_shrink(const Sizes &z, bool f16, const void *rows, const void
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     count_launch();
-    return launch_k(kern, dim3((unsigned)((tiles + a.extra) * a.cluster)), dim3(kShrinkThreads), smem, s,
+    return launch_k(kern, dim3((unsigned)((tiles * a.subsets + a.extra) * a.cluster)), dim3(kShrinkThreads), smem, s,
                     (unsigned)a.cluster, mx, mp, a);
 }
 

@@ -403,11 +403,18 @@ def lora_linear_fwd(x, weight, a, b, adapters, scales, bias=None, keep=False, st
     s, empty, workspace = _begin(x, stream)
     y = empty((M, N), dtype, device)
     nu = _bytes(_b.lib.carbon_lora_linear_u_elements(M, r))
-    u = empty((M, 3, nu // (3 * M) if M else 0), dtype, device)
     nbytes = _bytes(_b.lib.carbon_lora_linear_fwd_workspace(M, K, N, n, r))
-    ws = workspace(nbytes, device)
-    st = _b.lib.carbon_lora_linear_fwd(y.data_ptr(), u.data_ptr(), x.data_ptr(), weight.data_ptr(), _p(bias), a.data_ptr(),
-                                       b.data_ptr(), adapters.data_ptr(), scales.data_ptr(), M, K, N, n, r, ws.data_ptr(),
+    u, at_u = None, 0
+    if keep:
+        u = empty((M, 3, nu // (3 * M) if M else 0), dtype, device)
+        ws = workspace(nbytes, device)
+        at_u, at_ws = u.data_ptr(), ws.data_ptr()
+    else:                                        # behind the workspace
+        ws = workspace(nbytes + 2 * nu, device)
+        at_ws = ws.data_ptr()
+        at_u = at_ws + nbytes
+    st = _b.lib.carbon_lora_linear_fwd(y.data_ptr(), at_u, x.data_ptr(), weight.data_ptr(), _p(bias), a.data_ptr(),
+                                       b.data_ptr(), adapters.data_ptr(), scales.data_ptr(), M, K, N, n, r, at_ws,
                                        nbytes, code, s)
     if st:
         _b._check(st, "carbon_lora_linear_fwd")
