@@ -182,6 +182,7 @@ struct ShrinkArgs {
 
 constexpr int kShrinkThreads = 192;      // producer, MMA issuer, epilogue
 constexpr int kShrinkA = 3, kShrinkB = 12;            // stages of rows, and of adapters at most
+constexpr size_t kShrinkSmem = 78 << 10;              // at least: no third CTA on an SM
 
 struct ShrinkLayout {
     uint32_t b_stage, b, groups, bars, total;
@@ -289,8 +290,8 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         }
         return;
     }
-    const int wide = a.rp * a.each;                       // accumulators of this CTA's pieces, at most 128 columns
-    const uint32_t cols = wide <= 32 ? 32u : wide <= 64 ? 64u : 128u;
+    const int wide = a.rp * a.each;                       // accumulators of this CTA's pieces
+    const uint32_t cols = wide <= 32 ? 32u : wide <= 64 ? 64u : wide <= 128 ? 128u : 256u;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kShrinkA; ++s) { mbar_init(a_full(s), 1); mbar_init(a_empty(s), 1); }
         for (int s = 0; s < kShrinkB; ++s) { mbar_init(b_full(s), 1); mbar_init(b_empty(s), 1); }
@@ -858,17 +859,16 @@ __device__ __forceinline__ Piece find_piece(const int *counts, int64_t n, int64_
 }
 
 constexpr int kGradThreads = 160;        // four warps that load and store, the MMA issuer
-constexpr int kGradStages = 3;
 
 struct GradLayout {
     uint32_t plane, stage, bars, total;
 };
-__host__ __device__ inline GradLayout grad_layout(int rp) {
+__host__ __device__ inline GradLayout grad_layout(int rp, int stages) {
     GradLayout l;
     l.plane = (rp > 64 ? 2u : 1u) * kBlock;
     l.stage = 2 * kBlock + 2 * l.plane;
-    l.bars = kGradStages * l.stage;
-    l.total = l.bars + (2 * kGradStages + 1) * 8 + 16 + sizeof(Piece) + 1024;
+    l.bars = (uint32_t)stages * l.stage;
+    l.total = l.bars + (2 * stages + 1) * 8 + 16 + sizeof(Piece) + 1024;
     return l;
 }
 
@@ -885,25 +885,26 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <bool F16>
+// STAGES: as many as leave room for two CTAs on an SM.
+template <bool F16, int STAGES>
 __global__ void __launch_bounds__(kGradThreads)
 lora_grads_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy,
                   const __grid_constant__ CUtensorMap map_u, const __grid_constant__ CUtensorMap map_du, const GradArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const GradLayout l = grad_layout(a.rp);
+    const GradLayout l = grad_layout(a.rp, STAGES);
     const uint32_t sbase = smem_addr(smem), bars = sbase + l.bars;
     auto full = [&](int s) { return bars + 8u * s; };
-    auto empty = [&](int s) { return bars + 8u * (kGradStages + s); };
-    const uint32_t done = bars + 8u * (2 * kGradStages);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + l.bars + (2 * kGradStages + 1) * 8);
+    auto empty = [&](int s) { return bars + 8u * (STAGES + s); };
+    const uint32_t done = bars + 8u * (2 * STAGES);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + l.bars + (2 * STAGES + 1) * 8);
     volatile uint32_t *abort_flag = tmem_slot + 1;
     Piece *shared_piece = reinterpret_cast<Piece *>(tmem_slot + 2);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t cols = a.rp <= 16 ? 32u : a.rp <= 32 ? 64u : a.rp <= 64 ? 128u : 256u;      // both terms' accumulators
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kGradStages; ++s) { mbar_init(full(s), 128); mbar_init(empty(s), 1); }
+        for (int s = 0; s < STAGES; ++s) { mbar_init(full(s), 128); mbar_init(empty(s), 1); }
         mbar_init(done, 1);
         *abort_flag = 0u;
         fence_mbar_init();
@@ -977,24 +978,24 @@ lora_grads_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
                 ++issued;
                 m = next;
                 run = next_run;
-                if (++s == kGradStages) { s = 0; ph ^= 1u; }
-                if (b - sent == kGradStages - 1) {
-                    copies_wait<kGradStages - 1>();
+                if (++s == STAGES) { s = 0; ph ^= 1u; }
+                if (b - sent == STAGES - 1) {
+                    copies_wait<STAGES - 1>();
                     fence_proxy_async_smem();             // the tensor cores read what this thread's copies wrote
                     mbar_arrive(full(sent_s));
                     ++sent;
-                    if (++sent_s == kGradStages) sent_s = 0;
+                    if (++sent_s == STAGES) sent_s = 0;
                 }
             }
             copies_wait<0>();
             fence_proxy_async_smem();
             for (; sent < issued; ++sent) {
                 mbar_arrive(full(sent_s));
-                if (++sent_s == kGradStages) sent_s = 0;
+                if (++sent_s == STAGES) sent_s = 0;
             }
             // after giving up: no bulk copy into a CTA that has left
-            for (int i = 0; !ok && i < kGradStages && i < issued; ++i) {
-                if (--s < 0) { s = kGradStages - 1; ph ^= 1u; }
+            for (int i = 0; !ok && i < STAGES && i < issued; ++i) {
+                if (--s < 0) { s = STAGES - 1; ph ^= 1u; }
                 if (!mbar_wait(full(s), ph)) break;
             }
         } else {
@@ -1016,7 +1017,7 @@ lora_grads_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_consta
                     mma_commit(empty(s));
                 }
                 __syncwarp();
-                if (++s == kGradStages) { s = 0; ph ^= 1u; }
+                if (++s == STAGES) { s = 0; ph ^= 1u; }
             }
             if (ok && elect_one()) mma_commit(done);
         }
@@ -1191,10 +1192,10 @@ cudaError_t launch_shrink(const Sizes &z, bool f16, const void *rows, const void
     a.pieces = a.k_blocks > 8 ? 8 : a.k_blocks > 4 ? 4 : a.k_blocks > 2 ? 2 : 1;
     a.per_piece = (a.k_blocks + a.pieces - 1) / a.pieces;
     const int64_t tiles = (z.M + 127) / 128;
-    // as many CTAs as run at once (two per SM); several accumulators a CTA: at most
-    // 128 columns, so that CTAs of a cluster on one SM never wait for each other's
+    // as many CTAs as run at once, two per SM (kShrinkSmem); the accumulators of
+    // both fit, so that CTAs of a cluster on one SM never wait for each other's
     a.cluster = a.pieces;
-    while (a.cluster > 1 && tiles * a.cluster > 256 && a.pieces / (a.cluster / 2) * a.rp <= 128) a.cluster /= 2;
+    while (a.cluster > 1 && tiles * a.cluster > 256 && a.pieces / (a.cluster / 2) * a.rp <= 256) a.cluster /= 2;
     a.each = a.pieces / a.cluster;
     // where that leaves CTAs idle, a tile of many adapters goes to several clusters
     const int64_t idle = 152 / (tiles * a.cluster), adapters = z.n < 128 ? z.n : 128;
@@ -1206,9 +1207,10 @@ cudaError_t launch_shrink(const Sizes &z, bool f16, const void *rows, const void
     // few CTAs: a tile's adapters one behind another are what takes the time, and
     // nothing else needs the shared memory
     const int most = a.rp > 64 ? 8 : kShrinkB;
-    a.stages_b = tiles * a.cluster <= 152 ? most : 4;
+    a.stages_b = tiles * a.cluster <= 152 ? most : a.rp > 64 ? 3 : 4;
     auto kern = f16 ? lora_shrink_kernel<BWD, true> : lora_shrink_kernel<BWD, false>;
-    const size_t smem = shrink_layout(BWD, a.rp, a.stages_b).total;
+    size_t smem = shrink_layout(BWD, a.rp, a.stages_b).total;
+    if (smem < kShrinkSmem) smem = kShrinkSmem;
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     count_launch();
@@ -1237,12 +1239,13 @@ cudaError_t launch_layer(const Sizes &z, bool f16, const void *rows, const void 
     a.rp = z.rp();
     a.k_blocks = (int)(((BWD ? z.N : z.K) + kBK - 1) / kBK);
     // The width that leaves the least idle in the last wave; narrower tiles take
-    // more operand bytes for their products.  (The width does not show in a result.)
+    // more operand bytes for their products: 0.29, 0.24 and 0.26 us per k-block of
+    // 256, 192 and 128 columns.  (The width does not show in a result.)
     const int64_t tm = (z.M + kPairRows - 1) / kPairRows, pairs = sms / 2;
     auto work = [&](int64_t bn, int64_t each) { return (tm * ((a.cols + bn - 1) / bn) + pairs - 1) / pairs * each; };
     a.bn = 256;
     if (work(192, 205) < work(256, 256)) a.bn = 192;
-    if (work(128, 150) < (a.bn == 192 ? work(192, 205) : work(256, 256))) a.bn = 128;
+    if (work(128, 225) < (a.bn == 192 ? work(192, 205) : work(256, 256))) a.bn = 128;
     a.tiles_n = (int)((a.cols + a.bn - 1) / a.bn);
     a.tiles = (int)(tm * a.tiles_n);
     const int low = BWD ? (a.rp > 64 ? 2 : 1) * a.bn / 2 * 128 : (a.bn / 2 + 63) / 64 * a.rp * 128;
@@ -1364,8 +1367,10 @@ carbon_status_t carbon_lora_linear_bwd(void *dx, void *da, void *db, const void 
         g.r = (int)r; g.rp = z.rp();
         g.tiles_k = (int)(up128(K) / 128);
         g.tiles = g.tiles_k + (int)(up128(N) / 128);
-        auto kern = f16 ? lora_grads_kernel<true> : lora_grads_kernel<false>;
-        const size_t smem = grad_layout(g.rp).total;
+        const int stages = g.rp > 64 ? 2 : 3;
+        auto kern = g.rp > 64 ? (f16 ? lora_grads_kernel<true, 2> : lora_grads_kernel<false, 2>)
+                              : (f16 ? lora_grads_kernel<true, 3> : lora_grads_kernel<false, 3>);
+        const size_t smem = grad_layout(g.rp, stages).total;
         CUtensorMap m[4];
         err = encode(&m[0], x, K, M, 64, 64);
         if (err == cudaSuccess) err = encode(&m[1], dy, N, M, 64, 64);
