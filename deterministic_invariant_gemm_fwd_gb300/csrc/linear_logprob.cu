@@ -24,7 +24,8 @@
 // lists, forms their logits again, from exact products with a compensated sum
 // (about 2^-44 relative to the sum of the products' magnitudes), and orders them by
 // these: logits that fp32 accumulators cannot tell apart come in the order of
-// float64, equal ones by entry.  (The tensor cores' values differ from these by a few units of 2^-24;
+// float64, equal ones by entry.  Up to 256 positions have their logits stored
+// instead: filling lists is what would take most of the time there.  (The tensor cores' values differ from these by a few units of 2^-24;
 // four spare candidates make room for as many that such an error could move
 // across the last place.)
 //
@@ -96,8 +97,97 @@ __device__ __forceinline__ void exact_logits(const uint4 *x, const uint4 *table,
     }
 }
 
+// The keys of a position's places, lane e that of place e in each of W warps, put
+// in their order and written.  hi_of, lo_of: shared memory for 32 places.
+template <bool F16, int W, typename Sync>
+__device__ __forceinline__ void put_top(const Plan &p, const JoinArgs &a, int64_t row, uint64_t mine, int places, int part,
+                                        float *hi_of, float *lo_of, Sync sync) {
+    const int lane = threadIdx.x % 32;
+    // their logits again, G at a time; lane e then has that of place e
+    const uint32_t entry = ~(uint32_t)mine;
+    const int64_t m = p.rowmap[row];
+    const int nvec = (int)(p.D / 8);
+    const uint4 *x = static_cast<const uint4 *>(a.x) + m * nvec, *table = static_cast<const uint4 *>(a.table);
+    constexpr int G = W == 1 ? 4 : 1;
+    for (int e = part * G; e < places; e += W * G) {
+        int64_t rows[G];
+        float h[G], l[G];
+#pragma unroll
+        for (int q = 0; q < G; ++q) {
+            const uint32_t r = __shfl_sync(0xffffffffu, entry, e + q < places ? e + q : e);
+            rows[q] = CHK(r, 1, p.V) ? r : 0;
+        }
+        exact_logits<F16, G>(x, table, rows, nvec, h, l);
+#pragma unroll
+        for (int q = 0; q < G; ++q)
+            if (lane == q && e + q < places) {
+                hi_of[e + q] = h[q];
+                lo_of[e + q] = l[q];
+            }
+    }
+    sync();
+    if (part != 0) return;
+    float hi = lane < places ? hi_of[lane] : 0.0f, lo = lane < places ? lo_of[lane] : 0.0f;
+    if (!(fabsf(hi) < INFINITY) || lo != lo) lo = 0.0f;
+    if (hi != hi) hi = -INFINITY;
+    int rank = 0;
+    for (int i = 0; i < places; ++i) {
+        const float ho = __shfl_sync(0xffffffffu, hi, i), lo_o = __shfl_sync(0xffffffffu, lo, i);
+        const uint32_t eo = __shfl_sync(0xffffffffu, entry, i);
+        const bool same = ho == hi && lo_o == lo;
+        rank += ho > hi || (ho == hi && lo_o > lo) || (same && eo < entry) ? 1 : 0;
+    }
+    // The logarithms from the same logits as log_probs and lse, whose errors have
+    // the same sign: those of the difference mostly cancel.  Not increasing: where
+    // the order was decided by less than these errors, the one before counts.
+    const float lse = a.lse[m];
+    float z = unordered((uint32_t)(mine >> 32)) * p.inv_t - lse;
+    int from = lane;                                      // the lane whose rank is this lane's number
+    for (int i = 0; i < places; ++i)
+        if (__shfl_sync(0xffffffffu, rank, i) == lane) from = i;
+    z = __shfl_sync(0xffffffffu, z, from);
+    const uint32_t id = __shfl_sync(0xffffffffu, entry, from);
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const float before = __shfl_up_sync(0xffffffffu, z, o);
+        if (lane >= o) z = fminf(z, before);
+    }
+    if (lane < p.top && CHK(m * p.top + lane, 1, p.M * p.top)) {
+        // fewer logits than places: the rest of them are -infinity
+        a.top_ids[m * p.top + lane] = lane < places ? (int64_t)id : -1;
+        a.top_logp[m * p.top + lane] = lse != lse ? lse : lane < places ? z : -INFINITY;
+    }
+}
+
+// The keys found (n of them, more than `places`), in their order: lane e gets that
+// of place e.  A key's place is the number of keys above it.
+template <int Q, typename Sync>
+__device__ __forceinline__ uint64_t in_order(uint64_t *found, int n, int places, int part, Sync sync) {
+    const int lane = threadIdx.x % 32;
+    uint64_t u[Q];
+    int above[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        u[q] = q * 32 + lane < n ? found[q * 32 + lane] : 0ull;
+        above[q] = 0;
+    }
+    for (int i = 0; i < n; ++i) {
+        const uint64_t w = found[i];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) above[q] += w > u[q] ? 1 : 0;
+    }
+    sync();
+    if (part == 0) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (u[q] != 0ull && above[q] < places) found[above[q]] = u[q];
+    }
+    sync();
+    return lane < places ? found[lane] : 0ull;
+}
+
 // The alternatives of a position, by W warps: eight where few positions would leave
-// most of the GPU idle (8 x 768 x 50257: 26 us with one), else one.
+// most of the GPU idle, else one.
 constexpr int kTopThreads = 256;
 
 template <bool F16, bool FEW, int W>
@@ -146,27 +236,7 @@ logp_top_kernel(const Plan p, const JoinArgs a) {
     const int n = found_count, places = n < p.listed ? n : p.listed;
     uint64_t mine = 0ull;
     if (n <= kFound) {
-        // a key's place: the number of keys above it
-        uint64_t u[Q];
-        int above[Q];
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            u[q] = q * 32 + lane < n ? found[q * 32 + lane] : 0ull;
-            above[q] = 0;
-        }
-        for (int i = 0; i < n; ++i) {
-            const uint64_t w = found[i];
-#pragma unroll
-            for (int q = 0; q < Q; ++q) above[q] += w > u[q] ? 1 : 0;
-        }
-        sync();
-        if (part == 0) {
-#pragma unroll
-            for (int q = 0; q < Q; ++q)
-                if (u[q] != 0ull && above[q] < places) found[above[q]] = u[q];
-        }
-        sync();
-        if (lane < places) mine = found[lane];
+        mine = in_order<Q>(found, n, places, part, sync);
     } else {
         // too many for that (equal logits): the largest key below the last one, over and over
         uint64_t last = ~0ull;
@@ -189,60 +259,84 @@ logp_top_kernel(const Plan p, const JoinArgs a) {
             last = best;
         }
     }
-    // their logits again, G at a time; lane e then has that of place e
-    const uint32_t entry = ~(uint32_t)mine;
-    const int64_t m = p.rowmap[row];
-    const int nvec = (int)(p.D / 8);
-    const uint4 *x = static_cast<const uint4 *>(a.x) + m * nvec, *table = static_cast<const uint4 *>(a.table);
-    constexpr int G = W == 1 ? 4 : 1;
-    for (int e = part * G; e < places; e += W * G) {
-        int64_t rows[G];
-        float h[G], l[G];
-#pragma unroll
-        for (int q = 0; q < G; ++q) {
-            const uint32_t r = __shfl_sync(0xffffffffu, entry, e + q < places ? e + q : e);
-            rows[q] = CHK(r, 1, p.V) ? r : 0;
+    put_top<F16, W>(p, a, row, mine, places, part, hi_all[mine_at], lo_all[mine_at], sync);
+}
+
+// The alternatives of a position whose logits were stored: a CTA per position.
+// The listed-th largest of the threads' own largest logits is a bound that about as
+// many logits reach.
+constexpr int kScanThreads = 1024;
+
+template <bool F16>
+__global__ void __launch_bounds__(kScanThreads)
+logp_scan_kernel(const Plan p, const JoinArgs a) {
+    constexpr int kFound = 256, W = kScanThreads / 32;
+    __shared__ uint64_t found[kFound];
+    __shared__ int found_count;
+    __shared__ float hi_of[32], lo_of[32];
+    __shared__ uint64_t part_best[W];
+    wait_prior_grid();
+    allow_next_grid();
+    const int t = threadIdx.x, lane = t % 32, part = t / 32;
+    const int64_t row = blockIdx.x;
+    if (row >= p.head->kept) return;                      // CTA-uniform
+    const float *z = p.logits + row * p.pitch;
+    // a key's upper half; 0: no candidate (NaN, -infinity)
+    auto key_of = [](float v) { return v > -INFINITY ? ordered(v) : 0u; };
+    auto each = [&](auto f) {
+#pragma unroll 8
+        for (int64_t i = 4 * t; i < p.V; i += 4 * kScanThreads) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(z + i));       // past V: -infinity
+            f(key_of(v.x), (int)i);
+            f(key_of(v.y), (int)i + 1);
+            f(key_of(v.z), (int)i + 2);
+            f(key_of(v.w), (int)i + 3);
         }
-        exact_logits<F16, G>(x, table, rows, nvec, h, l);
-#pragma unroll
-        for (int q = 0; q < G; ++q)
-            if (lane == q && e + q < places) {
-                hi_all[mine_at][e + q] = h[q];
-                lo_all[mine_at][e + q] = l[q];
+    };
+    if (t == 0) found_count = 0;
+    uint32_t largest = 0u;
+    each([&](uint32_t k, int) { largest = max(largest, k); });
+    uint32_t bound = 0u;
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t c = bound | 1u << bit;
+        if (__syncthreads_count(largest >= c) >= p.listed) bound = c;
+    }
+    if (largest >= bound)
+        each([&](uint32_t k, int entry) {
+            if (k >= bound && k != 0u) {
+                const int at = atomicAdd(&found_count, 1);        // in any order: places come from comparisons
+                if (at < kFound) found[at] = (uint64_t)k << 32 | (uint32_t)~entry;
             }
-    }
+        });
+    auto sync = [] { __syncthreads(); };
     sync();
-    if (part != 0) return;
-    float hi = lane < places ? hi_all[mine_at][lane] : 0.0f, lo = lane < places ? lo_all[mine_at][lane] : 0.0f;
-    if (!(fabsf(hi) < INFINITY) || lo != lo) lo = 0.0f;
-    if (hi != hi) hi = -INFINITY;
-    int rank = 0;
-    for (int i = 0; i < places; ++i) {
-        const float ho = __shfl_sync(0xffffffffu, hi, i), lo_o = __shfl_sync(0xffffffffu, lo, i);
-        const uint32_t eo = __shfl_sync(0xffffffffu, entry, i);
-        const bool same = ho == hi && lo_o == lo;
-        rank += ho > hi || (ho == hi && lo_o > lo) || (same && eo < entry) ? 1 : 0;
-    }
-    // The logarithms from the same logits as log_probs and lse, whose errors have
-    // the same sign: those of the difference mostly cancel.  Not increasing: where
-    // the order was decided by less than these errors, the one before counts.
-    const float lse = a.lse[m];
-    float z = unordered((uint32_t)(mine >> 32)) * p.inv_t - lse;
-    int from = lane;                                      // the lane whose rank is this lane's number
-    for (int i = 0; i < places; ++i)
-        if (__shfl_sync(0xffffffffu, rank, i) == lane) from = i;
-    z = __shfl_sync(0xffffffffu, z, from);
-    const uint32_t id = __shfl_sync(0xffffffffu, entry, from);
+    const int n = found_count, places = n < p.listed ? n : p.listed;
+    uint64_t mine = 0ull;
+    if (n <= kFound) {
+        mine = in_order<kFound / 32>(found, n, places, part, sync);
+    } else {
+        // many equal logits: the largest key below the last one, over and over
+        uint64_t last = ~0ull;
+        for (int e = 0; e < places; ++e) {
+            uint64_t best = 0ull;
+            each([&](uint32_t k, int entry) {
+                const uint64_t key = (uint64_t)k << 32 | (uint32_t)~entry;
+                if (k != 0u && key < last && key > best) best = key;
+            });
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const float before = __shfl_up_sync(0xffffffffu, z, o);
-        if (lane >= o) z = fminf(z, before);
+            for (int o = 16; o > 0; o >>= 1) {
+                const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
+                best = other > best ? other : best;
+            }
+            sync();
+            if (lane == 0) part_best[part] = best;
+            sync();
+            for (int w = 0; w < W; ++w) best = part_best[w] > best ? part_best[w] : best;
+            if (lane == e) mine = best;
+            last = best;
+        }
     }
-    if (lane < p.top && CHK(m * p.top + lane, 1, p.M * p.top)) {
-        // fewer logits than places: the rest of them are -infinity
-        a.top_ids[m * p.top + lane] = lane < places ? (int64_t)id : -1;
-        a.top_logp[m * p.top + lane] = lse != lse ? lse : lane < places ? z : -INFINITY;
-    }
+    put_top<F16, W>(p, a, row, mine, places, part, hi_of, lo_of, sync);
 }
 
 // 32 positions per CTA.  32 threads per position take every 32nd triple, in
@@ -288,6 +382,7 @@ logp_join_kernel(const Plan p, const JoinArgs a) {
 
 template <bool F16>
 cudaError_t launch_top(const Plan &p, const JoinArgs &j, int sms, cudaStream_t s) {
+    if (p.logits) return launch_k(logp_scan_kernel<F16>, dim3((unsigned)p.M), dim3(kScanThreads), 0, s, 1, p, j);
     const bool wide = p.M <= sms * (kTopThreads / 32), few = p.listed <= kTopFew;
     const int64_t rows = wide ? 1 : kTopThreads / 32;
     return launch_k(wide ? (few ? logp_top_kernel<F16, true, 8> : logp_top_kernel<F16, false, 8>)
@@ -359,7 +454,7 @@ carbon_status_t carbon_linear_logp_fwd(float *log_probs, float *entropy, float *
     a.losses = log_probs; a.lse_out = lse; a.entropy_out = entropy; a.top_ids = top_ids; a.top_logp = top_log_probs;
     cudaError_t err = launch_prepare<true>(p, a, x, s);
     if (err == cudaSuccess)
-        err = top == 0 ? launch_tiles<false, true, 0>(p, table, nullptr, sms, s)
+        err = p.lists == 0 ? launch_tiles<false, true, 0>(p, table, nullptr, sms, s)
             : p.listed <= kTopFew ? launch_tiles<false, true, kTopFew>(p, table, nullptr, sms, s)
                              : launch_tiles<false, true, 32>(p, table, nullptr, sms, s);
     if (err == cudaSuccess) {

@@ -234,7 +234,7 @@ xent_prepare_kernel(const Plan p, const ScanArgs a, const uint4 *__restrict__ x)
                         p.c1[pos] = -e * kLn2;
                         p.g1[pos] = g;
                     }
-                } else if (LOGP && p.top > 0) {
+                } else if (LOGP && p.lists > 0) {
                     p.floor[pos] = 0u;
                     for (int i = 0; i < top_classes(p.listed); ++i) p.largest[(int64_t)pos * top_classes(p.listed) + i] = 0u;
                 }
@@ -739,6 +739,12 @@ __device__ __forceinline__ void logp_rows(const Plan &p, const Unit &o, uint32_t
             for (int i = 0; i < 64; ++i)
                 if (i >= n) r[i] = __float_as_uint(-INFINITY);
         }
+        if (LIST == 0 && p.logits != nullptr && tgt + o.n0 >= 0) {
+            float *to = p.logits + (int64_t)row * p.pitch + o.n0 + c;
+            if (CHK(to - p.logits, 64, p.M * p.pitch))
+#pragma unroll
+                for (int i = 0; i < 64; i += 4) *reinterpret_cast<uint4 *>(to + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+        }
         float top = __uint_as_float(r[0]);
 #pragma unroll
         for (int i = 1; i < 64; ++i) top = fmaxf(top, __uint_as_float(r[i]));
@@ -829,23 +835,13 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
         const int row0 = o.m0 + (int)c.rank * 128 + quarter * 32, row = row0 + lane;
         const int c0 = half * (o.width / 2), c1 = c0 + o.width / 2;
         float lse2 = 0.0f, rfac = 0.0f, slope = 0.0f, hit = 0.0f;
+        uint32_t known = 0u;
         if constexpr (LIST > 0) {
-            // What other spans have proved.  Classes are looked at where a span
-            // starts, and as long as nothing is known; their result is left for
-            // the other threads of the row, which a tile costs one load.
-            constexpr int S = LIST <= kTopFew ? kTopClassesFew : kTopClassesMany;
-            const bool first = (o.left & kFirst) != 0;
-            if (first) {
+            // what other spans have proved, used below
+            known = __ldcg(p.floor + row);
+            if ((o.left & kFirst) != 0) {
                 list.floor = p.tgt[row] < 0 ? INFINITY : -INFINITY;
                 list.reset();
-            }
-            list.raise(just_below(__ldcg(p.floor + row)));
-            if (__any_sync(0xffffffffu, first || list.floor == -INFINITY)) {
-                const uint32_t t = class_bound<S>(p.largest + (int64_t)row * S, p.listed);
-                if (just_below(t) > list.floor) {
-                    list.raise(just_below(t));
-                    if (CHK(row, 1, p.Mp)) atomicMax(p.floor + row, t);
-                }
             }
         }
         int tgt = -1;
@@ -864,6 +860,20 @@ __device__ __forceinline__ void epilogue(const Plan &p, const Maps &maps, const 
         if (!__all_sync(0xffffffffu, c.wait(c.tfull(acc), aph))) return;
         tc_fence_after();
         const uint32_t tmem = c.tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kBN);
+        if constexpr (LIST > 0) {
+            // Classes are looked at where a span starts, and as long as nothing is
+            // known (for every tile: 511 us instead of 471 at 8192 x 768 x 50257);
+            // the result is left for the row's other threads, which a tile costs one load.
+            constexpr int S = LIST <= kTopFew ? kTopClassesFew : kTopClassesMany;
+            list.raise(just_below(known));
+            if (__any_sync(0xffffffffu, (o.left & kFirst) != 0 || list.floor == -INFINITY)) {
+                const uint32_t t = class_bound<S>(p.largest + (int64_t)row * S, p.listed);
+                if (just_below(t) > list.floor) {
+                    list.raise(just_below(t));
+                    if (CHK(row, 1, p.Mp)) atomicMax(p.floor + row, t);
+                }
+            }
+        }
         if (!GRAD) {
             if (LOGP) logp_rows<LIST>(p, o, tmem, row, half, list);
             else loss_rows(p, o, tmem, row, half);

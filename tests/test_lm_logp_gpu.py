@@ -95,8 +95,9 @@ def test_a_position_does_not_depend_on_the_others(top):
 
 # ---- the order of the alternatives -----------------------------------------------
 
-def test_equal_logits_come_by_entry():
-    M, D = 40, 64
+@pytest.mark.parametrize("M", [40, 300])
+def test_equal_logits_come_by_entry(M):
+    D = 64
     table = torch.randn(50, D, generator=gen(1), device="cuda").bfloat16()
     many = table.repeat(60, 1)                             # 3000 entries, sixty of each
     x = torch.randn(M, D, generator=gen(2), device="cuda").bfloat16()
