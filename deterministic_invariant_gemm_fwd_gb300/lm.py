@@ -102,18 +102,19 @@ _codes = {}                      # torch dtype -> code, filled on first use
 
 
 def _tensors(name, tensors, device):
-    """Host arrays (addresses, sizes, type codes) of contiguous tensors on one device."""
+    """Host arrays (addresses, sizes, type codes) of contiguous tensors on one
+    device.  Lists may hold hundreds: every step is one pass of C calls."""
+    import torch
     if not _codes:
-        import torch
         _codes.update({torch.float32: _b.F32, torch.bfloat16: _b.BF16, torch.float16: _b.F16})
+    tensor = torch.Tensor
     try:
-        kinds = [_codes[t.dtype] for t in tensors]
+        kinds = array.array("i", [_codes[t.dtype] for t in tensors])
     except KeyError as e:
         raise TypeError(f"{name} holds dtype {e.args[0]}; expected float32, bfloat16 or float16") from None
-    if not all([t.get_device() == device and t.is_contiguous() for t in tensors]) or device < 0:
+    if device < 0 or not set(map(tensor.get_device, tensors)) <= {device} or not all(map(tensor.is_contiguous, tensors)):
         raise ValueError(f"{name} must be contiguous CUDA tensors on one device")
-    return (array.array("Q", [t.data_ptr() for t in tensors]), array.array("q", [t.numel() for t in tensors]),
-            array.array("i", kinds))
+    return (array.array("Q", list(map(tensor.data_ptr, tensors))), array.array("q", list(map(tensor.numel, tensors))), kinds)
 
 
 def embedding_fwd(table, ids, scale=1.0, stream=None):

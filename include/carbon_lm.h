@@ -302,12 +302,11 @@ int64_t carbon_lora_linear_bwd_workspace(int64_t M, int64_t K, int64_t N, int64_
  * gradients makes the norm and all of out NaN; an infinity makes the norm
  * infinite and the factor 0.
  *
- * Squares are summed in fp32 by 64, in float64 from there on; squares outside
+ * Squares are summed in fp32 by 32, in float64 from there on; squares outside
  * fp32's range are scaled, so that the norm overflows only where it is no fp32
  * number itself.  An element's place in the sum depends on the sizes and the
  * order of the tensors, not on their addresses.  max_norm >= 0, eps >= 0.
- * Workspace: carbon_clip_grads_workspace bytes, at most 64 KiB and 8 more per
- * tensor. */
+ * Workspace: carbon_clip_grads_workspace bytes, 4864 for every 256 tensors. */
 carbon_status_t carbon_clip_grads(float *norm, void *const *out, const void *const *grads,
                                   const int64_t *sizes, const int *dtypes, int64_t count,
                                   float max_norm, float eps, void *workspace,

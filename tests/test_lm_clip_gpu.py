@@ -13,7 +13,7 @@ import deterministic_invariant_gemm_fwd_gb300 as cg  # noqa: E402
 from deterministic_invariant_gemm_fwd_gb300 import nn  # noqa: E402
 
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
-BLOCK = 256 * 8 * 8                     # elements that a CTA takes at a time
+BLOCK = 2048                            # elements that a warp takes at a time
 # Relative errors in units of 2^-24.  The norm: a chain of 16 fused additions and
 # two more, halved by the square root, and its own rounding.  The factor: the
 # norm's, an addition and a division.
@@ -40,6 +40,7 @@ def check(grads, max_norm, out, norm, eps=1e-6):
 @pytest.mark.parametrize("types", [[F32], [BF16], [F16], [BF16, F32, F16]], ids=["f32", "bf16", "f16", "mixed"])
 @pytest.mark.parametrize("sizes", [
     [1], [7, 0, 9], [BLOCK], [BLOCK - 1, BLOCK + 1], [3 * BLOCK + 5, 1, 2, 3], [257] * 300, [0, 0], [1000003],
+    [3] * 32, [3] * 33, [0] * 300 + [5], [2 * BLOCK + 1] * 257,
 ], ids=str)
 def test_norm_and_clipping(sizes, types):
     grads = make(sizes, types)
@@ -70,9 +71,9 @@ def test_addresses_do_not_matter(dtype):
             assert bool((o[:3] == 3.0).all()) and bool((o[3 + w.numel():] == 3.0).all())     # nothing beside it
 
 
-def test_large_count_of_chunks():
-    """More than 8192 blocks: several per chunk, the same formula."""
-    grads = make([8200 * BLOCK + 3, 5, BLOCK + 9], [BF16, F32, F16], std=1e-3)
+def test_several_chunks_per_warp():
+    """More chunks than warps, and runs of them that end inside a tensor."""
+    grads = make([5000 * BLOCK + 3, 5, 7 * BLOCK + 9], [BF16, F32, F16], std=1e-3)
     out = [torch.empty_like(t) for t in grads]
     check(grads, 0.25, out, cg.clip_grads(grads, 0.25, out=out))
 
