@@ -13,11 +13,14 @@ The operators around a language model's linear layers (``include/carbon_lm.h``:
 token embedding, RMS norm with an 8-bit checkpoint, output layer with softmax
 cross entropy, and their gradients) are ``embedding_fwd`` / ``_bwd``,
 ``rms_norm_fwd`` / ``_bwd`` / ``_expand`` and ``linear_cross_entropy_fwd`` /
-``_bwd``.
+``_bwd``.  For fine-tuning and scoring: ``lora_linear_fwd`` / ``_bwd`` (low-rank
+adapters beside a linear layer), ``linear_log_probs_fwd`` / ``_bwd`` (log
+probabilities of tokens, entropy, alternatives), ``grad_norm`` and ``clip_grads``.
 
 ``deterministic_invariant_gemm_fwd_gb300.nn`` wraps them in an autograd
 ``Linear`` / ``deterministic_linear`` (with a deterministic bias gradient),
-``Embedding``, ``RMSNorm``, ``norm_linear`` and ``linear_cross_entropy``.
+``Embedding``, ``RMSNorm``, ``norm_linear``, ``linear_cross_entropy``,
+``LoraLinear``, ``linear_log_probs`` and ``clip_grad_norm_``.
 """
 from __future__ import annotations
 

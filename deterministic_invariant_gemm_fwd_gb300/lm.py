@@ -1,6 +1,8 @@
 """The operators around a language model's linear layers as functions of
 torch tensors (``include/carbon_lm.h``): token embedding, root-mean-square
-norm with an 8-bit checkpoint, and the output layer's softmax cross entropy.
+norm with an 8-bit checkpoint, the output layer's softmax cross entropy, log
+probabilities of tokens with entropy and alternatives, low-rank adapters beside
+a linear layer, and the norm and clipping of all gradients.
 
 Each function checks its arguments, allocates the outputs and the workspace
 with torch's allocator and makes the library call on ``stream`` (default:

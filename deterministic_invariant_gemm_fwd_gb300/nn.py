@@ -25,7 +25,10 @@ exact column sum rounded once.
 Around the linear layers: ``Embedding`` / ``embedding``, ``RMSNorm`` /
 ``rms_norm``, ``norm_linear`` (norm and linear layer with an 8-bit
 checkpoint) and ``linear_cross_entropy`` (output layer and loss), each with a
-deterministic gradient.
+deterministic gradient.  For fine-tuning and scoring: ``LoraLinear`` /
+``lora_linear`` (low-rank adapters of many requests), ``linear_log_probs`` (log
+probabilities of tokens and their entropy, differentiable), ``top_log_probs``
+(the same with the most probable entries) and ``clip_grad_norm_``.
 
 Leading dimensions of the input are flattened into the token dimension.
 There is no CPU path: inputs must be CUDA tensors (float32, bfloat16 or
@@ -373,6 +376,8 @@ def lora_linear(x, weight, a, b, adapters, scales, bias=None):
     _width(x, weight.shape[0])
     if adapters.shape != x.shape[:-1]:
         raise ValueError(f"adapters has shape {tuple(adapters.shape)}; expected {tuple(x.shape[:-1])}")
+    if scales.requires_grad:
+        raise ValueError("scales are constants: no gradient of them is formed")
     return _LoraLinearFunction.apply(x, weight, bias, a, b, adapters, scales)
 
 
@@ -400,7 +405,8 @@ class LoraLinear(torch.nn.Module):
     def forward(self, x, adapters):
         if not isinstance(adapters, torch.Tensor):
             adapters = torch.full(x.shape[:-1], adapters, dtype=torch.int64, device=x.device)
-        return lora_linear(x, self.weight, self.a, self.b, adapters, self.scales, self.bias)
+        # fp32 also where the module was cast to another type
+        return lora_linear(x, self.weight, self.a, self.b, adapters, self.scales.float(), self.bias)
 
     def extra_repr(self):
         n, K, r = self.a.shape

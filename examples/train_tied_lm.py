@@ -8,7 +8,7 @@ cross entropy over the embedding's own table.  Every matrix product, norm,
 lookup and gradient of them runs in this package's kernels.  The data are
 synthetic: a fixed random walk over the vocabulary, so the loss can fall.
 
-    python examples/train_tied_lm.py [--steps N] [--vocab V] [--width D]
+    python examples/train_tied_lm.py [--steps N] [--vocab V] [--width D] [--clip NORM]
 """
 import argparse
 import hashlib
@@ -62,7 +62,7 @@ def batch(vocab, tokens, step):
     return ids.cuda(), targets.cuda()
 
 
-def train(vocab, width, blocks, tokens, steps, lr=0.5, seed=42):
+def train(vocab, width, blocks, tokens, steps, lr=0.5, seed=42, clip=None):
     torch.manual_seed(seed)
     model = TiedLanguageModel(vocab, width, blocks)
     optimizer = torch.optim.SGD(model.parameters(), lr=lr, foreach=False)
@@ -71,6 +71,8 @@ def train(vocab, width, blocks, tokens, steps, lr=0.5, seed=42):
         loss = model(*batch(vocab, tokens, step))
         optimizer.zero_grad(set_to_none=True)
         loss.backward()
+        if clip is not None:
+            cnn.clip_grad_norm_(model.parameters(), clip)
         optimizer.step()
         losses.append(loss.detach())
     digest = hashlib.sha256()
@@ -86,8 +88,9 @@ def main():
     ap.add_argument("--width", type=int, default=256)
     ap.add_argument("--blocks", type=int, default=2)
     ap.add_argument("--tokens", type=int, default=1000)
+    ap.add_argument("--clip", type=float, default=None, help="largest norm of all gradients")
     a = ap.parse_args()
-    runs = [train(a.vocab, a.width, a.blocks, a.tokens, a.steps) for _ in range(2)]
+    runs = [train(a.vocab, a.width, a.blocks, a.tokens, a.steps, clip=a.clip) for _ in range(2)]
     (losses, digest), (losses2, digest2) = runs
     print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f} in {a.steps} steps; weights sha256 {digest[:16]}")
     if losses != losses2 or digest != digest2:

@@ -277,6 +277,10 @@ def test_autograd_and_module():
     assert full.weight.grad.shape == (136, 264) and full.bias.grad.shape == (264,)
     with pytest.raises(ValueError):
         layer(x, ids.view(-1))
+    with pytest.raises(ValueError, match="scales"):
+        nn.lora_linear(x, layer.weight, layer.a, layer.b, ids, layer.scales.clone().requires_grad_())
+    layer.bfloat16()                                         # casts the scales as well
+    assert same_bits(layer(x, ids), y)
     (gx,) = torch.autograd.grad(layer(x, ids).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="no derivative"):
         gx.sum().backward()
