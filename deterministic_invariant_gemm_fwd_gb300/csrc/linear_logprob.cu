@@ -262,9 +262,10 @@ logp_top_kernel(const Plan p, const JoinArgs a) {
     put_top<F16, W>(p, a, row, mine, places, part, hi_all[mine_at], lo_all[mine_at], sync);
 }
 
-// The alternatives of a position whose logits were stored: a CTA per position.
-// The listed-th largest of the threads' own largest logits is a bound that about as
-// many logits reach.
+// The alternatives of a position whose logits were stored: a CTA per position.  The
+// largest logits of the groups of 128 entries, which the loss's sums come with, say
+// where to look: the listed-th largest of them is a bound that only about as many
+// groups reach.  (Threads with several groups, beyond 131072 entries, count once.)
 constexpr int kScanThreads = 1024;
 
 template <bool F16>
@@ -280,34 +281,37 @@ logp_scan_kernel(const Plan p, const JoinArgs a) {
     const int t = threadIdx.x, lane = t % 32, part = t / 32;
     const int64_t row = blockIdx.x;
     if (row >= p.head->kept) return;                      // CTA-uniform
-    const float *z = p.logits + row * p.pitch;
-    // a key's upper half; 0: no candidate (NaN, -infinity)
+    // 0: no candidate (NaN, -infinity)
     auto key_of = [](float v) { return v > -INFINITY ? ordered(v) : 0u; };
-    auto each = [&](auto f) {
-#pragma unroll 8
-        for (int64_t i = 4 * t; i < p.V; i += 4 * kScanThreads) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(z + i));       // past V: -infinity
-            f(key_of(v.x), (int)i);
-            f(key_of(v.y), (int)i + 1);
-            f(key_of(v.z), (int)i + 2);
-            f(key_of(v.w), (int)i + 3);
-        }
-    };
+    auto group_max = [&](int g) { return key_of(__ldcg(&p.pairs[(int64_t)g * p.Mp + row].x)); };
     if (t == 0) found_count = 0;
     uint32_t largest = 0u;
-    each([&](uint32_t k, int) { largest = max(largest, k); });
-    uint32_t bound = 0u;
+    for (int g = t; g < p.vocab_groups; g += kScanThreads) largest = max(largest, group_max(g));
+    uint32_t bound = 0u;                                  // of logits times zscale
     for (int bit = 31; bit >= 0; --bit) {
         const uint32_t c = bound | 1u << bit;
         if (__syncthreads_count(largest >= c) >= p.listed) bound = c;
     }
-    if (largest >= bound)
-        each([&](uint32_t k, int entry) {
-            if (k >= bound && k != 0u) {
-                const int at = atomicAdd(&found_count, 1);        // in any order: places come from comparisons
-                if (at < kFound) found[at] = (uint64_t)k << 32 | (uint32_t)~entry;
+    if (bound == 0u) bound = 1u;                          // fewer groups than that: all of their logits
+    // f(ordered logit, entry) for every logit that reaches the bound, a warp per group
+    auto each = [&](auto f) {
+        for (int g0 = part * 32; g0 < p.vocab_groups; g0 += W * 32) {
+            unsigned hit = __ballot_sync(0xffffffffu, g0 + lane < p.vocab_groups && group_max(g0 + lane) >= bound);
+            for (; hit != 0u; hit &= hit - 1u) {
+                const int at = (g0 + __ffs((int)hit) - 1) * kGroup + 4 * lane;
+                if (at >= p.V) continue;
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.logits + row * p.pitch + at));    // past V: -infinity
+                const float z[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (key_of(z[q] * p.zscale) >= bound) f(ordered(z[q]), at + q);
             }
-        });
+        }
+    };
+    each([&](uint32_t k, int entry) {
+        const int at = atomicAdd(&found_count, 1);        // in any order: places come from comparisons
+        if (at < kFound) found[at] = (uint64_t)k << 32 | (uint32_t)~entry;
+    });
     auto sync = [] { __syncthreads(); };
     sync();
     const int n = found_count, places = n < p.listed ? n : p.listed;
@@ -321,7 +325,7 @@ logp_scan_kernel(const Plan p, const JoinArgs a) {
             uint64_t best = 0ull;
             each([&](uint32_t k, int entry) {
                 const uint64_t key = (uint64_t)k << 32 | (uint32_t)~entry;
-                if (k != 0u && key < last && key > best) best = key;
+                if (key < last && key > best) best = key;
             });
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
