@@ -753,9 +753,14 @@ __device__ __forceinline__ void logp_rows(const Plan &p, const Unit &o, uint32_t
 #pragma unroll
                 for (int i = 0; i < 64; i += 4) *reinterpret_cast<uint4 *>(to + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
         }
-        float top = __uint_as_float(r[0]);
+        float most[2];                                    // of either half
 #pragma unroll
-        for (int i = 1; i < 64; ++i) top = fmaxf(top, __uint_as_float(r[i]));
+        for (int h = 0; h < 2; ++h) {
+            most[h] = __uint_as_float(r[32 * h]);
+#pragma unroll
+            for (int i = 1; i < 32; ++i) most[h] = fmaxf(most[h], __uint_as_float(r[32 * h + i]));
+        }
+        const float top = fmaxf(most[0], most[1]);
         if constexpr (LIST > 0) {
             if (__any_sync(0xffffffffu, top > list.cut)) {
                 if (LIST <= kTopFew && __any_sync(0xffffffffu, list.cut == -INFINITY)) {
@@ -768,14 +773,17 @@ __device__ __forceinline__ void logp_rows(const Plan &p, const Unit &o, uint32_t
                     list.raise(just_below(kth_largest(v, list.k)));
                 }
 #pragma unroll
-                for (int h = 0; h < 64; h += 32) {
+                for (int h = 0; h < 2; ++h) {
+                    if (!__any_sync(0xffffffffu, most[h] > list.cut)) continue;
+                    // bit i: the sign of cut - z (0 for NaN), two instructions each
                     uint32_t more = 0u;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) more |= __uint_as_float(r[h + i]) > list.cut ? 1u << i : 0u;
+                    for (int i = 31; i >= 0; --i)
+                        more = __funnelshift_l(__float_as_uint(list.cut - __uint_as_float(r[32 * h + i])), more, 1);
                     while (__any_sync(0xffffffffu, more != 0u)) {
                         const int i = __ffs((int)more) - 1;       // -1 (any value) where there is none
-                        const float z = select32(r + h, i);
-                        if (more != 0u && z > list.cut) list.template add<LIST>(z, o.n0 + c + h + i);
+                        const float z = select32(r + 32 * h, i);
+                        if (more != 0u && z > list.cut) list.template add<LIST>(z, o.n0 + c + 32 * h + i);
                         more &= more - 1u;
                     }
                 }
