@@ -729,6 +729,23 @@ __device__ __forceinline__ void logp_rows(const Plan &p, const Unit &o, uint32_t
     const int g = half * kGroup;
     if (g >= o.width || o.n0 + g >= p.V) return;
     const int tgt = p.tgt[row] - o.n0;
+    if (LIST == 0 && p.pilot) {                           // only the largest of every 32, for the classes
+        const int classes = top_classes(p.listed);
+#pragma unroll 1
+        for (int c = g; c < g + kGroup; c += 64) {
+            uint32_t r[64];
+            tmem_ld64(tmem + (uint32_t)c, r);
+#pragma unroll
+            for (int h = 0; h < 64; h += 32) {
+                float most = __uint_as_float(r[h]);
+#pragma unroll
+                for (int i = 1; i < 32; ++i) most = fmaxf(most, __uint_as_float(r[h + i]));
+                const int64_t at = (int64_t)row * classes + (o.n0 + c + h) / 32 % classes;
+                if (most > -INFINITY && tgt + o.n0 >= 0 && CHK(at, 1, p.Mp * classes)) atomicMax(p.largest + at, ordered(most));
+            }
+        }
+        return;
+    }
     float mx = -INFINITY, sum = 0.0f, weighted = 0.0f;    // of z log2(e) / temperature
     float largest = -INFINITY;                            // logit of the chunks that had a candidate
     // only what exceeds it can raise the floor

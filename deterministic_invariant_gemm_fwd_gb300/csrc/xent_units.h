@@ -31,6 +31,11 @@ constexpr int kTopSpare = 4;             // alternatives kept beyond those asked
 constexpr int kTopMost = 32 - kTopSpare;
 constexpr int kTopFew = 12, kTopClassesFew = 16, kTopClassesMany = 32;
 XENT_HD inline int top_classes(int listed) { return listed <= kTopFew ? kTopClassesFew : kTopClassesMany; }
+// Entries that a run ahead looks at, a multiple of a tile's, where there are eight
+// times as many.  Without it every thread's first list takes about fifty logits
+// (8192 x 768 x 50257: 463 us for 447 with top 8, 627 for 535 with top 20; 1024
+// entries: 456 and 557).
+constexpr int kPilot = 2048;
 constexpr int kSpan = 8;                 // tiles that a pair takes one after another for the alternatives, at most
 constexpr int64_t kCountAhead = 16384;   // longer lists of positions are counted by a kernel of their own
 
@@ -73,6 +78,7 @@ struct Plan {
     int top, listed;                     // alternatives asked for and kept
     float *logits;                       // [M][pitch]: few positions' logits; else null, and lists:
     int64_t pitch;
+    bool pilot;                          // a run ahead over few entries, which leaves floors for the lists
     int span, spans;                     // tiles of a row tile that form a unit of the ticket, and their number
     int lists;                           // lists of candidates per row: one per span and column half
     unsigned int *largest;               // [Mp][top_classes]: largest logits (ordered) so far of classes of entries; 0: none

@@ -31,6 +31,10 @@
  *   carbon_linear_xent_bwd   M (6 D + 24576) bytes (the logits would take
  *                            4 M V), and up to 128 MiB more below about 2500
  *                            positions.  M = 8192, D = 768: 240 MB
+ *   carbon_linear_logp_fwd   M (2 D + 3 V / 32) bytes; with alternatives 4 M V more
+ *                            up to 256 positions, above M (top + 5) V / 128 or, below
+ *                            some thousand positions, up to 8 times as much
+ *   carbon_linear_logp_bwd   as carbon_linear_xent_bwd
  *
  * Indices that name no row (a token id outside [0, V); a target that is
  * neither ignore_index nor in [0, V)): the lookup gives a row of zeros, the
