@@ -71,7 +71,7 @@ struct Plan {
     float *zt;                           // [Mp]
     // log probabilities
     bool logp;
-    float zscale, inv_t;                 // log2(e) / temperature, 1 / temperature
+    float zscale, zfactor, inv_t;        // log2(e) and 1 over the temperature, for logits as they are formed; 1 / temperature
     float range;                         // largest entropy + 1: bounds the gradient's entries
     float *weighted;                     // [vocab_groups][Mp]: sum of e^(z - max) (z - max), binary
     float *c1, *g1;                      // gradient per position: slope along log P, and that of the token's own entry

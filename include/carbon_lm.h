@@ -198,6 +198,8 @@ int64_t carbon_linear_xent_bwd_workspace(int64_t M, int64_t D, int64_t V);
  * top_log_probs come from the tensor cores' logits, as log_probs do (the same bits
  * for the same entry), but are never above the one before.
  *
+ * Logits are multiplied by 1 + D 2^-30, which makes up for the mean of what the
+ * tensor cores' accumulator drops.
  * Errors of log_probs and lse: those of the loss above, of z / temperature;
  * entropy: (16 + log2 V) 2^-23 (entropy + 1) and 2 (entropy + 1) times the largest
  * error of a logit, over the temperature.  A position's results do not depend on
