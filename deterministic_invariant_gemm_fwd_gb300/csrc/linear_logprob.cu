@@ -35,6 +35,8 @@
 // whose two warps per scheduler have no time left for them, and 52 for the exact
 // logits of twelve candidates each); with the gradient 1.44 ms alone, 1.67 under the
 // power limit.  8 positions, five alternatives: 41 us, 24 of them the table.
+#include <cfloat>
+
 #include "xent_tiles.cuh"
 
 namespace carbon {
@@ -399,25 +401,30 @@ cudaError_t launch_top(const Plan &p, const JoinArgs &j, int sms, cudaStream_t s
                     dim3((unsigned)((p.M + rows - 1) / rows)), dim3(kTopThreads), 0, s, 1, p, j);
 }
 
+constexpr double kLog2eDouble = 1.4426950408889634;
+
+// 1 / temperature for logits as they are formed.  The tensor cores' accumulator rounds
+// toward zero.  A step of 16 products takes about 2^-25 of the sum so far with it;
+// over D / 16 steps that sum is half the final one on average, so a logit comes out
+// smaller by D 2^-30 of itself: measured as 0.9 to 1.2 times that for D = 768 to
+// 16384, zero-mean inputs, bf16 and fp16.  The logits' factors put it back (200 x 2048
+// x 50257: mean error of lse 8e-6 without, 3e-7 with; entropy's 9e-7 and 4e-8 of
+// itself).  It is a 128th of the bound of one logit's error.
+double factor_of(int64_t D, float temperature) { return (1.0 + (double)D * 0x1p-30) / (double)temperature; }
+
 carbon_status_t check_logp(const void *x, const void *table, const int64_t *tokens, int64_t M, int64_t D, int64_t V,
                            float temperature, int dtype) {
     const carbon_status_t st = check(x, table, tokens, M, D, V, CARBON_REDUCE_NONE, dtype);
     if (st != CARBON_OK) return st;
-    if (!(temperature > 0.0f) || !(temperature < INFINITY) || !(1.0f / temperature < INFINITY)) return CARBON_ERR_INVALID_ARG;
+    if (!(temperature > 0.0f) || !(temperature < INFINITY)) return CARBON_ERR_INVALID_ARG;
+    if (!(kLog2eDouble * factor_of(D, temperature) < FLT_MAX)) return CARBON_ERR_INVALID_ARG;
     return CARBON_OK;
 }
 
-// The tensor cores' accumulator rounds toward zero.  A step of 16 products takes
-// about 2^-25 of the sum so far with it; over D / 16 steps that sum is half the final
-// one on average, so a logit comes out smaller by D 2^-30 of itself: measured as 0.9
-// to 1.2 times that for D = 768 to 16384, zero-mean inputs, bf16 and fp16.  The
-// logits' factors put it back (200 x 2048 x 50257: mean error of lse 8e-6 without,
-// 3e-7 with; entropy's 9e-7 and 4e-8 of itself).  It is a 128th of the bound of one
-// logit's error.
 void set_temperature(Plan *p, float temperature) {
-    const double back = (1.0 + (double)p->D * 0x1p-30) / (double)temperature;
-    p->zscale = (float)(1.4426950408889634 * back);
-    p->zfactor = (float)back;
+    const double factor = factor_of(p->D, temperature);
+    p->zscale = (float)(kLog2eDouble * factor);
+    p->zfactor = (float)factor;
     p->inv_t = (float)(1.0 / (double)temperature);
     p->range = logf((float)p->V) + 1.0f;
 }

@@ -187,10 +187,11 @@ int64_t carbon_linear_xent_bwd_workspace(int64_t M, int64_t D, int64_t V);
  *
  * all fp32 [M].  top_ids (int64) and top_log_probs (fp32), [M,top]: the `top`
  * largest entries of P with their logarithms, largest first; not read or written
- * for top = 0.  top <= 28 and top <= V, temperature > 0, else
- * CARBON_ERR_INVALID_ARG.  Positions whose token is ignore_index (or names no
- * entry, see above) cost nothing: log_probs, entropy, lse and top_log_probs 0,
- * top_ids -1.  Places for which no logit above -infinity is left: -1, -infinity.
+ * for top = 0.  top <= 28 and top <= V, temperature > 0 (and log2(e) / temperature
+ * an fp32 number), else CARBON_ERR_INVALID_ARG.  Positions whose token is
+ * ignore_index (or names no entry, see above) cost nothing: log_probs, entropy, lse
+ * and top_log_probs 0, top_ids -1.  Places for which no logit above -infinity is
+ * left: -1, -infinity.
  *
  * Order of the alternatives: the top + 4 largest logits as the tensor cores form
  * them (their error: see carbon_linear_xent_fwd), ordered by their logits as

@@ -51,7 +51,7 @@ MORE = [(c, d) for c in ALL for d in (dict(dtype=5), dict(dtype=-1), dict(nbytes
     (logp_fwd, dict(top=-1)), (logp_fwd, dict(top=29, V=100)), (logp_fwd, dict(top=6, V=5)), (logp_fwd, dict(V=0, top=0)),
     (logp_fwd, dict(D=0)), (logp_bwd, dict(V=0)), (lora_fwd, dict(r=136)), (lora_fwd, dict(K=0)), (lora_fwd, dict(N=0)),
     (lora_fwd, dict(n=0)), (lora_bwd, dict(r=0)), (lora_bwd, dict(dx=None, da=None, db=None)),
-] + [(c, dict(temp=t)) for c in (logp_fwd, logp_bwd) for t in (0.0, -1.0, float("nan"), float("inf"), 1e-42)]
+] + [(c, dict(temp=t)) for c in (logp_fwd, logp_bwd) for t in (0.0, -1.0, float("nan"), float("inf"), 1e-42, 3.5e-39)]
 
 
 @pytest.mark.parametrize("call,args", SIZES + NULL + MORE, ids=lambda v: v.__name__ if callable(v) else str(v))
