@@ -21,17 +21,18 @@
 // 32) classes of entries, which all CTAs keep up to date in global memory, prove
 // others too small: the 12th largest of 16 is about the 21st largest of all
 // logits so far.  A run over the first 2048 entries, ahead of the others, fills
-// these classes.  A warp per position takes the top + 4 largest of all
-// lists, forms their logits again, from exact products with a compensated sum
-// (about 2^-44 relative to the sum of the products' magnitudes), and orders them by
-// these: logits that fp32 accumulators cannot tell apart come in the order of
-// float64, equal ones by entry.  Up to 256 positions have their logits stored
-// instead: filling lists is what would take most of the time there.  (The tensor cores' values differ from these by a few units of 2^-24;
-// four spare candidates make room for as many that such an error could move
-// across the last place.)
+// these classes for them, in blocks of 32; the others' are groups of 128.  No entry
+// is in two classes, else a logit would count twice.  A warp per position takes the
+// top + 4 largest of all lists, forms their logits again, from exact products with a
+// compensated sum (about 2^-44 relative to the sum of the products' magnitudes), and
+// orders them by these: logits that fp32 accumulators cannot tell apart come in the
+// order of float64, equal ones by entry.  Up to 256 positions have their logits stored
+// instead: filling lists is what would take most of the time there.  (The tensor cores'
+// values differ from these by a few units of 2^-24; four spare candidates make room for
+// as many that such an error could move across the last place.)
 //
 // Bound: the tensor cores, as for the loss.  8192 x 768 x 50257 bf16, a call as a
-// graph: 327 us, with eight alternatives 447 (the lists in the tile kernel's epilogue,
+// graph: 332 us, with eight alternatives 454 (the lists in the tile kernel's epilogue,
 // whose two warps per scheduler have no time left for them, and 52 for the exact
 // logits of twelve candidates each); with the gradient 1.44 ms alone, 1.67 under the
 // power limit.  8 positions, five alternatives: 41 us, 24 of them the table.
@@ -478,10 +479,10 @@ carbon_status_t carbon_linear_logp_fwd(float *log_probs, float *entropy, float *
     a.targets = tokens; a.ignore_index = ignore_index; a.reduction = CARBON_REDUCE_NONE;
     a.losses = log_probs; a.lse_out = lse; a.entropy_out = entropy; a.top_ids = top_ids; a.top_logp = top_log_probs;
     cudaError_t err = launch_prepare<true>(p, a, x, s);
-    if (err == cudaSuccess && p.lists > 0 && V >= 8 * kPilot) {
+    if (err == cudaSuccess && p.piloted > 0) {
         Plan q = p;                                       // with a ticket of its own
         q.pilot = true;
-        q.V = kPilot;
+        q.V = p.piloted;
         q.ticket = p.joined;
         err = launch_tiles<false, true, 0>(q, table, nullptr, sms, s);
     }

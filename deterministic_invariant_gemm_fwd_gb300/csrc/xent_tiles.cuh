@@ -695,7 +695,8 @@ __device__ __forceinline__ float just_below(uint32_t t) {
 }
 
 // A logit below the k-th largest of the largest logits of S classes of entries is
-// none of the row's k largest.  (Of 16 classes the 12th largest is about the 21st
+// none of the row's k largest, the classes having no entry in common (xent_units.h).
+// (Of 16 classes the 12th largest is about the 21st
 // largest logit of all entries so far.)  Ordered; 0: fewer than k classes so far.
 template <int S>
 __device__ __forceinline__ uint32_t class_bound(const unsigned int *largest, int k) {
@@ -736,11 +737,11 @@ __device__ __forceinline__ void logp_rows(const Plan &p, const Unit &o, uint32_t
             uint32_t r[64];
             tmem_ld64(tmem + (uint32_t)c, r);
 #pragma unroll
-            for (int h = 0; h < 64; h += 32) {
+            for (int h = 0; h < 64; h += kPilotBlock) {
                 float most = __uint_as_float(r[h]);
 #pragma unroll
-                for (int i = 1; i < 32; ++i) most = fmaxf(most, __uint_as_float(r[h + i]));
-                const int64_t at = (int64_t)row * classes + (o.n0 + c + h) / 32 % classes;
+                for (int i = 1; i < kPilotBlock; ++i) most = fmaxf(most, __uint_as_float(r[h + i]));
+                const int64_t at = (int64_t)row * classes + pilot_class(p, o.n0 + c + h);
                 if (most > -INFINITY && tgt + o.n0 >= 0 && CHK(at, 1, p.Mp * classes)) atomicMax(p.largest + at, ordered(most));
             }
         }
@@ -827,9 +828,9 @@ __device__ __forceinline__ void logp_rows(const Plan &p, const Unit &o, uint32_t
         p.weighted[at] = weighted;
     }
     if constexpr (LIST > 0) {
-        constexpr int S = LIST <= kTopFew ? kTopClassesFew : kTopClassesMany;
-        if (largest > floor && CHK(row, 1, p.Mp))
-            atomicMax(p.largest + (int64_t)row * S + (o.n0 + g) / kGroup % S, ordered(largest));
+        const int cls = group_class(p, o.n0 + g);
+        const int64_t at = (int64_t)row * top_classes(p.listed) + cls;
+        if (cls >= 0 && largest > floor && CHK(at, 1, p.Mp * top_classes(p.listed))) atomicMax(p.largest + at, ordered(largest));
     }
 }
 

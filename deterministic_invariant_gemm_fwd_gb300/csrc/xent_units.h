@@ -33,9 +33,11 @@ constexpr int kTopFew = 12, kTopClassesFew = 16, kTopClassesMany = 32;
 XENT_HD inline int top_classes(int listed) { return listed <= kTopFew ? kTopClassesFew : kTopClassesMany; }
 // Entries that a run ahead looks at, a multiple of a tile's, where there are eight
 // times as many.  Without it every thread's first list takes about fifty logits
-// (8192 x 768 x 50257: 463 us for 447 with top 8, 627 for 535 with top 20; 1024
-// entries: 456 and 557).
+// (8192 x 768 x 50257: 465 us for 454 with top 8, 628 for 541 with top 20; 1024
+// entries: 453 and 561; where 40% of the alternatives are among the first 2048
+// entries 442 for 437 and 586 for 508).
 constexpr int kPilot = 2048;
+constexpr int kPilotBlock = 32;          // entries whose largest logit it takes
 constexpr int kSpan = 8;                 // tiles that a pair takes one after another for the alternatives, at most
 constexpr int64_t kCountAhead = 16384;   // longer lists of positions are counted by a kernel of their own
 
@@ -78,7 +80,8 @@ struct Plan {
     int top, listed;                     // alternatives asked for and kept
     float *logits;                       // [M][pitch]: few positions' logits; else null, and lists:
     int64_t pitch;
-    bool pilot;                          // a run ahead over few entries, which leaves floors for the lists
+    bool pilot;                          // this is the run ahead over few entries, which fills their classes
+    int piloted;                         // entries below this one have a run ahead for their classes; 0: there is none
     int span, spans;                     // tiles of a row tile that form a unit of the ticket, and their number
     int lists;                           // lists of candidates per row: one per span and column half
     unsigned int *largest;               // [Mp][top_classes]: largest logits (ordered) so far of classes of entries; 0: none
@@ -175,6 +178,7 @@ inline int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, b
             p.span = (int)(span < 1 ? 1 : span > kSpan ? kSpan : span);
             p.spans = (int)((tiles + p.span - 1) / p.span);
             p.lists = p.spans * (p.lwidth / kGroup);
+            p.piloted = V >= 8 * kPilot ? kPilot : 0;
             p.largest = reinterpret_cast<unsigned int *>(take(4 * p.Mp * top_classes(p.listed)));
             p.floor = reinterpret_cast<unsigned int *>(take(4 * p.Mp));
             p.list = reinterpret_cast<unsigned long long *>(take(8 * (int64_t)p.lists * (p.listed + 1) * p.Mp));
@@ -183,6 +187,18 @@ inline int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, b
     if (out) *out = p;
     return used + 128;                   // room to align the base to 128 bytes
 }
+
+// ---- classes of entries ----------------------------------------------------------
+//
+// The largest logits of k classes bound the k-th largest of all only where no entry
+// is in two of them.  The run ahead takes entries below `piloted` in blocks of
+// kPilotBlock, the run over all takes the others in groups of kGroup and leaves
+// those alone (its own classes for them would count a logit twice: of six large
+// ones below 2048, twelve classes).
+
+// The class of the block, or group, that starts at `entry`; -1: none of this run's.
+XENT_HD inline int pilot_class(const Plan &p, int entry) { return entry < p.piloted ? entry / kPilotBlock % top_classes(p.listed) : -1; }
+XENT_HD inline int group_class(const Plan &p, int entry) { return entry < p.piloted ? -1 : entry / kGroup % top_classes(p.listed); }
 
 // ---- the list of units -------------------------------------------------------------
 
