@@ -12,7 +12,7 @@
 // Entropy: with m the row's largest z' and S = sum exp(z' - m),
 //   entropy = log S - (sum exp(z' - m) (z' - m)) / S,
 // two terms that are not negative, so nothing cancels; each 128 entries give a
-// (max, sum, weighted sum) triple.
+// (max, sum, weighted sum) triple.  log_prob = (z'[token] - m) - log S likewise.
 //
 // Alternatives: a thread keeps the largest logits that it sees of its row, top + 4
 // of them, and a threshold that only a larger logit passes: after a thousand
@@ -55,6 +55,16 @@ __device__ __forceinline__ void two_sum(float a, float b, float &s, float &r) {
     s = __fadd_rn(a, b);
     const float d = __fsub_rn(s, a);
     r = __fadd_rn(__fsub_rn(a, __fsub_rn(s, d)), __fsub_rn(b, d));
+}
+
+// The log probability of a logit z, from the row's largest times log2(e) /
+// temperature and log2 of the sum of the others' powers relative to it: a difference of
+// logits, rounded once, in place of one of two large numbers (z' - lse was up to 1.5e-4
+// above 0 for logits of 8 at temperature 1e-3).  What the sum's own rounding leaves
+// above 0 is cut; NaN stays.
+__device__ __forceinline__ float log_prob(const Plan &p, float z, float mx, float l2) {
+    const float v = (fmaf(z, p.zscale, -mx) - l2) * kLn2;
+    return v > 0.0f ? 0.0f : v;
 }
 
 // Two 16-bit elements as fp32.
@@ -145,11 +155,11 @@ __device__ __forceinline__ void put_top(const Plan &p, const JoinArgs &a, int64_
         const bool same = ho == hi && lo_o == lo;
         rank += ho > hi || (ho == hi && lo_o > lo) || (same && eo < entry) ? 1 : 0;
     }
-    // The logarithms from the same logits as log_probs and lse, whose errors have
+    // The logarithms from the same logits as log_probs and the sums, whose errors have
     // the same sign: those of the difference mostly cancel.  Not increasing: where
     // the order was decided by less than these errors, the one before counts.
-    const float lse = a.lse[m];
-    float z = unordered((uint32_t)(mine >> 32)) * p.zfactor - lse;
+    const float mx = p.zt[row], l2 = p.weighted[row];     // as logp_join_kernel leaves them
+    float z = log_prob(p, unordered((uint32_t)(mine >> 32)), mx, l2);
     int from = lane;                                      // the lane whose rank is this lane's number
     for (int i = 0; i < places; ++i)
         if (__shfl_sync(0xffffffffu, rank, i) == lane) from = i;
@@ -163,7 +173,7 @@ __device__ __forceinline__ void put_top(const Plan &p, const JoinArgs &a, int64_
     if (lane < p.top && CHK(m * p.top + lane, 1, p.M * p.top)) {
         // fewer logits than places: the rest of them are -infinity
         a.top_ids[m * p.top + lane] = lane < places ? (int64_t)id : -1;
-        a.top_logp[m * p.top + lane] = lse != lse ? lse : lane < places ? z : -INFINITY;
+        a.top_logp[m * p.top + lane] = l2 != l2 ? l2 : lane < places ? z : -INFINITY;
     }
 }
 
@@ -384,11 +394,13 @@ logp_join_kernel(const Plan p, const JoinArgs a) {
     __syncthreads();
     if (t == 0 && row < kept) {
         for (int i = 1; i < 32; ++i) join(part[i][r].max, part[i][r].sum, part[i][r].weighted);
-        const float l = (mx + log2f(sum)) * kLn2;
+        const float l2 = log2f(sum), h = (l2 - __fdiv_rn(weighted, sum)) * kLn2;
         const int64_t m = p.rowmap[row];
-        a.lse[m] = l;
-        a.log_probs[m] = p.zt[row] * p.zfactor - l;
-        a.entropy[m] = (log2f(sum) - __fdiv_rn(weighted, sum)) * kLn2;
+        a.lse[m] = (mx + l2) * kLn2;
+        a.log_probs[m] = log_prob(p, p.zt[row], mx, l2);
+        a.entropy[m] = h < 0.0f ? 0.0f : h;               // NaN stays
+        p.zt[row] = mx;                                   // for the alternatives, read above for the last time
+        p.weighted[row] = l2;
     }
 }
 
@@ -425,7 +437,6 @@ carbon_status_t check_logp(const void *x, const void *table, const int64_t *toke
 void set_temperature(Plan *p, float temperature) {
     const double factor = factor_of(p->D, temperature);
     p->zscale = (float)(kLog2eDouble * factor);
-    p->zfactor = (float)factor;
     p->inv_t = (float)(1.0 / (double)temperature);
     p->range = logf((float)p->V) + 1.0f;
 }

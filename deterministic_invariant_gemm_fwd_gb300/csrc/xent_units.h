@@ -70,12 +70,14 @@ struct Plan {
     void *xc, *g;
     float *acc;                          // [slots][Mp][D]
     struct float2 *pairs;                // [vocab_groups][Mp]
-    float *zt;                           // [Mp]
+    float *zt;                           // [Mp]: the target's logit
     // log probabilities
     bool logp;
-    float zscale, zfactor, inv_t;        // log2(e) and 1 over the temperature, for logits as they are formed; 1 / temperature
+    float zscale, inv_t;                 // log2(e) over the temperature, for logits as they are formed; 1 / temperature
     float range;                         // largest entropy + 1: bounds the gradient's entries
     float *weighted;                     // [vocab_groups][Mp]: sum of e^(z - max) (z - max), binary
+                                         // once joined: zt is the largest logit times zscale, weighted's first
+                                         // group log2 of the sum of powers relative to it
     float *c1, *g1;                      // gradient per position: slope along log P, and that of the token's own entry
     int top, listed;                     // alternatives asked for and kept
     float *logits;                       // [M][pitch]: few positions' logits; else null, and lists:

@@ -203,8 +203,11 @@ int64_t carbon_linear_xent_bwd_workspace(int64_t M, int64_t D, int64_t V);
  * tensor cores' accumulator drops.
  * Errors of log_probs and lse: those of the loss above, of z / temperature;
  * entropy: (16 + log2 V) 2^-23 (entropy + 1) and 2 (entropy + 1) times the largest
- * error of a logit, over the temperature.  A position's results do not depend on
- * the other positions. */
+ * error of a logit, over the temperature.  log_probs and top_log_probs are formed as
+ * differences to the largest logit, so what is near 0 has small errors (where the
+ * logits are exact, (16 + log2 V + D / 128) 2^-23 (1 + |log_probs| + entropy)); they are never
+ * above 0, and entropy never below.  A position's results do not depend on the other
+ * positions. */
 carbon_status_t carbon_linear_logp_fwd(float *log_probs, float *entropy, float *lse,
                                        int64_t *top_ids, float *top_log_probs, const void *x,
                                        const void *table, const int64_t *tokens, int64_t M,
