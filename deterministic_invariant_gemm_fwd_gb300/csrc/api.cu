@@ -6,6 +6,8 @@
 // sgemm-bi page, "Use") with weights stored [in, out].
 #include "carbon_internal.h"
 
+#include <cudaTypedefs.h>
+
 #include <atomic>
 #include <cstdio>
 #include <cstdlib>
@@ -29,6 +31,19 @@ carbon_status_t note_cuda(cudaError_t err) {
 
 void count_launch(int n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 
+// Whether the calling thread has a current CUDA context.
+static bool has_context() {
+    static const PFN_cuCtxGetCurrent_v4000 get = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *fn = nullptr;
+        const bool found = cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &fn, 4000, cudaEnableDefault, &q) == cudaSuccess &&
+                           q == cudaDriverEntryPointSuccess;
+        return found ? reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(fn) : nullptr;
+    }();
+    CUcontext c = nullptr;
+    return get != nullptr && get(&c) == CUDA_SUCCESS && c != nullptr;
+}
+
 carbon_status_t current_device(int *device, int *sm_count) {
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -47,7 +62,9 @@ carbon_status_t current_device(int *device, int *sm_count) {
     if (cached < 0) return CARBON_ERR_UNSUPPORTED;
     // A thread's first CUDA call may be this one (an autograd worker's): the
     // driver's tensor-map encoder needs a context that is bound to the thread.
-    if ((err = cudaSetDevice(dev)) != cudaSuccess) return note_cuda(err);
+    // cudaSetDevice binds the device's primary one, so a thread that has a
+    // context, maybe its own, keeps it.
+    if (!has_context() && (err = cudaSetDevice(dev)) != cudaSuccess) return note_cuda(err);
     if (device) *device = dev;
     if (sm_count) *sm_count = cached;
     return CARBON_OK;
