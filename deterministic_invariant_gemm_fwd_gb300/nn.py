@@ -468,9 +468,8 @@ def clip_grad_norm_(parameters, max_norm, eps=1e-6):
     their device.  The norm's sum has a fixed order, so it and the gradients
     are the same bits in every run.  Gradients: contiguous CUDA tensors of one
     device, none of them sharing memory."""
-    if isinstance(parameters, torch.Tensor):
-        parameters = [parameters]
+    parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
     grads = [p.grad for p in parameters if p.grad is not None]
     if not grads:
-        return torch.zeros(())
+        return torch.zeros((), dtype=torch.float32, device=parameters[0].device if parameters else None)
     return clip_grads(grads, max_norm, eps)
