@@ -244,7 +244,9 @@ clip_scale_kernel(const __grid_constant__ Table<N> t, const double *__restrict__
     const float n = (float)sqrt(block_sum(s));
     if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
     if (!scale) return;
-    const float ratio = __fdiv_rn(max_norm, n + eps), factor = ratio > 1.0f ? 1.0f : ratio;     // NaN stays
+    // 0 / 0 (only zeros) and an infinite bound scale nothing; a NaN norm stays
+    const float ratio = n + eps == 0.0f || (max_norm == INFINITY && n == n) ? 1.0f : __fdiv_rn(max_norm, n + eps);
+    const float factor = ratio > 1.0f ? 1.0f : ratio;
     int from, to;
     run_of(t, &from, &to);
     if (from >= to) return;

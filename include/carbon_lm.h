@@ -310,7 +310,8 @@ int64_t carbon_lora_linear_bwd_workspace(int64_t M, int64_t K, int64_t N, int64_
  * grads[i] (in place: where the factor is 1 nothing is written); what is written
  * may not overlap anything else (CARBON_ERR_INVALID_ARG).  A NaN among the
  * gradients makes the norm and all of out NaN; an infinity makes the norm
- * infinite and the factor 0.
+ * infinite and the factor 0.  The factor is 1 for max_norm = infinity (unless the
+ * norm is NaN), and where norm + eps = 0.
  *
  * Squares are summed in fp32 by 32, in float64 from there on; squares outside
  * fp32's range are scaled, so that the norm overflows only where it is no fp32
