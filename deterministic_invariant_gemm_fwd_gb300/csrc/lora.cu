@@ -169,7 +169,7 @@ struct ShrinkArgs {
     void *u;                             // [M][kPlanes][rp]
     TileList *lists;                     // [row tiles of 256]
     int64_t M, n;
-    int rp;                              // rank, rounded up to 16
+    int r, rp;                           // rank, and rounded up to 16
     int k_blocks, per_piece, pieces;     // the reduction in 1, 2, 4 or 8 pieces of per_piece k-blocks
     int cluster, each;                   // CTAs per tile, and their pieces each
     int subsets;                         // clusters per tile: each takes part of the tile's adapters
@@ -482,12 +482,13 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                     v[q] = make_float4(v[q].x + v[q + step].x, v[q].y + v[q + step].y, v[q].z + v[q + step].z, v[q].w + v[q + step].w);
         const float4 s = v[0];
         const int id = g.id[row];
-        const float scale = id >= 0 ? a.scales[id] : 0.0f;
+        const bool live = id >= 0 && c < a.r;             // what pads the rank is zero, not infinity times zero
+        const float scale = live ? a.scales[id] : 0.0f;
         const float w[4] = {s.x * scale, s.y * scale, s.z * scale, s.w * scale};
         float hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float v = id >= 0 ? w[k] : 0.0f;
+            const float v = live ? w[k] : 0.0f;
             hi[k] = F16 ? __half2float(__float2half_rn(v)) : __bfloat162float(__float2bfloat16_rn(v));
             lo[k] = fabsf(hi[k]) < INFINITY ? v - hi[k] : 0.0f;
         }
@@ -1185,7 +1186,7 @@ cudaError_t launch_shrink(const Sizes &z, bool f16, const void *rows, const void
     if (err != cudaSuccess) return err;
     ShrinkArgs a = {};
     a.ids = ids; a.scales = scales; a.u = u; a.lists = k.lists;
-    a.M = z.M; a.n = z.n; a.rp = z.rp();
+    a.M = z.M; a.n = z.n; a.r = (int)z.r; a.rp = z.rp();
     a.k_blocks = (int)((R + kBK - 1) / kBK);
     // pieces by the reduction's length alone, so that a row's sum does not depend
     // on the number of rows

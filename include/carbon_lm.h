@@ -257,7 +257,9 @@ int64_t carbon_linear_logp_bwd_workspace(int64_t M, int64_t D, int64_t V);
  * the forward and read by the backward pass: [M][3][r rounded up to 16], the
  * 16-bit terms hi and lo of u (u = hi + lo to 2^-17 in bf16, 2^-22 in fp16,
  * relative, and to fp16's smallest step 2^-24), and lo times 2^11.  With fp16 a
- * |u| above 65504 is infinite.
+ * |u| above 65504 is infinite.  An infinity in x (dy) goes where the formulas take it;
+ * one in an adapter's b (a; for the adapters' gradients one in x or dy) may give NaN
+ * in place of infinity, for it meets both terms.
  *
  * dtype: CARBON_BF16 or CARBON_F16 (CARBON_F32: CARBON_ERR_UNSUPPORTED).  K, N
  * and r multiples of 8, and y, u, x, w, a, b (dx, da, db, dy) 16-byte aligned, else
