@@ -378,6 +378,8 @@ def lora_linear(x, weight, a, b, adapters, scales, bias=None):
         raise ValueError(f"adapters has shape {tuple(adapters.shape)}; expected {tuple(x.shape[:-1])}")
     if scales.requires_grad:
         raise ValueError("scales are constants: no gradient of them is formed")
+    if x.dtype == torch.float32:
+        raise TypeError("low-rank adapters take bfloat16 or float16, as the tensor-core tier does")
     return _LoraLinearFunction.apply(x, weight, bias, a, b, adapters, scales)
 
 
@@ -385,11 +387,18 @@ class LoraLinear(torch.nn.Module):
     """A linear layer, frozen unless train_base, with `adapters` low-rank adapters
     of rank `rank` and factor alpha / rank: forward(x, adapters) -> y, adapters
     int64 of x's leading shape or one number for all rows.  b starts at zero: a
-    new adapter changes nothing."""
+    new adapter changes nothing.  rank: a multiple of 8 up to 128; the layer's widths:
+    multiples of 8; its type when it is called: bfloat16 or float16."""
 
     def __init__(self, linear: Linear, adapters, rank, alpha=None, train_base=False):
         super().__init__()
         K, N = linear.weight.shape
+        if rank % 8 or not 8 <= rank <= 128:
+            raise ValueError(f"rank {rank}; expected a multiple of 8 up to 128")
+        if adapters < 1:
+            raise ValueError(f"{adapters} adapters; expected one or more")
+        if K % 8 or N % 8:
+            raise ValueError(f"a layer of {K} x {N}; widths must be multiples of 8")
         self.weight, self.bias = linear.weight, linear.bias
         if not train_base:
             for p in (self.weight, self.bias):
@@ -404,6 +413,8 @@ class LoraLinear(torch.nn.Module):
 
     def forward(self, x, adapters):
         if not isinstance(adapters, torch.Tensor):
+            if not -1 <= adapters < len(self.scales):
+                raise ValueError(f"adapter {adapters}; expected -1 to {len(self.scales) - 1}")
             adapters = torch.full(x.shape[:-1], adapters, dtype=torch.int64, device=x.device)
         # fp32 also where the module was cast to another type
         return lora_linear(x, self.weight, self.a, self.b, adapters, self.scales.float(), self.bias)
