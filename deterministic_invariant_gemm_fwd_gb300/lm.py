@@ -328,17 +328,23 @@ def linear_log_probs_fwd(x, table, tokens, temperature=1.0, top=0, ignore_index=
     distribution's entropy, and the `top` (at most 28) most probable entries,
     most probable first.  Positions of token ignore_index give zeros, and -1
     among the ids."""
+    return _log_probs(x, table, tokens, temperature, top, ignore_index, stream, tokens.shape)
+
+
+def _log_probs(x, table, tokens, temperature, top, ignore_index, stream, shape):
+    """linear_log_probs_fwd with results of another shape of M positions."""
     import torch
     M, D, V, code = _logp_args(x, table, tokens, temperature)
     if not 0 <= top <= min(28, V):
         raise ValueError(f"top {top!r}; expected 0 to 28, and at most the {V} rows of the table")
     device = x.device
     s, empty, workspace = _begin(x, stream)
-    log_probs, entropy, lse = empty((3, M), torch.float32, device).unbind(0)
+    # allocations of their own: a user may keep one and change another in place
+    log_probs, entropy, lse = (empty(shape, torch.float32, device) for _ in range(3))
     best = ids = None
     if top:
-        best = empty((M, top), torch.float32, device)
-        ids = empty((M, top), torch.int64, device)
+        best = empty((*shape, top), torch.float32, device)
+        ids = empty((*shape, top), torch.int64, device)
     nbytes = _bytes(_b.lib.carbon_linear_logp_fwd_workspace(M, D, V, top))
     ws = workspace(nbytes, device)
     st = _b.lib.carbon_linear_logp_fwd(log_probs.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _p(ids), _p(best),

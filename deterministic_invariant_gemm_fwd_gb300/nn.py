@@ -43,7 +43,8 @@ import torch
 
 from . import (_dtype_code, carbon_gemm_dw, clip_grads, embedding_bwd, embedding_fwd,
                linear_cross_entropy_bwd, linear_cross_entropy_fwd, linear_dw, linear_dx, linear_fwd,
-               linear_log_probs_bwd, linear_log_probs_fwd, lora_linear_bwd, lora_linear_fwd, rms_norm_bwd, rms_norm_fwd)
+               linear_log_probs_bwd, lora_linear_bwd, lora_linear_fwd, rms_norm_bwd, rms_norm_fwd)
+from .lm import _log_probs
 
 
 def bias_grad(dY, stream=None, tier="exact"):
@@ -429,12 +430,12 @@ class _LinearLogProbsFunction(torch.autograd.Function):
     def forward(ctx, x, table, tokens, temperature, ignore_index):
         x2 = _flat(x, table.shape[1])
         t = tokens.reshape(-1).contiguous()
-        r = linear_log_probs_fwd(x2, table, t, temperature, 0, ignore_index)
-        ctx.save_for_backward(x2, table, t, r.lse, r.entropy)
+        r = _log_probs(x2, table, t, temperature, 0, ignore_index, None, tokens.shape)
+        # a copy: the result may be changed in place by its user
+        ctx.save_for_backward(x2, table, t, r.lse.view(-1), r.entropy.view(-1).clone())
         ctx.shape, ctx.temperature, ctx.ignore_index = x.shape, temperature, ignore_index
         ctx.set_materialize_grads(False)
-        # copies: views of one allocation could not be changed in place by their user
-        return r.log_probs.view(tokens.shape).clone(), r.entropy.view(tokens.shape).clone()
+        return r.log_probs, r.entropy
 
     @staticmethod
     @_once
@@ -454,9 +455,12 @@ def _token_shape(x, table, tokens):
 def linear_log_probs(x, table, tokens, temperature=1.0, ignore_index=-100):
     """(log probabilities, entropies), fp32 of tokens' shape: of tokens under the
     logits x . table^T / temperature, and of each position's distribution,
-    without storing the logits; both differentiable in x and table.  Zero where
-    the token is ignore_index."""
+    without storing the logits; both differentiable in x and table (the backward
+    pass forms both gradients, also where only one is required).  Zero where the
+    token is ignore_index."""
     _token_shape(x, table, tokens)
+    if not (torch.is_grad_enabled() and (x.requires_grad or table.requires_grad)):
+        return top_log_probs(x, table, tokens, 0, float(temperature), ignore_index)[:2]
     return _LinearLogProbsFunction.apply(x, table, tokens, float(temperature), ignore_index)
 
 
@@ -465,10 +469,8 @@ def top_log_probs(x, table, tokens, top, temperature=1.0, ignore_index=-100):
     each position (last dimension); not differentiable."""
     _token_shape(x, table, tokens)
     with torch.no_grad():
-        r = linear_log_probs_fwd(_flat(x, table.shape[1]), table, tokens.reshape(-1).contiguous(), temperature, top,
-                                 ignore_index)
-    shape = tokens.shape
-    return type(r)(*(v.view(shape) for v in r[:3]), *(None if v is None else v.view(*shape, top) for v in r[3:]))
+        return _log_probs(_flat(x, table.shape[1]), table, tokens.reshape(-1).contiguous(), temperature, top, ignore_index,
+                          None, tokens.shape)
 
 
 @torch.no_grad()
