@@ -373,7 +373,8 @@ def lora_linear(x, weight, a, b, adapters, scales, bias=None):
     plus scales[i] (x . a[i]) . b[i] for the rows whose adapter is i, in the same
     accumulator.  x [..., K], weight [K, N], a [n, K, r], b [n, r, N], adapters
     int64 of x's leading shape (-1: none), scales fp32 [n].  Differentiable in x,
-    weight, bias, a and b; gradients of what does not require one are not formed."""
+    weight, bias, a and b; gradients of what does not require one are not formed,
+    and without any no intermediate result is kept."""
     _width(x, weight.shape[0])
     if adapters.shape != x.shape[:-1]:
         raise ValueError(f"adapters has shape {tuple(adapters.shape)}; expected {tuple(x.shape[:-1])}")
@@ -381,6 +382,9 @@ def lora_linear(x, weight, a, b, adapters, scales, bias=None):
         raise ValueError("scales are constants: no gradient of them is formed")
     if x.dtype == torch.float32:
         raise TypeError("low-rank adapters take bfloat16 or float16, as the tensor-core tier does")
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias, a, b))):
+        y = lora_linear_fwd(_flat(x, weight.shape[0]), weight, a, b, adapters.reshape(-1).contiguous(), scales, bias)
+        return y.view(*x.shape[:-1], weight.shape[1])
     return _LoraLinearFunction.apply(x, weight, bias, a, b, adapters, scales)
 
 
