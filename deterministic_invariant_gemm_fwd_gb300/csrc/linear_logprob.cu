@@ -121,6 +121,7 @@ template <bool F16, int W, typename Sync>
 __device__ __forceinline__ void put_top(const Plan &p, const JoinArgs &a, int64_t row, uint64_t mine, int places, int part,
                                         float *hi_of, float *lo_of, Sync sync) {
     const int lane = threadIdx.x % 32;
+    const float mx = p.zt[row], l2 = p.weighted[row];     // as logp_join_kernel leaves them
     // their logits again, G at a time; lane e then has that of place e
     const uint32_t entry = ~(uint32_t)mine;
     const int64_t m = p.rowmap[row];
@@ -158,7 +159,6 @@ __device__ __forceinline__ void put_top(const Plan &p, const JoinArgs &a, int64_
     // The logarithms from the same logits as log_probs and the sums, whose errors have
     // the same sign: those of the difference mostly cancel.  Not increasing: where
     // the order was decided by less than these errors, the one before counts.
-    const float mx = p.zt[row], l2 = p.weighted[row];     // as logp_join_kernel leaves them
     float z = log_prob(p, unordered((uint32_t)(mine >> 32)), mx, l2);
     int from = lane;                                      // the lane whose rank is this lane's number
     for (int i = 0; i < places; ++i)
@@ -419,8 +419,10 @@ constexpr double kLog2eDouble = 1.4426950408889634;
 // 1 / temperature for logits as they are formed.  The tensor cores' accumulator rounds
 // toward zero.  A step of 16 products takes about 2^-25 of the sum so far with it;
 // over D / 16 steps that sum is half the final one on average, so a logit comes out
-// smaller by D 2^-30 of itself: measured as 0.9 to 1.2 times that for D = 768 to
-// 16384, zero-mean inputs, bf16 and fp16.  The logits' factors put it back (200 x 2048
+// smaller by D 2^-30 of itself: measured as 1.0 to 1.1 times that in bf16 and 1.1 to
+// 1.3 in fp16 for D = 768 to 16384 and zero-mean inputs, 1.1 and 1.6 to 1.8 for
+// inputs of mean 1/2 (a sum that fp32 holds exactly loses nothing and gets this
+// error instead).  The logits' factors put it back (200 x 2048
 // x 50257: mean error of lse 8e-6 without, 3e-7 with; entropy's 9e-7 and 4e-8 of
 // itself).  It is a 128th of the bound of one logit's error.
 double factor_of(int64_t D, float temperature) { return (1.0 + (double)D * 0x1p-30) / (double)temperature; }
