@@ -65,3 +65,16 @@ def test_the_number_of_positions_does_not_show(top):
         part = cg.linear_log_probs_fwd(x[a:b], table, t[a:b], top=top)
         assert all(torch.equal(p, q[a:b]) for p, q in zip(part, r))
     assert status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_equal_logits_with_a_run_ahead(dtype):
+    M, V = 300, 20000
+    g = gen(7)
+    t = torch.zeros(M, dtype=torch.long, device="cuda")
+    x = torch.randn(M, WIDTH, generator=g, device="cuda").to(DT[dtype])
+    some = torch.randn(400, WIDTH, generator=g, device="cuda").to(DT[dtype])
+    for top in (8, 28):
+        check_forward(x, some.repeat(50, 1), t, 1.0, top)               # fifty of each, every 400 entries
+        check_forward(x, some[:100].repeat_interleave(200, 0), t, 1.0, top)      # and side by side
+        check_forward(torch.zeros_like(x), some.repeat(50, 1), t, 1.0, top)
