@@ -35,7 +35,7 @@
 // graph: 332 us, with eight alternatives 454 (the lists in the tile kernel's epilogue,
 // whose two warps per scheduler have no time left for them, and 52 for the exact
 // logits of twelve candidates each); with the gradient 1.44 ms alone, 1.67 under the
-// power limit.  8 positions, five alternatives: 41 us, 24 of them the table.
+// power limit.  8 positions, five alternatives: 43 us, 24 of them the table.
 #include <cfloat>
 
 #include "xent_tiles.cuh"

@@ -1,8 +1,8 @@
 // tcgen05.cuh - inline-PTX wrappers for the fifth-generation tensor cores
 // (tcgen05: tensor-memory allocation, MMA issue and commit, tensor-memory
-// loads and stores) and the shared-memory matrix descriptor, used by the
-// tensor-core tier (tc_gemm.cu) and the exact tier's tensor-core kernel
-// (exact_tc.cu).
+// loads and stores) and the shared-memory matrix descriptor, used by every
+// tensor-core kernel: the tensor-core tier (tc_gemm.cu), the exact tier's
+// (exact_tc.cu), the output layer's (xent_tiles.cuh) and the adapters' (lora.cu).
 #pragma once
 
 #include <stdint.h>

@@ -1,7 +1,8 @@
-// xent_units.h - the output layer's loss and gradients as a list of units: sizes
-// and workspace addresses, the order of the units, and what each of them waits
-// for.  Used by linear_xent.cu; plain C++ as well, so that the order and the
-// waits can be checked on the host (tests/c/xent_units.cpp).
+// xent_units.h - the output layer's products as a list of units: sizes and
+// workspace addresses, the order of the units, what each of them waits for, and the
+// classes that bound the alternatives.  Used by linear_xent.cu and
+// linear_logprob.cu (through xent_tiles.cuh); plain C++ as well, so that the order,
+// the waits and the classes can be checked on the host (tests/c/xent_*.cpp).
 #pragma once
 
 #include <stdint.h>
@@ -168,7 +169,7 @@ inline int64_t make_plan(Plan *out, void *ws, int64_t M, int64_t D, int64_t V, b
         if (p.top > 0 && p.Mp == kBM) {
             // one row tile: its logits are less than what they are made of, and a
             // row of them is read in less time than lists take to fill
-            // (8 x 768 x 50257, top 5: 41 us instead of 61)
+            // (8 x 768 x 50257, top 5: 43 us instead of 61)
             p.pitch = round_up(V, kGroup);
             p.logits = reinterpret_cast<float *>(take(4 * M * p.pitch));
         } else if (p.top > 0) {

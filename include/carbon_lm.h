@@ -200,7 +200,9 @@ int64_t carbon_linear_xent_bwd_workspace(int64_t M, int64_t D, int64_t V);
  * for the same entry), but are never above the one before.
  *
  * Logits are multiplied by 1 + D 2^-30, which makes up for the mean of what the
- * tensor cores' accumulator drops.
+ * tensor cores' accumulator drops (sums that fp32 holds exactly are off by that much
+ * instead).  carbon_linear_xent_fwd does not: its loss and -log_probs of the same
+ * operands differ by about D 2^-30 of a logit.
  * Errors of log_probs and lse: those of the loss above, of z / temperature;
  * entropy: (16 + log2 V) 2^-23 (entropy + 1) and 2 (entropy + 1) times the largest
  * error of a logit, over the temperature.  log_probs and top_log_probs are formed as
